@@ -2,7 +2,8 @@
  * sg.h - C ABI of the GB300 mini-batch pipeline for sampling-based GNN
  * training: multi-hop neighbour sampling, ID dedup + relabel into per-hop
  * blocks, feature gather through an HBM hot-node cache, and mean
- * aggregation forward and backward.
+ * aggregation forward and backward; and what a training step needs beside
+ * them: learned embeddings, the loss, and the weights' update.
  *
  * The operations follow the GARDEN page ("GARDEN: Efficient GPU-Accelerated
  * Billion-Scale GNN Training via Caching-Sampling-Batching Co-Design"):
@@ -65,6 +66,11 @@ typedef int32_t sg_status;
 
 #define SG_F32 0                /* IEEE binary32 */
 #define SG_BF16 1               /* bfloat16, stored as uint16 bit patterns */
+
+/* Forms of a table gradient (sg_embed_bwd). */
+#define SG_GRAD_ROWS 0          /* one row per distinct ID, IDs ascending */
+#define SG_GRAD_DENSE 1         /* the whole table, zero rows included */
+#define SG_GRAD_ADD 2           /* added into rows that the caller holds */
 
 #define SG_MAX_HOPS 8
 #define SG_MAX_SUB 64           /* mini-batches per super-batch */
@@ -556,6 +562,125 @@ sg_status sg_sage_bwd(const void* d_h, const void* d_m, const void* d_W, int32_t
 
 /* Bytes of the workspace of sg_sage_bwd; 0 on bad arguments. */
 size_t sg_sage_bwd_workspace(int32_t n_cap, int32_t dim, int32_t dtype);
+
+/* ------------------------------------------------------ learned embeddings */
+/* Lookup of learned node (or token) embeddings with a scale:
+ *   out[i, :] = scale * table[ids[i], :]      i < n
+ * and a zero row where ids[i] = -1 (padding).  The product is taken in fp32 and
+ * rounded once to dtype_out.
+ *   d_table   device [n_rows x dim], row stride ld_table elements (>= dim)
+ *   d_ids     device int32 [n_cap]; in a pipeline the sampler's unique array,
+ *             so that out holds the input nodes' rows
+ *   d_n       device int32 count (n = *d_n <= n_cap) or NULL (n = n_cap)
+ *   d_out     device [n_cap x dim], row stride ld_out (>= dim); must not overlap
+ *             the table; rows i >= n and columns past dim are not touched
+ *   dtypes    SG_F32 or SG_BF16, in any combination
+ * Any dim >= 1 and any element alignment; rows of 8- or 16-byte units on
+ * matching boundaries move in such units.  Another ID out of range sets the
+ * device error word and its row is zero-filled. */
+sg_status sg_embed_fwd(const void* d_table, int32_t dtype_table, int64_t n_rows, int32_t dim, int64_t ld_table,
+                       const int32_t* d_ids, int64_t n_cap, const int32_t* d_n, float scale, void* d_out,
+                       int32_t dtype_out, int64_t ld_out, sg_stream_t stream);
+
+/* Gradient of the lookup with respect to the table, for g = dL/dout:
+ *   grad[v, :] = scale * sum over i < n with ids[i] = v, in ascending i, of g[i, :]
+ * The positions are sorted by ID (stable), so every sum has a fixed order: no
+ * float atomics, the same bits on every run.  Sums are held in fp32.
+ *   mode SG_GRAD_ROWS   d_rows (device int32 [n_cap]) gets the distinct IDs in
+ *                       ascending order, *d_n_rows (device int32) their number,
+ *                       and row j of d_grad [n_cap x dim] the gradient of table
+ *                       row d_rows[j]; entries past the count are not touched
+ *   mode SG_GRAD_DENSE  d_grad [n_rows x dim] is written whole (zero rows for
+ *                       IDs that do not occur); d_rows, d_n_rows NULL
+ *   mode SG_GRAD_ADD    grad is added into the rows of d_grad [n_rows x dim]
+ *                       that occur (accumulation over mini-batches; with
+ *                       scale = -rate * (the lookup's scale) and d_grad the
+ *                       table, a sparse SGD step); d_rows, d_n_rows NULL
+ *   d_g       device [n_cap x dim], row stride ld_g (>= dim); it must not
+ *             overlap d_grad
+ *   d_grad    row stride ld_grad (>= dim); columns past dim are not touched
+ *   dtypes    SG_F32 or SG_BF16, in any combination
+ *   d_workspace  device scratch of sg_embed_bwd_workspace(...) bytes, 256-byte
+ *             aligned, in no particular state
+ * IDs of -1 contribute nothing; another ID out of range sets the device error
+ * word and contributes nothing. */
+size_t sg_embed_bwd_workspace(int64_t n_cap, int64_t n_rows, int32_t dim, int32_t mode);
+sg_status sg_embed_bwd(const int32_t* d_ids, int64_t n_cap, const int32_t* d_n, int64_t n_rows, const void* d_g,
+                       int32_t dtype_g, int32_t dim, int64_t ld_g, float scale, int32_t mode, int32_t* d_rows,
+                       int32_t* d_n_rows, void* d_grad, int32_t dtype_grad, int64_t ld_grad, void* d_workspace,
+                       size_t workspace_bytes, sg_stream_t stream);
+
+/* ------------------------------------------------------------------- loss */
+/* Softmax cross-entropy of n rows of logits x with its gradient:
+ *   loss[r]    = log(sum_c exp(x[r, c])) - x[r, label[r]]
+ *   total      = {sum of loss (divided by max(1, v) with mean != 0), v},
+ *                v = the number of rows r < n whose label is not -1
+ *   grad[r, c] = w * (exp(x[r, c]) / sum_c' exp(x[r, c']) - (c == label[r])),
+ *                w = grad_scale, divided by max(1, v) with mean != 0
+ * A row with label -1 has loss 0 and a zero gradient.  Logits of -inf take no
+ * part (classes that are masked off: their gradient is 0).  A label whose own
+ * logit is -inf has loss +inf; in a row whose logits are all -inf the gradient
+ * is 0 as well.  +inf or NaN logits give NaN in their row (and in the total).
+ * Statistics are held in fp32; total's order of summation is fixed.
+ *   d_logits   device [n_cap x n_classes], row stride ld elements (>= n_classes),
+ *              SG_F32 or SG_BF16, any element alignment
+ *   d_n        device int32 count (n = *d_n <= n_cap) or NULL (n = n_cap)
+ *   d_labels   device int32 [n_cap]; -1 is ignored, another label out of range
+ *              sets the device error word and the row is ignored (it does count
+ *              in v)
+ *   d_loss     device fp32 [n_cap]: rows r < n written
+ *   d_total    device fp32 [2], or NULL
+ *   d_grad     device, dtype as the logits, row stride ld_grad (>= n_classes), or NULL
+ *              (loss only); may be d_logits itself with the same stride (in
+ *              place), but must not overlap it in any other way
+ *   d_workspace  device scratch of sg_xent_workspace(...) bytes, 256-byte
+ *              aligned, in no particular state */
+size_t sg_xent_workspace(int32_t n_cap, int32_t n_classes);
+sg_status sg_xent(const void* d_logits, int32_t dtype, int32_t n_cap, const int32_t* d_n, int32_t n_classes, int64_t ld,
+                  const int32_t* d_labels, int32_t mean, float grad_scale, float* d_loss, float* d_total, void* d_grad,
+                  int64_t ld_grad, void* d_workspace, size_t workspace_bytes, sg_stream_t stream);
+
+/* ------------------------------------------------- orthogonalised updates */
+#define SG_MAX_NS_STEPS 16
+
+/* Approximate orthogonalisation of `count` matrices by Newton-Schulz steps, as
+ * the Muon optimiser does: with G one matrix and s[k] its steps' coefficients
+ *   X = G / (||G||_F + eps), transposed when rows > cols
+ *   for k < steps:  A = X X^T;  X = (a_k I + b_k A + c_k A A) X
+ *   out = scale * X, transposed back
+ * Every singular value t of G / (||G||_F + eps) becomes f_k(..f_1(t)),
+ * f(t) = a t + b t^3 + c t^5.  The products run on the tensor cores with each
+ * operand held as two fp16 terms (22 bits), fp32 accumulation; the norm is
+ * summed in fp32 and fp64.
+ *   d_g, d_out  device, `dtype` (SG_F32 or SG_BF16); matrix q starts at element
+ *               q * rows * ld, its rows are ld (>= cols) elements apart
+ *               (ld_out for d_out).  d_out may be d_g with the same stride.
+ *   rows, cols  1 .. 65536; the smaller one at most 8192
+ *   steps       0 .. SG_MAX_NS_STEPS
+ *   h_coef      host, 3 * steps floats (a, b, c of each step), or NULL for
+ *               (3.4445, -4.7750, 2.0315) in every step.  |values| up to about
+ *               64 can be held on the way; a schedule that diverges gives inf
+ *               or NaN.
+ *   d_workspace device scratch of sg_orthogonalise_workspace(...) bytes,
+ *               256-byte aligned, in no particular state */
+size_t sg_orthogonalise_workspace(int32_t count, int32_t rows, int32_t cols);
+sg_status sg_orthogonalise(const void* d_g, int32_t dtype, int32_t count, int32_t rows, int32_t cols, int64_t ld,
+                           int32_t steps, const float* h_coef, float eps, float scale, void* d_out, int64_t ld_out,
+                           void* d_workspace, size_t workspace_bytes, sg_stream_t stream);
+
+/* One Muon step of `count` weight matrices (for instance a SAGE layer's W from
+ * sg_sage_bwd's dW):
+ *   m' = momentum * m + g;   u = nesterov ? g + momentum * m' : m'
+ *   w' = (1 - rate * weight_decay) * w - rate * scale * orthogonalise(u)
+ * with orthogonalise as above (scale 1).
+ *   d_w, d_w_out   device, dtype_w (SG_F32 or SG_BF16); may be the same array
+ *   d_g            device fp32; d_m, d_m_out device fp32, may be the same array
+ * All arrays hold count x rows x cols elements without gaps.  Other arguments
+ * as in sg_orthogonalise (and its workspace). */
+sg_status sg_muon_step(const void* d_w, int32_t dtype_w, const float* d_g, const float* d_m, int32_t count, int32_t rows,
+                       int32_t cols, float rate, float momentum, int32_t nesterov, float weight_decay, float scale,
+                       int32_t steps, const float* h_coef, float eps, void* d_w_out, float* d_m_out,
+                       void* d_workspace, size_t workspace_bytes, sg_stream_t stream);
 
 /* ------------------------------------------------------------ measurement */
 /* Streams `bytes` of device-accessible memory at d_src with 16-byte loads

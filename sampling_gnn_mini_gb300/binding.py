@@ -29,6 +29,10 @@ SG_ERR_TIMEOUT = 6
 SG_ERR_UNSUPPORTED = 7
 SG_F32 = 0
 SG_BF16 = 1
+SG_GRAD_ROWS = 0
+SG_GRAD_DENSE = 1
+SG_GRAD_ADD = 2
+SG_MAX_NS_STEPS = 16
 SG_MAX_HOPS = 8
 SG_MAX_SUB = 64
 SG_MAX_FANOUT = 256
@@ -45,7 +49,9 @@ EXPORTS = ["sg_version", "sg_last_error", "sg_stream_check", "sg_graph_load", "s
            "sg_sage_fwd", "sg_sage_bwd", "sg_sage_bwd_workspace", "sg_wait_probe", "sg_wait_probe_workspace",
            "sg_access_stats", "sg_rank_workspace", "sg_rank_by_score", "sg_graph_renumber", "sg_graph_copy_out",
            "sg_dyn_cache_create", "sg_dyn_cache_batch", "sg_dyn_cache_info", "sg_gather_reuse", "sg_match",
-           "sg_overlap", "sg_greedy_order", "sg_graph_in_degree"]
+           "sg_overlap", "sg_greedy_order", "sg_graph_in_degree", "sg_embed_fwd", "sg_embed_bwd_workspace",
+           "sg_embed_bwd", "sg_xent_workspace", "sg_xent", "sg_orthogonalise_workspace", "sg_orthogonalise",
+           "sg_muon_step"]
 
 
 class SgError(RuntimeError):
@@ -95,6 +101,7 @@ def load(build_if_missing: bool = True):
             raise RuntimeError("libsg.so is missing; run sampling_gnn_mini_gb300.build.build()")
         lib = ctypes.CDLL(_build.LIB)
         vp, i32, i64, u64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_size_t
+        f32 = ctypes.c_float
         sig = {
             "sg_version": (i32, []),
             "sg_last_error": (i32, [ctypes.c_char_p, sz]),
@@ -140,6 +147,15 @@ def load(build_if_missing: bool = True):
             "sg_match": (i32, [vp, i64, vp, vp, i64, vp, vp, i64, vp, vp, vp]),
             "sg_overlap": (i32, [vp, vp, i32, vp, i64, vp, vp]),
             "sg_greedy_order": (i32, [vp, i32, i32, vp]),
+            "sg_embed_fwd": (i32, [vp, i32, i64, i32, i64, vp, i64, vp, f32, vp, i32, i64, vp]),
+            "sg_embed_bwd_workspace": (sz, [i64, i64, i32, i32]),
+            "sg_embed_bwd": (i32, [vp, i64, vp, i64, vp, i32, i32, i64, f32, i32, vp, vp, vp, i32, i64, vp, sz, vp]),
+            "sg_xent_workspace": (sz, [i32, i32]),
+            "sg_xent": (i32, [vp, i32, i32, vp, i32, i64, vp, i32, f32, vp, vp, vp, i64, vp, sz, vp]),
+            "sg_orthogonalise_workspace": (sz, [i32, i32, i32]),
+            "sg_orthogonalise": (i32, [vp, i32, i32, i32, i32, i64, i32, vp, f32, f32, vp, i64, vp, sz, vp]),
+            "sg_muon_step": (i32, [vp, i32, vp, vp, i32, i32, i32, f32, f32, i32, f32, f32, i32, vp, f32, vp, vp, vp,
+                                   sz, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -641,3 +657,160 @@ def sg_aggregate_bwd_t(tptr: torch.Tensor, tdst: torch.Tensor, tw: torch.Tensor,
     _check(load().sg_aggregate_bwd_t(tptr.data_ptr(), tdst.data_ptr(), tw.data_ptr(), int(n_src_cap), int(n_dst_cap),
                                      _ptr(dims), gdst.data_ptr(), _dtype_code(gdst), int(dim), gsrc.data_ptr(),
                                      _dtype_code(gsrc), _stream(stream)))
+
+
+# ---------------------------------------------------- training operators
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise SgError(SG_ERR_INVALID_ARG, what)
+
+
+def _matrix(name: str, t: torch.Tensor, rows: int, cols: int, dev) -> int:
+    """Checks a 2-D float32 / bfloat16 device matrix of at least rows x cols
+    with unit column stride; returns its row stride in elements."""
+    _need(isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype in (torch.float32, torch.bfloat16),
+          "%s must be a 2-D float32 or bfloat16 tensor" % name)
+    _need(t.device == dev, "%s must be on %s" % (name, dev))
+    _need(t.shape[0] >= rows and t.shape[1] == cols, "%s must have %d columns and at least %d rows" % (name, cols, rows))
+    _need(cols <= 1 or t.stride(1) == 1, "%s must have unit column stride" % name)
+    ld = t.stride(0) if t.shape[0] > 1 else max(cols, t.stride(0))
+    _need(ld >= cols, "%s: rows overlap" % name)
+    return ld
+
+
+def _vector(name: str, t: Optional[torch.Tensor], n: int, dtype, dev) -> None:
+    _need(isinstance(t, torch.Tensor) and t.dtype == dtype and t.is_contiguous() and t.numel() >= n
+          and t.device == dev, "%s must be a contiguous %s tensor of %d entries on %s" % (name, dtype, n, dev))
+
+
+def sg_embed_fwd(table: torch.Tensor, ids: torch.Tensor, n_cap: int, d_n: Optional[torch.Tensor], scale: float,
+                 out: torch.Tensor, stream=None) -> None:
+    """out[i] = scale * table[ids[i]] for the first n rows (a zero row for id
+    -1); see sg.h."""
+    dev = table.device
+    _need(table.is_cuda and table.dim() == 2, "sg_embed_fwd: table must be a 2-D device tensor")
+    n_rows, dim = table.shape
+    ld_t = _matrix("sg_embed_fwd: table", table, n_rows, dim, dev)
+    ld_o = _matrix("sg_embed_fwd: out", out, n_cap, dim, dev)
+    _vector("sg_embed_fwd: ids", ids, n_cap, torch.int32, dev)
+    if d_n is not None:
+        _vector("sg_embed_fwd: d_n", d_n, 1, torch.int32, dev)
+    _check(load().sg_embed_fwd(table.data_ptr(), _dtype_code(table), n_rows, dim, ld_t, ids.data_ptr(), int(n_cap),
+                               _ptr(d_n), float(scale), out.data_ptr(), _dtype_code(out), ld_o, _stream(stream)))
+
+
+def sg_embed_bwd_workspace(n_cap: int, n_rows: int, dim: int, mode: int) -> int:
+    return int(load().sg_embed_bwd_workspace(int(n_cap), int(n_rows), int(dim), int(mode)))
+
+
+def sg_embed_bwd(ids: torch.Tensor, n_cap: int, d_n: Optional[torch.Tensor], n_rows: int, g: torch.Tensor, scale: float,
+                 grad: torch.Tensor, mode: int, workspace: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                 n_out: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradient of sg_embed_fwd with respect to the table (see sg.h): mode
+    SG_GRAD_ROWS fills rows (distinct ids), n_out (their number) and the first
+    rows of grad; SG_GRAD_DENSE writes the whole table's gradient; SG_GRAD_ADD
+    adds into grad's rows."""
+    dev = g.device
+    _need(g.is_cuda and g.dim() == 2, "sg_embed_bwd: g must be a 2-D device tensor")
+    dim = g.shape[1]
+    ld_g = _matrix("sg_embed_bwd: g", g, n_cap, dim, dev)
+    ld_o = _matrix("sg_embed_bwd: grad", grad, n_cap if mode == SG_GRAD_ROWS else n_rows, dim, dev)
+    _vector("sg_embed_bwd: ids", ids, n_cap, torch.int32, dev)
+    if d_n is not None:
+        _vector("sg_embed_bwd: d_n", d_n, 1, torch.int32, dev)
+    if mode == SG_GRAD_ROWS:
+        _vector("sg_embed_bwd: rows", rows, n_cap, torch.int32, dev)
+        _vector("sg_embed_bwd: n_out", n_out, 1, torch.int32, dev)
+    _check(load().sg_embed_bwd(ids.data_ptr(), int(n_cap), _ptr(d_n), int(n_rows), g.data_ptr(), _dtype_code(g), dim,
+                               ld_g, float(scale), int(mode), _ptr(rows), _ptr(n_out), grad.data_ptr(),
+                               _dtype_code(grad), ld_o, workspace.data_ptr(), workspace.numel(), _stream(stream)))
+
+
+def sg_xent_workspace(n_cap: int, n_classes: int) -> int:
+    return int(load().sg_xent_workspace(int(n_cap), int(n_classes)))
+
+
+def sg_xent(logits: torch.Tensor, labels: torch.Tensor, n_cap: int, d_n: Optional[torch.Tensor], loss: torch.Tensor,
+            total: Optional[torch.Tensor], grad: Optional[torch.Tensor], workspace: torch.Tensor, mean: bool = True,
+            grad_scale: float = 1.0, stream=None) -> None:
+    """Softmax cross-entropy per row, its sum or mean (total[0], with the
+    number of labelled rows in total[1]) and the gradient; see sg.h."""
+    dev = logits.device
+    _need(logits.is_cuda and logits.dim() == 2, "sg_xent: logits must be a 2-D device tensor")
+    c = logits.shape[1]
+    ld = _matrix("sg_xent: logits", logits, n_cap, c, dev)
+    ld_g = 0
+    if grad is not None:
+        ld_g = _matrix("sg_xent: grad", grad, n_cap, c, dev)
+        _need(grad.dtype == logits.dtype, "sg_xent: grad must have the logits' dtype")
+    _vector("sg_xent: labels", labels, n_cap, torch.int32, dev)
+    _vector("sg_xent: loss", loss, n_cap, torch.float32, dev)
+    if total is not None:
+        _vector("sg_xent: total", total, 2, torch.float32, dev)
+    if d_n is not None:
+        _vector("sg_xent: d_n", d_n, 1, torch.int32, dev)
+    _check(load().sg_xent(logits.data_ptr(), _dtype_code(logits), int(n_cap), _ptr(d_n), c, ld, labels.data_ptr(),
+                          1 if mean else 0, float(grad_scale), loss.data_ptr(), _ptr(total), _ptr(grad), ld_g,
+                          workspace.data_ptr(), workspace.numel(), _stream(stream)))
+
+
+def sg_orthogonalise_workspace(count: int, rows: int, cols: int) -> int:
+    return int(load().sg_orthogonalise_workspace(int(count), int(rows), int(cols)))
+
+
+def _coef(steps: int, coef) -> Optional[np.ndarray]:
+    """The steps' (a, b, c) as a host array, or None for the default."""
+    if coef is None:
+        return None
+    c = np.ascontiguousarray(coef, dtype=np.float32).reshape(-1)
+    _need(c.size == 3 * steps, "coef must hold (a, b, c) of each of the %d steps" % steps)
+    return c
+
+
+def _stack(name: str, t: torch.Tensor) -> torch.Tensor:
+    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() in (2, 3), "%s must be a 2-D or 3-D device tensor" % name)
+    return t if t.dim() == 3 else t[None]
+
+
+def sg_orthogonalise(g: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor, steps: int = 5, scale: float = 1.0,
+                     eps: float = 1e-7, coef=None, stream=None) -> None:
+    """out = scale * the Newton-Schulz orthogonalisation of each matrix of g
+    ([rows, cols] or [count, rows, cols]); coef: (a, b, c) per step; see
+    sg.h."""
+    a, b = _stack("sg_orthogonalise: g", g), _stack("sg_orthogonalise: out", out)
+    k, r, c = a.shape
+    _need(a.shape == b.shape and a.dtype == b.dtype and a.device == b.device,
+          "sg_orthogonalise: out must have g's shape, dtype and device")
+    ld = []
+    for name, t in (("g", a), ("out", b)):
+        stride = t.stride(1) if r > 1 else max(c, 1)
+        _need(c <= 1 or t.stride(2) == 1, "sg_orthogonalise: %s must have unit column stride" % name)
+        _need(k <= 1 or (t.stride(0) == r * t.stride(1) if r > 1 else t.stride(0) == stride),
+              "sg_orthogonalise: %s: matrices must follow one another" % name)
+        ld.append(stride)
+    cf = _coef(steps, coef)
+    _check(load().sg_orthogonalise(a.data_ptr(), _dtype_code(a), k, r, c, ld[0], int(steps), _ptr(cf), float(eps),
+                                   float(scale), b.data_ptr(), ld[1], workspace.data_ptr(), workspace.numel(),
+                                   _stream(stream)))
+
+
+def sg_muon_step(w: torch.Tensor, g: torch.Tensor, m: torch.Tensor, w_out: torch.Tensor, m_out: torch.Tensor,
+                 workspace: torch.Tensor, lr: float, momentum: float = 0.95, nesterov: bool = True,
+                 weight_decay: float = 0.0, scale: float = 1.0, steps: int = 5, eps: float = 1e-7, coef=None,
+                 stream=None) -> None:
+    """One Muon step of the weights w ([rows, cols] or [count, rows, cols],
+    float32 or bfloat16) from their float32 gradient g and momentum m, into
+    w_out and m_out (which may be w and m); see sg.h."""
+    a = _stack("sg_muon_step: w", w)
+    _dtype_code(w)
+    for name, t in (("w", w), ("g", g), ("m", m), ("w_out", w_out), ("m_out", m_out)):
+        _need(isinstance(t, torch.Tensor) and t.shape == w.shape and t.is_contiguous() and t.device == w.device,
+              "sg_muon_step: %s must be a contiguous tensor of w's shape on its device" % name)
+    _need(g.dtype == m.dtype == m_out.dtype == torch.float32 and w_out.dtype == w.dtype,
+          "sg_muon_step: g, m and m_out must be float32, w_out of w's dtype")
+    k, r, c = a.shape
+    cf = _coef(steps, coef)
+    _check(load().sg_muon_step(w.data_ptr(), _dtype_code(w), g.data_ptr(), m.data_ptr(), k, r, c, float(lr),
+                               float(momentum), 1 if nesterov else 0, float(weight_decay), float(scale), int(steps),
+                               _ptr(cf), float(eps), w_out.data_ptr(), m_out.data_ptr(), workspace.data_ptr(),
+                               workspace.numel(), _stream(stream)))

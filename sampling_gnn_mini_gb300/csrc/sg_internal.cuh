@@ -51,6 +51,9 @@ unsigned fetch_err_update(cudaStream_t);
 unsigned fetch_err_recode(cudaStream_t);
 unsigned fetch_err_dyncache(cudaStream_t);
 unsigned fetch_err_match(cudaStream_t);
+unsigned fetch_err_embed(cudaStream_t);
+unsigned fetch_err_loss(cudaStream_t);
+unsigned fetch_err_muon(cudaStream_t);
 
 // ------------------------------------------------------------- ranking
 // Nodes by descending 32-bit score, ties by ascending ID, into order[n]
