@@ -5,10 +5,23 @@
 // sg_muon_step, and the weights updated from the result.
 //
 // Here m = min(rows, cols), n = max(rows, cols); X is held as m rows of n.
+//
+// Number format.  The iteration multiplies small singular values by up to
+// a = 3.44 a step (485 in five), and an operand's rounding error with them, so
+// one 16-bit operand a product (2^-9 in bf16, 2^-12 in fp16) would leave
+// errors of a percent and more.  Every operand is held as two fp16 terms,
+// hi + lo, of 256 times its value: the iterates are bounded (singular values
+// up to about 1.2), so 256 x stays inside fp16's range and lo above its
+// subnormals, and the pair carries 22 bits.  A product is three tensor-core
+// products, hi hi + hi lo + lo hi, with fp32 accumulation in tensor memory.
+// Folding a I into B makes X <- B X one product with nothing to add.
+#include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <string.h>
 
 #include "sg_internal.cuh"
+#include "sg_tc.cuh"
 
 SGI_ERROR_WORD(muon)
 
@@ -17,15 +30,34 @@ using namespace sgi;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTile = 32;
 constexpr int kNormBlocks = 64;  // partial sums of squares of a matrix
+constexpr float kScale = 256.f;  // of every fp16 pair
+constexpr int kTile = 128;       // rows of an output tile (and columns of a symmetric one)
+constexpr int kBK = 64;          // K elements of a stage: one 128-byte swizzle row
+constexpr int kOperand = kTile * kBK * 2;  // bytes of one operand tile: 16 KB
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// What enters: a matrix of type T (momentum NULL), or gradient and momentum.
+// v as hi + lo, both fp16 (round to nearest; v is kScale times a value)
+__device__ __forceinline__ void split(float v, __half& hi, __half& lo) {
+    hi = __float2half_rn(v);
+    lo = __float2half_rn(v - __half2float(hi));
+}
+__device__ __forceinline__ uint32_t pack(__half a, __half b) {
+    const __half2 t = __halves2half2(a, b);
+    return *reinterpret_cast<const uint32_t*>(&t);
+}
+
+// A matrix held as two fp16 planes of `ld` columns (a multiple of 8).
+struct Planes {
+    __half* hi;
+    __half* lo;
+};
+
+// What enters: a matrix of type T (mom_out NULL), or gradient and momentum.
 template <typename T>
 struct Source {
     const T* g;
@@ -36,9 +68,10 @@ struct Source {
     int32_t nesterov;
 };
 
-// U into X (transposed when tall) and partial sums of its squares.
+// ------------------------------------------------------------ norm and split
+// New momentum, and partial sums of the squares of U.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_ns_load(Source<T> src, int32_t rows, int32_t cols, float* __restrict__ X,
+__global__ void __launch_bounds__(kThreads) k_ns_norm(Source<T> src, int32_t rows, int32_t cols,
                                                       double* __restrict__ part) {
     pdl_start();
     __shared__ double sh[kThreads / 32];
@@ -47,13 +80,12 @@ __global__ void __launch_bounds__(kThreads) k_ns_load(Source<T> src, int32_t row
     for (int64_t t = blockIdx.x * (int64_t)kThreads + threadIdx.x; t < total; t += (int64_t)gridDim.x * kThreads) {
         const int64_t r = t / cols, c = t - r * cols;
         float u = to_f(src.g[(q * rows + r) * src.ld + c]);
-        if (src.mom) {
+        if (src.mom_out) {
             const float m = src.mu * src.mom[q * total + t] + u;
             src.mom_out[q * total + t] = m;
             u = src.nesterov ? u + src.mu * m : m;
         }
-        X[q * total + (rows > cols ? c * rows + r : t)] = u;
-        sum += (double)(u * u);
+        sum += (double)u * (double)u;
     }
     sum = warp_sum(sum);
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = sum;
@@ -64,89 +96,526 @@ __global__ void __launch_bounds__(kThreads) k_ns_load(Source<T> src, int32_t row
     }
 }
 
-__global__ void __launch_bounds__(kThreads) k_ns_scale(float* __restrict__ X, int64_t total, const double* __restrict__ part,
-                                                       int32_t parts, float eps) {
-    pdl_start();
-    const int64_t q = blockIdx.y;
-    double s = 0.0;
-    for (int i = 0; i < parts; ++i) s += part[q * parts + i];
-    const float inv = 1.f / ((float)sqrt(s) + eps);
-    for (int64_t t = blockIdx.x * (int64_t)kThreads + threadIdx.x; t < total; t += (int64_t)gridDim.x * kThreads)
-        X[q * total + t] *= inv;
-}
-
-// D[i, j] = alpha * sum_k A[i, k] B(k, j) + beta * C[i, j] + gamma (i == j)
-// with B(k, j) = B[j, k] (TB) or B[k, j]; row-major, one 32 x 32 tile a block.
-template <bool TB>
-__global__ void __launch_bounds__(kThreads) k_ns_mm(const float* __restrict__ A, const float* __restrict__ B,
-                                                    const float* __restrict__ C, float* __restrict__ D, int32_t M,
-                                                    int32_t N, int32_t K, float alpha, float beta, float gamma) {
-    pdl_start();
-    __shared__ float sa[kTile][kTile + 1], sb[kTile][kTile + 1];
-    const int64_t q = blockIdx.z;
-    A += q * (int64_t)M * K;
-    B += q * (int64_t)N * K;
-    D += q * (int64_t)M * N;
-    if (C) C += q * (int64_t)M * N;
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int32_t i0 = (int32_t)blockIdx.y * kTile, j0 = (int32_t)blockIdx.x * kTile;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int32_t k0 = 0; k0 < K; k0 += kTile) {
-        for (int r = ty; r < kTile; r += 8) {
-            sa[r][tx] = i0 + r < M && k0 + tx < K ? A[(int64_t)(i0 + r) * K + k0 + tx] : 0.f;
-            if (TB) sb[r][tx] = j0 + r < N && k0 + tx < K ? B[(int64_t)(j0 + r) * K + k0 + tx] : 0.f;
-            else sb[tx][r] = k0 + r < K && j0 + tx < N ? B[(int64_t)(k0 + r) * N + j0 + tx] : 0.f;
-        }
-        __syncthreads();
-        for (int k = 0; k < kTile; ++k)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[r] += sa[ty + 8 * r][k] * sb[tx][k];
-        __syncthreads();
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int32_t i = i0 + ty + 8 * r, j = j0 + tx;
-        if (i < M && j < N)
-            D[(int64_t)i * N + j] = alpha * acc[r] + (C ? beta * C[(int64_t)i * N + j] : 0.f) + (i == j ? gamma : 0.f);
-    }
-}
-
-// out = keep * w + step * X, transposed back (w NULL: out = step * X)
+// X = U / (||U|| + eps) as planes, transposed when rows > cols; one 32 x 32
+// tile of U a block step.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_ns_store(const float* __restrict__ X, int32_t rows, int32_t cols,
-                                                       const T* w, float keep, float step, T* out, int64_t ld_out) {
+__global__ void __launch_bounds__(kThreads) k_ns_split(Source<T> src, int32_t rows, int32_t cols,
+                                                       const double* __restrict__ part, float eps, Planes X,
+                                                       int64_t ldx) {
+    pdl_start();
+    __shared__ float tile[32][33];
+    const int64_t q = blockIdx.z, total = (int64_t)rows * cols;
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    double s = part[q * kNormBlocks + tx] + part[q * kNormBlocks + 32 + tx];
+    s = warp_sum(s);
+    const float mul = kScale / ((float)sqrt(s) + eps);
+    const bool tall = rows > cols;
+    const int32_t m = tall ? cols : rows, n = tall ? rows : cols;
+    const int32_t r0 = (int32_t)blockIdx.y * 32, c0 = (int32_t)blockIdx.x * 32;
+    for (int i = ty; i < 32; i += 8) {
+        const int32_t r = r0 + i, c = c0 + tx;
+        float u = 0.f;
+        if (r < rows && c < cols) {
+            u = to_f(src.g[(q * rows + r) * src.ld + c]);
+            if (src.mom_out) {
+                const float mo = src.mom_out[q * total + (int64_t)r * cols + c];
+                u = src.nesterov ? u + src.mu * mo : mo;
+            }
+        }
+        tile[i][tx] = u * mul;
+    }
+    __syncthreads();
+    const int32_t x0 = tall ? c0 : r0, y0 = tall ? r0 : c0;  // the tile's place in X
+    for (int i = ty; i < 32; i += 8) {
+        const int32_t r = x0 + i, c = y0 + tx;
+        if (r >= m || c >= n) continue;
+        __half hi, lo;
+        split(tall ? tile[tx][i] : tile[i][tx], hi, lo);
+        X.hi[(q * m + r) * ldx + c] = hi;
+        X.lo[(q * m + r) * ldx + c] = lo;
+    }
+}
+
+// ----------------------------------------------------------------- products
+// Instruction descriptor of kind::f16 with fp16 operands (formats 0), fp32
+// accumulation (bits 4-5 = 1), B MN-major (bit 16) or not, N >> 3 in bits
+// 17-22, M >> 4 (M = 128) in bits 24-28.
+__host__ __device__ constexpr uint32_t desc_f16(bool b_mn, int n) {
+    return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+}
+
+struct PairMaps {
+    CUtensorMap hi, lo;
+};
+
+// Ring of kStages stages of BYTES; a full and an empty barrier a stage.
+template <int STAGES>
+struct Ring {
+    uint64_t full[STAGES], empty[STAGES], done;
+};
+
+template <int STAGES>
+__device__ __forceinline__ void ring_init(Ring<STAGES>& r) {
+    for (int s = 0; s < STAGES; ++s) {
+        mbar_init(&r.full[s], 1);
+        mbar_init(&r.empty[s], 1);
+    }
+    mbar_init(&r.done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+}
+
+template <int COLS>
+__device__ __forceinline__ void tmem_alloc(uint32_t* base) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_addr(base)), "r"(COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+}
+template <int COLS>
+__device__ __forceinline__ void tmem_free(uint32_t base) {
+    tmem_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(base), "r"(COLS) : "memory");
+}
+
+// Every load issued into the ring has landed (normally the MMA issuer has
+// waited for them already).
+template <int STAGES>
+__device__ __forceinline__ void ring_drain(Ring<STAGES>& r, int issued) {
+    for (int k = issued > STAGES ? issued - STAGES : 0; k < issued; ++k)
+        if (!mbar_wait(&r.full[k % STAGES], (uint32_t)(k / STAGES) & 1u)) dev_err(ERR_TIMEOUT);
+}
+
+// Symmetric product: a 128 x 128 tile (i0, j0), j0 >= i0, of
+//   GRAM    A = X X^T                      (K = n)
+//   SQUARE  B = a I + b A + c A A          (K = m; A is symmetric, so A A = A A^T)
+// both operands K-major rows of one matrix.  The tiles below the diagonal are
+// written as mirror images.  The K tiles are split over the S CTAs of a
+// cluster: each leaves its partial sum in shared memory, and CTA r adds
+// columns [r, r + 1) 128 / S of all parts in rank order.
+constexpr int kSymStages = 3;
+constexpr int kSymStage = 4 * kOperand;  // hi and lo of both operands: 64 KB
+constexpr int kSymSmem = kSymStages * kSymStage + 1024;
+enum { GRAM = 0, SQUARE = 1 };
+
+template <int S, int KIND>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_ns_sym(const __grid_constant__ PairMaps maps, int32_t m, int32_t K, float a, float b, float c, Planes in, Planes out,
+             int64_t ld) {
+    extern __shared__ uint8_t dsm[];
+    __shared__ __align__(8) Ring<kSymStages> ring;
+    __shared__ uint32_t tmem_base;
+    pdl_start();
+    const int warp = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31);
+    const int rank = (int)(blockIdx.x % S);
+    const int32_t q = (int32_t)blockIdx.y;
+    // tile t of the upper triangle, row by row
+    const int32_t nt = (m + kTile - 1) / kTile;
+    int32_t t = (int32_t)(blockIdx.x / S), ti = 0;
+    while (t >= nt - ti) {
+        t -= nt - ti;
+        ++ti;
+    }
+    const int32_t i0 = ti * kTile, j0 = (ti + t) * kTile;
+    const bool diag = t == 0;
+    uint8_t* tiles = dsm + ((1024 - (smem_addr(dsm) & 1023)) & 1023);
+    if (threadIdx.x == 0) ring_init(ring);
+    if (warp == 1) tmem_alloc<kTile>(&tmem_base);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = tmem_base;
+    const int n_kt = (K + kBK - 1) / kBK, per = (n_kt + S - 1) / S;
+    const int kt0 = min(n_kt, rank * per), n_k = min(n_kt, kt0 + per) - kt0;
+    if (warp == 0 && lane == 0) {
+        int issued = 0;
+        for (int i = 0; i < n_k; ++i) {
+            const int s = i % kSymStages;
+            if (i >= kSymStages && !mbar_wait(&ring.empty[s], (uint32_t)((i / kSymStages) - 1) & 1u)) {
+                dev_err(ERR_TIMEOUT);
+                break;
+            }
+            uint8_t* p = tiles + s * kSymStage;
+            const int32_t x = (kt0 + i) * kBK;
+            mbar_expect_tx(&ring.full[s], diag ? 2 * kOperand : 4 * kOperand);
+            tma_load_3d(p, &maps.hi, x, i0, q, &ring.full[s]);
+            tma_load_3d(p + kOperand, &maps.lo, x, i0, q, &ring.full[s]);
+            if (!diag) {
+                tma_load_3d(p + 2 * kOperand, &maps.hi, x, j0, q, &ring.full[s]);
+                tma_load_3d(p + 3 * kOperand, &maps.lo, x, j0, q, &ring.full[s]);
+            }
+            ++issued;
+        }
+        ring_drain(ring, issued);
+    } else if (warp == 1 && lane == 0) {
+        constexpr uint32_t idesc = desc_f16(false, kTile);
+        for (int i = 0; i < n_k; ++i) {
+            const int s = i % kSymStages;
+            if (!mbar_wait(&ring.full[s], (uint32_t)(i / kSymStages) & 1u)) {
+                dev_err(ERR_TIMEOUT);
+                break;
+            }
+            tmem_fence_after();
+            const uint32_t ah = smem_addr(tiles + s * kSymStage), al = ah + kOperand;
+            const uint32_t bh = diag ? ah : ah + 2 * kOperand, bl = bh + kOperand;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                const uint32_t o = kk * 32;
+                mma_issue(tmem, smem_desc_sw128(ah + o), smem_desc_sw128(bh + o), idesc, (uint32_t)((i | kk) != 0), false);
+                mma_issue(tmem, smem_desc_sw128(ah + o), smem_desc_sw128(bl + o), idesc, 1u, false);
+                mma_issue(tmem, smem_desc_sw128(al + o), smem_desc_sw128(bh + o), idesc, 1u, false);
+            }
+            mma_commit(&ring.empty[s]);
+        }
+        mma_commit(&ring.done);
+    }
+    __syncwarp();
+    if (!mbar_wait(&ring.done, 0) && lane == 0) dev_err(ERR_TIMEOUT);
+    tmem_fence_after();
+    __syncthreads();  // the producer has drained: the ring is free
+    // partial sums to shared memory as [column][row]: warps w and w + 4 read
+    // tensor-memory lanes 32 (w % 4).. of columns [0, 64) and [64, 128)
+    float* dump = reinterpret_cast<float*>(tiles);
+    {
+        const int row = (warp & 3) * 32 + lane;
+#pragma unroll 1
+        for (int c0 = (warp >> 2) * 64; c0 < (warp >> 2) * 64 + 64; c0 += 32) {
+            float v[32];
+            tmem_load_32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)c0, v);
+#pragma unroll
+            for (int u = 0; u < 32; ++u) dump[(c0 + u) * kTile + row] = n_k ? v[u] : 0.f;
+        }
+    }
+    tmem_fence_before();
+    if constexpr (S > 1) cluster_sync();
+    else __syncthreads();
+    if (warp == 1) tmem_free<kTile>(tmem);
+    constexpr int kW = kTile / S;  // columns of this CTA
+    const int row = (int)(threadIdx.x & 127);
+    const int32_t i = i0 + row;
+    const uint32_t base = smem_addr(dump);
+#pragma unroll 1
+    for (int c0 = (int)(threadIdx.x >> 7) * 8; c0 < kW; c0 += 16) {
+        const int col = rank * kW + c0;
+        float v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = 0.f;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const uint32_t from = S > 1 ? map_rank(base, (uint32_t)s) : base;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const uint32_t at = (uint32_t)(((col + u) * kTile + row) * 4);
+                v[u] += S > 1 ? ld_cluster(from + at) : dump[(col + u) * kTile + row];
+            }
+        }
+        const int32_t j = j0 + col;
+        if (i < m && j < m) {
+            const int64_t at = ((int64_t)q * m + i) * ld + j;
+            if (KIND == GRAM) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) v[u] *= 1.f / kScale;
+            } else {
+                const uint4 h4 = *reinterpret_cast<const uint4*>(in.hi + at), l4 = *reinterpret_cast<const uint4*>(in.lo + at);
+                const __half2* h2 = reinterpret_cast<const __half2*>(&h4);
+                const __half2* l2 = reinterpret_cast<const __half2*>(&l4);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const float2 h = __half22float2(h2[u >> 1]), l = __half22float2(l2[u >> 1]);
+                    const float A = u & 1 ? h.y + l.y : h.x + l.x;
+                    v[u] = c * (v[u] * (1.f / kScale)) + b * A + (i == j + u ? a * kScale : 0.f);
+                }
+            }
+            __half hi[8], lo[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) split(v[u], hi[u], lo[u]);
+            *reinterpret_cast<uint4*>(out.hi + at) =
+                make_uint4(pack(hi[0], hi[1]), pack(hi[2], hi[3]), pack(hi[4], hi[5]), pack(hi[6], hi[7]));
+            *reinterpret_cast<uint4*>(out.lo + at) =
+                make_uint4(pack(lo[0], lo[1]), pack(lo[2], lo[3]), pack(lo[4], lo[5]), pack(lo[6], lo[7]));
+            if (!diag) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    if (j + u >= m) continue;
+                    const int64_t mir = ((int64_t)q * m + j + u) * ld + i;
+                    out.hi[mir] = hi[u];
+                    out.lo[mir] = lo[u];
+                }
+            }
+        }
+    }
+    if constexpr (S > 1) cluster_sync();  // no CTA leaves while another reads its part
+}
+
+// X' = B X: a 128 x BN tile.  B's tile is K-major (B is m x m), X's MN-major
+// (its rows are K, n contiguous).
+// EPI 0: X' as planes; 1: out = keep w + step X', transposed back when tall.
+struct FinalArgs {
+    const void* w;
+    void* out;
+    float keep, step;
+    int64_t ld_out;
+    int32_t tall;
+};
+
+template <int BN>
+constexpr int kApplyStage = 2 * kOperand + 2 * BN * kBK * 2;
+template <int BN>
+constexpr int kApplyStages = BN == 256 ? 2 : 3;
+template <int BN>
+constexpr int kApplySmem = kApplyStages<BN> * kApplyStage<BN> + 1024;
+
+struct ApplyMaps {
+    CUtensorMap bhi, blo, xhi, xlo;
+};
+
+template <int BN, typename TW, bool FINAL>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_ns_apply(const __grid_constant__ ApplyMaps maps, int32_t m, int32_t n, Planes out, int64_t ldx, FinalArgs fin) {
+    constexpr int kStages = kApplyStages<BN>, kStage = kApplyStage<BN>, kBox = kBK * 128;  // 64 K rows of 64 columns
+    extern __shared__ uint8_t dsm[];
+    __shared__ __align__(8) Ring<kStages> ring;
+    __shared__ uint32_t tmem_base;
+    pdl_start();
+    const int warp = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31);
+    const int32_t q = (int32_t)blockIdx.z, i0 = (int32_t)blockIdx.y * kTile, j0 = (int32_t)blockIdx.x * BN;
+    uint8_t* tiles = dsm + ((1024 - (smem_addr(dsm) & 1023)) & 1023);
+    if (threadIdx.x == 0) ring_init(ring);
+    if (warp == 1) tmem_alloc<BN>(&tmem_base);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = tmem_base;
+    const int n_k = (m + kBK - 1) / kBK;
+    if (warp == 0 && lane == 0) {
+        int issued = 0;
+        for (int i = 0; i < n_k; ++i) {
+            const int s = i % kStages;
+            if (i >= kStages && !mbar_wait(&ring.empty[s], (uint32_t)((i / kStages) - 1) & 1u)) {
+                dev_err(ERR_TIMEOUT);
+                break;
+            }
+            uint8_t* p = tiles + s * kStage;
+            mbar_expect_tx(&ring.full[s], kStage);
+            tma_load_3d(p, &maps.bhi, i * kBK, i0, q, &ring.full[s]);
+            tma_load_3d(p + kOperand, &maps.blo, i * kBK, i0, q, &ring.full[s]);
+#pragma unroll
+            for (int h = 0; h < BN / 64; ++h) {
+                tma_load_3d(p + 2 * kOperand + h * kBox, &maps.xhi, j0 + h * 64, i * kBK, q, &ring.full[s]);
+                tma_load_3d(p + 2 * kOperand + (BN / 64 + h) * kBox, &maps.xlo, j0 + h * 64, i * kBK, q, &ring.full[s]);
+            }
+            ++issued;
+        }
+        ring_drain(ring, issued);
+    } else if (warp == 1 && lane == 0) {
+        constexpr uint32_t idesc = desc_f16(true, BN);
+        for (int i = 0; i < n_k; ++i) {
+            const int s = i % kStages;
+            if (!mbar_wait(&ring.full[s], (uint32_t)(i / kStages) & 1u)) {
+                dev_err(ERR_TIMEOUT);
+                break;
+            }
+            tmem_fence_after();
+            const uint32_t bh = smem_addr(tiles + s * kStage), bl = bh + kOperand;
+            const uint32_t xh = bh + 2 * kOperand, xl = xh + (BN / 64) * kBox;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                const uint32_t o = kk * 32, ox = kk * 16 * 128;  // 16 K elements of a row; 16 K rows
+                mma_issue(tmem, smem_desc_sw128(bh + o), smem_desc_mn_sw128(xh + ox, kBox), idesc,
+                          (uint32_t)((i | kk) != 0), false);
+                mma_issue(tmem, smem_desc_sw128(bh + o), smem_desc_mn_sw128(xl + ox, kBox), idesc, 1u, false);
+                mma_issue(tmem, smem_desc_sw128(bl + o), smem_desc_mn_sw128(xh + ox, kBox), idesc, 1u, false);
+            }
+            mma_commit(&ring.empty[s]);
+        }
+        mma_commit(&ring.done);
+    }
+    __syncwarp();
+    if (!mbar_wait(&ring.done, 0) && lane == 0) dev_err(ERR_TIMEOUT);
+    tmem_fence_after();
+    __syncthreads();  // the producer has drained: the ring is free
+    // the tile through shared memory, so that rows go out whole: [row][BN + 1]
+    float* dump = reinterpret_cast<float*>(tiles);
+    constexpr int kLd = BN + 1;
+    {
+        const int row = (warp & 3) * 32 + lane;
+#pragma unroll 1
+        for (int c0 = (warp >> 2) * (BN / 2); c0 < ((warp >> 2) + 1) * (BN / 2); c0 += 32) {
+            float v[32];
+            tmem_load_32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)c0, v);
+#pragma unroll
+            for (int u = 0; u < 32; ++u) dump[row * kLd + c0 + u] = v[u];
+        }
+    }
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_free<BN>(tmem);
+    if constexpr (!FINAL) {
+#pragma unroll 2
+        for (int row = warp; row < kTile; row += kThreads / 32) {
+            const int32_t i = i0 + row;
+            if (i >= m) break;
+            const int64_t at = ((int64_t)q * m + i) * ldx + j0;
+#pragma unroll
+            for (int c = 2 * lane; c < BN; c += 64) {
+                if (j0 + c >= n) break;
+                __half h0, l0, h1, l1;
+                split(dump[row * kLd + c] * (1.f / kScale), h0, l0);
+                split(dump[row * kLd + c + 1] * (1.f / kScale), h1, l1);
+                *reinterpret_cast<uint32_t*>(out.hi + at + c) = pack(h0, h1);
+                *reinterpret_cast<uint32_t*>(out.lo + at + c) = pack(l0, l1);
+            }
+        }
+    } else {
+        const float mul = fin.step * (1.f / (kScale * kScale));
+        const TW* w = (const TW*)fin.w;
+        TW* o = (TW*)fin.out;
+        if (fin.tall) {  // element (i, j) of X is (j, i) of the matrix
+            for (int c = warp; c < BN && j0 + c < n; c += kThreads / 32) {
+                const int64_t at = ((int64_t)q * n + j0 + c) * fin.ld_out + i0;
+                for (int row = lane; row < kTile && i0 + row < m; row += 32) {
+                    const float x = mul * dump[row * kLd + c];
+                    put(o + at + row, w ? fin.keep * to_f(w[at + row]) + x : x);
+                }
+            }
+        } else {
+            for (int row = warp; row < kTile && i0 + row < m; row += kThreads / 32) {
+                const int64_t at = ((int64_t)q * m + i0 + row) * fin.ld_out + j0;
+                for (int c = lane; c < BN && j0 + c < n; c += 32) {
+                    const float x = mul * dump[row * kLd + c];
+                    put(o + at + c, w ? fin.keep * to_f(w[at + c]) + x : x);
+                }
+            }
+        }
+    }
+}
+
+// out = keep w + step X of the planes (no steps at all)
+template <typename TW>
+__global__ void __launch_bounds__(kThreads) k_ns_store(Planes X, int64_t ldx, int32_t rows, int32_t cols, FinalArgs fin) {
     pdl_start();
     const int64_t q = blockIdx.y, total = (int64_t)rows * cols;
+    const int32_t m = fin.tall ? cols : rows;
+    const TW* w = (const TW*)fin.w;
+    TW* o = (TW*)fin.out;
     for (int64_t t = blockIdx.x * (int64_t)kThreads + threadIdx.x; t < total; t += (int64_t)gridDim.x * kThreads) {
         const int64_t r = t / cols, c = t - r * cols;
-        const float x = step * X[q * total + (rows > cols ? c * rows + r : t)];
-        const int64_t o = (q * rows + r) * ld_out + c;
-        put(out + o, w ? keep * to_f(w[o]) + x : x);
+        const int64_t p = (q * m + (fin.tall ? c : r)) * ldx + (fin.tall ? r : c);
+        const float x = fin.step * ((__half2float(X.hi[p]) + __half2float(X.lo[p])) * (1.f / kScale));
+        const int64_t at = (q * rows + r) * fin.ld_out + c;
+        put(o + at, w ? fin.keep * to_f(w[at]) + x : x);
     }
 }
 
+// -------------------------------------------------------------------- host
 size_t a256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+int64_t r8(int64_t x) { return (x + 7) & ~(int64_t)7; }
+
 struct Layout {
-    size_t x0, x1, a, b, part, total;
+    int64_t m, n, ldx, lda;
+    size_t x[2][2], a[2], b[2], part, total;  // [buffer][plane]
 };
 
 Layout layout(int64_t count, int64_t rows, int64_t cols) {
-    const int64_t m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
     Layout L;
+    L.m = rows < cols ? rows : cols;
+    L.n = rows < cols ? cols : rows;
+    L.ldx = r8(L.n);
+    L.lda = r8(L.m);
     size_t o = 0;
-    const auto place = [&o](size_t bytes) {
+    const auto place = [&o](int64_t bytes) {
         const size_t at = o;
-        o += a256(bytes);
+        o += a256((size_t)bytes);
         return at;
     };
-    L.x0 = place((size_t)(count * m * n) * 4);
-    L.x1 = place((size_t)(count * m * n) * 4);
-    L.a = place((size_t)(count * m * m) * 4);
-    L.b = place((size_t)(count * m * m) * 4);
-    L.part = place((size_t)(count * kNormBlocks) * 8);
+    for (int p = 0; p < 2; ++p) {
+        L.x[0][p] = place(count * L.m * L.ldx * 2);
+        L.x[1][p] = place(count * L.m * L.ldx * 2);
+        L.a[p] = place(count * L.m * L.lda * 2);
+        L.b[p] = place(count * L.m * L.lda * 2);
+    }
+    L.part = place(count * kNormBlocks * 8);
     L.total = o;
     return L;
+}
+
+// Map of `count` matrices [rows x cols] of fp16, ld elements a row, read in
+// boxes of 64 columns x box_rows rows; reads past a matrix give zeros.
+bool map_f16(CUtensorMap* map, const __half* base, int64_t cols, int64_t rows, int64_t count, int64_t ld, int box_rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)count};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(ld * rows) * 2};
+    const cuuint32_t box[3] = {(cuuint32_t)kBK, (cuuint32_t)box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Dependent launch of clusters of S CTAs along x.
+template <int S, typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, size_t smem, cudaStream_t s, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = S;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+// Raises a kernel's dynamic shared memory limit once.
+#define NS_SMEM(kernel, bytes)                                                                                  \
+    do {                                                                                                        \
+        static bool set_ = false;                                                                               \
+        if (!set_) {                                                                                            \
+            SG_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(bytes)));    \
+            set_ = true;                                                                                        \
+        }                                                                                                       \
+    } while (0)
+
+template <int S, int KIND>
+sg_status launch_sym(const PairMaps& maps, int64_t tiles, int32_t count, int32_t m, int32_t K, const float* coef,
+                     Planes in, Planes out, int64_t ld, cudaStream_t s) {
+    NS_SMEM((k_ns_sym<S, KIND>), kSymSmem);
+    SG_CUDA(launch_cluster<S>(k_ns_sym<S, KIND>, dim3((unsigned)(tiles * S), (unsigned)count), kSymSmem, s, maps, m, K,
+                              coef[0], coef[1], coef[2], in, out, ld));
+    return SG_OK;
+}
+
+// The upper triangle's tiles are few when m is small, and K is long: K is
+// split over up to 8 CTAs while that many more still fit the SMs and each
+// keeps two K tiles or more.
+template <int KIND>
+sg_status run_sym(const PairMaps& maps, int32_t count, int32_t m, int32_t K, const float* coef, Planes in, Planes out,
+                  int64_t ld, cudaStream_t s) {
+    const int64_t nt = cdiv(m, kTile), tiles = nt * (nt + 1) / 2, kt = cdiv(K, kBK);
+    int split = 1;
+    while (split < 8 && tiles * count * split * 2 <= num_sms() && kt >= split * 4) split *= 2;
+    switch (split) {
+        case 1: return launch_sym<1, KIND>(maps, tiles, count, m, K, coef, in, out, ld, s);
+        case 2: return launch_sym<2, KIND>(maps, tiles, count, m, K, coef, in, out, ld, s);
+        case 4: return launch_sym<4, KIND>(maps, tiles, count, m, K, coef, in, out, ld, s);
+        default: return launch_sym<8, KIND>(maps, tiles, count, m, K, coef, in, out, ld, s);
+    }
+}
+
+template <int BN, typename TW, bool FINAL>
+sg_status launch_apply(const ApplyMaps& maps, int32_t count, int32_t m, int32_t n, Planes out, int64_t ldx,
+                       const FinalArgs& fin, cudaStream_t s) {
+    constexpr int smem = kApplySmem<BN>;
+    NS_SMEM((k_ns_apply<BN, TW, FINAL>), smem);
+    SG_CUDA(launch_pdl(k_ns_apply<BN, TW, FINAL>, dim3((unsigned)cdiv(n, BN), (unsigned)cdiv(m, kTile), (unsigned)count),
+                       dim3(kThreads), smem, s, maps, m, n, out, ldx, fin));
+    return SG_OK;
 }
 
 const float kCoef[3] = {3.4445f, -4.7750f, 2.0315f};
@@ -155,34 +624,53 @@ template <typename TS, typename TW>
 sg_status run(Source<TS> src, int32_t count, int32_t rows, int32_t cols, int32_t steps, const float* coef, float eps,
               const TW* w, float keep, float step, TW* out, int64_t ld_out, char* ws, cudaStream_t s) {
     const Layout L = layout(count, rows, cols);
-    const int32_t m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
-    float* x = (float*)(ws + L.x0);
-    float* x2 = (float*)(ws + L.x1);
-    float* a = (float*)(ws + L.a);
-    float* b = (float*)(ws + L.b);
+    const int32_t m = (int32_t)L.m, n = (int32_t)L.n;
+    Planes x[2], a, b;
+    for (int i = 0; i < 2; ++i) x[i] = {(__half*)(ws + L.x[i][0]), (__half*)(ws + L.x[i][1])};
+    a = {(__half*)(ws + L.a[0]), (__half*)(ws + L.a[1])};
+    b = {(__half*)(ws + L.b[0]), (__half*)(ws + L.b[1])};
     double* part = (double*)(ws + L.part);
-    const int64_t total = (int64_t)rows * cols;
-    const int64_t eb = cdiv(total, kThreads) < 1024 ? cdiv(total, kThreads) : 1024;
-    const dim3 flat((unsigned)eb, (unsigned)count);
-    SG_CUDA(launch_pdl(k_ns_load<TS>, dim3(kNormBlocks, (unsigned)count), dim3(kThreads), 0, s, src, rows, cols, x,
-                       part));
-    SG_CUDA(launch_pdl(k_ns_scale, flat, dim3(kThreads), 0, s, x, total, (const double*)part, (int32_t)kNormBlocks,
-                       eps));
-    const unsigned tm = (unsigned)cdiv(m, kTile), tn = (unsigned)cdiv(n, kTile);
+    SG_CUDA(launch_pdl(k_ns_norm<TS>, dim3(kNormBlocks, (unsigned)count), dim3(kThreads), 0, s, src, rows, cols, part));
+    SG_CUDA(launch_pdl(k_ns_split<TS>, dim3((unsigned)cdiv(cols, 32), (unsigned)cdiv(rows, 32), (unsigned)count),
+                       dim3(kThreads), 0, s, src, rows, cols, (const double*)part, eps, x[0], L.ldx));
+    FinalArgs fin = {w, out, keep, step, ld_out, rows > cols ? 1 : 0};
+    if (steps == 0) {
+        const int64_t eb = cdiv((int64_t)rows * cols, kThreads) < 1024 ? cdiv((int64_t)rows * cols, kThreads) : 1024;
+        SG_CUDA(launch_pdl(k_ns_store<TW>, dim3((unsigned)eb, (unsigned)count), dim3(kThreads), 0, s, x[0], L.ldx, rows,
+                           cols, fin));
+        return SG_OK;
+    }
+    PairMaps mx[2], ma;   // rows as 128-row K-major operands
+    ApplyMaps mb[2];      // B K-major, X MN-major
+    memset(mx, 0, sizeof(mx));
+    memset(&ma, 0, sizeof(ma));
+    memset(mb, 0, sizeof(mb));
+    bool ok = map_f16(&ma.hi, a.hi, m, m, count, L.lda, kTile) && map_f16(&ma.lo, a.lo, m, m, count, L.lda, kTile);
+    for (int i = 0; i < 2 && ok; ++i)
+        ok = map_f16(&mx[i].hi, x[i].hi, n, m, count, L.ldx, kTile) &&
+             map_f16(&mx[i].lo, x[i].lo, n, m, count, L.ldx, kTile) &&
+             map_f16(&mb[i].bhi, b.hi, m, m, count, L.lda, kTile) &&
+             map_f16(&mb[i].blo, b.lo, m, m, count, L.lda, kTile) &&
+             map_f16(&mb[i].xhi, x[i].hi, n, m, count, L.ldx, kBK) &&
+             map_f16(&mb[i].xlo, x[i].lo, n, m, count, L.ldx, kBK);
+    if (!ok) return fail(SG_ERR_CUDA, "orthogonalise: tensor map encoding failed");
+    // 256-column tiles read each operand row half as often; 128-column ones
+    // when the wide ones would not give every SM a tile
+    const bool wide = cdiv(n, 256) * cdiv(m, kTile) * count >= num_sms() * 3 / 4;
     for (int32_t k = 0; k < steps; ++k) {
         const float* c = coef ? coef + 3 * k : kCoef;
-        SG_CUDA(launch_pdl(k_ns_mm<true>, dim3(tm, tm, (unsigned)count), dim3(kThreads), 0, s, (const float*)x,
-                           (const float*)x, (const float*)nullptr, a, m, m, n, 1.f, 0.f, 0.f));
-        SG_CUDA(launch_pdl(k_ns_mm<true>, dim3(tm, tm, (unsigned)count), dim3(kThreads), 0, s, (const float*)a,
-                           (const float*)a, (const float*)a, b, m, m, m, c[2], c[1], c[0]));
-        SG_CUDA(launch_pdl(k_ns_mm<false>, dim3(tn, tm, (unsigned)count), dim3(kThreads), 0, s, (const float*)b,
-                           (const float*)x, (const float*)nullptr, x2, m, n, m, 1.f, 0.f, 0.f));
-        float* t = x;
-        x = x2;
-        x2 = t;
+        sg_status st = run_sym<GRAM>(mx[k & 1], count, m, n, c, a, a, L.lda, s);
+        if (st == SG_OK) st = run_sym<SQUARE>(ma, count, m, m, c, a, b, L.lda, s);
+        if (st != SG_OK) return st;
+        const Planes to = x[(k & 1) ^ 1];
+        if (k + 1 < steps)
+            st = wide ? launch_apply<256, float, false>(mb[k & 1], count, m, n, to, L.ldx, fin, s)
+                      : launch_apply<128, float, false>(mb[k & 1], count, m, n, to, L.ldx, fin, s);
+        else
+            st = wide ? launch_apply<256, TW, true>(mb[k & 1], count, m, n, to, L.ldx, fin, s)
+                      : launch_apply<128, TW, true>(mb[k & 1], count, m, n, to, L.ldx, fin, s);
+        if (st != SG_OK) return st;
     }
-    SG_CUDA(launch_pdl(k_ns_store<TW>, flat, dim3(kThreads), 0, s, (const float*)x, rows, cols, w, keep, step, out,
-                       ld_out));
     return SG_OK;
 }
 
