@@ -660,43 +660,63 @@ def sg_aggregate_bwd_t(tptr: torch.Tensor, tdst: torch.Tensor, tw: torch.Tensor,
 
 
 # ---------------------------------------------------- training operators
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise SgError(SG_ERR_INVALID_ARG, what)
+# Small calls of these cost a few microseconds on the device, so the checks
+# here read each tensor property once and format messages only to raise.
+_CODES = {torch.float32: SG_F32, torch.bfloat16: SG_BF16}
 
 
-def _matrix(name: str, t: torch.Tensor, rows: int, cols: int, dev) -> int:
-    """Checks a 2-D float32 / bfloat16 device matrix of at least rows x cols
-    with unit column stride; returns its row stride in elements."""
-    _need(isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype in (torch.float32, torch.bfloat16),
-          "%s must be a 2-D float32 or bfloat16 tensor" % name)
-    _need(t.device == dev, "%s must be on %s" % (name, dev))
-    _need(t.shape[0] >= rows and t.shape[1] == cols, "%s must have %d columns and at least %d rows" % (name, cols, rows))
-    _need(cols <= 1 or t.stride(1) == 1, "%s must have unit column stride" % name)
-    ld = t.stride(0) if t.shape[0] > 1 else max(cols, t.stride(0))
-    _need(ld >= cols, "%s: rows overlap" % name)
-    return ld
+def _invalid(what: str):
+    raise SgError(SG_ERR_INVALID_ARG, what)
 
 
-def _vector(name: str, t: Optional[torch.Tensor], n: int, dtype, dev) -> None:
-    _need(isinstance(t, torch.Tensor) and t.dtype == dtype and t.is_contiguous() and t.numel() >= n
-          and t.device == dev, "%s must be a contiguous %s tensor of %d entries on %s" % (name, dtype, n, dev))
+def _matrix(name: str, t: torch.Tensor, rows: int, cols: int, dev: int):
+    """Checks a 2-D float32 / bfloat16 matrix on device dev of at least rows x
+    cols with unit column stride; returns (dtype code, row stride in
+    elements)."""
+    try:
+        code = _CODES[t.dtype]
+        r, c = t.shape
+        ld, unit = t.stride()
+    except (KeyError, ValueError, AttributeError):
+        _invalid("%s must be a 2-D float32 or bfloat16 tensor" % name)
+    if t.get_device() != dev or dev < 0:
+        _invalid("%s must be on the device of the other arguments" % name)
+    if c != cols or r < rows:
+        _invalid("%s must have %d columns and at least %d rows" % (name, cols, rows))
+    if r <= 1 and ld < c:
+        ld = c
+    if (unit != 1 and c > 1) or ld < c:
+        _invalid("%s must have unit column stride and rows that do not overlap" % name)
+    return code, ld
+
+
+def _vector(name: str, t: Optional[torch.Tensor], n: int, dtype, dev: int) -> int:
+    """Checks a contiguous vector of at least n entries on device dev;
+    returns its address."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or t.numel() < n \
+            or not t.is_contiguous():
+        _invalid("%s must be a contiguous %s device tensor of %d entries" % (name, dtype, n))
+    return t.data_ptr()
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def sg_embed_fwd(table: torch.Tensor, ids: torch.Tensor, n_cap: int, d_n: Optional[torch.Tensor], scale: float,
                  out: torch.Tensor, stream=None) -> None:
     """out[i] = scale * table[ids[i]] for the first n rows (a zero row for id
     -1); see sg.h."""
-    dev = table.device
-    _need(table.is_cuda and table.dim() == 2, "sg_embed_fwd: table must be a 2-D device tensor")
-    n_rows, dim = table.shape
-    ld_t = _matrix("sg_embed_fwd: table", table, n_rows, dim, dev)
-    ld_o = _matrix("sg_embed_fwd: out", out, n_cap, dim, dev)
-    _vector("sg_embed_fwd: ids", ids, n_cap, torch.int32, dev)
-    if d_n is not None:
-        _vector("sg_embed_fwd: d_n", d_n, 1, torch.int32, dev)
-    _check(load().sg_embed_fwd(table.data_ptr(), _dtype_code(table), n_rows, dim, ld_t, ids.data_ptr(), int(n_cap),
-                               _ptr(d_n), float(scale), out.data_ptr(), _dtype_code(out), ld_o, _stream(stream)))
+    dev = table.get_device()
+    n_rows, dim = table.shape if table.dim() == 2 else _invalid("sg_embed_fwd: table must be 2-D")
+    dt_t, ld_t = _matrix("sg_embed_fwd: table", table, 0, dim, dev)
+    dt_o, ld_o = _matrix("sg_embed_fwd: out", out, n_cap, dim, dev)
+    p_ids = _vector("sg_embed_fwd: ids", ids, n_cap, torch.int32, dev)
+    p_n = None if d_n is None else _vector("sg_embed_fwd: d_n", d_n, 1, torch.int32, dev)
+    st = (_lib or load()).sg_embed_fwd(table.data_ptr(), dt_t, n_rows, dim, ld_t, p_ids, n_cap, p_n, scale,
+                                       out.data_ptr(), dt_o, ld_o, _raw_stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def sg_embed_bwd_workspace(n_cap: int, n_rows: int, dim: int, mode: int) -> int:
@@ -710,20 +730,21 @@ def sg_embed_bwd(ids: torch.Tensor, n_cap: int, d_n: Optional[torch.Tensor], n_r
     SG_GRAD_ROWS fills rows (distinct ids), n_out (their number) and the first
     rows of grad; SG_GRAD_DENSE writes the whole table's gradient; SG_GRAD_ADD
     adds into grad's rows."""
-    dev = g.device
-    _need(g.is_cuda and g.dim() == 2, "sg_embed_bwd: g must be a 2-D device tensor")
-    dim = g.shape[1]
-    ld_g = _matrix("sg_embed_bwd: g", g, n_cap, dim, dev)
-    ld_o = _matrix("sg_embed_bwd: grad", grad, n_cap if mode == SG_GRAD_ROWS else n_rows, dim, dev)
-    _vector("sg_embed_bwd: ids", ids, n_cap, torch.int32, dev)
-    if d_n is not None:
-        _vector("sg_embed_bwd: d_n", d_n, 1, torch.int32, dev)
+    dev = g.get_device()
+    dim = g.shape[1] if g.dim() == 2 else _invalid("sg_embed_bwd: g must be 2-D")
+    dt_g, ld_g = _matrix("sg_embed_bwd: g", g, n_cap, dim, dev)
+    dt_o, ld_o = _matrix("sg_embed_bwd: grad", grad, n_cap if mode == SG_GRAD_ROWS else n_rows, dim, dev)
+    p_ids = _vector("sg_embed_bwd: ids", ids, n_cap, torch.int32, dev)
+    p_n = None if d_n is None else _vector("sg_embed_bwd: d_n", d_n, 1, torch.int32, dev)
+    p_rows, p_out = _ptr(rows), _ptr(n_out)
     if mode == SG_GRAD_ROWS:
-        _vector("sg_embed_bwd: rows", rows, n_cap, torch.int32, dev)
-        _vector("sg_embed_bwd: n_out", n_out, 1, torch.int32, dev)
-    _check(load().sg_embed_bwd(ids.data_ptr(), int(n_cap), _ptr(d_n), int(n_rows), g.data_ptr(), _dtype_code(g), dim,
-                               ld_g, float(scale), int(mode), _ptr(rows), _ptr(n_out), grad.data_ptr(),
-                               _dtype_code(grad), ld_o, workspace.data_ptr(), workspace.numel(), _stream(stream)))
+        p_rows = _vector("sg_embed_bwd: rows", rows, n_cap, torch.int32, dev)
+        p_out = _vector("sg_embed_bwd: n_out", n_out, 1, torch.int32, dev)
+    st = (_lib or load()).sg_embed_bwd(p_ids, n_cap, p_n, n_rows, g.data_ptr(), dt_g, dim, ld_g, scale, mode, p_rows,
+                                       p_out, grad.data_ptr(), dt_o, ld_o, workspace.data_ptr(), workspace.numel(),
+                                       _raw_stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def sg_xent_workspace(n_cap: int, n_classes: int) -> int:
@@ -735,23 +756,24 @@ def sg_xent(logits: torch.Tensor, labels: torch.Tensor, n_cap: int, d_n: Optiona
             grad_scale: float = 1.0, stream=None) -> None:
     """Softmax cross-entropy per row, its sum or mean (total[0], with the
     number of labelled rows in total[1]) and the gradient; see sg.h."""
-    dev = logits.device
-    _need(logits.is_cuda and logits.dim() == 2, "sg_xent: logits must be a 2-D device tensor")
-    c = logits.shape[1]
-    ld = _matrix("sg_xent: logits", logits, n_cap, c, dev)
-    ld_g = 0
+    dev = logits.get_device()
+    c = logits.shape[1] if logits.dim() == 2 else _invalid("sg_xent: logits must be 2-D")
+    dt, ld = _matrix("sg_xent: logits", logits, n_cap, c, dev)
+    p_grad, ld_g = None, 0
     if grad is not None:
-        ld_g = _matrix("sg_xent: grad", grad, n_cap, c, dev)
-        _need(grad.dtype == logits.dtype, "sg_xent: grad must have the logits' dtype")
-    _vector("sg_xent: labels", labels, n_cap, torch.int32, dev)
-    _vector("sg_xent: loss", loss, n_cap, torch.float32, dev)
-    if total is not None:
-        _vector("sg_xent: total", total, 2, torch.float32, dev)
-    if d_n is not None:
-        _vector("sg_xent: d_n", d_n, 1, torch.int32, dev)
-    _check(load().sg_xent(logits.data_ptr(), _dtype_code(logits), int(n_cap), _ptr(d_n), c, ld, labels.data_ptr(),
-                          1 if mean else 0, float(grad_scale), loss.data_ptr(), _ptr(total), _ptr(grad), ld_g,
-                          workspace.data_ptr(), workspace.numel(), _stream(stream)))
+        dt_g, ld_g = _matrix("sg_xent: grad", grad, n_cap, c, dev)
+        if dt_g != dt:
+            _invalid("sg_xent: grad must have the logits' dtype")
+        p_grad = grad.data_ptr()
+    p_y = _vector("sg_xent: labels", labels, n_cap, torch.int32, dev)
+    p_loss = _vector("sg_xent: loss", loss, n_cap, torch.float32, dev)
+    p_total = None if total is None else _vector("sg_xent: total", total, 2, torch.float32, dev)
+    p_n = None if d_n is None else _vector("sg_xent: d_n", d_n, 1, torch.int32, dev)
+    st = (_lib or load()).sg_xent(logits.data_ptr(), dt, n_cap, p_n, c, ld, p_y, 1 if mean else 0, grad_scale, p_loss,
+                                  p_total, p_grad, ld_g, workspace.data_ptr(), workspace.numel(),
+                                  _raw_stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def sg_orthogonalise_workspace(count: int, rows: int, cols: int) -> int:
@@ -763,13 +785,26 @@ def _coef(steps: int, coef) -> Optional[np.ndarray]:
     if coef is None:
         return None
     c = np.ascontiguousarray(coef, dtype=np.float32).reshape(-1)
-    _need(c.size == 3 * steps, "coef must hold (a, b, c) of each of the %d steps" % steps)
+    if c.size != 3 * steps:
+        _invalid("coef must hold (a, b, c) of each of the %d steps" % steps)
     return c
 
 
-def _stack(name: str, t: torch.Tensor) -> torch.Tensor:
-    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() in (2, 3), "%s must be a 2-D or 3-D device tensor" % name)
-    return t if t.dim() == 3 else t[None]
+def _stack(name: str, t: torch.Tensor):
+    """(dtype code, count, rows, cols, row stride) of a matrix or a stack of
+    matrices that follow one another."""
+    try:
+        code = _CODES[t.dtype]
+        shape, stride = tuple(t.shape), t.stride()
+        k, r, c = shape if len(shape) == 3 else (1,) + shape
+    except (KeyError, ValueError, AttributeError):
+        _invalid("%s must be a 2-D or 3-D float32 or bfloat16 tensor" % name)
+    if t.get_device() < 0:
+        _invalid("%s must be on a device" % name)
+    ld = stride[-2] if r > 1 else stride[0] if k > 1 else max(c, 1)
+    if (stride[-1] != 1 and c > 1) or (k > 1 and stride[0] != r * ld):
+        _invalid("%s must have unit column stride and matrices that follow one another" % name)
+    return code, k, r, c, ld
 
 
 def sg_orthogonalise(g: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor, steps: int = 5, scale: float = 1.0,
@@ -777,21 +812,16 @@ def sg_orthogonalise(g: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor
     """out = scale * the Newton-Schulz orthogonalisation of each matrix of g
     ([rows, cols] or [count, rows, cols]); coef: (a, b, c) per step; see
     sg.h."""
-    a, b = _stack("sg_orthogonalise: g", g), _stack("sg_orthogonalise: out", out)
-    k, r, c = a.shape
-    _need(a.shape == b.shape and a.dtype == b.dtype and a.device == b.device,
-          "sg_orthogonalise: out must have g's shape, dtype and device")
-    ld = []
-    for name, t in (("g", a), ("out", b)):
-        stride = t.stride(1) if r > 1 else max(c, 1)
-        _need(c <= 1 or t.stride(2) == 1, "sg_orthogonalise: %s must have unit column stride" % name)
-        _need(k <= 1 or (t.stride(0) == r * t.stride(1) if r > 1 else t.stride(0) == stride),
-              "sg_orthogonalise: %s: matrices must follow one another" % name)
-        ld.append(stride)
+    dt, k, r, c, ld = _stack("sg_orthogonalise: g", g)
+    dt_o, k_o, r_o, c_o, ld_o = _stack("sg_orthogonalise: out", out)
+    dev = g.get_device()
+    if (dt, k, r, c) != (dt_o, k_o, r_o, c_o) or out.get_device() != dev:
+        _invalid("sg_orthogonalise: out must have g's shape, dtype and device")
     cf = _coef(steps, coef)
-    _check(load().sg_orthogonalise(a.data_ptr(), _dtype_code(a), k, r, c, ld[0], int(steps), _ptr(cf), float(eps),
-                                   float(scale), b.data_ptr(), ld[1], workspace.data_ptr(), workspace.numel(),
-                                   _stream(stream)))
+    st = (_lib or load()).sg_orthogonalise(g.data_ptr(), dt, k, r, c, ld, steps, _ptr(cf), eps, scale, out.data_ptr(),
+                                           ld_o, workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+    if st:
+        _check(st)
 
 
 def sg_muon_step(w: torch.Tensor, g: torch.Tensor, m: torch.Tensor, w_out: torch.Tensor, m_out: torch.Tensor,
@@ -801,16 +831,17 @@ def sg_muon_step(w: torch.Tensor, g: torch.Tensor, m: torch.Tensor, w_out: torch
     """One Muon step of the weights w ([rows, cols] or [count, rows, cols],
     float32 or bfloat16) from their float32 gradient g and momentum m, into
     w_out and m_out (which may be w and m); see sg.h."""
-    a = _stack("sg_muon_step: w", w)
-    _dtype_code(w)
-    for name, t in (("w", w), ("g", g), ("m", m), ("w_out", w_out), ("m_out", m_out)):
-        _need(isinstance(t, torch.Tensor) and t.shape == w.shape and t.is_contiguous() and t.device == w.device,
-              "sg_muon_step: %s must be a contiguous tensor of w's shape on its device" % name)
-    _need(g.dtype == m.dtype == m_out.dtype == torch.float32 and w_out.dtype == w.dtype,
-          "sg_muon_step: g, m and m_out must be float32, w_out of w's dtype")
-    k, r, c = a.shape
+    dt, k, r, c, _ = _stack("sg_muon_step: w", w)
+    dev, shape = w.get_device(), w.shape
+    for t, dtype in ((w, w.dtype), (w_out, w.dtype), (g, torch.float32), (m, torch.float32), (m_out, torch.float32)):
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != dev \
+                or not t.is_contiguous():
+            _invalid("sg_muon_step: w, w_out (of one dtype) and g, m, m_out (float32) must be contiguous tensors of "
+                     "one shape on one device")
     cf = _coef(steps, coef)
-    _check(load().sg_muon_step(w.data_ptr(), _dtype_code(w), g.data_ptr(), m.data_ptr(), k, r, c, float(lr),
-                               float(momentum), 1 if nesterov else 0, float(weight_decay), float(scale), int(steps),
-                               _ptr(cf), float(eps), w_out.data_ptr(), m_out.data_ptr(), workspace.data_ptr(),
-                               workspace.numel(), _stream(stream)))
+    st = (_lib or load()).sg_muon_step(w.data_ptr(), dt, g.data_ptr(), m.data_ptr(), k, r, c, lr, momentum,
+                                       1 if nesterov else 0, weight_decay, scale, steps, _ptr(cf), eps,
+                                       w_out.data_ptr(), m_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                       _raw_stream(stream, dev))
+    if st:
+        _check(st)

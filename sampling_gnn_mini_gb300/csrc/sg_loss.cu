@@ -47,14 +47,19 @@ __device__ __forceinline__ int32_t rows_of(const int32_t* d_n, int32_t n_cap) {
     return d_n ? min(max(*d_n, 0), n_cap) : n_cap;
 }
 
-// 2^x; the hardware's approximation is within 2^-22 of the value
+// 2^x; the hardware's approximation is within 2^-22 of the value, results
+// below the normal range are 0
 __device__ __forceinline__ float ex2(float x) {
     float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 // exp(x - m), m finite
 __device__ __forceinline__ float exp_from(float x, float m) { return ex2((x - m) * kLog2e); }
+
+__device__ __forceinline__ float loss_of(float m, float z, float xy) {
+    return xy == -INFINITY && z == z ? INFINITY : __logf(z) + (m - xy);
+}
 
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
@@ -62,106 +67,179 @@ __device__ __forceinline__ float warp_max(float x) {
     return x;
 }
 
+// ------------------------------------------------------ pairs of fp32 values
+// (one instruction for two values: the exponentials' arguments and sums are
+// what this file's kernels issue most of)
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(f2 p, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // --------------------------------------------------- 16-byte parts of a row
 template <typename T>
 constexpr int kE = 16 / (int)sizeof(T);  // elements of a vector
 
-__device__ __forceinline__ void unpack(const uint4& u, float (&v)[4]) {
-    v[0] = __uint_as_float(u.x), v[1] = __uint_as_float(u.y), v[2] = __uint_as_float(u.z), v[3] = __uint_as_float(u.w);
+// A row as its elements before the first 16-byte boundary (head), its whole
+// vectors, and its elements after the last of them.  Whole vectors are dealt
+// to threads; the up to 7 + 7 others go to lanes 0.. and 8.. of one warp.
+template <typename T>
+struct RowParts {
+    int32_t head, vecs, tail;
+    __device__ __forceinline__ RowParts(const T* row, int32_t classes) {
+        const int32_t off = (int32_t)(((uintptr_t)row & 15) / sizeof(T));
+        head = off ? min(classes, kE<T> - off) : 0;
+        vecs = (classes - head) / kE<T>;
+        tail = classes - head - vecs * kE<T>;
+    }
+    // element of edge lane l, or -1
+    __device__ __forceinline__ int32_t edge(int l) const {
+        if (l < 8) return l < head ? l : -1;
+        return l - 8 < tail ? head + vecs * kE<T> + l - 8 : -1;
+    }
+    // where element c sits: vector >= 0, or -1 - (edge lane)
+    __device__ __forceinline__ int32_t place(int32_t c) const {
+        if (c < head) return -1 - c;
+        const int32_t v = (c - head) / kE<T>;
+        return v < vecs ? v : -1 - (8 + c - head - vecs * kE<T>);
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ bool same_phase(const T* a, const T* b) {
+    return (((uintptr_t)a ^ (uintptr_t)b) & 15) == 0;
 }
-__device__ __forceinline__ void unpack(const uint4& u, float (&v)[8]) {
+
+template <typename T>
+__device__ __forceinline__ uint4 empty_part() {
+    const uint32_t w = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;  // -inf
+    return make_uint4(w, w, w, w);
+}
+
+__device__ __forceinline__ void pairs_of(const uint4& u, f2 (&p)[2]) {
+    p[0] = pair(__uint_as_float(u.x), __uint_as_float(u.y));
+    p[1] = pair(__uint_as_float(u.z), __uint_as_float(u.w));
+}
+__device__ __forceinline__ void pairs_of(const uint4& u, f2 (&p)[4]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i) p[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
-__device__ __forceinline__ uint4 pack(const float (&v)[4]) {
-    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+__device__ __forceinline__ uint4 part_of(const f2 (&p)[2]) {
+    float a, b, c, d;
+    unpair(p[0], a, b);
+    unpair(p[1], c, d);
+    return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
 }
-__device__ __forceinline__ uint4 pack(const float (&v)[8]) {
+__device__ __forceinline__ uint4 part_of(const f2 (&p)[4]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        float a, b;
+        unpair(p[i], a, b);
+        const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
         w[i] = *reinterpret_cast<const uint32_t*>(&t);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Elements of the row before the 16-byte boundary at or below its start:
-// vector v of the row holds elements v E - off .. v E - off + E - 1.
-template <typename T>
-__device__ __forceinline__ int32_t phase(const T* row) {
-    return (int32_t)(((uintptr_t)row & 15) / sizeof(T));
-}
-
-// Vector at element e0; elements outside the row read as -inf.
-template <typename T>
-__device__ __forceinline__ uint4 load_part(const T* row, int32_t e0, int32_t classes) {
-    if (e0 >= 0 && e0 + kE<T> <= classes) return *reinterpret_cast<const uint4*>(row + e0);
-    float v[kE<T>];
-#pragma unroll
-    for (int q = 0; q < kE<T>; ++q) v[q] = e0 + q >= 0 && e0 + q < classes ? to_f(row[e0 + q]) : -INFINITY;
-    return pack(v);
-}
-
-template <typename T>
-__device__ __forceinline__ uint4 empty_part() {
-    float v[kE<T>];
-#pragma unroll
-    for (int q = 0; q < kE<T>; ++q) v[q] = -INFINITY;
-    return pack(v);
-}
-
-// Stores the vector at element e0; same: the gradient's row has the logits'
-// 16-byte phase.
-template <typename T>
-__device__ __forceinline__ void store_part(T* row, int32_t e0, int32_t classes, bool same, const float (&v)[kE<T>]) {
-    if (same && e0 >= 0 && e0 + kE<T> <= classes) {
-        *reinterpret_cast<uint4*>(row + e0) = pack(v);
-        return;
-    }
-#pragma unroll
-    for (int q = 0; q < kE<T>; ++q)
-        if (e0 + q >= 0 && e0 + q < classes) put(row + e0 + q, v[q]);
+// Keeps the compiler from carrying a vector's unpacked elements (twice its
+// registers) from one use to the next: they are unpacked again instead.
+__device__ __forceinline__ void repack(uint4& u) {
+    asm volatile("" : "+r"(u.x), "+r"(u.y), "+r"(u.z), "+r"(u.w));
 }
 
 template <typename T>
 __device__ __forceinline__ float part_max(const uint4& u) {
-    float v[kE<T>];
-    unpack(u, v);
-    float m = v[0];
-#pragma unroll
-    for (int q = 1; q < kE<T>; ++q) m = fmaxf(m, v[q]);
-    return m;
+    if constexpr (sizeof(T) == 2) {  // pairwise on the packed elements
+        const auto h = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+        const __nv_bfloat162 m = __hmax2(__hmax2(h(u.x), h(u.y)), __hmax2(h(u.z), h(u.w)));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+    return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
 }
 
-// Sum of exp(x - m); fp32 vectors keep the exponentials in place of x.
-template <typename T>
-__device__ __forceinline__ float part_exp(uint4& u, float m) {
-    float v[kE<T>], s = 0.f;
-    unpack(u, v);
-#pragma unroll
-    for (int q = 0; q < kE<T>; ++q) {
-        v[q] = exp_from(v[q], m);
-        s += v[q];
+// exp(x - m) is formed as 2^(x log2(e) - m log2(e)), one fused operation a
+// value; m log2(e) has to stay finite.
+struct Base {
+    f2 l, b;
+    float mb;
+    __device__ __forceinline__ explicit Base(float m) : mb(-m * kLog2e) {
+        l = pair(kLog2e, kLog2e);
+        b = pair(mb, mb);
     }
-    if constexpr (sizeof(T) == 4) u = pack(v);
-    return s;
+    __device__ __forceinline__ float of(float x) const { return ex2(fmaf(x, kLog2e, mb)); }
+    __device__ __forceinline__ f2 of(f2 x) const {
+        float a, c;
+        unpair(fma2(x, l, b), a, c);
+        return pair(ex2(a), ex2(c));
+    }
+};
+constexpr float kHuge = 1e37f;  // |m| from which m log2(e) may overflow
+
+// x - m, for |m| >= kHuge: such differences are 0, or so large that their
+// exponentials are 0 however they are rounded.
+template <typename T>
+__device__ __forceinline__ void part_shift(uint4& u, float m) {
+    f2 p[kE<T> / 2];
+    pairs_of(u, p);
+#pragma unroll
+    for (int i = 0; i < kE<T> / 2; ++i) p[i] = add2(p[i], pair(-m, -m));
+    u = part_of(p);
+}
+
+// Adds exp(x - m) to sum; fp32 vectors keep the exponentials in place of x.
+template <typename T>
+__device__ __forceinline__ void part_exp(uint4& u, const Base& m, f2& sum) {
+    f2 p[kE<T> / 2];
+    pairs_of(u, p);
+#pragma unroll
+    for (int i = 0; i < kE<T> / 2; ++i) {
+        p[i] = m.of(p[i]);
+        sum = add2(sum, p[i]);
+    }
+    if constexpr (sizeof(T) == 4) u = part_of(p);
 }
 
 // The gradient (without its -w at the label) of a vector that part_exp saw.
 template <typename T>
-__device__ __forceinline__ void part_grad(const uint4& u, float m, float inv, float (&v)[kE<T>]) {
-    unpack(u, v);
+__device__ __forceinline__ uint4 part_grad(const uint4& u, const Base& m, f2 inv) {
+    f2 p[kE<T> / 2];
+    pairs_of(u, p);
 #pragma unroll
-    for (int q = 0; q < kE<T>; ++q) v[q] = inv * (sizeof(T) == 4 ? v[q] : exp_from(v[q], m));
+    for (int i = 0; i < kE<T> / 2; ++i) p[i] = mul2(inv, sizeof(T) == 4 ? p[i] : m.of(p[i]));
+    return part_of(p);
 }
 
-__device__ __forceinline__ float loss_of(float m, float z, float xy) {
-    return xy == -INFINITY && z == z ? INFINITY : __logf(z) + (m - xy);
+// Stores a vector at p; whole: p is on a 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ void store_part(T* p, bool whole, const uint4& u) {
+    if (whole) {
+        *reinterpret_cast<uint4*>(p) = u;
+        return;
+    }
+    const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int q = 0; q < kE<T>; ++q) p[q] = e[q];
 }
 
 template <typename T>
@@ -186,8 +264,8 @@ template <typename T, int NV, int R>
 __device__ __forceinline__ void warp_rows(const RowArgs<T>& a, int32_t r0, int32_t n, float w, float (&loss)[R]) {
     const int lane = (int)lane_id();
     uint4 x[R][NV];
-    int32_t off[R], y[R];
-    float xy[R];
+    float xe[R], xy[R];  // this lane's edge element; the label's logit
+    int32_t y[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         y[r] = r0 + r < n ? __ldg(a.labels + r0 + r) : -1;
@@ -198,15 +276,18 @@ __device__ __forceinline__ void warp_rows(const RowArgs<T>& a, int32_t r0, int32
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const T* row = a.x + (int64_t)(r0 + r) * a.ld;
-        off[r] = phase(row);
         xy[r] = 0.f;
-        if (y[r] >= 0) {
+        if (y[r] < 0) continue;
+        const T* row = a.x + (int64_t)(r0 + r) * a.ld;
+        const RowParts<T> part(row, a.classes);
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
-                x[r][k] = load_part(row, (lane + 32 * k) * kE<T> - off[r], a.classes);
-            if (((y[r] + off[r]) / kE<T>) % 32 == lane) xy[r] = to_f(row[y[r]]);
+        for (int k = 0; k < NV; ++k) {
+            const int32_t v = lane + 32 * k;
+            x[r][k] = v < part.vecs ? *reinterpret_cast<const uint4*>(row + part.head + v * kE<T>) : empty_part<T>();
         }
+        const int32_t e = part.edge(lane);
+        xe[r] = e >= 0 ? to_f(row[e]) : -INFINITY;
+        xy[r] = to_f(row[y[r]]);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -219,30 +300,42 @@ __device__ __forceinline__ void warp_rows(const RowArgs<T>& a, int32_t r0, int32
                 for (int32_t c = lane; c < a.classes; c += 32) put(out + c, 0.f);
             continue;
         }
-        float m = part_max<T>(x[r][0]);
+        float m = xe[r];
 #pragma unroll
-        for (int k = 1; k < NV; ++k) m = fmaxf(m, part_max<T>(x[r][k]));
+        for (int k = 0; k < NV; ++k) m = fmaxf(m, part_max<T>(x[r][k]));
         m = warp_max(m);
         if (m == -INFINITY) m = 0.f;
-        float z = 0.f;
+        const float m_row = m;
+        if (!(fabsf(m) < kHuge)) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k) z += part_exp<T>(x[r][k], m);
-        z = warp_sum(z);
-        const int owner = ((y[r] + off[r]) / kE<T>) % 32;
-        const float at = __shfl_sync(0xFFFFFFFFu, xy[r], owner);
-        loss[r] = loss_of(m, z, at);
-        if (lane == owner) a.loss[r0 + r] = loss[r];
+            for (int k = 0; k < NV; ++k) part_shift<T>(x[r][k], m);
+            xe[r] -= m;
+            m = 0.f;
+        }
+        const Base base(m);
+        f2 sum = pair(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) part_exp<T>(x[r][k], base, sum);
+        float z, z1;
+        unpair(sum, z, z1);
+        z = warp_sum(z + z1 + base.of(xe[r]));
+        loss[r] = loss_of(m_row, z, xy[r]);
+        if (lane == 0) a.loss[r0 + r] = loss[r];
         if (!out) continue;
+        const T* row = a.x + (int64_t)(r0 + r) * a.ld;
+        const RowParts<T> part(row, a.classes);
+        const bool same = same_phase(row, (const T*)out);
         const float inv = z == 0.f ? 0.f : w / z;
-        const bool same = phase(out) == off[r];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            float v[kE<T>];
-            part_grad<T>(x[r][k], m, inv, v);
-            store_part(out, (lane + 32 * k) * kE<T> - off[r], a.classes, same, v);
+            const int32_t v = lane + 32 * k;
+            if (v < part.vecs)
+                store_part(out + part.head + v * kE<T>, same, part_grad<T>(x[r][k], base, pair(inv, inv)));
         }
-        // this lane stored the label's element above: it may now replace it
-        if (lane == owner) put(out + y[r], z == 0.f ? 0.f : fmaf(inv, exp_from(at, m), -w));
+        const int32_t e = part.edge(lane), at = part.place(y[r]);
+        if (e >= 0) put(out + e, inv * base.of(xe[r]));
+        // the lane that stored the label's element above may now replace it
+        if ((at < 0 ? -1 - at : at % 32) == lane) put(out + y[r], z == 0.f ? 0.f : fmaf(inv, exp_from(xy[r], m_row), -w));
     }
 }
 
@@ -314,61 +407,55 @@ __global__ void __launch_bounds__(kThreads) k_xent_small(RowArgs<T> a) {
 }
 
 // --------------------------------------------------------- rows by clusters
-template <typename T, int NT, int S>
-__global__ void __launch_bounds__(NT, 1024 / NT) k_xent_row(RowArgs<T> a) {
-    pdl_start();
-    constexpr int kWarps = NT / 32, kParts = S * kWarps;
-    __shared__ float pm[kParts], pz[kParts];  // (m, z) of every warp of the cluster
-    __shared__ bool last;
-    const int warp = (int)(threadIdx.x >> 5), lane = (int)lane_id();
-    const int32_t r = (int32_t)(blockIdx.x / S), rank = (int32_t)(blockIdx.x % S);
-    const int32_t n = rows_of(a.d_n, a.n_cap);
-    if (r >= n) return;  // the whole cluster
-    if constexpr (S > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
-    if (threadIdx.x == 0) last = false;
-    const T* row = a.x + (int64_t)r * a.ld;
-    T* out = a.grad ? a.grad + (int64_t)r * a.ld_grad : nullptr;
-    const int32_t off = phase(row), classes = a.classes;
-    const bool same = out && phase(out) == off;
-    const int32_t nv = (classes + off + kE<T> - 1) / kE<T>, per = (nv + S - 1) / S;
-    const int32_t v0 = rank * per, v1 = min(nv, v0 + per);
-    int32_t y = __ldg(a.labels + r);
-    if (y < -1 || y >= classes) {
-        if (rank == 0 && threadIdx.x == 0) dev_err(ERR_INDEX);
-        y = -1;
-    }
-    const bool used = y >= 0;  // the same in the whole cluster
-    const int32_t vy = used ? (y + off) / kE<T> : 0;
-    const bool owner = vy >= v0 && vy < v0 + per && (vy - v0) % NT == (int32_t)threadIdx.x;
+// What a thread holds of a row: up to kVecs vectors of its CTA's slice, NT
+// apart, and for the lanes of warp 0 of CTA 0 an edge element.
+template <typename T, int NT>
+struct Held {
     uint4 x[kVecs];
-    float m = -INFINITY, z = 0.f, xy = 0.f;
-    if (used) {
+    float xe;
+    float m, z;  // of this warp: z = sum of exp(x - m)
+    float base;  // what the kept x are relative to: m, or 0 after a shift
+};
+
+// (m, z) of the warp from its vectors and, when given, the part (mr, zr) of
+// each thread that is not held.
+template <typename T, int NT>
+__device__ __forceinline__ void reduce_held(Held<T, NT>& h, int32_t count, float mr, float zr) {
+    float m = fmaxf(h.xe, mr);
 #pragma unroll
-        for (int k = 0; k < kVecs; ++k) {
-            const int32_t v = v0 + (int32_t)threadIdx.x + k * NT;
-            x[k] = v < v1 ? load_part(row, v * kE<T> - off, classes) : empty_part<T>();
-        }
-        if (owner) xy = to_f(row[y]);
+    for (int k = 0; k < kVecs; ++k)
+        if ((int32_t)threadIdx.x + k * NT < count) m = fmaxf(m, part_max<T>(h.x[k]));
+    m = warp_max(m);
+    if (m == -INFINITY) m = 0.f;
+    h.m = h.base = m;
+    if (!(fabsf(m) < kHuge)) {
 #pragma unroll
-        for (int k = 0; k < kVecs; ++k) m = fmaxf(m, part_max<T>(x[k]));
-        float mr = -INFINITY, zr = 0.f;  // the part past the registers
-        for (int32_t v = v0 + (int32_t)threadIdx.x + kVecs * NT; v < v1; v += NT) {
-            uint4 u = load_part(row, v * kE<T> - off, classes);
-            const float top = fmaxf(mr, part_max<T>(u)), base = top == -INFINITY ? 0.f : top;
-            zr = zr * exp_from(mr, base) + part_exp<T>(u, base);
-            mr = top;
-        }
-        m = warp_max(fmaxf(m, mr));
-        if (m == -INFINITY) m = 0.f;
-        if (zr != 0.f) z = zr * exp_from(mr == -INFINITY ? 0.f : mr, m);
-#pragma unroll
-        for (int k = 0; k < kVecs; ++k) z += part_exp<T>(x[k], m);
-        z = warp_sum(z);
+        for (int k = 0; k < kVecs; ++k) part_shift<T>(h.x[k], m);
+        h.xe -= m;
+        h.base = 0.f;
     }
+    const Base base(h.base);
+    f2 sum = pair(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k)
+        if ((int32_t)threadIdx.x + k * NT < count) {
+            repack(h.x[k]);
+            part_exp<T>(h.x[k], base, sum);
+        }
+    float z, z1;
+    unpair(sum, z, z1);
+    z += z1 + base.of(h.xe);
+    if (zr != 0.f) z += zr * exp_from(mr == -INFINITY ? 0.f : mr, m);
+    h.z = warp_sum(z);
+}
+
+// The warps' (m, z) into every CTA of the cluster, and a barrier.
+template <int NT, int S>
+__device__ __forceinline__ void share_parts(float* pm, float* pz, int32_t rank, float m, float z) {
+    const int warp = (int)(threadIdx.x >> 5), lane = (int)lane_id();
     if constexpr (S > 1) {
-        asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");  // every CTA runs: its shared memory may be written
         if (lane < S) {
-            const uint32_t slot = (uint32_t)(rank * kWarps + warp) * 4;
+            const uint32_t slot = (uint32_t)(rank * (NT / 32) + warp) * 4;
             asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(map_rank(smem_addr(pm) + slot, (uint32_t)lane)), "f"(m)
                          : "memory");
             asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(map_rank(smem_addr(pz) + slot, (uint32_t)lane)), "f"(z)
@@ -379,36 +466,122 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_xent_row(RowArgs<T> a) {
         if (lane == 0) pm[warp] = m, pz[warp] = z;
         __syncthreads();
     }
+}
+
+// The row's (M, Z); parts without a finite logit (z = 0) take no part.
+template <int PARTS>
+__device__ __forceinline__ void join_parts(const float* pm, const float* pz, float& M, float& Z) {
+    const int lane = (int)lane_id();
+    M = -INFINITY, Z = 0.f;
+#pragma unroll
+    for (int i = lane; i < PARTS; i += 32)
+        if (pz[i] != 0.f) M = fmaxf(M, pm[i]);
+    M = warp_max(M);
+    if (M == -INFINITY) M = 0.f;
+#pragma unroll
+    for (int i = lane; i < PARTS; i += 32)
+        if (pz[i] != 0.f) Z += pz[i] * exp_from(pm[i], M);
+    Z = warp_sum(Z);
+}
+
+// Gradient of what the thread holds; first: the slice's first vector.
+template <typename T, int NT>
+__device__ __forceinline__ void store_held(Held<T, NT>& h, T* first, int32_t count, bool same, float inv) {
+    const Base base(h.base);
+    const f2 inv2 = pair(inv, inv);
+    T* p = first + (int32_t)threadIdx.x * kE<T>;
+    if (same) {
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k)
+            if ((int32_t)threadIdx.x + k * NT < count) {
+                repack(h.x[k]);
+                *reinterpret_cast<uint4*>(p + k * NT * kE<T>) = part_grad<T>(h.x[k], base, inv2);
+            }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k)
+            if ((int32_t)threadIdx.x + k * NT < count) {
+                repack(h.x[k]);
+                store_part(p + k * NT * kE<T>, false, part_grad<T>(h.x[k], base, inv2));
+            }
+    }
+}
+
+// A zero gradient for this CTA's part of an ignored row.
+template <typename T, int NT>
+__device__ __forceinline__ void zero_row(T* out, int32_t classes, int32_t rank, int32_t ctas) {
+    const int32_t per = (classes + ctas - 1) / ctas, c1 = min(classes, (rank + 1) * per);
+    for (int32_t c = rank * per + (int32_t)threadIdx.x; c < c1; c += NT) put(out + c, 0.f);
+}
+
+template <typename T, int NT, int S>
+__global__ void __launch_bounds__(NT, 1024 / NT) k_xent_row(RowArgs<T> a) {
+    pdl_start();
+    constexpr int kParts = S * NT / 32;
+    __shared__ float pm[kParts], pz[kParts];  // (m, z) of every warp of the cluster
+    __shared__ bool last;
+    const int32_t r = (int32_t)(blockIdx.x / S), rank = (int32_t)(blockIdx.x % S);
+    const int32_t n = rows_of(a.d_n, a.n_cap), classes = a.classes;
+    if (r >= n) return;  // the whole cluster
+    if constexpr (S > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
+    if (threadIdx.x == 0) last = false;
+    const T* row = a.x + (int64_t)r * a.ld;
+    T* out = a.grad ? a.grad + (int64_t)r * a.ld_grad : nullptr;
+    int32_t y = __ldg(a.labels + r);
+    if (y < -1 || y >= classes) {
+        if (rank == 0 && threadIdx.x == 0) dev_err(ERR_INDEX);
+        y = -1;
+    }
+    const bool used = y >= 0;  // the same in the whole cluster
+    const RowParts<T> part(row, classes);
+    const int32_t per = (part.vecs + S - 1) / S, v0 = min(part.vecs, rank * per), count = min(part.vecs, v0 + per) - v0;
+    const int32_t edge = rank == 0 && threadIdx.x < 32 ? part.edge((int)threadIdx.x) : -1;
+    // the thread that holds the label's element
+    const int32_t at = used ? part.place(y) : -1;
+    const bool owner = at < 0 ? rank == 0 && (int32_t)threadIdx.x == -1 - at
+                              : at >= v0 && at < v0 + count && (at - v0) % NT == (int32_t)threadIdx.x;
+    const T* p = row + part.head + (v0 + (int32_t)threadIdx.x) * kE<T>;
+    Held<T, NT> h;
+    h.m = 0.f, h.z = 0.f;
+    float xy = 0.f;
     if (used) {
-        // the row's (M, Z): parts without a finite logit have m = 0, z = 0 and
-        // are left out of the maximum
-        float M = -INFINITY, Z = 0.f;
 #pragma unroll
-        for (int i = lane; i < kParts; i += 32)
-            if (pz[i] != 0.f) M = fmaxf(M, pm[i]);
-        M = warp_max(M);
-        if (M == -INFINITY) M = 0.f;
+        for (int k = 0; k < kVecs; ++k)
+            h.x[k] = (int32_t)threadIdx.x + k * NT < count ? *reinterpret_cast<const uint4*>(p + k * NT * kE<T>)
+                                                           : empty_part<T>();
+        h.xe = edge >= 0 ? to_f(row[edge]) : -INFINITY;
+        if (owner) xy = to_f(row[y]);
+        float mr = -INFINITY, zr = 0.f;  // the part past the registers
+        for (int32_t i = (int32_t)threadIdx.x + kVecs * NT; i < count; i += NT) {
+            const T* q = row + part.head + (v0 + i) * kE<T>;
+            const float top = fmaxf(mr, part_max<T>(*reinterpret_cast<const uint4*>(q)));
+            const float b = top == -INFINITY ? 0.f : top;
+            zr *= exp_from(mr, b);
 #pragma unroll
-        for (int i = lane; i < kParts; i += 32)
-            if (pz[i] != 0.f) Z += pz[i] * exp_from(pm[i], M);
-        Z = warp_sum(Z);
+            for (int e = 0; e < kE<T>; ++e) zr += exp_from(to_f(q[e]), b);
+            mr = top;
+        }
+        reduce_held(h, count, mr, zr);
+    }
+    // every CTA runs: its shared memory may be written
+    if constexpr (S > 1) asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
+    share_parts<NT, S>(pm, pz, rank, h.m, h.z);
+    if (used) {
+        float M, Z;
+        join_parts<kParts>(pm, pz, M, Z);
         const float w = a.mean ? a.gs / (float)max(1, *a.valid) : a.gs;
         if (out) {
-            const float inv = z == 0.f || Z == 0.f ? 0.f : w / Z * exp_from(m, M);
+            const bool same = same_phase(row, (const T*)out);
+            const float inv = h.z == 0.f || Z == 0.f ? 0.f : w / Z * exp_from(h.m, M);
+            store_held(h, out + part.head + v0 * kE<T>, count, same, inv);
+            if (edge >= 0) put(out + edge, inv * Base(h.base).of(h.xe));
+            for (int32_t i = (int32_t)threadIdx.x + kVecs * NT; i < count; i += NT) {
+                const int32_t c = part.head + (v0 + i) * kE<T>;
+                float g[kE<T>];
 #pragma unroll
-            for (int k = 0; k < kVecs; ++k) {
-                const int32_t v = v0 + (int32_t)threadIdx.x + k * NT;
-                if (v >= v1) continue;
-                float g[kE<T>];
-                part_grad<T>(x[k], m, inv, g);
-                store_part(out, v * kE<T> - off, classes, same, g);
-            }
-            for (int32_t v = v0 + (int32_t)threadIdx.x + kVecs * NT; v < v1; v += NT) {
-                uint4 u = load_part(row, v * kE<T> - off, classes);
-                float g[kE<T>];
-                part_exp<T>(u, m);
-                part_grad<T>(u, m, inv, g);
-                store_part(out, v * kE<T> - off, classes, same, g);
+                for (int e = 0; e < kE<T>; ++e) g[e] = Z == 0.f ? 0.f : w / Z * exp_from(to_f(row[c + e]), M);
+#pragma unroll
+                for (int e = 0; e < kE<T>; ++e) put(out + c + e, g[e]);
             }
             // this thread stored the label's element above: it may now replace it
             if (owner) put(out + y, Z == 0.f ? 0.f : fmaf(w / Z, exp_from(xy, M), -w));
@@ -416,16 +589,118 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_xent_row(RowArgs<T> a) {
         if (owner) a.loss[r] = loss_of(M, Z, xy);
     } else {
         if (owner) a.loss[r] = 0.f;
-        if (out) {
-            const float none[kE<T>] = {};
-            for (int32_t v = v0 + (int32_t)threadIdx.x; v < v1; v += NT)
-                store_part(out, v * kE<T> - off, classes, same, none);
-        }
+        if (out) zero_row<T, NT>(out, classes, rank, S);
     }
     if (!a.total) return;
     if (owner) {
         __threadfence();
         if (atomicAdd(a.valid + 1, 1) == n - 1) last = true;
+    }
+    __syncthreads();
+    if (last) {
+        __threadfence();
+        put_total<NT>(a, n);
+    }
+}
+
+// Many long rows: the same, with each cluster walking over its rows and the
+// next two rows' slices on their way into shared memory (one bulk copy of a
+// slice's vectors) while the current row is worked on.
+constexpr int kStreamVecs = 3500;  // of a CTA's slice: two buffers of it, two CTAs an SM
+
+template <typename T, int NT, int S>
+__global__ void __launch_bounds__(NT, 1024 / NT) k_xent_stream(RowArgs<T> a, int32_t slots) {
+    extern __shared__ __align__(128) uint8_t dsm[];
+    pdl_start();
+    constexpr int kParts = S * NT / 32;
+    __shared__ float pm[2][kParts], pz[2][kParts];  // (m, z) of every warp of the cluster, by row parity
+    __shared__ __align__(8) uint64_t full[2];
+    __shared__ bool last;
+    const int32_t rank = (int32_t)(blockIdx.x % S), first = (int32_t)(blockIdx.x / S), step = (int32_t)(gridDim.x / S);
+    const int32_t n = rows_of(a.d_n, a.n_cap), classes = a.classes;
+    if (first >= n) return;  // the whole cluster
+    if (threadIdx.x == 0) {
+        last = false;
+        mbar_init(&full[0], 1);
+        mbar_init(&full[1], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    __syncthreads();
+    if constexpr (S > 1) cluster_sync();  // every CTA runs: its shared memory may be written
+    const auto label = [&](int32_t r) { return r < n ? __ldg(a.labels + r) : -1; };
+    // copies this CTA's slice of row r into buffer b (thread 0)
+    const auto fetch = [&](int32_t r, int32_t y, int b) {
+        if (r >= n || y < 0 || y >= classes) return;
+        const T* row = a.x + (int64_t)r * a.ld;
+        const RowParts<T> part(row, classes);
+        const int32_t per = (part.vecs + S - 1) / S, v0 = min(part.vecs, rank * per);
+        const uint32_t bytes = (uint32_t)(min(part.vecs, v0 + per) - v0) * 16;
+        mbar_expect_tx(&full[b], bytes);
+        if (bytes)
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                    smem_addr(dsm) + (uint32_t)(b * slots) * 16),
+                "l"(row + part.head + (int64_t)v0 * kE<T>), "r"(bytes), "r"(smem_addr(&full[b]))
+                : "memory");
+    };
+    int32_t y = label(first), y1 = label(first + step), y2;
+    if (threadIdx.x == 0) {
+        fetch(first, y, 0);
+        fetch(first + step, y1, 1);
+    }
+    const float w = a.mean ? a.gs / (float)max(1, *a.valid) : a.gs;
+    uint32_t phases = 0;  // bit b: parity of buffer b's next fill
+    int32_t par = 0;
+    for (int32_t r = first; r < n; r += step, par ^= 1, y = y1, y1 = y2) {
+        y2 = label(r + 2 * step);
+        const T* row = a.x + (int64_t)r * a.ld;
+        T* out = a.grad ? a.grad + (int64_t)r * a.ld_grad : nullptr;
+        if (y < 0 || y >= classes) {  // the same in the whole cluster
+            if (rank == 0 && threadIdx.x == 0) {
+                if (y != -1) dev_err(ERR_INDEX);
+                a.loss[r] = 0.f;
+            }
+            if (out) zero_row<T, NT>(out, classes, rank, S);
+            if (threadIdx.x == 0) fetch(r + 2 * step, y2, par);  // this row's buffer was not filled
+            continue;
+        }
+        const RowParts<T> part(row, classes);
+        const int32_t per = (part.vecs + S - 1) / S, v0 = min(part.vecs, rank * per), count = min(part.vecs, v0 + per) - v0;
+        const int32_t edge = rank == 0 && threadIdx.x < 32 ? part.edge((int)threadIdx.x) : -1;
+        const int32_t at = part.place(y);
+        const bool owner = at < 0 ? rank == 0 && (int32_t)threadIdx.x == -1 - at
+                                  : at >= v0 && at < v0 + count && (at - v0) % NT == (int32_t)threadIdx.x;
+        Held<T, NT> h;
+        h.xe = edge >= 0 ? to_f(row[edge]) : -INFINITY;
+        const float xy = owner ? to_f(row[y]) : 0.f;
+        if (!mbar_wait(&full[par], (phases >> par) & 1u) && lane_id() == 0) dev_err(ERR_TIMEOUT);
+        phases ^= 1u << par;
+        const uint4* buf = reinterpret_cast<const uint4*>(dsm) + par * slots + threadIdx.x;
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k)
+            h.x[k] = (int32_t)threadIdx.x + k * NT < count ? buf[k * NT] : empty_part<T>();
+        reduce_held(h, count, -INFINITY, 0.f);
+        share_parts<NT, S>(pm[par], pz[par], rank, h.m, h.z);
+        // every thread has its vectors in registers: the buffer is free
+        if (threadIdx.x == 0) fetch(r + 2 * step, y2, par);
+        float M, Z;
+        join_parts<kParts>(pm[par], pz[par], M, Z);
+        if (out) {
+            const float inv = h.z == 0.f || Z == 0.f ? 0.f : w / Z * exp_from(h.m, M);
+            store_held(h, out + part.head + v0 * kE<T>, count, same_phase(row, (const T*)out), inv);
+            if (edge >= 0) put(out + edge, inv * Base(h.base).of(h.xe));
+            // this thread stored the label's element above: it may now replace it
+            if (owner) put(out + y, Z == 0.f ? 0.f : fmaf(w / Z, exp_from(xy, M), -w));
+        }
+        if (owner) a.loss[r] = loss_of(M, Z, xy);
+    }
+    __threadfence();
+    if constexpr (S > 1) cluster_sync();
+    else __syncthreads();
+    if (!a.total) return;
+    if (rank == 0 && threadIdx.x == 0) {
+        __threadfence();
+        last = atomicAdd(a.valid + 1, 1) == min(step, n) - 1;
     }
     __syncthreads();
     if (last) {
@@ -455,10 +730,11 @@ __global__ void __launch_bounds__(kTotalThreads) k_xent_count(const int32_t* __r
 // -------------------------------------------------------------------- host
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned threads, unsigned cluster, cudaStream_t s,
-                           Args... args) {
+                           int smem, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -475,7 +751,7 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned thr
 template <typename T, int NV, int R>
 sg_status run_warp(const RowArgs<T>& a, bool small, cudaStream_t s) {
     if (small)
-        SG_CUDA(launch_cluster(k_xent_small<T, NV, R>, kSmallCtas, kThreads, kSmallCtas, s, a));
+        SG_CUDA(launch_cluster(k_xent_small<T, NV, R>, kSmallCtas, kThreads, kSmallCtas, s, 0, a));
     else
         SG_CUDA(launch_pdl(k_xent_warp<T, NV, R>, dim3((unsigned)cdiv(a.n_cap, kThreads / 32 * R)), dim3(kThreads), 0, s, a));
     return SG_OK;
@@ -483,13 +759,29 @@ sg_status run_warp(const RowArgs<T>& a, bool small, cudaStream_t s) {
 
 template <typename T, int NT, int S>
 sg_status run_row(const RowArgs<T>& a, cudaStream_t s) {
-    SG_CUDA(launch_cluster(k_xent_row<T, NT, S>, (unsigned)((int64_t)a.n_cap * S), NT, S, s, a));
+    SG_CUDA(launch_cluster(k_xent_row<T, NT, S>, (unsigned)((int64_t)a.n_cap * S), NT, S, s, 0, a));
+    return SG_OK;
+}
+
+template <typename T, int NT, int S>
+sg_status run_stream(const RowArgs<T>& a, int64_t nv, cudaStream_t s) {
+    const int32_t slots = (int32_t)cdiv(nv, S);  // of a buffer
+    const int smem = 2 * slots * 16;
+    static bool set = false;
+    if (!set) {
+        SG_CUDA(cudaFuncSetAttribute(k_xent_stream<T, NT, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     2 * kStreamVecs * 16));
+        set = true;
+    }
+    int64_t clusters = (int64_t)num_sms() * (1024 / NT) / S;
+    if (clusters > a.n_cap) clusters = a.n_cap;
+    SG_CUDA(launch_cluster(k_xent_stream<T, NT, S>, (unsigned)(clusters * S), NT, S, s, smem, a, slots));
     return SG_OK;
 }
 
 template <typename T>
 sg_status run(RowArgs<T> a, cudaStream_t s) {
-    const int64_t nv = cdiv((int64_t)a.classes + kE<T> - 1, kE<T>);  // vectors of a row, at any phase
+    const int64_t nv = cdiv((int64_t)a.classes, kE<T>);  // vectors of a row, at most
     const bool by_warp = nv <= 32 * kVecs;
     // one cluster serves a call whose vectors its warps hold in a few turns
     const bool small = by_warp && a.n_cap <= 1024 && a.n_cap * nv <= kSmallCtas * kThreads * kVecs;
@@ -501,6 +793,17 @@ sg_status run(RowArgs<T> a, cudaStream_t s) {
         if (nv <= 64) return run_warp<T, 2, 2>(a, small, s);
         if (nv <= 128) return run_warp<T, 4, 2>(a, small, s);
         return run_warp<T, 8, 1>(a, small, s);
+    }
+    // rows for several turns of every cluster: streamed
+    const int wide = nv <= 7 * kThreads ? 1 : nv <= kStreamVecs ? 2 : nv <= 2 * kStreamVecs ? 4 : nv <= 4 * kStreamVecs ? 8 : 16;
+    if (nv <= 8 * kStreamVecs && (int64_t)a.n_cap * wide >= 3 * 4 * num_sms()) {
+        switch (wide) {
+            case 1: return run_stream<T, kThreads, 1>(a, nv, s);
+            case 2: return run_stream<T, 512, 1>(a, nv, s);
+            case 4: return run_stream<T, 512, 2>(a, nv, s);
+            case 8: return run_stream<T, 512, 4>(a, nv, s);
+            default: return run_stream<T, 512, 8>(a, nv, s);
+        }
     }
     // smallest cluster whose registers hold the row, widened while the rows do
     // not fill the SMs; 512 threads when 8 CTAs of 256 do not hold it

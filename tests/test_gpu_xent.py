@@ -119,6 +119,33 @@ def test_loss_and_gradient(n, c, dt):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n,c", [(2000, 2500), (1100, 9001), (500, 20003), (470, 33000), (240, 60001), (300, 14000)])
+def test_many_long_rows(n, c, dt):
+    # more rows than the grid has clusters: rows follow one another in a cluster
+    rng = np.random.default_rng(n + c)
+    x = _logits(rng, n, c, dt)
+    labels = rng.integers(0, c, n).astype(np.int32)
+    labels[rng.random(n) < 0.15] = -1
+    labels[-3:] = -1
+    x[1, ::2] = float("-inf")
+    x[2, :] = float("-inf")
+    labels[1], labels[2] = 1, -1
+    loss, total = torch.full((n,), 7.0, device="cuda"), torch.full((2,), 7.0, device="cuda")
+    grad = torch.full_like(x, 7.0)
+    ws = _ws(n, c)
+    for m in (n, n - 101):
+        d_n = None if m == n else torch.tensor([m], dtype=torch.int32, device="cuda")
+        sg.sg_xent(x, torch.from_numpy(labels).cuda(), n, d_n, loss, total, grad, ws)
+        sg.sg_stream_check()
+        _check(x, labels, loss, total, grad, True, 1.0, m)
+    inplace = x.clone()
+    sg.sg_xent(inplace, torch.from_numpy(labels).cuda(), n, None, loss, total, inplace, ws)
+    sg.sg_xent(x, torch.from_numpy(labels).cuda(), n, None, loss, total, grad, ws)
+    sg.sg_stream_check()
+    assert torch.equal(inplace, grad)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("c,pad,shift", [(100, 4, 0), (100, 1, 1), (129, 0, 3), (1030, 5, 2), (9000, 3, 1),
                                          (20001, 0, 5), (64, 64, 8)])
 def test_strides_and_alignment(dt, c, pad, shift):
