@@ -596,6 +596,7 @@ sg_status sg_embed_fwd(const void* d_table, int32_t dtype_table, int64_t n_rows,
  *                       that occur (accumulation over mini-batches; with
  *                       scale = -rate * (the lookup's scale) and d_grad the
  *                       table, a sparse SGD step); d_rows, d_n_rows NULL
+ *   n_cap     below 2^30
  *   d_g       device [n_cap x dim], row stride ld_g (>= dim); it must not
  *             overlap d_grad
  *   d_grad    row stride ld_grad (>= dim); columns past dim are not touched

@@ -6,13 +6,20 @@
 // Both are bound by memory: the forward reads each row and writes it; the
 // backward reads every row of g once and writes each distinct ID's row once.
 //
-// The backward sorts the positions by ID (stable LSD radix sort, 8 bits a
-// pass, so equal IDs keep ascending positions), then cuts the sorted list
-// into chunks of equal length, whatever the IDs' frequencies: a warp sums the
-// rows of its chunk run by run.  A run that lies inside a chunk is written
-// at once; the pieces of a run that crosses chunk borders are left in the
-// workspace and joined in chunk order by k_embed_join.  So one hot ID costs no
-// more than many cold ones, and every sum has one order: no float atomics.
+// The backward sorts (ID, position) pairs by ID (stable radix sort, up to 8 bits
+// a pass, so equal IDs keep ascending positions), then cuts the sorted list
+// into chunks of equal length, whatever the IDs' frequencies: a group of lanes
+// that covers a row's columns sums the rows of its chunk, run by run.  A run
+// that lies inside a chunk is written at once; the pieces of a run that
+// crosses chunks meet in shared memory, in chunk order, and those of a run
+// that crosses blocks are left in the workspace and joined in block order by
+// k_embed_join.  So one hot ID costs no more than many cold ones, and every
+// sum has one order: no float atomics.
+//
+// The sort: up to kSmallSort positions in one block's shared memory
+// (k_sort_small); else one histogram launch for all passes, then one launch a
+// pass, whose tiles learn their digits' offsets from the tiles before them
+// (decoupled look-back, one thread a digit).
 #include <cuda_bf16.h>
 #include <string.h>
 
@@ -26,11 +33,13 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 8;
-constexpr int kSortItems = 16;                    // keys a thread of the sort
-constexpr int kSortTile = kThreads * kSortItems;  // 4096 keys a block
 constexpr int kDigits = 256;
-constexpr int kScanThreads = 1024;
-constexpr int kChunk = 32;  // sorted positions a warp sums
+constexpr int kMaxPasses = 4;
+constexpr int kSmallSort = 8192;      // positions sorted by one block
+constexpr int kSmallThreads = 1024;
+constexpr int kRunTile = kThreads * 16;   // sorted positions a block of k_runs looks at
+constexpr int kLongChunks = 65536;    // positions from which a chunk is 32 long, not 8
+constexpr uint32_t kNoKey = 0xFFFFFFFFu;  // beside the list's ends
 
 size_t a256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -157,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_fwd(const TI* __restrict__ t
 // ------------------------------------------------------------------- sort
 // Key of position i: its ID, or n_rows (sorted last) for one that takes no part.
 __device__ __forceinline__ uint32_t key_of(const int32_t* __restrict__ ids, int64_t i, int64_t n_rows) {
-    const int32_t g = ids[i];
+    const int32_t g = __ldg(ids + i);
     if (g < 0 || (int64_t)g >= n_rows) {
         if (g != -1) dev_err(ERR_INDEX);
         return (uint32_t)n_rows;
@@ -165,140 +174,287 @@ __device__ __forceinline__ uint32_t key_of(const int32_t* __restrict__ ids, int6
     return (uint32_t)g;
 }
 
-// Digit histogram of block b's tile, digit-major: hist[digit * nb + b].  The
-// first pass reads the IDs (keys NULL).
-__global__ void __launch_bounds__(kThreads) k_sort_hist(const uint32_t* __restrict__ keys,
-                                                        const int32_t* __restrict__ ids, int64_t n_rows, int64_t n_cap,
-                                                        const int32_t* __restrict__ d_n, int shift, int mask,
-                                                        uint32_t* __restrict__ hist, int64_t nb) {
+// How the keys' bits are dealt to passes of `per` bits.
+struct Digits {
+    int32_t passes, per;
+};
+
+// Device state of the multi-block sort; cleared before every use.
+struct SortState {
+    uint32_t hist[kMaxPasses][kDigits];
+    uint32_t ticket[kMaxPasses + 1];  // tiles handed out (the last: of k_runs)
+};
+
+// Digit counts of all passes.
+__global__ void __launch_bounds__(kThreads) k_sort_hist(const int32_t* __restrict__ ids, int64_t n_rows, int64_t n_cap,
+                                                        const int32_t* __restrict__ d_n, Digits dg,
+                                                        SortState* __restrict__ st) {
     pdl_start();
-    __shared__ uint32_t h[kDigits];
-    h[threadIdx.x] = 0;
+    __shared__ uint32_t h[kMaxPasses][kDigits];
+    for (int p = 0; p < dg.passes; ++p) h[p][threadIdx.x] = 0;
     __syncthreads();
-    const int64_t n = count_of(d_n, n_cap), i0 = (int64_t)blockIdx.x * kSortTile;
-    for (int r = 0; r < kSortItems; ++r) {
-        const int64_t i = i0 + r * kThreads + threadIdx.x;
-        if (i < n) atomicAdd(&h[((keys ? keys[i] : key_of(ids, i, n_rows)) >> shift) & mask], 1u);
+    const int64_t n = count_of(d_n, n_cap), stride = (int64_t)gridDim.x * kThreads;
+    const uint32_t mask = (1u << dg.per) - 1;
+    for (int64_t i0 = blockIdx.x * (int64_t)kThreads; i0 < n; i0 += 4 * stride) {
+        uint32_t k[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t i = i0 + u * stride + threadIdx.x;
+            k[u] = i < n ? key_of(ids, i, n_rows) : kNoKey;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (k[u] != kNoKey)
+                for (int p = 0; p < dg.passes; ++p) atomicAdd(&h[p][(k[u] >> (p * dg.per)) & mask], 1u);
     }
     __syncthreads();
-    hist[(int64_t)threadIdx.x * nb + blockIdx.x] = h[threadIdx.x];
+    for (int p = 0; p < dg.passes; ++p)
+        if (h[p][threadIdx.x]) atomicAdd(&st->hist[p][threadIdx.x], h[p][threadIdx.x]);
 }
 
-// Exclusive scan of m entries in place, one block.
-__global__ void __launch_bounds__(kScanThreads) k_sort_scan(uint32_t* __restrict__ a, int64_t m) {
-    pdl_start();
-    __shared__ uint32_t sh[kScanThreads / 32 + 1];
-    uint32_t base = 0;
-    for (int64_t i0 = 0; i0 < m; i0 += kScanThreads) {
-        const int64_t i = i0 + threadIdx.x;
-        const uint32_t x = i < m ? a[i] : 0;
-        uint32_t total;
-        const uint32_t e = block_excl_scan<kScanThreads, uint32_t>(x, sh, total);
-        if (i < m) a[i] = base + e;
-        base += total;
+// Ranks a warp's items (item i of lane l before item i of lane l + 1 and
+// before item i + 1) within their digits: on return rank[i] counts the warp's
+// earlier items of the same digit and cnt[digit] all of them.  Items that are
+// not valid have digit -1.
+template <int ITEMS, typename C>
+__device__ __forceinline__ void warp_rank(const int32_t (&d)[ITEMS], C* cnt, uint32_t (&rank)[ITEMS]) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        const unsigned peers = __match_any_sync(0xFFFFFFFFu, d[i]);
+        uint32_t old = 0;
+        const int leader = __ffs(peers) - 1;
+        if ((int)lane_id() == leader && d[i] >= 0) {
+            old = cnt[d[i]];
+            cnt[d[i]] = (C)(old + __popc(peers));
+        }
+        __syncwarp();
+        rank[i] = __shfl_sync(0xFFFFFFFFu, old, leader) + __popc(peers & lanemask_lt());
     }
 }
 
-// Stable scatter of block b's tile (in rounds of kThreads items): a warp ranks
-// its lanes by digit, the warps' counts become offsets.
-__global__ void __launch_bounds__(kThreads) k_sort_scatter(const uint32_t* __restrict__ keys_in,
-                                                           const int32_t* __restrict__ vals_in,
-                                                           const int32_t* __restrict__ ids, int64_t n_rows,
-                                                           int64_t n_cap, const int32_t* __restrict__ d_n, int shift,
-                                                           int mask, const uint32_t* __restrict__ offs, int64_t nb,
-                                                           uint32_t* __restrict__ keys_out,
-                                                           int32_t* __restrict__ vals_out) {
+__device__ __forceinline__ uint32_t ld_relaxed(const uint32_t* p) {
+    uint32_t v;
+    asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_relaxed(uint32_t* p, uint32_t v) {
+    asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+// One pass: a stable scatter of (key, position) pairs by the pass's digit.
+// Thread t looks back for digit t: status[tile][digit] = flag | count, flag 1
+// the tile's own count, 2 the count up to and including the tile.  Tiles are
+// handed out in order, so every tile looked at is running or done.
+template <int ITEMS>
+__global__ void __launch_bounds__(kThreads) k_sort_pass(const int32_t* __restrict__ ids, const uint2* __restrict__ in,
+                                                        int64_t n_rows, int64_t n_cap, const int32_t* __restrict__ d_n,
+                                                        int pass, int per, SortState* __restrict__ st,
+                                                        uint32_t* __restrict__ status, uint2* __restrict__ out) {
     pdl_start();
-    __shared__ uint32_t run[kDigits];
-    __shared__ uint32_t wcnt[kThreads / 32][kDigits];
+    constexpr int kWarps = kThreads / 32, kTile = kThreads * ITEMS;
+    __shared__ uint32_t cnt[kWarps][kDigits];
+    __shared__ uint32_t sh[kWarps + 1];
+    __shared__ uint32_t tile_sh;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    run[threadIdx.x] = offs[(int64_t)threadIdx.x * nb + blockIdx.x];
-    const int64_t n = count_of(d_n, n_cap), i0 = (int64_t)blockIdx.x * kSortTile;
-    for (int r = 0; r < kSortItems; ++r) {
-        if (i0 + r * kThreads >= n) break;  // the same in every thread
-        const int64_t i = i0 + r * kThreads + threadIdx.x;
-        const bool valid = i < n;
-        uint32_t key = 0;
-        int32_t val = 0;
-        if (valid) {
-            val = keys_in ? vals_in[i] : (int32_t)i;
-            key = keys_in ? keys_in[i] : key_of(ids, i, n_rows);
-        }
-        const uint32_t d = valid ? (key >> shift) & mask : 0x100u + (uint32_t)lane;  // invalid lanes match none
+    if (threadIdx.x == 0) tile_sh = atomicAdd(&st->ticket[pass], 1u);
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) wcnt[w][threadIdx.x] = 0;
-        __syncthreads();
-        const unsigned peers = __match_any_sync(0xFFFFFFFFu, d);
-        const uint32_t rank = __popc(peers & lanemask_lt());
-        if (valid && rank == 0) wcnt[warp][d] = __popc(peers);
-        __syncthreads();
-        {
-            uint32_t acc = run[threadIdx.x];
+    for (int w = 0; w < kWarps; ++w) cnt[w][threadIdx.x] = 0;
+    __syncthreads();
+    const uint32_t tile = tile_sh;
+    const int64_t n = count_of(d_n, n_cap), i0 = (int64_t)tile * kTile + warp * 32 * ITEMS + lane;
+    if ((int64_t)tile * kTile >= n) return;  // no later tile has items either
+    uint2 kv[ITEMS];
+    int32_t d[ITEMS];
+    uint32_t rank[ITEMS];
 #pragma unroll
-            for (int w = 0; w < kThreads / 32; ++w) {
-                const uint32_t c = wcnt[w][threadIdx.x];
-                wcnt[w][threadIdx.x] = acc;
-                acc += c;
-            }
-            run[threadIdx.x] = acc;
+    for (int i = 0; i < ITEMS; ++i) {
+        const int64_t p = i0 + i * 32;
+        d[i] = -1;
+        if (p < n) {
+            kv[i] = in ? in[p] : make_uint2(key_of(ids, p, n_rows), (uint32_t)p);
+            d[i] = (int32_t)((kv[i].x >> (pass * per)) & ((1u << per) - 1));
         }
-        __syncthreads();
-        if (valid) {
-            const uint32_t pos = wcnt[warp][d] + rank;
-            keys_out[pos] = key;
-            vals_out[pos] = val;
+    }
+    uint32_t total;
+    const uint32_t base = block_excl_scan<kThreads, uint32_t>(st->hist[pass][threadIdx.x], sh, total);
+    warp_rank<ITEMS>(d, cnt[warp], rank);
+    __syncthreads();
+    uint32_t mine = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) mine += cnt[w][threadIdx.x];
+    uint32_t* word = status + (int64_t)tile * kDigits + threadIdx.x;
+    uint32_t before = 0;
+    if (tile == 0) {
+        st_relaxed(word, (2u << 30) | mine);
+    } else {
+        st_relaxed(word, (1u << 30) | mine);
+        bool late = false;
+        for (const uint32_t* w = word - kDigits;; w -= kDigits) {
+            uint32_t v = ld_relaxed(w);
+            for (int spins = 0; (v >> 30) == 0 && spins < kLookbackSpins; ++spins) v = ld_relaxed(w);
+            late |= (v >> 30) == 0;
+            before += v & 0x3FFFFFFFu;
+            if ((v >> 30) != 1) break;  // inclusive, or given up
         }
-        __syncthreads();
+        if (late) dev_err(ERR_TIMEOUT);
+        st_relaxed(word, (2u << 30) | (before + mine));
+    }
+    uint32_t run = base + before;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const uint32_t c = cnt[w][threadIdx.x];
+        cnt[w][threadIdx.x] = run;
+        run += c;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+        if (d[i] >= 0) {
+            const uint32_t to = cnt[warp][d[i]] + rank[i];
+            if (to < (uint32_t)n) out[to] = kv[i];  // always, unless a look-back gave up
+        }
+}
+
+// starts[p / span] = distinct IDs before sorted position p, for every p that
+// is a multiple of span (a power of two of at least 16) up to the end of the
+// list; the number of distinct IDs follows at the end.
+__global__ void __launch_bounds__(kThreads) k_runs(const uint2* __restrict__ kv, int64_t n_rows, int64_t n_cap,
+                                                   const int32_t* __restrict__ d_n, int32_t span,
+                                                   SortState* __restrict__ st, unsigned long long* __restrict__ status,
+                                                   int32_t* __restrict__ starts, int32_t* __restrict__ n_out) {
+    pdl_start();
+    __shared__ int32_t sh[kThreads / 32 + 1];
+    __shared__ int32_t tile_sh, before_sh;
+    if (threadIdx.x == 0) tile_sh = (int32_t)atomicAdd(&st->ticket[kMaxPasses], 1u);
+    __syncthreads();
+    const int32_t tile = tile_sh;
+    const int64_t n = count_of(d_n, n_cap), p0 = (int64_t)tile * kRunTile + threadIdx.x * 16;
+    if ((int64_t)tile * kRunTile >= n) {
+        if (tile == 0 && threadIdx.x == 0) *n_out = 0;
+        return;
+    }
+    uint32_t prev = p0 > 0 && p0 - 1 < n ? kv[p0 - 1].x : kNoKey;
+    int32_t mine = 0;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+        const uint32_t k = p0 + q < n ? kv[p0 + q].x : kNoKey;
+        mine += k < (uint32_t)n_rows && k != prev;
+        prev = k;
+    }
+    int32_t total;
+    const int32_t e = block_excl_scan<kThreads, int32_t>(mine, sh, total);
+    if (threadIdx.x < 32) {
+        bool late = false;
+        const int32_t x = chain_lookback(status, tile, 0, total, &late);
+        if (late && threadIdx.x == 0) dev_err(ERR_TIMEOUT);
+        if (threadIdx.x == 0) before_sh = x;
+    }
+    __syncthreads();
+    if (p0 < n && p0 % span == 0) starts[p0 / span] = before_sh + e;
+    if (threadIdx.x == 0 && (int64_t)(tile + 1) * kRunTile >= n) {
+        starts[(n + span - 1) / span] = before_sh + total;
+        *n_out = before_sh + total;
     }
 }
+
+// All of it for a short list, in one block: 8 items a thread, passes in shared
+// memory.
+__global__ void __launch_bounds__(kSmallThreads) k_sort_small(const int32_t* __restrict__ ids, int64_t n_rows,
+                                                              int32_t n_cap, const int32_t* __restrict__ d_n, Digits dg,
+                                                              int32_t span, uint2* __restrict__ out,
+                                                              int32_t* __restrict__ starts, int32_t* __restrict__ n_out) {
+    pdl_start();
+    constexpr int kItems = kSmallSort / kSmallThreads, kWarps = kSmallThreads / 32;
+    extern __shared__ __align__(16) uint8_t dsm[];
+    uint32_t* key = reinterpret_cast<uint32_t*>(dsm);                            // [kSmallSort]
+    uint16_t* pos = reinterpret_cast<uint16_t*>(key + kSmallSort);               // [kSmallSort]
+    uint16_t(*cnt)[kDigits] = reinterpret_cast<uint16_t(*)[kDigits]>(pos + kSmallSort);  // [kWarps][kDigits]
+    __shared__ uint32_t sh[kWarps + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t n = (int32_t)count_of(d_n, n_cap);
+    uint32_t k[kItems], v[kItems], rank[kItems], total;
+    int32_t d[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const int32_t p = warp * 32 * kItems + i * 32 + lane;
+        k[i] = p < n ? key_of(ids, p, n_rows) : kNoKey;
+        v[i] = (uint32_t)p;
+    }
+    for (int p = 0; p < dg.passes; ++p) {
+        uint32_t* zero = reinterpret_cast<uint32_t*>(&cnt[warp][0]);
+#pragma unroll
+        for (int i = 0; i < kDigits / 64; ++i) zero[lane + 32 * i] = 0;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kItems; ++i)
+            d[i] = k[i] != kNoKey ? (int32_t)((k[i] >> (p * dg.per)) & ((1u << dg.per) - 1)) : -1;
+        warp_rank<kItems>(d, cnt[warp], rank);
+        __syncthreads();
+        uint32_t mine = 0;
+        if (threadIdx.x < kDigits)
+            for (int w = 0; w < kWarps; ++w) mine += cnt[w][threadIdx.x];
+        uint32_t run = block_excl_scan<kSmallThreads, uint32_t>(mine, sh, total);
+        if (threadIdx.x < kDigits)
+            for (int w = 0; w < kWarps; ++w) {
+                const uint32_t c = cnt[w][threadIdx.x];
+                cnt[w][threadIdx.x] = (uint16_t)run;
+                run += c;
+            }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kItems; ++i)
+            if (d[i] >= 0) {
+                const uint32_t to = cnt[warp][d[i]] + rank[i];
+                key[to] = k[i];
+                pos[to] = (uint16_t)v[i];
+            }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int32_t q = warp * 32 * kItems + i * 32 + lane;
+            k[i] = q < n ? key[q] : kNoKey;
+            v[i] = q < n ? pos[q] : 0;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const int32_t q = warp * 32 * kItems + i * 32 + lane;
+        if (q < n) out[q] = make_uint2(k[i], v[i]);
+    }
+    if (!n_out) return;
+    const int32_t p0 = (int32_t)threadIdx.x * kItems;  // run starts, 8 positions a thread
+    uint32_t prev = p0 > 0 && p0 - 1 < n ? key[p0 - 1] : kNoKey, mine = 0;
+    for (int q = 0; q < kItems; ++q) {
+        const uint32_t x = p0 + q < n ? key[p0 + q] : kNoKey;
+        mine += x < (uint32_t)n_rows && x != prev;
+        prev = x;
+    }
+    const uint32_t e = block_excl_scan<kSmallThreads, uint32_t>(mine, sh, total);
+    if (p0 < n && p0 % span == 0) starts[p0 / span] = (int32_t)e;
+    if (threadIdx.x == 0) {
+        starts[(n + span - 1) / span] = (int32_t)total;
+        *n_out = (int32_t)total;
+    }
+}
+constexpr int kSmallSmem = kSmallSort * 6 + (kSmallThreads / 32) * kDigits * 2;
 
 // ------------------------------------------------------- runs of equal IDs
-// Run starts of each chunk of the sorted list (IDs that take part only).
-__global__ void __launch_bounds__(kThreads) k_run_count(const uint32_t* __restrict__ keys, int64_t n_rows,
-                                                        int64_t n_cap, const int32_t* __restrict__ d_n,
-                                                        int32_t* __restrict__ starts, int64_t chunks) {
-    pdl_start();
-    const int64_t n = count_of(d_n, n_cap);
-    const int64_t c = blockIdx.x * (int64_t)(kThreads / 32) + (threadIdx.x >> 5);
-    if (c >= chunks) return;
-    const int64_t p = c * kChunk + (threadIdx.x & 31);
-    const bool start = p < n && keys[p] < (uint32_t)n_rows && (p == 0 || keys[p - 1] != keys[p]);
-    const unsigned b = __ballot_sync(0xFFFFFFFFu, start);
-    if ((threadIdx.x & 31) == 0) starts[c] = __popc(b);
-}
-
-// starts -> exclusive prefix; the total is the number of distinct IDs.
-__global__ void __launch_bounds__(kScanThreads) k_run_base(int32_t* __restrict__ starts, int64_t chunks,
-                                                           int32_t* __restrict__ n_out) {
-    pdl_start();
-    __shared__ int32_t sh[kScanThreads / 32 + 1];
-    int32_t base = 0;
-    for (int64_t i0 = 0; i0 < chunks; i0 += kScanThreads) {
-        const int64_t i = i0 + threadIdx.x;
-        int32_t total;
-        const int32_t e = block_excl_scan<kScanThreads, int32_t>(i < chunks ? starts[i] : 0, sh, total);
-        if (i < chunks) starts[i] = base + e;
-        base += total;
-    }
-    if (threadIdx.x == 0) *n_out = base;
-}
-
 template <typename TO>
 struct SumArgs {
-    const uint32_t* keys;   // sorted
-    const int32_t* vals;    // positions
+    const uint2* kv;  // sorted (ID, position)
     const int32_t* d_n;
     int64_t n_cap, n_rows;
     int64_t ld_g;
-    int32_t dim, units, col_blocks, lanes;  // lanes: of a warp, for one chunk's rows
+    int32_t dim, units, col_blocks, lanes;  // units of VEC columns; lanes that cover a column block
     int32_t mode;
     float scale;
-    const int32_t* starts;  // SG_GRAD_ROWS: distinct IDs before each chunk
+    const int32_t* starts;  // SG_GRAD_ROWS: distinct IDs before each tile
     int32_t* rows;
     TO* grad;
     int64_t ld_grad;
-    float* head;  // [chunks][dim] sums of runs that began in an earlier chunk
-    float* tail;  // [chunks][dim] sums of runs that go on in the next chunk
+    float* head;          // [tiles][dim] sums of runs that began in an earlier tile
+    float* tail;          // [tiles][dim] sums of runs that go on in the next tile
+    int32_t zero_blocks;  // SG_GRAD_DENSE: first blocks, which fill the rows without an ID
 };
 
 // Row of the gradient for the run of `key` (the j-th run).
@@ -326,87 +482,191 @@ __device__ __forceinline__ void put_row(const SumArgs<TO>& a, uint32_t key, int3
     store_vec<VEC>(p, v);
 }
 
-// Lanes of a warp in groups of a.lanes; each group sums one chunk's rows over
-// 32 / lanes... units of VEC columns (column block cb), run by run.
-template <typename TI, typename TO, int VEC>
+// Zero rows for the IDs that do not occur: a warp looks 32 IDs up in the
+// sorted list, a lane each.
+template <typename TO, int VEC>
+__device__ __forceinline__ void zero_rows(const SumArgs<TO>& a, int64_t n) {
+    const int lane = (int)lane_id();
+    const int64_t r0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * 32;
+    if (r0 >= a.n_rows) return;
+    const uint32_t id = (uint32_t)(r0 + lane);
+    int64_t lo = 0, hi = n;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (__ldg(&a.kv[mid].x) < id) lo = mid + 1;
+        else hi = mid;
+    }
+    const bool absent = (int64_t)id < a.n_rows && (lo >= n || __ldg(&a.kv[lo].x) != id);
+    const float none[VEC] = {};
+    for (unsigned todo = __ballot_sync(0xFFFFFFFFu, absent); todo; todo &= todo - 1) {
+        TO* p = a.grad + (r0 + __ffs(todo) - 1) * a.ld_grad;
+        for (int32_t u = lane; u < a.units; u += 32) store_vec<VEC>(p + (int64_t)u * VEC, none);
+    }
+}
+
+// A block takes a tile of the sorted list and a column block of a.lanes units;
+// a group of a.lanes lanes takes a chunk of CH positions of it.
+template <typename TI, typename TO, int VEC, int CH>
 __global__ void __launch_bounds__(kThreads) k_embed_sum(const TI* __restrict__ g, SumArgs<TO> a) {
     pdl_start();
+    constexpr int kMaxTile = CH == 32 ? 1024 : 2048;  // 32-long chunks go with 8 lanes or more
+    __shared__ uint2 kv[kMaxTile + 2];                // the tile's pairs, and one on either side
+    __shared__ __align__(16) float part[kThreads * VEC];  // the chunks' heads
+    __shared__ int32_t first[kThreads];
+    __shared__ int32_t sh[kThreads / 32 + 1];
     const int64_t n = count_of(a.d_n, a.n_cap);
-    const int64_t group = (blockIdx.x * (int64_t)kThreads + threadIdx.x) / a.lanes;
-    const int32_t lane = (int32_t)(threadIdx.x % (unsigned)a.lanes);
-    const int64_t c = group / a.col_blocks;
-    const int32_t unit = (int32_t)(group - c * a.col_blocks) * a.lanes + lane;
-    const int64_t p0 = c * kChunk;
-    if (p0 >= n || unit >= a.units) return;
-    const int32_t col = unit * VEC;
-    const int64_t p1 = p0 + kChunk < n ? p0 + kChunk : n;
+    if ((int32_t)blockIdx.x < a.zero_blocks) {
+        zero_rows<TO, VEC>(a, n);
+        return;
+    }
+    const int32_t block = (int32_t)blockIdx.x - a.zero_blocks;
+    const int32_t tile = block / a.col_blocks, cb = block - tile * a.col_blocks;
+    const int32_t chunks = kThreads / a.lanes, span = chunks * CH;
+    const int64_t p0 = (int64_t)tile * span;
+    if (p0 >= n) return;
+    for (int32_t i = threadIdx.x; i < span + 2; i += kThreads) {
+        const int64_t p = p0 - 1 + i;
+        kv[i] = p >= 0 && p < n ? a.kv[p] : make_uint2(kNoKey, 0);
+    }
+    __syncthreads();
+    const int32_t chunk = (int32_t)threadIdx.x / a.lanes, lane = (int32_t)threadIdx.x - chunk * a.lanes;
+    const int32_t unit = cb * a.lanes + lane, col = unit * VEC;
+    const bool active = unit < a.units;
+    const uint2* c = kv + 1 + chunk * CH;  // the chunk; c[-1], c[CH] are its neighbours
     const uint32_t none = (uint32_t)a.n_rows;
-    uint32_t key = a.keys[p0];
-    if (key == none) return;
-    bool head = p0 > 0 && a.keys[p0 - 1] == key;
-    int32_t j = a.mode == SG_GRAD_ROWS ? a.starts[c] - (head ? 1 : 0) : 0;
+    int32_t j = 0;
+    if (a.mode == SG_GRAD_ROWS) {  // distinct IDs before the chunk
+        int32_t starts = 0;
+        if (lane == 0)
+            for (int i = 0; i < CH; ++i) starts += c[i].x < none && c[i].x != c[i - 1].x;
+        int32_t total;
+        const int32_t e = block_excl_scan<kThreads, int32_t>(starts, sh, total);
+        if (lane == 0) first[chunk] = a.starts[tile] + e;
+        __syncthreads();
+        j = first[chunk];
+    }
     float acc[VEC];
 #pragma unroll
     for (int q = 0; q < VEC; ++q) acc[q] = 0.f;
-    bool last = false;
-    for (int64_t p = p0; p < p1 && !last; p += kUnroll) {
-        uint32_t k[kUnroll];
-        float v[kUnroll][VEC];
+    uint32_t key = c[0].x;
+    const bool any = key < none && active;
+    const bool enters = any && c[-1].x == key;  // the first run began before this chunk
+    bool head = enters;
+    if (head) --j;
+    float* my_head = &part[threadIdx.x * VEC];
+    if (any) {
+#pragma unroll 1
+        for (int b = 0; b < CH; b += kUnroll) {
+            if (c[b].x >= none) break;
+            float v[kUnroll][VEC];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            k[u] = p + u < p1 ? a.keys[p + u] : none;
-            if (k[u] != none) load_vec<VEC>(g + (int64_t)a.vals[p + u] * a.ld_g + col, v[u]);
-        }
+            for (int u = 0; u < kUnroll; ++u)
+                if (c[b + u].x < none) load_vec<VEC>(g + (int64_t)(int32_t)c[b + u].y * a.ld_g + col, v[u]);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            if (last) continue;
-            if (p + u >= p1 || k[u] == none) {
-                last = true;
-                continue;
+            for (int u = 0; u < kUnroll; ++u) {
+                const uint32_t k = c[b + u].x;
+                if (k >= none) continue;
+                if (k != key) {
+                    if (head) store_vec<VEC>(my_head, acc);
+                    else put_row<TO, VEC>(a, key, j, col, acc);
+                    head = false;
+                    ++j;
+                    key = k;
+#pragma unroll
+                    for (int q = 0; q < VEC; ++q) acc[q] = 0.f;
+                }
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) acc[q] += v[u][q];
             }
-            if (k[u] != key) {
-                if (head) store_vec<VEC>(a.head + c * a.dim + col, acc);
-                else put_row<TO, VEC>(a, key, j, col, acc);
-                head = false;
-                ++j;
-                key = k[u];
-#pragma unroll
-                for (int q = 0; q < VEC; ++q) acc[q] = 0.f;
-            }
-#pragma unroll
-            for (int q = 0; q < VEC; ++q) acc[q] += v[u][q];
         }
+        if (head) store_vec<VEC>(my_head, acc);
     }
-    if (head) store_vec<VEC>(a.head + c * a.dim + col, acc);
-    else if (p1 < n && a.keys[p1] == key) store_vec<VEC>(a.tail + c * a.dim + col, acc);
-    else put_row<TO, VEC>(a, key, j, col, acc);
+    const bool goes_on = any && !head && c[CH].x == key;  // the last run began here and goes on
+    if (any && !head && !goes_on) put_row<TO, VEC>(a, key, j, col, acc);
+    __syncthreads();
+    // joins within the tile: the chunk a run begins in adds the heads of the
+    // chunks it enters; chunk 0 does so for the run that enters the tile
+    const auto add_heads = [&](uint32_t id) {
+        int32_t d = chunk + 1;
+        for (; d < chunks && kv[1 + d * CH].x == id; ++d) {
+            const float* h = &part[(d * a.lanes + lane) * VEC];
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) acc[q] += h[q];
+        }
+        return d;
+    };
+    if (goes_on) {
+        const int32_t d = add_heads(key);
+        if (d == chunks && kv[1 + span].x == key) store_vec<VEC>(a.tail + (int64_t)tile * a.dim + col, acc);
+        else put_row<TO, VEC>(a, key, j, col, acc);
+    }
+    if (enters && chunk == 0) {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) acc[q] = my_head[q];
+        add_heads(c[0].x);
+        store_vec<VEC>(a.head + (int64_t)tile * a.dim + col, acc);
+    }
 }
 
-// Joins the runs that cross chunks: chunk c owns the run that begins in it
-// and goes on; the sum is tail[c] + head[c + 1] + ..., in this order.
+// Joins the runs that cross tiles: the tile a run begins in adds, in order,
+// its tail and the heads of the tiles the run enters.  A block looks at one
+// tile and column block; the heads of a long run are split over its warps.
 template <typename TO, int VEC>
-__global__ void __launch_bounds__(kThreads) k_embed_join(SumArgs<TO> a) {
+__global__ void __launch_bounds__(kThreads) k_embed_join(SumArgs<TO> a, int32_t span) {
     pdl_start();
+    constexpr int kWarps = kThreads / 32;
+    __shared__ __align__(16) float part[kWarps][32 * VEC];
+    __shared__ int32_t end_sh;
     const int64_t n = count_of(a.d_n, a.n_cap);
-    const int64_t group = (blockIdx.x * (int64_t)kThreads + threadIdx.x) / a.lanes;
-    const int32_t lane = (int32_t)(threadIdx.x % (unsigned)a.lanes);
-    const int64_t c = group / a.col_blocks;
-    const int32_t unit = (int32_t)(group - c * a.col_blocks) * a.lanes + lane;
-    const int64_t p0 = c * kChunk, p1 = p0 + kChunk;
-    if (p1 >= n || unit >= a.units) return;  // nothing after this chunk
-    const uint32_t key = a.keys[p1 - 1];
-    if (key == (uint32_t)a.n_rows || a.keys[p1] != key) return;
-    if (p0 > 0 && a.keys[p0] == key && a.keys[p0 - 1] == key) return;  // the run began earlier
-    const int32_t col = unit * VEC;
-    float acc[VEC];
-    load_vec<VEC>(a.tail + c * a.dim + col, acc);
-    for (int64_t d = c + 1; d * kChunk < n && a.keys[d * kChunk] == key; ++d) {
-        float v[VEC];
-        load_vec<VEC>(a.head + d * a.dim + col, v);
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) acc[q] += v[q];
+    const int32_t tile = (int32_t)(blockIdx.x / a.col_blocks), cb = (int32_t)blockIdx.x - tile * a.col_blocks;
+    const int64_t p0 = (int64_t)tile * span, p1 = p0 + span;
+    if (p1 >= n) return;  // nothing after this tile
+    const uint32_t key = a.kv[p1 - 1].x;
+    if (key >= (uint32_t)a.n_rows || a.kv[p1].x != key) return;
+    if (p0 > 0 && a.kv[p0].x == key && a.kv[p0 - 1].x == key) return;  // the run began earlier
+    const int warp = (int)(threadIdx.x >> 5), lane = (int)lane_id();
+    if (warp == 0) {
+        // last tile the run enters: 32 probes at a time
+        int64_t lo = tile + 1, hi = (n - 1) / span;  // tile lo is entered, tiles past hi do not exist
+        while (lo < hi) {
+            const int64_t step = (hi - lo + 31) / 32, t = lo + (lane + 1) * step;
+            const bool in = t <= hi && a.kv[t * span].x == key;
+            const int hits = __popc(__ballot_sync(0xFFFFFFFFu, in));  // a prefix of the lanes
+            lo += hits * step;
+            if (hits < 32) hi = lo + step - 1 < hi ? lo + step - 1 : hi;
+        }
+        if (lane == 0) end_sh = (int32_t)lo;
     }
-    put_row<TO, VEC>(a, key, a.mode == SG_GRAD_ROWS ? a.starts[c + 1] - 1 : 0, col, acc);
+    __syncthreads();
+    const int32_t count = end_sh - tile;  // heads to add, at least 1
+    const int32_t unit = cb * a.lanes + lane, col = unit * VEC;
+    const bool active = lane < a.lanes && unit < a.units;
+    const int32_t per = (count + kWarps - 1) / kWarps, t0 = tile + 1 + warp * per;
+    const int32_t t1 = min(t0 + per, tile + 1 + count);
+    float acc[VEC];
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) acc[q] = 0.f;
+    if (active) {
+        if (warp == 0) load_vec<VEC>(a.tail + (int64_t)tile * a.dim + col, acc);
+        for (int32_t t = t0; t < t1; t += kUnroll) {
+            float v[kUnroll][VEC];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (t + u < t1) load_vec<VEC>(a.head + (int64_t)(t + u) * a.dim + col, v[u]);
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (t + u < t1)
+#pragma unroll
+                    for (int q = 0; q < VEC; ++q) acc[q] += v[u][q];
+        }
+        store_vec<VEC>(&part[warp][lane * VEC], acc);
+    }
+    __syncthreads();
+    if (warp || !active) return;
+    for (int w = 1; w < kWarps; ++w)
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) acc[q] += part[w][lane * VEC + q];
+    put_row<TO, VEC>(a, key, a.mode == SG_GRAD_ROWS ? a.starts[tile + 1] - 1 : 0, col, acc);
 }
 
 // ------------------------------------------------------------------- host
@@ -451,53 +711,108 @@ sg_status run_fwd(int vec, const void* table, int64_t n_rows, int32_t dim, int64
     return launch_fwd<TI, TO, 1>(table, n_rows, dim, ld_table, ids, n_cap, d_n, scale, out, ld_out, s);
 }
 
+// Chunk length: 32 positions where that still leaves many chunks, else 8 (one
+// batch of loads), so that a short list spreads over the SMs.
+bool long_chunks(int64_t n_cap, int lanes) { return n_cap >= kLongChunks && lanes >= 8; }
+
 struct BwdLayout {
-    int64_t nb, chunks;
-    size_t keys0, keys1, vals0, vals1, hist, starts, head, tail, total;
+    int64_t tiles;       // bound on the sum's tiles (the narrowest tile: 32 lanes)
+    int64_t sort_tiles;  // bound on a pass's tiles
+    size_t kv0, kv1, state, status, run_status, starts, head, tail, clear, total;  // clear: bytes from state on
 };
 
 BwdLayout bwd_layout(int64_t n_cap, int32_t dim) {
     BwdLayout L;
-    L.nb = cdiv(n_cap, kSortTile);
-    L.chunks = cdiv(n_cap, kChunk);
+    L.tiles = cdiv(n_cap, n_cap >= kLongChunks ? 256 : 64);
+    L.sort_tiles = n_cap <= kSmallSort ? 0 : cdiv(n_cap, kThreads * 8);
     size_t o = 0;
     const auto put = [&o](size_t bytes) {
         const size_t at = o;
         o += a256(bytes);
         return at;
     };
-    L.keys0 = put((size_t)n_cap * 4);
-    L.keys1 = put((size_t)n_cap * 4);
-    L.vals0 = put((size_t)n_cap * 4);
-    L.vals1 = put((size_t)n_cap * 4);
-    L.hist = put((size_t)kDigits * L.nb * 4);
-    L.starts = put((size_t)(L.chunks + 1) * 4);
-    L.head = put((size_t)L.chunks * dim * 4);
-    L.tail = put((size_t)L.chunks * dim * 4);
+    L.kv0 = put((size_t)n_cap * 8);
+    L.kv1 = put((size_t)n_cap * 8);
+    L.state = put(sizeof(SortState));
+    L.run_status = put((size_t)cdiv(n_cap, kRunTile) * 8);
+    L.status = put((size_t)L.sort_tiles * kDigits * kMaxPasses * 4);
+    L.clear = o - L.state;
+    L.starts = put((size_t)(L.tiles + 2) * 4);
+    L.head = put((size_t)L.tiles * dim * 4);
+    L.tail = put((size_t)L.tiles * dim * 4);
     L.total = o;
     return L;
 }
 
 template <typename TI, typename TO, int VEC>
-sg_status launch_sum(const void* g, SumArgs<TO> a, cudaStream_t s) {
-    a.units = a.dim / VEC;
-    a.lanes = 1;
-    while (a.lanes < 32 && a.lanes < a.units) a.lanes *= 2;
-    a.col_blocks = (int32_t)cdiv(a.units, a.lanes);
-    const int64_t threads = cdiv(a.n_cap, kChunk) * a.col_blocks * a.lanes;
-    const int64_t blocks = cdiv(threads, kThreads);
-    if (blocks > 2147483647LL) return fail(SG_ERR_INVALID_ARG, "sg_embed_bwd: n_cap x dim too large");
-    SG_CUDA(launch_pdl(k_embed_sum<TI, TO, VEC>, dim3((unsigned)blocks), dim3(kThreads), 0, s, (const TI*)g, a));
-    SG_CUDA(launch_pdl(k_embed_join<TO, VEC>, dim3((unsigned)blocks), dim3(kThreads), 0, s, a));
+sg_status launch_sum(const void* g, SumArgs<TO> a, int32_t span, cudaStream_t s) {
+    const int64_t tiles = cdiv(a.n_cap, span), blocks = tiles * a.col_blocks;
+    const int64_t zero = a.mode == SG_GRAD_DENSE ? cdiv(a.n_rows, kThreads) : 0;
+    if (blocks + zero > 2147483647LL) return fail(SG_ERR_INVALID_ARG, "sg_embed_bwd: n_cap x dim too large");
+    a.zero_blocks = (int32_t)zero;
+    if (span * a.lanes == kThreads * 32)
+        SG_CUDA(launch_pdl(k_embed_sum<TI, TO, VEC, 32>, dim3((unsigned)(blocks + zero)), dim3(kThreads), 0, s,
+                           (const TI*)g, a));
+    else
+        SG_CUDA(launch_pdl(k_embed_sum<TI, TO, VEC, 8>, dim3((unsigned)(blocks + zero)), dim3(kThreads), 0, s,
+                           (const TI*)g, a));
+    if (tiles > 1)
+        SG_CUDA(launch_pdl(k_embed_join<TO, VEC>, dim3((unsigned)blocks), dim3(kThreads), 0, s, a, span));
     return SG_OK;
 }
 
 template <typename TI, typename TO>
-sg_status run_sum(int vec, const void* g, SumArgs<TO> a, cudaStream_t s) {
+sg_status run_sum(int vec, const void* g, const SumArgs<TO>& a, int32_t span, cudaStream_t s) {
     if constexpr (sizeof(TI) == 2)
-        if (vec == 8) return launch_sum<TI, TO, 8>(g, a, s);
-    if (vec == 4) return launch_sum<TI, TO, 4>(g, a, s);
-    return launch_sum<TI, TO, 1>(g, a, s);
+        if (vec == 8) return launch_sum<TI, TO, 8>(g, a, span, s);
+    if (vec == 4) return launch_sum<TI, TO, 4>(g, a, span, s);
+    return launch_sum<TI, TO, 1>(g, a, span, s);
+}
+
+// Sorted pairs in kv[*cur]; with rows, the distinct IDs before each tile of
+// `span` positions in starts.
+sg_status run_sort(const int32_t* ids, int64_t n_cap, const int32_t* d_n, int64_t n_rows, bool rows, int32_t span,
+                   int32_t* n_out, const BwdLayout& L, char* ws, uint2** sorted, cudaStream_t s) {
+    uint2* kv[2] = {(uint2*)(ws + L.kv0), (uint2*)(ws + L.kv1)};
+    SortState* st = (SortState*)(ws + L.state);
+    int32_t* starts = (int32_t*)(ws + L.starts);
+    int bits = 1;
+    while (bits < 32 && (n_rows >> bits) != 0) ++bits;  // keys 0 .. n_rows
+    Digits dg;
+    dg.passes = (bits + 7) / 8;
+    dg.per = (bits + dg.passes - 1) / dg.passes;
+    *sorted = kv[0];
+    if (n_cap <= kSmallSort) {
+        static bool set = false;
+        if (!set) {
+            SG_CUDA(cudaFuncSetAttribute(k_sort_small, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem));
+            set = true;
+        }
+        SG_CUDA(launch_pdl(k_sort_small, dim3(1), dim3(kSmallThreads), kSmallSmem, s, ids, n_rows, (int32_t)n_cap, d_n,
+                           dg, span, kv[0], starts, rows ? n_out : nullptr));
+        return SG_OK;
+    }
+    SG_CUDA(cudaMemsetAsync(ws + L.state, 0, L.clear, s));
+    const int64_t hb = cdiv(n_cap, kThreads * 8) < num_sms() * 2 ? cdiv(n_cap, kThreads * 8) : num_sms() * 2;
+    SG_CUDA(launch_pdl(k_sort_hist, dim3((unsigned)hb), dim3(kThreads), 0, s, ids, n_rows, n_cap, d_n, dg, st));
+    // 16 items a thread once that still gives every SM a tile
+    const bool big = n_cap >= (int64_t)num_sms() * kThreads * 16;
+    for (int p = 0; p < dg.passes; ++p) {
+        uint32_t* status = (uint32_t*)(ws + L.status) + (int64_t)p * L.sort_tiles * kDigits;
+        const uint2* in = p ? kv[(p & 1) ^ 1] : nullptr;
+        uint2* out = kv[p & 1];
+        if (big)
+            SG_CUDA(launch_pdl(k_sort_pass<16>, dim3((unsigned)cdiv(n_cap, kThreads * 16)), dim3(kThreads), 0, s, ids, in,
+                               n_rows, n_cap, d_n, p, (int)dg.per, st, status, out));
+        else
+            SG_CUDA(launch_pdl(k_sort_pass<8>, dim3((unsigned)cdiv(n_cap, kThreads * 8)), dim3(kThreads), 0, s, ids, in,
+                               n_rows, n_cap, d_n, p, (int)dg.per, st, status, out));
+        *sorted = out;
+    }
+    if (rows)
+        SG_CUDA(launch_pdl(k_runs, dim3((unsigned)cdiv(n_cap, kRunTile)), dim3(kThreads), 0, s, (const uint2*)*sorted,
+                           n_rows, n_cap, d_n, span, st, (unsigned long long*)(ws + L.run_status), starts, n_out));
+    return SG_OK;
 }
 
 template <typename TO>
@@ -505,36 +820,18 @@ sg_status run_bwd(const int32_t* ids, int64_t n_cap, const int32_t* d_n, int64_t
                   int32_t dim, int64_t ld_g, float scale, int32_t mode, int32_t* rows, int32_t* n_out, TO* grad,
                   int32_t dtype_grad, int64_t ld_grad, char* ws, cudaStream_t s) {
     const BwdLayout L = bwd_layout(n_cap, dim);
-    uint32_t* keys[2] = {(uint32_t*)(ws + L.keys0), (uint32_t*)(ws + L.keys1)};
-    int32_t* vals[2] = {(int32_t*)(ws + L.vals0), (int32_t*)(ws + L.vals1)};
-    uint32_t* hist = (uint32_t*)(ws + L.hist);
-    int bits = 1;
-    while (bits < 32 && (n_rows >> bits) != 0) ++bits;  // keys 0 .. n_rows
-    const int passes = (bits + 7) / 8, per = (bits + passes - 1) / passes;
-    int cur = 0;
-    for (int p = 0; p < passes; ++p) {
-        const uint32_t* ki = p ? keys[cur] : nullptr;
-        const int32_t* vi = p ? vals[cur] : nullptr;
-        const int shift = p * per, mask = (1 << per) - 1;
-        SG_CUDA(launch_pdl(k_sort_hist, dim3((unsigned)L.nb), dim3(kThreads), 0, s, ki, ids, n_rows, n_cap, d_n, shift,
-                           mask, hist, L.nb));
-        SG_CUDA(launch_pdl(k_sort_scan, dim3(1), dim3(kScanThreads), 0, s, hist, (int64_t)kDigits * L.nb));
-        SG_CUDA(launch_pdl(k_sort_scatter, dim3((unsigned)L.nb), dim3(kThreads), 0, s, ki, vi, ids, n_rows, n_cap, d_n,
-                           shift, mask, (const uint32_t*)hist, L.nb, keys[cur ^ 1], vals[cur ^ 1]));
-        cur ^= 1;
-    }
-    int32_t* starts = (int32_t*)(ws + L.starts);
-    if (mode == SG_GRAD_ROWS) {
-        SG_CUDA(launch_pdl(k_run_count, dim3((unsigned)cdiv(L.chunks + 1, kThreads / 32)), dim3(kThreads), 0, s,
-                           (const uint32_t*)keys[cur], n_rows, n_cap, d_n, starts, L.chunks + 1));
-        SG_CUDA(launch_pdl(k_run_base, dim3(1), dim3(kScanThreads), 0, s, starts, L.chunks + 1, n_out));
-    } else if (mode == SG_GRAD_DENSE) {
-        SG_CUDA(cudaMemset2DAsync(grad, (size_t)ld_grad * sizeof(TO), 0, (size_t)dim * sizeof(TO), (size_t)n_rows, s));
-    }
+    const int vec = vec_for(g, dtype_g, ld_g, grad, dtype_grad, ld_grad, dim);
     SumArgs<TO> a;
     memset(&a, 0, sizeof(a));
-    a.keys = keys[cur];
-    a.vals = vals[cur];
+    a.units = dim / vec;
+    a.lanes = 1;
+    while (a.lanes < 32 && a.lanes < a.units) a.lanes *= 2;
+    a.col_blocks = (int32_t)cdiv(a.units, a.lanes);
+    const int32_t span = kThreads / a.lanes * (long_chunks(n_cap, a.lanes) ? 32 : 8);
+    uint2* sorted = nullptr;
+    const sg_status st = run_sort(ids, n_cap, d_n, n_rows, mode == SG_GRAD_ROWS, span, n_out, L, ws, &sorted, s);
+    if (st != SG_OK) return st;
+    a.kv = sorted;
     a.d_n = d_n;
     a.n_cap = n_cap;
     a.n_rows = n_rows;
@@ -542,14 +839,13 @@ sg_status run_bwd(const int32_t* ids, int64_t n_cap, const int32_t* d_n, int64_t
     a.dim = dim;
     a.mode = mode;
     a.scale = scale;
-    a.starts = starts;
+    a.starts = (const int32_t*)(ws + L.starts);
     a.rows = rows;
     a.grad = grad;
     a.ld_grad = ld_grad;
     a.head = (float*)(ws + L.head);
     a.tail = (float*)(ws + L.tail);
-    const int vec = vec_for(g, dtype_g, ld_g, grad, dtype_grad, ld_grad, dim);
-    return dtype_g == SG_F32 ? run_sum<float, TO>(vec, g, a, s) : run_sum<__nv_bfloat16, TO>(vec, g, a, s);
+    return dtype_g == SG_F32 ? run_sum<float, TO>(vec, g, a, span, s) : run_sum<__nv_bfloat16, TO>(vec, g, a, span, s);
 }
 
 }  // namespace
@@ -576,7 +872,7 @@ extern "C" sg_status sg_embed_fwd(const void* d_table, int32_t dtype_table, int6
 }
 
 extern "C" size_t sg_embed_bwd_workspace(int64_t n_cap, int64_t n_rows, int32_t dim, int32_t mode) {
-    if (n_cap <= 0 || n_cap > 2147483647LL || n_rows <= 0 || n_rows > 2147483647LL || dim <= 0 || mode < SG_GRAD_ROWS ||
+    if (n_cap <= 0 || n_cap >= (1LL << 30) || n_rows <= 0 || n_rows > 2147483647LL || dim <= 0 || mode < SG_GRAD_ROWS ||
         mode > SG_GRAD_ADD)
         return 0;
     return bwd_layout(n_cap, dim).total;
@@ -588,7 +884,7 @@ extern "C" sg_status sg_embed_bwd(const int32_t* d_ids, int64_t n_cap, const int
                                   int64_t ld_grad, void* d_workspace, size_t workspace_bytes, sg_stream_t stream) {
     if (!dtype_ok(dtype_g) || !dtype_ok(dtype_grad)) return fail(SG_ERR_UNSUPPORTED, "sg_embed_bwd: dtype");
     if (mode < SG_GRAD_ROWS || mode > SG_GRAD_ADD) return fail(SG_ERR_INVALID_ARG, "sg_embed_bwd: mode");
-    if (n_cap < 0 || n_cap > 2147483647LL || n_rows <= 0 || n_rows > 2147483647LL || dim <= 0)
+    if (n_cap < 0 || n_cap >= (1LL << 30) || n_rows <= 0 || n_rows > 2147483647LL || dim <= 0)
         return fail(SG_ERR_INVALID_ARG, "sg_embed_bwd: bad sizes");
     if (ld_g < dim || ld_grad < dim) return fail(SG_ERR_INVALID_ARG, "sg_embed_bwd: a row stride is below dim");
     if (mode == SG_GRAD_ROWS && (!d_rows || !d_n_rows))
