@@ -84,6 +84,29 @@ __device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&v)[VEC]
         for (int q = 0; q < VEC; ++q) v[q] = __bfloat162float(p[q]);
     }
 }
+// VEC elements as they were loaded (16 bytes at most), unpacked when used.
+template <typename T, int VEC>
+struct Raw {
+    uint32_t w[(VEC * sizeof(T) + 3) / 4];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (VEC * sizeof(T) == 16) {
+            const uint4 t = __ldg(reinterpret_cast<const uint4*>(p));
+            w[0] = t.x, w[1] = t.y, w[2] = t.z, w[3] = t.w;
+        } else if constexpr (VEC * sizeof(T) == 8) {
+            const uint2 t = __ldg(reinterpret_cast<const uint2*>(p));
+            w[0] = t.x, w[1] = t.y;
+        } else if constexpr (sizeof(T) == 4) {
+            w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+        } else {
+            w[0] = (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p)) << 16;
+        }
+    }
+    __device__ __forceinline__ float operator[](int q) const {
+        if constexpr (sizeof(T) == 4 || VEC == 1) return __uint_as_float(w[q]);
+        else return __uint_as_float(q & 1 ? w[q / 2] & 0xFFFF0000u : w[q / 2] << 16);
+    }
+};
+
 template <int VEC>
 __device__ __forceinline__ void store_vec(float* p, const float (&v)[VEC]) {
     if constexpr (VEC % 4 == 0) {
@@ -204,8 +227,12 @@ __global__ void __launch_bounds__(kThreads) k_sort_hist(const int32_t* __restric
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            if (k[u] != kNoKey)
-                for (int p = 0; p < dg.passes; ++p) atomicAdd(&h[p][(k[u] >> (p * dg.per)) & mask], 1u);
+            for (int p = 0; p < dg.passes; ++p) {
+                // the lanes of one digit add together: power-law IDs share their high digits
+                const uint32_t d = k[u] != kNoKey ? (k[u] >> (p * dg.per)) & mask : kNoKey;
+                const unsigned peers = __match_any_sync(0xFFFFFFFFu, d);
+                if (d != kNoKey && (peers & lanemask_lt()) == 0) atomicAdd(&h[p][d], (uint32_t)__popc(peers));
+            }
     }
     __syncthreads();
     for (int p = 0; p < dg.passes; ++p)
@@ -288,14 +315,28 @@ __global__ void __launch_bounds__(kThreads) k_sort_pass(const int32_t* __restric
         st_relaxed(word, (2u << 30) | mine);
     } else {
         st_relaxed(word, (1u << 30) | mine);
-        bool late = false;
-        for (const uint32_t* w = word - kDigits;; w -= kDigits) {
-            uint32_t v = ld_relaxed(w);
-            for (int spins = 0; (v >> 30) == 0 && spins < kLookbackSpins; ++spins) v = ld_relaxed(w);
-            late |= (v >> 30) == 0;
-            before += v & 0x3FFFFFFFu;
-            if ((v >> 30) != 1) break;  // inclusive, or given up
+        // kBack tiles' words at a time: most tiles of one wave are still at
+        // flag 1, so a walk one by one would cost a memory latency a tile
+        constexpr int kBack = 16;
+        int64_t t = (int64_t)tile - 1;  // next tile to add
+        bool done = false;
+        int spins = 0;
+        while (!done && spins < kLookbackSpins) {
+            uint32_t v[kBack];
+#pragma unroll
+            for (int u = 0; u < kBack; ++u) v[u] = t - u >= 0 ? ld_relaxed(word - (tile - t + u) * kDigits) : 2u << 30;
+#pragma unroll
+            for (int u = 0; u < kBack; ++u) {
+                if (done || (v[u] >> 30) == 0) {  // not there yet: ask again from here
+                    ++spins;
+                    break;
+                }
+                before += v[u] & 0x3FFFFFFFu;
+                done = (v[u] >> 30) == 2;
+                --t;
+            }
         }
+        const bool late = !done;
         if (late) dev_err(ERR_TIMEOUT);
         st_relaxed(word, (2u << 30) | (before + mine));
     }
@@ -316,7 +357,7 @@ __global__ void __launch_bounds__(kThreads) k_sort_pass(const int32_t* __restric
 }
 
 // starts[p / span] = distinct IDs before sorted position p, for every p that
-// is a multiple of span (a power of two of at least 16) up to the end of the
+// is a multiple of span (a power of two of at least 32) up to the end of the
 // list; the number of distinct IDs follows at the end.
 __global__ void __launch_bounds__(kThreads) k_runs(const uint2* __restrict__ kv, int64_t n_rows, int64_t n_cap,
                                                    const int32_t* __restrict__ d_n, int32_t span,
@@ -328,21 +369,29 @@ __global__ void __launch_bounds__(kThreads) k_runs(const uint2* __restrict__ kv,
     if (threadIdx.x == 0) tile_sh = (int32_t)atomicAdd(&st->ticket[kMaxPasses], 1u);
     __syncthreads();
     const int32_t tile = tile_sh;
-    const int64_t n = count_of(d_n, n_cap), p0 = (int64_t)tile * kRunTile + threadIdx.x * 16;
+    const int warp = (int)(threadIdx.x >> 5), lane = (int)lane_id();
+    const int64_t n = count_of(d_n, n_cap), p0 = (int64_t)tile * kRunTile + warp * 512;  // a warp's 16 x 32 positions
     if ((int64_t)tile * kRunTile >= n) {
         if (tile == 0 && threadIdx.x == 0) *n_out = 0;
         return;
     }
-    uint32_t prev = p0 > 0 && p0 - 1 < n ? kv[p0 - 1].x : kNoKey;
-    int32_t mine = 0;
+    uint32_t k[16];
 #pragma unroll
     for (int q = 0; q < 16; ++q) {
-        const uint32_t k = p0 + q < n ? kv[p0 + q].x : kNoKey;
-        mine += k < (uint32_t)n_rows && k != prev;
-        prev = k;
+        const int64_t p = p0 + q * 32 + lane;
+        k[q] = p < n ? kv[p].x : kNoKey;
+    }
+    uint32_t last = p0 > 0 && p0 - 1 < n ? kv[p0 - 1].x : kNoKey;
+    int32_t before[16], mine = 0;  // run starts of the warp before round q
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+        const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, k[q], 1), prev = lane ? up : last;
+        before[q] = mine;
+        mine += __popc(__ballot_sync(0xFFFFFFFFu, k[q] < (uint32_t)n_rows && k[q] != prev));
+        last = __shfl_sync(0xFFFFFFFFu, k[q], 31);
     }
     int32_t total;
-    const int32_t e = block_excl_scan<kThreads, int32_t>(mine, sh, total);
+    const int32_t e = block_excl_scan<kThreads, int32_t>(lane == 0 ? mine : 0, sh, total);  // lane 0: the warps before
     if (threadIdx.x < 32) {
         bool late = false;
         const int32_t x = chain_lookback(status, tile, 0, total, &late);
@@ -350,7 +399,13 @@ __global__ void __launch_bounds__(kThreads) k_runs(const uint2* __restrict__ kv,
         if (threadIdx.x == 0) before_sh = x;
     }
     __syncthreads();
-    if (p0 < n && p0 % span == 0) starts[p0 / span] = before_sh + e;
+    if (lane == 0) {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+            const int64_t p = p0 + q * 32;
+            if (p < n && p % span == 0) starts[p / span] = before_sh + e + before[q];
+        }
+    }
     if (threadIdx.x == 0 && (int64_t)(tile + 1) * kRunTile >= n) {
         starts[(n + span - 1) / span] = before_sh + total;
         *n_out = before_sh + total;
@@ -454,7 +509,7 @@ struct SumArgs {
     int64_t ld_grad;
     float* head;          // [tiles][dim] sums of runs that began in an earlier tile
     float* tail;          // [tiles][dim] sums of runs that go on in the next tile
-    int32_t zero_blocks;  // SG_GRAD_DENSE: first blocks, which fill the rows without an ID
+    int32_t zero_blocks;  // SG_GRAD_DENSE: blocks that fill the rows without an ID
 };
 
 // Row of the gradient for the run of `key` (the j-th run).
@@ -485,9 +540,9 @@ __device__ __forceinline__ void put_row(const SumArgs<TO>& a, uint32_t key, int3
 // Zero rows for the IDs that do not occur: a warp looks 32 IDs up in the
 // sorted list, a lane each.
 template <typename TO, int VEC>
-__device__ __forceinline__ void zero_rows(const SumArgs<TO>& a, int64_t n) {
+__device__ __forceinline__ void zero_rows(const SumArgs<TO>& a, int64_t n, int32_t block) {
     const int lane = (int)lane_id();
-    const int64_t r0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * 32;
+    const int64_t r0 = ((int64_t)block * (kThreads / 32) + (threadIdx.x >> 5)) * 32;
     if (r0 >= a.n_rows) return;
     const uint32_t id = (uint32_t)(r0 + lane);
     int64_t lo = 0, hi = n;
@@ -515,11 +570,16 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(const TI* __restrict__ g
     __shared__ int32_t first[kThreads];
     __shared__ int32_t sh[kThreads / 32 + 1];
     const int64_t n = count_of(a.d_n, a.n_cap);
-    if ((int32_t)blockIdx.x < a.zero_blocks) {
-        zero_rows<TO, VEC>(a, n);
-        return;
+    int32_t block = (int32_t)blockIdx.x;
+    if (a.zero_blocks) {
+        // zero blocks are spread evenly over the grid: their look-ups are latency, the sums bandwidth
+        const int32_t z = (int32_t)(((int64_t)block * a.zero_blocks) / gridDim.x);
+        if ((int32_t)(((int64_t)(block + 1) * a.zero_blocks) / gridDim.x) != z) {
+            zero_rows<TO, VEC>(a, n, z);
+            return;
+        }
+        block -= z;
     }
-    const int32_t block = (int32_t)blockIdx.x - a.zero_blocks;
     const int32_t tile = block / a.col_blocks, cb = block - tile * a.col_blocks;
     const int32_t chunks = kThreads / a.lanes, span = chunks * CH;
     const int64_t p0 = (int64_t)tile * span;
@@ -558,10 +618,10 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(const TI* __restrict__ g
 #pragma unroll 1
         for (int b = 0; b < CH; b += kUnroll) {
             if (c[b].x >= none) break;
-            float v[kUnroll][VEC];
+            Raw<TI, VEC> v[kUnroll];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u)
-                if (c[b + u].x < none) load_vec<VEC>(g + (int64_t)(int32_t)c[b + u].y * a.ld_g + col, v[u]);
+                if (c[b + u].x < none) v[u].load(g + (int64_t)(int32_t)c[b + u].y * a.ld_g + col);
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 const uint32_t k = c[b + u].x;
@@ -609,64 +669,92 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(const TI* __restrict__ g
 }
 
 // Joins the runs that cross tiles: the tile a run begins in adds, in order,
-// its tail and the heads of the tiles the run enters.  A block looks at one
-// tile and column block; the heads of a long run are split over its warps.
+// its tail and the heads of the tiles the run enters.  A warp looks at one
+// tile and column block and joins a short run itself; a run of more than
+// kUnroll heads is split over the block's warps, whose sums are then added in
+// order.
 template <typename TO, int VEC>
-__global__ void __launch_bounds__(kThreads) k_embed_join(SumArgs<TO> a, int32_t span) {
+__global__ void __launch_bounds__(kThreads) k_embed_join(SumArgs<TO> a, int32_t span, int64_t items) {
     pdl_start();
     constexpr int kWarps = kThreads / 32;
     __shared__ __align__(16) float part[kWarps][32 * VEC];
-    __shared__ int32_t end_sh;
+    __shared__ int32_t heads[kWarps];  // of the run that begins in the warp's tile
     const int64_t n = count_of(a.d_n, a.n_cap);
-    const int32_t tile = (int32_t)(blockIdx.x / a.col_blocks), cb = (int32_t)blockIdx.x - tile * a.col_blocks;
-    const int64_t p0 = (int64_t)tile * span, p1 = p0 + span;
-    if (p1 >= n) return;  // nothing after this tile
-    const uint32_t key = a.kv[p1 - 1].x;
-    if (key >= (uint32_t)a.n_rows || a.kv[p1].x != key) return;
-    if (p0 > 0 && a.kv[p0].x == key && a.kv[p0 - 1].x == key) return;  // the run began earlier
     const int warp = (int)(threadIdx.x >> 5), lane = (int)lane_id();
-    if (warp == 0) {
-        // last tile the run enters: 32 probes at a time
-        int64_t lo = tile + 1, hi = (n - 1) / span;  // tile lo is entered, tiles past hi do not exist
-        while (lo < hi) {
-            const int64_t step = (hi - lo + 31) / 32, t = lo + (lane + 1) * step;
-            const bool in = t <= hi && a.kv[t * span].x == key;
-            const int hits = __popc(__ballot_sync(0xFFFFFFFFu, in));  // a prefix of the lanes
-            lo += hits * step;
-            if (hits < 32) hi = lo + step - 1 < hi ? lo + step - 1 : hi;
-        }
-        if (lane == 0) end_sh = (int32_t)lo;
-    }
-    __syncthreads();
-    const int32_t count = end_sh - tile;  // heads to add, at least 1
-    const int32_t unit = cb * a.lanes + lane, col = unit * VEC;
-    const bool active = lane < a.lanes && unit < a.units;
-    const int32_t per = (count + kWarps - 1) / kWarps, t0 = tile + 1 + warp * per;
-    const int32_t t1 = min(t0 + per, tile + 1 + count);
-    float acc[VEC];
-#pragma unroll
-    for (int q = 0; q < VEC; ++q) acc[q] = 0.f;
-    if (active) {
-        if (warp == 0) load_vec<VEC>(a.tail + (int64_t)tile * a.dim + col, acc);
-        for (int32_t t = t0; t < t1; t += kUnroll) {
+    const int64_t item0 = (int64_t)blockIdx.x * kWarps;
+    // the key whose run begins in tile t and goes on, or kNoKey
+    const auto owned = [&](int64_t t) {
+        const int64_t p0 = t * span, p1 = p0 + span;
+        if (p1 >= n) return kNoKey;
+        const uint32_t k0 = p0 > 0 ? a.kv[p0 - 1].x : kNoKey, k1 = a.kv[p0].x, k2 = a.kv[p1 - 1].x, k3 = a.kv[p1].x;
+        if (k2 >= (uint32_t)a.n_rows || k3 != k2 || (k1 == k2 && k0 == k2)) return kNoKey;
+        return k2;
+    };
+    const auto add = [&](float (&acc)[VEC], int64_t t0, int64_t t1, int32_t col) {
+        for (int64_t t = t0; t < t1; t += kUnroll) {
             float v[kUnroll][VEC];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u)
-                if (t + u < t1) load_vec<VEC>(a.head + (int64_t)(t + u) * a.dim + col, v[u]);
+                if (t + u < t1) load_vec<VEC>(a.head + (t + u) * a.dim + col, v[u]);
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u)
                 if (t + u < t1)
 #pragma unroll
                     for (int q = 0; q < VEC; ++q) acc[q] += v[u][q];
         }
-        store_vec<VEC>(&part[warp][lane * VEC], acc);
+    };
+    {
+        const int64_t item = item0 + warp, tile = item / a.col_blocks;
+        const uint32_t key = item < items ? owned(tile) : kNoKey;
+        int32_t count = 0;
+        if (key != kNoKey) {  // the same in the whole warp
+            // last tile the run enters: 32 probes at a time
+            int64_t lo = tile + 1, hi = (n - 1) / span;  // tile lo is entered, tiles past hi do not exist
+            while (lo < hi) {
+                const int64_t step = (hi - lo + 31) / 32, t = lo + (lane + 1) * step;
+                const bool in = t <= hi && a.kv[t * span].x == key;
+                const int hits = __popc(__ballot_sync(0xFFFFFFFFu, in));  // a prefix of the lanes
+                lo += hits * step;
+                if (hits < 32) hi = lo + step - 1 < hi ? lo + step - 1 : hi;
+            }
+            count = (int32_t)(lo - tile);
+            const int32_t unit = (int32_t)(item - tile * a.col_blocks) * a.lanes + lane, col = unit * VEC;
+            if (count <= kUnroll && lane < a.lanes && unit < a.units) {
+                float acc[VEC];
+                load_vec<VEC>(a.tail + tile * a.dim + col, acc);
+                add(acc, tile + 1, tile + 1 + count, col);
+                put_row<TO, VEC>(a, key, a.mode == SG_GRAD_ROWS ? a.starts[tile + 1] - 1 : 0, col, acc);
+            }
+        }
+        if (lane == 0) heads[warp] = count;
     }
     __syncthreads();
-    if (warp || !active) return;
-    for (int w = 1; w < kWarps; ++w)
+#pragma unroll 1
+    for (int w = 0; w < kWarps; ++w) {
+        const int32_t count = heads[w];
+        if (count <= kUnroll) continue;
+        const int64_t item = item0 + w, tile = item / a.col_blocks;
+        const int32_t unit = (int32_t)(item - tile * a.col_blocks) * a.lanes + lane, col = unit * VEC;
+        const bool active = lane < a.lanes && unit < a.units;
+        const int64_t per = (count + kWarps - 1) / kWarps, t0 = min((int64_t)count, warp * per), t1 = min((int64_t)count, t0 + per);
+        float acc[VEC];
 #pragma unroll
-        for (int q = 0; q < VEC; ++q) acc[q] += part[w][lane * VEC + q];
-    put_row<TO, VEC>(a, key, a.mode == SG_GRAD_ROWS ? a.starts[tile + 1] - 1 : 0, col, acc);
+        for (int q = 0; q < VEC; ++q) acc[q] = 0.f;
+        if (active) {
+            if (warp == 0) load_vec<VEC>(a.tail + tile * a.dim + col, acc);
+            add(acc, tile + 1 + t0, tile + 1 + t1, col);
+            store_vec<VEC>(&part[warp][lane * VEC], acc);
+        }
+        __syncthreads();
+        if (warp == 0 && active) {
+            for (int i = 1; i < kWarps; ++i)
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) acc[q] += part[i][lane * VEC + q];
+            const uint32_t key = a.kv[(tile + 1) * span].x;
+            put_row<TO, VEC>(a, key, a.mode == SG_GRAD_ROWS ? a.starts[tile + 1] - 1 : 0, col, acc);
+        }
+        __syncthreads();
+    }
 }
 
 // ------------------------------------------------------------------- host
@@ -757,7 +845,8 @@ sg_status launch_sum(const void* g, SumArgs<TO> a, int32_t span, cudaStream_t s)
         SG_CUDA(launch_pdl(k_embed_sum<TI, TO, VEC, 8>, dim3((unsigned)(blocks + zero)), dim3(kThreads), 0, s,
                            (const TI*)g, a));
     if (tiles > 1)
-        SG_CUDA(launch_pdl(k_embed_join<TO, VEC>, dim3((unsigned)blocks), dim3(kThreads), 0, s, a, span));
+        SG_CUDA(launch_pdl(k_embed_join<TO, VEC>, dim3((unsigned)cdiv(blocks, kThreads / 32)), dim3(kThreads), 0, s, a,
+                           span, blocks));
     return SG_OK;
 }
 

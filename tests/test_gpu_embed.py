@@ -174,7 +174,8 @@ def _check_bwd(got, ids, n_rows, g, scale, mode, to, base=None):
     (1000, 33, 3000, "distinct", "f32", "f32"), (777, 130, 65535, "power", "f32", "f32"),
     (20000, 256, 65536, "power", "f32", "f32"), (3000, 1024, 40, "power", "bf16", "bf16"),
     (70001, 8, 9, "same", "f32", "f32"), (70001, 12, 2, "sorted", "bf16", "f32"), (500, 20, 300, "none", "f32", "f32"),
-    (40000, 32, 1, "same", "f32", "f32")])
+    (40000, 32, 1, "same", "f32", "f32"), (66000, 64, 500, "power", "f32", "f32"),
+    (700001, 4, 3000, "power", "f32", "f32"), (650000, 40, 2, "same", "bf16", "f32")])
 def test_gradient(n, dim, n_rows, kind, tg, to, mode):
     rng = np.random.default_rng(n * 7 + dim)
     ids = _ids(rng, n, n_rows, kind)
