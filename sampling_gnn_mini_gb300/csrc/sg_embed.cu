@@ -35,6 +35,8 @@ constexpr int kThreads = 256;
 constexpr int kUnroll = 8;
 constexpr int kDigits = 256;
 constexpr int kMaxPasses = 4;
+constexpr int kCopies = 8;            // of the digit counts: blocks add to them in turn (one copy's atomics cost 10 us)
+constexpr int kSortThreads = 512;     // of a pass
 constexpr int kSmallSort = 8192;      // positions sorted by one block
 constexpr int kSmallThreads = 1024;
 constexpr int kRunTile = kThreads * 16;   // sorted positions a block of k_runs looks at
@@ -187,9 +189,10 @@ __global__ void __launch_bounds__(kThreads) k_embed_fwd(const TI* __restrict__ t
 }
 
 // ------------------------------------------------------------------- sort
-// Key of position i: its ID, or n_rows (sorted last) for one that takes no part.
-__device__ __forceinline__ uint32_t key_of(const int32_t* __restrict__ ids, int64_t i, int64_t n_rows) {
-    const int32_t g = __ldg(ids + i);
+// Key of an ID: itself, or n_rows (sorted last) for one that takes no part.
+// (Taken from loaded IDs, so that a thread's loads are all issued before the
+// first is looked at.)
+__device__ __forceinline__ uint32_t key_of(int32_t g, int64_t n_rows) {
     if (g < 0 || (int64_t)g >= n_rows) {
         if (g != -1) dev_err(ERR_INDEX);
         return (uint32_t)n_rows;
@@ -204,9 +207,23 @@ struct Digits {
 
 // Device state of the multi-block sort; cleared before every use.
 struct SortState {
-    uint32_t hist[kMaxPasses][kDigits];
+    uint32_t hist[kCopies][kMaxPasses][kDigits];
     uint32_t ticket[kMaxPasses + 1];  // tiles handed out (the last: of k_runs)
 };
+
+// The lanes of `valid` whose digit (below 256) is this lane's: one ballot a
+// bit.  (match_any takes a turn for each distinct digit of the warp: measured
+// 1,235 cycles for 16 items of few digits and 6,000 of many.)
+__device__ __forceinline__ unsigned digit_peers(int32_t d, unsigned valid) {
+    unsigned peers = valid;
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+        const bool bit = (d >> b) & 1;
+        const unsigned with = __ballot_sync(0xFFFFFFFFu, bit);
+        peers &= bit ? with : ~with;
+    }
+    return peers;
+}
 
 // Digit counts of all passes.
 __global__ void __launch_bounds__(kThreads) k_sort_hist(const int32_t* __restrict__ ids, int64_t n_rows, int64_t n_cap,
@@ -218,25 +235,23 @@ __global__ void __launch_bounds__(kThreads) k_sort_hist(const int32_t* __restric
     __syncthreads();
     const int64_t n = count_of(d_n, n_cap), stride = (int64_t)gridDim.x * kThreads;
     const uint32_t mask = (1u << dg.per) - 1;
-    for (int64_t i0 = blockIdx.x * (int64_t)kThreads; i0 < n; i0 += 4 * stride) {
-        uint32_t k[4];
+    for (int64_t i0 = blockIdx.x * (int64_t)kThreads; i0 < n; i0 += 8 * stride) {
+        int32_t g[8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 8; ++u) {
             const int64_t i = i0 + u * stride + threadIdx.x;
-            k[u] = i < n ? key_of(ids, i, n_rows) : kNoKey;
+            g[u] = i < n ? __ldg(ids + i) : -2;
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            for (int p = 0; p < dg.passes; ++p) {
-                // the lanes of one digit add together: power-law IDs share their high digits
-                const uint32_t d = k[u] != kNoKey ? (k[u] >> (p * dg.per)) & mask : kNoKey;
-                const unsigned peers = __match_any_sync(0xFFFFFFFFu, d);
-                if (d != kNoKey && (peers & lanemask_lt()) == 0) atomicAdd(&h[p][d], (uint32_t)__popc(peers));
-            }
+        for (int u = 0; u < 8; ++u) {
+            if (i0 + u * stride + threadIdx.x >= n) continue;
+            const uint32_t k = key_of(g[u], n_rows);
+            for (int p = 0; p < dg.passes; ++p) atomicAdd(&h[p][(k >> (p * dg.per)) & mask], 1u);
+        }
     }
     __syncthreads();
     for (int p = 0; p < dg.passes; ++p)
-        if (h[p][threadIdx.x]) atomicAdd(&st->hist[p][threadIdx.x], h[p][threadIdx.x]);
+        if (h[p][threadIdx.x]) atomicAdd(&st->hist[blockIdx.x % kCopies][p][threadIdx.x], h[p][threadIdx.x]);
 }
 
 // Ranks a warp's items (item i of lane l before item i of lane l + 1 and
@@ -246,16 +261,16 @@ __global__ void __launch_bounds__(kThreads) k_sort_hist(const int32_t* __restric
 template <int ITEMS, typename C>
 __device__ __forceinline__ void warp_rank(const int32_t (&d)[ITEMS], C* cnt, uint32_t (&rank)[ITEMS]) {
 #pragma unroll
+    for (int i = 0; i < ITEMS; ++i) rank[i] = digit_peers(d[i], __ballot_sync(0xFFFFFFFFu, d[i] >= 0));
+#pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-        const unsigned peers = __match_any_sync(0xFFFFFFFFu, d[i]);
-        uint32_t old = 0;
-        const int leader = __ffs(peers) - 1;
-        if ((int)lane_id() == leader && d[i] >= 0) {
-            old = cnt[d[i]];
-            cnt[d[i]] = (C)(old + __popc(peers));
-        }
+        const unsigned peers = rank[i];
+        const uint32_t before = __popc(peers & lanemask_lt());
+        const uint32_t old = d[i] >= 0 ? cnt[d[i]] : 0;  // all lanes of a digit read the same count
         __syncwarp();
-        rank[i] = __shfl_sync(0xFFFFFFFFu, old, leader) + __popc(peers & lanemask_lt());
+        if (d[i] >= 0 && before == 0) cnt[d[i]] = (C)(old + __popc(peers));
+        __syncwarp();
+        rank[i] = old + before;
     }
 }
 
@@ -273,79 +288,90 @@ __device__ __forceinline__ void st_relaxed(uint32_t* p, uint32_t v) {
 // the tile's own count, 2 the count up to and including the tile.  Tiles are
 // handed out in order, so every tile looked at is running or done.
 template <int ITEMS>
-__global__ void __launch_bounds__(kThreads) k_sort_pass(const int32_t* __restrict__ ids, const uint2* __restrict__ in,
+__global__ void __launch_bounds__(kSortThreads, 2) k_sort_pass(const int32_t* __restrict__ ids, const uint2* __restrict__ in,
                                                         int64_t n_rows, int64_t n_cap, const int32_t* __restrict__ d_n,
                                                         int pass, int per, SortState* __restrict__ st,
                                                         uint32_t* __restrict__ status, uint2* __restrict__ out) {
     pdl_start();
-    constexpr int kWarps = kThreads / 32, kTile = kThreads * ITEMS;
+    constexpr int kWarps = kSortThreads / 32, kTile = kSortThreads * ITEMS;
     __shared__ uint32_t cnt[kWarps][kDigits];
     __shared__ uint32_t sh[kWarps + 1];
     __shared__ uint32_t tile_sh;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool digit = threadIdx.x < kDigits;  // threads that look after a digit
     if (threadIdx.x == 0) tile_sh = atomicAdd(&st->ticket[pass], 1u);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) cnt[w][threadIdx.x] = 0;
+    for (int i = threadIdx.x; i < kWarps * kDigits; i += kSortThreads) (&cnt[0][0])[i] = 0;
     __syncthreads();
     const uint32_t tile = tile_sh;
     const int64_t n = count_of(d_n, n_cap), i0 = (int64_t)tile * kTile + warp * 32 * ITEMS + lane;
     if ((int64_t)tile * kTile >= n) return;  // no later tile has items either
+    uint32_t count = 0;
+    if (digit)
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c) count += st->hist[c][pass][threadIdx.x];
     uint2 kv[ITEMS];
     int32_t d[ITEMS];
     uint32_t rank[ITEMS];
+    if (in) {
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-        const int64_t p = i0 + i * 32;
-        d[i] = -1;
-        if (p < n) {
-            kv[i] = in ? in[p] : make_uint2(key_of(ids, p, n_rows), (uint32_t)p);
-            d[i] = (int32_t)((kv[i].x >> (pass * per)) & ((1u << per) - 1));
-        }
+        for (int i = 0; i < ITEMS; ++i)
+            kv[i] = i0 + i * 32 < n ? in[i0 + i * 32] : make_uint2(0, 0);
+    } else {
+        int32_t g[ITEMS];
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) g[i] = i0 + i * 32 < n ? __ldg(ids + i0 + i * 32) : -1;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) kv[i] = make_uint2(key_of(g[i], n_rows), (uint32_t)(i0 + i * 32));
     }
     uint32_t total;
-    const uint32_t base = block_excl_scan<kThreads, uint32_t>(st->hist[pass][threadIdx.x], sh, total);
+    const uint32_t base = block_excl_scan<kSortThreads, uint32_t>(count, sh, total);
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+        d[i] = i0 + i * 32 < n ? (int32_t)((kv[i].x >> (pass * per)) & ((1u << per) - 1)) : -1;
     warp_rank<ITEMS>(d, cnt[warp], rank);
     __syncthreads();
-    uint32_t mine = 0;
+    if (digit) {
+        uint32_t mine = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) mine += cnt[w][threadIdx.x];
-    uint32_t* word = status + (int64_t)tile * kDigits + threadIdx.x;
-    uint32_t before = 0;
-    if (tile == 0) {
-        st_relaxed(word, (2u << 30) | mine);
-    } else {
-        st_relaxed(word, (1u << 30) | mine);
-        // kBack tiles' words at a time: most tiles of one wave are still at
-        // flag 1, so a walk one by one would cost a memory latency a tile
-        constexpr int kBack = 16;
-        int64_t t = (int64_t)tile - 1;  // next tile to add
-        bool done = false;
-        int spins = 0;
-        while (!done && spins < kLookbackSpins) {
-            uint32_t v[kBack];
+        for (int w = 0; w < kWarps; ++w) mine += cnt[w][threadIdx.x];
+        uint32_t* word = status + (int64_t)tile * kDigits + threadIdx.x;
+        uint32_t before = 0;
+        if (tile == 0) {
+            st_relaxed(word, (2u << 30) | mine);
+        } else {
+            st_relaxed(word, (1u << 30) | mine);
+            // kBack tiles' words at a time: most tiles of one wave are still at
+            // flag 1, so a walk one by one would cost a memory latency a tile
+            constexpr int kBack = 16;
+            int64_t t = (int64_t)tile - 1;  // next tile to add
+            bool done = false;
+            int spins = 0;
+            while (!done && spins < kLookbackSpins) {
+                uint32_t v[kBack];
 #pragma unroll
-            for (int u = 0; u < kBack; ++u) v[u] = t - u >= 0 ? ld_relaxed(word - (tile - t + u) * kDigits) : 2u << 30;
+                for (int u = 0; u < kBack; ++u) v[u] = t - u >= 0 ? ld_relaxed(word - (tile - t + u) * kDigits) : 2u << 30;
 #pragma unroll
-            for (int u = 0; u < kBack; ++u) {
-                if (done || (v[u] >> 30) == 0) {  // not there yet: ask again from here
-                    ++spins;
-                    break;
+                for (int u = 0; u < kBack; ++u) {
+                    if (done || (v[u] >> 30) == 0) {  // not there yet: ask again from here
+                        ++spins;
+                        break;
+                    }
+                    before += v[u] & 0x3FFFFFFFu;
+                    done = (v[u] >> 30) == 2;
+                    --t;
                 }
-                before += v[u] & 0x3FFFFFFFu;
-                done = (v[u] >> 30) == 2;
-                --t;
             }
+            const bool late = !done;
+            if (late) dev_err(ERR_TIMEOUT);
+            st_relaxed(word, (2u << 30) | (before + mine));
         }
-        const bool late = !done;
-        if (late) dev_err(ERR_TIMEOUT);
-        st_relaxed(word, (2u << 30) | (before + mine));
-    }
-    uint32_t run = base + before;
+        uint32_t run = base + before;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        const uint32_t c = cnt[w][threadIdx.x];
-        cnt[w][threadIdx.x] = run;
-        run += c;
+        for (int w = 0; w < kWarps; ++w) {
+            const uint32_t c = cnt[w][threadIdx.x];
+            cnt[w][threadIdx.x] = run;
+            run += c;
+        }
     }
     __syncthreads();
 #pragma unroll
@@ -431,10 +457,11 @@ __global__ void __launch_bounds__(kSmallThreads) k_sort_small(const int32_t* __r
     int32_t d[kItems];
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-        const int32_t p = warp * 32 * kItems + i * 32 + lane;
-        k[i] = p < n ? key_of(ids, p, n_rows) : kNoKey;
-        v[i] = (uint32_t)p;
+        v[i] = (uint32_t)(warp * 32 * kItems + i * 32 + lane);
+        d[i] = (int32_t)v[i] < n ? __ldg(ids + v[i]) : -1;
     }
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) k[i] = (int32_t)v[i] < n ? key_of(d[i], n_rows) : kNoKey;
     for (int p = 0; p < dg.passes; ++p) {
         uint32_t* zero = reinterpret_cast<uint32_t*>(&cnt[warp][0]);
 #pragma unroll
@@ -812,7 +839,7 @@ struct BwdLayout {
 BwdLayout bwd_layout(int64_t n_cap, int32_t dim) {
     BwdLayout L;
     L.tiles = cdiv(n_cap, n_cap >= kLongChunks ? 256 : 64);
-    L.sort_tiles = n_cap <= kSmallSort ? 0 : cdiv(n_cap, kThreads * 8);
+    L.sort_tiles = n_cap <= kSmallSort ? 0 : cdiv(n_cap, kSortThreads * 4);
     size_t o = 0;
     const auto put = [&o](size_t bytes) {
         const size_t at = o;
@@ -884,17 +911,17 @@ sg_status run_sort(const int32_t* ids, int64_t n_cap, const int32_t* d_n, int64_
     SG_CUDA(cudaMemsetAsync(ws + L.state, 0, L.clear, s));
     const int64_t hb = cdiv(n_cap, kThreads * 8) < num_sms() * 2 ? cdiv(n_cap, kThreads * 8) : num_sms() * 2;
     SG_CUDA(launch_pdl(k_sort_hist, dim3((unsigned)hb), dim3(kThreads), 0, s, ids, n_rows, n_cap, d_n, dg, st));
-    // 16 items a thread once that still gives every SM a tile
-    const bool big = n_cap >= (int64_t)num_sms() * kThreads * 16;
+    // 8 items a thread once that still gives every SM a tile
+    const bool big = n_cap >= (int64_t)num_sms() * kSortThreads * 8;
     for (int p = 0; p < dg.passes; ++p) {
         uint32_t* status = (uint32_t*)(ws + L.status) + (int64_t)p * L.sort_tiles * kDigits;
         const uint2* in = p ? kv[(p & 1) ^ 1] : nullptr;
         uint2* out = kv[p & 1];
         if (big)
-            SG_CUDA(launch_pdl(k_sort_pass<16>, dim3((unsigned)cdiv(n_cap, kThreads * 16)), dim3(kThreads), 0, s, ids, in,
+            SG_CUDA(launch_pdl(k_sort_pass<8>, dim3((unsigned)cdiv(n_cap, kSortThreads * 8)), dim3(kSortThreads), 0, s, ids, in,
                                n_rows, n_cap, d_n, p, (int)dg.per, st, status, out));
         else
-            SG_CUDA(launch_pdl(k_sort_pass<8>, dim3((unsigned)cdiv(n_cap, kThreads * 8)), dim3(kThreads), 0, s, ids, in,
+            SG_CUDA(launch_pdl(k_sort_pass<4>, dim3((unsigned)cdiv(n_cap, kSortThreads * 4)), dim3(kSortThreads), 0, s, ids, in,
                                n_rows, n_cap, d_n, p, (int)dg.per, st, status, out));
         *sorted = out;
     }
