@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kThreads) k_ns_norm(Source<T> src, int32_t row
     pdl_start();
     __shared__ double sh[kThreads / 32];
     const int64_t q = blockIdx.y, total = (int64_t)rows * cols;
-    double sum = 0.0;
+    float sq = 0.f;
     for (int64_t t = blockIdx.x * (int64_t)kThreads + threadIdx.x; t < total; t += (int64_t)gridDim.x * kThreads) {
         const int64_t r = t / cols, c = t - r * cols;
         float u = to_f(src.g[(q * rows + r) * src.ld + c]);
@@ -85,9 +85,9 @@ __global__ void __launch_bounds__(kThreads) k_ns_norm(Source<T> src, int32_t row
             src.mom_out[q * total + t] = m;
             u = src.nesterov ? u + src.mu * m : m;
         }
-        sum += (double)u * (double)u;
+        sq += u * u;
     }
-    sum = warp_sum(sum);
+    double sum = warp_sum((double)sq);
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -505,6 +505,299 @@ __global__ void __launch_bounds__(kThreads) k_ns_store(Planes X, int64_t ldx, in
     }
 }
 
+// ------------------------------------------- m <= 128: one launch, on the chip
+// A cluster of S CTAs holds one matrix for the whole call: CTA r keeps columns
+// [r W, r W + W) of X in shared memory as fp16 pairs, in the swizzled layout
+// that serves both as K-major rows (A = X X^T) and as an MN-major operand
+// (X <- B X).  A step is
+//   each CTA's partial X X^T (K = W), left in its shared memory as fp32;
+//   CTA r adds columns [128 r / S, ..) of all parts in rank order and sends
+//   its columns of A, as pairs, to every CTA;
+//   every CTA forms B = a I + b A + c A A and X <- B X for its own columns.
+// No iterate goes to memory: the call reads its input and writes the result.  The time is a chain of latencies: two cluster barriers, three
+// 128-deep products and four passes over tensor memory a step.
+constexpr int kFusedM = 128;
+constexpr int kFusedMaxCtas = 16;
+constexpr int kPairTile = kFusedM * 128;  // bytes of a 128 x 64 fp16 tile
+
+template <int W>
+constexpr int kFusedSmem = 2 * (W / 64) * kPairTile + 4 * kPairTile + kFusedM * kFusedM * 4 + 1024;
+
+// Address of 8 elements (columns 8 c ..) of row r of a [128 x 64 t] swizzled
+// operand.
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    return (uint32_t)((c >> 3) * kPairTile + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ void split8(const float (&v)[8], uint4& hi, uint4& lo) {
+    __half h[8], l[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) split(v[q], h[q], l[q]);
+    hi = make_uint4(pack(h[0], h[1]), pack(h[2], h[3]), pack(h[4], h[5]), pack(h[6], h[7]));
+    lo = make_uint4(pack(l[0], l[1]), pack(l[2], l[3]), pack(l[4], l[5]), pack(l[6], l[7]));
+}
+
+struct Steps {
+    float coef[SG_MAX_NS_STEPS][3];
+    int32_t count;
+};
+
+template <int W, typename TS, typename TW>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_ns_fused(Source<TS> src, int32_t rows, int32_t cols, Steps steps, float eps, FinalArgs fin) {
+    extern __shared__ uint8_t dsm[];
+    __shared__ __align__(8) uint64_t done;
+    __shared__ uint32_t tmem_base;
+    __shared__ double norm[kFusedMaxCtas];
+    __shared__ double red[kThreads / 32];
+    constexpr int kXTiles = W / 64, kChunks = kFusedM * W / 8 / kThreads;  // 16-byte chunks of X a thread handles
+    pdl_start();
+    const int warp = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31);
+    const uint32_t rank = cluster_rank();
+    uint32_t S;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(S));
+    const int64_t q = blockIdx.y;
+    const bool tall = rows > cols;
+    const int32_t m = tall ? cols : rows, n = tall ? rows : cols, j0 = (int32_t)rank * W;
+    uint8_t* base = dsm + ((1024 - (smem_addr(dsm) & 1023)) & 1023);
+    uint8_t* xs = base;                          // X: hi tiles, then lo tiles
+    uint8_t* as = xs + 2 * kXTiles * kPairTile;  // A, then B: hi tiles (2), lo tiles (2)
+    float* dump = reinterpret_cast<float*>(as + 4 * kPairTile);  // [column / 4][row][4]
+    constexpr uint32_t kXLo = kXTiles * kPairTile, kALo = 2 * kPairTile;
+    if (threadIdx.x == 0) {
+        mbar_init(&done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (warp == 1) tmem_alloc<128>(&tmem_base);
+
+    // U of this CTA's columns, in registers; the new momentum on the way
+    float u[kChunks][8];
+    float sq = 0.f;
+#pragma unroll
+    for (int it = 0; it < kChunks; ++it) {
+        const int e = it * kThreads + (int)threadIdx.x;
+        // consecutive threads take consecutive addresses: columns of a row, or
+        // (tall: X is the transpose) rows of X
+        const int i = tall ? e % kFusedM : e / (W / 8), c = tall ? e / kFusedM : e % (W / 8);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int32_t j = j0 + c * 8 + k;
+            const int64_t r = tall ? j : i, cc = tall ? i : j;
+            float v = 0.f;
+            if (i < m && j < n) {
+                v = to_f(src.g[(q * rows + r) * src.ld + cc]);
+                if (src.mom_out) v = src.mu * src.mom[(q * rows + r) * cols + cc] + v;
+            }
+            u[it][k] = v;
+        }
+    }
+#pragma unroll
+    for (int it = 0; it < kChunks; ++it) {
+        const int e = it * kThreads + (int)threadIdx.x;
+        const int i = tall ? e % kFusedM : e / (W / 8), c = tall ? e / kFusedM : e % (W / 8);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int32_t j = j0 + c * 8 + k;
+            if (src.mom_out && i < m && j < n) {
+                const int64_t r = tall ? j : i, cc = tall ? i : j;
+                src.mom_out[(q * rows + r) * cols + cc] = u[it][k];
+                if (src.nesterov) u[it][k] = to_f(src.g[(q * rows + r) * src.ld + cc]) + src.mu * u[it][k];
+            }
+            sq += u[it][k] * u[it][k];
+        }
+    }
+    {
+        const double s = warp_sum((double)sq);
+        if (lane == 0) red[warp] = s;
+    }
+    tmem_fence_before();
+    cluster_sync();  // every CTA runs (and red, done and tmem_base are set)
+    tmem_fence_after();
+    const uint32_t tmem = tmem_base;
+    if (threadIdx.x < S) {
+        double s = 0.0;
+        for (int w = 0; w < kThreads / 32; ++w) s += red[w];
+        asm volatile("st.shared::cluster.f64 [%0], %1;\n" ::"r"(map_rank(smem_addr(norm + rank), threadIdx.x)), "d"(s)
+                     : "memory");
+    }
+    cluster_sync();
+    {
+        double s = 0.0;
+        for (uint32_t r = 0; r < S; ++r) s += norm[r];
+        const float mul = kScale / ((float)sqrt(s) + eps);
+#pragma unroll
+        for (int it = 0; it < kChunks; ++it) {
+            const int e = it * kThreads + (int)threadIdx.x;
+            const int i = tall ? e % kFusedM : e / (W / 8), c = tall ? e / kFusedM : e % (W / 8);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u[it][k] *= mul;
+            uint4 hi, lo;
+            split8(u[it], hi, lo);
+            *reinterpret_cast<uint4*>(xs + chunk_at(i, c)) = hi;
+            *reinterpret_cast<uint4*>(xs + kXLo + chunk_at(i, c)) = lo;
+        }
+    }
+    const uint32_t xa = smem_addr(xs), aa = smem_addr(as), da = smem_addr(dump);
+    const int row = (warp & 3) * 32 + lane;  // of tensor memory, in every pass over it
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    uint32_t phase = 0;
+    // runs `issue` on one thread once all shared memory is written, and waits for it
+    const auto product = [&](auto issue) {
+        tmem_fence_before();
+        fence_async();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            tmem_fence_after();
+            fence_async();
+            issue();
+            mma_commit(&done);
+        }
+        __syncwarp();
+        if (!mbar_wait(&done, phase) && lane == 0) dev_err(ERR_TIMEOUT);
+        phase ^= 1u;
+        tmem_fence_after();
+    };
+    // hi hi + hi lo + lo hi over K steps of 16; a and b give a step's descriptors
+    const auto pairs = [&](int ksteps, uint32_t idesc, auto a, auto b) {
+        for (int k = 0; k < ksteps; ++k) {
+            mma_issue(tmem, a(k, 0), b(k, 0), idesc, (uint32_t)(k != 0), false);
+            mma_issue(tmem, a(k, 0), b(k, 1), idesc, 1u, false);
+            mma_issue(tmem, a(k, 1), b(k, 0), idesc, 1u, false);
+        }
+    };
+    const auto x_rows = [&](int k, int lo) {
+        return smem_desc_sw128(xa + (lo ? kXLo : 0) + (uint32_t)((k >> 2) * kPairTile + (k & 3) * 32));
+    };
+    const auto a_rows = [&](int k, int lo) {
+        return smem_desc_sw128(aa + (lo ? kALo : 0) + (uint32_t)((k >> 2) * kPairTile + (k & 3) * 32));
+    };
+    const auto x_cols = [&](int k, int lo) {
+        return smem_desc_mn_sw128(xa + (lo ? kXLo : 0) + (uint32_t)(k * 16 * 128), kPairTile);
+    };
+#pragma unroll 1
+    for (int step = 0; step < steps.count; ++step) {
+        // partial A = X X^T
+        product([&] { pairs(W / 16, desc_f16(false, kFusedM), x_rows, x_rows); });
+#pragma unroll 1
+        for (int c0 = (warp >> 2) * 64; c0 < (warp >> 2) * 64 + 64; c0 += 32) {
+            float v[32];
+            tmem_load_32(tmem + lanes + (uint32_t)c0, v);
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+                *reinterpret_cast<float4*>(dump + ((c0 / 4 + t) * kFusedM + row) * 4) =
+                    make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]);
+        }
+        cluster_sync();
+        // this CTA's columns of A, 8 at a time, to every CTA
+        const int per = kFusedM / (int)S;  // columns of a CTA: 8 or more
+        for (int t = (int)threadIdx.x; t < kFusedM * per / 8; t += kThreads) {
+            const int r = t % kFusedM, c = ((int)rank * per) / 8 + t / kFusedM;
+            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+            for (uint32_t s = 0; s < S; ++s) {
+                const uint32_t at = map_rank(da, s) + (uint32_t)(((c * 2) * kFusedM + r) * 16);
+                const float4 x = ld_cluster4(at), y = ld_cluster4(at + kFusedM * 16);
+                v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+                v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] *= 1.f / kScale;
+            uint4 hi, lo;
+            split8(v, hi, lo);
+            for (uint32_t s = 0; s < S; ++s) {
+                const uint32_t to = map_rank(aa, s) + chunk_at(r, c);
+                st_cluster4(to, hi);
+                st_cluster4(to + kALo, lo);
+            }
+        }
+        fence_async();
+        cluster_sync();
+        // B = a I + b A + c A A, in A's place
+        product([&] { pairs(kFusedM / 16, desc_f16(false, kFusedM), a_rows, a_rows); });
+        const float ca = steps.coef[step][0] * kScale, cb = steps.coef[step][1], cc = steps.coef[step][2] * (1.f / kScale);
+#pragma unroll 1
+        for (int c0 = (warp >> 2) * 64; c0 < (warp >> 2) * 64 + 64; c0 += 32) {
+            float v[32];
+            tmem_load_32(tmem + lanes + (uint32_t)c0, v);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                uint4* ph = reinterpret_cast<uint4*>(as + chunk_at(row, c0 / 8 + t));
+                uint4* pl = reinterpret_cast<uint4*>(as + kALo + chunk_at(row, c0 / 8 + t));
+                const uint4 h4 = *ph, l4 = *pl;
+                const __half2* h2 = reinterpret_cast<const __half2*>(&h4);
+                const __half2* l2 = reinterpret_cast<const __half2*>(&l4);
+                float b[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 h = __half22float2(h2[k]), l = __half22float2(l2[k]);
+                    b[2 * k] = cc * v[8 * t + 2 * k] + cb * (h.x + l.x);
+                    b[2 * k + 1] = cc * v[8 * t + 2 * k + 1] + cb * (h.y + l.y);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) b[k] += row == c0 + 8 * t + k ? ca : 0.f;
+                uint4 hi, lo;
+                split8(b, hi, lo);
+                *ph = hi;
+                *pl = lo;
+            }
+        }
+        // X <- B X
+        product([&] { pairs(kFusedM / 16, desc_f16(true, W), a_rows, x_cols); });
+        if (step + 1 < steps.count) {
+#pragma unroll 1
+            for (int c0 = (warp >> 2) * (W / 2); c0 < (warp >> 2) * (W / 2) + W / 2; c0 += 32) {
+                float v[32];
+                tmem_load_32(tmem + lanes + (uint32_t)c0, v);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    float x[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[k] = v[8 * t + k] * (1.f / kScale);
+                    uint4 hi, lo;
+                    split8(x, hi, lo);
+                    *reinterpret_cast<uint4*>(xs + chunk_at(row, c0 / 8 + t)) = hi;
+                    *reinterpret_cast<uint4*>(xs + kXLo + chunk_at(row, c0 / 8 + t)) = lo;
+                }
+            }
+        }
+    }
+    // out = keep w + step X, through shared memory so that rows go out whole
+    float* tile = dump;  // [row][W + 1], or [column][129] when tall: A's place is free too
+    if constexpr (W == 128) tile = reinterpret_cast<float*>(as);
+    const int ld_row = tall ? 1 : W + 1, ld_col = tall ? kFusedM + 1 : 1;
+#pragma unroll 1
+    for (int c0 = (warp >> 2) * (W / 2); c0 < (warp >> 2) * (W / 2) + W / 2; c0 += 32) {
+        float v[32];
+        tmem_load_32(tmem + lanes + (uint32_t)c0, v);
+#pragma unroll
+        for (int t = 0; t < 32; ++t) tile[row * ld_row + (c0 + t) * ld_col] = v[t];
+    }
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_free<128>(tmem);
+    const float mul = fin.step * (1.f / (kScale * kScale));
+    const TW* w = (const TW*)fin.w;
+    TW* o = (TW*)fin.out;
+    const int32_t wn = min(W, n - j0);  // columns of X here
+    if (tall) {
+        for (int c = warp; c < wn; c += kThreads / 32) {
+            const int64_t at = (q * n + j0 + c) * fin.ld_out;
+            for (int r = lane; r < m; r += 32) {
+                const float x = mul * tile[r + c * (kFusedM + 1)];
+                put(o + at + r, w ? fin.keep * to_f(w[at + r]) + x : x);
+            }
+        }
+    } else {
+        for (int r = warp; r < m; r += kThreads / 32) {
+            const int64_t at = (q * m + r) * fin.ld_out + j0;
+            for (int c = lane; c < wn; c += 32) {
+                const float x = mul * tile[r * (W + 1) + c];
+                put(o + at + c, w ? fin.keep * to_f(w[at + c]) + x : x);
+            }
+        }
+    }
+}
+
 // -------------------------------------------------------------------- host
 size_t a256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -620,11 +913,54 @@ sg_status launch_apply(const ApplyMaps& maps, int32_t count, int32_t m, int32_t 
 
 const float kCoef[3] = {3.4445f, -4.7750f, 2.0315f};
 
+// The fused form: W columns a CTA, `ctas` of them (2, 4, 8 or 16, or 1).
+template <int W, typename TS, typename TW>
+sg_status launch_fused(const Source<TS>& src, int32_t count, int32_t rows, int32_t cols, int ctas, const Steps& steps,
+                       float eps, const FinalArgs& fin, cudaStream_t s) {
+    static bool set = false;
+    if (!set) {
+        SG_CUDA(cudaFuncSetAttribute(k_ns_fused<W, TS, TW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFusedSmem<W>));
+        SG_CUDA(cudaFuncSetAttribute(k_ns_fused<W, TS, TW>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+        set = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)count);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kFusedSmem<W>;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)ctas;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    SG_CUDA(cudaLaunchKernelEx(&cfg, k_ns_fused<W, TS, TW>, src, rows, cols, steps, eps, fin));
+    return SG_OK;
+}
+
 template <typename TS, typename TW>
 sg_status run(Source<TS> src, int32_t count, int32_t rows, int32_t cols, int32_t steps, const float* coef, float eps,
               const TW* w, float keep, float step, TW* out, int64_t ld_out, char* ws, cudaStream_t s) {
     const Layout L = layout(count, rows, cols);
     const int32_t m = (int32_t)L.m, n = (int32_t)L.n;
+    const FinalArgs fin = {w, out, keep, step, ld_out, rows > cols ? 1 : 0};
+    // a matrix that the shared memory of one cluster holds is done in one
+    // launch; 64 columns a CTA while 16 CTAs reach, since each product and each
+    // pass over tensor memory is then half as long
+    if (m <= kFusedM && n <= kFusedMaxCtas * 128 && steps > 0) {
+        Steps st;
+        st.count = steps;
+        for (int32_t k = 0; k < SG_MAX_NS_STEPS; ++k)
+            for (int i = 0; i < 3; ++i) st.coef[k][i] = k < steps ? (coef ? coef[3 * k + i] : kCoef[i]) : 0.f;
+        const int width = n <= kFusedMaxCtas * 64 ? 64 : 128;
+        int ctas = 1;
+        while (ctas * width < n) ctas *= 2;
+        return width == 64 ? launch_fused<64, TS, TW>(src, count, rows, cols, ctas, st, eps, fin, s)
+                           : launch_fused<128, TS, TW>(src, count, rows, cols, ctas, st, eps, fin, s);
+    }
     Planes x[2], a, b;
     for (int i = 0; i < 2; ++i) x[i] = {(__half*)(ws + L.x[i][0]), (__half*)(ws + L.x[i][1])};
     a = {(__half*)(ws + L.a[0]), (__half*)(ws + L.a[1])};
@@ -633,7 +969,6 @@ sg_status run(Source<TS> src, int32_t count, int32_t rows, int32_t cols, int32_t
     SG_CUDA(launch_pdl(k_ns_norm<TS>, dim3(kNormBlocks, (unsigned)count), dim3(kThreads), 0, s, src, rows, cols, part));
     SG_CUDA(launch_pdl(k_ns_split<TS>, dim3((unsigned)cdiv(cols, 32), (unsigned)cdiv(rows, 32), (unsigned)count),
                        dim3(kThreads), 0, s, src, rows, cols, (const double*)part, eps, x[0], L.ldx));
-    FinalArgs fin = {w, out, keep, step, ld_out, rows > cols ? 1 : 0};
     if (steps == 0) {
         const int64_t eb = cdiv((int64_t)rows * cols, kThreads) < 1024 ? cdiv((int64_t)rows * cols, kThreads) : 1024;
         SG_CUDA(launch_pdl(k_ns_store<TW>, dim3((unsigned)eb, (unsigned)count), dim3(kThreads), 0, s, x[0], L.ldx, rows,
