@@ -66,6 +66,7 @@ struct Source {
     float* mom_out;
     float mu;
     int32_t nesterov;
+    int32_t vec;  // 1: g, 2: the momentum may be read 16 bytes at a time
 };
 
 // ------------------------------------------------------------ norm and split
@@ -511,8 +512,8 @@ __global__ void __launch_bounds__(kThreads) k_ns_store(Planes X, int64_t ldx, in
 // that serves both as K-major rows (A = X X^T) and as an MN-major operand
 // (X <- B X).  A step is
 //   each CTA's partial X X^T (K = W), left in its shared memory as fp32;
-//   CTA r adds columns [128 r / S, ..) of all parts in rank order and sends
-//   its columns of A, as pairs, to every CTA;
+//   CTA r adds rows [128 r / S, ..) of all parts in rank order and copies its
+//   rows of A, as pairs, to every CTA;
 //   every CTA forms B = a I + b A + c A A and X <- B X for its own columns.
 // No iterate goes to memory: the call reads its input and writes the result.  The time is a chain of latencies: two cluster barriers, three
 // 128-deep products and four passes over tensor memory a step.
@@ -530,11 +531,69 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
 }
 
 __device__ __forceinline__ void split8(const float (&v)[8], uint4& hi, uint4& lo) {
-    __half h[8], l[8];
+    uint32_t h[4], l[4];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) split(v[q], h[q], l[q]);
-    hi = make_uint4(pack(h[0], h[1]), pack(h[2], h[3]), pack(h[4], h[5]), pack(h[6], h[7]));
-    lo = make_uint4(pack(l[0], l[1]), pack(l[2], l[3]), pack(l[4], l[5]), pack(l[6], l[7]));
+    for (int q = 0; q < 4; ++q) {
+        const __half2 h2 = __floats2half2_rn(v[2 * q], v[2 * q + 1]);
+        const float2 f = __half22float2(h2);
+        const __half2 l2 = __floats2half2_rn(v[2 * q] - f.x, v[2 * q + 1] - f.y);
+        h[q] = *reinterpret_cast<const uint32_t*>(&h2);
+        l[q] = *reinterpret_cast<const uint32_t*>(&l2);
+    }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// Rows [rank 128 / S, ..) of A from the S partial sums, added in rank order,
+// as pairs into this CTA's A (da: the partial sums' place, in every CTA).
+template <int S>
+__device__ __forceinline__ void reduce_rows(uint32_t da, uint32_t rank, uint8_t* as) {
+    constexpr int kRows = kFusedM / S, kHalves = kRows * 32;  // 4-column pieces of the rows
+#pragma unroll
+    for (int t0 = 0; t0 < kHalves; t0 += kThreads) {
+        const int t = t0 + (int)threadIdx.x;
+        const int r = (int)rank * kRows + t % kRows, c = t / kRows;
+        float4 x[S];
+#pragma unroll
+        for (int s = 0; s < S; ++s) x[s] = ld_cluster4(map_rank(da, (uint32_t)s) + (uint32_t)((c * kFusedM + r) * 16));
+#pragma unroll
+        for (int s = 1; s < S; ++s) x[0].x += x[s].x, x[0].y += x[s].y, x[0].z += x[s].z, x[0].w += x[s].w;
+        const __half2 h0 = __floats2half2_rn(x[0].x * (1.f / kScale), x[0].y * (1.f / kScale));
+        const __half2 h1 = __floats2half2_rn(x[0].z * (1.f / kScale), x[0].w * (1.f / kScale));
+        const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+        const __half2 l0 = __floats2half2_rn(x[0].x * (1.f / kScale) - f0.x, x[0].y * (1.f / kScale) - f0.y);
+        const __half2 l1 = __floats2half2_rn(x[0].z * (1.f / kScale) - f1.x, x[0].w * (1.f / kScale) - f1.y);
+        const uint32_t at = chunk_at(r, c >> 1) + (c & 1) * 8;
+        *reinterpret_cast<uint2*>(as + at) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+        *reinterpret_cast<uint2*>(as + 2 * kPairTile + at) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&l0), *reinterpret_cast<const uint32_t*>(&l1));
+    }
+}
+
+// 8 elements of U for X[i][8 c ..] (0 outside the matrix): consecutive in
+// memory, or (tall) one from each of 8 rows.  vec: such runs may be read 16
+// bytes at a time.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int64_t ld, bool tall, int32_t valid, bool vec, float (&v)[8]) {
+    if (!tall && vec && valid >= 8) {
+        if constexpr (sizeof(T) == 4) {
+            const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+            const uint4 a = *reinterpret_cast<const uint4*>(p);
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[2 * k] = __uint_as_float(w[k] << 16);
+                v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+            }
+        }
+        return;
+    }
+    const int64_t step = tall ? ld : 1;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = k < valid ? to_f(p[k * step]) : 0.f;
 }
 
 struct Steps {
@@ -546,10 +605,10 @@ template <int W, typename TS, typename TW>
 __global__ void __launch_bounds__(kThreads, 1)
     k_ns_fused(Source<TS> src, int32_t rows, int32_t cols, Steps steps, float eps, FinalArgs fin) {
     extern __shared__ uint8_t dsm[];
-    __shared__ __align__(8) uint64_t done;
+    __shared__ __align__(8) uint64_t done, full;  // products; the other CTAs' rows of A
     __shared__ uint32_t tmem_base;
-    __shared__ double norm[kFusedMaxCtas];
-    __shared__ double red[kThreads / 32];
+    __shared__ float norm[kFusedMaxCtas];
+    __shared__ float red[kThreads / 32];
     constexpr int kXTiles = W / 64, kChunks = kFusedM * W / 8 / kThreads;  // 16-byte chunks of X a thread handles
     pdl_start();
     const int warp = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31);
@@ -566,75 +625,111 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kXLo = kXTiles * kPairTile, kALo = 2 * kPairTile;
     if (threadIdx.x == 0) {
         mbar_init(&done, 1);
+        mbar_init(&full, 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (warp == 1) tmem_alloc<128>(&tmem_base);
 
-    // U of this CTA's columns, in registers; the new momentum on the way
+    // U of this CTA's columns, in registers; the new momentum on the way.
+    // Consecutive threads take consecutive addresses: columns of a row, or
+    // (tall: X is the transpose) rows of X.
+    const auto row_of = [&](int it) {
+        const int e = it * kThreads + (int)threadIdx.x;
+        return tall ? e % kFusedM : e / (W / 8);
+    };
+    const auto chunk_of = [&](int it) {
+        const int e = it * kThreads + (int)threadIdx.x;
+        return tall ? e / kFusedM : e % (W / 8);
+    };
+    const auto place = [&](int it, int64_t ld) {  // of the chunk's first element
+        const int64_t j = j0 + chunk_of(it) * 8, i = row_of(it);
+        return tall ? (q * rows + j) * ld + i : (q * rows + i) * ld + j;
+    };
+    const auto valid_of = [&](int it) { return row_of(it) < m ? n - j0 - chunk_of(it) * 8 : 0; };
     float u[kChunks][8];
     float sq = 0.f;
 #pragma unroll
-    for (int it = 0; it < kChunks; ++it) {
-        const int e = it * kThreads + (int)threadIdx.x;
-        // consecutive threads take consecutive addresses: columns of a row, or
-        // (tall: X is the transpose) rows of X
-        const int i = tall ? e % kFusedM : e / (W / 8), c = tall ? e / kFusedM : e % (W / 8);
+    for (int it = 0; it < kChunks; ++it)
+        load8(src.g + (valid_of(it) > 0 ? place(it, src.ld) : 0), src.ld, tall, valid_of(it), (src.vec & 1) != 0, u[it]);
+    if (src.mom_out) {
+        float mo[kChunks][8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int32_t j = j0 + c * 8 + k;
-            const int64_t r = tall ? j : i, cc = tall ? i : j;
-            float v = 0.f;
-            if (i < m && j < n) {
-                v = to_f(src.g[(q * rows + r) * src.ld + cc]);
-                if (src.mom_out) v = src.mu * src.mom[(q * rows + r) * cols + cc] + v;
+        for (int it = 0; it < kChunks; ++it)
+            load8(src.mom + (valid_of(it) > 0 ? place(it, cols) : 0), cols, tall, valid_of(it), (src.vec & 2) != 0, mo[it]);
+#pragma unroll
+        for (int it = 0; it < kChunks; ++it) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                mo[it][k] = src.mu * mo[it][k] + u[it][k];
+                u[it][k] = src.nesterov ? u[it][k] + src.mu * mo[it][k] : mo[it][k];
             }
-            u[it][k] = v;
+            float* p = src.mom_out + (valid_of(it) > 0 ? place(it, cols) : 0);
+            if (!tall && (src.vec & 2) && valid_of(it) >= 8) {
+                *reinterpret_cast<float4*>(p) = make_float4(mo[it][0], mo[it][1], mo[it][2], mo[it][3]);
+                *reinterpret_cast<float4*>(p + 4) = make_float4(mo[it][4], mo[it][5], mo[it][6], mo[it][7]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < valid_of(it)) p[tall ? (int64_t)k * cols : k] = mo[it][k];
+            }
         }
     }
 #pragma unroll
     for (int it = 0; it < kChunks; ++it) {
-        const int e = it * kThreads + (int)threadIdx.x;
-        const int i = tall ? e % kFusedM : e / (W / 8), c = tall ? e / kFusedM : e % (W / 8);
+        float s = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int32_t j = j0 + c * 8 + k;
-            if (src.mom_out && i < m && j < n) {
-                const int64_t r = tall ? j : i, cc = tall ? i : j;
-                src.mom_out[(q * rows + r) * cols + cc] = u[it][k];
-                if (src.nesterov) u[it][k] = to_f(src.g[(q * rows + r) * src.ld + cc]) + src.mu * u[it][k];
-            }
-            sq += u[it][k] * u[it][k];
-        }
+        for (int k = 0; k < 8; ++k) s += u[it][k] * u[it][k];
+        sq += s;
     }
-    {
-        const double s = warp_sum((double)sq);
-        if (lane == 0) red[warp] = s;
-    }
+    sq = warp_sum(sq);
+    if (lane == 0) red[warp] = sq;
     tmem_fence_before();
-    cluster_sync();  // every CTA runs (and red, done and tmem_base are set)
+    cluster_sync();  // every CTA runs (and red, the barriers and tmem_base are set)
     tmem_fence_after();
     const uint32_t tmem = tmem_base;
     if (threadIdx.x < S) {
-        double s = 0.0;
+        float s = 0.f;
+#pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) s += red[w];
-        asm volatile("st.shared::cluster.f64 [%0], %1;\n" ::"r"(map_rank(smem_addr(norm + rank), threadIdx.x)), "d"(s)
+        asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(map_rank(smem_addr(norm + rank), threadIdx.x)), "f"(s)
                      : "memory");
     }
     cluster_sync();
     {
-        double s = 0.0;
-        for (uint32_t r = 0; r < S; ++r) s += norm[r];
-        const float mul = kScale / ((float)sqrt(s) + eps);
+        const float mul = kScale / (sqrtf(warp_sum(lane < (int)S ? norm[lane] : 0.f)) + eps);
 #pragma unroll
         for (int it = 0; it < kChunks; ++it) {
-            const int e = it * kThreads + (int)threadIdx.x;
-            const int i = tall ? e % kFusedM : e / (W / 8), c = tall ? e / kFusedM : e % (W / 8);
 #pragma unroll
             for (int k = 0; k < 8; ++k) u[it][k] *= mul;
             uint4 hi, lo;
             split8(u[it], hi, lo);
-            *reinterpret_cast<uint4*>(xs + chunk_at(i, c)) = hi;
-            *reinterpret_cast<uint4*>(xs + kXLo + chunk_at(i, c)) = lo;
+            *reinterpret_cast<uint4*>(xs + chunk_at(row_of(it), chunk_of(it))) = hi;
+            *reinterpret_cast<uint4*>(xs + kXLo + chunk_at(row_of(it), chunk_of(it))) = lo;
+        }
+    }
+    // the weights, long before they are needed: element (a, b) of thread t is
+    // the a-th of this warp's rows (columns of X when tall) at lane + 32 b
+    const TW* w = (const TW*)fin.w;
+    TW* o = (TW*)fin.out;
+    const int32_t wn = min(W, n - j0);  // columns of X here
+    constexpr int kOut = kFusedM * W / kThreads;
+    const auto out_at = [&](int e, bool& in) -> int64_t {
+        if (tall) {
+            const int c = warp + 8 * (e / 4), r = lane + 32 * (e % 4);
+            in = c < wn && r < m;
+            return (q * n + j0 + c) * fin.ld_out + r;
+        }
+        const int r = warp + 8 * (e / (W / 32)), c = lane + 32 * (e % (W / 32));
+        in = c < wn && r < m;
+        return (q * m + r) * fin.ld_out + j0 + c;
+    };
+    float wr[kOut];
+    if (w) {
+#pragma unroll
+        for (int e = 0; e < kOut; ++e) {
+            bool in;
+            const int64_t at = out_at(e, in);
+            wr[e] = in ? to_f(w[at]) : 0.f;
         }
     }
     const uint32_t xa = smem_addr(xs), aa = smem_addr(as), da = smem_addr(dump);
@@ -687,33 +782,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<float4*>(dump + ((c0 / 4 + t) * kFusedM + row) * 4) =
                     make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]);
         }
+        if (threadIdx.x == 0 && S > 1) mbar_expect_tx(&full, (uint32_t)(4 * kPairTile) / S * (S - 1));
         cluster_sync();
-        // this CTA's columns of A, 8 at a time, to every CTA
-        const int per = kFusedM / (int)S;  // columns of a CTA: 8 or more
-        for (int t = (int)threadIdx.x; t < kFusedM * per / 8; t += kThreads) {
-            const int r = t % kFusedM, c = ((int)rank * per) / 8 + t / kFusedM;
-            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-            for (uint32_t s = 0; s < S; ++s) {
-                const uint32_t at = map_rank(da, s) + (uint32_t)(((c * 2) * kFusedM + r) * 16);
-                const float4 x = ld_cluster4(at), y = ld_cluster4(at + kFusedM * 16);
-                v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-                v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] *= 1.f / kScale;
-            uint4 hi, lo;
-            split8(v, hi, lo);
-            for (uint32_t s = 0; s < S; ++s) {
-                const uint32_t to = map_rank(aa, s) + chunk_at(r, c);
-                st_cluster4(to, hi);
-                st_cluster4(to + kALo, lo);
-            }
+        // this CTA's rows of A: into its own copy, then to the others' in
+        // pieces that lie in one run (8 rows are one 1024-byte swizzle group)
+        switch (S) {
+            case 1: reduce_rows<1>(da, rank, as); break;
+            case 2: reduce_rows<2>(da, rank, as); break;
+            case 4: reduce_rows<4>(da, rank, as); break;
+            case 8: reduce_rows<8>(da, rank, as); break;
+            default: reduce_rows<16>(da, rank, as); break;
         }
-        fence_async();
-        cluster_sync();
+        if (S > 1) {
+            fence_async();
+            __syncthreads();
+            if (warp < 4 && lane < (int)S && lane != (int)rank) {  // warp: one of the 4 tiles; lane: to whom
+                const uint32_t bytes = (uint32_t)kPairTile / S, from = aa + (uint32_t)warp * kPairTile + rank * bytes;
+                asm volatile(
+                    "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                        map_rank(from, (uint32_t)lane)),
+                    "r"(from), "r"(bytes), "r"(map_rank(smem_addr(&full), (uint32_t)lane))
+                    : "memory");
+            }
+            __syncwarp();
+            if (!mbar_wait(&full, (uint32_t)step & 1u) && lane == 0) dev_err(ERR_TIMEOUT);
+            __syncwarp();
+            asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+        }
         // B = a I + b A + c A A, in A's place
         product([&] { pairs(kFusedM / 16, desc_f16(false, kFusedM), a_rows, a_rows); });
+        // every CTA has A: this one's copies are done with its rows
+        if (S > 1) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
         const float ca = steps.coef[step][0] * kScale, cb = steps.coef[step][1], cc = steps.coef[step][2] * (1.f / kScale);
 #pragma unroll 1
         for (int c0 = (warp >> 2) * 64; c0 < (warp >> 2) * 64 + 64; c0 += 32) {
@@ -776,25 +875,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (warp == 1) tmem_free<128>(tmem);
     const float mul = fin.step * (1.f / (kScale * kScale));
-    const TW* w = (const TW*)fin.w;
-    TW* o = (TW*)fin.out;
-    const int32_t wn = min(W, n - j0);  // columns of X here
-    if (tall) {
-        for (int c = warp; c < wn; c += kThreads / 32) {
-            const int64_t at = (q * n + j0 + c) * fin.ld_out;
-            for (int r = lane; r < m; r += 32) {
-                const float x = mul * tile[r + c * (kFusedM + 1)];
-                put(o + at + r, w ? fin.keep * to_f(w[at + r]) + x : x);
-            }
-        }
-    } else {
-        for (int r = warp; r < m; r += kThreads / 32) {
-            const int64_t at = (q * m + r) * fin.ld_out + j0;
-            for (int c = lane; c < wn; c += 32) {
-                const float x = mul * tile[r * (W + 1) + c];
-                put(o + at + c, w ? fin.keep * to_f(w[at + c]) + x : x);
-            }
-        }
+#pragma unroll
+    for (int e = 0; e < kOut; ++e) {
+        bool in;
+        const int64_t at = out_at(e, in);
+        if (!in) continue;
+        const float x = mul * (tall ? tile[lane + 32 * (e % 4) + (warp + 8 * (e / 4)) * (kFusedM + 1)]
+                                    : tile[(warp + 8 * (e / (W / 32))) * (W + 1) + lane + 32 * (e % (W / 32))]);
+        put(o + at, w ? fin.keep * wr[e] + x : x);
     }
 }
 
@@ -1045,12 +1133,13 @@ extern "C" sg_status sg_orthogonalise(const void* d_g, int32_t dtype, int32_t co
         return fail(SG_ERR_INVALID_ARG, "sg_orthogonalise: an array is not aligned to its elements");
     if (d_g == d_out && ld != ld_out) return fail(SG_ERR_INVALID_ARG, "sg_orthogonalise: in place needs ld_out = ld");
     cudaStream_t s = (cudaStream_t)stream;
+    const int64_t elem = dtype == SG_F32 ? 4 : 2;
     if (dtype == SG_F32) {
-        const Source<float> src = {(const float*)d_g, ld, nullptr, nullptr, 0.f, 0};
+        const Source<float> src = {(const float*)d_g, ld, nullptr, nullptr, 0.f, 0, (uintptr_t)d_g % 16 == 0 && ld * elem % 16 == 0};
         return run<float, float>(src, count, rows, cols, steps, h_coef, eps, nullptr, 0.f, scale, (float*)d_out, ld_out,
                                  (char*)d_workspace, s);
     }
-    const Source<__nv_bfloat16> src = {(const __nv_bfloat16*)d_g, ld, nullptr, nullptr, 0.f, 0};
+    const Source<__nv_bfloat16> src = {(const __nv_bfloat16*)d_g, ld, nullptr, nullptr, 0.f, 0, (uintptr_t)d_g % 16 == 0 && ld * elem % 16 == 0};
     return run<__nv_bfloat16, __nv_bfloat16>(src, count, rows, cols, steps, h_coef, eps, nullptr, 0.f, scale,
                                              (__nv_bfloat16*)d_out, ld_out, (char*)d_workspace, s);
 }
@@ -1068,7 +1157,8 @@ extern "C" sg_status sg_muon_step(const void* d_w, int32_t dtype_w, const float*
         ((uintptr_t)d_g | (uintptr_t)d_m | (uintptr_t)d_m_out) % 4)
         return fail(SG_ERR_INVALID_ARG, "sg_muon_step: an array is not aligned to its elements");
     cudaStream_t s = (cudaStream_t)stream;
-    const Source<float> src = {d_g, cols, d_m, d_m_out, momentum, nesterov};
+    const int32_t vec = cols % 4 ? 0 : ((uintptr_t)d_g % 16 == 0 ? 1 : 0) + (((uintptr_t)d_m | (uintptr_t)d_m_out) % 16 == 0 ? 2 : 0);
+    const Source<float> src = {d_g, cols, d_m, d_m_out, momentum, nesterov, vec};
     const float keep = 1.f - rate * weight_decay, step = -rate * scale;
     if (dtype_w == SG_F32)
         return run<float, float>(src, count, rows, cols, steps, h_coef, eps, (const float*)d_w, keep, step,
