@@ -521,8 +521,12 @@ constexpr int kFusedM = 128;
 constexpr int kFusedMaxCtas = 16;
 constexpr int kPairTile = kFusedM * 128;  // bytes of a 128 x 64 fp16 tile
 
+// W = 256: one CTA for the whole matrix, of 512 threads; its A comes straight
+// from tensor memory and needs no fp32 copy in shared memory.
 template <int W>
-constexpr int kFusedSmem = 2 * (W / 64) * kPairTile + 4 * kPairTile + kFusedM * kFusedM * 4 + 1024;
+constexpr int kFusedThreads = W == 256 ? 512 : kThreads;
+template <int W>
+constexpr int kFusedSmem = 2 * (W / 64) * kPairTile + 4 * kPairTile + (W == 256 ? 0 : kFusedM * kFusedM * 4) + 1024;
 
 // Address of 8 elements (columns 8 c ..) of row r of a [128 x 64 t] swizzled
 // operand.
@@ -530,44 +534,45 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     return (uint32_t)((c >> 3) * kPairTile + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
+// Two values as packed hi and lo.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    lo = *reinterpret_cast<const uint32_t*>(&l);
+}
 __device__ __forceinline__ void split8(const float (&v)[8], uint4& hi, uint4& lo) {
-    uint32_t h[4], l[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const __half2 h2 = __floats2half2_rn(v[2 * q], v[2 * q + 1]);
-        const float2 f = __half22float2(h2);
-        const __half2 l2 = __floats2half2_rn(v[2 * q] - f.x, v[2 * q + 1] - f.y);
-        h[q] = *reinterpret_cast<const uint32_t*>(&h2);
-        l[q] = *reinterpret_cast<const uint32_t*>(&l2);
-    }
-    hi = make_uint4(h[0], h[1], h[2], h[3]);
-    lo = make_uint4(l[0], l[1], l[2], l[3]);
+    split2(v[0], v[1], hi.x, lo.x);
+    split2(v[2], v[3], hi.y, lo.y);
+    split2(v[4], v[5], hi.z, lo.z);
+    split2(v[6], v[7], hi.w, lo.w);
 }
 
 // Rows [rank 128 / S, ..) of A from the S partial sums, added in rank order,
 // as pairs into this CTA's A (da: the partial sums' place, in every CTA).
 template <int S>
 __device__ __forceinline__ void reduce_rows(uint32_t da, uint32_t rank, uint8_t* as) {
-    constexpr int kRows = kFusedM / S, kHalves = kRows * 32;  // 4-column pieces of the rows
+    constexpr int kRows = kFusedM / S, kTurns = kRows * 32 / kThreads;  // 4-column pieces of the rows a thread takes
+    float4 x[kTurns][S];  // 16 loads in flight, whatever S is
 #pragma unroll
-    for (int t0 = 0; t0 < kHalves; t0 += kThreads) {
-        const int t = t0 + (int)threadIdx.x;
-        const int r = (int)rank * kRows + t % kRows, c = t / kRows;
-        float4 x[S];
+    for (int i = 0; i < kTurns; ++i) {
+        const int t = i * kThreads + (int)threadIdx.x, r = (int)rank * kRows + t % kRows, c = t / kRows;
 #pragma unroll
-        for (int s = 0; s < S; ++s) x[s] = ld_cluster4(map_rank(da, (uint32_t)s) + (uint32_t)((c * kFusedM + r) * 16));
+        for (int s = 0; s < S; ++s) x[i][s] = ld_cluster4(map_rank(da, (uint32_t)s) + (uint32_t)((c * kFusedM + r) * 16));
+    }
 #pragma unroll
-        for (int s = 1; s < S; ++s) x[0].x += x[s].x, x[0].y += x[s].y, x[0].z += x[s].z, x[0].w += x[s].w;
-        const __half2 h0 = __floats2half2_rn(x[0].x * (1.f / kScale), x[0].y * (1.f / kScale));
-        const __half2 h1 = __floats2half2_rn(x[0].z * (1.f / kScale), x[0].w * (1.f / kScale));
-        const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
-        const __half2 l0 = __floats2half2_rn(x[0].x * (1.f / kScale) - f0.x, x[0].y * (1.f / kScale) - f0.y);
-        const __half2 l1 = __floats2half2_rn(x[0].z * (1.f / kScale) - f1.x, x[0].w * (1.f / kScale) - f1.y);
+    for (int i = 0; i < kTurns; ++i) {
+        const int t = i * kThreads + (int)threadIdx.x, r = (int)rank * kRows + t % kRows, c = t / kRows;
+        float4 v = x[i][0];
+#pragma unroll
+        for (int s = 1; s < S; ++s) v.x += x[i][s].x, v.y += x[i][s].y, v.z += x[i][s].z, v.w += x[i][s].w;
+        uint32_t h0, l0, h1, l1;
+        split2(v.x * (1.f / kScale), v.y * (1.f / kScale), h0, l0);
+        split2(v.z * (1.f / kScale), v.w * (1.f / kScale), h1, l1);
         const uint32_t at = chunk_at(r, c >> 1) + (c & 1) * 8;
-        *reinterpret_cast<uint2*>(as + at) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-        *reinterpret_cast<uint2*>(as + 2 * kPairTile + at) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&l0), *reinterpret_cast<const uint32_t*>(&l1));
+        *reinterpret_cast<uint2*>(as + at) = make_uint2(h0, h1);
+        *reinterpret_cast<uint2*>(as + 2 * kPairTile + at) = make_uint2(l0, l1);
     }
 }
 
@@ -602,19 +607,19 @@ struct Steps {
 };
 
 template <int W, typename TS, typename TW>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kFusedThreads<W>, 1)
     k_ns_fused(Source<TS> src, int32_t rows, int32_t cols, Steps steps, float eps, FinalArgs fin) {
     extern __shared__ uint8_t dsm[];
     __shared__ __align__(8) uint64_t done, full;  // products; the other CTAs' rows of A
     __shared__ uint32_t tmem_base;
     __shared__ float norm[kFusedMaxCtas];
-    __shared__ float red[kThreads / 32];
-    constexpr int kXTiles = W / 64, kChunks = kFusedM * W / 8 / kThreads;  // 16-byte chunks of X a thread handles
+    __shared__ float red[kFusedThreads<W> / 32];
+    constexpr int kNT = kFusedThreads<W>, kXTiles = W / 64, kChunks = kFusedM * W / 8 / kNT;  // 16-byte chunks of X a thread handles
     pdl_start();
     const int warp = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31);
     const uint32_t rank = cluster_rank();
-    uint32_t S;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(S));
+    uint32_t S = 1;
+    if constexpr (W < 256) asm volatile("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(S));
     const int64_t q = blockIdx.y;
     const bool tall = rows > cols;
     const int32_t m = tall ? cols : rows, n = tall ? rows : cols, j0 = (int32_t)rank * W;
@@ -628,17 +633,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&full, 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
-    if (warp == 1) tmem_alloc<128>(&tmem_base);
+    if (warp == 1) tmem_alloc<(W > 128 ? W : 128)>(&tmem_base);
 
     // U of this CTA's columns, in registers; the new momentum on the way.
     // Consecutive threads take consecutive addresses: columns of a row, or
     // (tall: X is the transpose) rows of X.
     const auto row_of = [&](int it) {
-        const int e = it * kThreads + (int)threadIdx.x;
+        const int e = it * kNT + (int)threadIdx.x;
         return tall ? e % kFusedM : e / (W / 8);
     };
     const auto chunk_of = [&](int it) {
-        const int e = it * kThreads + (int)threadIdx.x;
+        const int e = it * kNT + (int)threadIdx.x;
         return tall ? e / kFusedM : e % (W / 8);
     };
     const auto place = [&](int it, int64_t ld) {  // of the chunk's first element
@@ -652,25 +657,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int it = 0; it < kChunks; ++it)
         load8(src.g + (valid_of(it) > 0 ? place(it, src.ld) : 0), src.ld, tall, valid_of(it), (src.vec & 1) != 0, u[it]);
     if (src.mom_out) {
-        float mo[kChunks][8];
+        constexpr int kBatch = 4;  // chunks whose momentum is in registers at once
 #pragma unroll
-        for (int it = 0; it < kChunks; ++it)
-            load8(src.mom + (valid_of(it) > 0 ? place(it, cols) : 0), cols, tall, valid_of(it), (src.vec & 2) != 0, mo[it]);
+        for (int i0 = 0; i0 < kChunks; i0 += kBatch) {
+            float mo[kBatch][8];
 #pragma unroll
-        for (int it = 0; it < kChunks; ++it) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                mo[it][k] = src.mu * mo[it][k] + u[it][k];
-                u[it][k] = src.nesterov ? u[it][k] + src.mu * mo[it][k] : mo[it][k];
+            for (int i = 0; i < kBatch; ++i) {
+                const int it = i0 + i;
+                load8(src.mom + (valid_of(it) > 0 ? place(it, cols) : 0), cols, tall, valid_of(it), (src.vec & 2) != 0, mo[i]);
             }
-            float* p = src.mom_out + (valid_of(it) > 0 ? place(it, cols) : 0);
-            if (!tall && (src.vec & 2) && valid_of(it) >= 8) {
-                *reinterpret_cast<float4*>(p) = make_float4(mo[it][0], mo[it][1], mo[it][2], mo[it][3]);
-                *reinterpret_cast<float4*>(p + 4) = make_float4(mo[it][4], mo[it][5], mo[it][6], mo[it][7]);
-            } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < valid_of(it)) p[tall ? (int64_t)k * cols : k] = mo[it][k];
+            for (int i = 0; i < kBatch; ++i) {
+                const int it = i0 + i;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    mo[i][k] = src.mu * mo[i][k] + u[it][k];
+                    u[it][k] = src.nesterov ? u[it][k] + src.mu * mo[i][k] : mo[i][k];
+                }
+                float* p = src.mom_out + (valid_of(it) > 0 ? place(it, cols) : 0);
+                if (!tall && (src.vec & 2) && valid_of(it) >= 8) {
+                    *reinterpret_cast<float4*>(p) = make_float4(mo[i][0], mo[i][1], mo[i][2], mo[i][3]);
+                    *reinterpret_cast<float4*>(p + 4) = make_float4(mo[i][4], mo[i][5], mo[i][6], mo[i][7]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < valid_of(it)) p[tall ? (int64_t)k * cols : k] = mo[i][k];
+                }
             }
         }
     }
@@ -690,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x < S) {
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) s += red[w];
+        for (int w = 0; w < kNT / 32; ++w) s += red[w];
         asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(map_rank(smem_addr(norm + rank), threadIdx.x)), "f"(s)
                      : "memory");
     }
@@ -707,35 +719,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(xs + kXLo + chunk_at(row_of(it), chunk_of(it))) = lo;
         }
     }
-    // the weights, long before they are needed: element (a, b) of thread t is
-    // the a-th of this warp's rows (columns of X when tall) at lane + 32 b
+    // element e of the output for this thread: rows (columns of X when tall) go
+    // to warps in turn, 32 neighbours to its lanes
     const TW* w = (const TW*)fin.w;
     TW* o = (TW*)fin.out;
     const int32_t wn = min(W, n - j0);  // columns of X here
-    constexpr int kOut = kFusedM * W / kThreads;
+    constexpr int kOut = kFusedM * W / kNT, kWarps = kNT / 32;
     const auto out_at = [&](int e, bool& in) -> int64_t {
         if (tall) {
-            const int c = warp + 8 * (e / 4), r = lane + 32 * (e % 4);
+            const int c = warp + kWarps * (e / 4), r = lane + 32 * (e % 4);
             in = c < wn && r < m;
             return (q * n + j0 + c) * fin.ld_out + r;
         }
-        const int r = warp + 8 * (e / (W / 32)), c = lane + 32 * (e % (W / 32));
+        const int r = warp + kWarps * (e / (W / 32)), c = lane + 32 * (e % (W / 32));
         in = c < wn && r < m;
         return (q * m + r) * fin.ld_out + j0 + c;
     };
-    float wr[kOut];
-    if (w) {
-#pragma unroll
-        for (int e = 0; e < kOut; ++e) {
-            bool in;
-            const int64_t at = out_at(e, in);
-            wr[e] = in ? to_f(w[at]) : 0.f;
-        }
-    }
     const uint32_t xa = smem_addr(xs), aa = smem_addr(as), da = smem_addr(dump);
     const int row = (warp & 3) * 32 + lane;  // of tensor memory, in every pass over it
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    uint32_t phase = 0;
+    uint32_t phase = 0, a_phase = 0;
+    const int kx = max(1, (min(W, n - j0) + 15) / 16);  // 16-column pieces of X that are not empty
+    const int part = warp >> 2;  // which columns this warp takes in a pass over tensor memory
     // runs `issue` on one thread once all shared memory is written, and waits for it
     const auto product = [&](auto issue) {
         tmem_fence_before();
@@ -769,19 +774,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto x_cols = [&](int k, int lo) {
         return smem_desc_mn_sw128(xa + (lo ? kXLo : 0) + (uint32_t)(k * 16 * 128), kPairTile);
     };
-#pragma unroll 1
-    for (int step = 0; step < steps.count; ++step) {
-        // partial A = X X^T
-        product([&] { pairs(W / 16, desc_f16(false, kFusedM), x_rows, x_rows); });
-#pragma unroll 1
-        for (int c0 = (warp >> 2) * 64; c0 < (warp >> 2) * 64 + 64; c0 += 32) {
-            float v[32];
-            tmem_load_32(tmem + lanes + (uint32_t)c0, v);
-#pragma unroll
-            for (int t = 0; t < 8; ++t)
-                *reinterpret_cast<float4*>(dump + ((c0 / 4 + t) * kFusedM + row) * 4) =
-                    make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]);
-        }
+    // the partial sums of all CTAs into A, in every CTA
+    const auto gather = [&] {
         if (threadIdx.x == 0 && S > 1) mbar_expect_tx(&full, (uint32_t)(4 * kPairTile) / S * (S - 1));
         cluster_sync();
         // this CTA's rows of A: into its own copy, then to the others' in
@@ -805,9 +799,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                     : "memory");
             }
             __syncwarp();
-            if (!mbar_wait(&full, (uint32_t)step & 1u) && lane == 0) dev_err(ERR_TIMEOUT);
+            if (!mbar_wait(&full, (uint32_t)a_phase) && lane == 0) dev_err(ERR_TIMEOUT);
             __syncwarp();
             asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+        }
+            a_phase ^= 1u;
+    };
+#pragma unroll 1
+    for (int step = 0; step < steps.count; ++step) {
+        // partial A = X X^T
+        product([&] { pairs(kx, desc_f16(false, kFusedM), x_rows, x_rows); });
+        if constexpr (W == 256) {
+            float v[32];
+            tmem_load_32(tmem + lanes + (uint32_t)part * 32, v);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                float x[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = v[8 * t + k] * (1.f / kScale);
+                uint4 hi, lo;
+                split8(x, hi, lo);
+                *reinterpret_cast<uint4*>(as + chunk_at(row, part * 4 + t)) = hi;
+                *reinterpret_cast<uint4*>(as + kALo + chunk_at(row, part * 4 + t)) = lo;
+            }
+        } else {
+#pragma unroll 1
+            for (int c0 = part * 64; c0 < part * 64 + 64; c0 += 32) {
+                float v[32];
+                tmem_load_32(tmem + lanes + (uint32_t)c0, v);
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                    *reinterpret_cast<float4*>(dump + ((c0 / 4 + t) * kFusedM + row) * 4) =
+                        make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]);
+            }
+            gather();
         }
         // B = a I + b A + c A A, in A's place
         product([&] { pairs(kFusedM / 16, desc_f16(false, kFusedM), a_rows, a_rows); });
@@ -815,9 +840,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (S > 1) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
         const float ca = steps.coef[step][0] * kScale, cb = steps.coef[step][1], cc = steps.coef[step][2] * (1.f / kScale);
 #pragma unroll 1
-        for (int c0 = (warp >> 2) * 64; c0 < (warp >> 2) * 64 + 64; c0 += 32) {
+        for (int c0 = part * (kFusedM * 4 / kWarps); c0 < (part + 1) * (kFusedM * 4 / kWarps); c0 += 32) {
             float v[32];
             tmem_load_32(tmem + lanes + (uint32_t)c0, v);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] *= cc;
+            if ((c0 >> 5) == (warp & 3)) {  // the diagonal: column c0 + lane of row `row`
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] += k == lane ? ca : 0.f;
+            }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 uint4* ph = reinterpret_cast<uint4*>(as + chunk_at(row, c0 / 8 + t));
@@ -829,11 +860,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float2 h = __half22float2(h2[k]), l = __half22float2(l2[k]);
-                    b[2 * k] = cc * v[8 * t + 2 * k] + cb * (h.x + l.x);
-                    b[2 * k + 1] = cc * v[8 * t + 2 * k + 1] + cb * (h.y + l.y);
+                    b[2 * k] = fmaf(cb, h.x, fmaf(cb, l.x, v[8 * t + 2 * k]));
+                    b[2 * k + 1] = fmaf(cb, h.y, fmaf(cb, l.y, v[8 * t + 2 * k + 1]));
                 }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) b[k] += row == c0 + 8 * t + k ? ca : 0.f;
                 uint4 hi, lo;
                 split8(b, hi, lo);
                 *ph = hi;
@@ -841,10 +870,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         // X <- B X
-        product([&] { pairs(kFusedM / 16, desc_f16(true, W), a_rows, x_cols); });
+        product([&] { pairs(kFusedM / 16, desc_f16(true, 16 * kx), a_rows, x_cols); });
         if (step + 1 < steps.count) {
 #pragma unroll 1
-            for (int c0 = (warp >> 2) * (W / 2); c0 < (warp >> 2) * (W / 2) + W / 2; c0 += 32) {
+            for (int c0 = part * (W * 4 / kWarps); c0 < (part + 1) * (W * 4 / kWarps); c0 += 32) {
                 float v[32];
                 tmem_load_32(tmem + lanes + (uint32_t)c0, v);
 #pragma unroll
@@ -860,12 +889,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
-    // out = keep w + step X, through shared memory so that rows go out whole
+    // out = keep w + step X, through shared memory so that rows go out whole;
+    // the weights are all on their way before that
+    float wr[kOut];
+    if (w) {
+#pragma unroll
+        for (int e = 0; e < kOut; ++e) {
+            bool in;
+            const int64_t at = out_at(e, in);
+            wr[e] = in ? to_f(w[at]) : 0.f;
+        }
+    }
     float* tile = dump;  // [row][W + 1], or [column][129] when tall: A's place is free too
     if constexpr (W == 128) tile = reinterpret_cast<float*>(as);
+    if constexpr (W == 256) tile = reinterpret_cast<float*>(xs);
     const int ld_row = tall ? 1 : W + 1, ld_col = tall ? kFusedM + 1 : 1;
 #pragma unroll 1
-    for (int c0 = (warp >> 2) * (W / 2); c0 < (warp >> 2) * (W / 2) + W / 2; c0 += 32) {
+    for (int c0 = part * (W * 4 / kWarps); c0 < (part + 1) * (W * 4 / kWarps); c0 += 32) {
         float v[32];
         tmem_load_32(tmem + lanes + (uint32_t)c0, v);
 #pragma unroll
@@ -873,15 +913,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tmem_fence_before();
     __syncthreads();
-    if (warp == 1) tmem_free<128>(tmem);
+    if (warp == 1) tmem_free<(W > 128 ? W : 128)>(tmem);
     const float mul = fin.step * (1.f / (kScale * kScale));
 #pragma unroll
     for (int e = 0; e < kOut; ++e) {
         bool in;
         const int64_t at = out_at(e, in);
         if (!in) continue;
-        const float x = mul * (tall ? tile[lane + 32 * (e % 4) + (warp + 8 * (e / 4)) * (kFusedM + 1)]
-                                    : tile[(warp + 8 * (e / (W / 32))) * (W + 1) + lane + 32 * (e % (W / 32))]);
+        const float x = mul * (tall ? tile[lane + 32 * (e % 4) + (warp + kWarps * (e / 4)) * (kFusedM + 1)]
+                                    : tile[(warp + kWarps * (e / (W / 32))) * (W + 1) + lane + 32 * (e % (W / 32))]);
         put(o + at, w ? fin.keep * wr[e] + x : x);
     }
 }
@@ -1008,12 +1048,13 @@ sg_status launch_fused(const Source<TS>& src, int32_t count, int32_t rows, int32
     static bool set = false;
     if (!set) {
         SG_CUDA(cudaFuncSetAttribute(k_ns_fused<W, TS, TW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFusedSmem<W>));
-        SG_CUDA(cudaFuncSetAttribute(k_ns_fused<W, TS, TW>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+        if (W < 256)
+            SG_CUDA(cudaFuncSetAttribute(k_ns_fused<W, TS, TW>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
         set = true;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas, (unsigned)count);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kFusedThreads<W>);
     cfg.dynamicSmemBytes = kFusedSmem<W>;
     cfg.stream = s;
     cudaLaunchAttribute at[2];
@@ -1036,16 +1077,18 @@ sg_status run(Source<TS> src, int32_t count, int32_t rows, int32_t cols, int32_t
     const int32_t m = (int32_t)L.m, n = (int32_t)L.n;
     const FinalArgs fin = {w, out, keep, step, ld_out, rows > cols ? 1 : 0};
     // a matrix that the shared memory of one cluster holds is done in one
-    // launch; 64 columns a CTA while 16 CTAs reach, since each product and each
-    // pass over tensor memory is then half as long
+    // launch: up to 256 columns by one CTA, which has nothing to exchange; else
+    // 64 columns a CTA while 16 CTAs reach, since each product and each pass
+    // over tensor memory is then half as long
     if (m <= kFusedM && n <= kFusedMaxCtas * 128 && steps > 0) {
         Steps st;
         st.count = steps;
         for (int32_t k = 0; k < SG_MAX_NS_STEPS; ++k)
             for (int i = 0; i < 3; ++i) st.coef[k][i] = k < steps ? (coef ? coef[3 * k + i] : kCoef[i]) : 0.f;
-        const int width = n <= kFusedMaxCtas * 64 ? 64 : 128;
+        const int width = n <= 256 ? 256 : n <= kFusedMaxCtas * 64 ? 64 : 128;
         int ctas = 1;
         while (ctas * width < n) ctas *= 2;
+        if (width == 256) return launch_fused<256, TS, TW>(src, count, rows, cols, 1, st, eps, fin, s);
         return width == 64 ? launch_fused<64, TS, TW>(src, count, rows, cols, ctas, st, eps, fin, s)
                            : launch_fused<128, TS, TW>(src, count, rows, cols, ctas, st, eps, fin, s);
     }
