@@ -79,9 +79,15 @@ cudaError_t dev_alloc(void** p, size_t bytes);
 // completed and its writes are visible.  Every such kernel calls pdl_start()
 // first, before any early return, so a grid never completes ahead of the
 // kernel before it (which keeps the usual stream order for the kernels after
-// it).  No kernel triggers early: the next grid is scheduled as this one's
-// blocks exit.
+// it).  Unless a kernel calls pdl_next(), the next grid is scheduled as this
+// one's blocks exit.
 __device__ __forceinline__ void pdl_start() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next grid of the stream be scheduled once every block of this one
+// has got here (the steps of sg_muon.cu, whose kernels follow one another):
+// its blocks take the SMs as this grid's leave them, set up, and wait in
+// pdl_start() as above.  The stream's order is kept: a kernel that calls this
+// still waits for its own predecessor before it ends.
+__device__ __forceinline__ void pdl_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args... args) {

@@ -30,7 +30,7 @@ using namespace sgi;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kNormBlocks = 64;  // partial sums of squares of a matrix
+constexpr int kNormParts = 256;  // partial sums of squares of a matrix, at most
 constexpr float kScale = 256.f;  // of every fp16 pair
 constexpr int kTile = 128;       // rows of an output tile (and columns of a symmetric one)
 constexpr int kBK = 64;          // K elements of a stage: one 128-byte swizzle row
@@ -69,72 +69,140 @@ struct Source {
     int32_t vec;  // 1: g, 2: the momentum may be read 16 bytes at a time
 };
 
+// Two values as packed hi and lo.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+__device__ __forceinline__ void split8(const float (&v)[8], uint4& hi, uint4& lo) {
+    split2(v[0], v[1], hi.x, lo.x);
+    split2(v[2], v[3], hi.y, lo.y);
+    split2(v[4], v[5], hi.z, lo.z);
+    split2(v[6], v[7], hi.w, lo.w);
+}
+
 // ------------------------------------------------------------ norm and split
-// New momentum, and partial sums of the squares of U.
+// Elements t .. t + 3 of a row, as far as there are that many (0 past the end).
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, int32_t valid, bool vec, float (&v)[4]) {
+    if (vec && valid >= 4) {
+        if constexpr (sizeof(T) == 4) {
+            const float4 a = *reinterpret_cast<const float4*>(p);
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        } else {
+            const uint2 a = *reinterpret_cast<const uint2*>(p);
+            v[0] = __uint_as_float(a.x << 16), v[1] = __uint_as_float(a.x & 0xFFFF0000u);
+            v[2] = __uint_as_float(a.y << 16), v[3] = __uint_as_float(a.y & 0xFFFF0000u);
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = k < valid ? to_f(p[k]) : 0.f;
+}
+
+// New momentum, and partial sums of the squares of U: a warp takes rows in
+// turn, 4 x 4 elements a lane at a time.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_ns_norm(Source<T> src, int32_t rows, int32_t cols,
                                                       double* __restrict__ part) {
+    pdl_next();
     pdl_start();
     __shared__ double sh[kThreads / 32];
-    const int64_t q = blockIdx.y, total = (int64_t)rows * cols;
-    float sq = 0.f;
-    for (int64_t t = blockIdx.x * (int64_t)kThreads + threadIdx.x; t < total; t += (int64_t)gridDim.x * kThreads) {
-        const int64_t r = t / cols, c = t - r * cols;
-        float u = to_f(src.g[(q * rows + r) * src.ld + c]);
+    const int64_t q = blockIdx.y;
+    const int warp = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31);
+    const int32_t pieces = (cols + 511) / 512;  // of a row
+    const int64_t items = (int64_t)rows * pieces;
+    float sum = 0.f;
+    for (int64_t it = blockIdx.x * (int64_t)(kThreads / 32) + warp; it < items; it += (int64_t)gridDim.x * (kThreads / 32)) {
+        const int32_t r = (int32_t)(it / pieces), c0 = (int32_t)(it - (int64_t)r * pieces) * 512 + lane * 4;
+        const T* g = src.g + (q * rows + r) * src.ld + c0;
+        float u[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) load4(g + k * 128, cols - c0 - k * 128, (src.vec & 1) != 0, u[k]);
         if (src.mom_out) {
-            const float m = src.mu * src.mom[q * total + t] + u;
-            src.mom_out[q * total + t] = m;
-            u = src.nesterov ? u + src.mu * m : m;
+            const int64_t at = (q * rows + r) * cols + c0;
+            float m[4][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) load4(src.mom + at + k * 128, cols - c0 - k * 128, (src.vec & 2) != 0, m[k]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    m[k][e] = src.mu * m[k][e] + u[k][e];
+                    if (c0 + k * 128 + e < cols) src.mom_out[at + k * 128 + e] = m[k][e];
+                    u[k][e] = src.nesterov ? u[k][e] + src.mu * m[k][e] : m[k][e];
+                }
         }
-        sq += u * u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum += u[k][e] * u[k][e];
     }
-    double sum = warp_sum((double)sq);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = sum;
+    double s = warp_sum((double)sum);
+    if (lane == 0) sh[warp] = s;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int w = 1; w < kThreads / 32; ++w) sum += sh[w];
-        part[q * gridDim.x + blockIdx.x] = sum;
+        for (int w = 1; w < kThreads / 32; ++w) s += sh[w];
+        part[q * gridDim.x + blockIdx.x] = s;
     }
 }
 
-// X = U / (||U|| + eps) as planes, transposed when rows > cols; one 32 x 32
-// tile of U a block step.
+// X = U / (||U|| + eps) as planes, transposed when rows > cols; a block takes
+// 64 rows x 32 columns of U (tall) or 32 x 64, and writes 8 elements a thread.
+constexpr int kSplitN = 64, kSplitM = 32;  // of X
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_ns_split(Source<T> src, int32_t rows, int32_t cols,
-                                                       const double* __restrict__ part, float eps, Planes X,
-                                                       int64_t ldx) {
+                                                       const double* __restrict__ part, int32_t parts, float eps,
+                                                       Planes X, int64_t ldx) {
+    pdl_next();
     pdl_start();
-    __shared__ float tile[32][33];
-    const int64_t q = blockIdx.z, total = (int64_t)rows * cols;
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    double s = part[q * kNormBlocks + tx] + part[q * kNormBlocks + 32 + tx];
-    s = warp_sum(s);
-    const float mul = kScale / ((float)sqrt(s) + eps);
+    __shared__ float tile[kSplitM][kSplitN + 1];
+    __shared__ double sh[kThreads / 32];
+    const int64_t q = blockIdx.z;
     const bool tall = rows > cols;
     const int32_t m = tall ? cols : rows, n = tall ? rows : cols;
-    const int32_t r0 = (int32_t)blockIdx.y * 32, c0 = (int32_t)blockIdx.x * 32;
-    for (int i = ty; i < 32; i += 8) {
-        const int32_t r = r0 + i, c = c0 + tx;
-        float u = 0.f;
-        if (r < rows && c < cols) {
-            u = to_f(src.g[(q * rows + r) * src.ld + c]);
-            if (src.mom_out) {
-                const float mo = src.mom_out[q * total + (int64_t)r * cols + c];
-                u = src.nesterov ? u + src.mu * mo : mo;
-            }
+    const int32_t i0 = (int32_t)blockIdx.y * kSplitM, j0 = (int32_t)blockIdx.x * kSplitN;
+    const auto u_at = [&](int64_t r, int64_t c) {
+        float u = to_f(src.g[(q * rows + r) * src.ld + c]);
+        if (src.mom_out) {
+            const float mo = src.mom_out[(q * rows + r) * cols + c];
+            u = src.nesterov ? u + src.mu * mo : mo;
         }
-        tile[i][tx] = u * mul;
+        return u;
+    };
+    float u[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {  // consecutive threads on consecutive columns of U
+        const int e = k * kThreads + (int)threadIdx.x;
+        const int i = tall ? e % kSplitM : e / kSplitN, j = tall ? e / kSplitM : e % kSplitN;
+        u[k] = i0 + i < m && j0 + j < n ? (tall ? u_at(j0 + j, i0 + i) : u_at(i0 + i, j0 + j)) : 0.f;
+    }
+    double s = warp_sum((int)threadIdx.x < parts ? part[q * parts + threadIdx.x] : 0.0);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = 0.0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) s += sh[w];
+    const float mul = kScale / (sqrtf((float)s) + eps);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int e = k * kThreads + (int)threadIdx.x;
+        tile[tall ? e % kSplitM : e / kSplitN][tall ? e / kSplitM : e % kSplitN] = u[k] * mul;
     }
     __syncthreads();
-    const int32_t x0 = tall ? c0 : r0, y0 = tall ? r0 : c0;  // the tile's place in X
-    for (int i = ty; i < 32; i += 8) {
-        const int32_t r = x0 + i, c = y0 + tx;
-        if (r >= m || c >= n) continue;
-        __half hi, lo;
-        split(tall ? tile[tx][i] : tile[i][tx], hi, lo);
-        X.hi[(q * m + r) * ldx + c] = hi;
-        X.lo[(q * m + r) * ldx + c] = lo;
-    }
+    const int i = (int)threadIdx.x >> 3, j = ((int)threadIdx.x & 7) * 8;
+    if (i0 + i >= m || j0 + j >= n) return;  // a row's padding (to a multiple of 8) takes zeros
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = tile[i][j + k];
+    uint4 hi, lo;
+    split8(v, hi, lo);
+    const int64_t at = (q * m + i0 + i) * ldx + j0 + j;
+    *reinterpret_cast<uint4*>(X.hi + at) = hi;
+    *reinterpret_cast<uint4*>(X.lo + at) = lo;
 }
 
 // ----------------------------------------------------------------- products
@@ -204,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t dsm[];
     __shared__ __align__(8) Ring<kSymStages> ring;
     __shared__ uint32_t tmem_base;
-    pdl_start();
+    pdl_next();
     const int warp = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31);
     const int rank = (int)(blockIdx.x % S);
     const int32_t q = (int32_t)blockIdx.y;
@@ -218,12 +286,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t i0 = ti * kTile, j0 = (ti + t) * kTile;
     const bool diag = t == 0;
     uint8_t* tiles = dsm + ((1024 - (smem_addr(dsm) & 1023)) & 1023);
-    if (threadIdx.x == 0) ring_init(ring);
+    if (threadIdx.x == 0) {
+        ring_init(ring);
+        prefetch_map(&maps.hi);
+        prefetch_map(&maps.lo);
+    }
     if (warp == 1) tmem_alloc<kTile>(&tmem_base);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = tmem_base;
+    pdl_start();
     const int n_kt = (K + kBK - 1) / kBK, per = (n_kt + S - 1) / S;
     const int kt0 = min(n_kt, rank * per), n_k = min(n_kt, kt0 + per) - kt0;
     if (warp == 0 && lane == 0) {
@@ -375,16 +448,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t dsm[];
     __shared__ __align__(8) Ring<kStages> ring;
     __shared__ uint32_t tmem_base;
-    pdl_start();
+    pdl_next();
     const int warp = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31);
     const int32_t q = (int32_t)blockIdx.z, i0 = (int32_t)blockIdx.y * kTile, j0 = (int32_t)blockIdx.x * BN;
     uint8_t* tiles = dsm + ((1024 - (smem_addr(dsm) & 1023)) & 1023);
-    if (threadIdx.x == 0) ring_init(ring);
+    if (threadIdx.x == 0) {
+        ring_init(ring);
+        prefetch_map(&maps.bhi);
+        prefetch_map(&maps.blo);
+        prefetch_map(&maps.xhi);
+        prefetch_map(&maps.xlo);
+    }
     if (warp == 1) tmem_alloc<BN>(&tmem_base);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = tmem_base;
+    pdl_start();
     const int n_k = (m + kBK - 1) / kBK;
     if (warp == 0 && lane == 0) {
         int issued = 0;
@@ -532,21 +612,6 @@ constexpr int kFusedSmem = 2 * (W / 64) * kPairTile + 4 * kPairTile + (W == 256 
 // operand.
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     return (uint32_t)((c >> 3) * kPairTile + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-}
-
-// Two values as packed hi and lo.
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-    const __half2 h = __floats2half2_rn(a, b);
-    const float2 f = __half22float2(h);
-    const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
-    hi = *reinterpret_cast<const uint32_t*>(&h);
-    lo = *reinterpret_cast<const uint32_t*>(&l);
-}
-__device__ __forceinline__ void split8(const float (&v)[8], uint4& hi, uint4& lo) {
-    split2(v[0], v[1], hi.x, lo.x);
-    split2(v[2], v[3], hi.y, lo.y);
-    split2(v[4], v[5], hi.z, lo.z);
-    split2(v[6], v[7], hi.w, lo.w);
 }
 
 // Rows [rank 128 / S, ..) of A from the S partial sums, added in rank order,
@@ -954,7 +1019,7 @@ Layout layout(int64_t count, int64_t rows, int64_t cols) {
         L.a[p] = place(count * L.m * L.lda * 2);
         L.b[p] = place(count * L.m * L.lda * 2);
     }
-    L.part = place(count * kNormBlocks * 8);
+    L.part = place(count * kNormParts * 8);
     L.total = o;
     return L;
 }
@@ -1097,9 +1162,12 @@ sg_status run(Source<TS> src, int32_t count, int32_t rows, int32_t cols, int32_t
     a = {(__half*)(ws + L.a[0]), (__half*)(ws + L.a[1])};
     b = {(__half*)(ws + L.b[0]), (__half*)(ws + L.b[1])};
     double* part = (double*)(ws + L.part);
-    SG_CUDA(launch_pdl(k_ns_norm<TS>, dim3(kNormBlocks, (unsigned)count), dim3(kThreads), 0, s, src, rows, cols, part));
-    SG_CUDA(launch_pdl(k_ns_split<TS>, dim3((unsigned)cdiv(cols, 32), (unsigned)cdiv(rows, 32), (unsigned)count),
-                       dim3(kThreads), 0, s, src, rows, cols, (const double*)part, eps, x[0], L.ldx));
+    // one part for every 8 row pieces of 512 columns (a warp each), up to kNormParts
+    int64_t parts = cdiv((int64_t)rows * cdiv(cols, 512), 8);
+    if (parts > kNormParts) parts = kNormParts;
+    SG_CUDA(launch_pdl(k_ns_norm<TS>, dim3((unsigned)parts, (unsigned)count), dim3(kThreads), 0, s, src, rows, cols, part));
+    SG_CUDA(launch_pdl(k_ns_split<TS>, dim3((unsigned)cdiv(n, kSplitN), (unsigned)cdiv(m, kSplitM), (unsigned)count),
+                       dim3(kThreads), 0, s, src, rows, cols, (const double*)part, (int32_t)parts, eps, x[0], L.ldx));
     if (steps == 0) {
         const int64_t eb = cdiv((int64_t)rows * cols, kThreads) < 1024 ? cdiv((int64_t)rows * cols, kThreads) : 1024;
         SG_CUDA(launch_pdl(k_ns_store<TW>, dim3((unsigned)eb, (unsigned)count), dim3(kThreads), 0, s, x[0], L.ldx, rows,
