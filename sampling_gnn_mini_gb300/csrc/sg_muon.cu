@@ -41,16 +41,6 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// v as hi + lo, both fp16 (round to nearest; v is kScale times a value)
-__device__ __forceinline__ void split(float v, __half& hi, __half& lo) {
-    hi = __float2half_rn(v);
-    lo = __float2half_rn(v - __half2float(hi));
-}
-__device__ __forceinline__ uint32_t pack(__half a, __half b) {
-    const __half2 t = __halves2half2(a, b);
-    return *reinterpret_cast<const uint32_t*>(&t);
-}
-
 // A matrix held as two fp16 planes of `ld` columns (a multiple of 8).
 struct Planes {
     __half* hi;
@@ -345,78 +335,111 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!mbar_wait(&ring.done, 0) && lane == 0) dev_err(ERR_TIMEOUT);
     tmem_fence_after();
     __syncthreads();  // the producer has drained: the ring is free
-    // partial sums to shared memory as [column][row]: warps w and w + 4 read
-    // tensor-memory lanes 32 (w % 4).. of columns [0, 64) and [64, 128)
+    // SQUARE also adds b A: on its way while the parts are exchanged.  Thread t
+    // takes 8 columns at a time of row t % 128.
+    constexpr int kW = kTile / S, kTurns = kW / 16;  // columns of this CTA; turns of 16 of them
+    const int row = (int)(threadIdx.x & 127);
+    const int32_t i = i0 + row;
+    const auto col_of = [&](int turn) { return rank * kW + turn * 16 + (int)(threadIdx.x >> 7) * 8; };
+    uint4 ah[kTurns], al[kTurns];
+    if (KIND == SQUARE) {
+#pragma unroll
+        for (int u = 0; u < kTurns; ++u) {
+            const int32_t j = j0 + col_of(u);
+            const int64_t at = ((int64_t)q * m + i) * ld + j;
+            const bool in_range = i < m && j < m;
+            ah[u] = in_range ? *reinterpret_cast<const uint4*>(in.hi + at) : make_uint4(0, 0, 0, 0);
+            al[u] = in_range ? *reinterpret_cast<const uint4*>(in.lo + at) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    // partial sums to shared memory as [column / 4][row][4]: warps w and w + 4
+    // read tensor-memory lanes 32 (w % 4).. of columns [0, 64) and [64, 128)
     float* dump = reinterpret_cast<float*>(tiles);
     {
-        const int row = (warp & 3) * 32 + lane;
+        const int r = (warp & 3) * 32 + lane;
 #pragma unroll 1
         for (int c0 = (warp >> 2) * 64; c0 < (warp >> 2) * 64 + 64; c0 += 32) {
             float v[32];
             tmem_load_32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)c0, v);
+            if (!n_k) {
 #pragma unroll
-            for (int u = 0; u < 32; ++u) dump[(c0 + u) * kTile + row] = n_k ? v[u] : 0.f;
+                for (int u = 0; u < 32; ++u) v[u] = 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                *reinterpret_cast<float4*>(dump + ((c0 / 4 + u) * kTile + r) * 4) =
+                    make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
         }
     }
     tmem_fence_before();
     if constexpr (S > 1) cluster_sync();
     else __syncthreads();
     if (warp == 1) tmem_free<kTile>(tmem);
-    constexpr int kW = kTile / S;  // columns of this CTA
-    const int row = (int)(threadIdx.x & 127);
-    const int32_t i = i0 + row;
     const uint32_t base = smem_addr(dump);
-#pragma unroll 1
-    for (int c0 = (int)(threadIdx.x >> 7) * 8; c0 < kW; c0 += 16) {
-        const int col = rank * kW + c0;
-        float v[8];
+    float4 x[kTurns][S][2];  // 16 loads in flight, whatever S is
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = 0.f;
+    for (int u = 0; u < kTurns; ++u)
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            const uint32_t from = S > 1 ? map_rank(base, (uint32_t)s) : base;
+            const uint32_t at = (uint32_t)((col_of(u) / 4 * kTile + row) * 16);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const uint32_t at = (uint32_t)(((col + u) * kTile + row) * 4);
-                v[u] += S > 1 ? ld_cluster(from + at) : dump[(col + u) * kTile + row];
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (S > 1) x[u][s][h] = ld_cluster4(map_rank(base, (uint32_t)s) + at + h * kTile * 16);
+                else x[u][s][h] = *reinterpret_cast<const float4*>(dump + (col_of(u) / 4 + h) * kTile * 4 + row * 4);
             }
         }
-        const int32_t j = j0 + col;
-        if (i < m && j < m) {
-            const int64_t at = ((int64_t)q * m + i) * ld + j;
-            if (KIND == GRAM) {
+    // (the loads above are volatile: they are issued before the arrival, and
+    // used before the wait)
 #pragma unroll
-                for (int u = 0; u < 8; ++u) v[u] *= 1.f / kScale;
-            } else {
-                const uint4 h4 = *reinterpret_cast<const uint4*>(in.hi + at), l4 = *reinterpret_cast<const uint4*>(in.lo + at);
-                const __half2* h2 = reinterpret_cast<const __half2*>(&h4);
-                const __half2* l2 = reinterpret_cast<const __half2*>(&l4);
+    for (int u = 0; u < kTurns; ++u) {
+        float v[8];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const float2 h = __half22float2(h2[u >> 1]), l = __half22float2(l2[u >> 1]);
-                    const float A = u & 1 ? h.y + l.y : h.x + l.x;
-                    v[u] = c * (v[u] * (1.f / kScale)) + b * A + (i == j + u ? a * kScale : 0.f);
-                }
+        for (int h = 0; h < 2; ++h) {
+            float4 t = x[u][0][h];
+#pragma unroll
+            for (int s = 1; s < S; ++s) t.x += x[u][s][h].x, t.y += x[u][s][h].y, t.z += x[u][s][h].z, t.w += x[u][s][h].w;
+            v[4 * h] = t.x, v[4 * h + 1] = t.y, v[4 * h + 2] = t.z, v[4 * h + 3] = t.w;
+        }
+        if (S > 1 && u == kTurns - 1) asm volatile("barrier.cluster.arrive.release;\n" ::: "memory");  // done reading
+        const int32_t j = j0 + col_of(u);
+        if (i >= m || j >= m) continue;
+        if (KIND == GRAM) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] *= 1.f / kScale;
+        } else {
+            const __half2* h2 = reinterpret_cast<const __half2*>(&ah[u]);
+            const __half2* l2 = reinterpret_cast<const __half2*>(&al[u]);
+            const float cs = c * (1.f / kScale);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 h = __half22float2(h2[k]), l = __half22float2(l2[k]);
+                v[2 * k] = fmaf(b, h.x, fmaf(b, l.x, cs * v[2 * k]));
+                v[2 * k + 1] = fmaf(b, h.y, fmaf(b, l.y, cs * v[2 * k + 1]));
             }
-            __half hi[8], lo[8];
+            if (diag && (i & ~7) == (j & ~7)) {
 #pragma unroll
-            for (int u = 0; u < 8; ++u) split(v[u], hi[u], lo[u]);
-            *reinterpret_cast<uint4*>(out.hi + at) =
-                make_uint4(pack(hi[0], hi[1]), pack(hi[2], hi[3]), pack(hi[4], hi[5]), pack(hi[6], hi[7]));
-            *reinterpret_cast<uint4*>(out.lo + at) =
-                make_uint4(pack(lo[0], lo[1]), pack(lo[2], lo[3]), pack(lo[4], lo[5]), pack(lo[6], lo[7]));
-            if (!diag) {
+                for (int k = 0; k < 8; ++k) v[k] += i == j + k ? a * kScale : 0.f;
+            }
+        }
+        uint4 hi, lo;
+        split8(v, hi, lo);
+        const int64_t at = ((int64_t)q * m + i) * ld + j;
+        *reinterpret_cast<uint4*>(out.hi + at) = hi;
+        *reinterpret_cast<uint4*>(out.lo + at) = lo;
+        if (!diag) {
+            const __half* ph = reinterpret_cast<const __half*>(&hi);
+            const __half* pl = reinterpret_cast<const __half*>(&lo);
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    if (j + u >= m) continue;
-                    const int64_t mir = ((int64_t)q * m + j + u) * ld + i;
-                    out.hi[mir] = hi[u];
-                    out.lo[mir] = lo[u];
-                }
+            for (int k = 0; k < 8; ++k) {
+                if (j + k >= m) continue;
+                const int64_t mir = ((int64_t)q * m + j + k) * ld + i;
+                out.hi[mir] = ph[k];
+                out.lo[mir] = pl[k];
             }
         }
     }
-    if constexpr (S > 1) cluster_sync();  // no CTA leaves while another reads its part
+    // no CTA leaves while another reads its part
+    if constexpr (S > 1) asm volatile("barrier.cluster.wait.acquire;\n" ::: "memory");
 }
 
 // X' = B X: a 128 x BN tile.  B's tile is K-major (B is m x m), X's MN-major
@@ -433,7 +456,7 @@ struct FinalArgs {
 template <int BN>
 constexpr int kApplyStage = 2 * kOperand + 2 * BN * kBK * 2;
 template <int BN>
-constexpr int kApplyStages = BN == 256 ? 2 : 3;
+constexpr int kApplyStages = BN == 256 ? 2 : BN == 128 ? 3 : 4;
 template <int BN>
 constexpr int kApplySmem = kApplyStages<BN> * kApplyStage<BN> + 1024;
 
@@ -513,9 +536,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!mbar_wait(&ring.done, 0) && lane == 0) dev_err(ERR_TIMEOUT);
     tmem_fence_after();
     __syncthreads();  // the producer has drained: the ring is free
-    // the tile through shared memory, so that rows go out whole: [row][BN + 1]
+    // the tile through shared memory, so that rows go out whole: [row][BN + 4]
+    // (rows on 16-byte boundaries, 8 rows in different banks)
     float* dump = reinterpret_cast<float*>(tiles);
-    constexpr int kLd = BN + 1;
+    constexpr int kLd = BN + 4;
     {
         const int row = (warp & 3) * 32 + lane;
 #pragma unroll 1
@@ -523,26 +547,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             float v[32];
             tmem_load_32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)c0, v);
 #pragma unroll
-            for (int u = 0; u < 32; ++u) dump[row * kLd + c0 + u] = v[u];
+            for (int u = 0; u < 8; ++u)
+                *reinterpret_cast<float4*>(dump + row * kLd + c0 + 4 * u) =
+                    make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
         }
     }
     tmem_fence_before();
     __syncthreads();
     if (warp == 1) tmem_free<BN>(tmem);
     if constexpr (!FINAL) {
-#pragma unroll 2
-        for (int row = warp; row < kTile; row += kThreads / 32) {
-            const int32_t i = i0 + row;
-            if (i >= m) break;
-            const int64_t at = ((int64_t)q * m + i) * ldx + j0;
-#pragma unroll
-            for (int c = 2 * lane; c < BN; c += 64) {
-                if (j0 + c >= n) break;
-                __half h0, l0, h1, l1;
-                split(dump[row * kLd + c] * (1.f / kScale), h0, l0);
-                split(dump[row * kLd + c + 1] * (1.f / kScale), h1, l1);
-                *reinterpret_cast<uint32_t*>(out.hi + at + c) = pack(h0, h1);
-                *reinterpret_cast<uint32_t*>(out.lo + at + c) = pack(l0, l1);
+        constexpr int kLanes = BN / 8, kRows = kThreads / kLanes;  // 8 columns a lane; rows at a time
+        const int c = (int)(threadIdx.x % kLanes) * 8;
+        if (j0 + c < n) {
+#pragma unroll 4
+            for (int row = (int)threadIdx.x / kLanes; row < kTile; row += kRows) {
+                if (i0 + row >= m) break;
+                const float4 x = *reinterpret_cast<const float4*>(dump + row * kLd + c);
+                const float4 y = *reinterpret_cast<const float4*>(dump + row * kLd + c + 4);
+                constexpr float d = 1.f / kScale;
+                const float v[8] = {x.x * d, x.y * d, x.z * d, x.w * d, y.x * d, y.y * d, y.z * d, y.w * d};
+                uint4 hi, lo;
+                split8(v, hi, lo);
+                const int64_t at = ((int64_t)q * m + i0 + row) * ldx + j0 + c;
+                *reinterpret_cast<uint4*>(out.hi + at) = hi;
+                *reinterpret_cast<uint4*>(out.lo + at) = lo;
             }
         }
     } else {
@@ -1104,6 +1132,14 @@ sg_status launch_apply(const ApplyMaps& maps, int32_t count, int32_t m, int32_t 
     return SG_OK;
 }
 
+template <typename TW, bool FINAL>
+sg_status run_apply(int bn, const ApplyMaps& maps, int32_t count, int32_t m, int32_t n, Planes out, int64_t ldx,
+                    const FinalArgs& fin, cudaStream_t s) {
+    if (bn == 256) return launch_apply<256, TW, FINAL>(maps, count, m, n, out, ldx, fin, s);
+    if (bn == 128) return launch_apply<128, TW, FINAL>(maps, count, m, n, out, ldx, fin, s);
+    return launch_apply<64, TW, FINAL>(maps, count, m, n, out, ldx, fin, s);
+}
+
 const float kCoef[3] = {3.4445f, -4.7750f, 2.0315f};
 
 // The fused form: W columns a CTA, `ctas` of them (2, 4, 8 or 16, or 1).
@@ -1188,21 +1224,19 @@ sg_status run(Source<TS> src, int32_t count, int32_t rows, int32_t cols, int32_t
              map_f16(&mb[i].xhi, x[i].hi, n, m, count, L.ldx, kBK) &&
              map_f16(&mb[i].xlo, x[i].lo, n, m, count, L.ldx, kBK);
     if (!ok) return fail(SG_ERR_CUDA, "orthogonalise: tensor map encoding failed");
-    // 256-column tiles read each operand row half as often; 128-column ones
-    // when the wide ones would not give every SM a tile
-    const bool wide = cdiv(n, 256) * cdiv(m, kTile) * count >= num_sms() * 3 / 4;
+    // 256-column tiles read B least often, when they give three SMs of four a
+    // tile; 64-column ones are the quickest when even they leave SMs idle
+    // (1001 x 603: 80 tiles of 64 columns against 40 of 128)
+    const int64_t bands = cdiv(m, kTile) * count;
+    const int bn = cdiv(n, 256) * bands >= num_sms() * 3 / 4 ? 256 : cdiv(n, 64) * bands <= num_sms() ? 64 : 128;
     for (int32_t k = 0; k < steps; ++k) {
         const float* c = coef ? coef + 3 * k : kCoef;
         sg_status st = run_sym<GRAM>(mx[k & 1], count, m, n, c, a, a, L.lda, s);
         if (st == SG_OK) st = run_sym<SQUARE>(ma, count, m, m, c, a, b, L.lda, s);
         if (st != SG_OK) return st;
         const Planes to = x[(k & 1) ^ 1];
-        if (k + 1 < steps)
-            st = wide ? launch_apply<256, float, false>(mb[k & 1], count, m, n, to, L.ldx, fin, s)
-                      : launch_apply<128, float, false>(mb[k & 1], count, m, n, to, L.ldx, fin, s);
-        else
-            st = wide ? launch_apply<256, TW, true>(mb[k & 1], count, m, n, to, L.ldx, fin, s)
-                      : launch_apply<128, TW, true>(mb[k & 1], count, m, n, to, L.ldx, fin, s);
+        st = k + 1 < steps ? run_apply<float, false>(bn, mb[k & 1], count, m, n, to, L.ldx, fin, s)
+                           : run_apply<TW, true>(bn, mb[k & 1], count, m, n, to, L.ldx, fin, s);
         if (st != SG_OK) return st;
     }
     return SG_OK;
