@@ -451,6 +451,7 @@ struct FinalArgs {
     float keep, step;
     int64_t ld_out;
     int32_t tall;
+    int32_t vec;  // rows of w and out are on boundaries of 4 elements
 };
 
 template <int BN>
@@ -669,29 +670,35 @@ __device__ __forceinline__ void reduce_rows(uint32_t da, uint32_t rank, uint8_t*
     }
 }
 
-// 8 elements of U for X[i][8 c ..] (0 outside the matrix): consecutive in
-// memory, or (tall) one from each of 8 rows.  vec: such runs may be read 16
-// bytes at a time.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int64_t ld, bool tall, int32_t valid, bool vec, float (&v)[8]) {
-    if (!tall && vec && valid >= 8) {
-        if constexpr (sizeof(T) == 4) {
-            const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        } else {
-            const uint4 a = *reinterpret_cast<const uint4*>(p);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// 8 consecutive elements, 16 bytes at a time.
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                v[2 * k] = __uint_as_float(w[k] << 16);
-                v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-            }
-        }
-        return;
+    for (int k = 0; k < 4; ++k) {
+        v[2 * k] = __uint_as_float(w[k] << 16);
+        v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
     }
-    const int64_t step = tall ? ld : 1;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = k < valid ? to_f(p[k * step]) : 0.f;
+}
+__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&v)[4]) {
+    const uint2 a = *reinterpret_cast<const uint2*>(p);
+    v[0] = __uint_as_float(a.x << 16), v[1] = __uint_as_float(a.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(a.y << 16), v[3] = __uint_as_float(a.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
 struct Steps {
@@ -707,7 +714,7 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
     __shared__ uint32_t tmem_base;
     __shared__ float norm[kFusedMaxCtas];
     __shared__ float red[kFusedThreads<W> / 32];
-    constexpr int kNT = kFusedThreads<W>, kXTiles = W / 64, kChunks = kFusedM * W / 8 / kNT;  // 16-byte chunks of X a thread handles
+    constexpr int kNT = kFusedThreads<W>, kWarps = kNT / 32, kXTiles = W / 64, kChunks = kFusedM * W / 8 / kNT;  // 16-byte chunks of X a thread handles
     pdl_start();
     const int warp = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31);
     const uint32_t rank = cluster_rank();
@@ -744,38 +751,67 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
         return tall ? (q * rows + j) * ld + i : (q * rows + i) * ld + j;
     };
     const auto valid_of = [&](int it) { return row_of(it) < m ? n - j0 - chunk_of(it) * 8 : 0; };
+    // Wide: every chunk is whole or empty and its rows may be read 16 bytes at a
+    // time.  (Nothing else may write the registers of a load on its way, not
+    // even for other lanes, or the loads wait for one another.)
+    const bool wide = !tall && n % 8 == 0 && (src.vec & 1) && (!src.mom_out || (src.vec & 2));
     float u[kChunks][8];
     float sq = 0.f;
 #pragma unroll
     for (int it = 0; it < kChunks; ++it)
-        load8(src.g + (valid_of(it) > 0 ? place(it, src.ld) : 0), src.ld, tall, valid_of(it), (src.vec & 1) != 0, u[it]);
-    if (src.mom_out) {
-        constexpr int kBatch = 4;  // chunks whose momentum is in registers at once
 #pragma unroll
-        for (int i0 = 0; i0 < kChunks; i0 += kBatch) {
-            float mo[kBatch][8];
+        for (int k = 0; k < 8; ++k) u[it][k] = 0.f;
+    constexpr int kBatch = 4;  // chunks whose momentum is in registers at once
+    if (wide) {
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int it = i0 + i;
-                load8(src.mom + (valid_of(it) > 0 ? place(it, cols) : 0), cols, tall, valid_of(it), (src.vec & 2) != 0, mo[i]);
-            }
+        for (int it = 0; it < kChunks; ++it)
+            if (valid_of(it) > 0) load8(src.g + place(it, src.ld), u[it]);
+        if (src.mom_out) {
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int it = i0 + i;
+            for (int i0 = 0; i0 < kChunks; i0 += kBatch) {
+                float mo[kBatch][8] = {};
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    mo[i][k] = src.mu * mo[i][k] + u[it][k];
-                    u[it][k] = src.nesterov ? u[it][k] + src.mu * mo[i][k] : mo[i][k];
+                for (int i = 0; i < kBatch; ++i)
+                    if (valid_of(i0 + i) > 0) load8(src.mom + place(i0 + i, cols), mo[i]);
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        mo[i][k] = src.mu * mo[i][k] + u[i0 + i][k];
+                        u[i0 + i][k] = src.nesterov ? u[i0 + i][k] + src.mu * mo[i][k] : mo[i][k];
+                    }
+                    if (valid_of(i0 + i) > 0) {
+                        float* p = src.mom_out + place(i0 + i, cols);
+                        *reinterpret_cast<float4*>(p) = make_float4(mo[i][0], mo[i][1], mo[i][2], mo[i][3]);
+                        *reinterpret_cast<float4*>(p + 4) = make_float4(mo[i][4], mo[i][5], mo[i][6], mo[i][7]);
+                    }
                 }
-                float* p = src.mom_out + (valid_of(it) > 0 ? place(it, cols) : 0);
-                if (!tall && (src.vec & 2) && valid_of(it) >= 8) {
-                    *reinterpret_cast<float4*>(p) = make_float4(mo[i][0], mo[i][1], mo[i][2], mo[i][3]);
-                    *reinterpret_cast<float4*>(p + 4) = make_float4(mo[i][4], mo[i][5], mo[i][6], mo[i][7]);
-                } else {
+            }
+        }
+    } else {
+        const int64_t step_g = tall ? src.ld : 1, step_m = tall ? cols : 1;
+#pragma unroll
+        for (int it = 0; it < kChunks; ++it)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < valid_of(it)) u[it][k] = to_f(src.g[place(it, src.ld) + k * step_g]);
+        if (src.mom_out) {
+#pragma unroll
+            for (int i0 = 0; i0 < kChunks; i0 += kBatch) {
+                float mo[kBatch][8] = {};
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        if (k < valid_of(it)) p[tall ? (int64_t)k * cols : k] = mo[i][k];
-                }
+                        if (k < valid_of(i0 + i)) mo[i][k] = src.mom[place(i0 + i, cols) + k * step_m];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        mo[i][k] = src.mu * mo[i][k] + u[i0 + i][k];
+                        u[i0 + i][k] = src.nesterov ? u[i0 + i][k] + src.mu * mo[i][k] : mo[i][k];
+                        if (k < valid_of(i0 + i)) src.mom_out[place(i0 + i, cols) + k * step_m] = mo[i][k];
+                    }
             }
         }
     }
@@ -812,22 +848,6 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
             *reinterpret_cast<uint4*>(xs + kXLo + chunk_at(row_of(it), chunk_of(it))) = lo;
         }
     }
-    // element e of the output for this thread: rows (columns of X when tall) go
-    // to warps in turn, 32 neighbours to its lanes
-    const TW* w = (const TW*)fin.w;
-    TW* o = (TW*)fin.out;
-    const int32_t wn = min(W, n - j0);  // columns of X here
-    constexpr int kOut = kFusedM * W / kNT, kWarps = kNT / 32;
-    const auto out_at = [&](int e, bool& in) -> int64_t {
-        if (tall) {
-            const int c = warp + kWarps * (e / 4), r = lane + 32 * (e % 4);
-            in = c < wn && r < m;
-            return (q * n + j0 + c) * fin.ld_out + r;
-        }
-        const int r = warp + kWarps * (e / (W / 32)), c = lane + 32 * (e % (W / 32));
-        in = c < wn && r < m;
-        return (q * m + r) * fin.ld_out + j0 + c;
-    };
     const uint32_t xa = smem_addr(xs), aa = smem_addr(as), da = smem_addr(dump);
     const int row = (warp & 3) * 32 + lane;  // of tensor memory, in every pass over it
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -984,39 +1004,69 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
     }
     // out = keep w + step X, through shared memory so that rows go out whole;
     // the weights are all on their way before that
-    float wr[kOut];
-    if (w) {
-#pragma unroll
-        for (int e = 0; e < kOut; ++e) {
-            bool in;
-            const int64_t at = out_at(e, in);
-            wr[e] = in ? to_f(w[at]) : 0.f;
-        }
-    }
-    float* tile = dump;  // [row][W + 1], or [column][129] when tall: A's place is free too
+    const TW* w = (const TW*)fin.w;
+    TW* o = (TW*)fin.out;
+    const int32_t wn = min(W, n - j0);  // columns of X here
+    const float mul = fin.step * (1.f / (kScale * kScale));
+    float* tile = dump;  // A's place, and X's, are free too
     if constexpr (W == 128) tile = reinterpret_cast<float*>(as);
     if constexpr (W == 256) tile = reinterpret_cast<float*>(xs);
-    const int ld_row = tall ? 1 : W + 1, ld_col = tall ? kFusedM + 1 : 1;
-#pragma unroll 1
-    for (int c0 = part * (W * 4 / kWarps); c0 < (part + 1) * (W * 4 / kWarps); c0 += 32) {
-        float v[32];
-        tmem_load_32(tmem + lanes + (uint32_t)c0, v);
+    constexpr int kCols = W * 4 / kWarps;  // columns a warp takes of tensor memory
+    if (!tall && wn % 4 == 0 && fin.vec) {
+        // 4 columns at a time: [row][W + 4]
+        constexpr int kFours = kFusedM * W / 4 / kNT, kRow = W / 4;
+        float wr[kFours][4] = {};
+        if (w) {
 #pragma unroll
-        for (int t = 0; t < 32; ++t) tile[row * ld_row + (c0 + t) * ld_col] = v[t];
+            for (int e = 0; e < kFours; ++e) {
+                const int t = e * kNT + (int)threadIdx.x, r = t / kRow, c = t % kRow * 4;
+                if (r < m && c < wn) load4(w + (q * m + r) * fin.ld_out + j0 + c, wr[e]);
+            }
+        }
+#pragma unroll 1
+        for (int c0 = part * kCols; c0 < (part + 1) * kCols; c0 += 32) {
+            float v[32];
+            tmem_load_32(tmem + lanes + (uint32_t)c0, v);
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+                *reinterpret_cast<float4*>(tile + row * (W + 4) + c0 + 4 * t) =
+                    make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < kFours; ++e) {
+            const int t = e * kNT + (int)threadIdx.x, r = t / kRow, c = t % kRow * 4;
+            if (r >= m || c >= wn) continue;
+            const float4 x = *reinterpret_cast<const float4*>(tile + r * (W + 4) + c);
+            float v[4] = {mul * x.x, mul * x.y, mul * x.z, mul * x.w};
+            if (w) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = fin.keep * wr[e][k] + v[k];
+            }
+            store4(o + (q * m + r) * fin.ld_out + j0 + c, v);
+        }
+    } else {
+        // one element at a time: [row][W + 1], or [column][129] when tall
+        const int ld_row = tall ? 1 : W + 1, ld_col = tall ? kFusedM + 1 : 1;
+#pragma unroll 1
+        for (int c0 = part * kCols; c0 < (part + 1) * kCols; c0 += 32) {
+            float v[32];
+            tmem_load_32(tmem + lanes + (uint32_t)c0, v);
+#pragma unroll
+            for (int t = 0; t < 32; ++t) tile[row * ld_row + (c0 + t) * ld_col] = v[t];
+        }
+        __syncthreads();
+        const int lines = tall ? wn : m, width = tall ? m : wn;  // rows of the output here
+        for (int l = warp; l < lines; l += kWarps) {
+            const int64_t at = tall ? (q * n + j0 + l) * fin.ld_out : (q * m + l) * fin.ld_out + j0;
+            const float* x = tile + l * (tall ? kFusedM + 1 : W + 1);
+#pragma unroll 4
+            for (int c = lane; c < width; c += 32) put(o + at + c, w ? fin.keep * to_f(w[at + c]) + mul * x[c] : mul * x[c]);
+        }
     }
     tmem_fence_before();
     __syncthreads();
     if (warp == 1) tmem_free<(W > 128 ? W : 128)>(tmem);
-    const float mul = fin.step * (1.f / (kScale * kScale));
-#pragma unroll
-    for (int e = 0; e < kOut; ++e) {
-        bool in;
-        const int64_t at = out_at(e, in);
-        if (!in) continue;
-        const float x = mul * (tall ? tile[lane + 32 * (e % 4) + (warp + kWarps * (e / 4)) * (kFusedM + 1)]
-                                    : tile[(warp + kWarps * (e / (W / 32))) * (W + 1) + lane + 32 * (e % (W / 32))]);
-        put(o + at, w ? fin.keep * wr[e] + x : x);
-    }
 }
 
 // -------------------------------------------------------------------- host
@@ -1176,7 +1226,8 @@ sg_status run(Source<TS> src, int32_t count, int32_t rows, int32_t cols, int32_t
               const TW* w, float keep, float step, TW* out, int64_t ld_out, char* ws, cudaStream_t s) {
     const Layout L = layout(count, rows, cols);
     const int32_t m = (int32_t)L.m, n = (int32_t)L.n;
-    const FinalArgs fin = {w, out, keep, step, ld_out, rows > cols ? 1 : 0};
+    const FinalArgs fin = {w, out, keep, step, ld_out, rows > cols ? 1 : 0,
+                           (((uintptr_t)w | (uintptr_t)out) % (4 * sizeof(TW)) == 0 && ld_out % 4 == 0) ? 1 : 0};
     // a matrix that the shared memory of one cluster holds is done in one
     // launch: up to 256 columns by one CTA, which has nothing to exchange; else
     // 64 columns a CTA while 16 CTAs reach, since each product and each pass
