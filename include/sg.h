@@ -569,7 +569,7 @@ size_t sg_sage_bwd_workspace(int32_t n_cap, int32_t dim, int32_t dtype);
  * and a zero row where ids[i] = -1 (padding).  The product is taken in fp32 and
  * rounded once to dtype_out.
  *   d_table   device [n_rows x dim], row stride ld_table elements (>= dim)
- *   d_ids     device int32 [n_cap]; in a pipeline the sampler's unique array,
+ *   d_ids     device int32 [n_cap], n_cap below 2^30; in a pipeline the sampler's unique array,
  *             so that out holds the input nodes' rows
  *   d_n       device int32 count (n = *d_n <= n_cap) or NULL (n = n_cap)
  *   d_out     device [n_cap x dim], row stride ld_out (>= dim); must not overlap
