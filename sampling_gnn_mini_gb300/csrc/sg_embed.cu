@@ -429,18 +429,21 @@ __global__ void __launch_bounds__(kThreads) k_runs(const uint2* __restrict__ kv,
 
 // All of it for a short list, in one block: 8 items a thread, passes in shared
 // memory.
+template <int ITEMS>
 __global__ void __launch_bounds__(kSmallThreads) k_sort_small(const int32_t* __restrict__ ids, int64_t n_rows,
                                                               int32_t n_cap, const int32_t* __restrict__ d_n, Digits dg,
                                                               int32_t span, uint2* __restrict__ out,
                                                               int32_t* __restrict__ starts, int32_t* __restrict__ n_out) {
     pdl_start();
-    constexpr int kItems = kSmallSort / kSmallThreads, kWarps = kSmallThreads / 32;
+    constexpr int kItems = ITEMS, kWarps = kSmallThreads / 32, kParts = kSmallThreads / kDigits, kPer = kWarps / kParts;
     extern __shared__ __align__(16) uint8_t dsm[];
     uint32_t* key = reinterpret_cast<uint32_t*>(dsm);                            // [kSmallSort]
     uint16_t* pos = reinterpret_cast<uint16_t*>(key + kSmallSort);               // [kSmallSort]
     uint16_t(*cnt)[kDigits] = reinterpret_cast<uint16_t(*)[kDigits]>(pos + kSmallSort);  // [kWarps][kDigits]
     __shared__ uint32_t sh[kWarps + 1];
+    __shared__ uint32_t psum[kParts][kDigits];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int digit = threadIdx.x % kDigits, q4 = threadIdx.x / kDigits;  // a digit, and kPer of the warps
     const int32_t n = (int32_t)count_of(d_n, n_cap);
     uint32_t k[kItems], v[kItems], rank[kItems], total;
     int32_t d[kItems];
@@ -462,15 +465,26 @@ __global__ void __launch_bounds__(kSmallThreads) k_sort_small(const int32_t* __r
         warp_rank<kItems>(d, cnt[warp], rank);
         __syncthreads();
         uint32_t mine = 0;
-        if (threadIdx.x < kDigits)
-            for (int w = 0; w < kWarps; ++w) mine += cnt[w][threadIdx.x];
-        uint32_t run = block_excl_scan<kSmallThreads, uint32_t>(mine, sh, total);
-        if (threadIdx.x < kDigits)
-            for (int w = 0; w < kWarps; ++w) {
-                const uint32_t c = cnt[w][threadIdx.x];
-                cnt[w][threadIdx.x] = (uint16_t)run;
-                run += c;
-            }
+#pragma unroll
+        for (int w = 0; w < kPer; ++w) mine += cnt[q4 * kPer + w][digit];
+        psum[q4][digit] = mine;
+        __syncthreads();
+        uint32_t all = 0, before = 0;
+#pragma unroll
+        for (int p4 = 0; p4 < kParts; ++p4) {
+            all += psum[p4][digit];
+            before += p4 < q4 ? psum[p4][digit] : 0;
+        }
+        const uint32_t e = block_excl_scan<kSmallThreads, uint32_t>(q4 == 0 ? all : 0, sh, total);
+        if (q4 == 0) psum[0][digit] = e;  // (its own total has been read: the scan has barriers)
+        __syncthreads();
+        uint32_t run = psum[0][digit] + before;
+#pragma unroll
+        for (int w = 0; w < kPer; ++w) {
+            const uint32_t c = cnt[q4 * kPer + w][digit];
+            cnt[q4 * kPer + w][digit] = (uint16_t)run;
+            run += c;
+        }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kItems; ++i)
@@ -493,9 +507,10 @@ __global__ void __launch_bounds__(kSmallThreads) k_sort_small(const int32_t* __r
         if (q < n) out[q] = make_uint2(k[i], v[i]);
     }
     if (!n_out) return;
-    const int32_t p0 = (int32_t)threadIdx.x * kItems;  // run starts, 8 positions a thread
+    constexpr int kEight = 8;  // run starts, 8 positions a thread
+    const int32_t p0 = (int32_t)threadIdx.x * kEight;
     uint32_t prev = p0 > 0 && p0 - 1 < n ? key[p0 - 1] : kNoKey, mine = 0;
-    for (int q = 0; q < kItems; ++q) {
+    for (int q = 0; q < kEight; ++q) {
         const uint32_t x = p0 + q < n ? key[p0 + q] : kNoKey;
         mine += x < (uint32_t)n_rows && x != prev;
         prev = x;
@@ -554,14 +569,31 @@ __device__ __forceinline__ void put_row(const SumArgs<TO>& a, uint32_t key, int3
 }
 
 // Zero rows for the IDs that do not occur: a warp looks 32 IDs up in the
-// sorted list, a lane each.
+// sorted list, a lane each, first among kSamples keys that the block has taken
+// at equal distances into shared memory (a search in memory alone costs a
+// latency a step: 16 for 65,536 positions, instead of 5).
+constexpr int kSamples = 2048;
 template <typename TO, int VEC>
-__device__ __forceinline__ void zero_rows(const SumArgs<TO>& a, int64_t n, int32_t block) {
+__device__ __forceinline__ void zero_rows(const SumArgs<TO>& a, int64_t n, int32_t block, uint32_t* sample) {
     const int lane = (int)lane_id();
+    const int64_t every = n > kSamples ? cdiv(n, kSamples) : 1;
+    const int32_t samples = n > 0 ? (int32_t)cdiv(n, every) : 0;
+#pragma unroll
+    for (int u = 0; u < kSamples / kThreads; ++u) {
+        const int32_t i = u * kThreads + (int32_t)threadIdx.x;
+        if (i < samples) sample[i] = __ldg(&a.kv[i * every].x);
+    }
+    __syncthreads();
     const int64_t r0 = ((int64_t)block * (kThreads / 32) + (threadIdx.x >> 5)) * 32;
     if (r0 >= a.n_rows) return;
     const uint32_t id = (uint32_t)(r0 + lane);
-    int64_t lo = 0, hi = n;
+    int32_t s0 = 0, s1 = samples;  // first sample that is not below id
+    while (s0 < s1) {
+        const int32_t mid = (s0 + s1) >> 1;
+        if (sample[mid] < id) s0 = mid + 1;
+        else s1 = mid;
+    }
+    int64_t lo = s0 > 0 ? (s0 - 1) * every + 1 : 0, hi = s0 < samples ? s0 * every : n;
     while (lo < hi) {
         const int64_t mid = (lo + hi) >> 1;
         if (__ldg(&a.kv[mid].x) < id) lo = mid + 1;
@@ -591,7 +623,7 @@ __global__ void __launch_bounds__(kThreads) k_embed_sum(const TI* __restrict__ g
         // zero blocks are spread evenly over the grid: their look-ups are latency, the sums bandwidth
         const int32_t z = (int32_t)(((int64_t)block * a.zero_blocks) / gridDim.x);
         if ((int32_t)(((int64_t)(block + 1) * a.zero_blocks) / gridDim.x) != z) {
-            zero_rows<TO, VEC>(a, n, z);
+            zero_rows<TO, VEC>(a, n, z, reinterpret_cast<uint32_t*>(kv));
             return;
         }
         block -= z;
@@ -820,7 +852,7 @@ bool long_chunks(int64_t n_cap, int lanes) { return n_cap >= kLongChunks && lane
 struct BwdLayout {
     int64_t tiles;       // bound on the sum's tiles (the narrowest tile: 32 lanes)
     int64_t sort_tiles;  // bound on a pass's tiles
-    size_t kv0, kv1, state, status, run_status, starts, head, tail, clear, total;  // clear: bytes from state on
+    size_t kv0, kv1, state, status, run_status, starts, head, tail, total;  // state .. status: cleared for a sort
 };
 
 BwdLayout bwd_layout(int64_t n_cap, int32_t dim) {
@@ -838,7 +870,6 @@ BwdLayout bwd_layout(int64_t n_cap, int32_t dim) {
     L.state = put(sizeof(SortState));
     L.run_status = put((size_t)cdiv(n_cap, kRunTile) * 8);
     L.status = put((size_t)L.sort_tiles * kDigits * kMaxPasses * 4);
-    L.clear = o - L.state;
     L.starts = put((size_t)(L.tiles + 2) * 4);
     L.head = put((size_t)L.tiles * dim * 4);
     L.tail = put((size_t)L.tiles * dim * 4);
@@ -886,29 +917,40 @@ sg_status run_sort(const int32_t* ids, int64_t n_cap, const int32_t* d_n, int64_
     dg.per = (bits + dg.passes - 1) / dg.passes;
     *sorted = kv[0];
     if (n_cap <= kSmallSort) {
+        const int32_t items = (int32_t)cdiv(n_cap, kSmallThreads);  // a thread
+        const auto go = [&](auto kernel) {
+            return launch_pdl(kernel, dim3(1), dim3(kSmallThreads), kSmallSmem, s, ids, n_rows, (int32_t)n_cap, d_n, dg,
+                              span, kv[0], starts, rows ? n_out : nullptr);
+        };
         static bool set = false;
         if (!set) {
-            SG_CUDA(cudaFuncSetAttribute(k_sort_small, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem));
+            SG_CUDA(cudaFuncSetAttribute(k_sort_small<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem));
+            SG_CUDA(cudaFuncSetAttribute(k_sort_small<3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem));
+            SG_CUDA(cudaFuncSetAttribute(k_sort_small<5>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem));
+            SG_CUDA(cudaFuncSetAttribute(k_sort_small<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem));
             set = true;
         }
-        SG_CUDA(launch_pdl(k_sort_small, dim3(1), dim3(kSmallThreads), kSmallSmem, s, ids, n_rows, (int32_t)n_cap, d_n,
-                           dg, span, kv[0], starts, rows ? n_out : nullptr));
+        SG_CUDA(items <= 1   ? go(k_sort_small<1>)
+                : items <= 3 ? go(k_sort_small<3>)
+                : items <= 5 ? go(k_sort_small<5>)
+                             : go(k_sort_small<8>));
         return SG_OK;
     }
-    SG_CUDA(cudaMemsetAsync(ws + L.state, 0, L.clear, s));
-    const int64_t hb = cdiv(n_cap, kThreads * 8) < num_sms() * 2 ? cdiv(n_cap, kThreads * 8) : num_sms() * 2;
-    SG_CUDA(launch_pdl(k_sort_hist, dim3((unsigned)hb), dim3(kThreads), 0, s, ids, n_rows, n_cap, d_n, dg, st));
     // 8 items a thread once that still gives every SM a tile
     const bool big = n_cap >= (int64_t)num_sms() * kSortThreads * 8;
+    const int64_t tiles = cdiv(n_cap, kSortThreads * (big ? 8 : 4));
+    SG_CUDA(cudaMemsetAsync(ws + L.state, 0, L.status - L.state + (size_t)(dg.passes * tiles) * kDigits * 4, s));
+    const int64_t hb = cdiv(n_cap, kThreads * 8) < num_sms() * 2 ? cdiv(n_cap, kThreads * 8) : num_sms() * 2;
+    SG_CUDA(launch_pdl(k_sort_hist, dim3((unsigned)hb), dim3(kThreads), 0, s, ids, n_rows, n_cap, d_n, dg, st));
     for (int p = 0; p < dg.passes; ++p) {
-        uint32_t* status = (uint32_t*)(ws + L.status) + (int64_t)p * L.sort_tiles * kDigits;
+        uint32_t* status = (uint32_t*)(ws + L.status) + p * tiles * kDigits;
         const uint2* in = p ? kv[(p & 1) ^ 1] : nullptr;
         uint2* out = kv[p & 1];
         if (big)
-            SG_CUDA(launch_pdl(k_sort_pass<8>, dim3((unsigned)cdiv(n_cap, kSortThreads * 8)), dim3(kSortThreads), 0, s, ids, in,
+            SG_CUDA(launch_pdl(k_sort_pass<8>, dim3((unsigned)tiles), dim3(kSortThreads), 0, s, ids, in,
                                n_rows, n_cap, d_n, p, (int)dg.per, st, status, out));
         else
-            SG_CUDA(launch_pdl(k_sort_pass<4>, dim3((unsigned)cdiv(n_cap, kSortThreads * 4)), dim3(kSortThreads), 0, s, ids, in,
+            SG_CUDA(launch_pdl(k_sort_pass<4>, dim3((unsigned)tiles), dim3(kSortThreads), 0, s, ids, in,
                                n_rows, n_cap, d_n, p, (int)dg.per, st, status, out));
         *sorted = out;
     }

@@ -83,7 +83,7 @@ cudaError_t dev_alloc(void** p, size_t bytes);
 // one's blocks exit.
 __device__ __forceinline__ void pdl_start() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Lets the next grid of the stream be scheduled once every block of this one
-// has got here (the steps of sg_muon.cu, whose kernels follow one another):
+// has got here (the steps of sg_muon.cu):
 // its blocks take the SMs as this grid's leave them, set up, and wait in
 // pdl_start() as above.  The stream's order is kept: a kernel that calls this
 // still waits for its own predecessor before it ends.
