@@ -40,7 +40,7 @@ constexpr int kSortThreads = 512;     // of a pass
 constexpr int kSmallSort = 8192;      // positions sorted by one block
 constexpr int kSmallThreads = 1024;
 constexpr int kRunTile = kThreads * 16;   // sorted positions a block of k_runs looks at
-constexpr int kLongChunks = 65536;    // positions from which a chunk is 32 long, not 8
+constexpr int kFewBlocks = 76;           // half the SMs: below this many blocks chunks are 8 positions, not 32
 constexpr uint32_t kNoKey = 0xFFFFFFFFu;  // beside the list's ends
 
 size_t a256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kThreads) k_runs(const uint2* __restrict__ kv,
     }
 }
 
-// All of it for a short list, in one block: 8 items a thread, passes in shared
+// All of it for a short list, in one block: up to 8 items a thread, passes in shared
 // memory.
 template <int ITEMS>
 __global__ void __launch_bounds__(kSmallThreads) k_sort_small(const int32_t* __restrict__ ids, int64_t n_rows,
@@ -845,19 +845,40 @@ sg_status run_fwd(int vec, const void* table, int64_t n_rows, int32_t dim, int64
     return launch_fwd<TI, TO, 1>(table, n_rows, dim, ld_table, ids, n_cap, d_n, scale, out, ld_out, s);
 }
 
-// Chunk length: 32 positions where that still leaves many chunks, else 8 (one
-// batch of loads), so that a short list spreads over the SMs.
-bool long_chunks(int64_t n_cap, int lanes) { return n_cap >= kLongChunks && lanes >= 8; }
+// How the sum is cut for units of vec columns.  A chunk is 32 positions, or 8
+// (one batch of loads) when that leaves too few blocks.  Measured, us for the
+// whole gradient, 8 / 32: 256 fp32 columns, 4,999 positions (40 blocks of 32)
+// 28 / 31, 20,000 (158 blocks) 43 / 42; 1024 bf16 columns, 4,999 positions (80
+// blocks) 49 / 40, 65,536 (1,024 blocks) 85 / 75.
+struct Cut {
+    int32_t units, lanes, col_blocks, span;  // span: positions of a tile
+};
+Cut cut_for(int64_t n_cap, int32_t dim, int vec) {
+    Cut c;
+    c.units = dim / vec;
+    c.lanes = 1;
+    while (c.lanes < 32 && c.lanes < c.units) c.lanes *= 2;
+    c.col_blocks = (int32_t)cdiv(c.units, c.lanes);
+    const int32_t chunks = kThreads / c.lanes;
+    const bool wide = c.lanes >= 8 && cdiv(n_cap, chunks * 32) * c.col_blocks >= kFewBlocks;
+    c.span = chunks * (wide ? 32 : 8);
+    return c;
+}
 
 struct BwdLayout {
-    int64_t tiles;       // bound on the sum's tiles (the narrowest tile: 32 lanes)
+    int64_t tiles;       // bound on the sum's tiles
     int64_t sort_tiles;  // bound on a pass's tiles
     size_t kv0, kv1, state, status, run_status, starts, head, tail, total;  // state .. status: cleared for a sort
 };
 
 BwdLayout bwd_layout(int64_t n_cap, int32_t dim) {
     BwdLayout L;
-    L.tiles = cdiv(n_cap, n_cap >= kLongChunks ? 256 : 64);
+    L.tiles = 0;
+    for (int vec = 1; vec <= 8; vec *= 2)  // the strides and addresses decide between units of 1, 4 and 8
+        if (vec != 2 && dim % vec == 0) {
+            const int64_t t = cdiv(n_cap, cut_for(n_cap, dim, vec).span);
+            if (t > L.tiles) L.tiles = t;
+        }
     L.sort_tiles = n_cap <= kSmallSort ? 0 : cdiv(n_cap, kSortThreads * 4);
     size_t o = 0;
     const auto put = [&o](size_t bytes) {
@@ -968,11 +989,11 @@ sg_status run_bwd(const int32_t* ids, int64_t n_cap, const int32_t* d_n, int64_t
     const int vec = vec_for(g, dtype_g, ld_g, grad, dtype_grad, ld_grad, dim);
     SumArgs<TO> a;
     memset(&a, 0, sizeof(a));
-    a.units = dim / vec;
-    a.lanes = 1;
-    while (a.lanes < 32 && a.lanes < a.units) a.lanes *= 2;
-    a.col_blocks = (int32_t)cdiv(a.units, a.lanes);
-    const int32_t span = kThreads / a.lanes * (long_chunks(n_cap, a.lanes) ? 32 : 8);
+    const Cut cut = cut_for(n_cap, dim, vec);
+    a.units = cut.units;
+    a.lanes = cut.lanes;
+    a.col_blocks = cut.col_blocks;
+    const int32_t span = cut.span;
     uint2* sorted = nullptr;
     const sg_status st = run_sort(ids, n_cap, d_n, n_rows, mode == SG_GRAD_ROWS, span, n_out, L, ws, &sorted, s);
     if (st != SG_OK) return st;
