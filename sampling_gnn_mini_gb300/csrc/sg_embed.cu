@@ -568,11 +568,12 @@ __device__ __forceinline__ void put_row(const SumArgs<TO>& a, uint32_t key, int3
     store_vec<VEC>(p, v);
 }
 
-// Zero rows for the IDs that do not occur: a warp looks 32 IDs up in the
+// Zero rows for the IDs that do not occur: a warp looks kZeroRows IDs up in the
 // sorted list, a lane each, first among kSamples keys that the block has taken
 // at equal distances into shared memory (a search in memory alone costs a
 // latency a step: 16 for 65,536 positions, instead of 5).
 constexpr int kSamples = 2048;
+constexpr int kZeroRows = 8;  // few, so that the rows of a wide table spread evenly over the SMs
 template <typename TO, int VEC>
 __device__ __forceinline__ void zero_rows(const SumArgs<TO>& a, int64_t n, int32_t block, uint32_t* sample) {
     const int lane = (int)lane_id();
@@ -584,9 +585,9 @@ __device__ __forceinline__ void zero_rows(const SumArgs<TO>& a, int64_t n, int32
         if (i < samples) sample[i] = __ldg(&a.kv[i * every].x);
     }
     __syncthreads();
-    const int64_t r0 = ((int64_t)block * (kThreads / 32) + (threadIdx.x >> 5)) * 32;
+    const int64_t r0 = ((int64_t)block * (kThreads / 32) + (threadIdx.x >> 5)) * kZeroRows;
     if (r0 >= a.n_rows) return;
-    const uint32_t id = (uint32_t)(r0 + lane);
+    const uint32_t id = (uint32_t)(r0 + lane % kZeroRows);
     int32_t s0 = 0, s1 = samples;  // first sample that is not below id
     while (s0 < s1) {
         const int32_t mid = (s0 + s1) >> 1;
@@ -601,7 +602,7 @@ __device__ __forceinline__ void zero_rows(const SumArgs<TO>& a, int64_t n, int32
     }
     const bool absent = (int64_t)id < a.n_rows && (lo >= n || __ldg(&a.kv[lo].x) != id);
     const float none[VEC] = {};
-    for (unsigned todo = __ballot_sync(0xFFFFFFFFu, absent); todo; todo &= todo - 1) {
+    for (unsigned todo = __ballot_sync(0xFFFFFFFFu, absent && lane < kZeroRows); todo; todo &= todo - 1) {
         TO* p = a.grad + (r0 + __ffs(todo) - 1) * a.ld_grad;
         for (int32_t u = lane; u < a.units; u += 32) store_vec<VEC>(p + (int64_t)u * VEC, none);
     }
@@ -901,7 +902,7 @@ BwdLayout bwd_layout(int64_t n_cap, int32_t dim) {
 template <typename TI, typename TO, int VEC>
 sg_status launch_sum(const void* g, SumArgs<TO> a, int32_t span, cudaStream_t s) {
     const int64_t tiles = cdiv(a.n_cap, span), blocks = tiles * a.col_blocks;
-    const int64_t zero = a.mode == SG_GRAD_DENSE ? cdiv(a.n_rows, kThreads) : 0;
+    const int64_t zero = a.mode == SG_GRAD_DENSE ? cdiv(a.n_rows, kThreads / 32 * kZeroRows) : 0;
     if (blocks + zero > 2147483647LL) return fail(SG_ERR_INVALID_ARG, "sg_embed_bwd: n_cap x dim too large");
     a.zero_blocks = (int32_t)zero;
     if (span * a.lanes == kThreads * 32)
