@@ -451,36 +451,34 @@ __device__ __forceinline__ void reduce_held(Held<T, NT>& h, int32_t count, float
 
 // The warps' (m, z) into every CTA of the cluster, and a barrier.
 template <int NT, int S>
-__device__ __forceinline__ void share_parts(float* pm, float* pz, int32_t rank, float m, float z) {
+__device__ __forceinline__ void share_parts(float2* parts, int32_t rank, float m, float z) {
     const int warp = (int)(threadIdx.x >> 5), lane = (int)lane_id();
     if constexpr (S > 1) {
-        if (lane < S) {
-            const uint32_t slot = (uint32_t)(rank * (NT / 32) + warp) * 4;
-            asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(map_rank(smem_addr(pm) + slot, (uint32_t)lane)), "f"(m)
+        if (lane < S)
+            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};\n" ::"r"(
+                             map_rank(smem_addr(parts + rank * (NT / 32) + warp), (uint32_t)lane)),
+                         "f"(m), "f"(z)
                          : "memory");
-            asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(map_rank(smem_addr(pz) + slot, (uint32_t)lane)), "f"(z)
-                         : "memory");
-        }
         cluster_sync();
     } else {
-        if (lane == 0) pm[warp] = m, pz[warp] = z;
+        if (lane == 0) parts[warp] = make_float2(m, z);
         __syncthreads();
     }
 }
 
 // The row's (M, Z); parts without a finite logit (z = 0) take no part.
 template <int PARTS>
-__device__ __forceinline__ void join_parts(const float* pm, const float* pz, float& M, float& Z) {
+__device__ __forceinline__ void join_parts(const float2* parts, float& M, float& Z) {
     const int lane = (int)lane_id();
     M = -INFINITY, Z = 0.f;
 #pragma unroll
     for (int i = lane; i < PARTS; i += 32)
-        if (pz[i] != 0.f) M = fmaxf(M, pm[i]);
+        if (parts[i].y != 0.f) M = fmaxf(M, parts[i].x);
     M = warp_max(M);
     if (M == -INFINITY) M = 0.f;
 #pragma unroll
     for (int i = lane; i < PARTS; i += 32)
-        if (pz[i] != 0.f) Z += pz[i] * exp_from(pm[i], M);
+        if (parts[i].y != 0.f) Z += parts[i].y * exp_from(parts[i].x, M);
     Z = warp_sum(Z);
 }
 
@@ -518,7 +516,7 @@ template <typename T, int NT, int S>
 __global__ void __launch_bounds__(NT, 1024 / NT) k_xent_row(RowArgs<T> a) {
     pdl_start();
     constexpr int kParts = S * NT / 32;
-    __shared__ float pm[kParts], pz[kParts];  // (m, z) of every warp of the cluster
+    __shared__ __align__(8) float2 parts[kParts];  // (m, z) of every warp of the cluster
     __shared__ bool last;
     const int32_t r = (int32_t)(blockIdx.x / S), rank = (int32_t)(blockIdx.x % S);
     const int32_t n = rows_of(a.d_n, a.n_cap), classes = a.classes;
@@ -565,10 +563,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_xent_row(RowArgs<T> a) {
     }
     // every CTA runs: its shared memory may be written
     if constexpr (S > 1) asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
-    share_parts<NT, S>(pm, pz, rank, h.m, h.z);
+    share_parts<NT, S>(parts, rank, h.m, h.z);
     if (used) {
         float M, Z;
-        join_parts<kParts>(pm, pz, M, Z);
+        join_parts<kParts>(parts, M, Z);
         const float w = a.mean ? a.gs / (float)max(1, *a.valid) : a.gs;
         if (out) {
             const bool same = same_phase(row, (const T*)out);
@@ -613,8 +611,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_xent_stream(RowArgs<T> a, int
     extern __shared__ __align__(128) uint8_t dsm[];
     pdl_start();
     constexpr int kParts = S * NT / 32;
-    __shared__ float pm[2][kParts], pz[2][kParts];  // (m, z) of every warp of the cluster, by row parity
-    __shared__ __align__(8) uint64_t full[2];
+    __shared__ __align__(8) float2 parts[2][kParts];  // (m, z) of every warp of the cluster, by row parity
+    __shared__ __align__(8) uint64_t full[2], met[2];  // buffers; parts
     __shared__ bool last;
     const int32_t rank = (int32_t)(blockIdx.x % S), first = (int32_t)(blockIdx.x / S), step = (int32_t)(gridDim.x / S);
     const int32_t n = rows_of(a.d_n, a.n_cap), classes = a.classes;
@@ -623,6 +621,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_xent_stream(RowArgs<T> a, int
         last = false;
         mbar_init(&full[0], 1);
         mbar_init(&full[1], 1);
+        mbar_init(&met[0], 1);
+        mbar_init(&met[1], 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     __syncthreads();
@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_xent_stream(RowArgs<T> a, int
         fetch(first + step, y1, 1);
     }
     const float w = a.mean ? a.gs / (float)max(1, *a.valid) : a.gs;
-    uint32_t phases = 0;  // bit b: parity of buffer b's next fill
+    uint32_t phases = 0;  // bit b: parity of the next phase of full[b] and met[b]
     int32_t par = 0;
     for (int32_t r = first; r < n; r += step, par ^= 1, y = y1, y1 = y2) {
         y2 = label(r + 2 * step);
@@ -674,17 +674,31 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_xent_stream(RowArgs<T> a, int
         h.xe = edge >= 0 ? to_f(row[edge]) : -INFINITY;
         const float xy = owner ? to_f(row[y]) : 0.f;
         if (!mbar_wait(&full[par], (phases >> par) & 1u) && lane_id() == 0) dev_err(ERR_TIMEOUT);
-        phases ^= 1u << par;
         const uint4* buf = reinterpret_cast<const uint4*>(dsm) + par * slots + threadIdx.x;
 #pragma unroll
         for (int k = 0; k < kVecs; ++k)
             h.x[k] = (int32_t)threadIdx.x + k * NT < count ? buf[k * NT] : empty_part<T>();
         reduce_held(h, count, -INFINITY, 0.f);
-        share_parts<NT, S>(pm[par], pz[par], rank, h.m, h.z);
+        // The parts meet by asynchronous stores that complete on the receiver's
+        // barrier.  (A cluster barrier here would first wait for this row's
+        // predecessor's gradient to be stored: with one, 144 us and the memory
+        // fence the largest stall.)  A slot is written again two rows later, when
+        // its readers have sent the row between.
+        if (threadIdx.x == 0) mbar_expect_tx(&met[par], kParts * 8);
+        if (lane_id() < S) {
+            const uint32_t slot = smem_addr(&parts[par][rank * (NT / 32) + (threadIdx.x >> 5)]);
+            asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];\n" ::"r"(
+                             map_rank(slot, lane_id())),
+                         "f"(h.m), "f"(h.z), "r"(map_rank(smem_addr(&met[par]), lane_id()))
+                         : "memory");
+        }
+        __syncwarp();
+        if (!mbar_wait(&met[par], (phases >> par) & 1u) && lane_id() == 0) dev_err(ERR_TIMEOUT);
+        phases ^= 1u << par;
         // every thread has its vectors in registers: the buffer is free
         if (threadIdx.x == 0) fetch(r + 2 * step, y2, par);
         float M, Z;
-        join_parts<kParts>(pm[par], pz[par], M, Z);
+        join_parts<kParts>(parts[par], M, Z);
         if (out) {
             const float inv = h.z == 0.f || Z == 0.f ? 0.f : w / Z * exp_from(h.m, M);
             store_held(h, out + part.head + v0 * kE<T>, count, same_phase(row, (const T*)out), inv);
