@@ -652,16 +652,17 @@ sg_status sg_xent(const void* d_logits, int32_t dtype, int32_t n_cap, const int3
  * Every singular value t of G / (||G||_F + eps) becomes f_k(..f_1(t)),
  * f(t) = a t + b t^3 + c t^5.  The products run on the tensor cores with each
  * operand held as two fp16 terms (22 bits), fp32 accumulation; the norm is
- * summed in fp32 and fp64.
+ * summed in fp32 (of squares: norms from about 1e-18 to 1e19).
  *   d_g, d_out  device, `dtype` (SG_F32 or SG_BF16); matrix q starts at element
  *               q * rows * ld, its rows are ld (>= cols) elements apart
  *               (ld_out for d_out).  d_out may be d_g with the same stride.
  *   rows, cols  1 .. 65536; the smaller one at most 8192
  *   steps       0 .. SG_MAX_NS_STEPS
  *   h_coef      host, 3 * steps floats (a, b, c of each step), or NULL for
- *               (3.4445, -4.7750, 2.0315) in every step.  |values| up to about
- *               64 can be held on the way; a schedule that diverges gives inf
- *               or NaN.
+ *               (3.4445, -4.7750, 2.0315) in every step.  Singular values up to
+ *               15 and entries of a I + b A + c A A up to 255 can be held on the
+ *               way; a schedule that goes beyond gives inf or NaN.
+ *   eps         > 0 for a zero matrix to give zeros
  *   d_workspace device scratch of sg_orthogonalise_workspace(...) bytes,
  *               256-byte aligned, in no particular state */
 size_t sg_orthogonalise_workspace(int32_t count, int32_t rows, int32_t cols);
@@ -674,8 +675,9 @@ sg_status sg_orthogonalise(const void* d_g, int32_t dtype, int32_t count, int32_
  *   m' = momentum * m + g;   u = nesterov ? g + momentum * m' : m'
  *   w' = (1 - rate * weight_decay) * w - rate * scale * orthogonalise(u)
  * with orthogonalise as above (scale 1).
- *   d_w, d_w_out   device, dtype_w (SG_F32 or SG_BF16); may be the same array
- *   d_g            device fp32; d_m, d_m_out device fp32, may be the same array
+ *   d_w, d_w_out   device, dtype_w (SG_F32 or SG_BF16); may be the same array,
+ *                  but must not overlap in any other way
+ *   d_g            device fp32; d_m, d_m_out device fp32, likewise
  * All arrays hold count x rows x cols elements without gaps.  Other arguments
  * as in sg_orthogonalise (and its workspace). */
 sg_status sg_muon_step(const void* d_w, int32_t dtype_w, const float* d_g, const float* d_m, int32_t count, int32_t rows,

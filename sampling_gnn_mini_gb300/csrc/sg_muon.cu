@@ -15,6 +15,12 @@
 // subnormals, and the pair carries 22 bits.  A product is three tensor-core
 // products, hi hi + hi lo + lo hi, with fp32 accumulation in tensor memory.
 // Folding a I into B makes X <- B X one product with nothing to add.
+// The tensor core cuts a sum's low bits at every accumulation, always towards
+// zero: with all 3 x 256 accumulations of a 4096-deep product in one place the
+// result of 1024 x 4096 was off by 1.9e-5, an fp32 product's by 3.2e-6 (the
+// pairs themselves, in exact arithmetic: 5e-7).  So the two cross products,
+// 2^-11 as large, have an accumulator of their own, and hi hi is taken out of
+// tensor memory every 16 or 32 accumulations and summed in registers.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -35,6 +41,10 @@ constexpr float kScale = 256.f;  // of every fp16 pair
 constexpr int kTile = 128;       // rows of an output tile (and columns of a symmetric one)
 constexpr int kBK = 64;          // K elements of a stage: one 128-byte swizzle row
 constexpr int kOperand = kTile * kBK * 2;  // bytes of one operand tile: 16 KB
+// A product's block: kSumWarps warps sum and write the tile, one more feeds the
+// copies, one the tensor core.
+constexpr int kSumWarps = kThreads / 32;
+constexpr int kProductThreads = kThreads + 64;
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -210,7 +220,8 @@ struct PairMaps {
 // Ring of kStages stages of BYTES; a full and an empty barrier a stage.
 template <int STAGES>
 struct Ring {
-    uint64_t full[STAGES], empty[STAGES], done;
+    uint64_t full[STAGES], empty[STAGES];
+    uint64_t sum[2], read[2];  // hi hi's accumulators: complete, and taken out
 };
 
 template <int STAGES>
@@ -219,8 +230,64 @@ __device__ __forceinline__ void ring_init(Ring<STAGES>& r) {
         mbar_init(&r.full[s], 1);
         mbar_init(&r.empty[s], 1);
     }
-    mbar_init(&r.done, 1);
+    for (int b = 0; b < 2; ++b) {
+        mbar_init(&r.sum[b], 1);
+        mbar_init(&r.read[b], kSumWarps);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+}
+
+// How hi hi is summed: kBufs accumulators of COLS columns in turn, kTurn K tiles
+// (4 accumulations each) in each; the accumulator of the cross products is at
+// column 512 - COLS.  (At 256 columns there is room for one only, and the
+// products wait while it is read, so it is read half as often.)
+template <int COLS>
+constexpr int kBufs = COLS > 128 ? 1 : 2;
+template <int COLS>
+constexpr int kTurn = COLS > 128 ? 8 : 4;
+
+// K tile i of the products: waits for its accumulator if it is the tile that
+// begins a turn; returns it.
+template <int COLS, int STAGES>
+__device__ __forceinline__ uint32_t turn_begin(Ring<STAGES>& r, uint32_t tmem, int i, bool& ok) {
+    const int turn = i / kTurn<COLS>, b = turn % kBufs<COLS>;
+    if (i % kTurn<COLS> == 0 && turn >= kBufs<COLS> && !mbar_wait(&r.read[b], (uint32_t)(turn / kBufs<COLS> - 1) & 1u))
+        ok = false;
+    return tmem + (uint32_t)b * COLS;
+}
+template <int COLS, int STAGES>
+__device__ __forceinline__ void turn_end(Ring<STAGES>& r, int i, int n_k) {
+    if (i % kTurn<COLS> == kTurn<COLS> - 1 || i == n_k - 1) mma_commit(&r.sum[i / kTurn<COLS> % kBufs<COLS>]);
+}
+
+// The products' sum of this warp's 32 rows and COLS / 2 columns (warps w and
+// w + 4 share tensor-memory lanes 32 (w % 4) ..), as the turns complete.
+template <int COLS, int STAGES>
+__device__ __forceinline__ void sum_turns(Ring<STAGES>& r, uint32_t tmem, int n_k, float (&acc)[COLS / 2]) {
+    const int warp = (int)(threadIdx.x >> 5), lane = (int)(threadIdx.x & 31);
+    const uint32_t at = ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)((warp >> 2) * (COLS / 2));
+    const int turns = (n_k + kTurn<COLS> - 1) / kTurn<COLS>;
+#pragma unroll
+    for (int u = 0; u < COLS / 2; ++u) acc[u] = 0.f;
+    const auto add = [&](uint32_t from) {
+#pragma unroll
+        for (int c = 0; c < COLS / 2; c += 32) {
+            float v[32];
+            tmem_load_32(from + at + (uint32_t)c, v);
+#pragma unroll
+            for (int u = 0; u < 32; ++u) acc[c + u] += v[u];
+        }
+    };
+    for (int t = 0; t < turns; ++t) {
+        const int b = t % kBufs<COLS>;
+        if (!mbar_wait(&r.sum[b], (uint32_t)(t / kBufs<COLS>) & 1u) && lane == 0) dev_err(ERR_TIMEOUT);
+        tmem_fence_after();
+        add(tmem + (uint32_t)b * COLS);
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&r.read[b]);
+    }
+    if (turns) add(tmem + 512 - COLS);  // complete with the last turn
 }
 
 template <int COLS>
@@ -256,7 +323,7 @@ constexpr int kSymSmem = kSymStages * kSymStage + 1024;
 enum { GRAM = 0, SQUARE = 1 };
 
 template <int S, int KIND>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kProductThreads, 1)
     k_ns_sym(const __grid_constant__ PairMaps maps, int32_t m, int32_t K, float a, float b, float c, Planes in, Planes out,
              int64_t ld) {
     extern __shared__ uint8_t dsm[];
@@ -281,15 +348,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_map(&maps.hi);
         prefetch_map(&maps.lo);
     }
-    if (warp == 1) tmem_alloc<kTile>(&tmem_base);
+    if (warp == kSumWarps + 1) tmem_alloc<512>(&tmem_base);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tmem = tmem_base;
+    const uint32_t tmem = tmem_base, cross = tmem + 512 - kTile;
     pdl_start();
     const int n_kt = (K + kBK - 1) / kBK, per = (n_kt + S - 1) / S;
     const int kt0 = min(n_kt, rank * per), n_k = min(n_kt, kt0 + per) - kt0;
-    if (warp == 0 && lane == 0) {
+    float acc[kTile / 2];
+    if (warp == kSumWarps && lane == 0) {
         int issued = 0;
         for (int i = 0; i < n_k; ++i) {
             const int s = i % kSymStages;
@@ -309,11 +377,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++issued;
         }
         ring_drain(ring, issued);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == kSumWarps + 1 && lane == 0) {
         constexpr uint32_t idesc = desc_f16(false, kTile);
         for (int i = 0; i < n_k; ++i) {
             const int s = i % kSymStages;
-            if (!mbar_wait(&ring.full[s], (uint32_t)(i / kSymStages) & 1u)) {
+            bool ok = true;
+            const uint32_t main = turn_begin<kTile>(ring, tmem, i, ok);
+            if (!ok || !mbar_wait(&ring.full[s], (uint32_t)(i / kSymStages) & 1u)) {
                 dev_err(ERR_TIMEOUT);
                 break;
             }
@@ -323,17 +393,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
                 const uint32_t o = kk * 32;
-                mma_issue(tmem, smem_desc_sw128(ah + o), smem_desc_sw128(bh + o), idesc, (uint32_t)((i | kk) != 0), false);
-                mma_issue(tmem, smem_desc_sw128(ah + o), smem_desc_sw128(bl + o), idesc, 1u, false);
-                mma_issue(tmem, smem_desc_sw128(al + o), smem_desc_sw128(bh + o), idesc, 1u, false);
+                mma_issue(main, smem_desc_sw128(ah + o), smem_desc_sw128(bh + o), idesc,
+                          (uint32_t)((i % kTurn<kTile> | kk) != 0), false);
+                mma_issue(cross, smem_desc_sw128(ah + o), smem_desc_sw128(bl + o), idesc, (uint32_t)((i | kk) != 0), false);
+                mma_issue(cross, smem_desc_sw128(al + o), smem_desc_sw128(bh + o), idesc, 1u, false);
             }
             mma_commit(&ring.empty[s]);
+            turn_end<kTile>(ring, i, n_k);
         }
-        mma_commit(&ring.done);
+    } else if (warp < kSumWarps) {
+        sum_turns<kTile>(ring, tmem, n_k, acc);
     }
     __syncwarp();
-    if (!mbar_wait(&ring.done, 0) && lane == 0) dev_err(ERR_TIMEOUT);
-    tmem_fence_after();
     __syncthreads();  // the producer has drained: the ring is free
     // SQUARE also adds b A: on its way while the parts are exchanged.  Thread t
     // takes 8 columns at a time of row t % 128.
@@ -342,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t i = i0 + row;
     const auto col_of = [&](int turn) { return rank * kW + turn * 16 + (int)(threadIdx.x >> 7) * 8; };
     uint4 ah[kTurns], al[kTurns];
-    if (KIND == SQUARE) {
+    if (KIND == SQUARE && warp < kSumWarps) {
 #pragma unroll
         for (int u = 0; u < kTurns; ++u) {
             const int32_t j = j0 + col_of(u);
@@ -352,29 +423,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             al[u] = in_range ? *reinterpret_cast<const uint4*>(in.lo + at) : make_uint4(0, 0, 0, 0);
         }
     }
-    // partial sums to shared memory as [column / 4][row][4]: warps w and w + 4
-    // read tensor-memory lanes 32 (w % 4).. of columns [0, 64) and [64, 128)
+    // partial sums to shared memory as [column / 4][row][4]
     float* dump = reinterpret_cast<float*>(tiles);
-    {
-        const int r = (warp & 3) * 32 + lane;
-#pragma unroll 1
-        for (int c0 = (warp >> 2) * 64; c0 < (warp >> 2) * 64 + 64; c0 += 32) {
-            float v[32];
-            tmem_load_32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)c0, v);
-            if (!n_k) {
+    if (warp < kSumWarps) {
+        const int r = (warp & 3) * 32 + lane, c0 = (warp >> 2) * (kTile / 2);
 #pragma unroll
-                for (int u = 0; u < 32; ++u) v[u] = 0.f;
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                *reinterpret_cast<float4*>(dump + ((c0 / 4 + u) * kTile + r) * 4) =
-                    make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
-        }
+        for (int u = 0; u < kTile / 2; u += 4)
+            *reinterpret_cast<float4*>(dump + ((c0 + u) / 4 * kTile + r) * 4) =
+                make_float4(acc[u], acc[u + 1], acc[u + 2], acc[u + 3]);
     }
     tmem_fence_before();
     if constexpr (S > 1) cluster_sync();
     else __syncthreads();
-    if (warp == 1) tmem_free<kTile>(tmem);
+    if (warp == kSumWarps + 1) tmem_free<512>(tmem);
+    if (warp >= kSumWarps) return;
     const uint32_t base = smem_addr(dump);
     float4 x[kTurns][S][2];  // 16 loads in flight, whatever S is
 #pragma unroll
@@ -466,7 +528,7 @@ struct ApplyMaps {
 };
 
 template <int BN, typename TW, bool FINAL>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kProductThreads, 1)
     k_ns_apply(const __grid_constant__ ApplyMaps maps, int32_t m, int32_t n, Planes out, int64_t ldx, FinalArgs fin) {
     constexpr int kStages = kApplyStages<BN>, kStage = kApplyStage<BN>, kBox = kBK * 128;  // 64 K rows of 64 columns
     extern __shared__ uint8_t dsm[];
@@ -483,14 +545,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_map(&maps.xhi);
         prefetch_map(&maps.xlo);
     }
-    if (warp == 1) tmem_alloc<BN>(&tmem_base);
+    if (warp == kSumWarps + 1) tmem_alloc<512>(&tmem_base);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tmem = tmem_base;
+    const uint32_t tmem = tmem_base, cross = tmem + 512 - BN;
     pdl_start();
     const int n_k = (m + kBK - 1) / kBK;
-    if (warp == 0 && lane == 0) {
+    float acc[BN / 2];
+    if (warp == kSumWarps && lane == 0) {
         int issued = 0;
         for (int i = 0; i < n_k; ++i) {
             const int s = i % kStages;
@@ -510,11 +573,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++issued;
         }
         ring_drain(ring, issued);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == kSumWarps + 1 && lane == 0) {
         constexpr uint32_t idesc = desc_f16(true, BN);
         for (int i = 0; i < n_k; ++i) {
             const int s = i % kStages;
-            if (!mbar_wait(&ring.full[s], (uint32_t)(i / kStages) & 1u)) {
+            bool ok = true;
+            const uint32_t main = turn_begin<BN>(ring, tmem, i, ok);
+            if (!ok || !mbar_wait(&ring.full[s], (uint32_t)(i / kStages) & 1u)) {
                 dev_err(ERR_TIMEOUT);
                 break;
             }
@@ -524,38 +589,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
                 const uint32_t o = kk * 32, ox = kk * 16 * 128;  // 16 K elements of a row; 16 K rows
-                mma_issue(tmem, smem_desc_sw128(bh + o), smem_desc_mn_sw128(xh + ox, kBox), idesc,
-                          (uint32_t)((i | kk) != 0), false);
-                mma_issue(tmem, smem_desc_sw128(bh + o), smem_desc_mn_sw128(xl + ox, kBox), idesc, 1u, false);
-                mma_issue(tmem, smem_desc_sw128(bl + o), smem_desc_mn_sw128(xh + ox, kBox), idesc, 1u, false);
+                mma_issue(main, smem_desc_sw128(bh + o), smem_desc_mn_sw128(xh + ox, kBox), idesc,
+                          (uint32_t)((i % kTurn<BN> | kk) != 0), false);
+                mma_issue(cross, smem_desc_sw128(bh + o), smem_desc_mn_sw128(xl + ox, kBox), idesc, (uint32_t)((i | kk) != 0),
+                          false);
+                mma_issue(cross, smem_desc_sw128(bl + o), smem_desc_mn_sw128(xh + ox, kBox), idesc, 1u, false);
             }
             mma_commit(&ring.empty[s]);
+            turn_end<BN>(ring, i, n_k);
         }
-        mma_commit(&ring.done);
+    } else if (warp < kSumWarps) {
+        sum_turns<BN>(ring, tmem, n_k, acc);
     }
     __syncwarp();
-    if (!mbar_wait(&ring.done, 0) && lane == 0) dev_err(ERR_TIMEOUT);
-    tmem_fence_after();
     __syncthreads();  // the producer has drained: the ring is free
     // the tile through shared memory, so that rows go out whole: [row][BN + 4]
     // (rows on 16-byte boundaries, 8 rows in different banks)
     float* dump = reinterpret_cast<float*>(tiles);
     constexpr int kLd = BN + 4;
-    {
-        const int row = (warp & 3) * 32 + lane;
-#pragma unroll 1
-        for (int c0 = (warp >> 2) * (BN / 2); c0 < ((warp >> 2) + 1) * (BN / 2); c0 += 32) {
-            float v[32];
-            tmem_load_32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)c0, v);
+    if (warp < kSumWarps) {
+        const int row = (warp & 3) * 32 + lane, c0 = (warp >> 2) * (BN / 2);
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                *reinterpret_cast<float4*>(dump + row * kLd + c0 + 4 * u) =
-                    make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
-        }
+        for (int u = 0; u < BN / 2; u += 4)
+            *reinterpret_cast<float4*>(dump + row * kLd + c0 + u) = make_float4(acc[u], acc[u + 1], acc[u + 2], acc[u + 3]);
     }
     tmem_fence_before();
     __syncthreads();
-    if (warp == 1) tmem_free<BN>(tmem);
+    if (warp == kSumWarps + 1) tmem_free<512>(tmem);
+    if (warp >= kSumWarps) return;
     if constexpr (!FINAL) {
         constexpr int kLanes = BN / 8, kRows = kThreads / kLanes;  // 8 columns a lane; rows at a time
         const int c = (int)(threadIdx.x % kLanes) * 8;
@@ -733,7 +794,7 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
         mbar_init(&full, 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
-    if (warp == 1) tmem_alloc<(W > 128 ? W : 128)>(&tmem_base);
+    if (warp == 1) tmem_alloc<512>(&tmem_base);
 
     // U of this CTA's columns, in registers; the new momentum on the way.
     // Consecutive threads take consecutive addresses: columns of a row, or
@@ -870,14 +931,30 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
         phase ^= 1u;
         tmem_fence_after();
     };
-    // hi hi + hi lo + lo hi over K steps of 16; a and b give a step's descriptors
-    const auto pairs = [&](int ksteps, uint32_t idesc, auto a, auto b) {
+    // hi hi, and hi lo + lo hi, over K steps of 16; a and b give a step's
+    // descriptors.  hi hi is dealt to `mains` accumulators: three of 128 columns,
+    // or one of 256.
+    const auto pairs = [&](int ksteps, int mains, int cols, uint32_t idesc, auto a, auto b) {
+        const uint32_t cross = tmem + (uint32_t)(mains * cols);
         for (int k = 0; k < ksteps; ++k) {
-            mma_issue(tmem, a(k, 0), b(k, 0), idesc, (uint32_t)(k != 0), false);
-            mma_issue(tmem, a(k, 0), b(k, 1), idesc, 1u, false);
-            mma_issue(tmem, a(k, 1), b(k, 0), idesc, 1u, false);
+            mma_issue(tmem + (uint32_t)(k % mains * cols), a(k, 0), b(k, 0), idesc, (uint32_t)(k >= mains), false);
+            mma_issue(cross, a(k, 0), b(k, 1), idesc, (uint32_t)(k != 0), false);
+            mma_issue(cross, a(k, 1), b(k, 0), idesc, 1u, false);
         }
     };
+    // 32 columns of their sum
+    const auto load_sum = [&](int ksteps, int mains, int cols, uint32_t at, float (&v)[32]) {
+        float w[32];
+        tmem_load_32(tmem + (uint32_t)(mains * cols) + at, v);
+#pragma unroll
+        for (int i = 2; i >= 0; --i) {
+            if (i >= mains || i >= ksteps) continue;
+            tmem_load_32(tmem + (uint32_t)(i * cols) + at, w);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] += w[k];
+        }
+    };
+    constexpr int kXMains = W == 256 ? 1 : 3, kXCols = W == 256 ? 256 : 128;  // of X <- B X
     const auto x_rows = [&](int k, int lo) {
         return smem_desc_sw128(xa + (lo ? kXLo : 0) + (uint32_t)((k >> 2) * kPairTile + (k & 3) * 32));
     };
@@ -921,10 +998,10 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
 #pragma unroll 1
     for (int step = 0; step < steps.count; ++step) {
         // partial A = X X^T
-        product([&] { pairs(kx, desc_f16(false, kFusedM), x_rows, x_rows); });
+        product([&] { pairs(kx, 3, 128, desc_f16(false, kFusedM), x_rows, x_rows); });
         if constexpr (W == 256) {
             float v[32];
-            tmem_load_32(tmem + lanes + (uint32_t)part * 32, v);
+            load_sum(kx, 3, 128, lanes + (uint32_t)part * 32, v);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 float x[8];
@@ -939,7 +1016,7 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
 #pragma unroll 1
             for (int c0 = part * 64; c0 < part * 64 + 64; c0 += 32) {
                 float v[32];
-                tmem_load_32(tmem + lanes + (uint32_t)c0, v);
+                load_sum(kx, 3, 128, lanes + (uint32_t)c0, v);
 #pragma unroll
                 for (int t = 0; t < 8; ++t)
                     *reinterpret_cast<float4*>(dump + ((c0 / 4 + t) * kFusedM + row) * 4) =
@@ -948,14 +1025,14 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
             gather();
         }
         // B = a I + b A + c A A, in A's place
-        product([&] { pairs(kFusedM / 16, desc_f16(false, kFusedM), a_rows, a_rows); });
+        product([&] { pairs(kFusedM / 16, 3, 128, desc_f16(false, kFusedM), a_rows, a_rows); });
         // every CTA has A: this one's copies are done with its rows
         if (S > 1) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
         const float ca = steps.coef[step][0] * kScale, cb = steps.coef[step][1], cc = steps.coef[step][2] * (1.f / kScale);
 #pragma unroll 1
         for (int c0 = part * (kFusedM * 4 / kWarps); c0 < (part + 1) * (kFusedM * 4 / kWarps); c0 += 32) {
             float v[32];
-            tmem_load_32(tmem + lanes + (uint32_t)c0, v);
+            load_sum(kFusedM / 16, 3, 128, lanes + (uint32_t)c0, v);
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] *= cc;
             if ((c0 >> 5) == (warp & 3)) {  // the diagonal: column c0 + lane of row `row`
@@ -983,12 +1060,12 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
             }
         }
         // X <- B X
-        product([&] { pairs(kFusedM / 16, desc_f16(true, 16 * kx), a_rows, x_cols); });
+        product([&] { pairs(kFusedM / 16, kXMains, kXCols, desc_f16(true, 16 * kx), a_rows, x_cols); });
         if (step + 1 < steps.count) {
 #pragma unroll 1
             for (int c0 = part * (W * 4 / kWarps); c0 < (part + 1) * (W * 4 / kWarps); c0 += 32) {
                 float v[32];
-                tmem_load_32(tmem + lanes + (uint32_t)c0, v);
+                load_sum(kFusedM / 16, kXMains, kXCols, lanes + (uint32_t)c0, v);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     float x[8];
@@ -1026,7 +1103,7 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
 #pragma unroll 1
         for (int c0 = part * kCols; c0 < (part + 1) * kCols; c0 += 32) {
             float v[32];
-            tmem_load_32(tmem + lanes + (uint32_t)c0, v);
+            load_sum(kFusedM / 16, kXMains, kXCols, lanes + (uint32_t)c0, v);
 #pragma unroll
             for (int t = 0; t < 8; ++t)
                 *reinterpret_cast<float4*>(tile + row * (W + 4) + c0 + 4 * t) =
@@ -1051,7 +1128,7 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
 #pragma unroll 1
         for (int c0 = part * kCols; c0 < (part + 1) * kCols; c0 += 32) {
             float v[32];
-            tmem_load_32(tmem + lanes + (uint32_t)c0, v);
+            load_sum(kFusedM / 16, kXMains, kXCols, lanes + (uint32_t)c0, v);
 #pragma unroll
             for (int t = 0; t < 32; ++t) tile[row * ld_row + (c0 + t) * ld_col] = v[t];
         }
@@ -1066,7 +1143,7 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
     }
     tmem_fence_before();
     __syncthreads();
-    if (warp == 1) tmem_free<(W > 128 ? W : 128)>(tmem);
+    if (warp == 1) tmem_free<512>(tmem);
 }
 
 // -------------------------------------------------------------------- host
@@ -1121,7 +1198,7 @@ template <int S, typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, size_t smem, cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kProductThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at[2];
@@ -1178,7 +1255,7 @@ sg_status launch_apply(const ApplyMaps& maps, int32_t count, int32_t m, int32_t 
     constexpr int smem = kApplySmem<BN>;
     NS_SMEM((k_ns_apply<BN, TW, FINAL>), smem);
     SG_CUDA(launch_pdl(k_ns_apply<BN, TW, FINAL>, dim3((unsigned)cdiv(n, BN), (unsigned)cdiv(m, kTile), (unsigned)count),
-                       dim3(kThreads), smem, s, maps, m, n, out, ldx, fin));
+                       dim3(kProductThreads), smem, s, maps, m, n, out, ldx, fin));
     return SG_OK;
 }
 
@@ -1221,6 +1298,32 @@ sg_status launch_fused(const Source<TS>& src, int32_t count, int32_t rows, int32
     return SG_OK;
 }
 
+// Whether the device takes clusters of 16 CTAs with all of an SM's shared
+// memory each (looked up once).
+bool clusters_of_16() {
+    static int ok = -1;
+    if (ok < 0) {
+        const auto kernel = k_ns_fused<128, float, float>;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(16);
+        cfg.blockDim = dim3(kFusedThreads<128>);
+        cfg.dynamicSmemBytes = kFusedSmem<128>;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 16;
+        at[0].val.clusterDim.y = 1;
+        at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFusedSmem<128>) == cudaSuccess &&
+             cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+             cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0;
+        if (!ok) cudaGetLastError();
+    }
+    return ok != 0;
+}
+
 template <typename TS, typename TW>
 sg_status run(Source<TS> src, int32_t count, int32_t rows, int32_t cols, int32_t steps, const float* coef, float eps,
               const TW* w, float keep, float step, TW* out, int64_t ld_out, char* ws, cudaStream_t s) {
@@ -1232,7 +1335,7 @@ sg_status run(Source<TS> src, int32_t count, int32_t rows, int32_t cols, int32_t
     // launch: up to 256 columns by one CTA, which has nothing to exchange; else
     // 64 columns a CTA while 16 CTAs reach, since each product and each pass
     // over tensor memory is then half as long
-    if (m <= kFusedM && n <= kFusedMaxCtas * 128 && steps > 0) {
+    if (m <= kFusedM && n <= kFusedMaxCtas * 128 && steps > 0 && (n <= 8 * 64 || clusters_of_16())) {
         Steps st;
         st.count = steps;
         for (int32_t k = 0; k < SG_MAX_NS_STEPS; ++k)
