@@ -270,12 +270,25 @@ __device__ __forceinline__ void sum_turns(Ring<STAGES>& r, uint32_t tmem, int n_
 #pragma unroll
     for (int u = 0; u < COLS / 2; ++u) acc[u] = 0.f;
     const auto add = [&](uint32_t from) {
-#pragma unroll
-        for (int c = 0; c < COLS / 2; c += 32) {
+        if constexpr (COLS == 64) {
             float v[32];
-            tmem_load_32(from + at + (uint32_t)c, v);
+            tmem_load_32(from + at, v);
 #pragma unroll
-            for (int u = 0; u < 32; ++u) acc[c + u] += v[u];
+            for (int u = 0; u < 32; ++u) acc[u] += v[u];
+        } else {
+#pragma unroll
+            for (int c = 0; c < COLS / 2; c += 64) {
+                uint32_t x[32], y[32];
+                tmem_load_issue(from + at + (uint32_t)c, x);
+                tmem_load_issue(from + at + (uint32_t)c + 32, y);
+                tmem_load_wait(x);
+                tmem_load_wait(y);
+#pragma unroll
+                for (int u = 0; u < 32; ++u) {
+                    acc[c + u] += __uint_as_float(x[u]);
+                    acc[c + 32 + u] += __uint_as_float(y[u]);
+                }
+            }
         }
     };
     for (int t = 0; t < turns; ++t) {
@@ -932,8 +945,8 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
         tmem_fence_after();
     };
     // hi hi, and hi lo + lo hi, over K steps of 16; a and b give a step's
-    // descriptors.  hi hi is dealt to `mains` accumulators: three of 128 columns,
-    // or one of 256.
+    // descriptors.  hi hi is dealt to `mains` accumulators: two of 128 columns, or
+    // one of 256.
     const auto pairs = [&](int ksteps, int mains, int cols, uint32_t idesc, auto a, auto b) {
         const uint32_t cross = tmem + (uint32_t)(mains * cols);
         for (int k = 0; k < ksteps; ++k) {
@@ -944,17 +957,21 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
     };
     // 32 columns of their sum
     const auto load_sum = [&](int ksteps, int mains, int cols, uint32_t at, float (&v)[32]) {
-        float w[32];
-        tmem_load_32(tmem + (uint32_t)(mains * cols) + at, v);
+        uint32_t x[32], y[32];
+        tmem_load_issue(tmem + (uint32_t)(mains * cols) + at, x);
+        tmem_load_issue(tmem + at, y);
+        tmem_load_wait(x);
+        tmem_load_wait(y);
 #pragma unroll
-        for (int i = 2; i >= 0; --i) {
-            if (i >= mains || i >= ksteps) continue;
-            tmem_load_32(tmem + (uint32_t)(i * cols) + at, w);
+        for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(x[k]) + __uint_as_float(y[k]);
+        if (mains > 1 && ksteps > 1) {
+            tmem_load_issue(tmem + (uint32_t)cols + at, x);
+            tmem_load_wait(x);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] += w[k];
+            for (int k = 0; k < 32; ++k) v[k] += __uint_as_float(x[k]);
         }
     };
-    constexpr int kXMains = W == 256 ? 1 : 3, kXCols = W == 256 ? 256 : 128;  // of X <- B X
+    constexpr int kXMains = W == 256 ? 1 : 2, kXCols = W == 256 ? 256 : 128;  // of X <- B X
     const auto x_rows = [&](int k, int lo) {
         return smem_desc_sw128(xa + (lo ? kXLo : 0) + (uint32_t)((k >> 2) * kPairTile + (k & 3) * 32));
     };
@@ -998,10 +1015,10 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
 #pragma unroll 1
     for (int step = 0; step < steps.count; ++step) {
         // partial A = X X^T
-        product([&] { pairs(kx, 3, 128, desc_f16(false, kFusedM), x_rows, x_rows); });
+        product([&] { pairs(kx, 2, 128, desc_f16(false, kFusedM), x_rows, x_rows); });
         if constexpr (W == 256) {
             float v[32];
-            load_sum(kx, 3, 128, lanes + (uint32_t)part * 32, v);
+            load_sum(kx, 2, 128, lanes + (uint32_t)part * 32, v);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 float x[8];
@@ -1016,7 +1033,7 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
 #pragma unroll 1
             for (int c0 = part * 64; c0 < part * 64 + 64; c0 += 32) {
                 float v[32];
-                load_sum(kx, 3, 128, lanes + (uint32_t)c0, v);
+                load_sum(kx, 2, 128, lanes + (uint32_t)c0, v);
 #pragma unroll
                 for (int t = 0; t < 8; ++t)
                     *reinterpret_cast<float4*>(dump + ((c0 / 4 + t) * kFusedM + row) * 4) =
@@ -1025,14 +1042,14 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
             gather();
         }
         // B = a I + b A + c A A, in A's place
-        product([&] { pairs(kFusedM / 16, 3, 128, desc_f16(false, kFusedM), a_rows, a_rows); });
+        product([&] { pairs(kFusedM / 16, 2, 128, desc_f16(false, kFusedM), a_rows, a_rows); });
         // every CTA has A: this one's copies are done with its rows
         if (S > 1) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
         const float ca = steps.coef[step][0] * kScale, cb = steps.coef[step][1], cc = steps.coef[step][2] * (1.f / kScale);
 #pragma unroll 1
         for (int c0 = part * (kFusedM * 4 / kWarps); c0 < (part + 1) * (kFusedM * 4 / kWarps); c0 += 32) {
             float v[32];
-            load_sum(kFusedM / 16, 3, 128, lanes + (uint32_t)c0, v);
+            load_sum(kFusedM / 16, 2, 128, lanes + (uint32_t)c0, v);
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] *= cc;
             if ((c0 >> 5) == (warp & 3)) {  // the diagonal: column c0 + lane of row `row`

@@ -36,7 +36,8 @@ class SageTrainer:
     128 classes."""
 
     def __init__(self, graph: sg.Graph, dim: int, n_classes: int, fanouts: Sequence[int], n_seeds: int,
-                 lr: float = 0.02, lr_table: float = 1.0, momentum: float = 0.95, seed: int = 0, device="cuda"):
+                 lr: float = 0.02, lr_table: float = 1.0, momentum: float = 0.95, scale: float = 1.0, seed: int = 0,
+                 device="cuda"):
         if not 1 <= n_classes <= HIDDEN:
             raise ValueError("SageTrainer: 1 to %d classes" % HIDDEN)
         if n_seeds < 1:
@@ -44,14 +45,16 @@ class SageTrainer:
         self.graph, self.n_classes, self.n_seeds = graph, int(n_classes), int(n_seeds)
         self.fanouts = [int(f) for f in fanouts]
         self.lr, self.lr_table, self.momentum = lr, lr_table, momentum
-        self.scale = math.sqrt(dim)  # of the looked-up rows, which start with unit norm
+        # of the looked-up rows, which start with unit norm; it multiplies the
+        # gradient as well, so a step moves the rows in use by lr_table * scale^2
+        self.scale = float(scale)
         H = self.H = len(self.fanouts)
         gen = torch.Generator(device=device)
         gen.manual_seed(seed)
 
         def randn(*shape, std):
             return torch.empty(shape, device=device).normal_(0, std, generator=gen)
-        self.table = randn(graph.n_nodes, dim, std=1 / dim)
+        self.table = randn(graph.n_nodes, dim, std=1 / (self.scale * math.sqrt(dim)))
         self.dims = [HIDDEN] * H + [dim]  # width of X_h, h = 0 .. H
         self.W = [None] + [randn(HIDDEN, 2 * self.dims[h], std=1 / math.sqrt(2 * self.dims[h])) for h in range(1, H + 1)]
         self.m = [None] + [torch.zeros_like(w) for w in self.W[1:]]
