@@ -277,7 +277,7 @@ __device__ __forceinline__ void st_relaxed(uint32_t* p, uint32_t v) {
 // the tile's own count, 2 the count up to and including the tile.  Tiles are
 // handed out in order, so every tile looked at is running or done.
 template <int ITEMS>
-__global__ void __launch_bounds__(kSortThreads, 2) k_sort_pass(const int32_t* __restrict__ ids, const uint2* __restrict__ in,
+__global__ void __launch_bounds__(kSortThreads, 1) k_sort_pass(const int32_t* __restrict__ ids, const uint2* __restrict__ in,
                                                         int64_t n_rows, int64_t n_cap, const int32_t* __restrict__ d_n,
                                                         int pass, int per, SortState* __restrict__ st,
                                                         uint32_t* __restrict__ status, uint2* __restrict__ out) {
@@ -958,9 +958,12 @@ sg_status run_sort(const int32_t* ids, int64_t n_cap, const int32_t* d_n, int64_
                              : go(k_sort_small<8>));
         return SG_OK;
     }
-    // 8 items a thread once that still gives every SM a tile
-    const bool big = n_cap >= (int64_t)num_sms() * kSortThreads * 8;
-    const int64_t tiles = cdiv(n_cap, kSortThreads * (big ? 8 : 4));
+    // the fewest items a thread (4, 8 or 12) with which every tile has an SM of
+    // its own: two tiles on an SM take twice as long as one, and every later
+    // tile waits for them
+    const int64_t wave = (int64_t)num_sms() * kSortThreads;
+    const int items = n_cap <= 4 * wave ? 4 : n_cap <= 8 * wave ? 8 : 12;
+    const int64_t tiles = cdiv(n_cap, kSortThreads * items);
     SG_CUDA(cudaMemsetAsync(ws + L.state, 0, L.status - L.state + (size_t)(dg.passes * tiles) * kDigits * 4, s));
     const int64_t hb = cdiv(n_cap, kThreads * 8) < num_sms() * 2 ? cdiv(n_cap, kThreads * 8) : num_sms() * 2;
     SG_CUDA(launch_pdl(k_sort_hist, dim3((unsigned)hb), dim3(kThreads), 0, s, ids, n_rows, n_cap, d_n, dg, st));
@@ -968,12 +971,9 @@ sg_status run_sort(const int32_t* ids, int64_t n_cap, const int32_t* d_n, int64_
         uint32_t* status = (uint32_t*)(ws + L.status) + p * tiles * kDigits;
         const uint2* in = p ? kv[(p & 1) ^ 1] : nullptr;
         uint2* out = kv[p & 1];
-        if (big)
-            SG_CUDA(launch_pdl(k_sort_pass<8>, dim3((unsigned)tiles), dim3(kSortThreads), 0, s, ids, in,
-                               n_rows, n_cap, d_n, p, (int)dg.per, st, status, out));
-        else
-            SG_CUDA(launch_pdl(k_sort_pass<4>, dim3((unsigned)tiles), dim3(kSortThreads), 0, s, ids, in,
-                               n_rows, n_cap, d_n, p, (int)dg.per, st, status, out));
+        const auto kernel = items == 4 ? k_sort_pass<4> : items == 8 ? k_sort_pass<8> : k_sort_pass<12>;
+        SG_CUDA(launch_pdl(kernel, dim3((unsigned)tiles), dim3(kSortThreads), 0, s, ids, in, n_rows, n_cap, d_n, p,
+                           (int)dg.per, st, status, out));
         *sorted = out;
     }
     if (rows)
