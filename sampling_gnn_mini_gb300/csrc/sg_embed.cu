@@ -17,13 +17,15 @@
 // sum has one order: no float atomics.
 //
 // The sort: up to kSmallSort positions in one block's shared memory
-// (k_sort_small); else one histogram launch for all passes, then one launch a
+// (k_sort_small); up to kClusterSort by one cluster (k_sort_cluster); else
+// one histogram launch for all passes, then one launch a
 // pass, whose tiles learn their digits' offsets from the tiles before them
 // (decoupled look-back, one thread a digit).
 #include <cuda_bf16.h>
 #include <string.h>
 
 #include "sg_internal.cuh"
+#include "sg_tc.cuh"
 
 SGI_ERROR_WORD(embed)
 
@@ -524,6 +526,129 @@ __global__ void __launch_bounds__(kSmallThreads) k_sort_small(const int32_t* __r
 }
 constexpr int kSmallSmem = kSmallSort * 6 + (kSmallThreads / 32) * kDigits * 2;
 
+// A list of up to kClusterSort positions, in one launch: a cluster of kSortCtas
+// blocks, block r holding positions [r, r + 1) ITEMS 1024 in every pass's
+// order.  The blocks exchange their digit counts in shared memory and the
+// pairs through memory (L2), written to their places and read back after a
+// cluster barrier.  Measured, us for the whole gradient, this / a launch a
+// pass: 20,000 positions of 1024 bf16 columns 48 / 52, of 64 fp32 columns
+// 24 / 27; 40,000 of 256 fp32 columns 51 / 49.  (With the pairs sent straight
+// into the other blocks' shared memory, 8 bytes at a time: 53 for the first.)
+constexpr int kSortCtas = 16;
+constexpr int kClusterSort = kSortCtas * 2 * kSmallThreads;
+template <int ITEMS>
+__global__ void __launch_bounds__(kSmallThreads) k_sort_cluster(const int32_t* __restrict__ ids, int64_t n_rows,
+                                                                int32_t n_cap, const int32_t* __restrict__ d_n, Digits dg,
+                                                                int32_t span, uint2* kv0, uint2* kv1,
+                                                                int32_t* __restrict__ starts, int32_t* __restrict__ n_out) {
+    pdl_start();
+    constexpr int kWarps = kSmallThreads / 32, kParts = kSmallThreads / kDigits, kPer = kWarps / kParts;
+    __shared__ __align__(16) uint16_t cnt[kWarps][kDigits];
+    __shared__ uint32_t theirs[kSortCtas][kDigits];
+    __shared__ uint32_t sh[kWarps + 1];
+    __shared__ uint32_t psum[kParts][kDigits], base[kDigits];
+    __shared__ uint32_t runs[kSortCtas];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int digit = threadIdx.x % kDigits, q4 = threadIdx.x / kDigits;  // a digit, and kPer of the warps
+    const uint32_t rank = cluster_rank();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
+    const int32_t n = (int32_t)count_of(d_n, n_cap);
+    const int32_t first = (int32_t)rank * ITEMS * kSmallThreads + warp * 32 * ITEMS + lane;
+    uint2 x[ITEMS];
+    uint32_t rk[ITEMS], total;
+    int32_t d[ITEMS];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) d[i] = first + i * 32 < n ? __ldg(ids + first + i * 32) : -1;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+        x[i] = make_uint2(first + i * 32 < n ? key_of(d[i], n_rows) : kNoKey, (uint32_t)(first + i * 32));
+    for (int p = 0; p < dg.passes; ++p) {
+        uint2* to_kv = p & 1 ? kv1 : kv0;
+        uint32_t* zero = reinterpret_cast<uint32_t*>(&cnt[warp][0]);
+#pragma unroll
+        for (int i = 0; i < kDigits / 64; ++i) zero[lane + 32 * i] = 0;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)
+            d[i] = x[i].x != kNoKey ? (int32_t)((x[i].x >> (p * dg.per)) & ((1u << dg.per) - 1)) : -1;
+        warp_rank<ITEMS>(d, cnt[warp], rk);
+        __syncthreads();
+        uint32_t part = 0;
+#pragma unroll
+        for (int w = 0; w < kPer; ++w) part += cnt[q4 * kPer + w][digit];
+        psum[q4][digit] = part;
+        __syncthreads();
+        uint32_t all = 0, run = 0, lower = 0;  // this block's; of the warps before; of the blocks before
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) {
+            all += psum[k][digit];
+            run += k < q4 ? psum[k][digit] : 0;
+        }
+        // every block runs: its shared memory may be written
+        if (p == 0) asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
+#pragma unroll
+        for (int c = 0; c < kSortCtas / kParts; ++c)
+            asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(
+                             map_rank(smem_addr(&theirs[rank][digit]), (uint32_t)(c * kParts + q4))),
+                         "r"(all)
+                         : "memory");
+        cluster_sync();
+        all = 0;
+#pragma unroll
+        for (uint32_t c = 0; c < kSortCtas; ++c) {
+            all += theirs[c][digit];
+            lower += c < rank ? theirs[c][digit] : 0;
+        }
+        const uint32_t e = block_excl_scan<kSmallThreads, uint32_t>(q4 == 0 ? all : 0, sh, total);
+        if (q4 == 0) base[digit] = e + lower;
+#pragma unroll
+        for (int w = 0; w < kPer; ++w) {
+            const uint32_t c = cnt[q4 * kPer + w][digit];
+            cnt[q4 * kPer + w][digit] = (uint16_t)run;
+            run += c;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)
+            if (d[i] >= 0) to_kv[base[d[i]] + cnt[warp][d[i]] + rk[i]] = x[i];
+        if (p + 1 == dg.passes && !n_out) return;
+        cluster_sync();
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)  // (past L1, which may hold what an earlier pass read here)
+            x[i] = first + i * 32 < n ? __ldcg(to_kv + first + i * 32) : make_uint2(kNoKey, 0);
+    }
+    // run starts: round i of a warp is 32 positions in a row
+    uint32_t last = first - lane > 0 && first - lane - 1 < n ? __ldcg(((dg.passes & 1 ? kv0 : kv1) + first - lane - 1)).x : kNoKey;
+    int32_t before[ITEMS], mine = 0;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, x[i].x, 1), prev = lane ? up : last;
+        before[i] = mine;
+        mine += __popc(__ballot_sync(0xFFFFFFFFu, x[i].x < (uint32_t)n_rows && x[i].x != prev));
+        last = __shfl_sync(0xFFFFFFFFu, x[i].x, 31);
+    }
+    int32_t e = (int32_t)block_excl_scan<kSmallThreads, uint32_t>(lane == 0 ? (uint32_t)mine : 0, sh, total);
+    if (threadIdx.x < kSortCtas)
+        asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(map_rank(smem_addr(runs + rank), threadIdx.x)), "r"(total)
+                     : "memory");
+    cluster_sync();
+    uint32_t sum = 0;
+#pragma unroll
+    for (uint32_t c = 0; c < kSortCtas; ++c) {
+        e += c < rank ? (int32_t)runs[c] : 0;
+        sum += runs[c];
+    }
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)
+            if (first + i * 32 < n && (first + i * 32) % span == 0) starts[(first + i * 32) / span] = e + before[i];
+    }
+    if (rank == 0 && threadIdx.x == 0) {
+        starts[(n + span - 1) / span] = (int32_t)sum;
+        *n_out = (int32_t)sum;
+    }
+}
+
 // ------------------------------------------------------- runs of equal IDs
 template <typename TO>
 struct SumArgs {
@@ -880,7 +1005,7 @@ BwdLayout bwd_layout(int64_t n_cap, int32_t dim) {
             const int64_t t = cdiv(n_cap, cut_for(n_cap, dim, vec).span);
             if (t > L.tiles) L.tiles = t;
         }
-    L.sort_tiles = n_cap <= kSmallSort ? 0 : cdiv(n_cap, kSortThreads * 4);
+    L.sort_tiles = n_cap <= kClusterSort ? 0 : cdiv(n_cap, kSortThreads * 4);
     size_t o = 0;
     const auto put = [&o](size_t bytes) {
         const size_t at = o;
@@ -925,7 +1050,33 @@ sg_status run_sum(int vec, const void* g, const SumArgs<TO>& a, int32_t span, cu
     return launch_sum<TI, TO, 1>(g, a, span, s);
 }
 
-// Sorted pairs in kv[*cur]; with rows, the distinct IDs before each tile of
+template <int ITEMS>
+cudaError_t launch_cluster(const int32_t* ids, int64_t n_rows, int64_t n_cap, const int32_t* d_n, Digits dg, int32_t span,
+                           uint2* const (&kv)[2], int32_t* starts, int32_t* n_out, cudaStream_t s) {
+    static bool set = false;
+    if (!set) {
+        const cudaError_t e = cudaFuncSetAttribute(k_sort_cluster<ITEMS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        set = true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kSortCtas);
+    cfg.blockDim = dim3(kSmallThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = kSortCtas;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_sort_cluster<ITEMS>, ids, n_rows, (int32_t)n_cap, d_n, dg, span, kv[0], kv[1], starts,
+                              n_out);
+}
+
+// Sorted pairs in *sorted; with rows, the distinct IDs before each tile of
 // `span` positions in starts.
 sg_status run_sort(const int32_t* ids, int64_t n_cap, const int32_t* d_n, int64_t n_rows, bool rows, int32_t span,
                    int32_t* n_out, const BwdLayout& L, char* ws, uint2** sorted, cudaStream_t s) {
@@ -956,6 +1107,13 @@ sg_status run_sort(const int32_t* ids, int64_t n_cap, const int32_t* d_n, int64_
                 : items <= 3 ? go(k_sort_small<3>)
                 : items <= 5 ? go(k_sort_small<5>)
                              : go(k_sort_small<8>));
+        return SG_OK;
+    }
+    if (n_cap <= kClusterSort) {
+        int32_t* const distinct = rows ? n_out : nullptr;
+        SG_CUDA(n_cap <= kClusterSort / 2 ? launch_cluster<1>(ids, n_rows, n_cap, d_n, dg, span, kv, starts, distinct, s)
+                                          : launch_cluster<2>(ids, n_rows, n_cap, d_n, dg, span, kv, starts, distinct, s));
+        *sorted = kv[(dg.passes & 1) ^ 1];
         return SG_OK;
     }
     // the fewest items a thread (4, 8 or 12) with which every tile has an SM of

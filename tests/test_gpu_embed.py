@@ -175,7 +175,7 @@ def _check_bwd(got, ids, n_rows, g, scale, mode, to, base=None):
     (20000, 256, 65536, "power", "f32", "f32"), (3000, 1024, 40, "power", "bf16", "bf16"),
     (70001, 8, 9, "same", "f32", "f32"), (70001, 12, 2, "sorted", "bf16", "f32"), (500, 20, 300, "none", "f32", "f32"),
     (40000, 32, 1, "same", "f32", "f32"), (66000, 64, 500, "power", "f32", "f32"),
-    (16384, 16, 70000, "power", "f32", "f32"), (30000, 12, 300, "same", "f32", "f32"),
+    (16384, 16, 70000, "power", "f32", "f32"), (16385, 20, 3000, "sorted", "f32", "f32"), (32768, 8, 1 << 20, "power", "bf16", "f32"), (30000, 12, 300, "same", "f32", "f32"),
     (65536, 8, 20000, "power", "f32", "bf16"), (131072, 4, 100000, "power", "f32", "f32"),
     (131073, 4, 256, "sorted", "bf16", "f32"), (140000, 20, 5000, "none", "f32", "f32"),
     (700001, 4, 3000, "power", "f32", "f32"), (650000, 40, 2, "same", "bf16", "f32")])
