@@ -39,7 +39,8 @@ constexpr int kDigits = 256;
 constexpr int kMaxPasses = 4;
 constexpr int kCopies = 8;            // of the digit counts: blocks add to them in turn (one copy's atomics cost 10 us)
 constexpr int kSortThreads = 512;     // of a pass
-constexpr int kSmallSort = 8192;      // positions sorted by one block
+constexpr int kSmallSort = 5120;      // positions sorted by one block (us for the gradient of 64 / 128 columns, one block /
+                                      // a cluster: 2,048 positions 18, 21 / 20, 27; 4,999: 21, 27 / 22, 28; 8,192: 27, 35 / 22, 29)
 constexpr int kSmallThreads = 1024;
 constexpr int kRunTile = kThreads * 16;   // sorted positions a block of k_runs looks at
 constexpr int kFewBlocks = 76;           // half the SMs: below this many blocks chunks are 8 positions, not 32
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(kThreads) k_runs(const uint2* __restrict__ kv,
     }
 }
 
-// All of it for a short list, in one block: up to 8 items a thread, passes in shared
+// All of it for a short list, in one block: up to 5 items a thread, passes in shared
 // memory.
 template <int ITEMS>
 __global__ void __launch_bounds__(kSmallThreads) k_sort_small(const int32_t* __restrict__ ids, int64_t n_rows,
@@ -1100,13 +1101,11 @@ sg_status run_sort(const int32_t* ids, int64_t n_cap, const int32_t* d_n, int64_
             SG_CUDA(cudaFuncSetAttribute(k_sort_small<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem));
             SG_CUDA(cudaFuncSetAttribute(k_sort_small<3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem));
             SG_CUDA(cudaFuncSetAttribute(k_sort_small<5>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem));
-            SG_CUDA(cudaFuncSetAttribute(k_sort_small<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem));
             set = true;
         }
         SG_CUDA(items <= 1   ? go(k_sort_small<1>)
                 : items <= 3 ? go(k_sort_small<3>)
-                : items <= 5 ? go(k_sort_small<5>)
-                             : go(k_sort_small<8>));
+                             : go(k_sort_small<5>));
         return SG_OK;
     }
     if (n_cap <= kClusterSort) {
