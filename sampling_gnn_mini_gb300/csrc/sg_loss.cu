@@ -258,37 +258,46 @@ struct RowArgs {
 };
 
 // ------------------------------------------------------------ rows by warps
-// R rows (r0, r0 + 1, ..) at once, each in NV vectors a lane; returns their
-// losses (the same in every lane; 0 for rows past n).
+template <int R>
+__device__ __forceinline__ void load_labels(const int32_t* labels, int32_t r0, int32_t n, int32_t (&y)[R]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) y[r] = r0 + r < n ? __ldg(labels + r0 + r) : -1;
+}
+
+// R rows (r0, r0 + 1, ..) with labels y at once, each in NV vectors a lane;
+// returns their losses (the same in every lane; 0 for rows past n).  The labels
+// of the rows at r_next are loaded into y on the way.
 template <typename T, int NV, int R>
-__device__ __forceinline__ void warp_rows(const RowArgs<T>& a, int32_t r0, int32_t n, float w, float (&loss)[R]) {
+__device__ __forceinline__ void warp_rows(const RowArgs<T>& a, int32_t r0, int32_t n, float w, int32_t r_next,
+                                          int32_t (&y_next)[R], float (&loss)[R]) {
     const int lane = (int)lane_id();
     uint4 x[R][NV];
     float xe[R], xy[R];  // this lane's edge element; the label's logit
     int32_t y[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        y[r] = r0 + r < n ? __ldg(a.labels + r0 + r) : -1;
+        y[r] = y_next[r];
+        xe[r] = -INFINITY;
+        xy[r] = 0.f;
         if (y[r] < -1 || y[r] >= a.classes) {
             if (lane == 0) dev_err(ERR_INDEX);
             y[r] = -1;
         }
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        xy[r] = 0.f;
-        if (y[r] < 0) continue;
         const T* row = a.x + (int64_t)(r0 + r) * a.ld;
         const RowParts<T> part(row, a.classes);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int32_t v = lane + 32 * k;
-            x[r][k] = v < part.vecs ? *reinterpret_cast<const uint4*>(row + part.head + v * kE<T>) : empty_part<T>();
+            x[r][k] = y[r] >= 0 && v < part.vecs ? *reinterpret_cast<const uint4*>(row + part.head + v * kE<T>)
+                                                 : empty_part<T>();
         }
         const int32_t e = part.edge(lane);
-        xe[r] = e >= 0 ? to_f(row[e]) : -INFINITY;
-        xy[r] = to_f(row[y[r]]);
+        if (y[r] >= 0) {
+            if (e >= 0) xe[r] = to_f(row[e]);
+            xy[r] = to_f(row[y[r]]);
+        }
     }
+    load_labels(a.labels, r_next, n, y_next);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         loss[r] = 0.f;
@@ -339,12 +348,24 @@ __device__ __forceinline__ void warp_rows(const RowArgs<T>& a, int32_t r0, int32
     }
 }
 
-// Sum of the losses in a fixed order, by the last block to finish.
+// Sum of the losses in a fixed order, by the last block to finish: 16 bytes and
+// 8 loads a thread at a time (65,536 rows one by one took 35 us).
 template <int NT, typename T>
 __device__ __forceinline__ void put_total(const RowArgs<T>& a, int32_t n) {
     __shared__ float sh[NT / 32];
+    // a row or so before the first 16-byte boundary, whole vectors, the rest
+    const int32_t head = min(n, (int32_t)((4 - ((uintptr_t)a.loss >> 2 & 3)) & 3)), vecs = (n - head) / 4;
+    const float4* v = reinterpret_cast<const float4*>(a.loss + head);
     float s = 0.f;
-    for (int32_t i = threadIdx.x; i < n; i += NT) s += __ldcg(a.loss + i);
+    for (int32_t i0 = threadIdx.x; i0 < vecs; i0 += 8 * NT) {
+        float4 x[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) x[u] = i0 + u * NT < vecs ? __ldcg(v + i0 + u * NT) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s += (x[u].x + x[u].y) + (x[u].z + x[u].w);
+    }
+    const int32_t rest = n - 4 * vecs, i = (int32_t)threadIdx.x;  // head and tail together
+    if (i < rest) s += __ldcg(a.loss + (i < head ? i : i + 4 * vecs));
     s = warp_sum(s);
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
     __syncthreads();
@@ -354,21 +375,82 @@ __device__ __forceinline__ void put_total(const RowArgs<T>& a, int32_t n) {
     }
 }
 
+// Blocks of k_xent_warp an SM: by the registers of what a lane holds.
+template <int NV, int R>
+constexpr int kWarpBlocks = NV * R > 4 ? 2 : 3;
+
+// Each warp walks over its rows with the next rows' labels a turn ahead (65,536
+// rows of 128 fp32: 33 us for the call; with a block for every 32 rows 44).
 template <typename T, int NV, int R>
-__global__ void __launch_bounds__(kThreads) k_xent_warp(RowArgs<T> a) {
+__global__ void __launch_bounds__(kThreads, kWarpBlocks<NV, R>) k_xent_warp(RowArgs<T> a) {
     pdl_start();
     __shared__ bool last;
-    constexpr int kRows = kThreads / 32 * R;  // rows of a block
+    constexpr int kRows = kThreads / 32 * R;  // rows of a block's turn
     const int32_t n = rows_of(a.d_n, a.n_cap);
-    const int64_t b0 = (int64_t)blockIdx.x * kRows;
-    if (b0 >= n) return;
+    const int32_t blocks = min((int32_t)gridDim.x, (n + kRows - 1) / kRows);  // that have rows
+    if ((int32_t)blockIdx.x >= blocks) return;
     const float w = a.mean ? a.gs / (float)max(1, *a.valid) : a.gs;
-    float loss[R];
-    warp_rows<T, NV, R>(a, (int32_t)b0 + (int)(threadIdx.x >> 5) * R, n, w, loss);
+    const int32_t step = (int32_t)gridDim.x * kRows;
+    int32_t r0 = (int32_t)blockIdx.x * kRows + (int)(threadIdx.x >> 5) * R;
+    int32_t y[R];
+    load_labels(a.labels, r0, n, y);
+    for (; r0 < n; r0 += step) {
+        float loss[R];
+        warp_rows<T, NV, R>(a, r0, n, w, r0 + step, y, loss);
+    }
     if (!a.total) return;
     __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) last = atomicAdd(a.valid + 1, 1) == (n + kRows - 1) / kRows - 1;
+    if (threadIdx.x == 0) last = atomicAdd(a.valid + 1, 1) == blocks - 1;
+    __syncthreads();
+    if (last) put_total<kThreads>(a, n);
+}
+
+// Many rows of a few classes: a thread a row.
+constexpr int kFewClasses = 16;
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_xent_thread(RowArgs<T> a) {
+    pdl_start();
+    __shared__ bool last;
+    const int32_t n = rows_of(a.d_n, a.n_cap), blocks = (n + kThreads - 1) / kThreads;
+    if ((int32_t)blockIdx.x >= blocks) return;
+    const int32_t r = (int32_t)blockIdx.x * kThreads + (int32_t)threadIdx.x;
+    if (r < n) {
+        const T* row = a.x + (int64_t)r * a.ld;
+        T* out = a.grad ? a.grad + (int64_t)r * a.ld_grad : nullptr;
+        int32_t y = __ldg(a.labels + r);
+        if (y < -1 || y >= a.classes) {
+            dev_err(ERR_INDEX);
+            y = -1;
+        }
+        float x[kFewClasses], m = -INFINITY, xy = 0.f, z = 0.f, loss = 0.f;
+#pragma unroll
+        for (int c = 0; c < kFewClasses; ++c) x[c] = y >= 0 && c < a.classes ? to_f(row[c]) : -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kFewClasses; ++c) {
+            m = fmaxf(m, x[c]);
+            if (c == y) xy = x[c];
+        }
+        if (m == -INFINITY) m = 0.f;
+#pragma unroll
+        for (int c = 0; c < kFewClasses; ++c) {
+            x[c] = exp_from(x[c], m);
+            z += x[c];
+        }
+        const float w = a.mean ? a.gs / (float)max(1, *a.valid) : a.gs;
+        const float inv = y < 0 || z == 0.f ? 0.f : w / z;
+        if (y >= 0) loss = loss_of(m, z, xy);
+        a.loss[r] = loss;
+        if (out) {
+#pragma unroll
+            for (int c = 0; c < kFewClasses; ++c)
+                if (c < a.classes) put(out + c, y < 0 || z == 0.f ? 0.f : fmaf(inv, x[c], c == y ? -w : 0.f));
+        }
+    }
+    if (!a.total) return;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(a.valid + 1, 1) == blocks - 1;
     __syncthreads();
     if (last) put_total<kThreads>(a, n);
 }
@@ -388,9 +470,12 @@ __global__ void __launch_bounds__(kThreads) k_xent_small(RowArgs<T> a) {
     v = block_sum<kThreads, int32_t>(v, sh);
     const float w = a.mean ? a.gs / (float)max(1, v) : a.gs;
     float sum = 0.f;
-    for (int32_t r0 = ((int32_t)blockIdx.x * kWarps + warp) * R; r0 < n; r0 += kSmallCtas * kWarps * R) {
+    int32_t r0 = ((int32_t)blockIdx.x * kWarps + warp) * R;
+    int32_t y[R];
+    load_labels(a.labels, r0, n, y);
+    for (; r0 < n; r0 += kSmallCtas * kWarps * R) {
         float loss[R];
-        warp_rows<T, NV, R>(a, r0, n, w, loss);
+        warp_rows<T, NV, R>(a, r0, n, w, r0 + kSmallCtas * kWarps * R, y, loss);
 #pragma unroll
         for (int r = 0; r < R; ++r) sum += loss[r];
     }
@@ -723,22 +808,38 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_xent_stream(RowArgs<T> a, int
     }
 }
 
-// Rows whose label is not -1 (one block); clears the count of finished blocks.
+// Rows whose label is not -1 (one cluster: one block, or kCountCtas when there
+// are many); clears the count of finished blocks.
+constexpr int kCountCtas = 8, kCountMany = 8192;
 __global__ void __launch_bounds__(kTotalThreads) k_xent_count(const int32_t* __restrict__ labels, int32_t n_cap,
                                                               const int32_t* __restrict__ d_n,
                                                               int32_t* __restrict__ valid, float* __restrict__ total) {
     pdl_start();
     __shared__ int32_t sh[kTotalThreads / 32 + 1];
-    const int32_t n = rows_of(d_n, n_cap);
+    __shared__ float part;  // a count's bits
+    const int32_t n = rows_of(d_n, n_cap), stride = (int32_t)(gridDim.x * kTotalThreads);
     int32_t v = 0;
-#pragma unroll 8
-    for (int32_t i = threadIdx.x; i < n; i += kTotalThreads) v += labels[i] != -1;
+    for (int32_t i0 = (int32_t)(blockIdx.x * kTotalThreads + threadIdx.x); i0 < n; i0 += 8 * stride) {
+        int32_t y[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int32_t i = i0 + u * stride;
+            y[u] = i < n ? __ldg(labels + i) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v += y[u] != -1;
+    }
     v = block_sum<kTotalThreads, int32_t>(v, sh);
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0) part = __int_as_float(v);
+    cluster_sync();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        v = 0;
+        for (uint32_t c = 0; c < gridDim.x; ++c) v += __float_as_int(ld_cluster(map_rank(smem_addr(&part), c)));
         valid[0] = v;
         valid[1] = 0;
         if (total) total[0] = 0.f, total[1] = (float)v;
     }
+    cluster_sync();  // the parts stay until they are read
 }
 
 // -------------------------------------------------------------------- host
@@ -764,10 +865,13 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned thr
 
 template <typename T, int NV, int R>
 sg_status run_warp(const RowArgs<T>& a, bool small, cudaStream_t s) {
-    if (small)
+    if (small) {
         SG_CUDA(launch_cluster(k_xent_small<T, NV, R>, kSmallCtas, kThreads, kSmallCtas, s, 0, a));
-    else
-        SG_CUDA(launch_pdl(k_xent_warp<T, NV, R>, dim3((unsigned)cdiv(a.n_cap, kThreads / 32 * R)), dim3(kThreads), 0, s, a));
+        return SG_OK;
+    }
+    int64_t blocks = cdiv(a.n_cap, kThreads / 32 * R);
+    if (blocks > (int64_t)num_sms() * kWarpBlocks<NV, R>) blocks = (int64_t)num_sms() * kWarpBlocks<NV, R>;
+    SG_CUDA(launch_pdl(k_xent_warp<T, NV, R>, dim3((unsigned)blocks), dim3(kThreads), 0, s, a));
     return SG_OK;
 }
 
@@ -799,9 +903,18 @@ sg_status run(RowArgs<T> a, cudaStream_t s) {
     const bool by_warp = nv <= 32 * kVecs;
     // one cluster serves a call whose vectors its warps hold in a few turns
     const bool small = by_warp && a.n_cap <= 1024 && a.n_cap * nv <= kSmallCtas * kThreads * kVecs;
-    if (!small)
-        SG_CUDA(launch_pdl(k_xent_count, dim3(1), dim3(kTotalThreads), 0, s, a.labels, a.n_cap, a.d_n, a.valid, a.total));
+    if (!small) {
+        if (a.n_cap > kCountMany)
+            SG_CUDA(launch_cluster(k_xent_count, kCountCtas, kTotalThreads, kCountCtas, s, 0, a.labels, a.n_cap, a.d_n,
+                                   a.valid, a.total));
+        else
+            SG_CUDA(launch_pdl(k_xent_count, dim3(1), dim3(kTotalThreads), 0, s, a.labels, a.n_cap, a.d_n, a.valid, a.total));
+    }
     if (a.n_cap == 0 && !small) return SG_OK;
+    if (!small && a.classes <= kFewClasses) {
+        SG_CUDA(launch_pdl(k_xent_thread<T>, dim3((unsigned)cdiv(a.n_cap, kThreads)), dim3(kThreads), 0, s, a));
+        return SG_OK;
+    }
     if (by_warp) {
         if (nv <= 32) return run_warp<T, 1, 4>(a, small, s);
         if (nv <= 64) return run_warp<T, 2, 2>(a, small, s);

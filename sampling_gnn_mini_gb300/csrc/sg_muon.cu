@@ -926,6 +926,7 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
     const int row = (warp & 3) * 32 + lane;  // of tensor memory, in every pass over it
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t phase = 0, a_phase = 0;
+    const int km = (m + 15) / 16;  // 16-row pieces of X, and columns of A
     const int kx = max(1, (min(W, n - j0) + 15) / 16);  // 16-column pieces of X that are not empty
     const int part = warp >> 2;  // which columns this warp takes in a pass over tensor memory
     // runs `issue` on one thread once all shared memory is written, and waits for it
@@ -1042,14 +1043,14 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
             gather();
         }
         // B = a I + b A + c A A, in A's place
-        product([&] { pairs(kFusedM / 16, 2, 128, desc_f16(false, kFusedM), a_rows, a_rows); });
+        product([&] { pairs(km, 2, 128, desc_f16(false, kFusedM), a_rows, a_rows); });
         // every CTA has A: this one's copies are done with its rows
         if (S > 1) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
         const float ca = steps.coef[step][0] * kScale, cb = steps.coef[step][1], cc = steps.coef[step][2] * (1.f / kScale);
 #pragma unroll 1
         for (int c0 = part * (kFusedM * 4 / kWarps); c0 < (part + 1) * (kFusedM * 4 / kWarps); c0 += 32) {
             float v[32];
-            load_sum(kFusedM / 16, 2, 128, lanes + (uint32_t)c0, v);
+            load_sum(km, 2, 128, lanes + (uint32_t)c0, v);
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] *= cc;
             if ((c0 >> 5) == (warp & 3)) {  // the diagonal: column c0 + lane of row `row`
@@ -1077,12 +1078,12 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
             }
         }
         // X <- B X
-        product([&] { pairs(kFusedM / 16, kXMains, kXCols, desc_f16(true, 16 * kx), a_rows, x_cols); });
+        product([&] { pairs(km, kXMains, kXCols, desc_f16(true, 16 * kx), a_rows, x_cols); });
         if (step + 1 < steps.count) {
 #pragma unroll 1
             for (int c0 = part * (W * 4 / kWarps); c0 < (part + 1) * (W * 4 / kWarps); c0 += 32) {
                 float v[32];
-                load_sum(kFusedM / 16, kXMains, kXCols, lanes + (uint32_t)c0, v);
+                load_sum(km, kXMains, kXCols, lanes + (uint32_t)c0, v);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     float x[8];
@@ -1120,7 +1121,7 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
 #pragma unroll 1
         for (int c0 = part * kCols; c0 < (part + 1) * kCols; c0 += 32) {
             float v[32];
-            load_sum(kFusedM / 16, kXMains, kXCols, lanes + (uint32_t)c0, v);
+            load_sum(km, kXMains, kXCols, lanes + (uint32_t)c0, v);
 #pragma unroll
             for (int t = 0; t < 8; ++t)
                 *reinterpret_cast<float4*>(tile + row * (W + 4) + c0 + 4 * t) =
@@ -1145,7 +1146,7 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
 #pragma unroll 1
         for (int c0 = part * kCols; c0 < (part + 1) * kCols; c0 += 32) {
             float v[32];
-            load_sum(kFusedM / 16, kXMains, kXCols, lanes + (uint32_t)c0, v);
+            load_sum(km, kXMains, kXCols, lanes + (uint32_t)c0, v);
 #pragma unroll
             for (int t = 0; t < 32; ++t) tile[row * ld_row + (c0 + t) * ld_col] = v[t];
         }

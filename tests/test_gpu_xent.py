@@ -89,7 +89,8 @@ def _ws(n, c):
 
 @pytest.mark.parametrize("n,c", [(1, 1), (1, 2), (3, 31), (5, 32), (256, 128), (300, 172), (129, 127), (40, 1000),
                                  (17, 1025), (9, 4096), (7, 8191), (5, 8193), (4, 16385), (3, 32771), (3, 50257),
-                                 (2, 65536), (1, 131072), (2, 131075), (1, 300001), (5000, 7), (4097, 40)])
+                                 (2, 65536), (1, 131072), (2, 131075), (1, 300001), (5000, 7), (4097, 40),
+                                 (30001, 16), (20000, 17), (70000, 3), (9000, 130), (3000, 1000), (5001, 600)])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_loss_and_gradient(n, c, dt):
     rng = np.random.default_rng(n * 13 + c)
