@@ -4,14 +4,16 @@
 // Bound by memory: the logits are read and the gradient is written once, so a
 // row has to stay on the chip between the two.  It stays in registers, as the
 // 16-byte vectors it was read in (up to kVecs a thread), spread over
+//   a thread            rows of up to 16 classes (k_xent_thread)
 //   a warp              rows of up to 32 kVecs vectors (k_xent_warp)
 //   a cluster of CTAs   longer rows (k_xent_row): 1 to 8 CTAs of 256 or 512 threads
 // Each warp reduces its part of the row to (m, z) relative to its own
 // maximum; the parts meet once, in shared memory (of every CTA of the
 // cluster), and a warp scales its exponentials by exp(m_warp - m) w / z, so a
-// row costs one barrier.  Vectors past the registers' reach (rows above 65,536
-// fp32 or 131,072 bf16 logits, or one vector of a misaligned row) are read
-// again for the gradient, from L2.
+// row costs one barrier.  Vectors past the registers' reach (rows above 131,072
+// fp32 or 262,144 bf16 logits, or one vector of a misaligned row) are read
+// again for the gradient, from L2.  Many long rows are streamed through shared
+// memory instead, ahead of their use (k_xent_stream).
 //
 // The mean needs the number of labelled rows before the first gradient:
 // k_xent_count finds it, and the last block to finish sums the losses in
@@ -456,7 +458,8 @@ __global__ void __launch_bounds__(kThreads) k_xent_thread(RowArgs<T> a) {
 }
 
 // The whole of a small call in one cluster: each CTA counts the labels, the
-// cluster's warps take the rows in turn, the warps' sums meet in CTA 0.
+// cluster's warps take the rows in turn, the warps' sums meet in CTA 0.  256
+// rows of 128 fp32: 6.3 us with the host's time, which bounds it.
 template <typename T, int NV, int R>
 __global__ void __launch_bounds__(kThreads) k_xent_small(RowArgs<T> a) {
     pdl_start();

@@ -8,7 +8,7 @@
 //
 // Number format.  The iteration multiplies small singular values by up to
 // a = 3.44 a step (485 in five), and an operand's rounding error with them, so
-// one 16-bit operand a product (2^-9 in bf16, 2^-12 in fp16) would leave
+// one 16-bit operand a product (off by up to 2^-8 in bf16, 2^-11 in fp16) would leave
 // errors of a percent and more.  Every operand is held as two fp16 terms,
 // hi + lo, of 256 times its value: the iterates are bounded (singular values
 // up to about 1.2), so 256 x stays inside fp16's range and lo above its
@@ -330,6 +330,9 @@ __device__ __forceinline__ void ring_drain(Ring<STAGES>& r, int issued) {
 // written as mirror images.  The K tiles are split over the S CTAs of a
 // cluster: each leaves its partial sum in shared memory, and CTA r adds
 // columns [r, r + 1) 128 / S of all parts in rank order.
+// 1024 x 4096: GRAM 15.2 us (144 CTAs, K split over 4; main loop 9.6, bound by the
+// ring's loads), SQUARE 10.3 (main loop 3.3: the rest is set-up, the exchange
+// of parts and the writes).
 constexpr int kSymStages = 3;
 constexpr int kSymStage = 4 * kOperand;  // hi and lo of both operands: 64 KB
 constexpr int kSymSmem = kSymStages * kSymStage + 1024;
@@ -519,7 +522,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 
 // X' = B X: a 128 x BN tile.  B's tile is K-major (B is m x m), X's MN-major
 // (its rows are K, n contiguous).
-// EPI 0: X' as planes; 1: out = keep w + step X', transposed back when tall.
+// FINAL: out = keep w + step X', transposed back when tall; else X' as planes.
+// 1024 x 4096 (128 tiles of 256 columns): 19.5 us, of them 14.6 in the main
+// loop, which the ring's loads bound (110 bytes/ns an SM, 96 KB a stage of 1,536
+// cycles of products; tensor pipe active 55 %).
 struct FinalArgs {
     const void* w;
     void* out;
@@ -698,8 +704,13 @@ __global__ void __launch_bounds__(kThreads) k_ns_store(Planes X, int64_t ldx, in
 //   CTA r adds rows [128 r / S, ..) of all parts in rank order and copies its
 //   rows of A, as pairs, to every CTA;
 //   every CTA forms B = a I + b A + c A A and X <- B X for its own columns.
-// No iterate goes to memory: the call reads its input and writes the result.  The time is a chain of latencies: two cluster barriers, three
-// 128-deep products and four passes over tensor memory a step.
+// No iterate goes to memory: the call reads its input and writes the result.
+// The time is a chain of latencies: two cluster barriers, three products and
+// four passes over tensor memory a step.  Cycles of a step, 128 x 200 on one SM
+// (49 us for five steps) / 128 x 2048 on 16 (68 us): partial Gram 3,800 / 2,800,
+// taking it out 1,100 / 2,100 with the barrier, exchange - / 8,500 (distributed
+// shared memory gives 16 bytes a clock an SM), square 2,800 / 2,700, B 1,700 /
+// 2,300, B X 4,000 / 2,700, X 2,100 / 1,300; the tensor pipe is active 24 % / 13 %.
 constexpr int kFusedM = 128;
 constexpr int kFusedMaxCtas = 16;
 constexpr int kPairTile = kFusedM * 128;  // bytes of a 128 x 64 fp16 tile
