@@ -39,8 +39,9 @@ constexpr int kDigits = 256;
 constexpr int kMaxPasses = 4;
 constexpr int kCopies = 8;            // of the digit counts, which blocks add to in turn
 constexpr int kSortThreads = 512;     // of a pass
-constexpr int kSmallSort = 5120;      // positions sorted by one block (us for the gradient of 64 / 128 columns, one block /
-                                      // a cluster: 2,048 positions 18, 21 / 20, 27; 4,999: 21, 27 / 22, 28; 8,192: 27, 35 / 22, 29)
+constexpr int kSmallSort = 5120;      // positions sorted by one block (us for the dense / compact gradient of 128 columns,
+                                      // one block: 1,000 positions 10.8 / 11.6, 3,000 14.1 / 14.9, 5,000 17.7 / 18.5; a
+                                      // cluster: 15.4 / 18.0, 15.9 / 18.5, 16.4 / 19.0)
 constexpr int kSmallThreads = 1024;
 constexpr int kRunTile = kThreads * 16;   // sorted positions a block of k_runs looks at
 constexpr int kFewBlocks = 76;           // half the SMs: below this many blocks chunks are 8 positions, not 32
@@ -1126,7 +1127,8 @@ sg_status run_sort(const int32_t* ids, int64_t n_cap, const int32_t* d_n, int64_
     }
     // the fewest items a thread (4, 8 or 12) with which every tile has an SM of
     // its own: two tiles on an SM take twice as long as one, and every later
-    // tile waits for them
+    // tile waits for them (us for the whole gradient of 256 columns, 4 / 8 / 12:
+    // 100,000 positions 65 / 70 / -, 620,000 191 / 189 / 193, 800,003 242 / 245 / 238)
     const int64_t wave = (int64_t)num_sms() * kSortThreads;
     const int items = n_cap <= 4 * wave ? 4 : n_cap <= 8 * wave ? 8 : 12;
     const int64_t tiles = cdiv(n_cap, kSortThreads * items);

@@ -1263,7 +1263,8 @@ sg_status launch_sym(const PairMaps& maps, int64_t tiles, int32_t count, int32_t
 
 // The upper triangle's tiles are few when m is small, and K is long: K is
 // split over up to 8 CTAs while that many more still fit the SMs and each
-// keeps two K tiles or more.
+// keeps two K tiles or more.  us for five steps, split 1 / 2 / 4 / 8 at most: 256 x
+// 4096 324 / 213 / 162 / 142; 1024 x 4096 461 / 330 / 269 / -.
 template <int KIND>
 sg_status run_sym(const PairMaps& maps, int32_t count, int32_t m, int32_t K, const float* coef, Planes in, Planes out,
                   int64_t ld, cudaStream_t s) {
@@ -1363,7 +1364,9 @@ sg_status run(Source<TS> src, int32_t count, int32_t rows, int32_t cols, int32_t
     // a matrix that the shared memory of one cluster holds is done in one
     // launch: up to 256 columns by one CTA, which has nothing to exchange; else
     // 64 columns a CTA while 16 CTAs reach, since each product and each pass
-    // over tensor memory is then half as long
+    // over tensor memory is then half as long.  us, cold: 128 x 200 by 256 / 64 /
+    // 128 columns a CTA 59 / 64 / 70, launches of products 125; 128 x 1024 by 64 / 128
+    // columns 72 / 78, launches 123; 128 x 2048 88, launches 127
     if (m <= kFusedM && n <= kFusedMaxCtas * 128 && steps > 0 && (n <= 8 * 64 || clusters_of_16())) {
         Steps st;
         st.count = steps;
@@ -1408,8 +1411,9 @@ sg_status run(Source<TS> src, int32_t count, int32_t rows, int32_t cols, int32_t
              map_f16(&mb[i].xlo, x[i].lo, n, m, count, L.ldx, kBK);
     if (!ok) return fail(SG_ERR_CUDA, "orthogonalise: tensor map encoding failed");
     // 256-column tiles read B least often, when they give three SMs of four a
-    // tile; 64-column ones are the quickest when even they leave SMs idle
-    // (1001 x 603: 80 tiles of 64 columns against 40 of 128)
+    // tile; 64-column ones are the quickest when even they leave SMs idle.  us,
+    // 64 / 128 / 256: 1001 x 603 148 / 154 / 185; 512 x 4096 188 / 163 / 184; 768 x
+    // 2000 215 / 182 / 207; 1024 x 4096 398 / 302 / 273
     const int64_t bands = cdiv(m, kTile) * count;
     const int bn = cdiv(n, 256) * bands >= num_sms() * 3 / 4 ? 256 : cdiv(n, 64) * bands <= num_sms() ? 64 : 128;
     for (int32_t k = 0; k < steps; ++k) {
