@@ -701,16 +701,16 @@ __global__ void __launch_bounds__(kThreads) k_ns_store(Planes X, int64_t ldx, in
 // that serves both as K-major rows (A = X X^T) and as an MN-major operand
 // (X <- B X).  A step is
 //   each CTA's partial X X^T (K = W), left in its shared memory as fp32;
-//   CTA r adds rows [128 r / S, ..) of all parts in rank order and copies its
-//   rows of A, as pairs, to every CTA;
+//   CTA r adds its share of the parts' 8 x 8 blocks (half of A: it is
+//   symmetric) and copies them, as pairs, to every CTA, which completes A;
 //   every CTA forms B = a I + b A + c A A and X <- B X for its own columns.
 // No iterate goes to memory: the call reads its input and writes the result.
 // The time is a chain of latencies: two cluster barriers, three products and
 // four passes over tensor memory a step.  Cycles of a step, 128 x 200 on one SM
-// (49 us for five steps) / 128 x 2048 on 16 (68 us): partial Gram 3,800 / 2,800,
-// taking it out 1,100 / 2,100 with the barrier, exchange - / 8,500 (distributed
-// shared memory gives 16 bytes a clock an SM), square 2,800 / 2,700, B 1,700 /
-// 2,300, B X 4,000 / 2,700, X 2,100 / 1,300; the tensor pipe is active 24 % / 13 %.
+// (49 us for five steps) / 128 x 2048 on 16 (59 us): partial Gram 3,800 / 2,800,
+// taking it out 1,100 / 1,700 with the barrier, exchange - / 5,000 (8,500 with all
+// blocks of A; distributed shared memory gives 16 bytes a clock an SM), square
+// 2,800 / 2,700, B 1,700 / 2,300, B X 4,000 / 2,700, X 2,100 / 1,300.
 constexpr int kFusedM = 128;
 constexpr int kFusedMaxCtas = 16;
 constexpr int kPairTile = kFusedM * 128;  // bytes of a 128 x 64 fp16 tile
@@ -719,8 +719,6 @@ constexpr int kPairTile = kFusedM * 128;  // bytes of a 128 x 64 fp16 tile
 // from tensor memory and needs no fp32 copy in shared memory.
 template <int W>
 constexpr int kFusedThreads = W == 256 ? 512 : kThreads;
-template <int W>
-constexpr int kFusedSmem = 2 * (W / 64) * kPairTile + 4 * kPairTile + (W == 256 ? 0 : kFusedM * kFusedM * 4) + 1024;
 
 // Address of 8 elements (columns 8 c ..) of row r of a [128 x 64 t] swizzled
 // operand.
@@ -728,30 +726,77 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     return (uint32_t)((c >> 3) * kPairTile + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-// Rows [rank 128 / S, ..) of A from the S partial sums, added in rank order,
-// as pairs into this CTA's A (da: the partial sums' place, in every CTA).
+// The exchange of A.  A is symmetric, so of its 16 x 16 blocks of 8 x 8 the
+// kHalf blocks (g, g + d mod 16), d = 0 .. 8, of each row group g are enough;
+// the pair (g, g + 8) = (g + 8, g) has two names, and owns_last picks one.
+constexpr int kHalf = 9;
+constexpr int kDumpBytes = kFusedM * kHalf * 8 * 4;   // partial sums: [d][half][row][4]
+constexpr int kGroupBytes = 2 * kHalf * 128;          // a row group's sums as pairs: [plane][d][8][8]
+constexpr int kStageBytes = kFusedM / 8 * kGroupBytes;
+__device__ __forceinline__ bool owns_last(int g) { return ((g ^ (g >> 3)) & 1) == 0; }
+
+template <int W>
+constexpr int kFusedSmem = 2 * (W / 64) * kPairTile + 4 * kPairTile + (W == 256 ? 0 : kDumpBytes + kStageBytes) + 1024;
+
+// The blocks of this rank's row groups from the S partial sums (da: their place,
+// in every CTA), as pairs into this CTA's stage.  They are added in the order
+// of ranks beginning with this one, so that not every CTA reads from the same one.
 template <int S>
-__device__ __forceinline__ void reduce_rows(uint32_t da, uint32_t rank, uint8_t* as) {
-    constexpr int kRows = kFusedM / S, kTurns = kRows * 32 / kThreads;  // 4-column pieces of the rows a thread takes
-    float4 x[kTurns][S];  // 16 loads in flight, whatever S is
+__device__ __forceinline__ void reduce_blocks(uint32_t da, uint32_t rank, uint8_t* stage) {
+    constexpr int kGroups = kFusedM / 8 / S, kItems = kGroups * kHalf * 16;  // 4 columns of a block's row
+    constexpr int kTurns = (kItems + kThreads - 1) / kThreads;
+    float4 x[kTurns][S];
 #pragma unroll
     for (int i = 0; i < kTurns; ++i) {
-        const int t = i * kThreads + (int)threadIdx.x, r = (int)rank * kRows + t % kRows, c = t / kRows;
+        const int t = i * kThreads + (int)threadIdx.x, r = t % 8, c = t / 8 % (2 * kHalf), g = (int)rank * kGroups + t / (16 * kHalf);
+        if (t < kItems && (c < 16 || owns_last(g))) {
 #pragma unroll
-        for (int s = 0; s < S; ++s) x[i][s] = ld_cluster4(map_rank(da, (uint32_t)s) + (uint32_t)((c * kFusedM + r) * 16));
+            for (int s = 0; s < S; ++s)
+                x[i][s] = ld_cluster4(map_rank(da, (rank + (uint32_t)s) % S) + (uint32_t)((c * kFusedM + 8 * g + r) * 16));
+        }
     }
 #pragma unroll
     for (int i = 0; i < kTurns; ++i) {
-        const int t = i * kThreads + (int)threadIdx.x, r = (int)rank * kRows + t % kRows, c = t / kRows;
-        float4 v = x[i][0];
+        const int t = i * kThreads + (int)threadIdx.x, r = t % 8, c = t / 8 % (2 * kHalf), g = (int)rank * kGroups + t / (16 * kHalf);
+        if (t < kItems && (c < 16 || owns_last(g))) {
+            float4 v = x[i][0];
 #pragma unroll
-        for (int s = 1; s < S; ++s) v.x += x[i][s].x, v.y += x[i][s].y, v.z += x[i][s].z, v.w += x[i][s].w;
-        uint32_t h0, l0, h1, l1;
-        split2(v.x * (1.f / kScale), v.y * (1.f / kScale), h0, l0);
-        split2(v.z * (1.f / kScale), v.w * (1.f / kScale), h1, l1);
-        const uint32_t at = chunk_at(r, c >> 1) + (c & 1) * 8;
-        *reinterpret_cast<uint2*>(as + at) = make_uint2(h0, h1);
-        *reinterpret_cast<uint2*>(as + 2 * kPairTile + at) = make_uint2(l0, l1);
+            for (int s = 1; s < S; ++s) v.x += x[i][s].x, v.y += x[i][s].y, v.z += x[i][s].z, v.w += x[i][s].w;
+            uint32_t h0, l0, h1, l1;
+            split2(v.x * (1.f / kScale), v.y * (1.f / kScale), h0, l0);
+            split2(v.z * (1.f / kScale), v.w * (1.f / kScale), h1, l1);
+            uint8_t* at = stage + g * kGroupBytes + c * 64 - (c & 1) * 56 + r * 16;
+            *reinterpret_cast<uint2*>(at) = make_uint2(h0, h1);
+            *reinterpret_cast<uint2*>(at + kHalf * 128) = make_uint2(l0, l1);
+        }
+    }
+}
+
+// A, both halves, from the staged blocks: four of them a warp at a time, as they
+// are and transposed (a diagonal block: transposed only).  Both names of a pair
+// write the same.
+__device__ __forceinline__ void spread_blocks(uint32_t stage, uint32_t as) {
+    const int lane = (int)(threadIdx.x & 31), r = lane & 7;
+#pragma unroll 3
+    for (int k = (int)(threadIdx.x >> 5); k < kHalf * 8; k += kThreads / 32) {
+        const int p = k / (kHalf * 4), q = k % (kHalf * 4), d = q >> 2;
+        int g = (q & 3) * 4 + (lane >> 3);
+        if (d == 8 && !owns_last(g)) g ^= 8;
+        const int c = (g + d) & 15;
+        uint32_t x0, x1, x2, x3;
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+                     : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3)
+                     : "r"(stage + (uint32_t)(g * kGroupBytes + p * kHalf * 128 + d * 128 + r * 16))
+                     : "memory");
+        if (d != 0)
+            asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(
+                             as + (uint32_t)(p * 2 * kPairTile) + chunk_at(8 * g + r, c)),
+                         "r"(x0), "r"(x1), "r"(x2), "r"(x3)
+                         : "memory");
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(
+                         as + (uint32_t)(p * 2 * kPairTile) + chunk_at(8 * c + r, g)),
+                     "r"(x0), "r"(x1), "r"(x2), "r"(x3)
+                     : "memory");
     }
 }
 
@@ -811,7 +856,8 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
     uint8_t* base = dsm + ((1024 - (smem_addr(dsm) & 1023)) & 1023);
     uint8_t* xs = base;                          // X: hi tiles, then lo tiles
     uint8_t* as = xs + 2 * kXTiles * kPairTile;  // A, then B: hi tiles (2), lo tiles (2)
-    float* dump = reinterpret_cast<float*>(as + 4 * kPairTile);  // [column / 4][row][4]
+    float* dump = reinterpret_cast<float*>(as + 4 * kPairTile);
+    [[maybe_unused]] uint8_t* stage = as + 4 * kPairTile + kDumpBytes;
     constexpr uint32_t kXLo = kXTiles * kPairTile, kALo = 2 * kPairTile;
     if (threadIdx.x == 0) {
         mbar_init(&done, 1);
@@ -933,7 +979,7 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
             *reinterpret_cast<uint4*>(xs + kXLo + chunk_at(row_of(it), chunk_of(it))) = lo;
         }
     }
-    const uint32_t xa = smem_addr(xs), aa = smem_addr(as), da = smem_addr(dump);
+    const uint32_t xa = smem_addr(xs), aa = smem_addr(as);
     const int row = (warp & 3) * 32 + lane;  // of tensor memory, in every pass over it
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t phase = 0, a_phase = 0;
@@ -994,35 +1040,34 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
         return smem_desc_mn_sw128(xa + (lo ? kXLo : 0) + (uint32_t)(k * 16 * 128), kPairTile);
     };
     // the partial sums of all CTAs into A, in every CTA
-    const auto gather = [&] {
-        if (threadIdx.x == 0 && S > 1) mbar_expect_tx(&full, (uint32_t)(4 * kPairTile) / S * (S - 1));
+    [[maybe_unused]] const auto gather = [&](bool last) {
+        if (threadIdx.x == 0) mbar_expect_tx(&full, (uint32_t)kStageBytes / S * (S - 1));
         cluster_sync();
-        // this CTA's rows of A: into its own copy, then to the others' in
-        // pieces that lie in one run (8 rows are one 1024-byte swizzle group)
-        switch (S) {
-            case 1: reduce_rows<1>(da, rank, as); break;
-            case 2: reduce_rows<2>(da, rank, as); break;
-            case 4: reduce_rows<4>(da, rank, as); break;
-            case 8: reduce_rows<8>(da, rank, as); break;
-            default: reduce_rows<16>(da, rank, as); break;
+        // this CTA's row groups into its own stage, then to the others'.  (The
+        // barrier: all partial sums are written, and all copies of the last
+        // step have been waited for, so the stage may be written.)
+        if (W == 128 || S == 16)
+            reduce_blocks<16>(smem_addr(dump), rank, stage);
+        else
+            reduce_blocks<8>(smem_addr(dump), rank, stage);
+        fence_async();
+        __syncthreads();
+        if (warp == 0 && lane < (int)S && lane != (int)rank) {  // lane: to whom
+            const uint32_t bytes = (uint32_t)kStageBytes / S, from = smem_addr(stage) + rank * bytes;
+            asm volatile(
+                "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                    map_rank(from, (uint32_t)lane)),
+                "r"(from), "r"(bytes), "r"(map_rank(smem_addr(&full), (uint32_t)lane))
+                : "memory");
         }
-        if (S > 1) {
-            fence_async();
-            __syncthreads();
-            if (warp < 4 && lane < (int)S && lane != (int)rank) {  // warp: one of the 4 tiles; lane: to whom
-                const uint32_t bytes = (uint32_t)kPairTile / S, from = aa + (uint32_t)warp * kPairTile + rank * bytes;
-                asm volatile(
-                    "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
-                        map_rank(from, (uint32_t)lane)),
-                    "r"(from), "r"(bytes), "r"(map_rank(smem_addr(&full), (uint32_t)lane))
-                    : "memory");
-            }
-            __syncwarp();
-            if (!mbar_wait(&full, (uint32_t)a_phase) && lane == 0) dev_err(ERR_TIMEOUT);
-            __syncwarp();
-            asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
-        }
-            a_phase ^= 1u;
+        __syncwarp();
+        // With every other CTA's blocks here, all of them have read this one's
+        // partial sums, so those may be overwritten.
+        if (!mbar_wait(&full, (uint32_t)a_phase) && lane == 0) dev_err(ERR_TIMEOUT);
+        __syncwarp();
+        a_phase ^= 1u;
+        if (last) asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+        spread_blocks(smem_addr(stage), aa);
     };
 #pragma unroll 1
     for (int step = 0; step < steps.count; ++step) {
@@ -1047,16 +1092,17 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
                 float v[32];
                 load_sum(kx, 2, 128, lanes + (uint32_t)c0, v);
 #pragma unroll
-                for (int t = 0; t < 8; ++t)
-                    *reinterpret_cast<float4*>(dump + ((c0 / 4 + t) * kFusedM + row) * 4) =
-                        make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]);
+                for (int t = 0; t < 8; ++t) {
+                    const int d = (c0 / 8 + t / 2 - row / 8) & 15;
+                    if (d < kHalf)
+                        *reinterpret_cast<float4*>(dump + ((d * 2 + t % 2) * kFusedM + row) * 4) =
+                            make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]);
+                }
             }
-            gather();
+            gather(step + 1 == steps.count);
         }
         // B = a I + b A + c A A, in A's place
         product([&] { pairs(km, 2, 128, desc_f16(false, kFusedM), a_rows, a_rows); });
-        // every CTA has A: this one's copies are done with its rows
-        if (S > 1) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
         const float ca = steps.coef[step][0] * kScale, cb = steps.coef[step][1], cc = steps.coef[step][2] * (1.f / kScale);
 #pragma unroll 1
         for (int c0 = part * (kFusedM * 4 / kWarps); c0 < (part + 1) * (kFusedM * 4 / kWarps); c0 += 32) {
@@ -1172,6 +1218,8 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
     }
     tmem_fence_before();
     __syncthreads();
+    // no CTA leaves before the others have its last blocks
+    if constexpr (W < 256) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
     if (warp == 1) tmem_free<512>(tmem);
 }
 
@@ -1299,7 +1347,7 @@ sg_status run_apply(int bn, const ApplyMaps& maps, int32_t count, int32_t m, int
 
 const float kCoef[3] = {3.4445f, -4.7750f, 2.0315f};
 
-// The fused form: W columns a CTA, `ctas` of them (2, 4, 8 or 16, or 1).
+// The fused form: W columns a CTA, `ctas` of them (8 or 16; 1 for W = 256).
 template <int W, typename TS, typename TW>
 sg_status launch_fused(const Source<TS>& src, int32_t count, int32_t rows, int32_t cols, int ctas, const Steps& steps,
                        float eps, const FinalArgs& fin, cudaStream_t s) {
@@ -1366,7 +1414,7 @@ sg_status run(Source<TS> src, int32_t count, int32_t rows, int32_t cols, int32_t
     // 64 columns a CTA while 16 CTAs reach, since each product and each pass
     // over tensor memory is then half as long.  us, cold: 128 x 200 by 256 / 64 /
     // 128 columns a CTA 59 / 64 / 70, launches of products 125; 128 x 1024 by 64 / 128
-    // columns 72 / 78, launches 123; 128 x 2048 88, launches 127
+    // columns 64 / 70, launches 123; 128 x 2048 78, launches 127
     if (m <= kFusedM && n <= kFusedMaxCtas * 128 && steps > 0 && (n <= 8 * 64 || clusters_of_16())) {
         Steps st;
         st.count = steps;
