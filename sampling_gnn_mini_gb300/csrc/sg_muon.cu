@@ -1412,9 +1412,9 @@ sg_status run(Source<TS> src, int32_t count, int32_t rows, int32_t cols, int32_t
     // a matrix that the shared memory of one cluster holds is done in one
     // launch: up to 256 columns by one CTA, which has nothing to exchange; else
     // 64 columns a CTA while 16 CTAs reach, since each product and each pass
-    // over tensor memory is then half as long.  us, cold: 128 x 200 by 256 / 64 /
-    // 128 columns a CTA 59 / 64 / 70, launches of products 125; 128 x 1024 by 64 / 128
-    // columns 64 / 70, launches 123; 128 x 2048 78, launches 127
+    // over tensor memory is then half as long.  us: 128 x 200 by 256 / 64 columns
+    // a CTA 50 / 56; 128 x 1024 by 64 / 128 59 / 65.  With cold caches and against the
+    // launches of products: 128 x 200 59 / 125, 128 x 2048 78 / 127
     if (m <= kFusedM && n <= kFusedMaxCtas * 128 && steps > 0 && (n <= 8 * 64 || clusters_of_16())) {
         Steps st;
         st.count = steps;
