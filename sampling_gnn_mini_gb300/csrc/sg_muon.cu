@@ -16,11 +16,12 @@
 // products, hi hi + hi lo + lo hi, with fp32 accumulation in tensor memory.
 // Folding a I into B makes X <- B X one product with nothing to add.
 // The tensor core cuts a sum's low bits at every accumulation, always towards
-// zero: with all 3 x 256 accumulations of a 4096-deep product in one place the
-// result of 1024 x 4096 was off by 1.9e-5, an fp32 product's by 3.2e-6 (the
-// pairs themselves, in exact arithmetic: 5e-7).  So the two cross products,
-// 2^-11 as large, have an accumulator of their own, and hi hi is taken out of
-// tensor memory every 16 or 32 accumulations and summed in registers.
+// zero.  So the two cross products, 2^-11 as large, have an accumulator of their
+// own, and hi hi is taken out of tensor memory every 4 or 8 accumulations and
+// summed in registers.  Relative error and time, 1024 x 4096: 1.9e-5 with all
+// accumulations in one place; 6.7e-6 and 263 us with 16 or 32 in one; 3.4e-6, 266
+// with 8 or 16; 1.9e-6, 276 with 4 or 8 (fp32 products: 3.8e-6; the pairs
+// themselves, in exact arithmetic: 5e-7).  512 x 2048: 6.5, 5.6 and 3.1e-6 (fp32 3.4e-6).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -239,12 +240,12 @@ __device__ __forceinline__ void ring_init(Ring<STAGES>& r) {
 
 // How hi hi is summed: kBufs accumulators of COLS columns in turn, kTurn K tiles
 // (4 accumulations each) in each; the accumulator of the cross products is at
-// column 512 - COLS.  (At 256 columns there is room for one only, and the
-// products wait while it is read, so it is read half as often.)
+// column 512 - COLS.  A tile's hi hi comes first and its cross products while
+// the turn's accumulator is read (at 256 columns there is room for one only).
 template <int COLS>
 constexpr int kBufs = COLS > 128 ? 1 : 2;
 template <int COLS>
-constexpr int kTurn = COLS > 128 ? 8 : 4;
+constexpr int kTurn = COLS > 128 ? 2 : 1;
 
 // K tile i of the products: waits for its accumulator if it is the tile that
 // begins a turn; returns it.
@@ -330,9 +331,9 @@ __device__ __forceinline__ void ring_drain(Ring<STAGES>& r, int issued) {
 // written as mirror images.  The K tiles are split over the S CTAs of a
 // cluster: each leaves its partial sum in shared memory, and CTA r adds
 // columns [r, r + 1) 128 / S of all parts in rank order.
-// 1024 x 4096: GRAM 15.2 us (144 CTAs, K split over 4; main loop 9.6, bound by the
-// ring's loads), SQUARE 10.3 (main loop 3.3: the rest is set-up, the exchange
-// of parts and the writes).
+// 1024 x 4096: GRAM 18.0 us (144 CTAs, K split over 4; bound by the ring's loads
+// and the emptying of accumulators), SQUARE 10.0 (a third of it the main loop: the
+// rest is set-up, the exchange of parts and the writes).
 constexpr int kSymStages = 3;
 constexpr int kSymStage = 4 * kOperand;  // hi and lo of both operands: 64 KB
 constexpr int kSymSmem = kSymStages * kSymStage + 1024;
@@ -407,15 +408,18 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             const uint32_t ah = smem_addr(tiles + s * kSymStage), al = ah + kOperand;
             const uint32_t bh = diag ? ah : ah + 2 * kOperand, bl = bh + kOperand;
 #pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_issue(main, smem_desc_sw128(ah + kk * 32), smem_desc_sw128(bh + kk * 32), idesc,
+                          (uint32_t)((i % kTurn<kTile> | kk) != 0), false);
+            if (i + 1 < n_k) turn_end<kTile>(ring, i, n_k);
+#pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
                 const uint32_t o = kk * 32;
-                mma_issue(main, smem_desc_sw128(ah + o), smem_desc_sw128(bh + o), idesc,
-                          (uint32_t)((i % kTurn<kTile> | kk) != 0), false);
                 mma_issue(cross, smem_desc_sw128(ah + o), smem_desc_sw128(bl + o), idesc, (uint32_t)((i | kk) != 0), false);
                 mma_issue(cross, smem_desc_sw128(al + o), smem_desc_sw128(bh + o), idesc, 1u, false);
             }
             mma_commit(&ring.empty[s]);
-            turn_end<kTile>(ring, i, n_k);
+            if (i + 1 == n_k) turn_end<kTile>(ring, i, n_k);
         }
     } else if (warp < kSumWarps) {
         sum_turns<kTile>(ring, tmem, n_k, acc);
@@ -523,9 +527,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 // X' = B X: a 128 x BN tile.  B's tile is K-major (B is m x m), X's MN-major
 // (its rows are K, n contiguous).
 // FINAL: out = keep w + step X', transposed back when tall; else X' as planes.
-// 1024 x 4096 (128 tiles of 256 columns): 19.5 us, of them 14.6 in the main
-// loop, which the ring's loads bound (110 bytes/ns an SM, 96 KB a stage of 1,536
-// cycles of products; tensor pipe active 55 %).
+// 1024 x 4096 (128 tiles of 256 columns): 21.3 us, three quarters of them in the
+// main loop, which the ring's loads bound (110 bytes/ns an SM, 96 KB a stage of
+// 1,536 cycles of products).
 struct FinalArgs {
     const void* w;
     void* out;
@@ -606,16 +610,19 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             const uint32_t bh = smem_addr(tiles + s * kStage), bl = bh + kOperand;
             const uint32_t xh = bh + 2 * kOperand, xl = xh + (BN / 64) * kBox;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                const uint32_t o = kk * 32, ox = kk * 16 * 128;  // 16 K elements of a row; 16 K rows
-                mma_issue(main, smem_desc_sw128(bh + o), smem_desc_mn_sw128(xh + ox, kBox), idesc,
+            for (int kk = 0; kk < 4; ++kk)  // 16 K elements of a row; 16 K rows
+                mma_issue(main, smem_desc_sw128(bh + kk * 32), smem_desc_mn_sw128(xh + kk * 2048, kBox), idesc,
                           (uint32_t)((i % kTurn<BN> | kk) != 0), false);
+            if (i + 1 < n_k) turn_end<BN>(ring, i, n_k);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                const uint32_t o = kk * 32, ox = kk * 2048;
                 mma_issue(cross, smem_desc_sw128(bh + o), smem_desc_mn_sw128(xl + ox, kBox), idesc, (uint32_t)((i | kk) != 0),
                           false);
                 mma_issue(cross, smem_desc_sw128(bl + o), smem_desc_mn_sw128(xh + ox, kBox), idesc, 1u, false);
             }
             mma_commit(&ring.empty[s]);
-            turn_end<BN>(ring, i, n_k);
+            if (i + 1 == n_k) turn_end<BN>(ring, i, n_k);
         }
     } else if (warp < kSumWarps) {
         sum_turns<BN>(ring, tmem, n_k, acc);
