@@ -485,12 +485,18 @@ __global__ void __launch_bounds__(kThreads) k_xent_small(RowArgs<T> a) {
     }
     if ((threadIdx.x & 31) == 0) part[warp] = sum;
     cluster_sync();
-    if (blockIdx.x == 0 && threadIdx.x == 0 && a.total) {
+    if (blockIdx.x == 0 && warp == 0 && a.total) {
         float s = 0.f;
-        for (int c = 0; c < kSmallCtas; ++c)
-            for (int i = 0; i < kWarps; ++i) s += ld_cluster(map_rank(smem_addr(part + i), (uint32_t)c));
-        a.total[0] = a.mean ? s / (float)max(1, v) : s;
-        a.total[1] = (float)v;
+#pragma unroll
+        for (int k = 0; k < kSmallCtas * kWarps; k += 32) {
+            const int t = k + (int)threadIdx.x;
+            s += ld_cluster(map_rank(smem_addr(part + t % kWarps), (uint32_t)(t / kWarps)));
+        }
+        s = warp_sum(s);
+        if (threadIdx.x == 0) {
+            a.total[0] = a.mean ? s / (float)max(1, v) : s;
+            a.total[1] = (float)v;
+        }
     }
     cluster_sync();  // the parts stay until they are read
 }
