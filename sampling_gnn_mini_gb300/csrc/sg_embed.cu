@@ -39,10 +39,14 @@ constexpr int kDigits = 256;
 constexpr int kMaxPasses = 4;
 constexpr int kCopies = 8;            // of the digit counts, which blocks add to in turn
 constexpr int kSortThreads = 512;     // of a pass
-constexpr int kSmallSort = 5120;      // positions sorted by one block (us for the dense / compact gradient of 128 columns,
-                                      // one block: 1,000 positions 10.8 / 11.6, 3,000 14.1 / 14.9, 5,000 17.7 / 18.5; a
-                                      // cluster: 15.4 / 18.0, 15.9 / 18.5, 16.4 / 19.0)
 constexpr int kSmallThreads = 1024;
+constexpr int kSmallSort = 3 * kSmallThreads;  // positions sorted by one block (us for the dense / compact gradient of 64
+                                               // columns, one block: 1,000 positions 11.0 / 11.5, 3,000 14.1 / 14.9, 4,000
+                                               // 16.7 / 17.7, 5,000 17.4 / 18.5; a cluster of 8: 14.6 / 16.7, 14.9 / 17.4,
+                                               // 15.4 / 17.4, 15.4 / 17.7)
+constexpr int kSortCtas = 16;                  // blocks of a cluster that sorts more; 8 where they hold the list (6,000
+                                               // positions 15.4 / 18.0, by 16 blocks 16.4 / 19.2)
+constexpr int kClusterSort = kSortCtas * 2 * kSmallThreads;
 constexpr int kRunTile = kThreads * 16;   // sorted positions a block of k_runs looks at
 constexpr int kFewBlocks = 76;           // half the SMs: below this many blocks chunks are 8 positions, not 32
 constexpr uint32_t kNoKey = 0xFFFFFFFFu;  // beside the list's ends
@@ -436,7 +440,7 @@ __global__ void __launch_bounds__(kThreads) k_runs(const uint2* __restrict__ kv,
     }
 }
 
-// All of it for a short list, in one block: up to 5 items a thread, passes in shared
+// All of it for a short list, in one block: up to 3 items a thread, passes in shared
 // memory.
 template <int ITEMS>
 __global__ void __launch_bounds__(kSmallThreads) k_sort_small(const int32_t* __restrict__ ids, int64_t n_rows,
@@ -516,10 +520,11 @@ __global__ void __launch_bounds__(kSmallThreads) k_sort_small(const int32_t* __r
         if (q < n) out[q] = make_uint2(k[i], v[i]);
     }
     if (!n_out) return;
-    constexpr int kEight = 8;  // run starts, 8 positions a thread
-    const int32_t p0 = (int32_t)threadIdx.x * kEight;
+    constexpr int kRun = 4;  // run starts, 4 positions a thread
+    static_assert(kRun * kSmallThreads >= kSmallSort);
+    const int32_t p0 = (int32_t)threadIdx.x * kRun;
     uint32_t prev = p0 > 0 && p0 - 1 < n ? key[p0 - 1] : kNoKey, mine = 0;
-    for (int q = 0; q < kEight; ++q) {
+    for (int q = 0; q < kRun; ++q) {
         const uint32_t x = p0 + q < n ? key[p0 + q] : kNoKey;
         mine += x < (uint32_t)n_rows && x != prev;
         prev = x;
@@ -533,7 +538,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_sort_small(const int32_t* __r
 }
 constexpr int kSmallSmem = kSmallSort * 6 + (kSmallThreads / 32) * kDigits * 2;
 
-// A list of up to kClusterSort positions, in one launch: a cluster of kSortCtas
+// A list of up to kClusterSort positions, in one launch: a cluster of CTAS
 // blocks, block r holding positions [r, r + 1) ITEMS 1024 in every pass's
 // order.  The blocks exchange their digit counts in shared memory and the
 // pairs through memory (L2), written to their places and read back after a
@@ -541,9 +546,7 @@ constexpr int kSmallSmem = kSmallSort * 6 + (kSmallThreads / 32) * kDigits * 2;
 // pass: 20,000 positions of 1024 bf16 columns 48 / 52, of 64 fp32 columns
 // 24 / 27; 40,000 of 256 fp32 columns 51 / 49.  (With the pairs sent straight
 // into the other blocks' shared memory, 8 bytes at a time: 53 for the first.)
-constexpr int kSortCtas = 16;
-constexpr int kClusterSort = kSortCtas * 2 * kSmallThreads;
-template <int ITEMS>
+template <int ITEMS, int CTAS>
 __global__ void __launch_bounds__(kSmallThreads) k_sort_cluster(const int32_t* __restrict__ ids, int64_t n_rows,
                                                                 int32_t n_cap, const int32_t* __restrict__ d_n, Digits dg,
                                                                 int32_t span, uint2* kv0, uint2* kv1,
@@ -551,10 +554,10 @@ __global__ void __launch_bounds__(kSmallThreads) k_sort_cluster(const int32_t* _
     pdl_start();
     constexpr int kWarps = kSmallThreads / 32, kParts = kSmallThreads / kDigits, kPer = kWarps / kParts;
     __shared__ __align__(16) uint16_t cnt[kWarps][kDigits];
-    __shared__ uint32_t theirs[kSortCtas][kDigits];
+    __shared__ uint32_t theirs[CTAS][kDigits];
     __shared__ uint32_t sh[kWarps + 1];
     __shared__ uint32_t psum[kParts][kDigits], base[kDigits];
-    __shared__ uint32_t runs[kSortCtas];
+    __shared__ uint32_t runs[CTAS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int digit = threadIdx.x % kDigits, q4 = threadIdx.x / kDigits;  // a digit, and kPer of the warps
     const uint32_t rank = cluster_rank();
@@ -594,7 +597,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_sort_cluster(const int32_t* _
         // every block runs: its shared memory may be written
         if (p == 0) asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
 #pragma unroll
-        for (int c = 0; c < kSortCtas / kParts; ++c)
+        for (int c = 0; c < CTAS / kParts; ++c)
             asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(
                              map_rank(smem_addr(&theirs[rank][digit]), (uint32_t)(c * kParts + q4))),
                          "r"(all)
@@ -602,7 +605,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_sort_cluster(const int32_t* _
         cluster_sync();
         all = 0;
 #pragma unroll
-        for (uint32_t c = 0; c < kSortCtas; ++c) {
+        for (uint32_t c = 0; c < CTAS; ++c) {
             all += theirs[c][digit];
             lower += c < rank ? theirs[c][digit] : 0;
         }
@@ -635,13 +638,13 @@ __global__ void __launch_bounds__(kSmallThreads) k_sort_cluster(const int32_t* _
         last = __shfl_sync(0xFFFFFFFFu, x[i].x, 31);
     }
     int32_t e = (int32_t)block_excl_scan<kSmallThreads, uint32_t>(lane == 0 ? (uint32_t)mine : 0, sh, total);
-    if (threadIdx.x < kSortCtas)
+    if (threadIdx.x < CTAS)
         asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(map_rank(smem_addr(runs + rank), threadIdx.x)), "r"(total)
                      : "memory");
     cluster_sync();
     uint32_t sum = 0;
 #pragma unroll
-    for (uint32_t c = 0; c < kSortCtas; ++c) {
+    for (uint32_t c = 0; c < CTAS; ++c) {
         e += c < rank ? (int32_t)runs[c] : 0;
         sum += runs[c];
     }
@@ -1061,29 +1064,29 @@ sg_status run_sum(int vec, const void* g, const SumArgs<TO>& a, int32_t span, cu
     return launch_sum<TI, TO, 1>(g, a, span, s);
 }
 
-template <int ITEMS>
-cudaError_t launch_cluster(const int32_t* ids, int64_t n_rows, int64_t n_cap, const int32_t* d_n, Digits dg, int32_t span,
+template <int ITEMS, int CTAS>
+cudaError_t sort_by_cluster(const int32_t* ids, int64_t n_rows, int64_t n_cap, const int32_t* d_n, Digits dg, int32_t span,
                            uint2* const (&kv)[2], int32_t* starts, int32_t* n_out, cudaStream_t s) {
     static bool set = false;
     if (!set) {
-        const cudaError_t e = cudaFuncSetAttribute(k_sort_cluster<ITEMS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        const cudaError_t e = cudaFuncSetAttribute(k_sort_cluster<ITEMS, CTAS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         set = true;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kSortCtas);
+    cfg.gridDim = dim3(CTAS);
     cfg.blockDim = dim3(kSmallThreads);
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = kSortCtas;
+    at[1].val.clusterDim.x = CTAS;
     at[1].val.clusterDim.y = 1;
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_sort_cluster<ITEMS>, ids, n_rows, (int32_t)n_cap, d_n, dg, span, kv[0], kv[1], starts,
+    return cudaLaunchKernelEx(&cfg, k_sort_cluster<ITEMS, CTAS>, ids, n_rows, (int32_t)n_cap, d_n, dg, span, kv[0], kv[1], starts,
                               n_out);
 }
 
@@ -1110,18 +1113,17 @@ sg_status run_sort(const int32_t* ids, int64_t n_cap, const int32_t* d_n, int64_
         if (!set) {
             SG_CUDA(cudaFuncSetAttribute(k_sort_small<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem));
             SG_CUDA(cudaFuncSetAttribute(k_sort_small<3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem));
-            SG_CUDA(cudaFuncSetAttribute(k_sort_small<5>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem));
             set = true;
         }
-        SG_CUDA(items <= 1   ? go(k_sort_small<1>)
-                : items <= 3 ? go(k_sort_small<3>)
-                             : go(k_sort_small<5>));
+        SG_CUDA(items <= 1 ? go(k_sort_small<1>) : go(k_sort_small<3>));
         return SG_OK;
     }
     if (n_cap <= kClusterSort) {
         int32_t* const distinct = rows ? n_out : nullptr;
-        SG_CUDA(n_cap <= kClusterSort / 2 ? launch_cluster<1>(ids, n_rows, n_cap, d_n, dg, span, kv, starts, distinct, s)
-                                          : launch_cluster<2>(ids, n_rows, n_cap, d_n, dg, span, kv, starts, distinct, s));
+        const auto sort = n_cap <= kClusterSort / 4   ? sort_by_cluster<1, kSortCtas / 2>
+                          : n_cap <= kClusterSort / 2 ? sort_by_cluster<1, kSortCtas>
+                                                      : sort_by_cluster<2, kSortCtas>;
+        SG_CUDA(sort(ids, n_rows, n_cap, d_n, dg, span, kv, starts, distinct, s));
         *sorted = kv[(dg.passes & 1) ^ 1];
         return SG_OK;
     }

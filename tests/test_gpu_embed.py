@@ -190,6 +190,22 @@ def test_gradient(n, dim, n_rows, kind, tg, to, mode):
     assert np.array_equal(got[1], again[1])
 
 
+@pytest.mark.parametrize("mode", ["rows", "dense"])
+@pytest.mark.parametrize("kind", ["power", "same", "distinct"])
+@pytest.mark.parametrize("n", [1023, 1024, 1025, 2048, 3071, 3073, 4095, 8191, 8192])
+def test_gradient_where_the_sort_changes(n, kind, mode):
+    # the largest lists of one form of the sort and the shortest of the next
+    rng = np.random.default_rng(n)
+    dim, n_rows = 8, 9000
+    ids = _ids(rng, n, n_rows, kind)
+    g = torch.from_numpy(rng.standard_normal((n, dim)).astype(np.float32)).cuda()
+    base = torch.zeros((n_rows, dim), device="cuda")
+    _check_bwd(_bwd(ids, n_rows, g, 1.5, mode, "f32", base), ids, n_rows, g, 1.5, mode, "f32", base)
+    part = n * 2 // 3  # fewer, counted on the device
+    g[part:] = float("nan")
+    _check_bwd(_bwd(ids, n_rows, g, 1.5, mode, "f32", base, n=part), ids[:part], n_rows, g[:part], 1.5, mode, "f32", base)
+
+
 @pytest.mark.parametrize("mode", ["rows", "dense", "add"])
 def test_gradient_wide_ids_and_sort_passes(mode):
     # IDs across all four digits of the sort where the table can be that long
