@@ -69,34 +69,6 @@ __device__ __forceinline__ float warp_max(float x) {
     return x;
 }
 
-// ------------------------------------------------------ pairs of fp32 values
-// (one instruction for two values: the exponentials' arguments and sums are
-// what this file's kernels issue most of)
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pair(float a, float b) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpair(f2 p, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // --------------------------------------------------- 16-byte parts of a row
 template <typename T>
 constexpr int kE = 16 / (int)sizeof(T);  // elements of a vector

@@ -70,19 +70,33 @@ struct Source {
     int32_t vec;  // 1: g, 2: the momentum may be read 16 bytes at a time
 };
 
-// Two values as packed hi and lo.
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-    const __half2 h = __floats2half2_rn(a, b);
-    const float2 f = __half22float2(h);
-    const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
-    hi = *reinterpret_cast<const uint32_t*>(&h);
-    lo = *reinterpret_cast<const uint32_t*>(&l);
+// Two values as packed hi and lo.  (x - hi is exact, in one instruction that
+// takes hi as fp16; with the sums in pairs of fp32 values the passes over tensor
+// memory are a third shorter in instructions: 128 x 200 49.3 -> 47.6 us.)
+__device__ __forceinline__ void split2(f2 x, uint32_t& hi, uint32_t& lo) {
+    asm("{\n"
+        ".reg .b16 h0, h1, m;\n"
+        ".reg .f32 a, b, r0, r1;\n"
+        "mov.b64 {a, b}, %2;\n"
+        "cvt.rn.f16x2.f32 %0, b, a;\n"
+        "mov.b32 {h0, h1}, %0;\n"
+        "mov.b16 m, 0xBC00;\n"  // -1
+        "fma.rn.f32.f16 r0, h0, m, a;\n"
+        "fma.rn.f32.f16 r1, h1, m, b;\n"
+        "cvt.rn.f16x2.f32 %1, r1, r0;\n"
+        "}\n"
+        : "=&r"(hi), "=r"(lo)
+        : "l"(x));
+}
+__device__ __forceinline__ void split8(const f2 (&v)[4], uint4& hi, uint4& lo) {
+    split2(v[0], hi.x, lo.x);
+    split2(v[1], hi.y, lo.y);
+    split2(v[2], hi.z, lo.z);
+    split2(v[3], hi.w, lo.w);
 }
 __device__ __forceinline__ void split8(const float (&v)[8], uint4& hi, uint4& lo) {
-    split2(v[0], v[1], hi.x, lo.x);
-    split2(v[2], v[3], hi.y, lo.y);
-    split2(v[4], v[5], hi.z, lo.z);
-    split2(v[6], v[7], hi.w, lo.w);
+    const f2 p[4] = {pair(v[0], v[1]), pair(v[2], v[3]), pair(v[4], v[5]), pair(v[6], v[7])};
+    split8(p, hi, lo);
 }
 
 // ------------------------------------------------------------ norm and split
@@ -714,7 +728,8 @@ __global__ void __launch_bounds__(kThreads) k_ns_store(Planes X, int64_t ldx, in
 // No iterate goes to memory: the call reads its input and writes the result.
 // The time is a chain of latencies: two cluster barriers, three products and
 // four passes over tensor memory a step.  Cycles of a step, 128 x 200 on one SM
-// (49 us for five steps) / 128 x 2048 on 16 (59 us): partial Gram 3,800 / 2,800,
+// (48 us for five steps) / 128 x 2048 on 16 (58 us), before the passes' arithmetic
+// was paired: partial Gram 3,800 / 2,800,
 // taking it out 1,100 / 1,700 with the barrier, exchange - / 5,000 (8,500 with all
 // blocks of A; distributed shared memory gives 16 bytes a clock an SM), square
 // 2,800 / 2,700, B 1,700 / 2,300, B X 4,000 / 2,700, X 2,100 / 1,300.
@@ -770,8 +785,8 @@ __device__ __forceinline__ void reduce_blocks(uint32_t da, uint32_t rank, uint8_
 #pragma unroll
             for (int s = 1; s < S; ++s) v.x += x[i][s].x, v.y += x[i][s].y, v.z += x[i][s].z, v.w += x[i][s].w;
             uint32_t h0, l0, h1, l1;
-            split2(v.x * (1.f / kScale), v.y * (1.f / kScale), h0, l0);
-            split2(v.z * (1.f / kScale), v.w * (1.f / kScale), h1, l1);
+            split2(pair(v.x * (1.f / kScale), v.y * (1.f / kScale)), h0, l0);
+            split2(pair(v.z * (1.f / kScale), v.w * (1.f / kScale)), h1, l1);
             uint8_t* at = stage + g * kGroupBytes + c * 64 - (c & 1) * 56 + r * 16;
             *reinterpret_cast<uint2*>(at) = make_uint2(h0, h1);
             *reinterpret_cast<uint2*>(at + kHalf * 128) = make_uint2(l0, l1);
@@ -1020,22 +1035,30 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
             mma_issue(cross, a(k, 1), b(k, 0), idesc, 1u, false);
         }
     };
-    // 32 columns of their sum
-    const auto load_sum = [&](int ksteps, int mains, int cols, uint32_t at, float (&v)[32]) {
+    // 32 columns of their sum, in pairs
+    const auto load_sum = [&](int ksteps, int mains, int cols, uint32_t at, f2 (&v)[16]) {
         uint32_t x[32], y[32];
+        const auto two = [](const uint32_t (&r)[32], int k) { return pair(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])); };
         tmem_load_issue(tmem + (uint32_t)(mains * cols) + at, x);
         tmem_load_issue(tmem + at, y);
         tmem_load_wait(x);
         tmem_load_wait(y);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(x[k]) + __uint_as_float(y[k]);
+        for (int k = 0; k < 16; ++k) v[k] = add2(two(x, k), two(y, k));
         if (mains > 1 && ksteps > 1) {
             tmem_load_issue(tmem + (uint32_t)cols + at, x);
             tmem_load_wait(x);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] += __uint_as_float(x[k]);
+            for (int k = 0; k < 16; ++k) v[k] = add2(v[k], two(x, k));
         }
     };
+    const auto load_sum_32 = [&](int ksteps, int mains, int cols, uint32_t at, float (&v)[32]) {
+        f2 p[16];
+        load_sum(ksteps, mains, cols, at, p);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) unpair(p[k], v[2 * k], v[2 * k + 1]);
+    };
+    const f2 unscale = pair(1.f / kScale, 1.f / kScale);
     constexpr int kXMains = W == 256 ? 1 : 2, kXCols = W == 256 ? 256 : 128;  // of X <- B X
     const auto x_rows = [&](int k, int lo) {
         return smem_desc_sw128(xa + (lo ? kXLo : 0) + (uint32_t)((k >> 2) * kPairTile + (k & 3) * 32));
@@ -1081,13 +1104,13 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
         // partial A = X X^T
         product([&] { pairs(kx, 2, 128, desc_f16(false, kFusedM), x_rows, x_rows); });
         if constexpr (W == 256) {
-            float v[32];
+            f2 v[16];
             load_sum(kx, 2, 128, lanes + (uint32_t)part * 32, v);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                float x[8];
+                f2 x[4];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) x[k] = v[8 * t + k] * (1.f / kScale);
+                for (int k = 0; k < 4; ++k) x[k] = mul2(v[4 * t + k], unscale);
                 uint4 hi, lo;
                 split8(x, hi, lo);
                 *reinterpret_cast<uint4*>(as + chunk_at(row, part * 4 + t)) = hi;
@@ -1097,7 +1120,7 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
 #pragma unroll 1
             for (int c0 = part * 64; c0 < part * 64 + 64; c0 += 32) {
                 float v[32];
-                load_sum(kx, 2, 128, lanes + (uint32_t)c0, v);
+                load_sum_32(kx, 2, 128, lanes + (uint32_t)c0, v);
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
                     const int d = (c0 / 8 + t / 2 - row / 8) & 15;
@@ -1111,15 +1134,17 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
         // B = a I + b A + c A A, in A's place
         product([&] { pairs(km, 2, 128, desc_f16(false, kFusedM), a_rows, a_rows); });
         const float ca = steps.coef[step][0] * kScale, cb = steps.coef[step][1], cc = steps.coef[step][2] * (1.f / kScale);
+        const f2 cb2 = pair(cb, cb), cc2 = pair(cc, cc);
 #pragma unroll 1
         for (int c0 = part * (kFusedM * 4 / kWarps); c0 < (part + 1) * (kFusedM * 4 / kWarps); c0 += 32) {
-            float v[32];
+            f2 v[16];
             load_sum(km, 2, 128, lanes + (uint32_t)c0, v);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] *= cc;
+            for (int k = 0; k < 16; ++k) v[k] = mul2(v[k], cc2);
             if ((c0 >> 5) == (warp & 3)) {  // the diagonal: column c0 + lane of row `row`
 #pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] += k == lane ? ca : 0.f;
+                for (int k = 0; k < 16; ++k)
+                    v[k] = add2(v[k], pair(2 * k == lane ? ca : 0.f, 2 * k + 1 == lane ? ca : 0.f));
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -1128,12 +1153,11 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
                 const uint4 h4 = *ph, l4 = *pl;
                 const __half2* h2 = reinterpret_cast<const __half2*>(&h4);
                 const __half2* l2 = reinterpret_cast<const __half2*>(&l4);
-                float b[8];
+                f2 b[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float2 h = __half22float2(h2[k]), l = __half22float2(l2[k]);
-                    b[2 * k] = fmaf(cb, h.x, fmaf(cb, l.x, v[8 * t + 2 * k]));
-                    b[2 * k + 1] = fmaf(cb, h.y, fmaf(cb, l.y, v[8 * t + 2 * k + 1]));
+                    b[k] = fma2(cb2, pair(h.x, h.y), fma2(cb2, pair(l.x, l.y), v[4 * t + k]));
                 }
                 uint4 hi, lo;
                 split8(b, hi, lo);
@@ -1146,13 +1170,13 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
         if (step + 1 < steps.count) {
 #pragma unroll 1
             for (int c0 = part * (W * 4 / kWarps); c0 < (part + 1) * (W * 4 / kWarps); c0 += 32) {
-                float v[32];
+                f2 v[16];
                 load_sum(km, kXMains, kXCols, lanes + (uint32_t)c0, v);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    float x[8];
+                    f2 x[4];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) x[k] = v[8 * t + k] * (1.f / kScale);
+                    for (int k = 0; k < 4; ++k) x[k] = mul2(v[4 * t + k], unscale);
                     uint4 hi, lo;
                     split8(x, hi, lo);
                     *reinterpret_cast<uint4*>(xs + chunk_at(row, c0 / 8 + t)) = hi;
@@ -1185,7 +1209,7 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
 #pragma unroll 1
         for (int c0 = part * kCols; c0 < (part + 1) * kCols; c0 += 32) {
             float v[32];
-            load_sum(km, kXMains, kXCols, lanes + (uint32_t)c0, v);
+            load_sum_32(km, kXMains, kXCols, lanes + (uint32_t)c0, v);
 #pragma unroll
             for (int t = 0; t < 8; ++t)
                 *reinterpret_cast<float4*>(tile + row * (W + 4) + c0 + 4 * t) =
@@ -1210,7 +1234,7 @@ __global__ void __launch_bounds__(kFusedThreads<W>, 1)
 #pragma unroll 1
         for (int c0 = part * kCols; c0 < (part + 1) * kCols; c0 += 32) {
             float v[32];
-            load_sum(km, kXMains, kXCols, lanes + (uint32_t)c0, v);
+            load_sum_32(km, kXMains, kXCols, lanes + (uint32_t)c0, v);
 #pragma unroll
             for (int t = 0; t < 32; ++t) tile[row * ld_row + (c0 + t) * ld_col] = v[t];
         }
