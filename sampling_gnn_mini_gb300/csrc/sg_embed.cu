@@ -223,6 +223,17 @@ __device__ __forceinline__ unsigned digit_peers(int32_t d, unsigned valid) {
     return peers;
 }
 
+// Clears the sort's state.  (A kernel, so that the next one's launch overlaps it;
+// with cudaMemsetAsync in its place the gradient of 65,536 positions of 1024 bf16
+// columns takes 69.5 us, not 66.7.)
+__global__ void __launch_bounds__(kThreads) k_sort_clear(uint4* __restrict__ p, int64_t words) {
+    pdl_start();
+    const int64_t i0 = blockIdx.x * (int64_t)(kThreads * 4) + threadIdx.x;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        if (i0 + u * kThreads < words) p[i0 + u * kThreads] = make_uint4(0, 0, 0, 0);
+}
+
 // Digit counts of all passes, in kCopies copies (800,003 positions: 6 us; with one
 // copy, whose counters 304 blocks add to in turn, 19).
 __global__ void __launch_bounds__(kThreads) k_sort_hist(const int32_t* __restrict__ ids, int64_t n_rows, int64_t n_cap,
@@ -1134,7 +1145,9 @@ sg_status run_sort(const int32_t* ids, int64_t n_cap, const int32_t* d_n, int64_
     const int64_t wave = (int64_t)num_sms() * kSortThreads;
     const int items = n_cap <= 4 * wave ? 4 : n_cap <= 8 * wave ? 8 : 12;
     const int64_t tiles = cdiv(n_cap, kSortThreads * items);
-    SG_CUDA(cudaMemsetAsync(ws + L.state, 0, L.status - L.state + (size_t)(dg.passes * tiles) * kDigits * 4, s));
+    const int64_t words = (int64_t)(L.status - L.state) / 16 + dg.passes * tiles * (kDigits / 4);  // of 16 bytes
+    SG_CUDA(launch_pdl(k_sort_clear, dim3((unsigned)cdiv(words, kThreads * 4)), dim3(kThreads), 0, s,
+                       (uint4*)(ws + L.state), words));
     const int64_t hb = cdiv(n_cap, kThreads * 8) < num_sms() * 2 ? cdiv(n_cap, kThreads * 8) : num_sms() * 2;
     SG_CUDA(launch_pdl(k_sort_hist, dim3((unsigned)hb), dim3(kThreads), 0, s, ids, n_rows, n_cap, d_n, dg, st));
     for (int p = 0; p < dg.passes; ++p) {
