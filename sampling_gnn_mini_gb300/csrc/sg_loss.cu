@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_xent_stream(RowArgs<T> a, int
     extern __shared__ __align__(128) uint8_t dsm[];
     pdl_start();
     constexpr int kParts = S * NT / 32;
-    __shared__ __align__(8) float2 parts[2][kParts];  // (m, z) of every warp of the cluster, by row parity
+    __shared__ __align__(8) float2 parts[2][kParts];  // (m, z) of every warp of the cluster, of used rows in turn
     __shared__ __align__(8) uint64_t full[2], met[2];  // buffers; parts
     __shared__ bool last;
     const int32_t rank = (int32_t)(blockIdx.x % S), first = (int32_t)(blockIdx.x / S), step = (int32_t)(gridDim.x / S);
@@ -717,8 +717,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_xent_stream(RowArgs<T> a, int
         fetch(first + step, y1, 1);
     }
     const float w = a.mean ? a.gs / (float)max(1, *a.valid) : a.gs;
-    uint32_t phases = 0;  // bit b: parity of the next phase of full[b] and met[b]
-    int32_t par = 0;
+    uint32_t phases = 0;  // bits 0, 1: parity of the next phase of full[0], full[1]; bits 2, 3: of met[0], met[1]
+    int32_t par = 0;      // the row's buffer: alternates over all rows
+    int32_t slot = 0;     // its parts and met: alternate over the used rows only
     for (int32_t r = first; r < n; r += step, par ^= 1, y = y1, y1 = y2) {
         y2 = label(r + 2 * step);
         const T* row = a.x + (int64_t)r * a.ld;
@@ -750,23 +751,26 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_xent_stream(RowArgs<T> a, int
         // The parts meet by asynchronous stores that complete on the receiver's
         // barrier.  (A cluster barrier here would first wait for this row's
         // predecessor's gradient to be stored: with one, 144 us and the memory
-        // fence the largest stall.)  A slot is written again two rows later, when
-        // its readers have sent the row between.
-        if (threadIdx.x == 0) mbar_expect_tx(&met[par], kParts * 8);
+        // fence the largest stall.)  A slot is written again two used rows later,
+        // by a warp that has met the used row between: to that one every reader
+        // of the slot has sent its part, after it had read.  (Ignored rows exchange
+        // nothing, so the slots may not go by the rows' own parity.)
+        if (threadIdx.x == 0) mbar_expect_tx(&met[slot], kParts * 8);
         if (lane_id() < S) {
-            const uint32_t slot = smem_addr(&parts[par][rank * (NT / 32) + (threadIdx.x >> 5)]);
+            const uint32_t to = smem_addr(&parts[slot][rank * (NT / 32) + (threadIdx.x >> 5)]);
             asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];\n" ::"r"(
-                             map_rank(slot, lane_id())),
-                         "f"(h.m), "f"(h.z), "r"(map_rank(smem_addr(&met[par]), lane_id()))
+                             map_rank(to, lane_id())),
+                         "f"(h.m), "f"(h.z), "r"(map_rank(smem_addr(&met[slot]), lane_id()))
                          : "memory");
         }
         __syncwarp();
-        if (!mbar_wait(&met[par], (phases >> par) & 1u) && lane_id() == 0) dev_err(ERR_TIMEOUT);
-        phases ^= 1u << par;
+        if (!mbar_wait(&met[slot], (phases >> (2 + slot)) & 1u) && lane_id() == 0) dev_err(ERR_TIMEOUT);
+        phases ^= (1u << par) | (4u << slot);
         // every thread has its vectors in registers: the buffer is free
         if (threadIdx.x == 0) fetch(r + 2 * step, y2, par);
         float M, Z;
-        join_parts<kParts>(parts[par], M, Z);
+        join_parts<kParts>(parts[slot], M, Z);
+        slot ^= 1;
         if (out) {
             const float inv = h.z == 0.f || Z == 0.f ? 0.f : w / Z * exp_from(h.m, M);
             store_held(h, out + part.head + v0 * kE<T>, count, same_phase(row, (const T*)out), inv);
