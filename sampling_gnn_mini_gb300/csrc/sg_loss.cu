@@ -22,7 +22,7 @@
 // -inf logits: m and x - m are kept apart from -inf - -inf by taking m = 0 when
 // a part has no finite logit (its exponentials are then 0); x - m is formed
 // before the scaling by log2(e), so rows at a type's lowest value do not
-// overflow.
+// overflow and a row's common level costs no accuracy.
 #include <cuda_bf16.h>
 
 #include "sg_internal.cuh"
@@ -152,34 +152,25 @@ __device__ __forceinline__ float part_max(const uint4& u) {
     return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
 }
 
-// exp(x - m) is formed as 2^(x log2(e) - m log2(e)), one fused operation a
-// value; m log2(e) has to stay finite.
+// exp(x - m) of values and pairs, the difference taken first, as in exp_from():
+// it is exact near m, so the largest logit's exponential is 1 whatever its level.
+// (One fused operation, x log2(e) - m log2(e), leaves the rounding of the second
+// product in every exponential: at |m| = 1e6 they are off by 1.5 %, at 1e10 by
+// more than the type's range.)
 struct Base {
     f2 l, b;
-    float mb;
-    __device__ __forceinline__ explicit Base(float m) : mb(-m * kLog2e) {
+    float m;
+    __device__ __forceinline__ explicit Base(float m_) : m(m_) {
         l = pair(kLog2e, kLog2e);
-        b = pair(mb, mb);
+        b = pair(-m_, -m_);
     }
-    __device__ __forceinline__ float of(float x) const { return ex2(fmaf(x, kLog2e, mb)); }
+    __device__ __forceinline__ float of(float x) const { return exp_from(x, m); }
     __device__ __forceinline__ f2 of(f2 x) const {
         float a, c;
-        unpair(fma2(x, l, b), a, c);
+        unpair(mul2(add2(x, b), l), a, c);
         return pair(ex2(a), ex2(c));
     }
 };
-constexpr float kHuge = 1e37f;  // |m| from which m log2(e) may overflow
-
-// x - m, for |m| >= kHuge: such differences are 0, or so large that their
-// exponentials are 0 however they are rounded.
-template <typename T>
-__device__ __forceinline__ void part_shift(uint4& u, float m) {
-    f2 p[kE<T> / 2];
-    pairs_of(u, p);
-#pragma unroll
-    for (int i = 0; i < kE<T> / 2; ++i) p[i] = add2(p[i], pair(-m, -m));
-    u = part_of(p);
-}
 
 // Adds exp(x - m) to sum; fp32 vectors keep the exponentials in place of x.
 template <typename T>
@@ -288,13 +279,6 @@ __device__ __forceinline__ void warp_rows(const RowArgs<T>& a, int32_t r0, int32
         for (int k = 0; k < NV; ++k) m = fmaxf(m, part_max<T>(x[r][k]));
         m = warp_max(m);
         if (m == -INFINITY) m = 0.f;
-        const float m_row = m;
-        if (!(fabsf(m) < kHuge)) {
-#pragma unroll
-            for (int k = 0; k < NV; ++k) part_shift<T>(x[r][k], m);
-            xe[r] -= m;
-            m = 0.f;
-        }
         const Base base(m);
         f2 sum = pair(0.f, 0.f);
 #pragma unroll
@@ -302,7 +286,7 @@ __device__ __forceinline__ void warp_rows(const RowArgs<T>& a, int32_t r0, int32
         float z, z1;
         unpair(sum, z, z1);
         z = warp_sum(z + z1 + base.of(xe[r]));
-        loss[r] = loss_of(m_row, z, xy[r]);
+        loss[r] = loss_of(m, z, xy[r]);
         if (lane == 0) a.loss[r0 + r] = loss[r];
         if (!out) continue;
         const T* row = a.x + (int64_t)(r0 + r) * a.ld;
@@ -318,7 +302,7 @@ __device__ __forceinline__ void warp_rows(const RowArgs<T>& a, int32_t r0, int32
         const int32_t e = part.edge(lane), at = part.place(y[r]);
         if (e >= 0) put(out + e, inv * base.of(xe[r]));
         // the lane that stored the label's element above may now replace it
-        if ((at < 0 ? -1 - at : at % 32) == lane) put(out + y[r], z == 0.f ? 0.f : fmaf(inv, exp_from(xy[r], m_row), -w));
+        if ((at < 0 ? -1 - at : at % 32) == lane) put(out + y[r], z == 0.f ? 0.f : fmaf(inv, exp_from(xy[r], m), -w));
     }
 }
 
@@ -481,7 +465,6 @@ struct Held {
     uint4 x[kVecs];
     float xe;
     float m, z;  // of this warp: z = sum of exp(x - m)
-    float base;  // what the kept x are relative to: m, or 0 after a shift
 };
 
 // (m, z) of the warp from its vectors and, when given, the part (mr, zr) of
@@ -494,14 +477,8 @@ __device__ __forceinline__ void reduce_held(Held<T, NT>& h, int32_t count, float
         if ((int32_t)threadIdx.x + k * NT < count) m = fmaxf(m, part_max<T>(h.x[k]));
     m = warp_max(m);
     if (m == -INFINITY) m = 0.f;
-    h.m = h.base = m;
-    if (!(fabsf(m) < kHuge)) {
-#pragma unroll
-        for (int k = 0; k < kVecs; ++k) part_shift<T>(h.x[k], m);
-        h.xe -= m;
-        h.base = 0.f;
-    }
-    const Base base(h.base);
+    h.m = m;
+    const Base base(m);
     f2 sum = pair(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < kVecs; ++k)
@@ -552,7 +529,7 @@ __device__ __forceinline__ void join_parts(const float2* parts, float& M, float&
 // Gradient of what the thread holds; first: the slice's first vector.
 template <typename T, int NT>
 __device__ __forceinline__ void store_held(Held<T, NT>& h, T* first, int32_t count, bool same, float inv) {
-    const Base base(h.base);
+    const Base base(h.m);
     const f2 inv2 = pair(inv, inv);
     T* p = first + (int32_t)threadIdx.x * kE<T>;
     if (same) {
@@ -639,7 +616,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_xent_row(RowArgs<T> a) {
             const bool same = same_phase(row, (const T*)out);
             const float inv = h.z == 0.f || Z == 0.f ? 0.f : w / Z * exp_from(h.m, M);
             store_held(h, out + part.head + v0 * kE<T>, count, same, inv);
-            if (edge >= 0) put(out + edge, inv * Base(h.base).of(h.xe));
+            if (edge >= 0) put(out + edge, inv * Base(h.m).of(h.xe));
             for (int32_t i = (int32_t)threadIdx.x + kVecs * NT; i < count; i += NT) {
                 const int32_t c = part.head + (v0 + i) * kE<T>;
                 float g[kE<T>];
@@ -774,7 +751,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_xent_stream(RowArgs<T> a, int
         if (out) {
             const float inv = h.z == 0.f || Z == 0.f ? 0.f : w / Z * exp_from(h.m, M);
             store_held(h, out + part.head + v0 * kE<T>, count, same_phase(row, (const T*)out), inv);
-            if (edge >= 0) put(out + edge, inv * Base(h.base).of(h.xe));
+            if (edge >= 0) put(out + edge, inv * Base(h.m).of(h.xe));
             // this thread stored the label's element above: it may now replace it
             if (owner) put(out + y, Z == 0.f ? 0.f : fmaf(w / Z, exp_from(xy, M), -w));
         }
