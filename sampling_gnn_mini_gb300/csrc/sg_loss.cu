@@ -526,6 +526,14 @@ __device__ __forceinline__ void join_parts(const float2* parts, float& M, float&
     Z = warp_sum(Z);
 }
 
+// What a warp's exponentials, relative to its own m, are multiplied by in the
+// gradient.  A warp without a finite logit (z = 0; its m says nothing) has
+// exponentials of 0: any finite factor will do, but a row with NaN has NaN there too.
+__device__ __forceinline__ float held_scale(float m, float z, float w, float M, float Z) {
+    if (Z == 0.f) return 0.f;
+    return z == 0.f ? w / Z : w / Z * exp_from(m, M);
+}
+
 // Gradient of what the thread holds; first: the slice's first vector.
 template <typename T, int NT>
 __device__ __forceinline__ void store_held(Held<T, NT>& h, T* first, int32_t count, bool same, float inv) {
@@ -614,7 +622,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_xent_row(RowArgs<T> a) {
         const float w = a.mean ? a.gs / (float)max(1, *a.valid) : a.gs;
         if (out) {
             const bool same = same_phase(row, (const T*)out);
-            const float inv = h.z == 0.f || Z == 0.f ? 0.f : w / Z * exp_from(h.m, M);
+            const float inv = held_scale(h.m, h.z, w, M, Z);
             store_held(h, out + part.head + v0 * kE<T>, count, same, inv);
             if (edge >= 0) put(out + edge, inv * Base(h.m).of(h.xe));
             for (int32_t i = (int32_t)threadIdx.x + kVecs * NT; i < count; i += NT) {
@@ -749,7 +757,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_xent_stream(RowArgs<T> a, int
         join_parts<kParts>(parts[slot], M, Z);
         slot ^= 1;
         if (out) {
-            const float inv = h.z == 0.f || Z == 0.f ? 0.f : w / Z * exp_from(h.m, M);
+            const float inv = held_scale(h.m, h.z, w, M, Z);
             store_held(h, out + part.head + v0 * kE<T>, count, same_phase(row, (const T*)out), inv);
             if (edge >= 0) put(out + edge, inv * Base(h.m).of(h.xe));
             // this thread stored the label's element above: it may now replace it

@@ -167,3 +167,24 @@ def test_sure_rows(n, c, dt):
         labels = ((at + shift) % c).int().cpu().numpy()
         loss, _, grad = _run(x, labels)
         _hold(x, labels, loss, grad)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n,c", FORMS)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_nan_reaches_the_masked_classes_of_its_row(n, c, dt, bad):
+    # all classes but a few masked with -inf: whole warps have nothing to add,
+    # and their part of a row's gradient is NaN all the same; other rows keep theirs
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(n + 5 * c)
+    x = torch.randn((n, c), generator=gen, device="cuda")
+    x[:, 8:] = float("-inf")
+    x = x.to(DT[dt])
+    labels = np.random.default_rng(c).integers(0, min(c, 8), n).astype(np.int32)
+    hit = torch.arange(n, device="cuda") % 3 == 1
+    clean = _run(x, labels)
+    _hold(x, labels, clean[0], clean[2])
+    x[hit, 5] = bad
+    loss, total, grad = _run(x, labels)
+    assert bool(torch.isnan(loss[hit]).all()) and bool(torch.isnan(grad[hit]).all()) and bool(torch.isnan(total[0]))
+    assert torch.equal(loss[~hit], clean[0][~hit]) and torch.equal(grad[~hit], clean[2][~hit])
