@@ -188,3 +188,27 @@ def test_nan_reaches_the_masked_classes_of_its_row(n, c, dt, bad):
     loss, total, grad = _run(x, labels)
     assert bool(torch.isnan(loss[hit]).all()) and bool(torch.isnan(grad[hit]).all()) and bool(torch.isnan(total[0]))
     assert torch.equal(loss[~hit], clean[0][~hit]) and torch.equal(grad[~hit], clean[2][~hit])
+
+
+@pytest.mark.parametrize("n,c", FORMS)
+def test_small_losses(n, c):
+    # two classes left of each row, d apart, the label the upper one: the sum is
+    # 1 + e, e = exp(-d), with one rounding (u) and e's own (8 + 2 d relative,
+    # 8 more where it comes from another warp); the logarithm is within an ulp
+    # of its value; the loss is never below 0
+    rng = np.random.default_rng(n + c)
+    for turn in range(max(1, 200 // n)):
+        d = np.exp(rng.uniform(np.log(1.0), np.log(16.0), n)).astype(np.float32)
+        top = rng.integers(0, c, n)
+        other = (top + 1 + rng.integers(0, c - 1, n)) % c
+        level = rng.integers(-4, 5, n).astype(np.float32) * 4  # so that level - d is rounded at most by 2^-20
+        x = torch.full((n, c), float("-inf"), device="cuda")
+        row = torch.arange(n, device="cuda")
+        x[row, torch.from_numpy(top).cuda()] = torch.from_numpy(level).cuda()
+        x[row, torch.from_numpy(other).cuda()] = torch.from_numpy(level - d).cuda()
+        gap = level.astype(np.float64) - (level - d).astype(np.float64)
+        loss, _, _ = _run(x, top.astype(np.int32))
+        e = np.exp(-gap)
+        want, got = np.log1p(e), loss.double().cpu().numpy()
+        assert np.all(got >= 0)
+        assert np.all(np.abs(got - want) <= U * (1 + e * (16 + 2 * gap) + 2 * want))
