@@ -602,7 +602,8 @@ sg_status sg_embed_fwd(const void* d_table, int32_t dtype_table, int64_t n_rows,
  *   d_grad    row stride ld_grad (>= dim); columns past dim are not touched
  *   dtypes    SG_F32 or SG_BF16, in any combination
  *   d_workspace  device scratch of sg_embed_bwd_workspace(...) bytes, 256-byte
- *             aligned, in no particular state
+ *             aligned, in no particular state; one sized for an n_cap serves
+ *             every smaller n_cap as well
  * IDs of -1 contribute nothing; another ID out of range sets the device error
  * word and contributes nothing. */
 size_t sg_embed_bwd_workspace(int64_t n_cap, int64_t n_rows, int32_t dim, int32_t mode);

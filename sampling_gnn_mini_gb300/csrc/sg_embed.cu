@@ -1003,6 +1003,7 @@ sg_status run_fwd(int vec, const void* table, int64_t n_rows, int32_t dim, int64
 // blocks) 49 / 40, 65,536 (1,024 blocks) 85 / 75.
 struct Cut {
     int32_t units, lanes, col_blocks, span;  // span: positions of a tile
+    int64_t most;                            // tiles of a list of up to n_cap positions
 };
 Cut cut_for(int64_t n_cap, int32_t dim, int vec) {
     Cut c;
@@ -1013,11 +1014,16 @@ Cut cut_for(int64_t n_cap, int32_t dim, int vec) {
     const int32_t chunks = kThreads / c.lanes;
     const bool wide = c.lanes >= 8 && cdiv(n_cap, chunks * 32) * c.col_blocks >= kFewBlocks;
     c.span = chunks * (wide ? 32 : 8);
+    c.most = cdiv(n_cap, c.span);
+    if (wide) {  // the longest list of short chunks, which may have more tiles
+        const int64_t few = (int64_t)((kFewBlocks - 1) / c.col_blocks) * 4;
+        if (few > c.most) c.most = few;
+    }
     return c;
 }
 
 struct BwdLayout {
-    int64_t tiles;       // bound on the sum's tiles
+    int64_t tiles;       // bound on the sum's tiles, of this list and of every shorter one
     int64_t sort_tiles;  // bound on a pass's tiles
     size_t kv0, kv1, state, status, run_status, starts, head, tail, total;  // state .. status: cleared for a sort
 };
@@ -1027,7 +1033,7 @@ BwdLayout bwd_layout(int64_t n_cap, int32_t dim) {
     L.tiles = 0;
     for (int vec = 1; vec <= 8; vec *= 2)  // the strides and addresses decide between units of 1, 4 and 8
         if (vec != 2 && dim % vec == 0) {
-            const int64_t t = cdiv(n_cap, cut_for(n_cap, dim, vec).span);
+            const int64_t t = cut_for(n_cap, dim, vec).most;
             if (t > L.tiles) L.tiles = t;
         }
     L.sort_tiles = n_cap <= kClusterSort ? 0 : cdiv(n_cap, kSortThreads * 4);
