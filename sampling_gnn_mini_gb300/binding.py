@@ -699,6 +699,14 @@ def _vector(name: str, t: Optional[torch.Tensor], n: int, dtype, dev: int) -> in
     return t.data_ptr()
 
 
+def _scratch(name: str, t: torch.Tensor, dev: int):
+    """Checks a contiguous workspace on device dev; returns its address and
+    bytes (their number and alignment are the library's to check)."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or not t.is_contiguous():
+        _invalid("%s: workspace must be a contiguous tensor on the device of the other arguments" % name)
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _raw_stream(stream, dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
@@ -740,9 +748,9 @@ def sg_embed_bwd(ids: torch.Tensor, n_cap: int, d_n: Optional[torch.Tensor], n_r
     if mode == SG_GRAD_ROWS:
         p_rows = _vector("sg_embed_bwd: rows", rows, n_cap, torch.int32, dev)
         p_out = _vector("sg_embed_bwd: n_out", n_out, 1, torch.int32, dev)
+    p_ws, n_ws = _scratch("sg_embed_bwd", workspace, dev)
     st = (_lib or load()).sg_embed_bwd(p_ids, n_cap, p_n, n_rows, g.data_ptr(), dt_g, dim, ld_g, scale, mode, p_rows,
-                                       p_out, grad.data_ptr(), dt_o, ld_o, workspace.data_ptr(), workspace.numel(),
-                                       _raw_stream(stream, dev))
+                                       p_out, grad.data_ptr(), dt_o, ld_o, p_ws, n_ws, _raw_stream(stream, dev))
     if st:
         _check(st)
 
@@ -769,9 +777,9 @@ def sg_xent(logits: torch.Tensor, labels: torch.Tensor, n_cap: int, d_n: Optiona
     p_loss = _vector("sg_xent: loss", loss, n_cap, torch.float32, dev)
     p_total = None if total is None else _vector("sg_xent: total", total, 2, torch.float32, dev)
     p_n = None if d_n is None else _vector("sg_xent: d_n", d_n, 1, torch.int32, dev)
+    p_ws, n_ws = _scratch("sg_xent", workspace, dev)
     st = (_lib or load()).sg_xent(logits.data_ptr(), dt, n_cap, p_n, c, ld, p_y, 1 if mean else 0, grad_scale, p_loss,
-                                  p_total, p_grad, ld_g, workspace.data_ptr(), workspace.numel(),
-                                  _raw_stream(stream, dev))
+                                  p_total, p_grad, ld_g, p_ws, n_ws, _raw_stream(stream, dev))
     if st:
         _check(st)
 
@@ -818,8 +826,9 @@ def sg_orthogonalise(g: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor
     if (dt, k, r, c) != (dt_o, k_o, r_o, c_o) or out.get_device() != dev:
         _invalid("sg_orthogonalise: out must have g's shape, dtype and device")
     cf = _coef(steps, coef)
+    p_ws, n_ws = _scratch("sg_orthogonalise", workspace, dev)
     st = (_lib or load()).sg_orthogonalise(g.data_ptr(), dt, k, r, c, ld, steps, _ptr(cf), eps, scale, out.data_ptr(),
-                                           ld_o, workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+                                           ld_o, p_ws, n_ws, _raw_stream(stream, dev))
     if st:
         _check(st)
 
@@ -839,9 +848,9 @@ def sg_muon_step(w: torch.Tensor, g: torch.Tensor, m: torch.Tensor, w_out: torch
             _invalid("sg_muon_step: w, w_out (of one dtype) and g, m, m_out (float32) must be contiguous tensors of "
                      "one shape on one device")
     cf = _coef(steps, coef)
+    p_ws, n_ws = _scratch("sg_muon_step", workspace, dev)
     st = (_lib or load()).sg_muon_step(w.data_ptr(), dt, g.data_ptr(), m.data_ptr(), k, r, c, lr, momentum,
                                        1 if nesterov else 0, weight_decay, scale, steps, _ptr(cf), eps,
-                                       w_out.data_ptr(), m_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                       _raw_stream(stream, dev))
+                                       w_out.data_ptr(), m_out.data_ptr(), p_ws, n_ws, _raw_stream(stream, dev))
     if st:
         _check(st)

@@ -119,3 +119,47 @@ def test_embed_bwd_workspace_grows_with_the_list(lib, dim):
     sizes = list(range(1, 12000, 7)) + [s for k in range(1, 400) for s in (512 * k, 512 * k + 1)] + [1 << k for k in range(30)]
     need = [lib.sg_embed_bwd_workspace(n, 1000, dim, sg.SG_GRAD_ADD) for n in sorted(set(sizes))]
     assert need[0] > 0 and all(a <= b for a, b in zip(need, need[1:]))
+
+
+class _OnDevice(torch.Tensor):
+    """A host tensor that says it is on device 0, so that the binding's checks
+    can be met one by one without a device."""
+    def get_device(self):
+        return 0
+
+
+def _on_device(*shape, dtype=torch.float32):
+    return torch.zeros(shape, dtype=dtype).as_subclass(_OnDevice)
+
+
+def test_binding_checks_the_workspace(monkeypatch):
+    class Refuses:  # the library is not reached
+        def __getattr__(self, name):
+            raise AssertionError("%s was called" % name)
+    monkeypatch.setattr(sg, "_lib", Refuses())
+    x, y, one = _on_device(4, 8), _on_device(4, dtype=torch.int32), _on_device(4)
+    table = _on_device(10, 8)
+    base = torch.zeros(1 << 16, dtype=torch.uint8)
+    for ws in (base,                                             # on the host
+               base.as_subclass(_OnDevice)[::2],                 # with gaps
+               None, base.numpy()):
+        for call in (lambda: sg.sg_embed_bwd(y, 4, None, 10, x, 1.0, table, sg.SG_GRAD_DENSE, ws, stream=0),
+                     lambda: sg.sg_xent(x, y, 4, None, one, None, None, ws, stream=0),
+                     lambda: sg.sg_orthogonalise(x, x, ws, stream=0),
+                     lambda: sg.sg_muon_step(x, x, x, x, x, ws, lr=0.1, stream=0)):
+            with pytest.raises(sg.SgError) as e:
+                call()
+            assert e.value.status == INVALID and "workspace" in str(e.value)
+
+
+def test_binding_passes_the_workspace_in_bytes(monkeypatch):
+    seen = []
+
+    class Records:
+        def __getattr__(self, name):
+            return lambda *args: seen.append(args) or 0
+    monkeypatch.setattr(sg, "_lib", Records())
+    for dtype, n in ((torch.uint8, 4096), (torch.float32, 1024), (torch.int64, 512)):
+        ws = _on_device(n, dtype=dtype)
+        sg.sg_orthogonalise(_on_device(4, 8), _on_device(4, 8), ws, stream=0)
+        assert seen[-1][-3:-1] == (ws.data_ptr(), 4096)
