@@ -19,7 +19,7 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libsg.so")
 SOURCES = ["sg_api.cu", "sg_sampler.cu", "sg_gather.cu", "sg_aggregate.cu", "sg_update.cu", "sg_recode.cu", "sg_dyncache.cu", "sg_match.cu",
            "sg_embed.cu", "sg_loss.cu", "sg_muon.cu"]
-HEADERS = ["sg_internal.cuh", "sg_objects.cuh", "sg_tc.cuh"]
+HEADERS = ["sg_internal.cuh", "sg_objects.cuh", "sg_once.h", "sg_tc.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

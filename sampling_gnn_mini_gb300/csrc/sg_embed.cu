@@ -1084,12 +1084,11 @@ sg_status run_sum(int vec, const void* g, const SumArgs<TO>& a, int32_t span, cu
 template <int ITEMS, int CTAS>
 cudaError_t sort_by_cluster(const int32_t* ids, int64_t n_rows, int64_t n_cap, const int32_t* d_n, Digits dg, int32_t span,
                            uint2* const (&kv)[2], int32_t* starts, int32_t* n_out, cudaStream_t s) {
-    static bool set = false;
-    if (!set) {
-        const cudaError_t e = cudaFuncSetAttribute(k_sort_cluster<ITEMS, CTAS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-        set = true;
-    }
+    static OncePerDevice set;
+    const cudaError_t e = once_on_device(set, [] {
+        return cudaFuncSetAttribute(k_sort_cluster<ITEMS, CTAS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    });
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(CTAS);
     cfg.blockDim = dim3(kSmallThreads);
@@ -1126,12 +1125,9 @@ sg_status run_sort(const int32_t* ids, int64_t n_cap, const int32_t* d_n, int64_
             return launch_pdl(kernel, dim3(1), dim3(kSmallThreads), kSmallSmem, s, ids, n_rows, (int32_t)n_cap, d_n, dg,
                               span, kv[0], starts, rows ? n_out : nullptr);
         };
-        static bool set = false;
-        if (!set) {
-            SG_CUDA(cudaFuncSetAttribute(k_sort_small<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem));
-            SG_CUDA(cudaFuncSetAttribute(k_sort_small<3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem));
-            set = true;
-        }
+        static OncePerDevice set1, set3;
+        SG_CUDA(allow_smem(set1, k_sort_small<1>, kSmallSmem));
+        SG_CUDA(allow_smem(set3, k_sort_small<3>, kSmallSmem));
         SG_CUDA(items <= 1 ? go(k_sort_small<1>) : go(k_sort_small<3>));
         return SG_OK;
     }

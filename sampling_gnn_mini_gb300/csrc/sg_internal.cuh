@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "../../include/sg.h"
+#include "sg_once.h"
 
 namespace sgi {
 
@@ -21,6 +22,19 @@ bool is_device_ptr(const void* p);
     } while (0)
 
 #define SG_CHECK_LAUNCH(what) SG_CUDA(cudaGetLastError())
+
+// Runs set() once for the current device (OncePerDevice).
+template <typename F>
+cudaError_t once_on_device(OncePerDevice& flags, F set) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    return e != cudaSuccess ? e : flags(dev, set);
+}
+// A kernel's limit of dynamic shared memory, raised once for each device.
+template <typename K>
+cudaError_t allow_smem(OncePerDevice& flags, K kernel, int bytes) {
+    return once_on_device(flags, [=] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+}
 
 // --------------------------------------------------------- device errors
 // Each translation unit owns one sticky error word; sg_stream_check ORs them.

@@ -856,12 +856,8 @@ template <typename T, int NT, int S>
 sg_status run_stream(const RowArgs<T>& a, int64_t nv, cudaStream_t s) {
     const int32_t slots = (int32_t)cdiv(nv, S);  // of a buffer
     const int smem = 2 * slots * 16;
-    static bool set = false;
-    if (!set) {
-        SG_CUDA(cudaFuncSetAttribute(k_xent_stream<T, NT, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     2 * kStreamVecs * 16));
-        set = true;
-    }
+    static OncePerDevice set;
+    SG_CUDA(allow_smem(set, k_xent_stream<T, NT, S>, 2 * kStreamVecs * 16));
     int64_t clusters = (int64_t)num_sms() * (1024 / NT) / S;
     if (clusters > a.n_cap) clusters = a.n_cap;
     SG_CUDA(launch_cluster(k_xent_stream<T, NT, S>, (unsigned)(clusters * S), NT, S, s, smem, a, slots));

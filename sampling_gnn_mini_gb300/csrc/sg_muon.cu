@@ -1321,20 +1321,11 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, size_t smem, cud
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-// Raises a kernel's dynamic shared memory limit once.
-#define NS_SMEM(kernel, bytes)                                                                                  \
-    do {                                                                                                        \
-        static bool set_ = false;                                                                               \
-        if (!set_) {                                                                                            \
-            SG_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(bytes)));    \
-            set_ = true;                                                                                        \
-        }                                                                                                       \
-    } while (0)
-
 template <int S, int KIND>
 sg_status launch_sym(const PairMaps& maps, int64_t tiles, int32_t count, int32_t m, int32_t K, const float* coef,
                      Planes in, Planes out, int64_t ld, cudaStream_t s) {
-    NS_SMEM((k_ns_sym<S, KIND>), kSymSmem);
+    static OncePerDevice set;
+    SG_CUDA(allow_smem(set, k_ns_sym<S, KIND>, kSymSmem));
     SG_CUDA(launch_cluster<S>(k_ns_sym<S, KIND>, dim3((unsigned)(tiles * S), (unsigned)count), kSymSmem, s, maps, m, K,
                               coef[0], coef[1], coef[2], in, out, ld));
     return SG_OK;
@@ -1362,7 +1353,8 @@ template <int BN, typename TW, bool FINAL>
 sg_status launch_apply(const ApplyMaps& maps, int32_t count, int32_t m, int32_t n, Planes out, int64_t ldx,
                        const FinalArgs& fin, cudaStream_t s) {
     constexpr int smem = kApplySmem<BN>;
-    NS_SMEM((k_ns_apply<BN, TW, FINAL>), smem);
+    static OncePerDevice set;
+    SG_CUDA(allow_smem(set, k_ns_apply<BN, TW, FINAL>, smem));
     SG_CUDA(launch_pdl(k_ns_apply<BN, TW, FINAL>, dim3((unsigned)cdiv(n, BN), (unsigned)cdiv(m, kTile), (unsigned)count),
                        dim3(kProductThreads), smem, s, maps, m, n, out, ldx, fin));
     return SG_OK;
@@ -1382,13 +1374,12 @@ const float kCoef[3] = {3.4445f, -4.7750f, 2.0315f};
 template <int W, typename TS, typename TW>
 sg_status launch_fused(const Source<TS>& src, int32_t count, int32_t rows, int32_t cols, int ctas, const Steps& steps,
                        float eps, const FinalArgs& fin, cudaStream_t s) {
-    static bool set = false;
-    if (!set) {
-        SG_CUDA(cudaFuncSetAttribute(k_ns_fused<W, TS, TW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFusedSmem<W>));
-        if (W < 256)
-            SG_CUDA(cudaFuncSetAttribute(k_ns_fused<W, TS, TW>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
-        set = true;
-    }
+    static OncePerDevice set;
+    SG_CUDA(once_on_device(set, [] {
+        const auto kernel = k_ns_fused<W, TS, TW>;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFusedSmem<W>);
+        return e != cudaSuccess || W == 256 ? e : cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    }));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas, (unsigned)count);
     cfg.blockDim = dim3(kFusedThreads<W>);
@@ -1407,11 +1398,17 @@ sg_status launch_fused(const Source<TS>& src, int32_t count, int32_t rows, int32
     return SG_OK;
 }
 
-// Whether the device takes clusters of 16 CTAs with all of an SM's shared
-// memory each (looked up once).
+// Whether the current device takes clusters of 16 CTAs with all of an SM's
+// shared memory each (looked up once for each device).
 bool clusters_of_16() {
-    static int ok = -1;
-    if (ok < 0) {
+    static OncePerDevice set;
+    static std::atomic<uint64_t> yes{0};  // by device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        cudaGetLastError();
+        return false;
+    }
+    set(dev, [&] {
         const auto kernel = k_ns_fused<128, float, float>;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(16);
@@ -1425,12 +1422,14 @@ bool clusters_of_16() {
         cfg.attrs = at;
         cfg.numAttrs = 1;
         int n = 0;
-        ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFusedSmem<128>) == cudaSuccess &&
-             cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-             cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0;
-        if (!ok) cudaGetLastError();
-    }
-    return ok != 0;
+        const bool ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFusedSmem<128>) == cudaSuccess &&
+                        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0;
+        if (ok) yes.fetch_or((uint64_t)1 << dev);
+        else cudaGetLastError();
+        return 0;
+    });
+    return (yes.load() >> dev) & 1;
 }
 
 template <typename TS, typename TW>

@@ -367,11 +367,8 @@ template <bool TF32>
 sg_status launch_fwd(const UpdateMaps& maps, int32_t n_cap, const int32_t* d_n, int32_t kt_half, float* out, float* y,
                      cudaStream_t s) {
     const size_t smem = (size_t)kSmemTiles + 1024;
-    static bool attr = false;
-    if (!attr) {
-        SG_CUDA(cudaFuncSetAttribute(k_sage_fwd<TF32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-        attr = true;
-    }
+    static OncePerDevice set;
+    SG_CUDA(allow_smem(set, k_sage_fwd<TF32>, (int)smem));
     const unsigned blocks = (unsigned)((n_cap + kBM - 1) / kBM);
     SG_CUDA(launch_pdl(k_sage_fwd<TF32>, dim3(blocks), dim3(kThreads), smem, s, maps, n_cap, d_n, kt_half, out, y));
     return SG_OK;
@@ -441,11 +438,8 @@ sg_status launch_gemm(const GemmMaps& maps, dim3 grid, int32_t m_cap, const int3
                       const int32_t* d_k, int32_t n_cols, int32_t split_col, float* o0, float* o1, int32_t ld1,
                       cudaStream_t s) {
     const size_t smem = (size_t)kSmemTiles + 1024;
-    static bool attr = false;
-    if (!attr) {
-        SG_CUDA(cudaFuncSetAttribute(k_sage_gemm<TF32, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-        attr = true;
-    }
+    static OncePerDevice set;
+    SG_CUDA(allow_smem(set, k_sage_gemm<TF32, EPI>, (int)smem));
     SG_CUDA(launch_pdl(k_sage_gemm<TF32, EPI>, grid, dim3(kThreads), smem, s, maps, m_cap, d_m, k_cap, d_k, n_cols,
                        split_col, o0, o1, ld1));
     return SG_OK;
