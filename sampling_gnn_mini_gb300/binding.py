@@ -704,7 +704,7 @@ def _scratch(name: str, t: torch.Tensor, dev: int):
     bytes (their number and alignment are the library's to check)."""
     if not isinstance(t, torch.Tensor) or t.get_device() != dev or not t.is_contiguous():
         _invalid("%s: workspace must be a contiguous tensor on the device of the other arguments" % name)
-    return t.data_ptr(), t.numel() * t.element_size()
+    return t.data_ptr(), t.nbytes
 
 
 def _raw_stream(stream, dev: int) -> int:
