@@ -17,8 +17,8 @@
 // sum has one order: no float atomics.
 //
 // The sort: up to kSmallSort positions in one block's shared memory
-// (k_sort_small); up to kClusterSort by one cluster (k_sort_cluster); else
-// one histogram launch for all passes, then one launch a
+// (k_sort_small); up to kClusterSort by one cluster, where the device takes it
+// (k_sort_cluster); else one histogram launch for all passes, then one launch a
 // pass, whose tiles learn their digits' offsets from the tiles before them
 // (decoupled look-back, one thread a digit).
 #include <cuda_bf16.h>
@@ -1036,7 +1036,7 @@ BwdLayout bwd_layout(int64_t n_cap, int32_t dim) {
             const int64_t t = cut_for(n_cap, dim, vec).most;
             if (t > L.tiles) L.tiles = t;
         }
-    L.sort_tiles = n_cap <= kClusterSort ? 0 : cdiv(n_cap, kSortThreads * 4);
+    L.sort_tiles = n_cap <= kSmallSort ? 0 : cdiv(n_cap, kSortThreads * 4);
     size_t o = 0;
     const auto put = [&o](size_t bytes) {
         const size_t at = o;
@@ -1081,27 +1081,58 @@ sg_status run_sum(int vec, const void* g, const SumArgs<TO>& a, int32_t span, cu
     return launch_sum<TI, TO, 1>(g, a, span, s);
 }
 
-template <int ITEMS, int CTAS>
-cudaError_t sort_by_cluster(const int32_t* ids, int64_t n_rows, int64_t n_cap, const int32_t* d_n, Digits dg, int32_t span,
-                           uint2* const (&kv)[2], int32_t* starts, int32_t* n_out, cudaStream_t s) {
-    static OncePerDevice set;
-    const cudaError_t e = once_on_device(set, [] {
-        return cudaFuncSetAttribute(k_sort_cluster<ITEMS, CTAS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    });
-    if (e != cudaSuccess) return e;
+// A launch of the sort by one cluster of CTAS blocks; at: its two attributes.
+template <int CTAS>
+cudaLaunchConfig_t cluster_config(cudaLaunchAttribute (&at)[2], cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(CTAS);
     cfg.blockDim = dim3(kSmallThreads);
     cfg.stream = s;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = CTAS;
-    at[1].val.clusterDim.y = 1;
-    at[1].val.clusterDim.z = 1;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CTAS;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
+    return cfg;
+}
+
+// Whether the current device takes such a cluster (looked up once for each
+// device): a part of a device may have fewer SMs side by side than it needs.
+template <int ITEMS, int CTAS>
+bool cluster_fits() {
+    static OncePerDevice set;
+    static std::atomic<uint64_t> yes{0};  // by device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        cudaGetLastError();
+        return false;
+    }
+    set(dev, [&] {
+        cudaLaunchAttribute at[2];
+        cudaLaunchConfig_t cfg = cluster_config<CTAS>(at, nullptr);
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaFuncSetAttribute(k_sort_cluster<ITEMS, CTAS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+            cudaOccupancyMaxActiveClusters(&n, k_sort_cluster<ITEMS, CTAS>, &cfg) == cudaSuccess && n > 0)
+            yes.fetch_or((uint64_t)1 << dev);
+        else
+            cudaGetLastError();
+        return 0;
+    });
+    return (yes.load() >> dev) & 1;
+}
+
+// Sorts by one cluster of CTAS blocks; *taken: whether the device takes it.
+template <int ITEMS, int CTAS>
+cudaError_t sort_by_cluster(const int32_t* ids, int64_t n_rows, int64_t n_cap, const int32_t* d_n, Digits dg, int32_t span,
+                            uint2* const (&kv)[2], int32_t* starts, int32_t* n_out, cudaStream_t s, bool* taken) {
+    *taken = cluster_fits<ITEMS, CTAS>();
+    if (!*taken) return cudaSuccess;
+    cudaLaunchAttribute at[2];
+    const cudaLaunchConfig_t cfg = cluster_config<CTAS>(at, s);
     return cudaLaunchKernelEx(&cfg, k_sort_cluster<ITEMS, CTAS>, ids, n_rows, (int32_t)n_cap, d_n, dg, span, kv[0], kv[1], starts,
                               n_out);
 }
@@ -1136,9 +1167,10 @@ sg_status run_sort(const int32_t* ids, int64_t n_cap, const int32_t* d_n, int64_
         const auto sort = n_cap <= kClusterSort / 4   ? sort_by_cluster<1, kSortCtas / 2>
                           : n_cap <= kClusterSort / 2 ? sort_by_cluster<1, kSortCtas>
                                                       : sort_by_cluster<2, kSortCtas>;
-        SG_CUDA(sort(ids, n_rows, n_cap, d_n, dg, span, kv, starts, distinct, s));
+        bool taken = false;
+        SG_CUDA(sort(ids, n_rows, n_cap, d_n, dg, span, kv, starts, distinct, s, &taken));
         *sorted = kv[(dg.passes & 1) ^ 1];
-        return SG_OK;
+        if (taken) return SG_OK;
     }
     // the fewest items a thread (4, 8 or 12) with which every tile has an SM of
     // its own: two tiles on an SM take twice as long as one, and every later

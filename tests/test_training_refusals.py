@@ -163,3 +163,12 @@ def test_binding_passes_the_workspace_in_bytes(monkeypatch):
         ws = _on_device(n, dtype=dtype)
         sg.sg_orthogonalise(_on_device(4, 8), _on_device(4, 8), ws, stream=0)
         assert seen[-1][-3:-1] == (ws.data_ptr(), 4096)
+
+
+def test_embed_bwd_workspace_has_room_for_the_passes(lib):
+    # where a device takes no cluster for a list of some thousands, the sort goes
+    # over it in passes: pairs in and out (16 bytes a position), counts of 256
+    # digits in 4 passes (8 copies), and a word a digit and pass for every 2,048 positions
+    for n in (3073, 5000, 8192, 16384, 32768, 32769, 100000):
+        room = 16 * n + 8 * 4 * 256 * 4 + -(-n // 2048) * 256 * 4 * 4
+        assert lib.sg_embed_bwd_workspace(n, 1 << 30, 1, sg.SG_GRAD_ADD) >= room
