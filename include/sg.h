@@ -652,8 +652,12 @@ sg_status sg_xent(const void* d_logits, int32_t dtype, int32_t n_cap, const int3
  *   out = scale * X, transposed back
  * Every singular value t of G / (||G||_F + eps) becomes f_k(..f_1(t)),
  * f(t) = a t + b t^3 + c t^5.  The products run on the tensor cores with each
- * operand held as two fp16 terms (22 bits), fp32 accumulation; the norm is
- * summed in fp32 (of squares: norms from about 1e-18 to 1e19).
+ * operand held as two fp16 terms, fp32 accumulation: entries of X, A and
+ * a I + b A + c A A have 22 bits down to about 5e-4 and are off by up to 2^-33
+ * below that (X has norm 1 at first: 22 bits are usual up to 1024 x 4096, 18 at
+ * the largest sizes; b A and c A A have entries of about 1 / m and 1 / m^2 then,
+ * so a schedule with a near 0 loses bits).  The norm is summed in fp32 (of
+ * squares: norms from about 1e-18 to 1e19).
  *   d_g, d_out  device, `dtype` (SG_F32 or SG_BF16); matrix q starts at element
  *               q * rows * ld, its rows are ld (>= cols) elements apart
  *               (ld_out for d_out).  d_out may be d_g with the same stride.

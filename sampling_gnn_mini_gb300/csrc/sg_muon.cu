@@ -11,8 +11,10 @@
 // one 16-bit operand a product (off by up to 2^-8 in bf16, 2^-11 in fp16) would leave
 // errors of a percent and more.  Every operand is held as two fp16 terms,
 // hi + lo, of 256 times its value: the iterates are bounded (singular values
-// up to about 1.2), so 256 x stays inside fp16's range and lo above its
-// subnormals, and the pair carries 22 bits.  A product is three tensor-core
+// up to about 1.2), so 256 x stays inside fp16's range, and the pair carries 22
+// bits while lo is above fp16's subnormals (entries from 2^-11, 5e-4); below, x is off by
+// up to 2^-33 (half of lo's last step).  A first iterate's entry is about 1 / sqrt(m n):
+// 5e-4 for 1024 x 4096, 4e-5 at the largest sizes (18 bits).  A product is three tensor-core
 // products, hi hi + hi lo + lo hi, with fp32 accumulation in tensor memory.
 // Folding a I into B makes X <- B X one product with nothing to add.
 // The tensor core cuts a sum's low bits at every accumulation, always towards
