@@ -342,7 +342,7 @@ template <int NV, int R>
 constexpr int kWarpBlocks = NV * R > 4 ? 2 : 3;
 
 // Each warp walks over its rows with the next rows' labels a turn ahead (65,536
-// rows of 128 fp32: 33 us for the call; with a block for every 32 rows 44).
+// rows of 128 fp32: 27 us for the call; with a block for every 32 rows 33).
 template <typename T, int NV, int R>
 __global__ void __launch_bounds__(kThreads, kWarpBlocks<NV, R>) k_xent_warp(RowArgs<T> a) {
     pdl_start();
@@ -365,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, kWarpBlocks<NV, R>) k_xent_warp(RowA
     if (last) put_total<kThreads>(a, n);
 }
 
-// Many rows of a few classes: a thread a row.  65,536 rows of 4 / 16 classes 16 /
-// 22 us, by warps 29 / 31.
+// Many rows of a few classes: a thread a row.  65,536 rows of 4 / 16 classes 11 /
+// 17 us, by warps 25 / 25.
 constexpr int kFewClasses = 16;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_xent_thread(RowArgs<T> a) {
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kThreads) k_xent_thread(RowArgs<T> a) {
 
 // The whole of a small call in one cluster: each CTA counts the labels, the
 // cluster's warps take the rows in turn, the warps' sums meet in CTA 0.  256
-// rows of 128 fp32: 6.3 us with the host's time, which bounds it.
+// rows of 128 fp32: 6.5 us with the host's time, which bounds it (5.1 without).
 template <typename T, int NV, int R>
 __global__ void __launch_bounds__(kThreads) k_xent_small(RowArgs<T> a) {
     pdl_start();
@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_xent_row(RowArgs<T> a) {
 // Many long rows: the same, with each cluster walking over its rows and the
 // next two rows' slices on their way into shared memory (one bulk copy of a
 // slice's vectors) while the current row is worked on.  4096 x 50,257 bf16:
-// 136 us, 6.1 TB/s; memory bounds it, with 65 % of the issue slots taken.
+// 138 us, 6.0 TB/s; memory bounds it, with 67 % of the issue slots taken.
 constexpr int kStreamVecs = 3500;  // of a CTA's slice: two buffers of it, two CTAs an SM
 
 template <typename T, int NT, int S>
@@ -780,7 +780,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_xent_stream(RowArgs<T> a, int
 
 // Rows whose label is not -1 (one cluster: one block, or kCountCtas when there
 // are many); clears the count of finished blocks.  us for the whole call, one block /
-// a cluster: 8,192 rows of 128 14.3 / 16.4, 16,384 20.5 / 18.4, 65,536 47 / 33.
+// a cluster: 8,192 rows of 128 8.7 / 9.7, 16,384 12.6 / 12.3, 65,536 32 / 27.
 constexpr int kCountCtas = 8, kCountMany = 8192;
 __global__ void __launch_bounds__(kTotalThreads) k_xent_count(const int32_t* __restrict__ labels, int32_t n_cap,
                                                               const int32_t* __restrict__ d_n,
@@ -870,8 +870,9 @@ sg_status run(RowArgs<T> a, cudaStream_t s) {
     const bool by_warp = nv <= 32 * kVecs;
     // one cluster serves a call whose rows its warps hold in a turn or two; a
     // turn costs as much as the second launch saves (fp32, cluster / two
-    // launches, us: 256 rows of 40 or 128 classes 5.7 / 7.2, 384 8.5 / 7.5; 256
-    // of 200 6.4 / 7.2; 128 of 400 5.2 / 7.4; 64 of 1000 5.1 / 7.2)
+    // launches, us on the device: 256 rows of 40 or 128 classes 5.1 / 7.4, 384 of
+    // 128 7.6 / 7.6, 1,000 of 40 12.5 / 7.7; 256 of 200 5.6 / 6.6; 128 of 400 4.5 /
+    // 7.0; 64 of 1000 4.3 / 6.8)
     const bool small = by_warp && a.n_cap <= 256 && a.n_cap * nv <= kSmallCtas * kThreads * kVecs;
     if (!small) {
         if (a.n_cap > kCountMany)
@@ -894,9 +895,9 @@ sg_status run(RowArgs<T> a, cudaStream_t s) {
     // rows for several turns of every cluster are streamed: one and a half turns
     // are enough for clusters of one or two CTAs, three for wider ones, which
     // idle together in a last turn (bf16, streamed / in registers, us: 1,300
-    // rows of 10,000 16.2 / 17.5, 450 of 20,000 13.6 / 15.2, 300 of 50,257 17.2
-    // / 19.0, but 200 14.9 / 15.4 and 100 12.5 / 10.5; 170 of 100,000 23.6 / 20.8;
-    // 4,096 of 50,257 141 / 182)
+    // rows of 10,000 18.5 / 19.3, 450 of 20,000 14.6 / 16.1, 300 of 50,257 20.4
+    // / 21.5, but 200 17.0 / 17.3 and 100 11.9 / 9.7; 170 of 100,000 26.5 / 23.1;
+    // 4,096 of 50,257 140 / 178)
     const int wide = nv <= 7 * kThreads ? 1 : nv <= kStreamVecs ? 2 : nv <= 2 * kStreamVecs ? 4 : nv <= 4 * kStreamVecs ? 8 : 16;
     if (nv <= 8 * kStreamVecs && (int64_t)a.n_cap * wide >= (wide <= 4 ? 6 : 12) * num_sms()) {
         switch (wide) {
@@ -908,7 +909,7 @@ sg_status run(RowArgs<T> a, cudaStream_t s) {
         }
     }
     // smallest cluster whose registers hold the row, widened while the rows do
-    // not fill the SMs (20 rows of 20,000 fp32: 8.2 us, 8.5 unwidened); 512
+    // not fill the SMs (20 rows of 20,000 fp32: 7.3 us, 7.8 unwidened); 512
     // threads when 8 CTAs of 256 do not hold it
     int split = 1;
     while (split < 8 && nv > (int64_t)split * kThreads * kVecs) split *= 2;
