@@ -116,7 +116,7 @@ def test_coefficients_are_checked():
 @pytest.mark.parametrize("dim", [1, 3, 8, 20, 32, 64, 100, 128, 256, 1000, 1024, 4096])
 def test_embed_bwd_workspace_grows_with_the_list(lib, dim):
     # sized for the longest list, a workspace serves every shorter one
-    sizes = list(range(1, 12000, 7)) + [s for k in range(1, 400) for s in (512 * k, 512 * k + 1)] + [1 << k for k in range(30)]
+    sizes = list(range(1, 12000, 7)) + [s for k in range(1, 400) for s in (640 * k, 640 * k + 1)] + [1 << k for k in range(30)]
     need = [lib.sg_embed_bwd_workspace(n, 1000, dim, sg.SG_GRAD_ADD) for n in sorted(set(sizes))]
     assert need[0] > 0 and all(a <= b for a, b in zip(need, need[1:]))
 
