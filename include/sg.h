@@ -75,6 +75,8 @@ typedef int32_t sg_status;
 #define SG_MAX_HOPS 8
 #define SG_MAX_SUB 64           /* mini-batches per super-batch */
 #define SG_MAX_FANOUT 256
+#define SG_MAX_TOP 128          /* top classes of a row (sg_logprobs, sg_distill) */
+#define SG_MAX_NORM_DIM 16384   /* width of a normalised row (sg_layernorm_*) */
 
 typedef void* sg_stream_t;      /* cudaStream_t */
 typedef void* sg_event_t;       /* cudaEvent_t */
@@ -641,6 +643,105 @@ size_t sg_xent_workspace(int32_t n_cap, int32_t n_classes);
 sg_status sg_xent(const void* d_logits, int32_t dtype, int32_t n_cap, const int32_t* d_n, int32_t n_classes, int64_t ld,
                   const int32_t* d_labels, int32_t mean, float grad_scale, float* d_loss, float* d_total, void* d_grad,
                   int64_t ld_grad, void* d_workspace, size_t workspace_bytes, sg_stream_t stream);
+
+/* ------------------------------------------------- answers and distillation */
+/* What n rows of logits x answer: with lse = log(sum_c exp(x[r, c])),
+ *   logp[r]        = x[r, label[r]] - lse
+ *   entropy[r]     = -sum_c p log p,  p = exp(x[r, c] - lse)
+ *   top_ids[r, j], top_logp[r, j]   the j-th most probable class (the lower class
+ *                    first among equal logits) and its x - lse, j < k
+ * Logits of -inf take no part (classes that are masked off): entries past the
+ * number of the others hold class -1 and -inf, as they do past n_classes, and a
+ * label there has -inf.  In a row whose logits are all -inf the entropy is 0.
+ * +inf or NaN logits give NaN in the row's numbers and classes of -1.
+ * Statistics are held in fp32; the same bits on every run.
+ *   d_logits   device [n_cap x n_classes], row stride ld elements (>= n_classes),
+ *              SG_F32 or SG_BF16, any element alignment; n_cap up to 2^27
+ *   d_n        device int32 count (n = *d_n <= n_cap) or NULL (n = n_cap); rows
+ *              from n on are not touched
+ *   d_labels, d_logp   device int32 [n_cap] and fp32 [n_cap], or both NULL; a label
+ *              of -1 gives 0, another one out of range sets the device error word
+ *              and gives 0
+ *   d_entropy  device fp32 [n_cap], or NULL
+ *   k          0 .. SG_MAX_TOP; d_top_ids device int32 [n_cap x k] and d_top_logp
+ *              device fp32 [n_cap x k], both NULL with k = 0 */
+sg_status sg_logprobs(const void* d_logits, int32_t dtype, int32_t n_cap, const int32_t* d_n, int32_t n_classes,
+                      int64_t ld, const int32_t* d_labels, int32_t k, float* d_logp, float* d_entropy,
+                      int32_t* d_top_ids, float* d_top_logp, sg_stream_t stream);
+
+/* Distillation of n rows of a student's logits x from a teacher's top logits,
+ * with its gradient: with T the temperature, q = softmax(v / T) over the row's k
+ * entries (class id_j, value v_j) and p = softmax(x / T) over all classes,
+ *   loss[r]    = T^2 sum_j q_j (log q_j - log p[id_j])
+ *   total      = {sum of loss (divided by max(1, m) with mean != 0), m},
+ *                m = the number of rows r < n with a teacher
+ *   grad[r, c] = w T (p[c] - sum of q_j over id_j = c),
+ *                w = grad_scale, divided by max(1, m) with mean != 0
+ * The values may be logits or log probabilities (sg_logprobs' top_logp): q does
+ * not depend on their level.  A row has a teacher when its first entry is one: a
+ * class in range with a value above -inf.  Without one its loss and gradient
+ * are 0.  Entries of class -1 and values of -inf take no part; a class that occurs
+ * more than once collects its entries.  Logits of -inf take no part; an entry of
+ * q > 0 there makes the loss +inf, and in a row whose logits are all -inf the
+ * gradient is 0.  +inf or NaN logits give NaN in their row, such values NaN in
+ * its loss and at the gradient of its entries' classes.  Statistics are held in
+ * fp32; total's order of summation is fixed.
+ *   d_logits   device [n_cap x n_classes], row stride ld elements (>= n_classes),
+ *              SG_F32 or SG_BF16, any element alignment; n_cap up to 2^27
+ *   d_n        device int32 count (n = *d_n <= n_cap) or NULL (n = n_cap)
+ *   d_ids, d_values  device int32 and fp32 [n_cap x k], k from 1 to SG_MAX_TOP;
+ *              another class out of range sets the device error word and takes no part
+ *   temperature  0.001 to 1000
+ *   d_loss     device fp32 [n_cap]: rows r < n written
+ *   d_total    device fp32 [2], or NULL
+ *   d_grad     device, dtype as the logits, row stride ld_grad (>= n_classes), or NULL
+ *              (loss only); must not overlap the logits
+ *   d_workspace  device scratch of sg_distill_workspace(...) bytes, 256-byte
+ *              aligned, in no particular state */
+size_t sg_distill_workspace(int32_t n_cap, int32_t n_classes);
+sg_status sg_distill(const void* d_logits, int32_t dtype, int32_t n_cap, const int32_t* d_n, int32_t n_classes,
+                     int64_t ld, const int32_t* d_ids, const float* d_values, int32_t k, float temperature, int32_t mean,
+                     float grad_scale, float* d_loss, float* d_total, void* d_grad, int64_t ld_grad, void* d_workspace,
+                     size_t workspace_bytes, sg_stream_t stream);
+
+/* ------------------------------------------------------------- layer norm */
+/* Layer norm of n rows of dim values:
+ *   mean[r] = mean of x[r, :],  rstd[r] = 1 / sqrt(mean of (x[r, :] - mean[r])^2 + eps)
+ *   y[r, c] = (x[r, c] - mean[r]) rstd[r] weight[c] + bias[c]
+ * in fp32 (the deviation about the mean, in a second pass over the row on the
+ * chip), rounded once to the output's type.
+ *   d_x, d_y   device [n_cap x dim], SG_F32 or SG_BF16, row strides ld and ld_y
+ *              elements (>= dim), any element alignment (rows and strides on 16
+ *              bytes are fastest); d_y may be d_x with the same stride, but must not
+ *              overlap it in any other way
+ *   d_n        device int32 count (n = *d_n <= n_cap) or NULL (n = n_cap); rows
+ *              from n on are not touched
+ *   dim        1 .. SG_MAX_NORM_DIM
+ *   d_weight, d_bias  device [dim] of dtype_w (SG_F32 or SG_BF16); NULL: 1, 0
+ *   d_mean, d_rstd    device fp32 [n_cap] for the gradient, or NULL */
+sg_status sg_layernorm_fwd(const void* d_x, int32_t dtype, int32_t n_cap, const int32_t* d_n, int32_t dim, int64_t ld,
+                           const void* d_weight, const void* d_bias, int32_t dtype_w, float eps, void* d_y, int64_t ld_y,
+                           float* d_mean, float* d_rstd, sg_stream_t stream);
+
+/* Its gradient for g = dL/dy, from the x, mean and rstd of the forward call:
+ * with h = (x - mean) rstd and u = g weight,
+ *   dx[r, :] = rstd (u - mean of u - h (mean of u h))
+ *   dweight  = sum over rows r < n of g h,  dbias = sum over rows r < n of g
+ * Sums are held in fp32, over the rows in a fixed order: no float atomics, the
+ * same bits on every run.
+ *   d_g, d_x, d_dx  device [n_cap x dim] of dtype, row strides ld_g, ld, ld_dx; d_dx
+ *              may be d_g or d_x with the same stride, but must not overlap them in
+ *              any other way
+ *   d_dweight, d_dbias  device [dim] of dtype_w, each may be NULL; written whole
+ *              (zeros with n = 0)
+ *   d_workspace  device scratch of sg_layernorm_bwd_workspace(...) bytes, 256-byte
+ *              aligned, in no particular state; one sized for an n_cap serves every
+ *              smaller n_cap of that dim as well */
+size_t sg_layernorm_bwd_workspace(int32_t n_cap, int32_t dim);
+sg_status sg_layernorm_bwd(const void* d_g, const void* d_x, int32_t dtype, int32_t n_cap, const int32_t* d_n, int32_t dim,
+                           int64_t ld_g, int64_t ld, const void* d_weight, int32_t dtype_w, const float* d_mean,
+                           const float* d_rstd, void* d_dx, int64_t ld_dx, void* d_dweight, void* d_dbias,
+                           void* d_workspace, size_t workspace_bytes, sg_stream_t stream);
 
 /* ------------------------------------------------- orthogonalised updates */
 #define SG_MAX_NS_STEPS 16

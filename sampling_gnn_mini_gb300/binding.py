@@ -36,6 +36,8 @@ SG_MAX_NS_STEPS = 16
 SG_MAX_HOPS = 8
 SG_MAX_SUB = 64
 SG_MAX_FANOUT = 256
+SG_MAX_TOP = 128
+SG_MAX_NORM_DIM = 16384
 
 _STATUS_NAMES = {0: "SG_OK", 1: "SG_ERR_INVALID_ARG", 2: "SG_ERR_INVALID_INDEX", 3: "SG_ERR_CAPACITY",
                  4: "SG_ERR_OOM", 5: "SG_ERR_CUDA", 6: "SG_ERR_TIMEOUT", 7: "SG_ERR_UNSUPPORTED"}
@@ -51,7 +53,8 @@ EXPORTS = ["sg_version", "sg_last_error", "sg_stream_check", "sg_graph_load", "s
            "sg_dyn_cache_create", "sg_dyn_cache_batch", "sg_dyn_cache_info", "sg_gather_reuse", "sg_match",
            "sg_overlap", "sg_greedy_order", "sg_graph_in_degree", "sg_embed_fwd", "sg_embed_bwd_workspace",
            "sg_embed_bwd", "sg_xent_workspace", "sg_xent", "sg_orthogonalise_workspace", "sg_orthogonalise",
-           "sg_muon_step"]
+           "sg_muon_step", "sg_logprobs", "sg_distill_workspace", "sg_distill", "sg_layernorm_fwd",
+           "sg_layernorm_bwd_workspace", "sg_layernorm_bwd"]
 
 
 class SgError(RuntimeError):
@@ -156,6 +159,12 @@ def load(build_if_missing: bool = True):
             "sg_orthogonalise": (i32, [vp, i32, i32, i32, i32, i64, i32, vp, f32, f32, vp, i64, vp, sz, vp]),
             "sg_muon_step": (i32, [vp, i32, vp, vp, i32, i32, i32, f32, f32, i32, f32, f32, i32, vp, f32, vp, vp, vp,
                                    sz, vp]),
+            "sg_logprobs": (i32, [vp, i32, i32, vp, i32, i64, vp, i32, vp, vp, vp, vp, vp]),
+            "sg_distill_workspace": (sz, [i32, i32]),
+            "sg_distill": (i32, [vp, i32, i32, vp, i32, i64, vp, vp, i32, f32, i32, f32, vp, vp, vp, i64, vp, sz, vp]),
+            "sg_layernorm_fwd": (i32, [vp, i32, i32, vp, i32, i64, vp, vp, i32, f32, vp, i64, vp, vp, vp]),
+            "sg_layernorm_bwd_workspace": (sz, [i32, i32]),
+            "sg_layernorm_bwd": (i32, [vp, vp, i32, i32, vp, i32, i64, i64, vp, i32, vp, vp, vp, i64, vp, vp, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -852,5 +861,155 @@ def sg_muon_step(w: torch.Tensor, g: torch.Tensor, m: torch.Tensor, w_out: torch
     st = (_lib or load()).sg_muon_step(w.data_ptr(), dt, g.data_ptr(), m.data_ptr(), k, r, c, lr, momentum,
                                        1 if nesterov else 0, weight_decay, scale, steps, _ptr(cf), eps,
                                        w_out.data_ptr(), m_out.data_ptr(), p_ws, n_ws, _raw_stream(stream, dev))
+    if st:
+        _check(st)
+
+
+# ------------------------------------------- answers, distillation, layer norm
+def _own_stream(what: str, stream, dev: int) -> int:
+    """The raw stream of a call whose tensors are on device dev, which has to
+    be the current one (a stream given by its address is taken as it is)."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        return int(stream)
+    if torch._C._cuda_getDevice() != dev or (stream is not None and stream.device_index != dev):
+        _invalid("%s: the tensors must be on the current device, and on the stream's" % what)
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def sg_logprobs(logits: torch.Tensor, labels: Optional[torch.Tensor], n_cap: int, d_n: Optional[torch.Tensor],
+                logp: Optional[torch.Tensor], entropy: Optional[torch.Tensor], top_ids: Optional[torch.Tensor] = None,
+                top_logp: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Log probability of each row's label, the row's entropy, and its
+    top_ids.shape[1] most probable classes with their log probabilities; see
+    sg.h."""
+    dev = logits.get_device()
+    c = logits.shape[1] if logits.dim() == 2 else _invalid("sg_logprobs: logits must be 2-D")
+    dt, ld = _matrix("sg_logprobs: logits", logits, n_cap, c, dev)
+    p_y = p_logp = p_ids = p_top = None
+    k = 0
+    if labels is not None or logp is not None:
+        p_y = _vector("sg_logprobs: labels", labels, n_cap, torch.int32, dev)
+        p_logp = _vector("sg_logprobs: logp", logp, n_cap, torch.float32, dev)
+    p_ent = None if entropy is None else _vector("sg_logprobs: entropy", entropy, n_cap, torch.float32, dev)
+    if top_ids is not None or top_logp is not None:
+        if not isinstance(top_ids, torch.Tensor) or top_ids.dim() != 2 or not 1 <= top_ids.shape[1] <= SG_MAX_TOP:
+            _invalid("sg_logprobs: top_ids must be 2-D with 1 to %d columns" % SG_MAX_TOP)
+        k = top_ids.shape[1]
+        p_ids = _vector("sg_logprobs: top_ids", top_ids, n_cap * k, torch.int32, dev)
+        p_top = _vector("sg_logprobs: top_logp", top_logp, n_cap * k, torch.float32, dev)
+        if top_logp.shape[-1] != k:
+            _invalid("sg_logprobs: top_logp must have top_ids' columns")
+    p_n = None if d_n is None else _vector("sg_logprobs: d_n", d_n, 1, torch.int32, dev)
+    raw = _own_stream("sg_logprobs", stream, dev)
+    st = (_lib or load()).sg_logprobs(logits.data_ptr(), dt, n_cap, p_n, c, ld, p_y, k, p_logp, p_ent, p_ids, p_top,
+                                      raw)
+    if st:
+        _check(st)
+
+
+def sg_distill_workspace(n_cap: int, n_classes: int) -> int:
+    return int(load().sg_distill_workspace(int(n_cap), int(n_classes)))
+
+
+def sg_distill(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, n_cap: int, d_n: Optional[torch.Tensor],
+               loss: torch.Tensor, total: Optional[torch.Tensor], grad: Optional[torch.Tensor], workspace: torch.Tensor,
+               temperature: float = 1.0, mean: bool = True, grad_scale: float = 1.0, stream=None) -> None:
+    """Distillation of each row from a teacher's ids.shape[1] top logits
+    (classes ids, their values), its sum or mean (total[0], with the number of
+    rows that have a teacher in total[1]) and the gradient; see sg.h."""
+    dev = logits.get_device()
+    c = logits.shape[1] if logits.dim() == 2 else _invalid("sg_distill: logits must be 2-D")
+    dt, ld = _matrix("sg_distill: logits", logits, n_cap, c, dev)
+    p_grad, ld_g = None, 0
+    if grad is not None:
+        dt_g, ld_g = _matrix("sg_distill: grad", grad, n_cap, c, dev)
+        if dt_g != dt:
+            _invalid("sg_distill: grad must have the logits' dtype")
+        p_grad = grad.data_ptr()
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or not 1 <= ids.shape[1] <= SG_MAX_TOP:
+        _invalid("sg_distill: ids must be 2-D with 1 to %d columns" % SG_MAX_TOP)
+    k = ids.shape[1]
+    p_ids = _vector("sg_distill: ids", ids, n_cap * k, torch.int32, dev)
+    p_v = _vector("sg_distill: values", values, n_cap * k, torch.float32, dev)
+    if values.shape[-1] != k:
+        _invalid("sg_distill: values must have ids' columns")
+    p_loss = _vector("sg_distill: loss", loss, n_cap, torch.float32, dev)
+    p_total = None if total is None else _vector("sg_distill: total", total, 2, torch.float32, dev)
+    p_n = None if d_n is None else _vector("sg_distill: d_n", d_n, 1, torch.int32, dev)
+    p_ws, n_ws = _scratch("sg_distill", workspace, dev)
+    raw = _own_stream("sg_distill", stream, dev)
+    st = (_lib or load()).sg_distill(logits.data_ptr(), dt, n_cap, p_n, c, ld, p_ids, p_v, k, temperature, 1 if mean else 0,
+                                     grad_scale, p_loss, p_total, p_grad, ld_g, p_ws, n_ws,
+                                     raw)
+    if st:
+        _check(st)
+
+
+def _param(name: str, t: Optional[torch.Tensor], dim: int, dtype, dev: int) -> Optional[int]:
+    return None if t is None else _vector(name, t, dim, dtype, dev)
+
+
+def _param_dtype(*params) -> torch.dtype:
+    """The dtype that the given weights and biases share (fp32 if there are
+    none)."""
+    kinds = {t.dtype for t in params if isinstance(t, torch.Tensor)}
+    if len(kinds) > 1 or not kinds <= set(_CODES):
+        _invalid("weight and bias (and their gradients) must be float32 or bfloat16 alike")
+    return kinds.pop() if kinds else torch.float32
+
+
+def sg_layernorm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optional[torch.Tensor], n_cap: int,
+                     d_n: Optional[torch.Tensor], out: torch.Tensor, mean: Optional[torch.Tensor] = None,
+                     rstd: Optional[torch.Tensor] = None, eps: float = 1e-5, stream=None) -> None:
+    """out = layer norm of the first n rows of x (which may be out), with the
+    rows' mean and 1 / deviation for the gradient; see sg.h."""
+    dev = x.get_device()
+    dim = x.shape[1] if x.dim() == 2 else _invalid("sg_layernorm_fwd: x must be 2-D")
+    dt, ld = _matrix("sg_layernorm_fwd: x", x, n_cap, dim, dev)
+    dt_o, ld_o = _matrix("sg_layernorm_fwd: out", out, n_cap, dim, dev)
+    if dt_o != dt:
+        _invalid("sg_layernorm_fwd: out must have x's dtype")
+    kind = _param_dtype(weight, bias)
+    p_w = _param("sg_layernorm_fwd: weight", weight, dim, kind, dev)
+    p_b = _param("sg_layernorm_fwd: bias", bias, dim, kind, dev)
+    p_m = _param("sg_layernorm_fwd: mean", mean, n_cap, torch.float32, dev)
+    p_r = _param("sg_layernorm_fwd: rstd", rstd, n_cap, torch.float32, dev)
+    p_n = _param("sg_layernorm_fwd: d_n", d_n, 1, torch.int32, dev)
+    raw = _own_stream("sg_layernorm_fwd", stream, dev)
+    st = (_lib or load()).sg_layernorm_fwd(x.data_ptr(), dt, n_cap, p_n, dim, ld, p_w, p_b, _CODES[kind], eps,
+                                           out.data_ptr(), ld_o, p_m, p_r, raw)
+    if st:
+        _check(st)
+
+
+def sg_layernorm_bwd_workspace(n_cap: int, dim: int) -> int:
+    return int(load().sg_layernorm_bwd_workspace(int(n_cap), int(dim)))
+
+
+def sg_layernorm_bwd(g: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], mean: torch.Tensor,
+                     rstd: torch.Tensor, n_cap: int, d_n: Optional[torch.Tensor], dx: torch.Tensor,
+                     dweight: Optional[torch.Tensor], dbias: Optional[torch.Tensor], workspace: torch.Tensor,
+                     stream=None) -> None:
+    """Gradient of sg_layernorm_fwd for g = dL/dout: dx (which may be g or x),
+    dweight and dbias (each may be None); see sg.h."""
+    dev = x.get_device()
+    dim = x.shape[1] if x.dim() == 2 else _invalid("sg_layernorm_bwd: x must be 2-D")
+    dt, ld = _matrix("sg_layernorm_bwd: x", x, n_cap, dim, dev)
+    dt_g, ld_g = _matrix("sg_layernorm_bwd: g", g, n_cap, dim, dev)
+    dt_d, ld_d = _matrix("sg_layernorm_bwd: dx", dx, n_cap, dim, dev)
+    if dt_g != dt or dt_d != dt:
+        _invalid("sg_layernorm_bwd: g and dx must have x's dtype")
+    kind = _param_dtype(weight, dweight, dbias)
+    p_w = _param("sg_layernorm_bwd: weight", weight, dim, kind, dev)
+    p_dw = _param("sg_layernorm_bwd: dweight", dweight, dim, kind, dev)
+    p_db = _param("sg_layernorm_bwd: dbias", dbias, dim, kind, dev)
+    p_m = _vector("sg_layernorm_bwd: mean", mean, n_cap, torch.float32, dev)
+    p_r = _vector("sg_layernorm_bwd: rstd", rstd, n_cap, torch.float32, dev)
+    p_n = _param("sg_layernorm_bwd: d_n", d_n, 1, torch.int32, dev)
+    p_ws, n_ws = _scratch("sg_layernorm_bwd", workspace, dev)
+    raw = _own_stream("sg_layernorm_bwd", stream, dev)
+    st = (_lib or load()).sg_layernorm_bwd(g.data_ptr(), x.data_ptr(), dt, n_cap, p_n, dim, ld_g, ld, p_w, _CODES[kind],
+                                           p_m, p_r, dx.data_ptr(), ld_d, p_dw, p_db, p_ws, n_ws,
+                                           raw)
     if st:
         _check(st)

@@ -1,0 +1,597 @@
+// Distillation from a teacher's top logits: per row of the student's logits x and
+// the teacher's k entries (id_j, v_j), with q = softmax(v / T) over the entries and
+// p = softmax(x / T) over all classes,
+//   loss[r]    = T^2 sum_j q_j (log q_j - log p[id_j])
+//   grad[r, c] = w T (p[c] - sum of q_j over id_j = c)
+// Bound by memory: the logits are read and the gradient is written once.  As in the
+// cross-entropy a row stays in registers in between, spread over a warp
+// (k_distill_warp) or a cluster of CTAs (k_distill_row), and many long rows are
+// streamed through shared memory ahead of their use (k_distill_stream).
+//
+// The entries are a row's small part: one warp of each CTA takes them (up to 4 a
+// lane) and forms q while the row is on its way.  Each thread first stores w T p of
+// its vectors; after a block's barrier the entries' classes are written again, from
+// their own logits.  An entry adds up all q of its class, so classes that occur more
+// than once are right, whichever of them writes last (they write the same).
+#include "sg_internal.cuh"
+#include "sg_rows.cuh"
+#include "sg_softmax.cuh"
+#include "sg_tc.cuh"
+
+SGI_ERROR_WORD(distill)
+
+using namespace sgi;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kCountThreads = 1024;
+constexpr int kPer = SG_MAX_TOP / 32;  // entries of a lane
+
+template <typename T>
+struct Args {
+    const T* x;
+    T* grad;
+    int64_t ld, ld_grad;
+    const int32_t* ids;
+    const float* values;
+    const int32_t* d_n;
+    int32_t n_cap, classes, k;
+    int32_t mean;
+    float gs, temp, l;  // l = log2(e) / temp
+    float* loss;
+    float* total;
+    int32_t* done;   // rows or blocks that are done; then `counts` counts of rows with a teacher
+    int32_t counts;
+};
+
+// Whether a row has a teacher: its first entry says so.
+__device__ __forceinline__ bool is_used(int32_t id, float v, int32_t classes) {
+    return id >= 0 && id < classes && v != -INFINITY;
+}
+template <typename T>
+__device__ __forceinline__ bool row_used(const Args<T>& a, int32_t r) {
+    return is_used(__ldg(a.ids + (int64_t)r * a.k), __ldg(a.values + (int64_t)r * a.k), a.classes);
+}
+
+// Rows with a teacher (a whole warp).
+template <typename T>
+__device__ __forceinline__ int32_t valid_of(const Args<T>& a) {
+    int32_t v = 0;
+    for (int32_t i = (int32_t)lane_id(); i < a.counts; i += 32) v += a.done[1 + i];
+    return warp_sum(v);
+}
+// What the gradient's softmax is multiplied by (a whole warp).
+template <typename T>
+__device__ __forceinline__ float weight_of(const Args<T>& a) {
+    const float w = a.gs * a.temp;
+    return a.mean ? w / (float)max(1, valid_of(a)) : w;
+}
+
+// A row's entries in shared memory, for the threads that write their classes.
+struct Entries {
+    int32_t id[SG_MAX_TOP];  // -1: none
+    float q[SG_MAX_TOP], x[SG_MAX_TOP];
+};
+
+// One warp: the entries as loaded, then as q.
+struct LaneEntries {
+    int32_t id[kPer];
+    float v[kPer], x[kPer];
+    float log_zq;
+};
+// report: names entries out of range in the error word
+template <typename T>
+__device__ __forceinline__ void load_entries(const Args<T>& a, int32_t r, const T* row, bool report, LaneEntries& n) {
+    const int lane = (int)lane_id();
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+        const int32_t j = lane + 32 * e;
+        n.id[e] = -1;
+        n.v[e] = -INFINITY;
+        if (j < a.k) {
+            const int32_t id = __ldg(a.ids + (int64_t)r * a.k + j);
+            const float v = __ldg(a.values + (int64_t)r * a.k + j);
+            if (id >= 0 && id < a.classes) n.id[e] = id, n.v[e] = v;
+            else if (id != -1 && report) dev_err(ERR_INDEX);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) n.x[e] = n.id[e] >= 0 ? to_f(row[n.id[e]]) : 0.f;
+}
+// v becomes (v - max) / T; the entries go to shared memory with their q (a used row:
+// at least one value is above -inf)
+template <typename T>
+__device__ __forceinline__ void share_entries(const Args<T>& a, LaneEntries& n, Entries& to) {
+    const int lane = (int)lane_id();
+    float m = -INFINITY, z = 0.f, q[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) m = fmaxf(m, n.v[e]);
+    m = warp_max(m);
+    if (m == -INFINITY) m = 0.f;  // all of them NaN
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+        q[e] = exp_from(n.v[e], m, a.l);
+        z += q[e];
+        n.v[e] = (n.v[e] - m) / a.temp;
+    }
+    z = warp_sum(z);
+    n.log_zq = logf(z);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+        const int32_t j = lane + 32 * e;
+        if (j >= a.k) break;
+        to.id[j] = n.id[e];
+        to.q[j] = q[e] / z;
+        to.x[j] = n.x[e];
+    }
+}
+// The row's loss (one warp, the same in every lane), from the row's maximum M and sum Z.
+template <typename T>
+__device__ __forceinline__ float loss_of(const Args<T>& a, const LaneEntries& n, const Entries& from, float M, float Z) {
+    const int lane = (int)lane_id();
+    const float log_z = logf(Z);
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+        const int32_t j = lane + 32 * e;
+        if (j >= a.k) break;
+        const float q = from.q[j];
+        if (q == 0.f) continue;
+        if (n.x[e] == -INFINITY && Z == Z) s += INFINITY;
+        else s = fmaf(q, (n.v[e] - n.log_zq) + (log_z - (n.x[e] - M) / a.temp), s);
+    }
+    return warp_sum(s) * (a.temp * a.temp);
+}
+// The gradient at entry j's class; false where there is none.
+template <typename T>
+__device__ __forceinline__ bool entry_grad(const Args<T>& a, const Entries& n, int32_t j, float w, float M, float Z,
+                                           float& g) {
+    const int32_t id = n.id[j];
+    if (id < 0) return false;
+    float q = 0.f;
+    for (int32_t i = 0; i < a.k; ++i)
+        if (n.id[i] == id) q += n.q[i];
+    g = Z == 0.f ? 0.f : fmaf(w / Z, exp_from(n.x[j], M, a.l), -w * q);
+    return true;
+}
+
+// The total, by the last block to finish.
+template <int NT, typename T>
+__device__ __forceinline__ void put_total(const Args<T>& a, int32_t n) {
+    const float s = block_sum_fixed<NT>(a.loss, n);
+    if (threadIdx.x >= 32) return;
+    const int32_t v = valid_of(a);
+    if (threadIdx.x == 0) {
+        a.total[0] = a.mean ? s / (float)max(1, v) : s;
+        a.total[1] = (float)v;
+    }
+}
+
+// ------------------------------------------------------------ rows by warps
+template <typename T, int NV>
+__global__ void __launch_bounds__(kThreads, 3) k_distill_warp(Args<T> a) {
+    pdl_start();
+    constexpr int kWarps = kThreads / 32;
+    __shared__ Entries entries[kWarps];
+    __shared__ bool last;
+    const int lane = (int)lane_id();
+    const int32_t n = rows_of(a.d_n, a.n_cap), blocks = min((int32_t)gridDim.x, (n + kWarps - 1) / kWarps);
+    if ((int32_t)blockIdx.x >= blocks) return;
+    const float w = weight_of(a);
+    Entries& mine = entries[threadIdx.x >> 5];
+    for (int32_t r = (int32_t)blockIdx.x * kWarps + (int32_t)(threadIdx.x >> 5); r < n; r += (int32_t)gridDim.x * kWarps) {
+        const T* row = a.x + (int64_t)r * a.ld;
+        T* out = a.grad ? a.grad + (int64_t)r * a.ld_grad : nullptr;
+        LaneEntries le;
+        load_entries(a, r, row, true, le);
+        const bool used = is_used(__shfl_sync(0xFFFFFFFFu, le.id[0], 0), __shfl_sync(0xFFFFFFFFu, le.v[0], 0), a.classes);
+        if (!used) {
+            if (lane == 0) a.loss[r] = 0.f;
+            if (out)
+                for (int32_t c = lane; c < a.classes; c += 32) put(out + c, 0.f);
+            continue;
+        }
+        const RowParts<T> part(row, a.classes);
+        uint4 x[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int32_t v = lane + 32 * k;
+            x[k] = v < part.vecs ? *reinterpret_cast<const uint4*>(row + part.head + v * kE<T>) : empty_part<T>();
+        }
+        const int32_t ce = part.edge(lane);
+        const float xe = ce >= 0 ? to_f(row[ce]) : -INFINITY;
+        share_entries(a, le, mine);
+        float m = xe;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) m = fmaxf(m, part_max<T>(x[k]));
+        m = warp_max(m);
+        if (m == -INFINITY) m = 0.f;
+        const Base base(m, a.l);
+        f2 sum = pair(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) part_exp<T>(x[k], base, sum);
+        float z, z1;
+        unpair(sum, z, z1);
+        z = warp_sum(z + z1 + base.of(xe));
+        const float loss = loss_of(a, le, mine, m, z);
+        if (lane == 0) a.loss[r] = loss;
+        if (!out) continue;
+        const bool same = same_phase(row, (const T*)out);
+        const float inv = z == 0.f ? 0.f : w / z;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int32_t v = lane + 32 * k;
+            if (v < part.vecs)
+                store_part(out + part.head + v * kE<T>, same, part_grad<T>(x[k], base, pair(inv, inv)));
+        }
+        if (ce >= 0) put(out + ce, inv * base.of(xe));
+        __syncwarp();  // the entries are there, the vectors stored
+        for (int32_t j = lane; j < a.k; j += 32) {
+            float g;
+            if (entry_grad(a, mine, j, w, m, z, g)) put(out + mine.id[j], g);
+        }
+        __syncwarp();  // before the next row's entries
+    }
+    if (!a.total) return;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(a.done, 1) == blocks - 1;
+    __syncthreads();
+    if (last) {
+        __threadfence();
+        put_total<kThreads>(a, n);
+    }
+}
+
+// --------------------------------------------------------- rows by clusters
+// This CTA's entries of a row whose vectors have been stored: the classes of its
+// vectors and, for CTA 0, the edge elements.
+template <typename T>
+__device__ __forceinline__ void put_entries(const Args<T>& a, const Entries& n, T* out, const RowParts<T>& part, int32_t v0,
+                                            int32_t count, int32_t rank, float w, float M, float Z) {
+    const int32_t j = (int32_t)threadIdx.x;
+    if (j >= a.k || n.id[j] < 0) return;
+    const int32_t at = part.place(n.id[j]);
+    if (at < 0 ? rank != 0 : at < v0 || at >= v0 + count) return;
+    float g;
+    if (entry_grad(a, n, j, w, M, Z, g)) put(out + n.id[j], g);
+}
+
+template <typename T, int NT, int S>
+__global__ void __launch_bounds__(NT, 1024 / NT) k_distill_row(Args<T> a) {
+    pdl_start();
+    constexpr int kParts = S * NT / 32;
+    __shared__ __align__(8) float2 parts[kParts];  // (m, z) of every warp of the cluster
+    __shared__ Entries entries;
+    __shared__ bool last;
+    const int32_t r = (int32_t)(blockIdx.x / S), rank = (int32_t)(blockIdx.x % S);
+    const int32_t n = rows_of(a.d_n, a.n_cap), classes = a.classes;
+    if (r >= n) return;  // the whole cluster
+    if constexpr (S > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
+    if (threadIdx.x == 0) last = false;
+    const T* row = a.x + (int64_t)r * a.ld;
+    T* out = a.grad ? a.grad + (int64_t)r * a.ld_grad : nullptr;
+    const bool used = row_used(a, r);  // the same in the whole cluster
+    const RowParts<T> part(row, classes);
+    const int32_t per = (part.vecs + S - 1) / S, v0 = min(part.vecs, rank * per), count = min(part.vecs, v0 + per) - v0;
+    const int32_t edge = rank == 0 && threadIdx.x < 32 ? part.edge((int)threadIdx.x) : -1;
+    const T* p = row + part.head + (v0 + (int32_t)threadIdx.x) * kE<T>;
+    const bool mine = threadIdx.x < 32 && (rank == 0 || out);  // the warp of the entries
+    LaneEntries le;
+    Held<T, NT> h;
+    h.m = 0.f, h.z = 0.f;
+    if (mine) load_entries(a, r, row, rank == 0, le);
+    if (used) {
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k)
+            h.x[k] = (int32_t)threadIdx.x + k * NT < count ? *reinterpret_cast<const uint4*>(p + k * NT * kE<T>)
+                                                           : empty_part<T>();
+        h.xe = edge >= 0 ? to_f(row[edge]) : -INFINITY;
+        if (mine) share_entries(a, le, entries);
+        float mr = -INFINITY, zr = 0.f;  // the part past the registers
+        for (int32_t i = (int32_t)threadIdx.x + kVecs * NT; i < count; i += NT) {
+            const T* q = row + part.head + (v0 + i) * kE<T>;
+            const float top = fmaxf(mr, part_max<T>(*reinterpret_cast<const uint4*>(q)));
+            const float b = top == -INFINITY ? 0.f : top;
+            zr *= exp_from(mr, b, a.l);
+#pragma unroll
+            for (int e = 0; e < kE<T>; ++e) zr += exp_from(to_f(q[e]), b, a.l);
+            mr = top;
+        }
+        reduce_held(h, count, mr, zr, a.l);
+    }
+    // every CTA runs: its shared memory may be written
+    if constexpr (S > 1) asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
+    share_parts<NT, S>(parts, rank, h.m, h.z);
+    if (used) {
+        float M, Z;
+        join_parts<kParts>(parts, M, Z, a.l);
+        const float w = weight_of(a);
+        if (out) {
+            const float inv = held_scale(h.m, h.z, w, M, Z, a.l);
+            store_held(h, out + part.head + v0 * kE<T>, count, same_phase(row, (const T*)out), inv, a.l);
+            if (edge >= 0) put(out + edge, inv * Base(h.m, a.l).of(h.xe));
+            for (int32_t i = (int32_t)threadIdx.x + kVecs * NT; i < count; i += NT) {
+                const int32_t c = part.head + (v0 + i) * kE<T>;
+#pragma unroll
+                for (int e = 0; e < kE<T>; ++e)
+                    put(out + c + e, Z == 0.f ? 0.f : w / Z * exp_from(to_f(row[c + e]), M, a.l));
+            }
+        }
+        if (rank == 0 && threadIdx.x < 32) {
+            const float loss = loss_of(a, le, entries, M, Z);
+            if (threadIdx.x == 0) a.loss[r] = loss;
+        }
+        __syncthreads();  // the vectors are stored
+        if (out) put_entries(a, entries, out, part, v0, count, rank, w, M, Z);
+    } else {
+        if (rank == 0 && threadIdx.x == 0) a.loss[r] = 0.f;
+        if (out) zero_row<T, NT>(out, classes, rank, S);
+    }
+    if (!a.total || rank != 0) return;
+    if (threadIdx.x == 0) {
+        __threadfence();
+        if (atomicAdd(a.done, 1) == n - 1) last = true;
+    }
+    __syncthreads();
+    if (last) {
+        __threadfence();
+        put_total<NT>(a, n);
+    }
+}
+
+// Many long rows: the same, with each cluster walking over its rows and the next two
+// rows' slices on their way into shared memory while the current row is worked on.
+constexpr int kStreamVecs = 3400;  // of a CTA's slice: two buffers of it and the entries, two CTAs an SM
+
+template <typename T, int NT, int S>
+__global__ void __launch_bounds__(NT, 1024 / NT) k_distill_stream(Args<T> a, int32_t slots) {
+    extern __shared__ __align__(128) uint8_t dsm[];
+    pdl_start();
+    constexpr int kParts = S * NT / 32;
+    __shared__ __align__(8) float2 parts[2][kParts];  // (m, z) of every warp of the cluster, of used rows in turn
+    __shared__ __align__(8) uint64_t full[2], met[2];  // buffers; parts
+    __shared__ Entries entries[2];                     // of used rows in turn
+    __shared__ bool last;
+    const int32_t rank = (int32_t)(blockIdx.x % S), first = (int32_t)(blockIdx.x / S), step = (int32_t)(gridDim.x / S);
+    const int32_t n = rows_of(a.d_n, a.n_cap), classes = a.classes;
+    if (first >= n) return;  // the whole cluster
+    if (threadIdx.x == 0) {
+        last = false;
+        mbar_init(&full[0], 1);
+        mbar_init(&full[1], 1);
+        mbar_init(&met[0], 1);
+        mbar_init(&met[1], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    __syncthreads();
+    if constexpr (S > 1) cluster_sync();  // every CTA runs: its shared memory may be written
+    const auto has = [&](int32_t r) { return r < n && row_used(a, r); };
+    // copies this CTA's slice of row r into buffer b (thread 0)
+    const auto fetch = [&](int32_t r, bool used, int b) {
+        if (!used) return;
+        const T* row = a.x + (int64_t)r * a.ld;
+        const RowParts<T> part(row, classes);
+        const int32_t per = (part.vecs + S - 1) / S, v0 = min(part.vecs, rank * per);
+        const uint32_t bytes = (uint32_t)(min(part.vecs, v0 + per) - v0) * 16;
+        mbar_expect_tx(&full[b], bytes);
+        if (bytes)
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                    smem_addr(dsm) + (uint32_t)(b * slots) * 16),
+                "l"(row + part.head + (int64_t)v0 * kE<T>), "r"(bytes), "r"(smem_addr(&full[b]))
+                : "memory");
+    };
+    bool u0 = has(first), u1 = has(first + step), u2;
+    if (threadIdx.x == 0) {
+        fetch(first, u0, 0);
+        fetch(first + step, u1, 1);
+    }
+    const float w = weight_of(a);
+    const bool mine = threadIdx.x < 32 && (rank == 0 || a.grad);  // the warp of the entries
+    uint32_t phases = 0;  // bits 0, 1: parity of the next phase of full[0], full[1]; bits 2, 3: of met[0], met[1]
+    int32_t par = 0;      // the row's buffer: alternates over all rows
+    int32_t slot = 0;     // its parts, met and entries: alternate over the used rows only
+    for (int32_t r = first; r < n; r += step, par ^= 1, u0 = u1, u1 = u2) {
+        u2 = has(r + 2 * step);
+        const T* row = a.x + (int64_t)r * a.ld;
+        T* out = a.grad ? a.grad + (int64_t)r * a.ld_grad : nullptr;
+        LaneEntries le;
+        if (mine) load_entries(a, r, row, rank == 0, le);
+        if (!u0) {  // the same in the whole cluster
+            if (rank == 0 && threadIdx.x == 0) a.loss[r] = 0.f;
+            if (out) zero_row<T, NT>(out, classes, rank, S);
+            if (threadIdx.x == 0) fetch(r + 2 * step, u2, par);  // this row's buffer was not filled
+            continue;
+        }
+        const RowParts<T> part(row, classes);
+        const int32_t per = (part.vecs + S - 1) / S, v0 = min(part.vecs, rank * per), count = min(part.vecs, v0 + per) - v0;
+        const int32_t edge = rank == 0 && threadIdx.x < 32 ? part.edge((int)threadIdx.x) : -1;
+        Held<T, NT> h;
+        h.xe = edge >= 0 ? to_f(row[edge]) : -INFINITY;
+        if (mine) share_entries(a, le, entries[slot]);
+        if (!mbar_wait(&full[par], (phases >> par) & 1u) && lane_id() == 0) dev_err(ERR_TIMEOUT);
+        const uint4* buf = reinterpret_cast<const uint4*>(dsm) + par * slots + threadIdx.x;
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k)
+            h.x[k] = (int32_t)threadIdx.x + k * NT < count ? buf[k * NT] : empty_part<T>();
+        reduce_held(h, count, -INFINITY, 0.f, a.l);
+        // The parts meet by asynchronous stores that complete on the receiver's
+        // barrier: a slot is written again two used rows later, by a warp that has
+        // met the used row between, to which every reader of the slot sent its part
+        // after it had read.
+        if (threadIdx.x == 0) mbar_expect_tx(&met[slot], kParts * 8);
+        if (lane_id() < S) {
+            const uint32_t to = smem_addr(&parts[slot][rank * (NT / 32) + (threadIdx.x >> 5)]);
+            asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];\n" ::"r"(
+                             map_rank(to, lane_id())),
+                         "f"(h.m), "f"(h.z), "r"(map_rank(smem_addr(&met[slot]), lane_id()))
+                         : "memory");
+        }
+        __syncwarp();
+        if (!mbar_wait(&met[slot], (phases >> (2 + slot)) & 1u) && lane_id() == 0) dev_err(ERR_TIMEOUT);
+        phases ^= (1u << par) | (4u << slot);
+        // every thread has its vectors in registers: the buffer is free
+        if (threadIdx.x == 0) fetch(r + 2 * step, u2, par);
+        float M, Z;
+        join_parts<kParts>(parts[slot], M, Z, a.l);
+        if (out) {
+            const float inv = held_scale(h.m, h.z, w, M, Z, a.l);
+            store_held(h, out + part.head + v0 * kE<T>, count, same_phase(row, (const T*)out), inv, a.l);
+            if (edge >= 0) put(out + edge, inv * Base(h.m, a.l).of(h.xe));
+        }
+        if (rank == 0 && threadIdx.x < 32) {
+            const float loss = loss_of(a, le, entries[slot], M, Z);
+            if (threadIdx.x == 0) a.loss[r] = loss;
+        }
+        if (out) {
+            // The vectors are stored.  (Entries are written again two used rows later,
+            // after this barrier of the used row between.)
+            __syncthreads();
+            put_entries(a, entries[slot], out, part, v0, count, rank, w, M, Z);
+        }
+        slot ^= 1;
+    }
+    __threadfence();
+    if constexpr (S > 1) cluster_sync();
+    else __syncthreads();
+    if (!a.total) return;
+    if (rank == 0 && threadIdx.x == 0) {
+        __threadfence();
+        last = atomicAdd(a.done, 1) == min(step, n) - 1;
+    }
+    __syncthreads();
+    if (last) {
+        __threadfence();
+        put_total<NT>(a, n);
+    }
+}
+
+// Counts the rows with a teacher, a part of them a block, and clears the count of
+// finished blocks.
+constexpr int kCounts = 256;  // blocks at most
+__global__ void __launch_bounds__(kCountThreads) k_distill_count(const int32_t* __restrict__ ids,
+                                                                 const float* __restrict__ values, int32_t k,
+                                                                 int32_t classes, int32_t n_cap,
+                                                                 const int32_t* __restrict__ d_n,
+                                                                 int32_t* __restrict__ done, float* __restrict__ total) {
+    pdl_start();
+    __shared__ int32_t sh[kCountThreads / 32 + 1];
+    const int32_t n = rows_of(d_n, n_cap), stride = (int32_t)gridDim.x * kCountThreads;
+    int32_t v = 0;
+#pragma unroll 4
+    for (int32_t i = (int32_t)(blockIdx.x * kCountThreads + threadIdx.x); i < n; i += stride)
+        v += is_used(__ldg(ids + (int64_t)i * k), __ldg(values + (int64_t)i * k), classes);
+    v = block_sum<kCountThreads, int32_t>(v, sh);
+    if (threadIdx.x != 0) return;
+    done[1 + blockIdx.x] = v;
+    if (blockIdx.x != 0) return;
+    done[0] = 0;
+    if (total && n == 0) total[0] = 0.f, total[1] = 0.f;  // nobody else writes it
+}
+
+// -------------------------------------------------------------------- host
+template <typename T, int NV>
+sg_status run_warp(const Args<T>& a, cudaStream_t s) {
+    int64_t blocks = cdiv(a.n_cap, kThreads / 32);
+    if (blocks > (int64_t)num_sms() * 3) blocks = (int64_t)num_sms() * 3;
+    SG_CUDA(launch_pdl(k_distill_warp<T, NV>, dim3((unsigned)blocks), dim3(kThreads), 0, s, a));
+    return SG_OK;
+}
+
+template <typename T, int NT, int S>
+sg_status run_row(const Args<T>& a, cudaStream_t s) {
+    SG_CUDA(launch_cluster(k_distill_row<T, NT, S>, (unsigned)((int64_t)a.n_cap * S), NT, S, s, 0, a));
+    return SG_OK;
+}
+
+template <typename T, int NT, int S>
+sg_status run_stream(const Args<T>& a, int64_t nv, cudaStream_t s) {
+    const int32_t slots = (int32_t)cdiv(nv, S);  // of a buffer
+    static OncePerDevice set;
+    SG_CUDA(allow_smem(set, k_distill_stream<T, NT, S>, 2 * kStreamVecs * 16));
+    int64_t clusters = (int64_t)num_sms() * (1024 / NT) / S;
+    if (clusters > a.n_cap) clusters = a.n_cap;
+    SG_CUDA(launch_cluster(k_distill_stream<T, NT, S>, (unsigned)(clusters * S), NT, S, s, 2 * slots * 16, a, slots));
+    return SG_OK;
+}
+
+template <typename T>
+sg_status run(Args<T> a, cudaStream_t s) {
+    a.counts = (int32_t)cdiv(a.n_cap, 2 * kCountThreads);
+    if (a.counts < 1) a.counts = 1;
+    if (a.counts > kCounts) a.counts = kCounts;
+    SG_CUDA(launch_pdl(k_distill_count, dim3((unsigned)a.counts), dim3(kCountThreads), 0, s, a.ids, a.values, a.k, a.classes,
+                       a.n_cap, a.d_n, a.done, a.total));
+    if (a.n_cap == 0) return SG_OK;
+    const int64_t nv = cdiv((int64_t)a.classes, kE<T>);  // vectors of a row, at most
+    if (nv <= 32) return run_warp<T, 1>(a, s);
+    if (nv <= 64) return run_warp<T, 2>(a, s);
+    if (nv <= 128) return run_warp<T, 4>(a, s);
+    if (nv <= 256) return run_warp<T, 8>(a, s);
+    const int wide = nv <= 7 * kThreads ? 1 : nv <= kStreamVecs ? 2 : nv <= 2 * kStreamVecs ? 4 : nv <= 4 * kStreamVecs ? 8 : 16;
+    if (nv <= 8 * kStreamVecs && (int64_t)a.n_cap * wide >= (wide <= 4 ? 6 : 12) * num_sms()) {
+        switch (wide) {
+            case 1: return run_stream<T, kThreads, 1>(a, nv, s);
+            case 2: return run_stream<T, 512, 1>(a, nv, s);
+            case 4: return run_stream<T, 512, 2>(a, nv, s);
+            case 8: return run_stream<T, 512, 4>(a, nv, s);
+            default: return run_stream<T, 512, 8>(a, nv, s);
+        }
+    }
+    // smallest cluster whose registers hold the row, widened while the rows do not
+    // fill the SMs; 512 threads when 8 CTAs of 256 do not hold it
+    if (nv > 8 * kThreads * kVecs) return run_row<T, 512, 8>(a, s);
+    int split = 1;
+    while (split < 8 && nv > (int64_t)split * kThreads * kVecs) split *= 2;
+    while (split < 8 && (int64_t)a.n_cap * split * 2 <= 2 * num_sms() && nv >= split * 2 * kThreads) split *= 2;
+    switch (split) {
+        case 1: return run_row<T, kThreads, 1>(a, s);
+        case 2: return run_row<T, kThreads, 2>(a, s);
+        case 4: return run_row<T, kThreads, 4>(a, s);
+        default: return run_row<T, kThreads, 8>(a, s);
+    }
+}
+
+size_t ws_bytes() { return 2048; }  // (1 + kCounts) counts
+
+}  // namespace
+
+extern "C" size_t sg_distill_workspace(int32_t n_cap, int32_t n_classes) {
+    if (n_cap < 0 || n_classes <= 0) return 0;
+    return ws_bytes();
+}
+
+extern "C" sg_status sg_distill(const void* d_logits, int32_t dtype, int32_t n_cap, const int32_t* d_n, int32_t n_classes,
+                                int64_t ld, const int32_t* d_ids, const float* d_values, int32_t k, float temperature,
+                                int32_t mean, float grad_scale, float* d_loss, float* d_total, void* d_grad,
+                                int64_t ld_grad, void* d_workspace, size_t workspace_bytes, sg_stream_t stream) {
+    if (dtype != SG_F32 && dtype != SG_BF16) return fail(SG_ERR_UNSUPPORTED, "sg_distill: dtype");
+    if (n_cap < 0 || n_cap > 1 << 27 || n_classes <= 0 || n_classes > 2147483647 - 1024)
+        return fail(SG_ERR_INVALID_ARG, "sg_distill: bad sizes");
+    if (k < 1 || k > SG_MAX_TOP) return fail(SG_ERR_INVALID_ARG, "sg_distill: k must be 1 to %d", SG_MAX_TOP);
+    if (!(temperature >= 1e-3f && temperature <= 1e3f))
+        return fail(SG_ERR_INVALID_ARG, "sg_distill: the temperature must be 0.001 to 1000");
+    if (ld < n_classes || (d_grad && ld_grad < n_classes))
+        return fail(SG_ERR_INVALID_ARG, "sg_distill: a row stride is below n_classes");
+    if (n_cap > 0 && (!d_logits || !d_ids || !d_values || !d_loss)) return fail(SG_ERR_INVALID_ARG, "sg_distill: NULL array");
+    if (!d_workspace || (uintptr_t)d_workspace % 256 || workspace_bytes < ws_bytes())
+        return fail(SG_ERR_INVALID_ARG, "sg_distill: workspace needs %zu bytes, 256-byte aligned", ws_bytes());
+    const int e = dtype == SG_F32 ? 4 : 2;
+    if ((uintptr_t)d_logits % e || (uintptr_t)d_grad % e ||
+        ((uintptr_t)d_ids | (uintptr_t)d_values | (uintptr_t)d_loss | (uintptr_t)d_total) % 4)
+        return fail(SG_ERR_INVALID_ARG, "sg_distill: an array is not aligned to its elements");
+    if (d_grad == d_logits && d_grad) return fail(SG_ERR_INVALID_ARG, "sg_distill: the gradient may not replace the logits");
+    cudaStream_t s = (cudaStream_t)stream;
+    const float l = kLog2e / temperature;
+    if (dtype == SG_F32) {
+        const Args<float> a = {(const float*)d_logits, (float*)d_grad, ld, ld_grad, d_ids, d_values, d_n, n_cap, n_classes,
+                               k, mean ? 1 : 0, grad_scale, temperature, l, d_loss, d_total, (int32_t*)d_workspace, 0};
+        return run(a, s);
+    }
+    const Args<__nv_bfloat16> a = {(const __nv_bfloat16*)d_logits, (__nv_bfloat16*)d_grad, ld, ld_grad, d_ids, d_values,
+                                   d_n, n_cap, n_classes, k, mean ? 1 : 0, grad_scale, temperature, l, d_loss, d_total,
+                                   (int32_t*)d_workspace, 0};
+    return run(a, s);
+}

@@ -1,0 +1,555 @@
+// What a model answers: per row of logits x the log probability of a given
+// class, the entropy, and the k most probable classes.  With m = max_c x[c],
+// d_c = m - x[c], z = sum_c exp(-d_c), t = sum_c exp(-d_c) (-d_c):
+//   logp = -d_label - log z,  entropy = log z - t / z,
+//   the k largest by (x descending, class ascending) with their log probabilities.
+// Bound by memory: the logits are read once and next to nothing is written.
+//
+// Rows of a few hundred classes stay in a warp's registers (k_logprobs_warp).
+// Longer ones stream past 256 threads, or a cluster of 2 to 8 such CTAs when rows
+// are few (k_logprobs_row).  Each thread keeps (m, z, t) of what it has seen,
+// relative to its own running maximum, and the maximum of each group of vectors.
+// The k-th largest of some of the threads' maxima is a lower bound of the k-th
+// largest logit, so only groups that reach it are read again (from L2), and only
+// the logits that reach it become candidates: about k of them, whatever the row's
+// length.  Where they are many all the same (equal logits, masks by one value),
+// the bound is raised by bisection, and logits equal to it are taken in order.
+//
+// Logits of -inf take no part.  x - m is formed before the scaling by log2(e), so
+// a row's level costs no accuracy, and exponents are cut off at -200, where the
+// exponential is 0, so that 0 * (-inf) never arises.
+#include "sg_internal.cuh"
+#include "sg_rows.cuh"
+#include "sg_tc.cuh"
+
+SGI_ERROR_WORD(logprobs)
+
+using namespace sgi;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kTurn = 4;      // vectors a thread loads at a time
+constexpr int kGroups = 16;   // groups of a thread's vectors, at most
+constexpr int kCap = 512;     // candidates a CTA holds; at least 4 SG_MAX_TOP for the bound's slack
+constexpr float kNone = -200.f;  // 2^x is 0 from here on
+
+template <typename T>
+struct Args {
+    const T* x;
+    int64_t ld;
+    const int32_t* labels;
+    const int32_t* d_n;
+    int32_t n_cap, classes, k;
+    float* logp;
+    float* entropy;
+    int32_t* top_ids;
+    float* top_logp;
+};
+
+// The larger of two, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Order of values as whole numbers (-0 with 0; no NaN).
+__device__ __forceinline__ uint32_t order_of(float x) {
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+    return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+}
+constexpr uint32_t kOrderNone = 0x007FFFFFu;  // of -inf
+// A candidate: the larger one is the better (larger logit, then lower class).
+__device__ __forceinline__ unsigned long long entry_of(uint32_t order, int32_t c) {
+    return (unsigned long long)order << 32 | (0xFFFFFFFFu - (uint32_t)c);
+}
+__device__ __forceinline__ int32_t class_of(unsigned long long e) { return (int32_t)(0xFFFFFFFFu - (uint32_t)e); }
+
+// z = sum exp(x - m), t = sum exp(x - m) (x - m) log2(e) of a part of a row; m = -inf: nothing yet
+struct Stat {
+    float m, z, t;
+};
+__device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.f : m; }
+// s relative to the maximum m >= s.m
+__device__ __forceinline__ void rebase(Stat& s, float m) {
+    const float a = fmaxf((s.m - finite_base(m)) * kLog2e, kNone), e = ex2(a);
+    s.t = e * fmaf(a, s.z, s.t);
+    s.z *= e;
+    s.m = m;
+}
+__device__ __forceinline__ Stat stat_of(float x) {
+    return {x, x == -INFINITY ? 0.f : 1.f + (x - x), 0.f};  // (NaN and +inf: z = NaN)
+}
+// Adds a vector; s.m is at least its maximum.
+template <typename T>
+__device__ __forceinline__ void add_part(const uint4& u, f2 base, f2& z, f2& t) {
+    f2 p[kE<T> / 2];
+    pairs_of(u, p);
+    const f2 l = pair(kLog2e, kLog2e);
+#pragma unroll
+    for (int i = 0; i < kE<T> / 2; ++i) {
+        float a, c;
+        unpair(mul2(add2(p[i], base), l), a, c);
+        a = max_nan(a, kNone);
+        c = max_nan(c, kNone);
+        const f2 e = pair(ex2(a), ex2(c));
+        z = add2(z, e);
+        t = fma2(e, pair(a, c), t);
+    }
+}
+__device__ __forceinline__ Stat warp_join(Stat s) {
+    rebase(s, warp_max(s.m));
+    s.z = warp_sum(s.z);
+    s.t = warp_sum(s.t);
+    return s;
+}
+__device__ __forceinline__ float logp_of(float x, float m, float log_z) {
+    return (x - finite_base(m)) - log_z;
+}
+
+// The row's label, -1 if there is none.
+template <typename T>
+__device__ __forceinline__ int32_t label_of(const Args<T>& a, int32_t r) {
+    const int32_t y = a.labels ? __ldg(a.labels + r) : -1;
+    if (y >= -1 && y < a.classes) return y;
+    dev_err(ERR_INDEX);
+    return -1;
+}
+
+// One thread: the row's own numbers.
+template <typename T>
+__device__ __forceinline__ void put_row(const Args<T>& a, int32_t r, const Stat& s, float log_z, int32_t y, float xy) {
+    if (a.logp) a.logp[r] = y < 0 ? 0.f : s.z == 0.f ? -INFINITY : logp_of(xy, s.m, log_z);
+    if (a.entropy) a.entropy[r] = s.z == 0.f ? 0.f : log_z - s.t / s.z * 0.69314718055994531f;
+}
+
+// Elements of a vector, one at a time.
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& u, float (&f)[kE<T>]) {
+    f2 p[kE<T> / 2];
+    pairs_of(u, p);
+#pragma unroll
+    for (int i = 0; i < kE<T> / 2; ++i) unpair(p[i], f[2 * i], f[2 * i + 1]);
+}
+
+// ------------------------------------------------------------ rows by warps
+// A warp a row, in NV vectors a lane.  The top classes are taken one by one: each
+// lane offers its best, the warp takes the best of them.
+template <typename T, int NV>
+__global__ void __launch_bounds__(kThreads) k_logprobs_warp(Args<T> a) {
+    pdl_start();
+    const int lane = (int)lane_id();
+    const int32_t n = rows_of(a.d_n, a.n_cap), r = (int32_t)blockIdx.x * kWarps + (int32_t)(threadIdx.x >> 5);
+    if (r >= n) return;
+    const T* row = a.x + (int64_t)r * a.ld;
+    const RowParts<T> part(row, a.classes);
+    uint4 x[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int32_t v = lane + 32 * k;
+        x[k] = v < part.vecs ? *reinterpret_cast<const uint4*>(row + part.head + v * kE<T>) : empty_part<T>();
+    }
+    const int32_t ce = part.edge(lane);
+    const float xe = ce >= 0 ? to_f(row[ce]) : -INFINITY;
+    int32_t y = -1;
+    float xy = 0.f;
+    if (lane == 0) {
+        y = label_of(a, r);
+        if (y >= 0) xy = to_f(row[y]);
+    }
+    Stat s = stat_of(xe);
+    float top = xe;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) top = fmaxf(top, part_max<T>(x[k]));
+    rebase(s, warp_max(top));
+    f2 z = pair(s.z, 0.f), t = pair(s.t, 0.f);
+    const float b = -finite_base(s.m);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) add_part<T>(x[k], pair(b, b), z, t);
+    float z0, z1, t0, t1;
+    unpair(z, z0, z1);
+    unpair(t, t0, t1);
+    s.z = warp_sum(z0 + z1);
+    s.t = warp_sum(t0 + t1);
+    const float log_z = logf(s.z);
+    if (lane == 0) put_row(a, r, s, log_z, y, xy);
+    int32_t* ids = a.top_ids + (int64_t)r * a.k;
+    float* lps = a.top_logp + (int64_t)r * a.k;
+    const bool bad = s.z != s.z;
+    float f[NV][kE<T>];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) unpack<T>(x[k], f[k]);
+    unsigned long long last = ~0ull;  // the entry taken last
+    for (int32_t j = 0; j < a.k; ++j) {
+        unsigned long long best = 0;
+        if (!bad) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int e = 0; e < kE<T>; ++e) {
+                    const unsigned long long q = entry_of(order_of(f[k][e]), part.head + (lane + 32 * k) * kE<T> + e);
+                    if (q < last && q > best) best = q;
+                }
+            const unsigned long long q = entry_of(order_of(xe), ce);
+            if (ce >= 0 && q < last && q > best) best = q;
+        }
+        const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(best >> 32));
+        if (hi <= kOrderNone) {  // nothing is left
+            for (int32_t i = j + lane; i < a.k; i += 32) {
+                ids[i] = -1;
+                lps[i] = bad ? s.z : -INFINITY;
+            }
+            break;
+        }
+        const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+        last = (unsigned long long)hi << 32 | lo;
+        if (lane == 0) {
+            ids[j] = class_of(last);
+            lps[j] = logp_of(value_of(hi), s.m, log_z);
+        }
+    }
+}
+
+// --------------------------------------------------------- rows by clusters
+// The candidates of a CTA's part of a row.
+struct Candidates {
+    unsigned long long e[kCap];
+    int32_t count;
+};
+__device__ __forceinline__ void offer(Candidates& l, float x, int32_t c) {
+    const int32_t at = atomicAdd(&l.count, 1);
+    if (at < kCap) l.e[at] = entry_of(order_of(x), c);
+}
+
+// A CTA's part of a row: vectors v0 .. v0 + count - 1, and for warp 0 of CTA 0 the
+// edge elements.
+template <typename T>
+struct Slice {
+    const T* row;
+    RowParts<T> part;
+    int32_t v0, count, edge;
+    float xe;
+    __device__ __forceinline__ int32_t first(int32_t i) const { return part.head + (v0 + i) * kE<T>; }
+    __device__ __forceinline__ uint4 load(int32_t i) const { return *reinterpret_cast<const uint4*>(row + first(i)); }
+};
+
+// Logits of the slice of order o and above (o above that of -inf), over the block.
+template <typename T>
+__device__ __noinline__ int32_t count_from(const Slice<T>& s, uint32_t o, int32_t* sh) {
+    int32_t c = s.edge >= 0 && order_of(s.xe) >= o;
+    for (int32_t i = threadIdx.x; i < s.count; i += kThreads) {
+        float f[kE<T>];
+        unpack<T>(s.load(i), f);
+#pragma unroll
+        for (int e = 0; e < kE<T>; ++e) c += order_of(f[e]) >= o;
+    }
+    return block_sum<kThreads, int32_t>(c, sh);
+}
+template <typename T>
+__device__ __noinline__ void offer_from(const Slice<T>& s, uint32_t o, Candidates& l) {
+    if (s.edge >= 0 && order_of(s.xe) >= o) offer(l, s.xe, s.edge);
+    for (int32_t i = threadIdx.x; i < s.count; i += kThreads) {
+        float f[kE<T>];
+        unpack<T>(s.load(i), f);
+#pragma unroll
+        for (int e = 0; e < kE<T>; ++e)
+            if (order_of(f[e]) >= o) offer(l, f[e], s.first(i) + e);
+    }
+}
+
+// The slice's k best when more than kCap of its logits have order o and above:
+// l.count is k at the end.  top: an order that none is above.  Each pass reads the
+// slice from L2.
+template <typename T>
+__device__ __noinline__ void select_exactly(const Slice<T>& s, int32_t rank, uint32_t o, uint32_t top, int32_t k,
+                                            Candidates& l, int32_t* sh) {
+    uint32_t lo = o;               // at least k from here on
+    int32_t have = kCap + 1;       // how many (or more)
+    const int32_t above = count_from(s, lo + 1, sh);
+    uint32_t hi = lo + 1;          // fewer than k from here on
+    if (above >= k) {
+        lo = lo + 1;
+        have = above;
+        hi = top + 1;
+        while (have > kCap && hi - lo > 1) {
+            const uint32_t mid = lo + (hi - lo) / 2;
+            const int32_t c = count_from(s, mid, sh);
+            if (c >= k) lo = mid, have = c;
+            else hi = mid;
+        }
+    }
+    if (threadIdx.x == 0) l.count = 0;
+    __syncthreads();
+    if (have <= kCap) {
+        offer_from(s, lo, l);
+        __syncthreads();
+        return;
+    }
+    offer_from(s, lo + 1, l);  // fewer than k
+    __syncthreads();
+    // the others are equal to lo: the lowest classes of them
+    int32_t filled = l.count;
+    __syncthreads();
+    const int32_t begin[2] = {rank == 0 ? 0 : s.first(0), s.part.head + s.part.vecs * kE<T>};
+    const int32_t end[2] = {s.first(s.count), rank == 0 ? s.part.head + s.part.vecs * kE<T> + s.part.tail : begin[1]};
+    for (int p = 0; p < 2; ++p)
+        for (int32_t c0 = begin[p]; c0 < end[p] && filled < k; c0 += kThreads) {
+            const int32_t c = c0 + (int32_t)threadIdx.x;
+            const bool eq = c < end[p] && order_of(to_f(s.row[c])) == lo;
+            int32_t total;
+            const int32_t at = filled + block_excl_scan<kThreads, int32_t>(eq, sh, total);
+            if (eq && at < k) l.e[at] = entry_of(lo, c);
+            filled += total;
+        }
+    if (threadIdx.x == 0) l.count = min(filled, k);
+    __syncthreads();
+}
+
+// Descending over the warp's lanes.
+__device__ __forceinline__ float warp_sort(float x) {
+    const int lane = (int)lane_id();
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+        for (int d = size / 2; d > 0; d /= 2) {
+            const float o = __shfl_xor_sync(0xFFFFFFFFu, x, d);
+            const bool larger = ((lane & d) == 0) == ((lane & size) == 0);  // this lane keeps the larger one
+            x = larger ? fmaxf(x, o) : fminf(x, o);
+        }
+    return x;
+}
+
+template <typename T, int S>
+__global__ void __launch_bounds__(kThreads, 4) k_logprobs_row(Args<T> a, int32_t turns) {
+    extern __shared__ __align__(16) uint8_t dsm[];  // groups' maxima; then all candidates
+    pdl_start();
+    constexpr int W = S * kWarps;
+    __shared__ __align__(16) float4 parts[W];
+    __shared__ float tops[SG_MAX_TOP + W];
+    __shared__ Candidates list;
+    __shared__ float bound;
+    __shared__ int32_t scan[kThreads / 32 + 1];
+    const int warp = (int)(threadIdx.x >> 5), lane = (int)lane_id();
+    const int32_t r = (int32_t)(blockIdx.x / S), rank = (int32_t)(blockIdx.x % S);
+    const int32_t n = rows_of(a.d_n, a.n_cap);
+    if (r >= n) return;  // the whole cluster
+    if constexpr (S > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
+    float* gmax = reinterpret_cast<float*>(dsm) + threadIdx.x;
+    const T* row = a.x + (int64_t)r * a.ld;
+    const RowParts<T> part(row, a.classes);
+    const int32_t per = (part.vecs + S - 1) / S, v0 = min(part.vecs, rank * per);
+    Slice<T> sl = {row, part, v0, min(part.vecs, v0 + per) - v0, rank == 0 && warp == 0 ? part.edge(lane) : -1, -INFINITY};
+    if (sl.edge >= 0) sl.xe = to_f(row[sl.edge]);
+    int32_t y = -1;
+    float xy = 0.f;
+    if (rank == 0 && threadIdx.x == 0) {
+        y = label_of(a, r);
+        if (y >= 0) xy = to_f(row[y]);
+    }
+    Stat s = stat_of(sl.xe);
+    float most = sl.xe;
+    const int32_t span = turns * kTurn * kThreads;  // vectors of a group, over the block
+    for (int32_t g0 = 0, g = 0; g0 < sl.count; g0 += span, ++g) {
+        float gm = -INFINITY;
+        for (int32_t i0 = g0; i0 < min(sl.count, g0 + span); i0 += kTurn * kThreads) {
+            uint4 u[kTurn];
+            float top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kTurn; ++k) {
+                const int32_t i = i0 + k * kThreads + (int32_t)threadIdx.x;
+                u[k] = i < sl.count ? sl.load(i) : empty_part<T>();
+            }
+#pragma unroll
+            for (int k = 0; k < kTurn; ++k) top = fmaxf(top, part_max<T>(u[k]));
+            gm = fmaxf(gm, top);
+            rebase(s, fmaxf(s.m, top));
+            f2 z = pair(s.z, 0.f), t = pair(s.t, 0.f);
+            const float b = -finite_base(s.m);
+#pragma unroll
+            for (int k = 0; k < kTurn; ++k) {
+                repack(u[k]);
+                add_part<T>(u[k], pair(b, b), z, t);
+            }
+            float z1, t1;
+            unpair(z, s.z, z1);
+            unpair(t, s.t, t1);
+            s.z += z1;
+            s.t += t1;
+        }
+        gmax[g * kThreads] = gm;
+        most = fmaxf(most, gm);
+    }
+    s = warp_join(s);
+    // the warp's j largest of its lanes' maxima
+    const int32_t j = (a.k + W - 1) / W, M = W * j;
+    if (j == 1) most = s.m;
+    else if (j > 1) most = warp_sort(most);
+    if constexpr (S > 1) asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");  // every CTA runs
+    const int32_t w = rank * kWarps + warp;
+    if constexpr (S > 1) {
+        if (lane < S)
+            st_cluster4(map_rank(smem_addr(parts + w), (uint32_t)lane),
+                        make_uint4(__float_as_uint(s.m), __float_as_uint(s.z), __float_as_uint(s.t), 0u));
+        if (lane < j)
+            for (uint32_t q = 0; q < S; ++q)
+                asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(map_rank(smem_addr(tops + w * j + lane), q)), "f"(most)
+                             : "memory");
+        cluster_sync();
+    } else {
+        if (lane == 0) parts[w] = make_float4(s.m, s.z, s.t, 0.f);
+        if (lane < j) tops[w * j + lane] = most;
+        __syncthreads();
+    }
+    // the whole row's, in every warp
+    s = {-INFINITY, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < (W + 31) / 32; ++i)
+        if (lane + 32 * i < W) {
+            const float4 p = parts[lane + 32 * i];
+            Stat o = {p.x, p.y, p.z};
+            const float m = fmaxf(s.m, o.m);
+            rebase(s, m);
+            rebase(o, m);
+            s.z += o.z;
+            s.t += o.t;
+        }
+    s = warp_join(s);
+    const float log_z = logf(s.z);
+    if (rank == 0 && threadIdx.x == 0) put_row(a, r, s, log_z, y, xy);
+    if (a.k == 0) return;  // (the last access to another CTA's memory is before the barrier)
+    if ((int32_t)threadIdx.x < M) {  // the k-th largest of tops
+        const float v = tops[threadIdx.x];
+        int32_t before = 0;
+        for (int32_t q = 0; q < M; ++q) before += tops[q] > v || (tops[q] == v && q < (int32_t)threadIdx.x);
+        if (before == a.k - 1) bound = v;
+    }
+    if (threadIdx.x == 0) list.count = 0;
+    __syncthreads();
+    const float tau = bound;
+    const bool bad = s.z != s.z;
+    if (!bad) {
+        if (sl.xe >= tau && sl.xe > -INFINITY) offer(list, sl.xe, sl.edge);
+        for (int32_t g0 = 0, g = 0; g0 < sl.count; g0 += span, ++g) {
+            const float gm = gmax[g * kThreads];
+            if (gm < tau || gm == -INFINITY) continue;
+            for (int32_t i = g0 + (int32_t)threadIdx.x; i < min(sl.count, g0 + span); i += kThreads) {
+                const uint4 u = sl.load(i);
+                if (part_max<T>(u) < tau) continue;
+                float f[kE<T>];
+                unpack<T>(u, f);
+#pragma unroll
+                for (int e = 0; e < kE<T>; ++e)
+                    if (f[e] >= tau && f[e] > -INFINITY) offer(list, f[e], sl.first(i) + e);
+            }
+        }
+    }
+    __syncthreads();
+    if (list.count > kCap)
+        select_exactly(sl, rank, max(order_of(tau), kOrderNone + 1), order_of(s.m), a.k, list, scan);
+    const unsigned long long* all = list.e;
+    int32_t total = list.count;
+    if constexpr (S > 1) {  // CTA 0 takes everybody's
+        cluster_sync();
+        if (rank == 0) {
+            unsigned long long* to = reinterpret_cast<unsigned long long*>(dsm);
+            total = 0;
+            for (uint32_t q = 0; q < S; ++q) {
+                const int32_t c = __float_as_int(ld_cluster(map_rank(smem_addr(&list.count), q)));
+                for (int32_t i = threadIdx.x; i < c; i += kThreads) {
+                    const uint32_t from = map_rank(smem_addr(&list.e[i]), q);
+                    asm volatile("ld.shared::cluster.b64 %0, [%1];\n" : "=l"(to[total + i]) : "r"(from) : "memory");
+                }
+                total += c;
+            }
+            all = to;
+        }
+        cluster_sync();  // the lists stay until they are read
+        if (rank != 0) return;
+    }
+    int32_t* ids = a.top_ids + (int64_t)r * a.k;
+    float* lps = a.top_logp + (int64_t)r * a.k;
+    for (int32_t i = threadIdx.x; i < total; i += kThreads) {
+        const unsigned long long e = all[i];
+        int32_t before = 0;
+        for (int32_t q = 0; q < total; ++q) before += all[q] > e;
+        if (before < a.k) {
+            ids[before] = class_of(e);
+            lps[before] = logp_of(value_of((uint32_t)(e >> 32)), s.m, log_z);
+        }
+    }
+    for (int32_t i = total + (int32_t)threadIdx.x; i < a.k; i += kThreads) {
+        ids[i] = -1;
+        lps[i] = bad ? s.z : -INFINITY;
+    }
+}
+
+// -------------------------------------------------------------------- host
+template <typename T, int NV>
+sg_status run_warp(const Args<T>& a, cudaStream_t s) {
+    SG_CUDA(launch_pdl(k_logprobs_warp<T, NV>, dim3((unsigned)cdiv(a.n_cap, kWarps)), dim3(kThreads), 0, s, a));
+    return SG_OK;
+}
+
+template <typename T, int S>
+sg_status run_row(const Args<T>& a, int64_t nv, cudaStream_t s) {
+    const int64_t per = cdiv(nv, S), all_turns = cdiv(per, kTurn * kThreads);
+    const int64_t turns = all_turns > kGroups ? cdiv(all_turns, kGroups) : 1;
+    int64_t smem = cdiv(all_turns, turns) * kThreads * 4;
+    if (S > 1 && smem < S * kCap * 8) smem = S * kCap * 8;
+    SG_CUDA(launch_cluster(k_logprobs_row<T, S>, (unsigned)((int64_t)a.n_cap * S), kThreads, S, s, (int)smem, a,
+                           (int32_t)turns));
+    return SG_OK;
+}
+
+template <typename T>
+sg_status run(const Args<T>& a, cudaStream_t s) {
+    if (a.n_cap == 0) return SG_OK;
+    const int64_t nv = cdiv((int64_t)a.classes, kE<T>);  // vectors of a row, at most
+    if (nv <= 32) return run_warp<T, 1>(a, s);
+    if (nv <= 64) return run_warp<T, 2>(a, s);
+    if (nv <= 128) return run_warp<T, 4>(a, s);
+    // clusters while the rows leave SMs idle and every CTA has a turn to do
+    int split = 1;
+    while (split < 8 && (int64_t)a.n_cap * split * 2 <= 2 * num_sms() && nv >= split * 2 * kThreads) split *= 2;
+    switch (split) {
+        case 1: return run_row<T, 1>(a, nv, s);
+        case 2: return run_row<T, 2>(a, nv, s);
+        case 4: return run_row<T, 4>(a, nv, s);
+        default: return run_row<T, 8>(a, nv, s);
+    }
+}
+
+}  // namespace
+
+extern "C" sg_status sg_logprobs(const void* d_logits, int32_t dtype, int32_t n_cap, const int32_t* d_n, int32_t n_classes,
+                                 int64_t ld, const int32_t* d_labels, int32_t k, float* d_logp, float* d_entropy,
+                                 int32_t* d_top_ids, float* d_top_logp, sg_stream_t stream) {
+    if (dtype != SG_F32 && dtype != SG_BF16) return fail(SG_ERR_UNSUPPORTED, "sg_logprobs: dtype");
+    if (n_cap < 0 || n_cap > 1 << 27 || n_classes <= 0 || n_classes > 2147483647 - 1024)
+        return fail(SG_ERR_INVALID_ARG, "sg_logprobs: bad sizes");
+    if (k < 0 || k > SG_MAX_TOP) return fail(SG_ERR_INVALID_ARG, "sg_logprobs: k must be 0 to %d", SG_MAX_TOP);
+    if (ld < n_classes) return fail(SG_ERR_INVALID_ARG, "sg_logprobs: the row stride is below n_classes");
+    if (n_cap > 0 && !d_logits) return fail(SG_ERR_INVALID_ARG, "sg_logprobs: NULL logits");
+    if (n_cap > 0 && !d_labels != !d_logp) return fail(SG_ERR_INVALID_ARG, "sg_logprobs: labels and logp come together");
+    if (n_cap > 0 && k > 0 && (!d_top_ids || !d_top_logp))
+        return fail(SG_ERR_INVALID_ARG, "sg_logprobs: k above 0 needs top_ids and top_logp");
+    if (k == 0 && (d_top_ids || d_top_logp)) return fail(SG_ERR_INVALID_ARG, "sg_logprobs: top arrays with k = 0");
+    const int e = dtype == SG_F32 ? 4 : 2;
+    if ((uintptr_t)d_logits % e ||
+        ((uintptr_t)d_labels | (uintptr_t)d_logp | (uintptr_t)d_entropy | (uintptr_t)d_top_ids | (uintptr_t)d_top_logp) % 4)
+        return fail(SG_ERR_INVALID_ARG, "sg_logprobs: an array is not aligned to its elements");
+    cudaStream_t s = (cudaStream_t)stream;
+    if (dtype == SG_F32) {
+        const Args<float> a = {(const float*)d_logits, ld, d_labels, d_n, n_cap, n_classes, k, d_logp, d_entropy, d_top_ids,
+                               d_top_logp};
+        return run(a, s);
+    }
+    const Args<__nv_bfloat16> a = {(const __nv_bfloat16*)d_logits, ld, d_labels, d_n, n_cap, n_classes, k, d_logp,
+                                   d_entropy, d_top_ids, d_top_logp};
+    return run(a, s);
+}

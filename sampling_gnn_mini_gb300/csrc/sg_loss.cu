@@ -23,9 +23,9 @@
 // a part has no finite logit (its exponentials are then 0); x - m is formed
 // before the scaling by log2(e), so rows at a type's lowest value do not
 // overflow and a row's common level costs no accuracy.
-#include <cuda_bf16.h>
-
 #include "sg_internal.cuh"
+#include "sg_rows.cuh"
+#include "sg_softmax.cuh"
 #include "sg_tc.cuh"
 
 SGI_ERROR_WORD(loss)
@@ -36,177 +36,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTotalThreads = 1024;
-constexpr int kVecs = 8;              // 16-byte vectors of a row a thread holds
 constexpr int kSmallCtas = 8;         // the one cluster of a small call
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void put(float* p, float x) { *p = x; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
-
-__device__ __forceinline__ int32_t rows_of(const int32_t* d_n, int32_t n_cap) {
-    return d_n ? min(max(*d_n, 0), n_cap) : n_cap;
-}
-
-// 2^x; the hardware's approximation is within 2^-22 of the value, results
-// below the normal range are 0
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// exp(x - m), m finite
-__device__ __forceinline__ float exp_from(float x, float m) { return ex2((x - m) * kLog2e); }
 
 // (logf, once a row: z is just above 1 in a row that is sure of its label, and the
 // fast logarithm is off by up to 2^-21 there, whatever the loss)
 __device__ __forceinline__ float loss_of(float m, float z, float xy) {
     return xy == -INFINITY && z == z ? INFINITY : logf(z) + (m - xy);
-}
-
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
-    return x;
-}
-
-// --------------------------------------------------- 16-byte parts of a row
-template <typename T>
-constexpr int kE = 16 / (int)sizeof(T);  // elements of a vector
-
-// A row as its elements before the first 16-byte boundary (head), its whole
-// vectors, and its elements after the last of them.  Whole vectors are dealt
-// to threads; the up to 7 + 7 others go to lanes 0.. and 8.. of one warp.
-template <typename T>
-struct RowParts {
-    int32_t head, vecs, tail;
-    __device__ __forceinline__ RowParts(const T* row, int32_t classes) {
-        const int32_t off = (int32_t)(((uintptr_t)row & 15) / sizeof(T));
-        head = off ? min(classes, kE<T> - off) : 0;
-        vecs = (classes - head) / kE<T>;
-        tail = classes - head - vecs * kE<T>;
-    }
-    // element of edge lane l, or -1
-    __device__ __forceinline__ int32_t edge(int l) const {
-        if (l < 8) return l < head ? l : -1;
-        return l - 8 < tail ? head + vecs * kE<T> + l - 8 : -1;
-    }
-    // where element c sits: vector >= 0, or -1 - (edge lane)
-    __device__ __forceinline__ int32_t place(int32_t c) const {
-        if (c < head) return -1 - c;
-        const int32_t v = (c - head) / kE<T>;
-        return v < vecs ? v : -1 - (8 + c - head - vecs * kE<T>);
-    }
-};
-
-template <typename T>
-__device__ __forceinline__ bool same_phase(const T* a, const T* b) {
-    return (((uintptr_t)a ^ (uintptr_t)b) & 15) == 0;
-}
-
-template <typename T>
-__device__ __forceinline__ uint4 empty_part() {
-    const uint32_t w = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;  // -inf
-    return make_uint4(w, w, w, w);
-}
-
-__device__ __forceinline__ void pairs_of(const uint4& u, f2 (&p)[2]) {
-    p[0] = pair(__uint_as_float(u.x), __uint_as_float(u.y));
-    p[1] = pair(__uint_as_float(u.z), __uint_as_float(u.w));
-}
-__device__ __forceinline__ void pairs_of(const uint4& u, f2 (&p)[4]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
-}
-__device__ __forceinline__ uint4 part_of(const f2 (&p)[2]) {
-    float a, b, c, d;
-    unpair(p[0], a, b);
-    unpair(p[1], c, d);
-    return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
-}
-__device__ __forceinline__ uint4 part_of(const f2 (&p)[4]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float a, b;
-        unpair(p[i], a, b);
-        const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
-        w[i] = *reinterpret_cast<const uint32_t*>(&t);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Keeps the compiler from carrying a vector's unpacked elements (twice its
-// registers) from one use to the next: they are unpacked again instead.
-__device__ __forceinline__ void repack(uint4& u) {
-    asm volatile("" : "+r"(u.x), "+r"(u.y), "+r"(u.z), "+r"(u.w));
-}
-
-template <typename T>
-__device__ __forceinline__ float part_max(const uint4& u) {
-    if constexpr (sizeof(T) == 2) {  // pairwise on the packed elements
-        const auto h = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
-        const __nv_bfloat162 m = __hmax2(__hmax2(h(u.x), h(u.y)), __hmax2(h(u.z), h(u.w)));
-        return fmaxf(__low2float(m), __high2float(m));
-    }
-    return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
-}
-
-// exp(x - m) of values and pairs, the difference taken first, as in exp_from():
-// it is exact near m, so the largest logit's exponential is 1 whatever its level.
-// (One fused operation, x log2(e) - m log2(e), leaves the rounding of the second
-// product in every exponential: at |m| = 1e6 they are off by 1.5 %, at 1e10 by
-// more than the type's range.)
-struct Base {
-    f2 l, b;
-    float m;
-    __device__ __forceinline__ explicit Base(float m_) : m(m_) {
-        l = pair(kLog2e, kLog2e);
-        b = pair(-m_, -m_);
-    }
-    __device__ __forceinline__ float of(float x) const { return exp_from(x, m); }
-    __device__ __forceinline__ f2 of(f2 x) const {
-        float a, c;
-        unpair(mul2(add2(x, b), l), a, c);
-        return pair(ex2(a), ex2(c));
-    }
-};
-
-// Adds exp(x - m) to sum; fp32 vectors keep the exponentials in place of x.
-template <typename T>
-__device__ __forceinline__ void part_exp(uint4& u, const Base& m, f2& sum) {
-    f2 p[kE<T> / 2];
-    pairs_of(u, p);
-#pragma unroll
-    for (int i = 0; i < kE<T> / 2; ++i) {
-        p[i] = m.of(p[i]);
-        sum = add2(sum, p[i]);
-    }
-    if constexpr (sizeof(T) == 4) u = part_of(p);
-}
-
-// The gradient (without its -w at the label) of a vector that part_exp saw.
-template <typename T>
-__device__ __forceinline__ uint4 part_grad(const uint4& u, const Base& m, f2 inv) {
-    f2 p[kE<T> / 2];
-    pairs_of(u, p);
-#pragma unroll
-    for (int i = 0; i < kE<T> / 2; ++i) p[i] = mul2(inv, sizeof(T) == 4 ? p[i] : m.of(p[i]));
-    return part_of(p);
-}
-
-// Stores a vector at p; whole: p is on a 16-byte boundary.
-template <typename T>
-__device__ __forceinline__ void store_part(T* p, bool whole, const uint4& u) {
-    if (whole) {
-        *reinterpret_cast<uint4*>(p) = u;
-        return;
-    }
-    const T* e = reinterpret_cast<const T*>(&u);
-#pragma unroll
-    for (int q = 0; q < kE<T>; ++q) p[q] = e[q];
 }
 
 template <typename T>
@@ -310,31 +145,11 @@ __device__ __forceinline__ float warp_rows(const RowArgs<T>& a, int32_t r0, int3
     return loss;
 }
 
-// Sum of the losses in a fixed order, by the last block to finish: 16 bytes and
-// 8 loads a thread at a time (65,536 rows one by one took 35 us).
+// The total, by the last block to finish.
 template <int NT, typename T>
 __device__ __forceinline__ void put_total(const RowArgs<T>& a, int32_t n) {
-    __shared__ float sh[NT / 32];
-    // a row or so before the first 16-byte boundary, whole vectors, the rest
-    const int32_t head = min(n, (int32_t)((4 - ((uintptr_t)a.loss >> 2 & 3)) & 3)), vecs = (n - head) / 4;
-    const float4* v = reinterpret_cast<const float4*>(a.loss + head);
-    float s = 0.f;
-    for (int32_t i0 = threadIdx.x; i0 < vecs; i0 += 8 * NT) {
-        float4 x[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) x[u] = i0 + u * NT < vecs ? __ldcg(v + i0 + u * NT) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) s += (x[u].x + x[u].y) + (x[u].z + x[u].w);
-    }
-    const int32_t rest = n - 4 * vecs, i = (int32_t)threadIdx.x;  // head and tail together
-    if (i < rest) s += __ldcg(a.loss + (i < head ? i : i + 4 * vecs));
-    s = warp_sum(s);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < NT / 32; ++w) s += sh[w];
-        a.total[0] = a.mean ? s / (float)max(1, *a.valid) : s;
-    }
+    const float s = block_sum_fixed<NT>(a.loss, n);
+    if (threadIdx.x == 0) a.total[0] = a.mean ? s / (float)max(1, *a.valid) : s;
 }
 
 // Blocks of k_xent_warp an SM: by the registers of what a lane holds.
@@ -456,112 +271,6 @@ __global__ void __launch_bounds__(kThreads) k_xent_small(RowArgs<T> a) {
 }
 
 // --------------------------------------------------------- rows by clusters
-// What a thread holds of a row: up to kVecs vectors of its CTA's slice, NT
-// apart, and for the lanes of warp 0 of CTA 0 an edge element.
-template <typename T, int NT>
-struct Held {
-    uint4 x[kVecs];
-    float xe;
-    float m, z;  // of this warp: z = sum of exp(x - m)
-};
-
-// (m, z) of the warp from its vectors and, when given, the part (mr, zr) of
-// each thread that is not held.
-template <typename T, int NT>
-__device__ __forceinline__ void reduce_held(Held<T, NT>& h, int32_t count, float mr, float zr) {
-    float m = fmaxf(h.xe, mr);
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k)
-        if ((int32_t)threadIdx.x + k * NT < count) m = fmaxf(m, part_max<T>(h.x[k]));
-    m = warp_max(m);
-    if (m == -INFINITY) m = 0.f;
-    h.m = m;
-    const Base base(m);
-    f2 sum = pair(0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k)
-        if ((int32_t)threadIdx.x + k * NT < count) {
-            repack(h.x[k]);
-            part_exp<T>(h.x[k], base, sum);
-        }
-    float z, z1;
-    unpair(sum, z, z1);
-    z += z1 + base.of(h.xe);
-    if (zr != 0.f) z += zr * exp_from(mr == -INFINITY ? 0.f : mr, m);
-    h.z = warp_sum(z);
-}
-
-// The warps' (m, z) into every CTA of the cluster, and a barrier.
-template <int NT, int S>
-__device__ __forceinline__ void share_parts(float2* parts, int32_t rank, float m, float z) {
-    const int warp = (int)(threadIdx.x >> 5), lane = (int)lane_id();
-    if constexpr (S > 1) {
-        if (lane < S)
-            asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};\n" ::"r"(
-                             map_rank(smem_addr(parts + rank * (NT / 32) + warp), (uint32_t)lane)),
-                         "f"(m), "f"(z)
-                         : "memory");
-        cluster_sync();
-    } else {
-        if (lane == 0) parts[warp] = make_float2(m, z);
-        __syncthreads();
-    }
-}
-
-// The row's (M, Z); parts without a finite logit (z = 0) take no part.
-template <int PARTS>
-__device__ __forceinline__ void join_parts(const float2* parts, float& M, float& Z) {
-    const int lane = (int)lane_id();
-    M = -INFINITY, Z = 0.f;
-#pragma unroll
-    for (int i = lane; i < PARTS; i += 32)
-        if (parts[i].y != 0.f) M = fmaxf(M, parts[i].x);
-    M = warp_max(M);
-    if (M == -INFINITY) M = 0.f;
-#pragma unroll
-    for (int i = lane; i < PARTS; i += 32)
-        if (parts[i].y != 0.f) Z += parts[i].y * exp_from(parts[i].x, M);
-    Z = warp_sum(Z);
-}
-
-// What a warp's exponentials, relative to its own m, are multiplied by in the
-// gradient.  A warp without a finite logit (z = 0; its m says nothing) has
-// exponentials of 0: any finite factor will do, but a row with NaN has NaN there too.
-__device__ __forceinline__ float held_scale(float m, float z, float w, float M, float Z) {
-    if (Z == 0.f) return 0.f;
-    return z == 0.f ? w / Z : w / Z * exp_from(m, M);
-}
-
-// Gradient of what the thread holds; first: the slice's first vector.
-template <typename T, int NT>
-__device__ __forceinline__ void store_held(Held<T, NT>& h, T* first, int32_t count, bool same, float inv) {
-    const Base base(h.m);
-    const f2 inv2 = pair(inv, inv);
-    T* p = first + (int32_t)threadIdx.x * kE<T>;
-    if (same) {
-#pragma unroll
-        for (int k = 0; k < kVecs; ++k)
-            if ((int32_t)threadIdx.x + k * NT < count) {
-                repack(h.x[k]);
-                *reinterpret_cast<uint4*>(p + k * NT * kE<T>) = part_grad<T>(h.x[k], base, inv2);
-            }
-    } else {
-#pragma unroll
-        for (int k = 0; k < kVecs; ++k)
-            if ((int32_t)threadIdx.x + k * NT < count) {
-                repack(h.x[k]);
-                store_part(p + k * NT * kE<T>, false, part_grad<T>(h.x[k], base, inv2));
-            }
-    }
-}
-
-// A zero gradient for this CTA's part of an ignored row.
-template <typename T, int NT>
-__device__ __forceinline__ void zero_row(T* out, int32_t classes, int32_t rank, int32_t ctas) {
-    const int32_t per = (classes + ctas - 1) / ctas, c1 = min(classes, (rank + 1) * per);
-    for (int32_t c = rank * per + (int32_t)threadIdx.x; c < c1; c += NT) put(out + c, 0.f);
-}
-
 template <typename T, int NT, int S>
 __global__ void __launch_bounds__(NT, 1024 / NT) k_xent_row(RowArgs<T> a) {
     pdl_start();
@@ -814,26 +523,6 @@ __global__ void __launch_bounds__(kTotalThreads) k_xent_count(const int32_t* __r
 }
 
 // -------------------------------------------------------------------- host
-template <typename... KArgs, typename... Args>
-cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned threads, unsigned cluster, cudaStream_t s,
-                           int smem, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = cluster;
-    at[1].val.clusterDim.y = 1;
-    at[1].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
-}
-
 template <typename T, int NV, int R>
 sg_status run_warp(const RowArgs<T>& a, bool small, cudaStream_t s) {
     if (small) {
