@@ -7,14 +7,19 @@ GARDEN page; H hops, hidden width 128):
   1. sg_sampler_run, sg_transpose_blocks
   2. sg_embed_fwd     X_H = scale * table[V_H]
   3. h = H .. 1:      M_h = sg_aggregate_fwd(block h, X_h);
-                      Y_h = [X_h | M_h] W_h^T, X_{h-1} = ReLU(Y_h)  (sg_sage_fwd)
+                      Y_h = [X_h | M_h] W_h^T, X_{h-1} = ReLU(Y_h)  (sg_sage_fwd),
+                      with norm=True the layer norm of that for h > 1 (sg_layernorm_fwd)
   4. sg_xent          on the first n_classes columns of Y_1 (no ReLU after the
-                      last layer): the seeds' loss and its gradient
+                      last layer): the seeds' loss and its gradient; with a teacher
+                      a share of sg_distill's
   5. h = 1 .. H:      dW_h, dX (own rows), dM_h  (sg_sage_bwd); the gradient of
                       X_h = the transpose of block h on dM_h (sg_aggregate_bwd_t)
-                      plus dX on the first |V_{h-1}| rows
+                      plus dX on the first |V_{h-1}| rows, taken through the norm
+                      (sg_layernorm_bwd)
   6. sg_muon_step     each W_h;  sg_embed_bwd (SG_GRAD_ADD) the table's rows,
-                      a sparse SGD step
+                      a sparse SGD step; SGD on the norms' weights and biases
+predict() runs 1 to 3 and reads the answers out (sg_logprobs); they can be the
+teacher of another trainer.
 Sizes that depend on the sample stay on the device; a step does not
 synchronise.
 """
@@ -37,7 +42,7 @@ class SageTrainer:
 
     def __init__(self, graph: sg.Graph, dim: int, n_classes: int, fanouts: Sequence[int], n_seeds: int,
                  lr: float = 0.02, lr_table: float = 1.0, momentum: float = 0.95, scale: float = 1.0, seed: int = 0,
-                 device="cuda"):
+                 device="cuda", norm: bool = False, lr_norm: float = 0.02):
         if not 1 <= n_classes <= HIDDEN:
             raise ValueError("SageTrainer: 1 to %d classes" % HIDDEN)
         if n_seeds < 1:
@@ -78,7 +83,19 @@ class SageTrainer:
         self.ones = torch.ones((nb[0], HIDDEN), device=device)  # "pre-activation" of the last layer: nothing is masked
         self.loss = torch.empty(n_seeds, device=device)
         self.total = torch.zeros(2, device=device)
+        # of the hidden states X_h, h = 1 .. H - 1: what is normalised (ReLU(Y_{h+1})), the
+        # rows' mean and 1 / deviation, and {weight, bias} with their gradient
+        self.norm, self.lr_norm = bool(norm) and H > 1, lr_norm
+        hidden = range(1, H) if self.norm else ()
+        self.R = {h: rows(h, HIDDEN) for h in hidden}
+        self.mean = {h: torch.empty(nb[h], device=device) for h in hidden}
+        self.rstd = {h: torch.empty(nb[h], device=device) for h in hidden}
+        self.N = {h: torch.stack([torch.ones(HIDDEN, device=device), torch.zeros(HIDDEN, device=device)]) for h in hidden}
+        self.dN = {h: torch.zeros((2, HIDDEN), device=device) for h in hidden}
+        self.ws_norm = sg.aligned_workspace(max([sg.sg_layernorm_bwd_workspace(nb[h], HIDDEN) for h in hidden] or [0]),
+                                            device)
         self.ws_xent = sg.aligned_workspace(sg.sg_xent_workspace(n_seeds, self.n_classes), device)
+        self.ws_distill = sg.aligned_workspace(sg.sg_distill_workspace(n_seeds, self.n_classes), device)
         self.ws_sage = sg.aligned_workspace(max(sg.sg_sage_bwd_workspace(nb[h - 1], self.dims[h], sg.SG_F32)
                                                 for h in range(1, H + 1)), device)
         self.ws_muon = sg.aligned_workspace(max(sg.sg_orthogonalise_workspace(1, HIDDEN, 2 * self.dims[h])
@@ -98,14 +115,41 @@ class SageTrainer:
         for h in range(H, 0, -1):
             sg.sg_aggregate_fwd(self.buf.indptr[h - 1], self.buf.idx[h - 1], nb[h - 1], nb[h], self.buf.dims(h),
                                 self.X[h], self.M[h])
-            sg.sg_sage_fwd(self.X[h], self.M[h], self.W[h], nb[h - 1], self.count(h - 1), self.X[h - 1], self.Y[h])
+            to = self.R.get(h - 1, self.X[h - 1])
+            sg.sg_sage_fwd(self.X[h], self.M[h], self.W[h], nb[h - 1], self.count(h - 1), to, self.Y[h])
+            if h - 1 in self.R:
+                sg.sg_layernorm_fwd(to, self.N[h - 1][0], self.N[h - 1][1], nb[h - 1], self.count(h - 1), self.X[h - 1],
+                                    self.mean[h - 1], self.rstd[h - 1])
         return self.Y[1][: self.n_seeds, : self.n_classes]
 
-    def backward(self, labels: torch.Tensor, logits: torch.Tensor) -> None:
-        """The loss and every gradient of the batch that forward() ran."""
+    def predict(self, seeds: torch.Tensor, hash_seed: int, k: int = 1, labels: Optional[torch.Tensor] = None):
+        """The answers for n_seeds seeds: their k most probable classes (int32
+        [n_seeds, k], -1 past the number of classes), those classes' log
+        probabilities, each seed's entropy and, with labels, its label's log
+        probability (else None)."""
+        if seeds.numel() != self.n_seeds or (labels is not None and labels.numel() != self.n_seeds):
+            raise ValueError("SageTrainer.predict: expected %d seeds (and labels)" % self.n_seeds)
+        logits, n = self.forward(seeds, hash_seed), self.n_seeds
+        ids = torch.empty((n, k), dtype=torch.int32, device=logits.device)
+        logps, entropy = torch.empty((n, k), device=logits.device), torch.empty(n, device=logits.device)
+        logp = None if labels is None else torch.empty(n, device=logits.device)
+        sg.sg_logprobs(logits, labels, n, None, logp, entropy, ids, logps)
+        return ids, logps, entropy, logp
+
+    def backward(self, labels: torch.Tensor, logits: torch.Tensor, teacher=None, share: float = 0.5,
+                 temperature: float = 2.0) -> None:
+        """The loss and every gradient of the batch that forward() ran; see
+        step() for the teacher."""
         H, nb = self.H, self.nb
-        sg.sg_xent(logits, labels, self.n_seeds, None, self.loss, self.total,
-                   self.G[0][: self.n_seeds, : self.n_classes], self.ws_xent)
+        g = self.G[0][: self.n_seeds, : self.n_classes]
+        own = 1.0 if teacher is None else 1.0 - share
+        sg.sg_xent(logits, labels, self.n_seeds, None, self.loss, self.total, g, self.ws_xent, grad_scale=own)
+        if teacher is not None:
+            taught, total = torch.empty_like(g, memory_format=torch.contiguous_format), torch.empty_like(self.total)
+            sg.sg_distill(logits, teacher[0], teacher[1], self.n_seeds, None, torch.empty_like(self.loss), total, taught,
+                          self.ws_distill, temperature=temperature, grad_scale=share)
+            g += taught
+            self.total[0].mul_(own).add_(total[0], alpha=share)
         sg.sg_transpose_blocks(self.buf, self.tbuf)
         t = self.tbuf
         for h in range(1, H + 1):
@@ -116,25 +160,36 @@ class SageTrainer:
             sg.sg_aggregate_bwd_t(t.tptr[h - 1], t.tdst[h - 1], t.tw[h - 1], nb[h], nb[h - 1], self.buf.dims(h),
                                   self.dM[h], self.G[h])
             self.G[h][: nb[h - 1]] += self.dX[h]
+            if h in self.R:
+                sg.sg_layernorm_bwd(self.G[h], self.R[h], self.N[h][0], self.mean[h], self.rstd[h], nb[h], self.count(h),
+                                    self.G[h], self.dN[h][0], self.dN[h][1], self.ws_norm)
 
     def update(self) -> None:
-        """Muon on the weights, sparse SGD on the table's rows of the batch."""
+        """Muon on the weights, SGD on the norms' weights and biases, sparse SGD
+        on the table's rows of the batch."""
         H = self.H
         for h in range(1, H + 1):
             r, c = self.W[h].shape
             sg.sg_muon_step(self.W[h], self.dW[h], self.m[h], self.W[h], self.m[h], self.ws_muon, lr=self.lr,
                             momentum=self.momentum, scale=math.sqrt(max(1.0, r / c)))
+        for h in self.N:
+            self.N[h].add_(self.dN[h], alpha=-self.lr_norm)
         sg.sg_embed_bwd(self.buf.unique, self.nb[H], self.count(H), self.graph.n_nodes, self.G[H],
                         -self.lr_table * self.scale, self.table, sg.SG_GRAD_ADD, self.ws_embed)
 
-    def step(self, seeds: torch.Tensor, labels: torch.Tensor, hash_seed: int) -> torch.Tensor:
+    def step(self, seeds: torch.Tensor, labels: torch.Tensor, hash_seed: int, teacher=None, share: float = 0.5,
+             temperature: float = 2.0) -> torch.Tensor:
         """One training step on n_seeds distinct seeds (device int32) with
         their labels (-1: none); returns {mean loss, labelled seeds} on the
-        device."""
+        device.  teacher: (classes, values), a teacher's top logits or log
+        probabilities of each seed (as predict() returns them), which then has
+        this share of the loss and its gradient."""
         if seeds.numel() != self.n_seeds or labels.numel() != self.n_seeds:
             raise ValueError("SageTrainer.step: expected %d seeds and labels" % self.n_seeds)
+        if not 0.0 <= share <= 1.0:
+            raise ValueError("SageTrainer.step: the teacher's share must be 0 to 1")
         logits = self.forward(seeds, hash_seed)
-        self.backward(labels, logits)
+        self.backward(labels, logits, teacher, share, temperature)
         self.update()
         return self.total
 
