@@ -11,94 +11,43 @@
 // columns' sums in registers, writes them once to the workspace, and a second kernel
 // adds up the blocks' sums in order: no float atomics, the same bits on every run.
 //
-// Values move in units of up to 16 bytes, the largest that every array and row
-// stride is a multiple of (odd widths in bf16: single values).
+// Values move in vectors of 16 bytes at any alignment of the rows: the up to 7 + 7
+// values before a row's first 16-byte boundary and after its last one go to the
+// group's first lanes, one each.  A group meets only rows that start at the same place
+// within 16 bytes (rows a multiple of 8 apart), so a thread's columns stay the same.
+// Arrays whose rows do not start alike are moved value by value.  30,011 x 1001 bf16
+// forward: SPEED_ODD us, all in single values 50.
 #include "sg_internal.cuh"
 #include "sg_rows.cuh"
+#include "sg_tc.cuh"
+
+SGI_ERROR_WORD(norm)
 
 using namespace sgi;
 
 namespace {
 
 constexpr int kHeld = 16;      // values of a row a thread holds
-constexpr int kThreads = 256;  // of a block of warps' rows
-
-// ------------------------------------------------- N values in one access
-template <int BYTES>
-struct Raw;
-template <>
-struct Raw<16> {
-    typedef uint4 type;
-};
-template <>
-struct Raw<8> {
-    typedef uint2 type;
-};
-template <>
-struct Raw<4> {
-    typedef uint32_t type;
-};
-template <>
-struct Raw<2> {
-    typedef uint16_t type;
-};
-template <typename T, int N>
-using raw_t = typename Raw<N * (int)sizeof(T)>::type;
-
-template <typename T, int N>
-__device__ __forceinline__ void values_of(const raw_t<T, N>& u, float (&f)[N]) {
-    const T* e = reinterpret_cast<const T*>(&u);
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = to_f(e[i]);
-}
-template <typename T, int N>
-__device__ __forceinline__ raw_t<T, N> raw_of(const float (&f)[N]) {
-    raw_t<T, N> u;
-    T* e = reinterpret_cast<T*>(&u);
-#pragma unroll
-    for (int i = 0; i < N; ++i) put(e + i, f[i]);
-    return u;
-}
-// N values of a weight or bias at column c (fp32 or bf16; none: `none`)
-template <int N>
-__device__ __forceinline__ void load_param(const void* w, int32_t bf16, int32_t c, float none, float (&f)[N]) {
-    if (!w) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) f[i] = none;
-    } else if (bf16) {
-        values_of<__nv_bfloat16, N>(__ldg(reinterpret_cast<const raw_t<__nv_bfloat16, N>*>((const __nv_bfloat16*)w + c)), f);
-    } else {
-        constexpr int M = N < 4 ? N : 4;
-#pragma unroll
-        for (int k = 0; k < N; k += M) {
-            float t[M];
-            values_of<float, M>(__ldg(reinterpret_cast<const raw_t<float, M>*>((const float*)w + c + k)), t);
-#pragma unroll
-            for (int i = 0; i < M; ++i) f[k + i] = t[i];
-        }
-    }
-}
+constexpr int kThreads = 256;  // of a block of groups' rows
 
 // -------------------------------------------------------- sums over a group
 // Sums of C values over the L threads that share a row, in every one of them.
 // L > 32: the whole block; sh holds two sets of warps' sums, used in turn (a set is
 // written again after the barrier of the other one, which follows its last reading).
 template <int L, int C>
-struct GroupSum {
-    __device__ __forceinline__ static void of(float (&x)[C], float*, int&) {
+__device__ __forceinline__ void lane_sum(float (&x)[C]) {
 #pragma unroll
-        for (int d = L / 2; d > 0; d >>= 1)
+    for (int d = L / 2; d > 0; d >>= 1)
 #pragma unroll
-            for (int c = 0; c < C; ++c) x[c] += __shfl_xor_sync(0xFFFFFFFFu, x[c], d);
-    }
-};
+        for (int c = 0; c < C; ++c) x[c] += __shfl_xor_sync(0xFFFFFFFFu, x[c], d);
+}
 template <int L, int C>
 __device__ __forceinline__ void group_sum(float (&x)[C], float* sh, int& turn) {
     if constexpr (L <= 32) {
-        GroupSum<L, C>::of(x, sh, turn);
+        lane_sum<L, C>(x);
     } else {
         constexpr int W = L / 32;
-        GroupSum<32, C>::of(x, sh, turn);
+        lane_sum<32, C>(x);
         float* to = sh + turn * 2 * W;
         turn ^= 1;
         if (lane_id() == 0)
@@ -106,14 +55,104 @@ __device__ __forceinline__ void group_sum(float (&x)[C], float* sh, int& turn) {
             for (int c = 0; c < C; ++c) to[c * W + (threadIdx.x >> 5)] = x[c];
         __syncthreads();
 #pragma unroll
-        for (int c = 0; c < C; ++c) x[c] = (int)lane_id() < W ? to[c * W + lane_id()] : 0.f;
-        GroupSum<(W < 32 ? W : 32), C>::of(x, sh, turn);
-        if constexpr (W < 32) {
-#pragma unroll
-            for (int c = 0; c < C; ++c) x[c] = __shfl_sync(0xFFFFFFFFu, x[c], 0);
-        }
+        for (int c = 0; c < C; ++c) x[c] = to[c * W + (int)lane_id() % W];
+        lane_sum<W, C>(x);
     }
 }
+
+// ------------------------------------------------- a thread's part of a row
+// A vector's values one by one, in a loop that takes few registers.
+__device__ __forceinline__ void push_front(uint4& v, float x) { v = make_uint4(__float_as_uint(x), v.x, v.y, v.z); }
+__device__ __forceinline__ void push_front(uint4& v, __nv_bfloat16 x) {
+    v = make_uint4((uint32_t)__bfloat16_as_ushort(x) | v.x << 16, __funnelshift_l(v.x, v.y, 16), __funnelshift_l(v.y, v.z, 16),
+                   __funnelshift_l(v.z, v.w, 16));
+}
+__device__ __forceinline__ void pop_front(uint4& v, float& x) {
+    x = __uint_as_float(v.x);
+    v = make_uint4(v.y, v.z, v.w, 0);
+}
+__device__ __forceinline__ void pop_front(uint4& v, __nv_bfloat16& x) {
+    x = __ushort_as_bfloat16((unsigned short)v.x);
+    v = make_uint4(__funnelshift_r(v.x, v.y, 16), __funnelshift_r(v.y, v.z, 16), __funnelshift_r(v.z, v.w, 16), v.w >> 16);
+}
+
+// What thread l of a group of L holds of each of its rows: vectors l, l + L, .. (V of
+// them at most) and ends l, l + L, .. (of 16: 8 lanes for the head, 8 for the tail).
+// alike: every array's rows start at the same place within 16 bytes; if not, all
+// vectors are moved by values and the ends are the tail's.
+template <typename T, int V, int L>
+struct Part {
+    static constexpr int P = kE<T> / 2;                // pairs of a vector
+    static constexpr int NE = L >= 16 ? 1 : 16 / L;    // ends of a thread
+    int32_t head, vecs, l;
+    int32_t ends[NE];  // columns, or -1
+    bool alike;
+    // rows of x from r on, 8 apart
+    __device__ __forceinline__ Part(const T* x, int64_t ld, int64_t r, int32_t dim, bool alike_)
+        : l((int)threadIdx.x % L), alike(alike_) {
+        const RowParts<T> part(alike ? x + r * ld : (const T*)nullptr, dim);
+        head = part.head;
+        vecs = part.vecs;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) ends[e] = l + e * L < 16 ? part.edge(l + e * L) : -1;
+    }
+    __device__ __forceinline__ bool has(int v) const { return l + v * L < vecs; }
+    __device__ __forceinline__ int32_t column(int v) const { return head + (l + v * L) * kE<T>; }
+    __device__ __forceinline__ uint4 load(const T* row, int v) const {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (!has(v)) return u;
+        const T* p = row + column(v);
+        if (alike) return *reinterpret_cast<const uint4*>(p);
+#pragma unroll 1
+        for (int i = kE<T> - 1; i >= 0; --i) push_front(u, p[i]);
+        return u;
+    }
+    __device__ __forceinline__ float load_end(const T* row, int e) const { return ends[e] >= 0 ? to_f(row[ends[e]]) : 0.f; }
+    __device__ __forceinline__ void store(T* row, int v, const f2 (&f)[P]) const {
+        if (!has(v)) return;
+        T* p = row + column(v);
+        uint4 u = part_of(f);
+        if (alike) {
+            *reinterpret_cast<uint4*>(p) = u;
+            return;
+        }
+#pragma unroll 1
+        for (int i = 0; i < kE<T>; ++i) {
+            T x;
+            pop_front(u, x);
+            p[i] = x;
+        }
+    }
+    __device__ __forceinline__ void store_end(T* row, int e, float x) const {
+        if (ends[e] >= 0) put(row + ends[e], x);
+    }
+};
+// A weight or bias (fp32 or bf16; none: `none`); 0 where the thread has no value
+__device__ __forceinline__ float param_at(const void* w, int32_t bf16, int32_t c, float none) {
+    return !w ? none : bf16 ? to_f(((const __nv_bfloat16*)w)[c]) : __ldg((const float*)w + c);
+}
+template <typename T, int V, int L>
+struct Param {
+    f2 f[V][kE<T> / 2];
+    float end[Part<T, V, L>::NE];
+    __device__ __forceinline__ Param(const Part<T, V, L>& p, const void* w, int32_t bf16, float none) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < kE<T> / 2; ++i) {
+                const int32_t c = p.column(v) + 2 * i;
+                f[v][i] = p.has(v) ? pair(param_at(w, bf16, c, none), param_at(w, bf16, c + 1, none)) : pair(0.f, 0.f);
+            }
+#pragma unroll
+        for (int e = 0; e < Part<T, V, L>::NE; ++e) end[e] = p.ends[e] >= 0 ? param_at(w, bf16, p.ends[e], none) : 0.f;
+    }
+};
+__device__ __forceinline__ float total_of(f2 a) {
+    float x, y;
+    unpair(a, x, y);
+    return x + y;
+}
+__device__ __forceinline__ f2 both(float x) { return pair(x, x); }
 
 // ----------------------------------------------------------------- forward
 template <typename T>
@@ -124,73 +163,106 @@ struct FwdArgs {
     const void* weight;
     const void* bias;
     const int32_t* d_n;
-    int32_t n_cap, dim, w_bf16;
+    int32_t n_cap, dim, w_bf16, alike;
     float eps;
     float* mean;
     float* rstd;
 };
 
-// R rows a group at once, their loads in flight together.
-template <typename T, int N, int V, int L, int NT, int R>
-__global__ void __launch_bounds__(NT) k_norm_fwd(FwdArgs<T> a) {
+// One row, from its vectors (get(v)) and ends; held(): called when all are in registers.
+template <typename T, int V, int L, typename Get, typename Held>
+__device__ __forceinline__ void norm_row(const FwdArgs<T>& a, const Part<T, V, L>& p, const Param<T, V, L>& w,
+                                         const Param<T, V, L>& b, int64_t r, int32_t n, float inv, float* sh, int& turn,
+                                         const float (&ends)[Part<T, V, L>::NE], Get get, Held held) {
+    constexpr int P = kE<T> / 2, NE = Part<T, V, L>::NE;
+    f2 f[V][P], t = both(0.f);
+    float fe[NE], s[1] = {0.f};
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        pairs_of(get(v), f[v]);
+#pragma unroll
+        for (int i = 0; i < P; ++i) t = add2(t, f[v][i]);
+    }
+#pragma unroll
+    for (int e = 0; e < NE; ++e) s[0] += fe[e] = ends[e];
+    s[0] += total_of(t);
+    group_sum<L, 1>(s, sh, turn);
+    held();
+    const float mu = s[0] * inv;
+    t = both(0.f);
+    s[0] = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        if (p.has(v)) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                f[v][i] = add2(f[v][i], both(-mu));
+                t = fma2(f[v][i], f[v][i], t);
+            }
+        }
+#pragma unroll
+    for (int e = 0; e < NE; ++e)
+        if (p.ends[e] >= 0) {
+            fe[e] -= mu;
+            s[0] = fmaf(fe[e], fe[e], s[0]);
+        }
+    s[0] += total_of(t);
+    group_sum<L, 1>(s, sh, turn);
+    const float rs = rsqrtf(fmaf(s[0], inv, a.eps));
+    if (r >= n) return;
+    if (p.l == 0) {
+        if (a.mean) a.mean[r] = mu;
+        if (a.rstd) a.rstd[r] = rs;
+    }
+    T* to = a.y + r * a.ld_y;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) f[v][i] = fma2(mul2(f[v][i], both(rs)), w.f[v][i], b.f[v][i]);
+        p.store(to, v, f[v]);
+    }
+#pragma unroll
+    for (int e = 0; e < NE; ++e) p.store_end(to, e, fmaf(fe[e] * rs, w.end[e], b.end[e]));
+}
+
+// Blocks walk over their rows, R rows a group at once, with the next rows' values on
+// their way into registers.
+template <typename T, int V, int L, int NT, int R>
+__global__ void __launch_bounds__(NT, NT == kThreads ? 4 : 1) k_norm_fwd(FwdArgs<T> a) {
     pdl_start();
     constexpr int kRows = L <= 32 ? NT / L : 1;  // of a block at once
+    constexpr int NE = Part<T, V, L>::NE;
     __shared__ float sh[L > 32 ? 4 * (L / 32) : 1];
     int turn = 0;
-    const int32_t n = rows_of(a.d_n, a.n_cap), units = a.dim / N;
-    const int l = (int)threadIdx.x % L;
-    const int64_t r0 = (int64_t)blockIdx.x * (kRows * R) + (int)threadIdx.x / L;
-    if ((int64_t)blockIdx.x * (kRows * R) >= n) return;
-    raw_t<T, N> x[R][V];
+    const int32_t n = rows_of(a.d_n, a.n_cap);
+    const int64_t step = (int64_t)gridDim.x * (kRows * R);
+    int64_t b0 = (int64_t)blockIdx.x * (kRows * R);
+    if (b0 >= n) return;
+    const Part<T, V, L> p(a.x, a.ld, b0 + (int)threadIdx.x / L, a.dim, a.alike != 0);
+    const Param<T, V, L> w(p, a.weight, a.w_bf16, 1.f), b(p, a.bias, a.w_bf16, 0.f);
+    struct Rows {
+        uint4 x[R][V];
+        float ends[R][NE];
+    } next;
+    const auto load = [&](int64_t b1, Rows& o) {
 #pragma unroll
-    for (int q = 0; q < R; ++q)
+        for (int q = 0; q < R; ++q) {
+            const int64_t r = b1 + q * kRows + (int)threadIdx.x / L;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int32_t u = l + v * L;
-            const int64_t r = r0 + q * kRows;
-            if (r < n && u < units) x[q][v] = *reinterpret_cast<const raw_t<T, N>*>(a.x + r * a.ld + u * N);
-            else x[q][v] = raw_t<T, N>{};
+            for (int v = 0; v < V; ++v) o.x[q][v] = r < n ? p.load(a.x + r * a.ld, v) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < NE; ++e) o.ends[q][e] = r < n ? p.load_end(a.x + r * a.ld, e) : 0.f;
         }
+    };
     const float inv = 1.f / (float)a.dim;
+    load(b0, next);
+    for (; b0 < n; b0 += step) {  // the same in the whole block
+        const Rows cur = next;
+        load(b0 + step, next);
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
-        const int64_t r = r0 + q * kRows;
-        float f[V][N], s[1] = {0.f};
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            values_of<T, N>(x[q][v], f[v]);
-#pragma unroll
-            for (int i = 0; i < N; ++i) s[0] += f[v][i];
-        }
-        group_sum<L, 1>(s, sh, turn);
-        const float mu = s[0] * inv;
-        s[0] = 0.f;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (l + v * L < units)
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    f[v][i] -= mu;
-                    s[0] = fmaf(f[v][i], f[v][i], s[0]);
-                }
-        group_sum<L, 1>(s, sh, turn);
-        const float rs = __frsqrt_rn(fmaf(s[0], inv, a.eps));
-        if (r >= n) continue;
-        if (l == 0) {
-            if (a.mean) a.mean[r] = mu;
-            if (a.rstd) a.rstd[r] = rs;
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int32_t u = l + v * L;
-            if (u >= units) continue;
-            float w[N], b[N];
-            load_param<N>(a.weight, a.w_bf16, u * N, 1.f, w);
-            load_param<N>(a.bias, a.w_bf16, u * N, 0.f, b);
-#pragma unroll
-            for (int i = 0; i < N; ++i) f[v][i] = fmaf(f[v][i] * rs, w[i], b[i]);
-            *reinterpret_cast<raw_t<T, N>*>(a.y + r * a.ld_y + u * N) = raw_of<T, N>(f[v]);
-        }
+        for (int q = 0; q < R; ++q)
+            norm_row<T, V, L>(a, p, w, b, b0 + q * kRows + (int)threadIdx.x / L, n, inv, sh, turn, cur.ends[q],
+                              [&](int v) { return cur.x[q][v]; }, [] {});
     }
 }
 
@@ -205,110 +277,285 @@ struct BwdArgs {
     const float* mean;
     const float* rstd;
     const int32_t* d_n;
-    int32_t n_cap, dim, w_bf16;
+    int32_t n_cap, dim, w_bf16, alike;
     float* parts;  // per block: sums of g h by column, then of g; NULL: not wanted
 };
 
-template <typename T, int N, int V, int L, int NT, int R>
-__global__ void __launch_bounds__(NT) k_norm_bwd(BwdArgs<T> a) {
-    pdl_start();
-    constexpr int kRows = L <= 32 ? NT / L : 1;
-    __shared__ float sh[L > 32 ? 4 * (L / 32) : 1];
-    __shared__ float cols[L > 32 ? 1 : NT * V * N];  // the warps' sums of a column
-    int turn = 0;
-    const int32_t n = rows_of(a.d_n, a.n_cap), units = a.dim / N;
-    const int l = (int)threadIdx.x % L;
-    float sw[V][N], sb[V][N], w[V][N];
+// A thread's columns' sums over its rows.
+template <typename T, int V, int L>
+struct Sums {
+    f2 w[V][kE<T> / 2], b[V][kE<T> / 2];
+    float we[Part<T, V, L>::NE], be[Part<T, V, L>::NE];
+    __device__ __forceinline__ Sums() {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < kE<T> / 2; ++i) w[v][i] = b[v][i] = both(0.f);
+#pragma unroll
+        for (int e = 0; e < Part<T, V, L>::NE; ++e) we[e] = be[e] = 0.f;
+    }
+    // one of the two into o
+    __device__ __forceinline__ void put(const Part<T, V, L>& p, bool bias, float* o) const {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (p.has(v))
+#pragma unroll
+                for (int i = 0; i < kE<T> / 2; ++i) unpair(bias ? b[v][i] : w[v][i], o[p.column(v) + 2 * i], o[p.column(v) + 2 * i + 1]);
+#pragma unroll
+        for (int e = 0; e < Part<T, V, L>::NE; ++e)
+            if (p.ends[e] >= 0) o[p.ends[e]] = bias ? be[e] : we[e];
+    }
+};
+
+// One row: the columns' sums and dx.  The row's values are asked for twice (x(v), g(v)
+// and the ends): held over the sums they would take the registers of half the threads.
+// between(): called when the group's sums are there.
+template <typename T, int V, int L, typename GetX, typename GetG, typename Between>
+__device__ __forceinline__ void grad_row(const BwdArgs<T>& a, const Part<T, V, L>& p, const Param<T, V, L>& w,
+                                         Sums<T, V, L>& sums, int64_t r, int32_t n, float inv, float* sh, int& turn,
+                                         float mean, float rstd, const float (&xe)[Part<T, V, L>::NE],
+                                         const float (&ge)[Part<T, V, L>::NE], GetX x, GetG g, Between between) {
+    constexpr int P = kE<T> / 2, NE = Part<T, V, L>::NE;
+    const f2 mu = both(-mean), rs = both(rstd);
+    f2 t0 = both(0.f), t1 = both(0.f);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
+        f2 h[P], f[P];
+        pairs_of(x(v), h);
+        pairs_of(g(v), f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) sw[v][i] = 0.f, sb[v][i] = 0.f, w[v][i] = 0.f;
-        if (l + v * L < units) load_param<N>(a.weight, a.w_bf16, (l + v * L) * N, 1.f, w[v]);
+        for (int i = 0; i < P; ++i) {  // (a vector that is not there: g = 0, w = 0)
+            h[i] = mul2(add2(h[i], mu), rs);
+            sums.w[v][i] = fma2(f[i], h[i], sums.w[v][i]);
+            sums.b[v][i] = add2(sums.b[v][i], f[i]);
+            f[i] = mul2(f[i], w.f[v][i]);
+            t0 = add2(t0, f[i]);
+            t1 = fma2(f[i], h[i], t1);
+        }
     }
-    const float inv = 1.f / (float)a.dim;
+    float s[2] = {total_of(t0), total_of(t1)}, he[NE];
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+        he[e] = (xe[e] - mean) * rstd;
+        sums.we[e] = fmaf(ge[e], he[e], sums.we[e]);
+        sums.be[e] += ge[e];
+        s[0] = fmaf(ge[e], w.end[e], s[0]);
+        s[1] = fmaf(ge[e] * w.end[e], he[e], s[1]);
+    }
+    group_sum<L, 2>(s, sh, turn);
+    between();
+    if (r >= n) return;
+    const float mg = -s[0] * inv, mh = -s[1] * inv;
+    T* to = a.dx + r * a.ld_dx;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        f2 h[P], f[P];
+        pairs_of(x(v), h);
+        pairs_of(g(v), f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            h[i] = mul2(add2(h[i], mu), rs);
+            f[i] = mul2(add2(mul2(f[i], w.f[v][i]), fma2(h[i], both(mh), both(mg))), rs);
+        }
+        p.store(to, v, f);
+    }
+#pragma unroll
+    for (int e = 0; e < NE; ++e) p.store_end(to, e, rstd * (ge[e] * w.end[e] + fmaf(he[e], mh, mg)));
+}
+
+// Blocks an SM: bf16 vectors hold twice the values.
+template <typename T, int NT>
+constexpr int kBwdBlocks = NT == kThreads ? (sizeof(T) == 2 ? 2 : 3) : 1;
+
+template <typename T, int V, int L, int NT, int R>
+__global__ void __launch_bounds__(NT, kBwdBlocks<T, NT>) k_norm_bwd(BwdArgs<T> a) {
+    pdl_start();
+    constexpr int kRows = L <= 32 ? NT / L : 1;
+    constexpr int NE = Part<T, V, L>::NE;
+    __shared__ float sh[L > 32 ? 4 * (L / 32) : 1];
+    __shared__ float cols[L > 32 ? 1 : NT * (V * kE<T> + (16 + L - 1) / L)];  // the groups' sums of a column
+    int turn = 0;
+    const int32_t n = rows_of(a.d_n, a.n_cap);
     const int64_t step = (int64_t)gridDim.x * (kRows * R);
-    for (int64_t b0 = (int64_t)blockIdx.x * (kRows * R); b0 < n; b0 += step) {  // the same in the whole block
-        const int64_t r0 = b0 + (int)threadIdx.x / L;
-        raw_t<T, N> x[R][V], g[R][V];
+    int64_t b0 = (int64_t)blockIdx.x * (kRows * R);
+    const Part<T, V, L> p(a.x, a.ld, b0 + (int)threadIdx.x / L, a.dim, a.alike != 0);
+    const Param<T, V, L> w(p, a.weight, a.w_bf16, 1.f);
+    Sums<T, V, L> sums;
+    struct Rows {
+        uint4 x[R][V], g[R][V];
+        float xe[R][NE], ge[R][NE];
         float mu[R], rs[R];
+    } next;
+    const auto load = [&](int64_t b1, Rows& o) {
 #pragma unroll
         for (int q = 0; q < R; ++q) {
-            const int64_t r = r0 + q * kRows;
-            mu[q] = r < n ? __ldg(a.mean + r) : 0.f;
-            rs[q] = r < n ? __ldg(a.rstd + r) : 0.f;
+            const int64_t r = b1 + q * kRows + (int)threadIdx.x / L;
+            o.mu[q] = r < n ? __ldg(a.mean + r) : 0.f;
+            o.rs[q] = r < n ? __ldg(a.rstd + r) : 0.f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const int32_t u = l + v * L;
-                x[q][v] = raw_t<T, N>{};
-                g[q][v] = raw_t<T, N>{};
-                if (r < n && u < units) {
-                    x[q][v] = *reinterpret_cast<const raw_t<T, N>*>(a.x + r * a.ld + u * N);
-                    g[q][v] = *reinterpret_cast<const raw_t<T, N>*>(a.g + r * a.ld_g + u * N);
-                }
+                o.x[q][v] = r < n ? p.load(a.x + r * a.ld, v) : make_uint4(0, 0, 0, 0);
+                o.g[q][v] = r < n ? p.load(a.g + r * a.ld_g, v) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int e = 0; e < NE; ++e) {
+                o.xe[q][e] = r < n ? p.load_end(a.x + r * a.ld, e) : 0.f;
+                o.ge[q][e] = r < n ? p.load_end(a.g + r * a.ld_g, e) : 0.f;
             }
         }
+    };
+    const float inv = 1.f / (float)a.dim;
+    load(b0, next);
+    for (; b0 < n; b0 += step) {  // the same in the whole block
+        Rows cur = next;
+        load(b0 + step, next);
 #pragma unroll
-        for (int q = 0; q < R; ++q) {
-            const int64_t r = r0 + q * kRows;
-            float h[V][N], f[V][N], s[2] = {0.f, 0.f};
+        for (int q = 0; q < R; ++q)
+            grad_row<T, V, L>(
+                a, p, w, sums, b0 + q * kRows + (int)threadIdx.x / L, n, inv, sh, turn, cur.mu[q], cur.rs[q], cur.xe[q], cur.ge[q],
+                [&](int v) { return cur.x[q][v]; }, [&](int v) { return cur.g[q][v]; },
+                [&] {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                values_of<T, N>(x[q][v], h[v]);
-                values_of<T, N>(g[q][v], f[v]);
-#pragma unroll
-                for (int i = 0; i < N; ++i) {  // (values past the row's end: g = 0, w = 0)
-                    h[v][i] = (h[v][i] - mu[q]) * rs[q];
-                    sw[v][i] = fmaf(f[v][i], h[v][i], sw[v][i]);
-                    sb[v][i] += f[v][i];
-                    f[v][i] *= w[v][i];
-                    s[0] += f[v][i];
-                    s[1] = fmaf(f[v][i], h[v][i], s[1]);
-                }
-            }
-            group_sum<L, 2>(s, sh, turn);
-            if (r >= n) continue;
-            const float mg = s[0] * inv, mh = s[1] * inv;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int32_t u = l + v * L;
-                if (u >= units) continue;
-#pragma unroll
-                for (int i = 0; i < N; ++i) f[v][i] = rs[q] * (f[v][i] - fmaf(h[v][i], mh, mg));
-                *reinterpret_cast<raw_t<T, N>*>(a.dx + r * a.ld_dx + u * N) = raw_of<T, N>(f[v]);
-            }
-        }
+                    for (int v = 0; v < V; ++v) {
+                        repack(cur.x[q][v]);
+                        repack(cur.g[q][v]);
+                    }
+                });
     }
     if (!a.parts) return;
     float* to = a.parts + (int64_t)blockIdx.x * 2 * a.dim;
     if constexpr (L > 32) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int32_t u = l + v * L;
-            if (u >= units) continue;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                to[u * N + i] = sw[v][i];
-                to[a.dim + u * N + i] = sb[v][i];
-            }
-        }
+        sums.put(p, false, to);
+        sums.put(p, true, to + a.dim);
     } else {
-        constexpr int W = L * V * N;  // columns of a group
-        for (int p = 0; p < 2; ++p) {
+        constexpr int W = L * V * kE<T> + 16;  // columns of a group
+        for (int k = 0; k < 2; ++k) {
             __syncthreads();
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    cols[((int)threadIdx.x / L) * W + (l + v * L) * N + i] = p ? sb[v][i] : sw[v][i];
+            sums.put(p, k != 0, cols + ((int)threadIdx.x / L) * W);
             __syncthreads();
             for (int c = threadIdx.x; c < a.dim; c += NT) {
                 float s = 0.f;
 #pragma unroll 8
                 for (int q = 0; q < kRows; ++q) s += cols[q * W + c];
-                to[p * a.dim + c] = s;
+                to[k * a.dim + c] = s;
             }
         }
     }
+}
+
+// ------------------------------------------------------ long rows by blocks
+// A block's rows arrive in a ring of `stages` slots of shared memory, their vectors by
+// one bulk copy a row (and array); the ends are loaded a row ahead.
+constexpr int kStages = 8;              // slots at most
+constexpr int kRingThreads = 768;       // of an SM: 80 registers a thread
+constexpr int kRingBytes = 208 * 1024;  // of an SM
+
+__device__ __forceinline__ void copy_in(const void* from, uint32_t to, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(to),
+                 "l"(from), "r"(bytes), "r"(smem_addr(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void ring_init(uint64_t* full, int32_t stages) {
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    __syncthreads();
+}
+
+template <typename T, int V, int NT>
+__global__ void __launch_bounds__(NT, kRingThreads / NT > 0 ? kRingThreads / NT : 1)
+    k_norm_fwd_ring(FwdArgs<T> a, int32_t stages, int32_t slot) {
+    extern __shared__ __align__(128) uint8_t dsm[];
+    pdl_start();
+    __shared__ __align__(8) uint64_t full[kStages];
+    __shared__ float sh[4 * (NT / 32)];
+    int turn = 0;
+    const int32_t n = rows_of(a.d_n, a.n_cap), first = (int32_t)blockIdx.x, step = (int32_t)gridDim.x;
+    if (first >= n) return;
+    ring_init(full, stages);
+    const Part<T, V, NT> p(a.x, a.ld, first, a.dim, true);
+    const auto fetch = [&](int64_t r, int32_t at) {  // row r into slot `at` (thread 0)
+        if (r >= n) return;
+        mbar_expect_tx(&full[at], (uint32_t)p.vecs * 16);
+        copy_in(a.x + r * a.ld + p.head, smem_addr(dsm) + (uint32_t)(at * slot), (uint32_t)p.vecs * 16, &full[at]);
+    };
+    if (threadIdx.x == 0)
+        for (int i = 0; i < stages; ++i) fetch(first + (int64_t)i * step, i);
+    const Param<T, V, NT> w(p, a.weight, a.w_bf16, 1.f), b(p, a.bias, a.w_bf16, 0.f);
+    const float inv = 1.f / (float)a.dim;
+    int32_t at = 0;
+    uint32_t parity = 0;
+    float next = p.load_end(a.x + first * a.ld, 0);
+    for (int64_t r = first; r < n; r += step) {
+        const float end[1] = {next};
+        if (r + step < n) next = p.load_end(a.x + (r + step) * a.ld, 0);
+        if (!mbar_wait(&full[at], parity) && lane_id() == 0) dev_err(ERR_TIMEOUT);
+        const uint4* in = reinterpret_cast<const uint4*>(dsm + (size_t)at * slot);
+        norm_row<T, V, NT>(a, p, w, b, r, n, inv, sh, turn, end,
+                           [&](int v) { return p.has(v) ? in[p.l + v * NT] : make_uint4(0, 0, 0, 0); },
+                           [&] { if (threadIdx.x == 0) fetch(r + (int64_t)stages * step, at); });
+        if (++at == stages) at = 0, parity ^= 1;
+    }
+}
+
+template <typename T, int V, int NT>
+__global__ void __launch_bounds__(NT, kRingThreads / NT > 0 ? kRingThreads / NT : 1)
+    k_norm_bwd_ring(BwdArgs<T> a, int32_t stages, int32_t slot) {
+    extern __shared__ __align__(128) uint8_t dsm[];
+    pdl_start();
+    __shared__ __align__(8) uint64_t full[kStages];
+    __shared__ float sh[4 * (NT / 32)];
+    int turn = 0;
+    const int32_t n = rows_of(a.d_n, a.n_cap), first = (int32_t)blockIdx.x, step = (int32_t)gridDim.x;
+    ring_init(full, stages);
+    const Part<T, V, NT> p(a.x, a.ld, first, a.dim, true);
+    const auto fetch = [&](int64_t r, int32_t at) {  // row r of x and g into slot `at` (thread 0)
+        if (r >= n) return;
+        const uint32_t bytes = (uint32_t)p.vecs * 16, to = smem_addr(dsm) + (uint32_t)(at * slot);
+        mbar_expect_tx(&full[at], 2 * bytes);
+        copy_in(a.x + r * a.ld + p.head, to, bytes, &full[at]);
+        copy_in(a.g + r * a.ld_g + p.head, to + (uint32_t)slot / 2, bytes, &full[at]);
+    };
+    if (threadIdx.x == 0)
+        for (int i = 0; i < stages; ++i) fetch(first + (int64_t)i * step, i);
+    const Param<T, V, NT> w(p, a.weight, a.w_bf16, 1.f);
+    Sums<T, V, NT> sums;
+    const float inv = 1.f / (float)a.dim;
+    int32_t at = 0;
+    uint32_t parity = 0;
+    struct Next {
+        float mu, rs, xe, ge;
+    } next = {};
+    const auto load = [&](int64_t r) {
+        if (r < n) next = {__ldg(a.mean + r), __ldg(a.rstd + r), p.load_end(a.x + r * a.ld, 0), p.load_end(a.g + r * a.ld_g, 0)};
+    };
+    load(first);
+    for (int64_t r = first; r < n; r += step) {
+        const Next cur = next;
+        load(r + step);
+        if (!mbar_wait(&full[at], parity) && lane_id() == 0) dev_err(ERR_TIMEOUT);
+        const uint4* in = reinterpret_cast<const uint4*>(dsm + (size_t)at * slot);
+        const uint4* in_g = reinterpret_cast<const uint4*>(dsm + (size_t)at * slot + slot / 2);
+        const float xe[1] = {cur.xe}, ge[1] = {cur.ge};
+        grad_row<T, V, NT>(
+            a, p, w, sums, r, n, inv, sh, turn, cur.mu, cur.rs, xe, ge,
+            [&](int v) { return p.has(v) ? in[p.l + v * NT] : make_uint4(0, 0, 0, 0); },
+            [&](int v) { return p.has(v) ? in_g[p.l + v * NT] : make_uint4(0, 0, 0, 0); },
+            [&] {  // everybody is done with the row before this one: its slot is free
+                if (threadIdx.x == 0 && stages > 1 && r != first)
+                    fetch(r + (int64_t)(stages - 1) * step, at ? at - 1 : stages - 1);
+            });
+        if (stages == 1) {
+            __syncthreads();
+            if (threadIdx.x == 0) fetch(r + step, 0);
+        }
+        if (++at == stages) at = 0, parity ^= 1;
+    }
+    if (!a.parts) return;
+    float* to = a.parts + (int64_t)blockIdx.x * 2 * a.dim;
+    sums.put(p, false, to);
+    sums.put(p, true, to + a.dim);
 }
 
 // The blocks' sums in order: 32 columns a block, a 32nd of the blocks' sums a warp.
@@ -338,74 +585,90 @@ __global__ void __launch_bounds__(1024) k_norm_join(const float* __restrict__ pa
 // -------------------------------------------------------------------- host
 constexpr int kMaxDim = SG_MAX_NORM_DIM;
 
-// Blocks of the gradient at most: three of 256 threads an SM, one of 1024.
-int64_t max_parts(int32_t dim) { return (int64_t)num_sms() * (dim <= 4096 ? 4 : dim <= 8192 ? 2 : 1); }
 
-template <typename T, int N, int V, int L, int NT, int R>
+// Blocks that fill the device, a multiple of 8.
+int64_t all_blocks(int per_sm) { return (int64_t)num_sms() * per_sm / 8 * 8; }
+// Blocks of the gradient at most, whatever the form: the workspace has room for them.
+int64_t max_parts(int32_t dim) { return all_blocks(dim <= 1024 ? 12 : dim <= 2048 ? 6 : dim <= 4096 ? 3 : 1); }
+unsigned grid_of(int64_t rows, int per_sm) {
+    const int64_t most = all_blocks(per_sm);
+    return (unsigned)(rows < most ? rows : most);
+}
+template <typename T>
+unsigned grid_of(const BwdArgs<T>& a, int64_t rows, int per_sm) {
+    const unsigned blocks = grid_of(rows, per_sm);
+    return blocks < max_parts(a.dim) ? blocks : (unsigned)max_parts(a.dim);
+}
+
+template <typename T, int V, int L, int NT, int R>
 sg_status go(const FwdArgs<T>& a, cudaStream_t s) {
-    constexpr int kRows = (L <= 32 ? NT / L : 1) * R;
-    SG_CUDA(launch_pdl(k_norm_fwd<T, N, V, L, NT, R>, dim3((unsigned)cdiv(a.n_cap, kRows)), dim3(NT), 0, s, a));
+    const unsigned blocks = grid_of(cdiv(a.n_cap, (L <= 32 ? NT / L : 1) * R), NT == kThreads ? 4 : 1);
+    SG_CUDA(launch_pdl(k_norm_fwd<T, V, L, NT, R>, dim3(blocks), dim3(NT), 0, s, a));
     return SG_OK;
 }
-template <typename T, int N, int V, int L, int NT, int R>
+template <typename T, int V, int L, int NT, int R>
 sg_status go(const BwdArgs<T>& a, cudaStream_t s, int64_t* count) {
-    constexpr int kRows = (L <= 32 ? NT / L : 1) * R;
-    int64_t blocks = cdiv(a.n_cap, kRows);
-    if (blocks > max_parts(a.dim)) blocks = max_parts(a.dim);
+    const unsigned blocks = grid_of(a, cdiv(a.n_cap, (L <= 32 ? NT / L : 1) * R), kBwdBlocks<T, NT>);
     *count = blocks;
-    SG_CUDA(launch_pdl(k_norm_bwd<T, N, V, L, NT, R>, dim3((unsigned)blocks), dim3(NT), 0, s, a));
+    SG_CUDA(launch_pdl(k_norm_bwd<T, V, L, NT, R>, dim3(blocks), dim3(NT), 0, s, a));
     return SG_OK;
 }
 
-template <typename T, int N, typename A, typename... More>
-sg_status by_size(const A& a, More... more) {
-    constexpr int V = kHeld / N;
-    const int32_t units = a.dim / N;
-    if constexpr (N * sizeof(T) == 16) {
-        if (units <= 4) return go<T, N, 1, 4, kThreads, 4>(a, more...);
-        if (units <= 8) return go<T, N, 1, 8, kThreads, 4>(a, more...);
-        if (units <= 16) return go<T, N, 1, 16, kThreads, 4>(a, more...);
-        if (units <= 32) return go<T, N, 1, 32, kThreads, 4>(a, more...);
-        if (units <= 64) return go<T, N, 2, 32, kThreads, 2>(a, more...);
-    } else {
-        if (a.dim <= 128) return go<T, N, 4 / N, 32, kThreads, 2>(a, more...);
-    }
-    if (a.dim <= 32 * kHeld) return go<T, N, V, 32, kThreads, 1>(a, more...);
-    if (a.dim <= 64 * kHeld) return go<T, N, V, 64, 64, 1>(a, more...);
-    if (a.dim <= 128 * kHeld) return go<T, N, V, 128, 128, 1>(a, more...);
-    if (a.dim <= 256 * kHeld) return go<T, N, V, 256, 256, 1>(a, more...);
-    if (a.dim <= 512 * kHeld) return go<T, N, V, 512, 512, 1>(a, more...);
-    return go<T, N, V, 1024, 1024, 1>(a, more...);
+// Slots of a ring, by the rows that a block meets and the room.
+int32_t stages_of(int per_sm, int64_t slot, int64_t rows) {
+    int64_t k = (kRingBytes / per_sm - 2048) / slot;  // (2 KB: what is static, and the system's)
+    if (k > kStages) k = kStages;
+    if (k > rows) k = rows;
+    return k < 1 ? 1 : (int32_t)k;
+}
+template <typename T, int V, int NT>
+sg_status go_ring(const FwdArgs<T>& a, int32_t vecs, cudaStream_t s) {
+    constexpr int kPerSm = kRingThreads / NT > 0 ? kRingThreads / NT : 1;
+    const unsigned blocks = grid_of(a.n_cap, kPerSm);
+    const int32_t slot = vecs * 16, stages = stages_of(kPerSm, slot, cdiv(a.n_cap, blocks));
+    static OncePerDevice set;
+    SG_CUDA(allow_smem(set, k_norm_fwd_ring<T, V, NT>, kRingBytes));
+    SG_CUDA(launch_pdl(k_norm_fwd_ring<T, V, NT>, dim3(blocks), dim3(NT), (size_t)stages * slot, s, a, stages, slot));
+    return SG_OK;
+}
+template <typename T, int V, int NT>
+sg_status go_ring(const BwdArgs<T>& a, int32_t vecs, cudaStream_t s, int64_t* count) {
+    constexpr int kPerSm = kRingThreads / NT > 0 ? kRingThreads / NT : 1;
+    const unsigned blocks = grid_of(a, a.n_cap, kPerSm);
+    const int32_t slot = vecs * 32, stages = stages_of(kPerSm, slot, cdiv(a.n_cap, blocks));
+    *count = blocks;
+    static OncePerDevice set;
+    SG_CUDA(allow_smem(set, k_norm_bwd_ring<T, V, NT>, kRingBytes));
+    SG_CUDA(launch_pdl(k_norm_bwd_ring<T, V, NT>, dim3(blocks), dim3(NT), (size_t)stages * slot, s, a, stages, slot));
+    return SG_OK;
 }
 
-// Values of a unit: the largest power of two that the width, the arrays (bits: all
-// addresses and row strides in bytes) and the parameters (pbits) allow.
-int unit_of(int32_t dim, uintptr_t bits, uintptr_t pbits, int e, int ew) {
-    int n = 16 / e;
-    const auto fits = [&](int k) {
-        return dim % k == 0 && bits % (uintptr_t)(k * e) == 0 && pbits % (uintptr_t)(k * ew < 16 ? k * ew : 16) == 0;
-    };
-    while (n > 1 && !fits(n)) n /= 2;
-    return n;
-}
-
+// The smallest group that holds a row's vectors.
 template <typename T, typename A, typename... More>
-sg_status by_unit(int unit, const A& a, More... more) {
-    if constexpr (sizeof(T) == 2)
-        if (unit == 8) return by_size<T, 8>(a, more...);
-    if (unit == 4) return by_size<T, 4>(a, more...);
-    if (unit == 2) return by_size<T, 2>(a, more...);
-    return by_size<T, 1>(a, more...);
+sg_status by_size(const A& a, More... more) {
+    constexpr int V = kHeld / kE<T>;
+    const int32_t vecs = a.dim / kE<T> > 0 ? a.dim / kE<T> : 1;  // at most
+    if (vecs <= 4) return go<T, 1, 4, kThreads, 1>(a, more...);
+    if (vecs <= 8) return go<T, 1, 8, kThreads, 1>(a, more...);
+    if (vecs <= 16) return go<T, 1, 16, kThreads, 2>(a, more...);
+    if (vecs <= 32) return go<T, 1, 32, kThreads, 2>(a, more...);
+    if (vecs <= 64) return go<T, 2, 32, kThreads, 1>(a, more...);
+    if (!a.alike) return go<T, V, 1024, 1024, 1>(a, more...);
+    if (vecs <= 64 * V) return go_ring<T, V, 64>(a, vecs, more...);
+    if (vecs <= 128 * V) return go_ring<T, V, 128>(a, vecs, more...);
+    if (vecs <= 256 * V) return go_ring<T, V, 256>(a, vecs, more...);
+    if (vecs <= 512 * V) return go_ring<T, V, 512>(a, vecs, more...);
+    return go_ring<T, V, 1024>(a, vecs, more...);
 }
 
 bool known(int32_t dtype) { return dtype == SG_F32 || dtype == SG_BF16; }
 int size_of(int32_t dtype) { return dtype == SG_F32 ? 4 : 2; }
 
 template <typename T>
-sg_status bwd(BwdArgs<T> a, int unit, void* dw, void* db, cudaStream_t s) {
+sg_status bwd(BwdArgs<T> a, void* dw, void* db, cudaStream_t s) {
     int64_t count = 0;
     if (a.n_cap > 0) {
-        const sg_status st = by_unit<T>(unit, a, s, &count);
+        const sg_status st = by_size<T>(a, s, &count);
         if (st != SG_OK) return st;
     }
     if (!a.parts) return SG_OK;
@@ -432,16 +695,15 @@ extern "C" sg_status sg_layernorm_fwd(const void* d_x, int32_t dtype, int32_t n_
     if (d_x == d_y && ld != ld_y) return fail(SG_ERR_INVALID_ARG, "sg_layernorm_fwd: in place needs ld_y = ld");
     if (n_cap == 0) return SG_OK;
     cudaStream_t s = (cudaStream_t)stream;
-    const int unit = unit_of(dim, (uintptr_t)d_x | (uintptr_t)d_y | (uintptr_t)(ld * e) | (uintptr_t)(ld_y * e),
-                             (uintptr_t)d_weight | (uintptr_t)d_bias, e, ew);
+    const int32_t alike = ((((uintptr_t)d_x - (uintptr_t)d_y) | (uintptr_t)((ld - ld_y) * e)) & 15) == 0;
     if (dtype == SG_F32) {
         const FwdArgs<float> a = {(const float*)d_x, (float*)d_y, ld, ld_y, d_weight, d_bias, d_n, n_cap, dim,
-                                  dtype_w == SG_BF16, eps, d_mean, d_rstd};
-        return by_unit<float>(unit, a, s);
+                                  dtype_w == SG_BF16, alike, eps, d_mean, d_rstd};
+        return by_size<float>(a, s);
     }
     const FwdArgs<__nv_bfloat16> a = {(const __nv_bfloat16*)d_x, (__nv_bfloat16*)d_y, ld, ld_y, d_weight, d_bias, d_n,
-                                      n_cap, dim, dtype_w == SG_BF16, eps, d_mean, d_rstd};
-    return by_unit<__nv_bfloat16>(unit, a, s);
+                                      n_cap, dim, dtype_w == SG_BF16, alike, eps, d_mean, d_rstd};
+    return by_size<__nv_bfloat16>(a, s);
 }
 
 extern "C" size_t sg_layernorm_bwd_workspace(int32_t n_cap, int32_t dim) {
@@ -473,16 +735,15 @@ extern "C" sg_status sg_layernorm_bwd(const void* d_g, const void* d_x, int32_t 
     if ((d_dx == d_g && ld_dx != ld_g) || (d_dx == d_x && ld_dx != ld))
         return fail(SG_ERR_INVALID_ARG, "sg_layernorm_bwd: in place needs equal row strides");
     cudaStream_t s = (cudaStream_t)stream;
-    const int unit =
-        unit_of(dim, (uintptr_t)d_g | (uintptr_t)d_x | (uintptr_t)d_dx | (uintptr_t)((ld | ld_g | ld_dx) * e),
-                (uintptr_t)d_weight, e, ew);
+    const int32_t alike = ((((uintptr_t)d_x - (uintptr_t)d_g) | ((uintptr_t)d_x - (uintptr_t)d_dx) |
+                            (uintptr_t)((ld - ld_g) * e) | (uintptr_t)((ld - ld_dx) * e)) & 15) == 0;
     float* parts = d_dweight || d_dbias ? (float*)d_workspace : nullptr;
     if (dtype == SG_F32) {
         const BwdArgs<float> a = {(const float*)d_g, (const float*)d_x, (float*)d_dx, ld_g, ld, ld_dx, d_weight, d_mean,
-                                  d_rstd, d_n, n_cap, dim, dtype_w == SG_BF16, parts};
-        return bwd<float>(a, unit, d_dweight, d_dbias, s);
+                                  d_rstd, d_n, n_cap, dim, dtype_w == SG_BF16, alike, parts};
+        return bwd<float>(a, d_dweight, d_dbias, s);
     }
     const BwdArgs<__nv_bfloat16> a = {(const __nv_bfloat16*)d_g, (const __nv_bfloat16*)d_x, (__nv_bfloat16*)d_dx, ld_g, ld,
-                                      ld_dx, d_weight, d_mean, d_rstd, d_n, n_cap, dim, dtype_w == SG_BF16, parts};
-    return bwd<__nv_bfloat16>(a, unit, d_dweight, d_dbias, s);
+                                      ld_dx, d_weight, d_mean, d_rstd, d_n, n_cap, dim, dtype_w == SG_BF16, alike, parts};
+    return bwd<__nv_bfloat16>(a, d_dweight, d_dbias, s);
 }

@@ -74,6 +74,18 @@ def test_layernorm_workspace_grows_with_the_rows(lib, dim):
     assert need[0] > 0 and all(a <= b for a, b in zip(need, need[1:]))
 
 
+@pytest.mark.parametrize("dim", [1, 128, 250, 257, 500, 512, 513, 1000, 1024, 1025, 2048, 4096, 8192, 16384])
+def test_layernorm_workspace_has_room_for_the_blocks(lib, dim):
+    # a block for every row up to 768 threads an SM: 3 of 256 threads for rows up to 512,
+    # longer ones by the smallest of 64 to 1024 threads with 16 values each (fp32 rows of
+    # more than 252 already, as they need not start on 16 bytes)
+    threads = 64
+    while threads * 16 < dim:
+        threads *= 2
+    blocks = max(1, 768 // threads) * 148 // 8 * 8  # (148 SMs when there is no device)
+    assert lib.sg_layernorm_bwd_workspace(1 << 20, dim) >= blocks * 2 * dim * 4
+
+
 class _Refuses:  # the library is not reached
     def __getattr__(self, name):
         raise AssertionError("%s was called" % name)

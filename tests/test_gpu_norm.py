@@ -30,6 +30,19 @@ def _cuda():
     sg.load()
 
 
+class _Guarded:
+    """A workspace of exactly the bytes asked for, with bytes behind it that
+    have to stay as they are."""
+    def __init__(self, n, d):
+        need = sg.sg_layernorm_bwd_workspace(n, d)
+        self.all = sg.aligned_workspace(need + (1 << 20))
+        self.all.fill_(0xCD)
+        self.ws, self.rest = self.all[:need], self.all[need:]
+
+    def check(self):
+        assert bool((self.rest == 0xCD).all())
+
+
 def _ws(n, d):
     ws = sg.aligned_workspace(sg.sg_layernorm_bwd_workspace(n, d))
     ws.fill_(0xCD)
@@ -99,8 +112,10 @@ def _bwd(g, x, w, m, r, dtype_w=None, d_n=None):
     dx = torch.full_like(x, 7.0)
     dt = w.dtype if w is not None else dtype_w or torch.float32
     dw, db = torch.full((d,), 7.0, device="cuda", dtype=dt), torch.full((d,), 7.0, device="cuda", dtype=dt)
-    sg.sg_layernorm_bwd(g, x, w, m, r, n, d_n, dx, dw, db, _ws(n, d))
+    guarded = _Guarded(n, d)
+    sg.sg_layernorm_bwd(g, x, w, m, r, n, d_n, dx, dw, db, guarded.ws)
     sg.sg_stream_check()
+    guarded.check()
     return dx, dw, db
 
 
