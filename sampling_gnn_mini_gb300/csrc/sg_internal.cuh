@@ -70,7 +70,6 @@ unsigned fetch_err_loss(cudaStream_t);
 unsigned fetch_err_muon(cudaStream_t);
 unsigned fetch_err_logprobs(cudaStream_t);
 unsigned fetch_err_distill(cudaStream_t);
-unsigned fetch_err_norm(cudaStream_t);
 
 // ------------------------------------------------------------- ranking
 // Nodes by descending 32-bit score, ties by ascending ID, into order[n]

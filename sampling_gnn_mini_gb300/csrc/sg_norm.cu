@@ -21,8 +21,6 @@
 #include "sg_rows.cuh"
 #include "sg_tc.cuh"
 
-SGI_ERROR_WORD(norm)
-
 using namespace sgi;
 
 namespace {
@@ -278,8 +276,12 @@ struct BwdArgs {
     const float* rstd;
     const int32_t* d_n;
     int32_t n_cap, dim, w_bf16, alike;
-    float* parts;  // per block: sums of g h by column, then of g; NULL: not wanted
+    float* parts;  // per block: sums of g h, then of g, kLead before the first vector's; NULL: not wanted
 };
+// A block's sums of dim columns: kLead - head before the head's first, so that vectors
+// are on 16 bytes; the two rows are `pitch` apart.
+constexpr int kLead = 8;
+__host__ __device__ constexpr int32_t pitch_of(int32_t dim) { return (dim + kLead + 3) / 4 * 4; }
 
 // A thread's columns' sums over its rows.
 template <typename T, int V, int L>
@@ -294,16 +296,34 @@ struct Sums {
 #pragma unroll
         for (int e = 0; e < Part<T, V, L>::NE; ++e) we[e] = be[e] = 0.f;
     }
-    // one of the two into o
+    // one of the two into o[column + lead], which is 16-byte aligned at vectors if `wide`
+    template <bool wide>
     __device__ __forceinline__ void put(const Part<T, V, L>& p, bool bias, float* o) const {
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (p.has(v))
 #pragma unroll
-                for (int i = 0; i < kE<T> / 2; ++i) unpair(bias ? b[v][i] : w[v][i], o[p.column(v) + 2 * i], o[p.column(v) + 2 * i + 1]);
+                for (int i = 0; i < kE<T> / 2; i += 2) {
+                    float4 q;
+                    unpair(bias ? b[v][i] : w[v][i], q.x, q.y);
+                    unpair(bias ? b[v][i + 1] : w[v][i + 1], q.z, q.w);
+                    float* to = o + p.column(v) + 2 * i;
+                    if constexpr (wide) {
+                        *reinterpret_cast<float4*>(to) = q;
+                    } else {
+                        to[0] = q.x, to[1] = q.y, to[2] = q.z, to[3] = q.w;
+                    }
+                }
 #pragma unroll
         for (int e = 0; e < Part<T, V, L>::NE; ++e)
             if (p.ends[e] >= 0) o[p.ends[e]] = bias ? be[e] : we[e];
+    }
+    // a block's two rows of sums (L: the whole block)
+    __device__ __forceinline__ void put_block(const Part<T, V, L>& p, const BwdArgs<T>& a) const {
+        if (!a.parts) return;
+        float* to = a.parts + (int64_t)blockIdx.x * 2 * pitch_of(a.dim) + kLead - p.head;
+        put<true>(p, false, to);
+        put<true>(p, true, to + pitch_of(a.dim));
     }
 };
 
@@ -345,7 +365,8 @@ __device__ __forceinline__ void grad_row(const BwdArgs<T>& a, const Part<T, V, L
     group_sum<L, 2>(s, sh, turn);
     between();
     if (r >= n) return;
-    const float mg = -s[0] * inv, mh = -s[1] * inv;
+    // dx = rstd g w + (x - mean) ch + cg
+    const float cg = -s[0] * inv * rstd, ch = -s[1] * inv * rstd * rstd;
     T* to = a.dx + r * a.ld_dx;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -354,13 +375,12 @@ __device__ __forceinline__ void grad_row(const BwdArgs<T>& a, const Part<T, V, L
         pairs_of(g(v), f);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            h[i] = mul2(add2(h[i], mu), rs);
-            f[i] = mul2(add2(mul2(f[i], w.f[v][i]), fma2(h[i], both(mh), both(mg))), rs);
+            f[i] = fma2(mul2(f[i], w.f[v][i]), rs, fma2(add2(h[i], mu), both(ch), both(cg)));
         }
         p.store(to, v, f);
     }
 #pragma unroll
-    for (int e = 0; e < NE; ++e) p.store_end(to, e, rstd * (ge[e] * w.end[e] + fmaf(he[e], mh, mg)));
+    for (int e = 0; e < NE; ++e) p.store_end(to, e, fmaf(ge[e] * w.end[e], rstd, fmaf(xe[e] - mean, ch, cg)));
 }
 
 // Blocks an SM: bf16 vectors hold twice the values.
@@ -422,108 +442,115 @@ __global__ void __launch_bounds__(NT, kBwdBlocks<T, NT>) k_norm_bwd(BwdArgs<T> a
                     }
                 });
     }
-    if (!a.parts) return;
-    float* to = a.parts + (int64_t)blockIdx.x * 2 * a.dim;
     if constexpr (L > 32) {
-        sums.put(p, false, to);
-        sums.put(p, true, to + a.dim);
+        sums.put_block(p, a);
     } else {
+        if (!a.parts) return;
+        float* to = a.parts + (int64_t)blockIdx.x * 2 * pitch_of(a.dim) + kLead;
         constexpr int W = L * V * kE<T> + 16;  // columns of a group
         for (int k = 0; k < 2; ++k) {
             __syncthreads();
-            sums.put(p, k != 0, cols + ((int)threadIdx.x / L) * W);
+            sums.template put<false>(p, k != 0, cols + ((int)threadIdx.x / L) * W);
             __syncthreads();
             for (int c = threadIdx.x; c < a.dim; c += NT) {
                 float s = 0.f;
 #pragma unroll 8
                 for (int q = 0; q < kRows; ++q) s += cols[q * W + c];
-                to[k * a.dim + c] = s;
+                to[k * pitch_of(a.dim) + c] = s;
             }
         }
     }
 }
 
 // ------------------------------------------------------ long rows by blocks
-// A block's rows arrive in a ring of `stages` slots of shared memory, their vectors by
-// one bulk copy a row (and array); the ends are loaded a row ahead.
-constexpr int kStages = 8;              // slots at most
-constexpr int kRingThreads = 768;       // of an SM: 80 registers a thread
+// Each thread copies its own vectors of the block's next rows into a ring of slots in
+// shared memory, asynchronously, and waits for its own copies alone; the ends are
+// loaded a row ahead.
 constexpr int kRingBytes = 208 * 1024;  // of an SM
+// Blocks an SM.  A: arrays that are read (1 forward, 2 backward).
+template <int NT, int A>
+constexpr int kRingBlocks = (A == 1 ? 768 : 512) / NT > 0 ? (A == 1 ? 768 : 512) / NT : 1;
+// Slots: as many as there is room for, four at most.
+template <int V, int NT, int A>
+constexpr int kRoom = kRingBytes / kRingBlocks<NT, A> / (NT * V * A * 16);
+template <int V, int NT, int A>
+constexpr int kDepth = kRoom<V, NT, A> > 4 ? 4 : kRoom<V, NT, A>;
+template <int V, int NT, int A>
+constexpr int kRingSize = kDepth<V, NT, A> * NT * V * A * 16;
 
-__device__ __forceinline__ void copy_in(const void* from, uint32_t to, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(to),
-                 "l"(from), "r"(bytes), "r"(smem_addr(bar))
-                 : "memory");
+__device__ __forceinline__ void copy_async(const uint4* to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_addr(to)), "l"(from) : "memory");
 }
-__device__ __forceinline__ void ring_init(uint64_t* full, int32_t stages) {
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
-        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-    }
-    __syncthreads();
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+// Waits for all groups of copies but the last N.
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
 template <typename T, int V, int NT>
-__global__ void __launch_bounds__(NT, kRingThreads / NT > 0 ? kRingThreads / NT : 1)
-    k_norm_fwd_ring(FwdArgs<T> a, int32_t stages, int32_t slot) {
-    extern __shared__ __align__(128) uint8_t dsm[];
+__global__ void __launch_bounds__(NT, kRingBlocks<NT, 1>) k_norm_fwd_ring(FwdArgs<T> a) {
+    extern __shared__ __align__(128) uint4 ring[];
     pdl_start();
-    __shared__ __align__(8) uint64_t full[kStages];
+    constexpr int D = kDepth<V, NT, 1>;
     __shared__ float sh[4 * (NT / 32)];
     int turn = 0;
     const int32_t n = rows_of(a.d_n, a.n_cap), first = (int32_t)blockIdx.x, step = (int32_t)gridDim.x;
     if (first >= n) return;
-    ring_init(full, stages);
     const Part<T, V, NT> p(a.x, a.ld, first, a.dim, true);
-    const auto fetch = [&](int64_t r, int32_t at) {  // row r into slot `at` (thread 0)
-        if (r >= n) return;
-        mbar_expect_tx(&full[at], (uint32_t)p.vecs * 16);
-        copy_in(a.x + r * a.ld + p.head, smem_addr(dsm) + (uint32_t)(at * slot), (uint32_t)p.vecs * 16, &full[at]);
+    const auto slot = [&](int at, int v) { return ring + (at * V + v) * NT + (int)threadIdx.x; };
+    const auto fetch = [&](int64_t r, int at) {
+        if (r < n) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (p.has(v)) copy_async(slot(at, v), a.x + r * a.ld + p.column(v));
+        }
+        copies_end();
     };
-    if (threadIdx.x == 0)
-        for (int i = 0; i < stages; ++i) fetch(first + (int64_t)i * step, i);
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) fetch(first + (int64_t)i * step, i);
     const Param<T, V, NT> w(p, a.weight, a.w_bf16, 1.f), b(p, a.bias, a.w_bf16, 0.f);
     const float inv = 1.f / (float)a.dim;
-    int32_t at = 0;
-    uint32_t parity = 0;
+    int at = 0;
     float next = p.load_end(a.x + first * a.ld, 0);
     for (int64_t r = first; r < n; r += step) {
+        fetch(r + (int64_t)(D - 1) * step, at ? at - 1 : D - 1);
         const float end[1] = {next};
         if (r + step < n) next = p.load_end(a.x + (r + step) * a.ld, 0);
-        if (!mbar_wait(&full[at], parity) && lane_id() == 0) dev_err(ERR_TIMEOUT);
-        const uint4* in = reinterpret_cast<const uint4*>(dsm + (size_t)at * slot);
+        copies_wait<D - 1>();
         norm_row<T, V, NT>(a, p, w, b, r, n, inv, sh, turn, end,
-                           [&](int v) { return p.has(v) ? in[p.l + v * NT] : make_uint4(0, 0, 0, 0); },
-                           [&] { if (threadIdx.x == 0) fetch(r + (int64_t)stages * step, at); });
-        if (++at == stages) at = 0, parity ^= 1;
+                           [&](int v) { return p.has(v) ? *slot(at, v) : make_uint4(0, 0, 0, 0); }, [] {});
+        if (++at == D) at = 0;
     }
 }
 
 template <typename T, int V, int NT>
-__global__ void __launch_bounds__(NT, kRingThreads / NT > 0 ? kRingThreads / NT : 1)
-    k_norm_bwd_ring(BwdArgs<T> a, int32_t stages, int32_t slot) {
-    extern __shared__ __align__(128) uint8_t dsm[];
+__global__ void __launch_bounds__(NT, kRingBlocks<NT, 2>) k_norm_bwd_ring(BwdArgs<T> a) {
+    extern __shared__ __align__(128) uint4 ring[];
     pdl_start();
-    __shared__ __align__(8) uint64_t full[kStages];
+    constexpr int D = kDepth<V, NT, 2>;
     __shared__ float sh[4 * (NT / 32)];
     int turn = 0;
     const int32_t n = rows_of(a.d_n, a.n_cap), first = (int32_t)blockIdx.x, step = (int32_t)gridDim.x;
-    ring_init(full, stages);
     const Part<T, V, NT> p(a.x, a.ld, first, a.dim, true);
-    const auto fetch = [&](int64_t r, int32_t at) {  // row r of x and g into slot `at` (thread 0)
-        if (r >= n) return;
-        const uint32_t bytes = (uint32_t)p.vecs * 16, to = smem_addr(dsm) + (uint32_t)(at * slot);
-        mbar_expect_tx(&full[at], 2 * bytes);
-        copy_in(a.x + r * a.ld + p.head, to, bytes, &full[at]);
-        copy_in(a.g + r * a.ld_g + p.head, to + (uint32_t)slot / 2, bytes, &full[at]);
+    const auto slot = [&](int at, int v) { return ring + (at * 2 * V + v) * NT + (int)threadIdx.x; };  // (g: v + V)
+    const auto fetch = [&](int64_t r, int at) {
+        if (r < n) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (p.has(v)) {
+                    copy_async(slot(at, v), a.x + r * a.ld + p.column(v));
+                    copy_async(slot(at, v + V), a.g + r * a.ld_g + p.column(v));
+                }
+        }
+        copies_end();
     };
-    if (threadIdx.x == 0)
-        for (int i = 0; i < stages; ++i) fetch(first + (int64_t)i * step, i);
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) fetch(first + (int64_t)i * step, i);
     const Param<T, V, NT> w(p, a.weight, a.w_bf16, 1.f);
     Sums<T, V, NT> sums;
     const float inv = 1.f / (float)a.dim;
-    int32_t at = 0;
-    uint32_t parity = 0;
+    int at = 0;
     struct Next {
         float mu, rs, xe, ge;
     } next = {};
@@ -532,52 +559,45 @@ __global__ void __launch_bounds__(NT, kRingThreads / NT > 0 ? kRingThreads / NT 
     };
     load(first);
     for (int64_t r = first; r < n; r += step) {
+        fetch(r + (int64_t)(D - 1) * step, at ? at - 1 : D - 1);
         const Next cur = next;
         load(r + step);
-        if (!mbar_wait(&full[at], parity) && lane_id() == 0) dev_err(ERR_TIMEOUT);
-        const uint4* in = reinterpret_cast<const uint4*>(dsm + (size_t)at * slot);
-        const uint4* in_g = reinterpret_cast<const uint4*>(dsm + (size_t)at * slot + slot / 2);
+        copies_wait<D - 1>();
         const float xe[1] = {cur.xe}, ge[1] = {cur.ge};
         grad_row<T, V, NT>(
             a, p, w, sums, r, n, inv, sh, turn, cur.mu, cur.rs, xe, ge,
-            [&](int v) { return p.has(v) ? in[p.l + v * NT] : make_uint4(0, 0, 0, 0); },
-            [&](int v) { return p.has(v) ? in_g[p.l + v * NT] : make_uint4(0, 0, 0, 0); },
-            [&] {  // everybody is done with the row before this one: its slot is free
-                if (threadIdx.x == 0 && stages > 1 && r != first)
-                    fetch(r + (int64_t)(stages - 1) * step, at ? at - 1 : stages - 1);
-            });
-        if (stages == 1) {
-            __syncthreads();
-            if (threadIdx.x == 0) fetch(r + step, 0);
-        }
-        if (++at == stages) at = 0, parity ^= 1;
+            [&](int v) { return p.has(v) ? *slot(at, v) : make_uint4(0, 0, 0, 0); },
+            [&](int v) { return p.has(v) ? *slot(at, v + V) : make_uint4(0, 0, 0, 0); }, [] {});
+        if (++at == D) at = 0;
     }
-    if (!a.parts) return;
-    float* to = a.parts + (int64_t)blockIdx.x * 2 * a.dim;
-    sums.put(p, false, to);
-    sums.put(p, true, to + a.dim);
+    sums.put_block(p, a);
 }
 
 // The blocks' sums in order: 32 columns a block, a 32nd of the blocks' sums a warp.
-__global__ void __launch_bounds__(1024) k_norm_join(const float* __restrict__ parts, int32_t count, int32_t dim,
-                                                    void* dweight, void* dbias, int32_t bf16) {
+// heads: block p's vectors begin at the head of row p (x, its row stride in bytes).
+__global__ void __launch_bounds__(1024) k_norm_join(const float* __restrict__ parts, int32_t count, int32_t dim, void* dweight,
+                                                    void* dbias, int32_t bf16, uintptr_t x, int64_t ld_bytes, int32_t size,
+                                                    int32_t heads) {
     pdl_start();
     __shared__ float sh[32][33];
     const int lane = (int)lane_id(), warp = (int)(threadIdx.x >> 5);
-    const int32_t c = (int32_t)blockIdx.x * 32 + lane;
+    const int32_t pitch = pitch_of(dim), o0 = (int32_t)blockIdx.x * 32, o = o0 + lane;
     float s = 0.f;
-    if (c < 2 * dim) {
+    if (o < 2 * dim) {
+        const int32_t at = o < dim ? o : o - dim + pitch;
 #pragma unroll 8
-        for (int32_t p = warp; p < count; p += 32) s += parts[(int64_t)p * 2 * dim + c];
+        for (int32_t p = warp; p < count; p += 32) {
+            const int32_t off = heads ? (int32_t)((x + (uintptr_t)(p * ld_bytes)) & 15) : 0;
+            s += parts[(int64_t)p * 2 * pitch + kLead - (off ? (16 - off) / size : 0) + at];
+        }
     }
     sh[warp][lane] = s;
     __syncthreads();
     s = warp_sum(sh[lane][warp]);  // column `warp` of the block
-    const int32_t o = (int32_t)blockIdx.x * 32 + warp;
-    if (lane != 0 || o >= 2 * dim) return;
-    void* to = o < dim ? dweight : dbias;
+    const int32_t i = o0 + warp < dim ? o0 + warp : o0 + warp - dim;
+    if (lane != 0 || o0 + warp >= 2 * dim) return;
+    void* to = o0 + warp < dim ? dweight : dbias;
     if (!to) return;
-    const int32_t i = o < dim ? o : o - dim;
     if (bf16) put((__nv_bfloat16*)to + i, s);
     else put((float*)to + i, s);
 }
@@ -607,39 +627,29 @@ sg_status go(const FwdArgs<T>& a, cudaStream_t s) {
     return SG_OK;
 }
 template <typename T, int V, int L, int NT, int R>
-sg_status go(const BwdArgs<T>& a, cudaStream_t s, int64_t* count) {
+sg_status go(const BwdArgs<T>& a, cudaStream_t s, int64_t* count, int32_t* heads) {
     const unsigned blocks = grid_of(a, cdiv(a.n_cap, (L <= 32 ? NT / L : 1) * R), kBwdBlocks<T, NT>);
     *count = blocks;
+    *heads = 0;  // (by columns, or rows that are moved value by value)
     SG_CUDA(launch_pdl(k_norm_bwd<T, V, L, NT, R>, dim3(blocks), dim3(NT), 0, s, a));
     return SG_OK;
 }
 
-// Slots of a ring, by the rows that a block meets and the room.
-int32_t stages_of(int per_sm, int64_t slot, int64_t rows) {
-    int64_t k = (kRingBytes / per_sm - 2048) / slot;  // (2 KB: what is static, and the system's)
-    if (k > kStages) k = kStages;
-    if (k > rows) k = rows;
-    return k < 1 ? 1 : (int32_t)k;
-}
 template <typename T, int V, int NT>
-sg_status go_ring(const FwdArgs<T>& a, int32_t vecs, cudaStream_t s) {
-    constexpr int kPerSm = kRingThreads / NT > 0 ? kRingThreads / NT : 1;
-    const unsigned blocks = grid_of(a.n_cap, kPerSm);
-    const int32_t slot = vecs * 16, stages = stages_of(kPerSm, slot, cdiv(a.n_cap, blocks));
+sg_status go_ring(const FwdArgs<T>& a, cudaStream_t s) {
     static OncePerDevice set;
-    SG_CUDA(allow_smem(set, k_norm_fwd_ring<T, V, NT>, kRingBytes));
-    SG_CUDA(launch_pdl(k_norm_fwd_ring<T, V, NT>, dim3(blocks), dim3(NT), (size_t)stages * slot, s, a, stages, slot));
+    SG_CUDA(allow_smem(set, k_norm_fwd_ring<T, V, NT>, kRingSize<V, NT, 1>));
+    SG_CUDA(launch_pdl(k_norm_fwd_ring<T, V, NT>, dim3(grid_of(a.n_cap, kRingBlocks<NT, 1>)), dim3(NT), kRingSize<V, NT, 1>, s, a));
     return SG_OK;
 }
 template <typename T, int V, int NT>
-sg_status go_ring(const BwdArgs<T>& a, int32_t vecs, cudaStream_t s, int64_t* count) {
-    constexpr int kPerSm = kRingThreads / NT > 0 ? kRingThreads / NT : 1;
-    const unsigned blocks = grid_of(a, a.n_cap, kPerSm);
-    const int32_t slot = vecs * 32, stages = stages_of(kPerSm, slot, cdiv(a.n_cap, blocks));
-    *count = blocks;
+sg_status go_ring(const BwdArgs<T>& a, cudaStream_t s, int64_t* count, int32_t* heads) {
     static OncePerDevice set;
-    SG_CUDA(allow_smem(set, k_norm_bwd_ring<T, V, NT>, kRingBytes));
-    SG_CUDA(launch_pdl(k_norm_bwd_ring<T, V, NT>, dim3(blocks), dim3(NT), (size_t)stages * slot, s, a, stages, slot));
+    SG_CUDA(allow_smem(set, k_norm_bwd_ring<T, V, NT>, kRingSize<V, NT, 2>));
+    const unsigned blocks = grid_of(a, a.n_cap, kRingBlocks<NT, 2>);
+    *count = blocks;
+    *heads = 1;
+    SG_CUDA(launch_pdl(k_norm_bwd_ring<T, V, NT>, dim3(blocks), dim3(NT), kRingSize<V, NT, 2>, s, a));
     return SG_OK;
 }
 
@@ -654,11 +664,11 @@ sg_status by_size(const A& a, More... more) {
     if (vecs <= 32) return go<T, 1, 32, kThreads, 2>(a, more...);
     if (vecs <= 64) return go<T, 2, 32, kThreads, 1>(a, more...);
     if (!a.alike) return go<T, V, 1024, 1024, 1>(a, more...);
-    if (vecs <= 64 * V) return go_ring<T, V, 64>(a, vecs, more...);
-    if (vecs <= 128 * V) return go_ring<T, V, 128>(a, vecs, more...);
-    if (vecs <= 256 * V) return go_ring<T, V, 256>(a, vecs, more...);
-    if (vecs <= 512 * V) return go_ring<T, V, 512>(a, vecs, more...);
-    return go_ring<T, V, 1024>(a, vecs, more...);
+    if (vecs <= 64 * V) return go_ring<T, V, 64>(a, more...);
+    if (vecs <= 128 * V) return go_ring<T, V, 128>(a, more...);
+    if (vecs <= 256 * V) return go_ring<T, V, 256>(a, more...);
+    if (vecs <= 512 * V) return go_ring<T, V, 512>(a, more...);
+    return go_ring<T, V, 1024>(a, more...);
 }
 
 bool known(int32_t dtype) { return dtype == SG_F32 || dtype == SG_BF16; }
@@ -667,13 +677,15 @@ int size_of(int32_t dtype) { return dtype == SG_F32 ? 4 : 2; }
 template <typename T>
 sg_status bwd(BwdArgs<T> a, void* dw, void* db, cudaStream_t s) {
     int64_t count = 0;
+    int32_t heads = 0;
     if (a.n_cap > 0) {
-        const sg_status st = by_size<T>(a, s, &count);
+        const sg_status st = by_size<T>(a, s, &count, &heads);
         if (st != SG_OK) return st;
     }
     if (!a.parts) return SG_OK;
     SG_CUDA(launch_pdl(k_norm_join, dim3((unsigned)cdiv(2 * (int64_t)a.dim, 32)), dim3(1024), 0, s, (const float*)a.parts,
-                       (int32_t)count, a.dim, dw, db, a.w_bf16));
+                       (int32_t)count, a.dim, dw, db, a.w_bf16, (uintptr_t)a.x, a.ld * (int64_t)sizeof(T), (int32_t)sizeof(T),
+                       heads));
     return SG_OK;
 }
 
@@ -710,7 +722,7 @@ extern "C" size_t sg_layernorm_bwd_workspace(int32_t n_cap, int32_t dim) {
     if (n_cap < 0 || dim <= 0 || dim > kMaxDim) return 0;
     int64_t parts = max_parts(dim);
     if (parts > n_cap) parts = n_cap;
-    return (size_t)cdiv((parts > 0 ? parts : 1) * 2 * dim * 4, 256) * 256;
+    return (size_t)cdiv((parts > 0 ? parts : 1) * 2 * pitch_of(dim) * 4, 256) * 256;
 }
 
 extern "C" sg_status sg_layernorm_bwd(const void* d_g, const void* d_x, int32_t dtype, int32_t n_cap, const int32_t* d_n,
