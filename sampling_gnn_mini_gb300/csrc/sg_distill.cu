@@ -70,78 +70,81 @@ __device__ __forceinline__ float weight_of(const Args<T>& a) {
 
 // A row's entries in shared memory, for the threads that write their classes.
 struct Entries {
-    int32_t id[SG_MAX_TOP];  // -1: none
-    float q[SG_MAX_TOP], x[SG_MAX_TOP];
+    int32_t __align__(16) id[SG_MAX_TOP];  // -1: none, from k on as well
+    float v[SG_MAX_TOP], x[SG_MAX_TOP], q[SG_MAX_TOP];
 };
-
-// One warp: the entries as loaded, then as q.
-struct LaneEntries {
-    int32_t id[kPer];
-    float v[kPer], x[kPer];
-    float log_zq;
-};
-// report: names entries out of range in the error word
+// Entry j of row r (-1 and -inf: none); report: names one out of range in the error word
 template <typename T>
-__device__ __forceinline__ void load_entries(const Args<T>& a, int32_t r, const T* row, bool report, LaneEntries& n) {
-    const int lane = (int)lane_id();
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-        const int32_t j = lane + 32 * e;
-        n.id[e] = -1;
-        n.v[e] = -INFINITY;
-        if (j < a.k) {
-            const int32_t id = __ldg(a.ids + (int64_t)r * a.k + j);
-            const float v = __ldg(a.values + (int64_t)r * a.k + j);
-            if (id >= 0 && id < a.classes) n.id[e] = id, n.v[e] = v;
-            else if (id != -1 && report) dev_err(ERR_INDEX);
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) n.x[e] = n.id[e] >= 0 ? to_f(row[n.id[e]]) : 0.f;
+__device__ __forceinline__ void load_entry(const Args<T>& a, int32_t r, int32_t j, bool report, int32_t& id, float& v) {
+    id = -1;
+    v = -INFINITY;
+    if (j >= a.k) return;
+    const int32_t i = __ldg(a.ids + (int64_t)r * a.k + j);
+    const float w = __ldg(a.values + (int64_t)r * a.k + j);
+    if (i >= 0 && i < a.classes) id = i, v = w;
+    else if (i != -1 && report) dev_err(ERR_INDEX);
 }
-// v becomes (v - max) / T; the entries go to shared memory with their q (a used row:
-// at least one value is above -inf)
+
+// One warp: max v and log sum exp((v - max) / T), once the entries are there; q is put
+// beside them (a used row: at least one value is above -inf)
+struct Scale {
+    float m, log_zq;
+};
 template <typename T>
-__device__ __forceinline__ void share_entries(const Args<T>& a, LaneEntries& n, Entries& to) {
+__device__ __forceinline__ Scale scale_entries(const Args<T>& a, Entries& n) {
     const int lane = (int)lane_id();
     float m = -INFINITY, z = 0.f, q[kPer];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) m = fmaxf(m, n.v[e]);
+    for (int e = 0; e < kPer; ++e) {
+        q[e] = lane + 32 * e < a.k ? n.v[lane + 32 * e] : -INFINITY;
+        m = fmaxf(m, q[e]);
+    }
     m = warp_max(m);
     if (m == -INFINITY) m = 0.f;  // all of them NaN
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
-        q[e] = exp_from(n.v[e], m, a.l);
+        q[e] = exp_from(q[e], m, a.l);
         z += q[e];
-        n.v[e] = (n.v[e] - m) / a.temp;
     }
     z = warp_sum(z);
-    n.log_zq = logf(z);
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-        const int32_t j = lane + 32 * e;
-        if (j >= a.k) break;
-        to.id[j] = n.id[e];
-        to.q[j] = q[e] / z;
-        to.x[j] = n.x[e];
-    }
+    for (int e = 0; e < kPer; ++e)
+        if (lane + 32 * e < a.k) n.q[lane + 32 * e] = q[e] / z;
+    return {m, logf(z)};
 }
 // The row's loss (one warp, the same in every lane), from the row's maximum M and sum Z.
 template <typename T>
-__device__ __forceinline__ float loss_of(const Args<T>& a, const LaneEntries& n, const Entries& from, float M, float Z) {
+__device__ __forceinline__ float loss_of(const Args<T>& a, const Scale& c, const Entries& n, float M, float Z) {
     const int lane = (int)lane_id();
-    const float log_z = logf(Z);
+    const float log_z = logf(Z), inv = 1.f / a.temp;
     float s = 0.f;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
         const int32_t j = lane + 32 * e;
         if (j >= a.k) break;
-        const float q = from.q[j];
+        const float q = n.q[j], x = n.x[j];
         if (q == 0.f) continue;
-        if (n.x[e] == -INFINITY && Z == Z) s += INFINITY;
-        else s = fmaf(q, (n.v[e] - n.log_zq) + (log_z - (n.x[e] - M) / a.temp), s);
+        if (x == -INFINITY && Z == Z) s += INFINITY;
+        else s = fmaf(q, ((n.v[j] - c.m) * inv - c.log_zq) + (log_z - (x - M) * inv), s);
     }
     return warp_sum(s) * (a.temp * a.temp);
+}
+// One warp: all entries of a row, for itself.
+template <typename T>
+__device__ __forceinline__ void load_entries(const Args<T>& a, int32_t r, const T* row, bool report, Entries& n) {
+    int32_t id[kPer];
+    float v[kPer], x[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) load_entry(a, r, (int32_t)lane_id() + 32 * e, report, id[e], v[e]);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) x[e] = id[e] >= 0 ? to_f(row[id[e]]) : 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+        const int32_t j = (int32_t)lane_id() + 32 * e;
+        n.id[j] = id[e];
+        n.v[j] = v[e];
+        n.x[j] = x[e];
+    }
 }
 // The gradient at entry j's class; false where there is none.
 template <typename T>
@@ -150,8 +153,13 @@ __device__ __forceinline__ bool entry_grad(const Args<T>& a, const Entries& n, i
     const int32_t id = n.id[j];
     if (id < 0) return false;
     float q = 0.f;
-    for (int32_t i = 0; i < a.k; ++i)
-        if (n.id[i] == id) q += n.q[i];
+    for (int32_t i = 0; i < a.k; i += 4) {
+        const int4 o = *reinterpret_cast<const int4*>(n.id + i);
+        if (o.x == id) q += n.q[i];
+        if (o.y == id) q += n.q[i + 1];
+        if (o.z == id) q += n.q[i + 2];
+        if (o.w == id) q += n.q[i + 3];
+    }
     g = Z == 0.f ? 0.f : fmaf(w / Z, exp_from(n.x[j], M, a.l), -w * q);
     return true;
 }
@@ -183,9 +191,8 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill_warp(Args<T> a) {
     for (int32_t r = (int32_t)blockIdx.x * kWarps + (int32_t)(threadIdx.x >> 5); r < n; r += (int32_t)gridDim.x * kWarps) {
         const T* row = a.x + (int64_t)r * a.ld;
         T* out = a.grad ? a.grad + (int64_t)r * a.ld_grad : nullptr;
-        LaneEntries le;
-        load_entries(a, r, row, true, le);
-        const bool used = is_used(__shfl_sync(0xFFFFFFFFu, le.id[0], 0), __shfl_sync(0xFFFFFFFFu, le.v[0], 0), a.classes);
+        const bool used = row_used(a, r);
+        load_entries(a, r, row, true, mine);
         if (!used) {
             if (lane == 0) a.loss[r] = 0.f;
             if (out)
@@ -201,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill_warp(Args<T> a) {
         }
         const int32_t ce = part.edge(lane);
         const float xe = ce >= 0 ? to_f(row[ce]) : -INFINITY;
-        share_entries(a, le, mine);
+        const Scale scale = scale_entries(a, mine);  // (each lane's own entries)
         float m = xe;
 #pragma unroll
         for (int k = 0; k < NV; ++k) m = fmaxf(m, part_max<T>(x[k]));
@@ -214,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill_warp(Args<T> a) {
         float z, z1;
         unpair(sum, z, z1);
         z = warp_sum(z + z1 + base.of(xe));
-        const float loss = loss_of(a, le, mine, m, z);
+        const float loss = loss_of(a, scale, mine, m, z);
         if (lane == 0) a.loss[r] = loss;
         if (!out) continue;
         const bool same = same_phase(row, (const T*)out);
@@ -278,17 +285,17 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_row(Args<T> a) {
     const int32_t edge = rank == 0 && threadIdx.x < 32 ? part.edge((int)threadIdx.x) : -1;
     const T* p = row + part.head + (v0 + (int32_t)threadIdx.x) * kE<T>;
     const bool mine = threadIdx.x < 32 && (rank == 0 || out);  // the warp of the entries
-    LaneEntries le;
+    Scale scale = {0.f, 0.f};
     Held<T, NT> h;
     h.m = 0.f, h.z = 0.f;
-    if (mine) load_entries(a, r, row, rank == 0, le);
+    if (mine) load_entries(a, r, row, rank == 0, entries);
     if (used) {
 #pragma unroll
         for (int k = 0; k < kVecs; ++k)
             h.x[k] = (int32_t)threadIdx.x + k * NT < count ? *reinterpret_cast<const uint4*>(p + k * NT * kE<T>)
                                                            : empty_part<T>();
         h.xe = edge >= 0 ? to_f(row[edge]) : -INFINITY;
-        if (mine) share_entries(a, le, entries);
+        if (mine) scale = scale_entries(a, entries);
         float mr = -INFINITY, zr = 0.f;  // the part past the registers
         for (int32_t i = (int32_t)threadIdx.x + kVecs * NT; i < count; i += NT) {
             const T* q = row + part.head + (v0 + i) * kE<T>;
@@ -320,7 +327,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_row(Args<T> a) {
             }
         }
         if (rank == 0 && threadIdx.x < 32) {
-            const float loss = loss_of(a, le, entries, M, Z);
+            const float loss = loss_of(a, scale, entries, M, Z);
             if (threadIdx.x == 0) a.loss[r] = loss;
         }
         __syncthreads();  // the vectors are stored
@@ -343,7 +350,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_row(Args<T> a) {
 
 // Many long rows: the same, with each cluster walking over its rows and the next two
 // rows' slices on their way into shared memory while the current row is worked on.
-constexpr int kStreamVecs = 3400;  // of a CTA's slice: two buffers of it and the entries, two CTAs an SM
+// The entries take two dependent loads (the class, then its logit), so they are
+// loaded two rows ahead and their logits one row ahead, an entry a thread, and handed
+// over at the block's barrier of the row before (loaded by one warp at the row's
+// start: 284 us for 4096 x 50,257 bf16, now SPEED_STREAM).
+constexpr int kStreamVecs = 3300;  // of a CTA's slice: two buffers of it and the entries, two CTAs an SM
 
 template <typename T, int NT, int S>
 __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_stream(Args<T> a, int32_t slots) {
@@ -352,7 +363,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_stream(Args<T> a, int
     constexpr int kParts = S * NT / 32;
     __shared__ __align__(8) float2 parts[2][kParts];  // (m, z) of every warp of the cluster, of used rows in turn
     __shared__ __align__(8) uint64_t full[2], met[2];  // buffers; parts
-    __shared__ Entries entries[2];                     // of used rows in turn
+    __shared__ Entries entries[3];                     // of rows in turn
     __shared__ bool last;
     const int32_t rank = (int32_t)(blockIdx.x % S), first = (int32_t)(blockIdx.x / S), step = (int32_t)(gridDim.x / S);
     const int32_t n = rows_of(a.d_n, a.n_cap), classes = a.classes;
@@ -389,20 +400,40 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_stream(Args<T> a, int
         fetch(first + step, u1, 1);
     }
     const float w = weight_of(a);
-    const bool mine = threadIdx.x < 32 && (rank == 0 || a.grad);  // the warp of the entries
+    const bool mine = threadIdx.x < 32 && (rank == 0 || a.grad);  // the warp that scales the entries
+    // this thread's entry: j of the next row, then of the row after it
+    const int32_t j = (int32_t)threadIdx.x;
+    int32_t id1 = -1, id2 = -1;
+    float v1 = -INFINITY, v2 = -INFINITY;
+    const auto hand_over = [&](Entries& to, float x) {
+        if (j < SG_MAX_TOP) to.id[j] = id1, to.v[j] = v1, to.x[j] = x;
+    };
+    const auto logit_at = [&](int32_t r, int32_t id) { return id >= 0 ? to_f(a.x[(int64_t)r * a.ld + id]) : 0.f; };
+    load_entry(a, first, j, rank == 0, id1, v1);
+    if (first + step < n) load_entry(a, first + step, j, rank == 0, id2, v2);
+    hand_over(entries[0], logit_at(first, id1));
+    id1 = id2, v1 = v2;
+    __syncthreads();
     uint32_t phases = 0;  // bits 0, 1: parity of the next phase of full[0], full[1]; bits 2, 3: of met[0], met[1]
     int32_t par = 0;      // the row's buffer: alternates over all rows
-    int32_t slot = 0;     // its parts, met and entries: alternate over the used rows only
+    int32_t slot = 0;     // its parts and met: alternate over the used rows only
+    int32_t turn = 0;     // its entries
     for (int32_t r = first; r < n; r += step, par ^= 1, u0 = u1, u1 = u2) {
         u2 = has(r + 2 * step);
         const T* row = a.x + (int64_t)r * a.ld;
         T* out = a.grad ? a.grad + (int64_t)r * a.ld_grad : nullptr;
-        LaneEntries le;
-        if (mine) load_entries(a, r, row, rank == 0, le);
+        const float x1 = logit_at(r + step, id1);
+        id2 = -1, v2 = -INFINITY;
+        if (r + 2 * step < n) load_entry(a, r + 2 * step, j, rank == 0, id2, v2);
+        Entries& entry = entries[turn];
+        turn = turn == 2 ? 0 : turn + 1;
         if (!u0) {  // the same in the whole cluster
             if (rank == 0 && threadIdx.x == 0) a.loss[r] = 0.f;
             if (out) zero_row<T, NT>(out, classes, rank, S);
             if (threadIdx.x == 0) fetch(r + 2 * step, u2, par);  // this row's buffer was not filled
+            hand_over(entries[turn], x1);
+            id1 = id2, v1 = v2;
+            __syncthreads();
             continue;
         }
         const RowParts<T> part(row, classes);
@@ -410,7 +441,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_stream(Args<T> a, int
         const int32_t edge = rank == 0 && threadIdx.x < 32 ? part.edge((int)threadIdx.x) : -1;
         Held<T, NT> h;
         h.xe = edge >= 0 ? to_f(row[edge]) : -INFINITY;
-        if (mine) share_entries(a, le, entries[slot]);
+        Scale scale = {0.f, 0.f};
+        if (mine) scale = scale_entries(a, entry);
         if (!mbar_wait(&full[par], (phases >> par) & 1u) && lane_id() == 0) dev_err(ERR_TIMEOUT);
         const uint4* buf = reinterpret_cast<const uint4*>(dsm) + par * slots + threadIdx.x;
 #pragma unroll
@@ -442,15 +474,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_stream(Args<T> a, int
             if (edge >= 0) put(out + edge, inv * Base(h.m, a.l).of(h.xe));
         }
         if (rank == 0 && threadIdx.x < 32) {
-            const float loss = loss_of(a, le, entries[slot], M, Z);
+            const float loss = loss_of(a, scale, entry, M, Z);
             if (threadIdx.x == 0) a.loss[r] = loss;
         }
-        if (out) {
-            // The vectors are stored.  (Entries are written again two used rows later,
-            // after this barrier of the used row between.)
-            __syncthreads();
-            put_entries(a, entries[slot], out, part, v0, count, rank, w, M, Z);
-        }
+        hand_over(entries[turn], x1);
+        id1 = id2, v1 = v2;
+        // The vectors are stored, and the next row's entries there.  (Entries are
+        // written again two rows later, after the barrier of the row between.)
+        __syncthreads();
+        if (out) put_entries(a, entry, out, part, v0, count, rank, w, M, Z);
         slot ^= 1;
     }
     __threadfence();

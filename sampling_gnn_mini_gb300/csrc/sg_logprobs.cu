@@ -5,15 +5,18 @@
 //   the k largest by (x descending, class ascending) with their log probabilities.
 // Bound by memory: the logits are read once and next to nothing is written.
 //
-// Rows of a few hundred classes stay in a warp's registers (k_logprobs_warp).
-// Longer ones stream past 256 threads, or a cluster of 2 to 8 such CTAs when rows
-// are few (k_logprobs_row).  Each thread keeps (m, z, t) of what it has seen,
-// relative to its own running maximum, and the maximum of each group of vectors.
-// The k-th largest of some of the threads' maxima is a lower bound of the k-th
-// largest logit, so only groups that reach it are read again (from L2), and only
-// the logits that reach it become candidates: about k of them, whatever the row's
-// length.  Where they are many all the same (equal logits, masks by one value),
-// the bound is raised by bisection, and logits equal to it are taken in order.
+// Many rows of up to 64 classes go through shared memory to a thread each
+// (k_logprobs_few), rows of a few hundred stay in a warp's registers
+// (k_logprobs_warp).  Longer ones stream past 256 threads, or a cluster of 2 to 8 such
+// CTAs when rows are few (k_logprobs_row): each thread copies its own vectors
+// asynchronously, those of the next row already while this row's classes are chosen.
+// A thread keeps (m, z, t) of what it has seen, relative to its own running maximum,
+// and the maximum of each group of vectors.  The k-th largest of some of the threads'
+// maxima is a lower bound of the k-th largest logit, so only groups that reach it are
+// read again (from L2), and only the logits that reach it become candidates: about k
+// of them, whatever the row's length.  Where they are many all the same (equal
+// logits, masks by one value), the bound is raised by bisection, and logits equal to it
+// are taken in order.
 //
 // Logits of -inf take no part.  x - m is formed before the scaling by log2(e), so
 // a row's level costs no accuracy, and exponents are cut off at -200, where the
@@ -30,9 +33,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTurn = 4;      // vectors a thread loads at a time
+constexpr int kTurn = 4;      // vectors a thread takes at a time
+constexpr int kRing = 2;      // turns of them in shared memory
 constexpr int kGroups = 16;   // groups of a thread's vectors, at most
 constexpr int kCap = 512;     // candidates a CTA holds; at least 4 SG_MAX_TOP for the bound's slack
+constexpr int kHits = 512;    // groups it reads again
+constexpr int kWarpCap = 256; // candidates a warp holds
 constexpr float kNone = -200.f;  // 2^x is 0 from here on
 
 template <typename T>
@@ -137,14 +143,157 @@ __device__ __forceinline__ void unpack(const uint4& u, float (&f)[kE<T>]) {
     for (int i = 0; i < kE<T> / 2; ++i) unpair(p[i], f[2 * i], f[2 * i + 1]);
 }
 
+// ------------------------------------------------------------ rows by threads
+// kFewRows rows of up to kFewClasses classes to a block, in shared memory (a pitch that
+// is odd, so that threads meet different banks), then a thread a row.  A thread's top
+// K sit in registers in order: a logit moves in where it is larger, so that equal ones
+// stay in the order of their classes.  magic: ceil(2^32 / classes).
+constexpr int kFewRows = 128, kFewClasses = 64, kFewTop = 8;
+
+template <typename T, int K>
+__global__ void __launch_bounds__(kFewRows) k_logprobs_few(Args<T> a, uint32_t magic) {
+    extern __shared__ float rows[];
+    pdl_start();
+    const int32_t n = rows_of(a.d_n, a.n_cap), r0 = (int32_t)blockIdx.x * kFewRows, classes = a.classes;
+    if (r0 >= n) return;
+    const int32_t pitch = classes | 1, all = min(kFewRows, n - r0) * classes;
+    const T* x = a.x + (int64_t)r0 * a.ld;
+    for (int32_t i0 = (int32_t)threadIdx.x; i0 < all; i0 += 8 * kFewRows) {
+        T v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int32_t i = i0 + u * kFewRows;
+            const int32_t row = (int32_t)__umulhi((uint32_t)i, magic);
+            if (i < all) v[u] = x[row * a.ld + (i - row * classes)];
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int32_t i = i0 + u * kFewRows;
+            const int32_t row = (int32_t)__umulhi((uint32_t)i, magic);
+            if (i < all) rows[row * pitch + (i - row * classes)] = to_f(v[u]);
+        }
+    }
+    __syncthreads();
+    const int32_t r = r0 + (int32_t)threadIdx.x;
+    if (r >= n) return;
+    const float* row = rows + (int32_t)threadIdx.x * pitch;
+    const int32_t y = label_of(a, r);
+    const float xy = y >= 0 ? row[y] : 0.f;
+    float top[K];
+    int32_t at[K];
+#pragma unroll
+    for (int j = 0; j < K; ++j) top[j] = -INFINITY, at[j] = -1;
+#pragma unroll 4
+    for (int32_t c = 0; c < classes; ++c) {
+        float v = row[c];
+        if (v > top[K - 1]) {
+            int32_t i = c;
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                if (v > top[j]) {
+                    const float w = top[j];
+                    const int32_t q = at[j];
+                    top[j] = v, at[j] = i;
+                    v = w, i = q;
+                }
+        }
+    }
+    Stat s = {top[0], 0.f, 0.f};
+    const float b = finite_base(s.m);
+#pragma unroll 4
+    for (int32_t c = 0; c < classes; ++c) {
+        const float d = max_nan((row[c] - b) * kLog2e, kNone), e = ex2(d);
+        s.z += e;
+        s.t = fmaf(e, d, s.t);
+    }
+    const float log_z = logf(s.z);
+    put_row(a, r, s, log_z, y, xy);
+    const bool bad = s.z != s.z;
+    int32_t* ids = a.top_ids + (int64_t)r * a.k;
+    float* lps = a.top_logp + (int64_t)r * a.k;
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+        if (j < a.k) {
+            ids[j] = bad ? -1 : at[j];
+            lps[j] = bad ? s.z : at[j] < 0 ? -INFINITY : logp_of(top[j], s.m, log_z);
+        }
+}
+
 // ------------------------------------------------------------ rows by warps
-// A warp a row, in NV vectors a lane.  The top classes are taken one by one: each
-// lane offers its best, the warp takes the best of them.
+// The logits of a lane as orders: 0 once taken.
+template <typename T, int NV>
+struct LaneOrders {
+    static constexpr int E = NV * kE<T>;
+    uint32_t o[E], edge;
+    int32_t first, edge_class;  // class of o[0]; element e's is first + (e / kE) 32 kE + e % kE
+    __device__ __forceinline__ int32_t class_at(int e) const { return first + e / kE<T> * 32 * kE<T> + e % kE<T>; }
+};
+// The k best one by one, each the best of what the lanes offer, into ids and lps.
+template <typename T, int NV>
+__device__ __forceinline__ void take_in_turn(LaneOrders<T, NV>& l, int32_t k, float m, float log_z, int32_t* ids, float* lps) {
+    constexpr int E = LaneOrders<T, NV>::E;
+    const int lane = (int)lane_id();
+    for (int32_t j = 0; j < k; ++j) {
+        uint32_t best = l.edge;
+#pragma unroll
+        for (int e = 0; e < E; ++e) best = max(best, l.o[e]);
+        best = __reduce_max_sync(0xFFFFFFFFu, best);
+        if (best <= kOrderNone) {  // nothing is left
+            for (int32_t i = j + lane; i < k; i += 32) ids[i] = -1, lps[i] = -INFINITY;
+            return;
+        }
+        uint32_t c = l.edge == best ? (uint32_t)l.edge_class : 0xFFFFFFFFu;
+#pragma unroll
+        for (int e = E - 1; e >= 0; --e)
+            if (l.o[e] == best) c = min(c, (uint32_t)l.class_at(e));
+        c = __reduce_min_sync(0xFFFFFFFFu, c);
+        if (l.edge == best && l.edge_class == (int32_t)c) l.edge = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (l.o[e] == best && l.class_at(e) == (int32_t)c) l.o[e] = 0;
+        if (lane == 0) {
+            ids[j] = (int32_t)c;
+            lps[j] = logp_of(value_of(best), m, log_z);
+        }
+    }
+}
+// A lower bound of the k-th largest order: the largest found by bisection that at
+// least k of the lanes' G maxima reach (the lowest order if they are fewer).
+template <int G>
+__device__ __forceinline__ uint32_t bound_of(const uint32_t (&g)[G], int32_t k, uint32_t top) {
+    const auto reach = [&](uint32_t o) {
+        int32_t c = 0;
+#pragma unroll
+        for (int i = 0; i < G; ++i) c += __popc(__ballot_sync(0xFFFFFFFFu, g[i] >= o));
+        return c;
+    };
+    uint32_t lo = kOrderNone + 1, hi = top + 1;
+    if (reach(lo) < k) return lo;
+    while (hi - lo > 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        const int32_t c = reach(mid);
+        if (c < k) {
+            hi = mid;
+        } else {
+            lo = mid;
+            if (c <= k + k / 8) break;
+        }
+    }
+    return lo;
+}
+
+// A warp a row, in NV vectors a lane.  Up to kInTurn top classes are taken one by one;
+// for more, the logits that reach a bound are listed and ranked.
+constexpr int kInTurn = 4;
+
 template <typename T, int NV>
 __global__ void __launch_bounds__(kThreads) k_logprobs_warp(Args<T> a) {
     pdl_start();
-    const int lane = (int)lane_id();
-    const int32_t n = rows_of(a.d_n, a.n_cap), r = (int32_t)blockIdx.x * kWarps + (int32_t)(threadIdx.x >> 5);
+    constexpr int E = NV * kE<T>;
+    __shared__ unsigned long long lists[kWarps][kWarpCap];
+    __shared__ int32_t counts[kWarps];
+    const int lane = (int)lane_id(), warp = (int)(threadIdx.x >> 5);
+    const int32_t n = rows_of(a.d_n, a.n_cap), r = (int32_t)blockIdx.x * kWarps + warp;
     if (r >= n) return;
     const T* row = a.x + (int64_t)r * a.ld;
     const RowParts<T> part(row, a.classes);
@@ -178,41 +327,68 @@ __global__ void __launch_bounds__(kThreads) k_logprobs_warp(Args<T> a) {
     s.t = warp_sum(t0 + t1);
     const float log_z = logf(s.z);
     if (lane == 0) put_row(a, r, s, log_z, y, xy);
+    if (a.k == 0) return;
     int32_t* ids = a.top_ids + (int64_t)r * a.k;
     float* lps = a.top_logp + (int64_t)r * a.k;
-    const bool bad = s.z != s.z;
-    float f[NV][kE<T>];
+    if (s.z != s.z) {
+        for (int32_t i = lane; i < a.k; i += 32) ids[i] = -1, lps[i] = s.z;
+        return;
+    }
+    LaneOrders<T, NV> l;
+    l.first = part.head + lane * kE<T>;
+    l.edge = order_of(xe);
+    l.edge_class = ce;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) unpack<T>(x[k], f[k]);
-    unsigned long long last = ~0ull;  // the entry taken last
-    for (int32_t j = 0; j < a.k; ++j) {
-        unsigned long long best = 0;
-        if (!bad) {
+    for (int k = 0; k < NV; ++k) {
+        float f[kE<T>];
+        unpack<T>(x[k], f);
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
+        for (int e = 0; e < kE<T>; ++e) l.o[k * kE<T> + e] = order_of(f[e]);
+    }
+    if (a.k <= kInTurn) {
+        take_in_turn(l, a.k, s.m, log_z, ids, lps);
+        return;
+    }
+    // groups: the lanes for few classes, up to 8 a lane for more
+    constexpr int G = E < 8 ? E : 8;
+    uint32_t g[G], all = l.edge;
 #pragma unroll
-                for (int e = 0; e < kE<T>; ++e) {
-                    const unsigned long long q = entry_of(order_of(f[k][e]), part.head + (lane + 32 * k) * kE<T> + e);
-                    if (q < last && q > best) best = q;
-                }
-            const unsigned long long q = entry_of(order_of(xe), ce);
-            if (ce >= 0 && q < last && q > best) best = q;
-        }
-        const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(best >> 32));
-        if (hi <= kOrderNone) {  // nothing is left
-            for (int32_t i = j + lane; i < a.k; i += 32) {
-                ids[i] = -1;
-                lps[i] = bad ? s.z : -INFINITY;
-            }
-            break;
-        }
-        const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
-        last = (unsigned long long)hi << 32 | lo;
-        if (lane == 0) {
-            ids[j] = class_of(last);
-            lps[j] = logp_of(value_of(hi), s.m, log_z);
+    for (int i = 0; i < G; ++i) {
+        g[i] = i == 0 ? l.edge : 0u;
+#pragma unroll
+        for (int e = 0; e < E / G; ++e) g[i] = max(g[i], l.o[i * (E / G) + e]);
+        all = max(all, g[i]);
+    }
+    const uint32_t one[1] = {all};
+    const uint32_t most = order_of(s.m);
+    const uint32_t tau = a.k <= 16 ? bound_of<1>(one, a.k, most) : bound_of<G>(g, a.k, most);
+    if (lane == 0) counts[warp] = 0;
+    __syncwarp();
+    unsigned long long* list = lists[warp];
+    const auto offer = [&](uint32_t o, int32_t c) {
+        if (o < tau) return;
+        const int32_t at = atomicAdd(&counts[warp], 1);
+        if (at < kWarpCap) list[at] = entry_of(o, c);
+    };
+    offer(l.edge, ce);
+#pragma unroll
+    for (int e = 0; e < E; ++e) offer(l.o[e], l.class_at(e));
+    __syncwarp();
+    const int32_t found = counts[warp];
+    if (found > kWarpCap) {  // equal logits by the hundred
+        take_in_turn(l, a.k, s.m, log_z, ids, lps);
+        return;
+    }
+    for (int32_t i = lane; i < found; i += 32) {
+        const unsigned long long e = list[i];
+        int32_t before = 0;
+        for (int32_t q = 0; q < found; ++q) before += list[q] > e;
+        if (before < a.k) {
+            ids[before] = class_of(e);
+            lps[before] = logp_of(value_of((uint32_t)(e >> 32)), s.m, log_z);
         }
     }
+    for (int32_t i = found + lane; i < a.k; i += 32) ids[i] = -1, lps[i] = -INFINITY;
 }
 
 // --------------------------------------------------------- rows by clusters
@@ -326,165 +502,216 @@ __device__ __forceinline__ float warp_sort(float x) {
 
 template <typename T, int S>
 __global__ void __launch_bounds__(kThreads, 4) k_logprobs_row(Args<T> a, int32_t turns) {
-    extern __shared__ __align__(16) uint8_t dsm[];  // groups' maxima; then all candidates
+    extern __shared__ __align__(16) uint4 ring[];  // kRing turns; CTA 0's candidates of all; then the groups' maxima
     pdl_start();
     constexpr int W = S * kWarps;
     __shared__ __align__(16) float4 parts[W];
     __shared__ float tops[SG_MAX_TOP + W];
     __shared__ Candidates list;
+    __shared__ int32_t hits[kHits], hit_count;
     __shared__ float bound;
     __shared__ int32_t scan[kThreads / 32 + 1];
     const int warp = (int)(threadIdx.x >> 5), lane = (int)lane_id();
-    const int32_t r = (int32_t)(blockIdx.x / S), rank = (int32_t)(blockIdx.x % S);
+    const int32_t first = (int32_t)(blockIdx.x / S), rank = (int32_t)(blockIdx.x % S), step = (int32_t)(gridDim.x / S);
     const int32_t n = rows_of(a.d_n, a.n_cap);
-    if (r >= n) return;  // the whole cluster
+    if (first >= n) return;  // the whole cluster
     if constexpr (S > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
-    float* gmax = reinterpret_cast<float*>(dsm) + threadIdx.x;
-    const T* row = a.x + (int64_t)r * a.ld;
-    const RowParts<T> part(row, a.classes);
-    const int32_t per = (part.vecs + S - 1) / S, v0 = min(part.vecs, rank * per);
-    Slice<T> sl = {row, part, v0, min(part.vecs, v0 + per) - v0, rank == 0 && warp == 0 ? part.edge(lane) : -1, -INFINITY};
-    if (sl.edge >= 0) sl.xe = to_f(row[sl.edge]);
-    int32_t y = -1;
-    float xy = 0.f;
-    if (rank == 0 && threadIdx.x == 0) {
-        y = label_of(a, r);
-        if (y >= 0) xy = to_f(row[y]);
-    }
-    Stat s = stat_of(sl.xe);
-    float most = sl.xe;
-    const int32_t span = turns * kTurn * kThreads;  // vectors of a group, over the block
-    for (int32_t g0 = 0, g = 0; g0 < sl.count; g0 += span, ++g) {
-        float gm = -INFINITY;
-        for (int32_t i0 = g0; i0 < min(sl.count, g0 + span); i0 += kTurn * kThreads) {
-            uint4 u[kTurn];
-            float top = -INFINITY;
+    float* gmax = reinterpret_cast<float*>(ring + (S > 1 && S * kCap > 2 * kRing * kTurn * kThreads ? S * kCap / 2 : kRing * kTurn * kThreads)) + threadIdx.x;
+    const auto slice_of = [&](int32_t r) {
+        const T* row = a.x + (int64_t)r * a.ld;
+        const RowParts<T> part(row, a.classes);
+        const int32_t per = (part.vecs + S - 1) / S, v0 = min(part.vecs, rank * per);
+        return Slice<T>{row, part, v0, min(part.vecs, v0 + per) - v0, -1, -INFINITY};
+    };
+    // The copies run ahead: turn ft of row fr is the next one to be copied.
+    int32_t fr = first, ft = 0, fcount;
+    const T* from;
+    const auto enter = [&] {
+        if (fr >= n) return;
+        const Slice<T> sl = slice_of(fr);
+        from = sl.row + sl.first((int32_t)threadIdx.x);
+        fcount = sl.count - (int32_t)threadIdx.x;
+    };
+    const auto fetch = [&](int at) {
+        if (fr < n) {
 #pragma unroll
             for (int k = 0; k < kTurn; ++k) {
-                const int32_t i = i0 + k * kThreads + (int32_t)threadIdx.x;
-                u[k] = i < sl.count ? sl.load(i) : empty_part<T>();
+                const int32_t i = (ft * kTurn + k) * kThreads;
+                if (i < fcount) copy_async(ring + (at * kTurn + k) * kThreads + threadIdx.x, from + i * kE<T>);
             }
-#pragma unroll
-            for (int k = 0; k < kTurn; ++k) top = fmaxf(top, part_max<T>(u[k]));
-            gm = fmaxf(gm, top);
-            rebase(s, fmaxf(s.m, top));
-            f2 z = pair(s.z, 0.f), t = pair(s.t, 0.f);
-            const float b = -finite_base(s.m);
-#pragma unroll
-            for (int k = 0; k < kTurn; ++k) {
-                repack(u[k]);
-                add_part<T>(u[k], pair(b, b), z, t);
+            if (++ft * kTurn * kThreads >= fcount + (int32_t)threadIdx.x) {  // the same in the whole block
+                fr += step;
+                ft = 0;
+                enter();
             }
-            float z1, t1;
-            unpair(z, s.z, z1);
-            unpair(t, s.t, t1);
-            s.z += z1;
-            s.t += t1;
         }
-        gmax[g * kThreads] = gm;
-        most = fmaxf(most, gm);
-    }
-    s = warp_join(s);
-    // the warp's j largest of its lanes' maxima
-    const int32_t j = (a.k + W - 1) / W, M = W * j;
-    if (j == 1) most = s.m;
-    else if (j > 1) most = warp_sort(most);
-    if constexpr (S > 1) asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");  // every CTA runs
-    const int32_t w = rank * kWarps + warp;
-    if constexpr (S > 1) {
-        if (lane < S)
-            st_cluster4(map_rank(smem_addr(parts + w), (uint32_t)lane),
-                        make_uint4(__float_as_uint(s.m), __float_as_uint(s.z), __float_as_uint(s.t), 0u));
-        if (lane < j)
-            for (uint32_t q = 0; q < S; ++q)
-                asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(map_rank(smem_addr(tops + w * j + lane), q)), "f"(most)
-                             : "memory");
-        cluster_sync();
-    } else {
-        if (lane == 0) parts[w] = make_float4(s.m, s.z, s.t, 0.f);
-        if (lane < j) tops[w * j + lane] = most;
-        __syncthreads();
-    }
-    // the whole row's, in every warp
-    s = {-INFINITY, 0.f, 0.f};
+        copies_end();
+    };
+    enter();
 #pragma unroll
-    for (int i = 0; i < (W + 31) / 32; ++i)
-        if (lane + 32 * i < W) {
-            const float4 p = parts[lane + 32 * i];
-            Stat o = {p.x, p.y, p.z};
-            const float m = fmaxf(s.m, o.m);
-            rebase(s, m);
-            rebase(o, m);
-            s.z += o.z;
-            s.t += o.t;
+    for (int i = 0; i < kRing - 1; ++i) fetch(i);
+    int at = 0;
+    for (int32_t r = first; r < n; r += step) {
+        Slice<T> sl = slice_of(r);
+        if (rank == 0 && warp == 0) sl.edge = sl.part.edge(lane);
+        if (sl.edge >= 0) sl.xe = to_f(sl.row[sl.edge]);
+        int32_t y = -1;
+        float xy = 0.f;
+        if (rank == 0 && threadIdx.x == 0) {
+            y = label_of(a, r);
+            if (y >= 0) xy = to_f(sl.row[y]);
         }
-    s = warp_join(s);
-    const float log_z = logf(s.z);
-    if (rank == 0 && threadIdx.x == 0) put_row(a, r, s, log_z, y, xy);
-    if (a.k == 0) return;  // (the last access to another CTA's memory is before the barrier)
-    if ((int32_t)threadIdx.x < M) {  // the k-th largest of tops
-        const float v = tops[threadIdx.x];
-        int32_t before = 0;
-        for (int32_t q = 0; q < M; ++q) before += tops[q] > v || (tops[q] == v && q < (int32_t)threadIdx.x);
-        if (before == a.k - 1) bound = v;
-    }
-    if (threadIdx.x == 0) list.count = 0;
-    __syncthreads();
-    const float tau = bound;
-    const bool bad = s.z != s.z;
-    if (!bad) {
-        if (sl.xe >= tau && sl.xe > -INFINITY) offer(list, sl.xe, sl.edge);
+        Stat s = stat_of(sl.xe);
+        float most = sl.xe;
+        const int32_t span = turns * kTurn * kThreads;  // vectors of a group, over the block
         for (int32_t g0 = 0, g = 0; g0 < sl.count; g0 += span, ++g) {
-            const float gm = gmax[g * kThreads];
-            if (gm < tau || gm == -INFINITY) continue;
-            for (int32_t i = g0 + (int32_t)threadIdx.x; i < min(sl.count, g0 + span); i += kThreads) {
-                const uint4 u = sl.load(i);
-                if (part_max<T>(u) < tau) continue;
-                float f[kE<T>];
-                unpack<T>(u, f);
+            float gm = -INFINITY;
+            for (int32_t i0 = g0; i0 < min(sl.count, g0 + span); i0 += kTurn * kThreads) {
+                fetch(at ? at - 1 : kRing - 1);
+                copies_wait<kRing - 1>();
+                uint4 u[kTurn];
+                float top = -INFINITY;
 #pragma unroll
-                for (int e = 0; e < kE<T>; ++e)
-                    if (f[e] >= tau && f[e] > -INFINITY) offer(list, f[e], sl.first(i) + e);
-            }
-        }
-    }
-    __syncthreads();
-    if (list.count > kCap)
-        select_exactly(sl, rank, max(order_of(tau), kOrderNone + 1), order_of(s.m), a.k, list, scan);
-    const unsigned long long* all = list.e;
-    int32_t total = list.count;
-    if constexpr (S > 1) {  // CTA 0 takes everybody's
-        cluster_sync();
-        if (rank == 0) {
-            unsigned long long* to = reinterpret_cast<unsigned long long*>(dsm);
-            total = 0;
-            for (uint32_t q = 0; q < S; ++q) {
-                const int32_t c = __float_as_int(ld_cluster(map_rank(smem_addr(&list.count), q)));
-                for (int32_t i = threadIdx.x; i < c; i += kThreads) {
-                    const uint32_t from = map_rank(smem_addr(&list.e[i]), q);
-                    asm volatile("ld.shared::cluster.b64 %0, [%1];\n" : "=l"(to[total + i]) : "r"(from) : "memory");
+                for (int k = 0; k < kTurn; ++k) {
+                    const int32_t i = i0 + k * kThreads + (int32_t)threadIdx.x;
+                    u[k] = i < sl.count ? ring[(at * kTurn + k) * kThreads + threadIdx.x] : empty_part<T>();
                 }
-                total += c;
+                if (++at == kRing) at = 0;
+#pragma unroll
+                for (int k = 0; k < kTurn; ++k) top = fmaxf(top, part_max<T>(u[k]));
+                gm = fmaxf(gm, top);
+                rebase(s, fmaxf(s.m, top));
+                f2 z = pair(s.z, 0.f), t = pair(s.t, 0.f);
+                const float b = -finite_base(s.m);
+#pragma unroll
+                for (int k = 0; k < kTurn; ++k) {
+                    repack(u[k]);
+                    add_part<T>(u[k], pair(b, b), z, t);
+                }
+                float z1, t1;
+                unpair(z, s.z, z1);
+                unpair(t, s.t, t1);
+                s.z += z1;
+                s.t += t1;
             }
-            all = to;
+            gmax[g * kThreads] = gm;
+            most = fmaxf(most, gm);
         }
-        cluster_sync();  // the lists stay until they are read
-        if (rank != 0) return;
-    }
-    int32_t* ids = a.top_ids + (int64_t)r * a.k;
-    float* lps = a.top_logp + (int64_t)r * a.k;
-    for (int32_t i = threadIdx.x; i < total; i += kThreads) {
-        const unsigned long long e = all[i];
-        int32_t before = 0;
-        for (int32_t q = 0; q < total; ++q) before += all[q] > e;
-        if (before < a.k) {
-            ids[before] = class_of(e);
-            lps[before] = logp_of(value_of((uint32_t)(e >> 32)), s.m, log_z);
+        s = warp_join(s);
+        // the warp's j largest of its lanes' maxima
+        const int32_t j = (a.k + W - 1) / W, M = W * j;
+        if (j == 1) most = s.m;
+        else if (j > 1) most = warp_sort(most);
+        const int32_t w = rank * kWarps + warp;
+        if constexpr (S > 1) {
+            asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");  // every CTA runs (a cluster has one row)
+            if (lane < S)
+                st_cluster4(map_rank(smem_addr(parts + w), (uint32_t)lane),
+                            make_uint4(__float_as_uint(s.m), __float_as_uint(s.z), __float_as_uint(s.t), 0u));
+            if (lane < j)
+                for (uint32_t q = 0; q < S; ++q)
+                    asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(map_rank(smem_addr(tops + w * j + lane), q)),
+                                 "f"(most)
+                                 : "memory");
+            cluster_sync();
+        } else {
+            if (lane == 0) parts[w] = make_float4(s.m, s.z, s.t, 0.f);
+            if (lane < j) tops[w * j + lane] = most;
+            __syncthreads();
         }
-    }
-    for (int32_t i = total + (int32_t)threadIdx.x; i < a.k; i += kThreads) {
-        ids[i] = -1;
-        lps[i] = bad ? s.z : -INFINITY;
+        // the whole row's, in every warp
+        s = {-INFINITY, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < (W + 31) / 32; ++i)
+            if (lane + 32 * i < W) {
+                const float4 p = parts[lane + 32 * i];
+                Stat o = {p.x, p.y, p.z};
+                const float m = fmaxf(s.m, o.m);
+                rebase(s, m);
+                rebase(o, m);
+                s.z += o.z;
+                s.t += o.t;
+            }
+        s = warp_join(s);
+        const float log_z = logf(s.z);
+        if (rank == 0 && threadIdx.x == 0) put_row(a, r, s, log_z, y, xy);
+        if (a.k == 0) {
+            __syncthreads();  // before the next row's parts
+            continue;
+        }
+        if ((int32_t)threadIdx.x < M) {  // the k-th largest of tops
+            const float v = tops[threadIdx.x];
+            int32_t before = 0;
+            for (int32_t q = 0; q < M; ++q) before += tops[q] > v || (tops[q] == v && q < (int32_t)threadIdx.x);
+            if (before == a.k - 1) bound = v;
+        }
+        if (threadIdx.x == 0) list.count = hit_count = 0;
+        __syncthreads();
+        const float tau = bound;
+        const bool bad = s.z != s.z;
+        if (!bad) {
+            if (sl.xe >= tau && sl.xe > -INFINITY) offer(list, sl.xe, sl.edge);
+            for (int32_t g0 = 0, g = 0; g0 < sl.count; g0 += span, ++g) {
+                const float gm = gmax[g * kThreads];
+                if (gm < tau || gm == -INFINITY) continue;
+                const int32_t h = atomicAdd(&hit_count, 1);
+                if (h < kHits) hits[h] = g * kThreads + (int32_t)threadIdx.x;
+            }
+        }
+        __syncthreads();
+        // the groups that reach the bound, their vectors over all threads
+        const int32_t each = turns * kTurn, items = min(hit_count, kHits) * each;
+        for (int32_t q = (int32_t)threadIdx.x; q < items; q += kThreads) {
+            const int32_t h = hits[q / each];
+            const int32_t i = (h / kThreads * each + q % each) * kThreads + h % kThreads;
+            if (i >= sl.count) continue;
+            const uint4 u = sl.load(i);
+            if (part_max<T>(u) < tau) continue;
+            float f[kE<T>];
+            unpack<T>(u, f);
+#pragma unroll
+            for (int e = 0; e < kE<T>; ++e)
+                if (f[e] >= tau && f[e] > -INFINITY) offer(list, f[e], sl.first(i) + e);
+        }
+        __syncthreads();
+        if (list.count > kCap || hit_count > kHits)
+            select_exactly(sl, rank, max(order_of(tau), kOrderNone + 1), order_of(s.m), a.k, list, scan);
+        const unsigned long long* all = list.e;
+        int32_t total = list.count;
+        if constexpr (S > 1) {  // CTA 0 takes everybody's
+            cluster_sync();
+            if (rank == 0) {
+                unsigned long long* to = reinterpret_cast<unsigned long long*>(ring);
+                total = 0;
+                for (uint32_t q = 0; q < S; ++q) {
+                    const int32_t c = __float_as_int(ld_cluster(map_rank(smem_addr(&list.count), q)));
+                    for (int32_t i = threadIdx.x; i < c; i += kThreads) {
+                        const uint32_t src = map_rank(smem_addr(&list.e[i]), q);
+                        asm volatile("ld.shared::cluster.b64 %0, [%1];\n" : "=l"(to[total + i]) : "r"(src) : "memory");
+                    }
+                    total += c;
+                }
+                all = to;
+            }
+            cluster_sync();  // the lists stay until they are read
+            if (rank != 0) return;
+        }
+        int32_t* ids = a.top_ids + (int64_t)r * a.k;
+        float* lps = a.top_logp + (int64_t)r * a.k;
+        for (int32_t i = threadIdx.x; i < total; i += kThreads) {
+            const unsigned long long e = all[i];
+            int32_t before = 0;
+#pragma unroll 4
+            for (int32_t q = 0; q < total; ++q) before += all[q] > e;
+            if (before < a.k) {
+                ids[before] = class_of(e);
+                lps[before] = logp_of(value_of((uint32_t)(e >> 32)), s.m, log_z);
+            }
+        }
+        for (int32_t i = total + (int32_t)threadIdx.x; i < a.k; i += kThreads) {
+            ids[i] = -1;
+            lps[i] = bad ? s.z : -INFINITY;
+        }
     }
 }
 
@@ -499,16 +726,35 @@ template <typename T, int S>
 sg_status run_row(const Args<T>& a, int64_t nv, cudaStream_t s) {
     const int64_t per = cdiv(nv, S), all_turns = cdiv(per, kTurn * kThreads);
     const int64_t turns = all_turns > kGroups ? cdiv(all_turns, kGroups) : 1;
-    int64_t smem = cdiv(all_turns, turns) * kThreads * 4;
-    if (S > 1 && smem < S * kCap * 8) smem = S * kCap * 8;
-    SG_CUDA(launch_cluster(k_logprobs_row<T, S>, (unsigned)((int64_t)a.n_cap * S), kThreads, S, s, (int)smem, a,
-                           (int32_t)turns));
+    int64_t lists = kRing * kTurn * kThreads * 16;
+    if (S > 1 && lists < S * kCap * 8) lists = S * kCap * 8;
+    const int64_t smem = lists + cdiv(all_turns, turns) * kThreads * 4;
+    static OncePerDevice set;
+    SG_CUDA(allow_smem(set, k_logprobs_row<T, S>, (int)(lists + kGroups * kThreads * 4)));
+    int64_t clusters = a.n_cap;  // a cluster of several CTAs has one row
+    if (S == 1 && clusters > 4 * num_sms()) clusters = 4 * num_sms();
+    SG_CUDA(launch_cluster(k_logprobs_row<T, S>, (unsigned)(clusters * S), kThreads, S, s, (int)smem, a, (int32_t)turns));
+    return SG_OK;
+}
+
+template <typename T, int K>
+sg_status run_few(const Args<T>& a, cudaStream_t s) {
+    const size_t smem = kFewRows * (size_t)(a.classes | 1) * 4;
+    const uint32_t magic = (uint32_t)((((uint64_t)1 << 32) + a.classes - 1) / a.classes);
+    SG_CUDA(launch_pdl(k_logprobs_few<T, K>, dim3((unsigned)cdiv(a.n_cap, kFewRows)), dim3(kFewRows), smem, s, a, magic));
     return SG_OK;
 }
 
 template <typename T>
 sg_status run(const Args<T>& a, cudaStream_t s) {
     if (a.n_cap == 0) return SG_OK;
+    // (a block for every SM at least)
+    if (a.classes > 1 && a.classes <= kFewClasses && a.k <= kFewTop && a.n_cap >= kFewRows * num_sms()) {
+        if (a.k <= 1) return run_few<T, 1>(a, s);
+        if (a.k <= 2) return run_few<T, 2>(a, s);
+        if (a.k <= 4) return run_few<T, 4>(a, s);
+        return run_few<T, 8>(a, s);
+    }
     const int64_t nv = cdiv((int64_t)a.classes, kE<T>);  // vectors of a row, at most
     if (nv <= 32) return run_warp<T, 1>(a, s);
     if (nv <= 64) return run_warp<T, 2>(a, s);

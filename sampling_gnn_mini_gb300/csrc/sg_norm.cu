@@ -19,7 +19,6 @@
 // forward: SPEED_ODD us, all in single values 50.
 #include "sg_internal.cuh"
 #include "sg_rows.cuh"
-#include "sg_tc.cuh"
 
 using namespace sgi;
 
@@ -477,16 +476,6 @@ template <int V, int NT, int A>
 constexpr int kDepth = kRoom<V, NT, A> > 4 ? 4 : kRoom<V, NT, A>;
 template <int V, int NT, int A>
 constexpr int kRingSize = kDepth<V, NT, A> * NT * V * A * 16;
-
-__device__ __forceinline__ void copy_async(const uint4* to, const void* from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_addr(to)), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-// Waits for all groups of copies but the last N.
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
-}
 
 template <typename T, int V, int NT>
 __global__ void __launch_bounds__(NT, kRingBlocks<NT, 1>) k_norm_fwd_ring(FwdArgs<T> a) {

@@ -131,6 +131,19 @@ __device__ __forceinline__ void store_part(T* p, bool whole, const uint4& u) {
     for (int q = 0; q < kE<T>; ++q) p[q] = e[q];
 }
 
+// ------------------------------------------- a thread's own copies, ahead of use
+// 16 bytes from global into shared memory (both addresses the address of a uint4 there).
+__device__ __forceinline__ void copy_async(const uint4* to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+// Waits for all groups of copies but the last N.
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
 // Sum of n fp32 values in a fixed order, by one block of NT threads (in thread 0):
 // 16 bytes and 8 loads a thread at a time (65,536 values one by one took 35 us).
 template <int NT>
