@@ -256,8 +256,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill_warp(Args<T> a) {
 // vectors and, for CTA 0, the edge elements.
 template <typename T>
 __device__ __forceinline__ void put_entries(const Args<T>& a, const Entries& n, T* out, const RowParts<T>& part, int32_t v0,
-                                            int32_t count, int32_t rank, float w, float M, float Z) {
-    const int32_t j = (int32_t)threadIdx.x;
+                                            int32_t count, int32_t rank, int32_t j, float w, float M, float Z) {
     if (j >= a.k || n.id[j] < 0) return;
     const int32_t at = part.place(n.id[j]);
     if (at < 0 ? rank != 0 : at < v0 || at >= v0 + count) return;
@@ -331,7 +330,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_row(Args<T> a) {
             if (threadIdx.x == 0) a.loss[r] = loss;
         }
         __syncthreads();  // the vectors are stored
-        if (out) put_entries(a, entries, out, part, v0, count, rank, w, M, Z);
+        if (out) put_entries(a, entries, out, part, v0, count, rank, (int32_t)threadIdx.x, w, M, Z);
     } else {
         if (rank == 0 && threadIdx.x == 0) a.loss[r] = 0.f;
         if (out) zero_row<T, NT>(out, classes, rank, S);
@@ -350,140 +349,189 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_row(Args<T> a) {
 
 // Many long rows: the same, with each cluster walking over its rows and the next two
 // rows' slices on their way into shared memory while the current row is worked on.
-// The entries take two dependent loads (the class, then its logit), so they are
-// loaded two rows ahead and their logits one row ahead, an entry a thread, and handed
-// over at the block's barrier of the row before (loaded by one warp at the row's
-// start: 284 us for 4096 x 50,257 bf16, now SPEED_STREAM).
+//
+// The last warps of a block do nothing but the entries, beside the others: the classes
+// are loaded two rows ahead, their logits one row ahead, q is formed while the row is
+// reduced, and the entries' classes are written once the row's vectors are stored
+// (`stored`), while the other warps are at the next row.  (By the warps that hold
+// vectors, at the row's start: 284 us for 4096 x 50,257 bf16 and 64 entries; loaded
+// ahead, with a barrier a row: 198, with a barrier for the entries' warps alone the
+// same: every row waits for the longest warp.  Now SPEED_STREAM; without entries at
+// all, the cross-entropy, 139.)
 constexpr int kStreamVecs = 3300;  // of a CTA's slice: two buffers of it and the entries, two CTAs an SM
+template <int NT>
+constexpr int kEntryWarps = NT == 512 ? 3 : 1;
+template <int NT>
+constexpr int kVecThreads = NT - 32 * kEntryWarps<NT>;  // kVecs vectors each: 3,328 or 1,792
 
 template <typename T, int NT, int S>
 __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_stream(Args<T> a, int32_t slots) {
     extern __shared__ __align__(128) uint8_t dsm[];
     pdl_start();
-    constexpr int kParts = S * NT / 32;
+    constexpr int NV = kVecThreads<NT>, ET = NT - NV, PE = (SG_MAX_TOP + ET - 1) / ET;  // PE: entries of a thread
+    constexpr int kParts = S * NV / 32;
     __shared__ __align__(8) float2 parts[2][kParts];  // (m, z) of every warp of the cluster, of used rows in turn
     __shared__ __align__(8) uint64_t full[2], met[2];  // buffers; parts
-    __shared__ Entries entries[3];                     // of rows in turn
+    __shared__ __align__(8) uint64_t stored[2], read[2];  // a row's vectors are stored; the entries' warps have met it
+    __shared__ Entries entries[2];                     // of used rows in turn
     __shared__ bool last;
     const int32_t rank = (int32_t)(blockIdx.x % S), first = (int32_t)(blockIdx.x / S), step = (int32_t)(gridDim.x / S);
     const int32_t n = rows_of(a.d_n, a.n_cap), classes = a.classes;
     if (first >= n) return;  // the whole cluster
     if (threadIdx.x == 0) {
         last = false;
-        mbar_init(&full[0], 1);
-        mbar_init(&full[1], 1);
-        mbar_init(&met[0], 1);
-        mbar_init(&met[1], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&met[i], 1);
+            mbar_init(&stored[i], NV / 32);
+            mbar_init(&read[i], S * kEntryWarps<NT>);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     __syncthreads();
     if constexpr (S > 1) cluster_sync();  // every CTA runs: its shared memory may be written
     const auto has = [&](int32_t r) { return r < n && row_used(a, r); };
-    // copies this CTA's slice of row r into buffer b (thread 0)
-    const auto fetch = [&](int32_t r, bool used, int b) {
-        if (!used) return;
-        const T* row = a.x + (int64_t)r * a.ld;
-        const RowParts<T> part(row, classes);
-        const int32_t per = (part.vecs + S - 1) / S, v0 = min(part.vecs, rank * per);
-        const uint32_t bytes = (uint32_t)(min(part.vecs, v0 + per) - v0) * 16;
-        mbar_expect_tx(&full[b], bytes);
-        if (bytes)
-            asm volatile(
-                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
-                    smem_addr(dsm) + (uint32_t)(b * slots) * 16),
-                "l"(row + part.head + (int64_t)v0 * kE<T>), "r"(bytes), "r"(smem_addr(&full[b]))
-                : "memory");
-    };
-    bool u0 = has(first), u1 = has(first + step), u2;
-    if (threadIdx.x == 0) {
-        fetch(first, u0, 0);
-        fetch(first + step, u1, 1);
-    }
     const float w = weight_of(a);
-    const bool mine = threadIdx.x < 32 && (rank == 0 || a.grad);  // the warp that scales the entries
-    // this thread's entry: j of the next row, then of the row after it
-    const int32_t j = (int32_t)threadIdx.x;
-    int32_t id1 = -1, id2 = -1;
-    float v1 = -INFINITY, v2 = -INFINITY;
-    const auto hand_over = [&](Entries& to, float x) {
-        if (j < SG_MAX_TOP) to.id[j] = id1, to.v[j] = v1, to.x[j] = x;
-    };
-    const auto logit_at = [&](int32_t r, int32_t id) { return id >= 0 ? to_f(a.x[(int64_t)r * a.ld + id]) : 0.f; };
-    load_entry(a, first, j, rank == 0, id1, v1);
-    if (first + step < n) load_entry(a, first + step, j, rank == 0, id2, v2);
-    hand_over(entries[0], logit_at(first, id1));
-    id1 = id2, v1 = v2;
-    __syncthreads();
-    uint32_t phases = 0;  // bits 0, 1: parity of the next phase of full[0], full[1]; bits 2, 3: of met[0], met[1]
-    int32_t par = 0;      // the row's buffer: alternates over all rows
-    int32_t slot = 0;     // its parts and met: alternate over the used rows only
-    int32_t turn = 0;     // its entries
-    for (int32_t r = first; r < n; r += step, par ^= 1, u0 = u1, u1 = u2) {
-        u2 = has(r + 2 * step);
-        const T* row = a.x + (int64_t)r * a.ld;
-        T* out = a.grad ? a.grad + (int64_t)r * a.ld_grad : nullptr;
-        const float x1 = logit_at(r + step, id1);
-        id2 = -1, v2 = -INFINITY;
-        if (r + 2 * step < n) load_entry(a, r + 2 * step, j, rank == 0, id2, v2);
-        Entries& entry = entries[turn];
-        turn = turn == 2 ? 0 : turn + 1;
-        if (!u0) {  // the same in the whole cluster
-            if (rank == 0 && threadIdx.x == 0) a.loss[r] = 0.f;
-            if (out) zero_row<T, NT>(out, classes, rank, S);
-            if (threadIdx.x == 0) fetch(r + 2 * step, u2, par);  // this row's buffer was not filled
-            hand_over(entries[turn], x1);
-            id1 = id2, v1 = v2;
-            __syncthreads();
-            continue;
+    // of the used rows so far: row u uses slot u % 2, for the (u / 2)-th time
+    uint32_t used = 0;
+    if (threadIdx.x < NV) {
+        // copies this CTA's slice of row r into buffer b (thread 0)
+        const auto fetch = [&](int32_t r, bool u, int b) {
+            if (!u) return;
+            const T* row = a.x + (int64_t)r * a.ld;
+            const RowParts<T> part(row, classes);
+            const int32_t per = (part.vecs + S - 1) / S, v0 = min(part.vecs, rank * per);
+            const uint32_t bytes = (uint32_t)(min(part.vecs, v0 + per) - v0) * 16;
+            mbar_expect_tx(&full[b], bytes);
+            if (bytes)
+                asm volatile(
+                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                        smem_addr(dsm) + (uint32_t)(b * slots) * 16),
+                    "l"(row + part.head + (int64_t)v0 * kE<T>), "r"(bytes), "r"(smem_addr(&full[b]))
+                    : "memory");
+        };
+        bool u0 = has(first), u1 = has(first + step), u2;
+        if (threadIdx.x == 0) {
+            fetch(first, u0, 0);
+            fetch(first + step, u1, 1);
         }
-        const RowParts<T> part(row, classes);
-        const int32_t per = (part.vecs + S - 1) / S, v0 = min(part.vecs, rank * per), count = min(part.vecs, v0 + per) - v0;
-        const int32_t edge = rank == 0 && threadIdx.x < 32 ? part.edge((int)threadIdx.x) : -1;
-        Held<T, NT> h;
-        h.xe = edge >= 0 ? to_f(row[edge]) : -INFINITY;
-        Scale scale = {0.f, 0.f};
-        if (mine) scale = scale_entries(a, entry);
-        if (!mbar_wait(&full[par], (phases >> par) & 1u) && lane_id() == 0) dev_err(ERR_TIMEOUT);
-        const uint4* buf = reinterpret_cast<const uint4*>(dsm) + par * slots + threadIdx.x;
+        uint32_t phases = 0;  // bits 0, 1: parity of the next phase of full[0], full[1]
+        int32_t par = 0;      // the row's buffer: alternates over all rows
+        for (int32_t r = first; r < n; r += step, par ^= 1, u0 = u1, u1 = u2) {
+            u2 = has(r + 2 * step);
+            const T* row = a.x + (int64_t)r * a.ld;
+            T* out = a.grad ? a.grad + (int64_t)r * a.ld_grad : nullptr;
+            if (!u0) {  // the same in the whole cluster
+                if (rank == 0 && threadIdx.x == 0) a.loss[r] = 0.f;
+                if (out) zero_row<T, NV>(out, classes, rank, S);
+                if (threadIdx.x == 0) fetch(r + 2 * step, u2, par);  // this row's buffer was not filled
+                continue;
+            }
+            const uint32_t slot = used & 1u, turn = (used >> 1) & 1u;
+            const RowParts<T> part(row, classes);
+            const int32_t per = (part.vecs + S - 1) / S, v0 = min(part.vecs, rank * per),
+                          count = min(part.vecs, v0 + per) - v0;
+            const int32_t edge = rank == 0 && threadIdx.x < 32 ? part.edge((int)threadIdx.x) : -1;
+            Held<T, NV> h;
+            h.xe = edge >= 0 ? to_f(row[edge]) : -INFINITY;
+            if (!mbar_wait(&full[par], (phases >> par) & 1u) && lane_id() == 0) dev_err(ERR_TIMEOUT);
+            const uint4* buf = reinterpret_cast<const uint4*>(dsm) + par * slots + threadIdx.x;
 #pragma unroll
-        for (int k = 0; k < kVecs; ++k)
-            h.x[k] = (int32_t)threadIdx.x + k * NT < count ? buf[k * NT] : empty_part<T>();
-        reduce_held(h, count, -INFINITY, 0.f, a.l);
-        // The parts meet by asynchronous stores that complete on the receiver's
-        // barrier: a slot is written again two used rows later, by a warp that has
-        // met the used row between, to which every reader of the slot sent its part
-        // after it had read.
-        if (threadIdx.x == 0) mbar_expect_tx(&met[slot], kParts * 8);
-        if (lane_id() < S) {
-            const uint32_t to = smem_addr(&parts[slot][rank * (NT / 32) + (threadIdx.x >> 5)]);
-            asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];\n" ::"r"(
-                             map_rank(to, lane_id())),
-                         "f"(h.m), "f"(h.z), "r"(map_rank(smem_addr(&met[slot]), lane_id()))
-                         : "memory");
-        }
-        __syncwarp();
-        if (!mbar_wait(&met[slot], (phases >> (2 + slot)) & 1u) && lane_id() == 0) dev_err(ERR_TIMEOUT);
-        phases ^= (1u << par) | (4u << slot);
-        // every thread has its vectors in registers: the buffer is free
-        if (threadIdx.x == 0) fetch(r + 2 * step, u2, par);
-        float M, Z;
-        join_parts<kParts>(parts[slot], M, Z, a.l);
-        if (out) {
+            for (int k = 0; k < kVecs; ++k)
+                h.x[k] = (int32_t)threadIdx.x + k * NV < count ? buf[k * NV] : empty_part<T>();
+            reduce_held(h, count, -INFINITY, 0.f, a.l);
+            // The parts meet by asynchronous stores that complete on the receiver's
+            // barrier.  A slot is written again two used rows later: by then its
+            // readers have read it, the warps with vectors before they sent their part
+            // of the used row between, the entries' warps before they arrived at `read`.
+            if (used >= 2 && !mbar_wait(&read[slot], turn ^ 1u) && lane_id() == 0) dev_err(ERR_TIMEOUT);
+            if (threadIdx.x == 0) mbar_expect_tx(&met[slot], kParts * 8);
+            if (lane_id() < S) {
+                const uint32_t to = smem_addr(&parts[slot][rank * (NV / 32) + (threadIdx.x >> 5)]);
+                asm volatile(
+                    "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];\n" ::"r"(
+                        map_rank(to, lane_id())),
+                    "f"(h.m), "f"(h.z), "r"(map_rank(smem_addr(&met[slot]), lane_id()))
+                    : "memory");
+            }
+            __syncwarp();
+            if (!mbar_wait(&met[slot], turn) && lane_id() == 0) dev_err(ERR_TIMEOUT);
+            phases ^= 1u << par;
+            ++used;
+            // every thread has its vectors in registers: the buffer is free
+            if (threadIdx.x == 0) fetch(r + 2 * step, u2, par);
+            if (!out) continue;
+            float M, Z;
+            join_parts<kParts>(parts[slot], M, Z, a.l);
             const float inv = held_scale(h.m, h.z, w, M, Z, a.l);
             store_held(h, out + part.head + v0 * kE<T>, count, same_phase(row, (const T*)out), inv, a.l);
             if (edge >= 0) put(out + edge, inv * Base(h.m, a.l).of(h.xe));
+            __syncwarp();
+            if (lane_id() == 0) mbar_arrive(&stored[slot]);
         }
-        if (rank == 0 && threadIdx.x < 32) {
-            const float loss = loss_of(a, scale, entry, M, Z);
-            if (threadIdx.x == 0) a.loss[r] = loss;
+    } else {
+        const int32_t t = (int32_t)threadIdx.x - NV;
+        const bool mine = rank == 0 || a.grad;
+        int32_t id1[PE], id2[PE];  // of the next row, and the one after it
+        float v1[PE], v2[PE], x1[PE];
+        const auto load = [&](int32_t r, int32_t (&id)[PE], float (&v)[PE]) {
+#pragma unroll
+            for (int e = 0; e < PE; ++e) {
+                id[e] = -1, v[e] = -INFINITY;
+                if (mine && r < n && t + e * ET < SG_MAX_TOP) load_entry(a, r, t + e * ET, rank == 0, id[e], v[e]);
+            }
+        };
+        const auto logits = [&](int32_t r) {  // of the entries id1 (-1 when row r is not there)
+#pragma unroll
+            for (int e = 0; e < PE; ++e) x1[e] = id1[e] >= 0 ? to_f(a.x[(int64_t)r * a.ld + id1[e]]) : 0.f;
+        };
+        load(first, id1, v1);
+        load(first + step, id2, v2);
+        logits(first);
+        bool u0 = has(first), u1;
+        for (int32_t r = first; r < n; r += step, u0 = u1) {
+            u1 = has(r + step);
+            T* out = a.grad ? a.grad + (int64_t)r * a.ld_grad : nullptr;
+            const uint32_t slot = used & 1u, turn = (used >> 1) & 1u;
+            // (the slot's last readers met the used row between at the entries' barrier)
+            Entries& entry = entries[slot];
+            if (u0) {
+#pragma unroll
+                for (int e = 0; e < PE; ++e)
+                    if (t + e * ET < SG_MAX_TOP) entry.id[t + e * ET] = id1[e], entry.v[t + e * ET] = v1[e], entry.x[t + e * ET] = x1[e];
+            }
+#pragma unroll
+            for (int e = 0; e < PE; ++e) id1[e] = id2[e], v1[e] = v2[e];
+            logits(r + step);
+            load(r + 2 * step, id2, v2);
+            if (!u0) continue;
+            Scale scale = {0.f, 0.f};
+            if (mine) {  // each warp scales all entries (they write the same)
+                asm volatile("bar.sync 1, %0;\n" ::"n"(ET) : "memory");
+                scale = scale_entries(a, entry);
+            }
+            if (!mbar_wait(&met[slot], turn) && lane_id() == 0) dev_err(ERR_TIMEOUT);
+            float M, Z;
+            join_parts<kParts>(parts[slot], M, Z, a.l);
+            if (rank == 0 && t < 32) {
+                const float loss = loss_of(a, scale, entry, M, Z);
+                if (t == 0) a.loss[r] = loss;
+            }
+            if (out && !mbar_wait(&stored[slot], turn) && lane_id() == 0) dev_err(ERR_TIMEOUT);
+            __syncwarp();
+            if (lane_id() < S)  // in every CTA of the cluster
+                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(
+                                 map_rank(smem_addr(&read[slot]), lane_id()))
+                             : "memory");
+            ++used;
+            if (!out) continue;
+            const T* row = a.x + (int64_t)r * a.ld;
+            const RowParts<T> part(row, classes);
+            const int32_t per = (part.vecs + S - 1) / S, v0 = min(part.vecs, rank * per),
+                          count = min(part.vecs, v0 + per) - v0;
+#pragma unroll
+            for (int e = 0; e < PE; ++e) put_entries(a, entry, out, part, v0, count, rank, t + e * ET, w, M, Z);
         }
-        hand_over(entries[turn], x1);
-        id1 = id2, v1 = v2;
-        // The vectors are stored, and the next row's entries there.  (Entries are
-        // written again two rows later, after the barrier of the row between.)
-        __syncthreads();
-        if (out) put_entries(a, entry, out, part, v0, count, rank, w, M, Z);
-        slot ^= 1;
     }
     __threadfence();
     if constexpr (S > 1) cluster_sync();
