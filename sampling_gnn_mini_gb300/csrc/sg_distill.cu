@@ -73,6 +73,26 @@ struct Entries {
     int32_t __align__(16) id[SG_MAX_TOP];  // -1: none, from k on as well
     float v[SG_MAX_TOP], x[SG_MAX_TOP], q[SG_MAX_TOP];
 };
+// Whether classes occur more than once: a table of 256 places for up to SG_MAX_TOP
+// classes, cleared beforehand.  (A comparison of every two entries took longer than
+// the row's other work from 64 entries on.)
+constexpr int kPlaces = 256;
+struct Table {
+    int32_t place[kPlaces];  // -1: free
+    __device__ __forceinline__ void clear(int t, int threads) {
+        for (int i = t; i < kPlaces; i += threads) place[i] = -1;
+    }
+    // true if the class was there (for one of two at least)
+    __device__ __forceinline__ bool insert(int32_t id) {
+        uint32_t at = (uint32_t)id * 0x9E3779B1u >> 24;
+        for (int i = 0; i < kPlaces; ++i, at = (at + 1) & (kPlaces - 1)) {
+            const int32_t was = atomicCAS(&place[at], -1, id);
+            if (was == -1) return false;
+            if (was == id) return true;
+        }
+        return false;
+    }
+};
 // Entry j of row r (-1 and -inf: none); report: names one out of range in the error word
 template <typename T>
 __device__ __forceinline__ void load_entry(const Args<T>& a, int32_t r, int32_t j, bool report, int32_t& id, float& v) {
@@ -146,19 +166,18 @@ __device__ __forceinline__ void load_entries(const Args<T>& a, int32_t r, const 
         n.x[j] = x[e];
     }
 }
-// The gradient at entry j's class; false where there is none.
+// The gradient at entry j's class; false where there is none.  twice: classes may occur
+// more than once
 template <typename T>
-__device__ __forceinline__ bool entry_grad(const Args<T>& a, const Entries& n, int32_t j, float w, float M, float Z,
-                                           float& g) {
+__device__ __forceinline__ bool entry_grad(const Args<T>& a, const Entries& n, int32_t j, bool twice, float w, float M,
+                                           float Z, float& g) {
     const int32_t id = n.id[j];
     if (id < 0) return false;
-    float q = 0.f;
-    for (int32_t i = 0; i < a.k; i += 4) {
-        const int4 o = *reinterpret_cast<const int4*>(n.id + i);
-        if (o.x == id) q += n.q[i];
-        if (o.y == id) q += n.q[i + 1];
-        if (o.z == id) q += n.q[i + 2];
-        if (o.w == id) q += n.q[i + 3];
+    float q = n.q[j];
+    if (twice) {
+        q = 0.f;
+        for (int32_t i = 0; i < a.k; ++i)
+            if (n.id[i] == id) q += n.q[i];
     }
     g = Z == 0.f ? 0.f : fmaf(w / Z, exp_from(n.x[j], M, a.l), -w * q);
     return true;
@@ -182,12 +201,14 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill_warp(Args<T> a) {
     pdl_start();
     constexpr int kWarps = kThreads / 32;
     __shared__ Entries entries[kWarps];
+    __shared__ Table tables[kWarps];
     __shared__ bool last;
     const int lane = (int)lane_id();
     const int32_t n = rows_of(a.d_n, a.n_cap), blocks = min((int32_t)gridDim.x, (n + kWarps - 1) / kWarps);
     if ((int32_t)blockIdx.x >= blocks) return;
     const float w = weight_of(a);
     Entries& mine = entries[threadIdx.x >> 5];
+    Table& table = tables[threadIdx.x >> 5];
     for (int32_t r = (int32_t)blockIdx.x * kWarps + (int32_t)(threadIdx.x >> 5); r < n; r += (int32_t)gridDim.x * kWarps) {
         const T* row = a.x + (int64_t)r * a.ld;
         T* out = a.grad ? a.grad + (int64_t)r * a.ld_grad : nullptr;
@@ -233,10 +254,15 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill_warp(Args<T> a) {
                 store_part(out + part.head + v * kE<T>, same, part_grad<T>(x[k], base, pair(inv, inv)));
         }
         if (ce >= 0) put(out + ce, inv * base.of(xe));
+        table.clear(lane, 32);
         __syncwarp();  // the entries are there, the vectors stored
+        bool twice = false;
+        for (int32_t j = lane; j < a.k; j += 32)
+            if (mine.id[j] >= 0) twice |= table.insert(mine.id[j]);
+        twice = __any_sync(0xFFFFFFFFu, twice);
         for (int32_t j = lane; j < a.k; j += 32) {
             float g;
-            if (entry_grad(a, mine, j, w, m, z, g)) put(out + mine.id[j], g);
+            if (entry_grad(a, mine, j, twice, w, m, z, g)) put(out + mine.id[j], g);
         }
         __syncwarp();  // before the next row's entries
     }
@@ -256,12 +282,13 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill_warp(Args<T> a) {
 // vectors and, for CTA 0, the edge elements.
 template <typename T>
 __device__ __forceinline__ void put_entries(const Args<T>& a, const Entries& n, T* out, const RowParts<T>& part, int32_t v0,
-                                            int32_t count, int32_t rank, int32_t j, float w, float M, float Z) {
+                                            int32_t count, int32_t rank, int32_t j, bool twice, float w, float M,
+                                            float Z) {
     if (j >= a.k || n.id[j] < 0) return;
     const int32_t at = part.place(n.id[j]);
     if (at < 0 ? rank != 0 : at < v0 || at >= v0 + count) return;
     float g;
-    if (entry_grad(a, n, j, w, M, Z, g)) put(out + n.id[j], g);
+    if (entry_grad(a, n, j, twice, w, M, Z, g)) put(out + n.id[j], g);
 }
 
 template <typename T, int NT, int S>
@@ -330,7 +357,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_row(Args<T> a) {
             if (threadIdx.x == 0) a.loss[r] = loss;
         }
         __syncthreads();  // the vectors are stored
-        if (out) put_entries(a, entries, out, part, v0, count, rank, (int32_t)threadIdx.x, w, M, Z);
+        if (out) put_entries(a, entries, out, part, v0, count, rank, (int32_t)threadIdx.x, true, w, M, Z);
     } else {
         if (rank == 0 && threadIdx.x == 0) a.loss[r] = 0.f;
         if (out) zero_row<T, NT>(out, classes, rank, S);
@@ -364,6 +391,18 @@ constexpr int kEntryWarps = NT == 512 ? 3 : 1;
 template <int NT>
 constexpr int kVecThreads = NT - 32 * kEntryWarps<NT>;  // kVecs vectors each: 3,328 or 1,792
 
+// A barrier of THREADS of a block's threads, whole warps; true in all if it is in any.
+template <int THREADS>
+__device__ __forceinline__ bool any_of(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)x), "n"(THREADS)
+        : "memory");
+    return r != 0;
+}
+
 template <typename T, int NT, int S>
 __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_stream(Args<T> a, int32_t slots) {
     extern __shared__ __align__(128) uint8_t dsm[];
@@ -374,6 +413,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_stream(Args<T> a, int
     __shared__ __align__(8) uint64_t full[2], met[2];  // buffers; parts
     __shared__ __align__(8) uint64_t stored[2], read[2];  // a row's vectors are stored; the entries' warps have met it
     __shared__ Entries entries[2];                     // of used rows in turn
+    __shared__ Table tables[2];
     __shared__ bool last;
     const int32_t rank = (int32_t)(blockIdx.x % S), first = (int32_t)(blockIdx.x / S), step = (int32_t)(gridDim.x / S);
     const int32_t n = rows_of(a.d_n, a.n_cap), classes = a.classes;
@@ -388,6 +428,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_stream(Args<T> a, int
         }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
+    tables[0].clear((int)threadIdx.x, NT);
+    tables[1].clear((int)threadIdx.x, NT);
     __syncthreads();
     if constexpr (S > 1) cluster_sync();  // every CTA runs: its shared memory may be written
     const auto has = [&](int32_t r) { return r < n && row_used(a, r); };
@@ -495,7 +537,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_stream(Args<T> a, int
             const uint32_t slot = used & 1u, turn = (used >> 1) & 1u;
             // (the slot's last readers met the used row between at the entries' barrier)
             Entries& entry = entries[slot];
+            bool twice = false;
             if (u0) {
+#pragma unroll
+                for (int e = 0; e < PE; ++e)
+                    if (id1[e] >= 0) twice |= tables[slot].insert(id1[e]);
+                // for the next used row (all have met the barrier after the last one's inserts)
+                tables[slot ^ 1u].clear(t, ET);
 #pragma unroll
                 for (int e = 0; e < PE; ++e)
                     if (t + e * ET < SG_MAX_TOP) entry.id[t + e * ET] = id1[e], entry.v[t + e * ET] = v1[e], entry.x[t + e * ET] = x1[e];
@@ -507,7 +555,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_stream(Args<T> a, int
             if (!u0) continue;
             Scale scale = {0.f, 0.f};
             if (mine) {  // each warp scales all entries (they write the same)
-                asm volatile("bar.sync 1, %0;\n" ::"n"(ET) : "memory");
+                twice = any_of<ET>(twice);
                 scale = scale_entries(a, entry);
             }
             if (!mbar_wait(&met[slot], turn) && lane_id() == 0) dev_err(ERR_TIMEOUT);
@@ -530,7 +578,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_stream(Args<T> a, int
             const int32_t per = (part.vecs + S - 1) / S, v0 = min(part.vecs, rank * per),
                           count = min(part.vecs, v0 + per) - v0;
 #pragma unroll
-            for (int e = 0; e < PE; ++e) put_entries(a, entry, out, part, v0, count, rank, t + e * ET, w, M, Z);
+            for (int e = 0; e < PE; ++e) put_entries(a, entry, out, part, v0, count, rank, t + e * ET, twice, w, M, Z);
         }
     }
     __threadfence();

@@ -21,6 +21,8 @@
 // Logits of -inf take no part.  x - m is formed before the scaling by log2(e), so
 // a row's level costs no accuracy, and exponents are cut off at -200, where the
 // exponential is 0, so that 0 * (-inf) never arises.
+#include <type_traits>
+
 #include "sg_internal.cuh"
 #include "sg_rows.cuh"
 #include "sg_tc.cuh"
@@ -134,6 +136,21 @@ __device__ __forceinline__ void put_row(const Args<T>& a, int32_t r, const Stat&
     if (a.entropy) a.entropy[r] = s.z == 0.f ? 0.f : log_z - s.t / s.z * 0.69314718055994531f;
 }
 
+// The largest element of several vectors (bf16: pairwise on the packed elements).
+template <typename T, int N>
+__device__ __forceinline__ float parts_max(const uint4 (&u)[N]) {
+    if constexpr (sizeof(T) == 2) {
+        const auto h = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+        __nv_bfloat162 m = __hmax2(__hmax2(h(u[0].x), h(u[0].y)), __hmax2(h(u[0].z), h(u[0].w)));
+#pragma unroll
+        for (int k = 1; k < N; ++k) m = __hmax2(m, __hmax2(__hmax2(h(u[k].x), h(u[k].y)), __hmax2(h(u[k].z), h(u[k].w))));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+    float m = part_max<T>(u[0]);
+#pragma unroll
+    for (int k = 1; k < N; ++k) m = fmaxf(m, part_max<T>(u[k]));
+    return m;
+}
 // Elements of a vector, one at a time.
 template <typename T>
 __device__ __forceinline__ void unpack(const uint4& u, float (&f)[kE<T>]) {
@@ -144,48 +161,60 @@ __device__ __forceinline__ void unpack(const uint4& u, float (&f)[kE<T>]) {
 }
 
 // ------------------------------------------------------------ rows by threads
-// kFewRows rows of up to kFewClasses classes to a block, in shared memory (a pitch that
-// is odd, so that threads meet different banks), then a thread a row.  A thread's top
-// K sit in registers in order: a logit moves in where it is larger, so that equal ones
-// stay in the order of their classes.  magic: ceil(2^32 / classes).
+// kFewRows rows of up to kFewClasses classes to a block, in shared memory, then a
+// thread a row.  A thread's top K sit in registers in order: a logit moves in where it
+// is larger, so that equal ones stay in the order of their classes.  RAW: the rows
+// follow one another from a 16-byte boundary and their length is odd, so that they
+// are copied as they are (threads meet different banks); if not, value by value at an
+// odd pitch (magic: ceil(2^32 / classes)).
 constexpr int kFewRows = 128, kFewClasses = 64, kFewTop = 8;
 
-template <typename T, int K>
+template <typename T, int K, bool RAW>
 __global__ void __launch_bounds__(kFewRows) k_logprobs_few(Args<T> a, uint32_t magic) {
-    extern __shared__ float rows[];
+    extern __shared__ __align__(16) uint4 few_smem[];
     pdl_start();
     const int32_t n = rows_of(a.d_n, a.n_cap), r0 = (int32_t)blockIdx.x * kFewRows, classes = a.classes;
     if (r0 >= n) return;
-    const int32_t pitch = classes | 1, all = min(kFewRows, n - r0) * classes;
+    const int32_t pitch = RAW ? classes : classes | 1, all = min(kFewRows, n - r0) * classes;
     const T* x = a.x + (int64_t)r0 * a.ld;
-    for (int32_t i0 = (int32_t)threadIdx.x; i0 < all; i0 += 8 * kFewRows) {
-        T v[8];
+    typedef std::conditional_t<RAW, T, float> M;
+    M* rows = reinterpret_cast<M*>(few_smem);
+    if constexpr (RAW) {
+        const int32_t vecs = all / kE<T>;
+        for (int32_t i = (int32_t)threadIdx.x; i < vecs; i += kFewRows) copy_async(few_smem + i, x + i * kE<T>);
+        copies_end();
+        const int32_t i = vecs * kE<T> + (int32_t)threadIdx.x;
+        if (i < all) rows[i] = x[i];
+        copies_wait<0>();
+    } else {
+        for (int32_t i0 = (int32_t)threadIdx.x; i0 < all; i0 += 16 * kFewRows) {
+            T v[16];
+            int32_t to[16];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int32_t i = i0 + u * kFewRows;
-            const int32_t row = (int32_t)__umulhi((uint32_t)i, magic);
-            if (i < all) v[u] = x[row * a.ld + (i - row * classes)];
-        }
+            for (int u = 0; u < 16; ++u) {
+                const int32_t i = i0 + u * kFewRows;
+                const int32_t row = (int32_t)__umulhi((uint32_t)i, magic), c = i - row * classes;
+                to[u] = i < all ? row * pitch + c : -1;
+                if (i < all) v[u] = x[row * a.ld + c];
+            }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int32_t i = i0 + u * kFewRows;
-            const int32_t row = (int32_t)__umulhi((uint32_t)i, magic);
-            if (i < all) rows[row * pitch + (i - row * classes)] = to_f(v[u]);
+            for (int u = 0; u < 16; ++u)
+                if (to[u] >= 0) rows[to[u]] = to_f(v[u]);
         }
     }
     __syncthreads();
     const int32_t r = r0 + (int32_t)threadIdx.x;
     if (r >= n) return;
-    const float* row = rows + (int32_t)threadIdx.x * pitch;
+    const M* row = rows + (int32_t)threadIdx.x * pitch;
     const int32_t y = label_of(a, r);
-    const float xy = y >= 0 ? row[y] : 0.f;
+    const float xy = y >= 0 ? to_f(row[y]) : 0.f;
     float top[K];
     int32_t at[K];
 #pragma unroll
     for (int j = 0; j < K; ++j) top[j] = -INFINITY, at[j] = -1;
 #pragma unroll 4
     for (int32_t c = 0; c < classes; ++c) {
-        float v = row[c];
+        float v = to_f(row[c]);
         if (v > top[K - 1]) {
             int32_t i = c;
 #pragma unroll
@@ -202,7 +231,7 @@ __global__ void __launch_bounds__(kFewRows) k_logprobs_few(Args<T> a, uint32_t m
     const float b = finite_base(s.m);
 #pragma unroll 4
     for (int32_t c = 0; c < classes; ++c) {
-        const float d = max_nan((row[c] - b) * kLog2e, kNone), e = ex2(d);
+        const float d = max_nan((to_f(row[c]) - b) * kLog2e, kNone), e = ex2(d);
         s.z += e;
         s.t = fmaf(e, d, s.t);
     }
@@ -394,7 +423,7 @@ __global__ void __launch_bounds__(kThreads) k_logprobs_warp(Args<T> a) {
 // --------------------------------------------------------- rows by clusters
 // The candidates of a CTA's part of a row.
 struct Candidates {
-    unsigned long long e[kCap];
+    unsigned long long __align__(16) e[kCap];
     int32_t count;
 };
 __device__ __forceinline__ void offer(Candidates& l, float x, int32_t c) {
@@ -506,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs_row(Args<T> a, int32_t
     pdl_start();
     constexpr int W = S * kWarps;
     __shared__ __align__(16) float4 parts[W];
-    __shared__ float tops[SG_MAX_TOP + W];
+    __shared__ __align__(16) float tops[kThreads];
     __shared__ Candidates list;
     __shared__ int32_t hits[kHits], hit_count;
     __shared__ float bound;
@@ -570,15 +599,13 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs_row(Args<T> a, int32_t
                 fetch(at ? at - 1 : kRing - 1);
                 copies_wait<kRing - 1>();
                 uint4 u[kTurn];
-                float top = -INFINITY;
 #pragma unroll
                 for (int k = 0; k < kTurn; ++k) {
                     const int32_t i = i0 + k * kThreads + (int32_t)threadIdx.x;
                     u[k] = i < sl.count ? ring[(at * kTurn + k) * kThreads + threadIdx.x] : empty_part<T>();
                 }
                 if (++at == kRing) at = 0;
-#pragma unroll
-                for (int k = 0; k < kTurn; ++k) top = fmaxf(top, part_max<T>(u[k]));
+                const float top = parts_max<T>(u);
                 gm = fmaxf(gm, top);
                 rebase(s, fmaxf(s.m, top));
                 f2 z = pair(s.z, 0.f), t = pair(s.t, 0.f);
@@ -598,8 +625,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs_row(Args<T> a, int32_t
             most = fmaxf(most, gm);
         }
         s = warp_join(s);
-        // the warp's j largest of its lanes' maxima
-        const int32_t j = (a.k + W - 1) / W, M = W * j;
+        // the warp's j largest of its lanes' maxima: half as many again as k needs, so that
+        // an uneven share of the warps does not lower the bound
+        const int32_t need = (a.k + W - 1) / W, j = min(need + (need + 1) / 2, kThreads / W), M = W * j;
         if (j == 1) most = s.m;
         else if (j > 1) most = warp_sort(most);
         const int32_t w = rank * kWarps + warp;
@@ -642,7 +670,13 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs_row(Args<T> a, int32_t
         if ((int32_t)threadIdx.x < M) {  // the k-th largest of tops
             const float v = tops[threadIdx.x];
             int32_t before = 0;
-            for (int32_t q = 0; q < M; ++q) before += tops[q] > v || (tops[q] == v && q < (int32_t)threadIdx.x);
+#pragma unroll 2
+            for (int32_t q = 0; q < M; q += 4) {
+                const float4 o = *reinterpret_cast<const float4*>(tops + q);
+                const int32_t i = (int32_t)threadIdx.x - q;
+                before += (o.x > v || (o.x == v && i > 0)) + (o.y > v || (o.y == v && i > 1)) +
+                          (o.z > v || (o.z == v && i > 2)) + (o.w > v || (o.w == v && i > 3));
+            }
             if (before == a.k - 1) bound = v;
         }
         if (threadIdx.x == 0) list.count = hit_count = 0;
@@ -700,9 +734,12 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs_row(Args<T> a, int32_t
         float* lps = a.top_logp + (int64_t)r * a.k;
         for (int32_t i = threadIdx.x; i < total; i += kThreads) {
             const unsigned long long e = all[i];
-            int32_t before = 0;
+            int32_t before = total % 2 && all[total - 1] > e;
 #pragma unroll 4
-            for (int32_t q = 0; q < total; ++q) before += all[q] > e;
+            for (int32_t q = 0; q + 1 < total; q += 2) {
+                const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(all + q);
+                before += (o.x > e) + (o.y > e);
+            }
             if (before < a.k) {
                 ids[before] = class_of(e);
                 lps[before] = logp_of(value_of((uint32_t)(e >> 32)), s.m, log_z);
@@ -739,9 +776,11 @@ sg_status run_row(const Args<T>& a, int64_t nv, cudaStream_t s) {
 
 template <typename T, int K>
 sg_status run_few(const Args<T>& a, cudaStream_t s) {
-    const size_t smem = kFewRows * (size_t)(a.classes | 1) * 4;
+    const bool raw = a.ld == a.classes && a.classes % 2 == 1 && (uintptr_t)a.x % 16 == 0;
     const uint32_t magic = (uint32_t)((((uint64_t)1 << 32) + a.classes - 1) / a.classes);
-    SG_CUDA(launch_pdl(k_logprobs_few<T, K>, dim3((unsigned)cdiv(a.n_cap, kFewRows)), dim3(kFewRows), smem, s, a, magic));
+    const dim3 grid((unsigned)cdiv(a.n_cap, kFewRows)), block(kFewRows);
+    if (raw) SG_CUDA(launch_pdl(k_logprobs_few<T, K, true>, grid, block, kFewRows * (size_t)a.classes * sizeof(T), s, a, magic));
+    else SG_CUDA(launch_pdl(k_logprobs_few<T, K, false>, grid, block, kFewRows * (size_t)(a.classes | 1) * 4, s, a, magic));
     return SG_OK;
 }
 
@@ -750,10 +789,17 @@ sg_status run(const Args<T>& a, cudaStream_t s) {
     if (a.n_cap == 0) return SG_OK;
     // (a block for every SM at least)
     if (a.classes > 1 && a.classes <= kFewClasses && a.k <= kFewTop && a.n_cap >= kFewRows * num_sms()) {
-        if (a.k <= 1) return run_few<T, 1>(a, s);
-        if (a.k <= 2) return run_few<T, 2>(a, s);
-        if (a.k <= 4) return run_few<T, 4>(a, s);
-        return run_few<T, 8>(a, s);
+        switch (a.k) {
+            case 0:
+            case 1: return run_few<T, 1>(a, s);
+            case 2: return run_few<T, 2>(a, s);
+            case 3: return run_few<T, 3>(a, s);
+            case 4: return run_few<T, 4>(a, s);
+            case 5: return run_few<T, 5>(a, s);
+            case 6: return run_few<T, 6>(a, s);
+            case 7: return run_few<T, 7>(a, s);
+            default: return run_few<T, 8>(a, s);
+        }
     }
     const int64_t nv = cdiv((int64_t)a.classes, kE<T>);  // vectors of a row, at most
     if (nv <= 32) return run_warp<T, 1>(a, s);
