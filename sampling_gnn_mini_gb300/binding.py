@@ -869,11 +869,41 @@ def sg_muon_step(w: torch.Tensor, g: torch.Tensor, m: torch.Tensor, w_out: torch
 def _own_stream(what: str, stream, dev: int) -> int:
     """The raw stream of a call whose tensors are on device dev, which has to
     be the current one (a stream given by its address is taken as it is)."""
-    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+    if stream is None:
+        if torch._C._cuda_getDevice() == dev:
+            return torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, torch.cuda.Stream):
         return int(stream)
-    if torch._C._cuda_getDevice() != dev or (stream is not None and stream.device_index != dev):
-        _invalid("%s: the tensors must be on the current device, and on the stream's" % what)
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    elif torch._C._cuda_getDevice() == dev and stream.device_index == dev:
+        return stream.cuda_stream
+    _invalid("%s: the tensors must be on the current device, and on the stream's" % what)
+
+
+def _array(name: str, t, n: int, dtype, dev: int) -> Optional[int]:
+    """_vector() for an argument that may be None, which is passed on."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.numel() >= n and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _invalid("%s must be a contiguous %s device tensor of %d entries" % (name, dtype, n))
+
+
+def _tops(what: str, ids, values, n_cap: int, dev: int):
+    """(k, address of ids, address of values) of rows of k classes with a value
+    each."""
+    try:
+        shape, k = ids.shape, ids.shape[1]
+        if len(shape) != 2 or values.shape[-1] != k:
+            k = 0
+    except (AttributeError, IndexError):
+        k = 0
+    if not 1 <= k <= SG_MAX_TOP:
+        _invalid("%s: classes and their values must be 2-D with the same 1 to %d columns" % (what, SG_MAX_TOP))
+    return k, _array(what + ": classes", ids, n_cap * k, torch.int32, dev), \
+        _array(what + ": values", values, n_cap * k, torch.float32, dev)
 
 
 def sg_logprobs(logits: torch.Tensor, labels: Optional[torch.Tensor], n_cap: int, d_n: Optional[torch.Tensor],
@@ -885,24 +915,17 @@ def sg_logprobs(logits: torch.Tensor, labels: Optional[torch.Tensor], n_cap: int
     dev = logits.get_device()
     c = logits.shape[1] if logits.dim() == 2 else _invalid("sg_logprobs: logits must be 2-D")
     dt, ld = _matrix("sg_logprobs: logits", logits, n_cap, c, dev)
-    p_y = p_logp = p_ids = p_top = None
-    k = 0
-    if labels is not None or logp is not None:
-        p_y = _vector("sg_logprobs: labels", labels, n_cap, torch.int32, dev)
-        p_logp = _vector("sg_logprobs: logp", logp, n_cap, torch.float32, dev)
-    p_ent = None if entropy is None else _vector("sg_logprobs: entropy", entropy, n_cap, torch.float32, dev)
+    if (labels is None) != (logp is None):
+        _invalid("sg_logprobs: labels and logp come together")
+    p_y = _array("sg_logprobs: labels", labels, n_cap, torch.int32, dev)
+    p_logp = _array("sg_logprobs: logp", logp, n_cap, torch.float32, dev)
+    p_ent = _array("sg_logprobs: entropy", entropy, n_cap, torch.float32, dev)
+    k, p_ids, p_top = 0, None, None
     if top_ids is not None or top_logp is not None:
-        if not isinstance(top_ids, torch.Tensor) or top_ids.dim() != 2 or not 1 <= top_ids.shape[1] <= SG_MAX_TOP:
-            _invalid("sg_logprobs: top_ids must be 2-D with 1 to %d columns" % SG_MAX_TOP)
-        k = top_ids.shape[1]
-        p_ids = _vector("sg_logprobs: top_ids", top_ids, n_cap * k, torch.int32, dev)
-        p_top = _vector("sg_logprobs: top_logp", top_logp, n_cap * k, torch.float32, dev)
-        if top_logp.shape[-1] != k:
-            _invalid("sg_logprobs: top_logp must have top_ids' columns")
-    p_n = None if d_n is None else _vector("sg_logprobs: d_n", d_n, 1, torch.int32, dev)
+        k, p_ids, p_top = _tops("sg_logprobs", top_ids, top_logp, n_cap, dev)
+    p_n = _array("sg_logprobs: d_n", d_n, 1, torch.int32, dev)
     raw = _own_stream("sg_logprobs", stream, dev)
-    st = (_lib or load()).sg_logprobs(logits.data_ptr(), dt, n_cap, p_n, c, ld, p_y, k, p_logp, p_ent, p_ids, p_top,
-                                      raw)
+    st = (_lib or load()).sg_logprobs(logits.data_ptr(), dt, n_cap, p_n, c, ld, p_y, k, p_logp, p_ent, p_ids, p_top, raw)
     if st:
         _check(st)
 
@@ -926,36 +949,27 @@ def sg_distill(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, n_
         if dt_g != dt:
             _invalid("sg_distill: grad must have the logits' dtype")
         p_grad = grad.data_ptr()
-    if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or not 1 <= ids.shape[1] <= SG_MAX_TOP:
-        _invalid("sg_distill: ids must be 2-D with 1 to %d columns" % SG_MAX_TOP)
-    k = ids.shape[1]
-    p_ids = _vector("sg_distill: ids", ids, n_cap * k, torch.int32, dev)
-    p_v = _vector("sg_distill: values", values, n_cap * k, torch.float32, dev)
-    if values.shape[-1] != k:
-        _invalid("sg_distill: values must have ids' columns")
+    k, p_ids, p_v = _tops("sg_distill", ids, values, n_cap, dev)
     p_loss = _vector("sg_distill: loss", loss, n_cap, torch.float32, dev)
-    p_total = None if total is None else _vector("sg_distill: total", total, 2, torch.float32, dev)
-    p_n = None if d_n is None else _vector("sg_distill: d_n", d_n, 1, torch.int32, dev)
+    p_total = _array("sg_distill: total", total, 2, torch.float32, dev)
+    p_n = _array("sg_distill: d_n", d_n, 1, torch.int32, dev)
     p_ws, n_ws = _scratch("sg_distill", workspace, dev)
     raw = _own_stream("sg_distill", stream, dev)
     st = (_lib or load()).sg_distill(logits.data_ptr(), dt, n_cap, p_n, c, ld, p_ids, p_v, k, temperature, 1 if mean else 0,
-                                     grad_scale, p_loss, p_total, p_grad, ld_g, p_ws, n_ws,
-                                     raw)
+                                     grad_scale, p_loss, p_total, p_grad, ld_g, p_ws, n_ws, raw)
     if st:
         _check(st)
 
 
-def _param(name: str, t: Optional[torch.Tensor], dim: int, dtype, dev: int) -> Optional[int]:
-    return None if t is None else _vector(name, t, dim, dtype, dev)
-
-
 def _param_dtype(*params) -> torch.dtype:
-    """The dtype that the given weights and biases share (fp32 if there are
-    none)."""
-    kinds = {t.dtype for t in params if isinstance(t, torch.Tensor)}
-    if len(kinds) > 1 or not kinds <= set(_CODES):
-        _invalid("weight and bias (and their gradients) must be float32 or bfloat16 alike")
-    return kinds.pop() if kinds else torch.float32
+    """The dtype of the first given weight, bias or gradient of them (fp32 if
+    there is none); the others' are checked against it."""
+    for t in params:
+        if t is not None:
+            kind = getattr(t, "dtype", None)
+            return kind if kind in _CODES else _invalid("weight and bias (and their gradients) must be float32 or "
+                                                        "bfloat16 alike")
+    return torch.float32
 
 
 def sg_layernorm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optional[torch.Tensor], n_cap: int,
@@ -970,11 +984,11 @@ def sg_layernorm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Opti
     if dt_o != dt:
         _invalid("sg_layernorm_fwd: out must have x's dtype")
     kind = _param_dtype(weight, bias)
-    p_w = _param("sg_layernorm_fwd: weight", weight, dim, kind, dev)
-    p_b = _param("sg_layernorm_fwd: bias", bias, dim, kind, dev)
-    p_m = _param("sg_layernorm_fwd: mean", mean, n_cap, torch.float32, dev)
-    p_r = _param("sg_layernorm_fwd: rstd", rstd, n_cap, torch.float32, dev)
-    p_n = _param("sg_layernorm_fwd: d_n", d_n, 1, torch.int32, dev)
+    p_w = _array("sg_layernorm_fwd: weight", weight, dim, kind, dev)
+    p_b = _array("sg_layernorm_fwd: bias", bias, dim, kind, dev)
+    p_m = _array("sg_layernorm_fwd: mean", mean, n_cap, torch.float32, dev)
+    p_r = _array("sg_layernorm_fwd: rstd", rstd, n_cap, torch.float32, dev)
+    p_n = _array("sg_layernorm_fwd: d_n", d_n, 1, torch.int32, dev)
     raw = _own_stream("sg_layernorm_fwd", stream, dev)
     st = (_lib or load()).sg_layernorm_fwd(x.data_ptr(), dt, n_cap, p_n, dim, ld, p_w, p_b, _CODES[kind], eps,
                                            out.data_ptr(), ld_o, p_m, p_r, raw)
@@ -1000,16 +1014,15 @@ def sg_layernorm_bwd(g: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Te
     if dt_g != dt or dt_d != dt:
         _invalid("sg_layernorm_bwd: g and dx must have x's dtype")
     kind = _param_dtype(weight, dweight, dbias)
-    p_w = _param("sg_layernorm_bwd: weight", weight, dim, kind, dev)
-    p_dw = _param("sg_layernorm_bwd: dweight", dweight, dim, kind, dev)
-    p_db = _param("sg_layernorm_bwd: dbias", dbias, dim, kind, dev)
+    p_w = _array("sg_layernorm_bwd: weight", weight, dim, kind, dev)
+    p_dw = _array("sg_layernorm_bwd: dweight", dweight, dim, kind, dev)
+    p_db = _array("sg_layernorm_bwd: dbias", dbias, dim, kind, dev)
     p_m = _vector("sg_layernorm_bwd: mean", mean, n_cap, torch.float32, dev)
     p_r = _vector("sg_layernorm_bwd: rstd", rstd, n_cap, torch.float32, dev)
-    p_n = _param("sg_layernorm_bwd: d_n", d_n, 1, torch.int32, dev)
+    p_n = _array("sg_layernorm_bwd: d_n", d_n, 1, torch.int32, dev)
     p_ws, n_ws = _scratch("sg_layernorm_bwd", workspace, dev)
     raw = _own_stream("sg_layernorm_bwd", stream, dev)
     st = (_lib or load()).sg_layernorm_bwd(g.data_ptr(), x.data_ptr(), dt, n_cap, p_n, dim, ld_g, ld, p_w, _CODES[kind],
-                                           p_m, p_r, dx.data_ptr(), ld_d, p_dw, p_db, p_ws, n_ws,
-                                           raw)
+                                           p_m, p_r, dx.data_ptr(), ld_d, p_dw, p_db, p_ws, n_ws, raw)
     if st:
         _check(st)

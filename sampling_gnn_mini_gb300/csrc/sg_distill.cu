@@ -196,6 +196,68 @@ __device__ __forceinline__ void put_total(const Args<T>& a, int32_t n) {
 }
 
 // ------------------------------------------------------------ rows by warps
+// A row in NV vectors a lane; returns its loss (in every lane).
+template <typename T, int NV>
+__device__ __forceinline__ float warp_row(const Args<T>& a, int32_t r, float w, Entries& mine, Table& table) {
+    const int lane = (int)lane_id();
+    const T* row = a.x + (int64_t)r * a.ld;
+    T* out = a.grad ? a.grad + (int64_t)r * a.ld_grad : nullptr;
+    const bool used = row_used(a, r);
+    load_entries(a, r, row, true, mine);
+    if (!used) {
+        if (lane == 0) a.loss[r] = 0.f;
+        if (out)
+            for (int32_t c = lane; c < a.classes; c += 32) put(out + c, 0.f);
+        return 0.f;
+    }
+    const RowParts<T> part(row, a.classes);
+    uint4 x[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int32_t v = lane + 32 * k;
+        x[k] = v < part.vecs ? *reinterpret_cast<const uint4*>(row + part.head + v * kE<T>) : empty_part<T>();
+    }
+    const int32_t ce = part.edge(lane);
+    const float xe = ce >= 0 ? to_f(row[ce]) : -INFINITY;
+    const Scale scale = scale_entries(a, mine);  // (each lane's own entries)
+    float m = xe;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) m = fmaxf(m, part_max<T>(x[k]));
+    m = warp_max(m);
+    if (m == -INFINITY) m = 0.f;
+    const Base base(m, a.l);
+    f2 sum = pair(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) part_exp<T>(x[k], base, sum);
+    float z, z1;
+    unpair(sum, z, z1);
+    z = warp_sum(z + z1 + base.of(xe));
+    const float loss = loss_of(a, scale, mine, m, z);
+    if (lane == 0) a.loss[r] = loss;
+    if (!out) return loss;
+    const bool same = same_phase(row, (const T*)out);
+    const float inv = z == 0.f ? 0.f : w / z;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int32_t v = lane + 32 * k;
+        if (v < part.vecs)
+            store_part(out + part.head + v * kE<T>, same, part_grad<T>(x[k], base, pair(inv, inv)));
+    }
+    if (ce >= 0) put(out + ce, inv * base.of(xe));
+    table.clear(lane, 32);
+    __syncwarp();  // the entries are there, the vectors stored
+    bool twice = false;
+    for (int32_t j = lane; j < a.k; j += 32)
+        if (mine.id[j] >= 0) twice |= table.insert(mine.id[j]);
+    twice = __any_sync(0xFFFFFFFFu, twice);
+    for (int32_t j = lane; j < a.k; j += 32) {
+        float g;
+        if (entry_grad(a, mine, j, twice, w, m, z, g)) put(out + mine.id[j], g);
+    }
+    __syncwarp();  // before the next row's entries
+    return loss;
+}
+
 template <typename T, int NV>
 __global__ void __launch_bounds__(kThreads, 3) k_distill_warp(Args<T> a) {
     pdl_start();
@@ -203,69 +265,12 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill_warp(Args<T> a) {
     __shared__ Entries entries[kWarps];
     __shared__ Table tables[kWarps];
     __shared__ bool last;
-    const int lane = (int)lane_id();
+    const int warp = (int)(threadIdx.x >> 5);
     const int32_t n = rows_of(a.d_n, a.n_cap), blocks = min((int32_t)gridDim.x, (n + kWarps - 1) / kWarps);
     if ((int32_t)blockIdx.x >= blocks) return;
     const float w = weight_of(a);
-    Entries& mine = entries[threadIdx.x >> 5];
-    Table& table = tables[threadIdx.x >> 5];
-    for (int32_t r = (int32_t)blockIdx.x * kWarps + (int32_t)(threadIdx.x >> 5); r < n; r += (int32_t)gridDim.x * kWarps) {
-        const T* row = a.x + (int64_t)r * a.ld;
-        T* out = a.grad ? a.grad + (int64_t)r * a.ld_grad : nullptr;
-        const bool used = row_used(a, r);
-        load_entries(a, r, row, true, mine);
-        if (!used) {
-            if (lane == 0) a.loss[r] = 0.f;
-            if (out)
-                for (int32_t c = lane; c < a.classes; c += 32) put(out + c, 0.f);
-            continue;
-        }
-        const RowParts<T> part(row, a.classes);
-        uint4 x[NV];
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int32_t v = lane + 32 * k;
-            x[k] = v < part.vecs ? *reinterpret_cast<const uint4*>(row + part.head + v * kE<T>) : empty_part<T>();
-        }
-        const int32_t ce = part.edge(lane);
-        const float xe = ce >= 0 ? to_f(row[ce]) : -INFINITY;
-        const Scale scale = scale_entries(a, mine);  // (each lane's own entries)
-        float m = xe;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) m = fmaxf(m, part_max<T>(x[k]));
-        m = warp_max(m);
-        if (m == -INFINITY) m = 0.f;
-        const Base base(m, a.l);
-        f2 sum = pair(0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < NV; ++k) part_exp<T>(x[k], base, sum);
-        float z, z1;
-        unpair(sum, z, z1);
-        z = warp_sum(z + z1 + base.of(xe));
-        const float loss = loss_of(a, scale, mine, m, z);
-        if (lane == 0) a.loss[r] = loss;
-        if (!out) continue;
-        const bool same = same_phase(row, (const T*)out);
-        const float inv = z == 0.f ? 0.f : w / z;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int32_t v = lane + 32 * k;
-            if (v < part.vecs)
-                store_part(out + part.head + v * kE<T>, same, part_grad<T>(x[k], base, pair(inv, inv)));
-        }
-        if (ce >= 0) put(out + ce, inv * base.of(xe));
-        table.clear(lane, 32);
-        __syncwarp();  // the entries are there, the vectors stored
-        bool twice = false;
-        for (int32_t j = lane; j < a.k; j += 32)
-            if (mine.id[j] >= 0) twice |= table.insert(mine.id[j]);
-        twice = __any_sync(0xFFFFFFFFu, twice);
-        for (int32_t j = lane; j < a.k; j += 32) {
-            float g;
-            if (entry_grad(a, mine, j, twice, w, m, z, g)) put(out + mine.id[j], g);
-        }
-        __syncwarp();  // before the next row's entries
-    }
+    for (int32_t r = (int32_t)blockIdx.x * kWarps + warp; r < n; r += (int32_t)gridDim.x * kWarps)
+        warp_row<T, NV>(a, r, w, entries[warp], tables[warp]);
     if (!a.total) return;
     __threadfence();
     __syncthreads();
@@ -275,6 +280,45 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill_warp(Args<T> a) {
         __threadfence();
         put_total<kThreads>(a, n);
     }
+}
+
+// The whole of a small call in one cluster: each CTA counts the rows with a teacher, the
+// cluster's warps take the rows in turn, the warps' sums meet in CTA 0.  256 rows of
+// 128 fp32, 8 entries: SPEED_SMALL us with the host's time, by two launches 9.7.
+constexpr int kSmallCtas = 8;
+template <typename T, int NV>
+__global__ void __launch_bounds__(kThreads) k_distill_small(Args<T> a) {
+    pdl_start();
+    constexpr int kWarps = kThreads / 32;
+    __shared__ Entries entries[kWarps];
+    __shared__ Table tables[kWarps];
+    __shared__ int32_t sh[kWarps + 1];
+    __shared__ float part[kWarps];
+    const int warp = (int)(threadIdx.x >> 5);
+    const int32_t n = rows_of(a.d_n, a.n_cap);
+    int32_t v = 0;
+    for (int32_t i = (int32_t)threadIdx.x; i < n; i += kThreads) v += row_used(a, i);
+    v = block_sum<kThreads, int32_t>(v, sh);
+    const float w = a.gs * a.temp / (a.mean ? (float)max(1, v) : 1.f);
+    float sum = 0.f;
+    for (int32_t r = (int32_t)blockIdx.x * kWarps + warp; r < n; r += kSmallCtas * kWarps)
+        sum += warp_row<T, NV>(a, r, w, entries[warp], tables[warp]);
+    if (lane_id() == 0) part[warp] = sum;
+    cluster_sync();
+    if (blockIdx.x == 0 && warp == 0 && a.total) {
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < kSmallCtas * kWarps; k += 32) {
+            const int t = k + (int)threadIdx.x;
+            s += ld_cluster(map_rank(smem_addr(part + t % kWarps), (uint32_t)(t / kWarps)));
+        }
+        s = warp_sum(s);
+        if (threadIdx.x == 0) {
+            a.total[0] = a.mean ? s / (float)max(1, v) : s;
+            a.total[1] = (float)v;
+        }
+    }
+    cluster_sync();  // the parts stay until they are read
 }
 
 // --------------------------------------------------------- rows by clusters
@@ -621,7 +665,11 @@ __global__ void __launch_bounds__(kCountThreads) k_distill_count(const int32_t* 
 
 // -------------------------------------------------------------------- host
 template <typename T, int NV>
-sg_status run_warp(const Args<T>& a, cudaStream_t s) {
+sg_status run_warp(const Args<T>& a, bool small, cudaStream_t s) {
+    if (small) {
+        SG_CUDA(launch_cluster(k_distill_small<T, NV>, kSmallCtas, kThreads, kSmallCtas, s, 0, a));
+        return SG_OK;
+    }
     int64_t blocks = cdiv(a.n_cap, kThreads / 32);
     if (blocks > (int64_t)num_sms() * 3) blocks = (int64_t)num_sms() * 3;
     SG_CUDA(launch_pdl(k_distill_warp<T, NV>, dim3((unsigned)blocks), dim3(kThreads), 0, s, a));
@@ -647,17 +695,22 @@ sg_status run_stream(const Args<T>& a, int64_t nv, cudaStream_t s) {
 
 template <typename T>
 sg_status run(Args<T> a, cudaStream_t s) {
-    a.counts = (int32_t)cdiv(a.n_cap, 2 * kCountThreads);
-    if (a.counts < 1) a.counts = 1;
-    if (a.counts > kCounts) a.counts = kCounts;
-    SG_CUDA(launch_pdl(k_distill_count, dim3((unsigned)a.counts), dim3(kCountThreads), 0, s, a.ids, a.values, a.k, a.classes,
-                       a.n_cap, a.d_n, a.done, a.total));
-    if (a.n_cap == 0) return SG_OK;
     const int64_t nv = cdiv((int64_t)a.classes, kE<T>);  // vectors of a row, at most
-    if (nv <= 32) return run_warp<T, 1>(a, s);
-    if (nv <= 64) return run_warp<T, 2>(a, s);
-    if (nv <= 128) return run_warp<T, 4>(a, s);
-    if (nv <= 256) return run_warp<T, 8>(a, s);
+    const bool by_warp = nv <= 256;
+    // one cluster serves a call whose rows its warps take in a few turns
+    const bool small = by_warp && a.n_cap <= 256 && a.n_cap * nv <= kSmallCtas * kThreads * kVecs;
+    if (!small) {
+        a.counts = (int32_t)cdiv(a.n_cap, 2 * kCountThreads);
+        if (a.counts < 1) a.counts = 1;
+        if (a.counts > kCounts) a.counts = kCounts;
+        SG_CUDA(launch_pdl(k_distill_count, dim3((unsigned)a.counts), dim3(kCountThreads), 0, s, a.ids, a.values, a.k,
+                           a.classes, a.n_cap, a.d_n, a.done, a.total));
+        if (a.n_cap == 0) return SG_OK;
+    }
+    if (nv <= 32) return run_warp<T, 1>(a, small, s);
+    if (nv <= 64) return run_warp<T, 2>(a, small, s);
+    if (nv <= 128) return run_warp<T, 4>(a, small, s);
+    if (nv <= 256) return run_warp<T, 8>(a, small, s);
     const int wide = nv <= 7 * kThreads ? 1 : nv <= kStreamVecs ? 2 : nv <= 2 * kStreamVecs ? 4 : nv <= 4 * kStreamVecs ? 8 : 16;
     if (nv <= 8 * kStreamVecs && (int64_t)a.n_cap * wide >= (wide <= 4 ? 6 : 12) * num_sms()) {
         switch (wide) {

@@ -33,13 +33,14 @@ using namespace sgi;
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of a block of warps' rows
 constexpr int kWarps = kThreads / 32;
 constexpr int kTurn = 4;      // vectors a thread takes at a time
 constexpr int kRing = 2;      // turns of them in shared memory
 constexpr int kGroups = 16;   // groups of a thread's vectors, at most
-constexpr int kCap = 512;     // candidates a CTA holds; at least 4 SG_MAX_TOP for the bound's slack
-constexpr int kHits = 512;    // groups it reads again
+// Candidates that a CTA of NT threads holds, and groups it reads again.
+template <int NT>
+constexpr int kCap = NT < 256 ? 2 * SG_MAX_TOP : 4 * SG_MAX_TOP;
 constexpr int kWarpCap = 256; // candidates a warp holds
 constexpr float kNone = -200.f;  // 2^x is 0 from here on
 
@@ -163,78 +164,117 @@ __device__ __forceinline__ void unpack(const uint4& u, float (&f)[kE<T>]) {
 // ------------------------------------------------------------ rows by threads
 // kFewRows rows of up to kFewClasses classes to a block, in shared memory, then a
 // thread a row.  A thread's top K sit in registers in order: a logit moves in where it
-// is larger, so that equal ones stay in the order of their classes.  RAW: the rows
-// follow one another from a 16-byte boundary and their length is odd, so that they
-// are copied as they are (threads meet different banks); if not, value by value at an
-// odd pitch (magic: ceil(2^32 / classes)).
-constexpr int kFewRows = 128, kFewClasses = 64, kFewTop = 8;
+// is larger, so that equal ones stay in the order of their classes.  The rows are
+// copied
+//   by vectors when every row is on 16 bytes, at an odd pitch of vectors, filled up
+//              with -inf (threads that read a vector each meet different banks);
+//   whole      when they follow one another from a 16-byte boundary (threads that
+//              read one element each meet at most in twos: the length is no multiple
+//              of 16 bytes);
+//   by values  if neither, at an odd pitch (up to kFewByValues classes: the index
+//              arithmetic costs more than a warp a row from there on).
+// us, 100,000 rows of fp32, k = 5, this / a warp a row: 47 classes 12 / 60, 101 21 / 61,
+// 128 30 / 60 (k = 8: 44 / 61).
+constexpr int kFewRows = 128, kFewClasses = 128, kFewByValues = 64, kFewTop = 8;
+enum Few { kWhole, kByVectors, kByValues };
 
-template <typename T, int K, bool RAW>
-__global__ void __launch_bounds__(kFewRows) k_logprobs_few(Args<T> a, uint32_t magic) {
+// Rows in shared memory: elements to f(value, class), in order.
+template <typename T, Few HOW, typename F>
+__device__ __forceinline__ void few_each(const uint4* smem, int32_t pitch, int32_t classes, F f) {
+    if constexpr (HOW == kByVectors) {
+        const uint4* row = smem + (int32_t)threadIdx.x * pitch;
+#pragma unroll 2
+        for (int32_t v = 0; v * kE<T> < classes; ++v) {
+            float e[kE<T>];
+            unpack<T>(row[v], e);
+#pragma unroll
+            for (int i = 0; i < kE<T>; ++i) f(e[i], v * kE<T> + i);
+        }
+    } else {
+        typedef std::conditional_t<HOW == kWhole, T, float> M;
+        const M* row = reinterpret_cast<const M*>(smem) + (int32_t)threadIdx.x * pitch;
+#pragma unroll 4
+        for (int32_t c = 0; c < classes; ++c) f(to_f(row[c]), c);
+    }
+}
+
+// pitch: of rows in shared memory (vectors or elements); magic: ceil(2^32 / d), d > 1 the
+// whole vectors or the elements of a row (i / d is exact for the i < 2^14 here)
+template <typename T, int K, Few HOW>
+__global__ void __launch_bounds__(kFewRows) k_logprobs_few(Args<T> a, int32_t pitch, uint32_t magic) {
     extern __shared__ __align__(16) uint4 few_smem[];
     pdl_start();
     const int32_t n = rows_of(a.d_n, a.n_cap), r0 = (int32_t)blockIdx.x * kFewRows, classes = a.classes;
     if (r0 >= n) return;
-    const int32_t pitch = RAW ? classes : classes | 1, all = min(kFewRows, n - r0) * classes;
+    const int32_t rows = min(kFewRows, n - r0);
     const T* x = a.x + (int64_t)r0 * a.ld;
-    typedef std::conditional_t<RAW, T, float> M;
-    M* rows = reinterpret_cast<M*>(few_smem);
-    if constexpr (RAW) {
-        const int32_t vecs = all / kE<T>;
+    if constexpr (HOW == kWhole) {
+        T* to = reinterpret_cast<T*>(few_smem);
+        const int32_t all = rows * classes, vecs = all / kE<T>;
         for (int32_t i = (int32_t)threadIdx.x; i < vecs; i += kFewRows) copy_async(few_smem + i, x + i * kE<T>);
-        copies_end();
         const int32_t i = vecs * kE<T> + (int32_t)threadIdx.x;
-        if (i < all) rows[i] = x[i];
-        copies_wait<0>();
-    } else {
-        for (int32_t i0 = (int32_t)threadIdx.x; i0 < all; i0 += 16 * kFewRows) {
-            T v[16];
-            int32_t to[16];
+        if (i < all) to[i] = x[i];
+    } else if constexpr (HOW == kByVectors) {
+        const int32_t vecs = classes / kE<T>, all = rows * vecs;
+        for (int32_t i = (int32_t)threadIdx.x; i < all; i += kFewRows) {
+            const int32_t row = vecs == 1 ? i : (int32_t)__umulhi((uint32_t)i, magic), v = i - row * vecs;
+            copy_async(few_smem + row * pitch + v, x + row * a.ld + v * kE<T>);
+        }
+        if (vecs * kE<T> < classes && (int32_t)threadIdx.x < rows) {  // a thread's own row
+            uint4 u = empty_part<T>();
+            T* e = reinterpret_cast<T*>(&u);
 #pragma unroll
-            for (int u = 0; u < 16; ++u) {
+            for (int i = 0; i < kE<T>; ++i)
+                if (vecs * kE<T> + i < classes) e[i] = x[(int32_t)threadIdx.x * a.ld + vecs * kE<T> + i];
+            few_smem[(int32_t)threadIdx.x * pitch + vecs] = u;
+        }
+    } else {
+        float* to = reinterpret_cast<float*>(few_smem);
+        const int32_t all = rows * classes;
+        for (int32_t i0 = (int32_t)threadIdx.x; i0 < all; i0 += 8 * kFewRows) {
+            T v[8];
+            int32_t at[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
                 const int32_t i = i0 + u * kFewRows;
                 const int32_t row = (int32_t)__umulhi((uint32_t)i, magic), c = i - row * classes;
-                to[u] = i < all ? row * pitch + c : -1;
+                at[u] = i < all ? row * pitch + c : -1;
                 if (i < all) v[u] = x[row * a.ld + c];
             }
 #pragma unroll
-            for (int u = 0; u < 16; ++u)
-                if (to[u] >= 0) rows[to[u]] = to_f(v[u]);
+            for (int u = 0; u < 8; ++u)
+                if (at[u] >= 0) to[at[u]] = to_f(v[u]);
         }
     }
+    copies_end();
+    copies_wait<0>();
     __syncthreads();
     const int32_t r = r0 + (int32_t)threadIdx.x;
     if (r >= n) return;
-    const M* row = rows + (int32_t)threadIdx.x * pitch;
     const int32_t y = label_of(a, r);
-    const float xy = y >= 0 ? to_f(row[y]) : 0.f;
+    const float xy = y >= 0 ? to_f(a.x[(int64_t)r * a.ld + y]) : 0.f;
     float top[K];
     int32_t at[K];
 #pragma unroll
     for (int j = 0; j < K; ++j) top[j] = -INFINITY, at[j] = -1;
-#pragma unroll 4
-    for (int32_t c = 0; c < classes; ++c) {
-        float v = to_f(row[c]);
-        if (v > top[K - 1]) {
-            int32_t i = c;
+    few_each<T, HOW>(few_smem, pitch, classes, [&](float v, int32_t c) {
+        if (v > top[K - 1]) {  // the entries below it move down, equal ones above it stay
 #pragma unroll
-            for (int j = 0; j < K; ++j)
-                if (v > top[j]) {
-                    const float w = top[j];
-                    const int32_t q = at[j];
-                    top[j] = v, at[j] = i;
-                    v = w, i = q;
-                }
+            for (int j = K - 1; j > 0; --j) {
+                const bool down = v > top[j - 1], here = v > top[j];
+                at[j] = down ? at[j - 1] : here ? c : at[j];
+                top[j] = down ? top[j - 1] : here ? v : top[j];
+            }
+            if (v > top[0]) top[0] = v, at[0] = c;
         }
-    }
+    });
     Stat s = {top[0], 0.f, 0.f};
     const float b = finite_base(s.m);
-#pragma unroll 4
-    for (int32_t c = 0; c < classes; ++c) {
-        const float d = max_nan((to_f(row[c]) - b) * kLog2e, kNone), e = ex2(d);
+    few_each<T, HOW>(few_smem, pitch, classes, [&](float v, int32_t) {
+        const float d = max_nan((v - b) * kLog2e, kNone), e = ex2(d);
         s.z += e;
         s.t = fmaf(e, d, s.t);
-    }
+    });
     const float log_z = logf(s.z);
     put_row(a, r, s, log_z, y, xy);
     const bool bad = s.z != s.z;
@@ -422,13 +462,15 @@ __global__ void __launch_bounds__(kThreads) k_logprobs_warp(Args<T> a) {
 
 // --------------------------------------------------------- rows by clusters
 // The candidates of a CTA's part of a row.
+template <int CAP>
 struct Candidates {
-    unsigned long long __align__(16) e[kCap];
+    unsigned long long __align__(16) e[CAP];
     int32_t count;
 };
-__device__ __forceinline__ void offer(Candidates& l, float x, int32_t c) {
+template <int CAP>
+__device__ __forceinline__ void offer(Candidates<CAP>& l, float x, int32_t c) {
     const int32_t at = atomicAdd(&l.count, 1);
-    if (at < kCap) l.e[at] = entry_of(order_of(x), c);
+    if (at < CAP) l.e[at] = entry_of(order_of(x), c);
 }
 
 // A CTA's part of a row: vectors v0 .. v0 + count - 1, and for warp 0 of CTA 0 the
@@ -444,21 +486,21 @@ struct Slice {
 };
 
 // Logits of the slice of order o and above (o above that of -inf), over the block.
-template <typename T>
+template <int NT, typename T>
 __device__ __noinline__ int32_t count_from(const Slice<T>& s, uint32_t o, int32_t* sh) {
     int32_t c = s.edge >= 0 && order_of(s.xe) >= o;
-    for (int32_t i = threadIdx.x; i < s.count; i += kThreads) {
+    for (int32_t i = threadIdx.x; i < s.count; i += NT) {
         float f[kE<T>];
         unpack<T>(s.load(i), f);
 #pragma unroll
         for (int e = 0; e < kE<T>; ++e) c += order_of(f[e]) >= o;
     }
-    return block_sum<kThreads, int32_t>(c, sh);
+    return block_sum<NT, int32_t>(c, sh);
 }
-template <typename T>
-__device__ __noinline__ void offer_from(const Slice<T>& s, uint32_t o, Candidates& l) {
+template <int NT, typename T, int CAP>
+__device__ __noinline__ void offer_from(const Slice<T>& s, uint32_t o, Candidates<CAP>& l) {
     if (s.edge >= 0 && order_of(s.xe) >= o) offer(l, s.xe, s.edge);
-    for (int32_t i = threadIdx.x; i < s.count; i += kThreads) {
+    for (int32_t i = threadIdx.x; i < s.count; i += NT) {
         float f[kE<T>];
         unpack<T>(s.load(i), f);
 #pragma unroll
@@ -467,35 +509,35 @@ __device__ __noinline__ void offer_from(const Slice<T>& s, uint32_t o, Candidate
     }
 }
 
-// The slice's k best when more than kCap of its logits have order o and above:
+// The slice's k best when more than CAP of its logits have order o and above:
 // l.count is k at the end.  top: an order that none is above.  Each pass reads the
 // slice from L2.
-template <typename T>
+template <int NT, typename T, int CAP>
 __device__ __noinline__ void select_exactly(const Slice<T>& s, int32_t rank, uint32_t o, uint32_t top, int32_t k,
-                                            Candidates& l, int32_t* sh) {
+                                            Candidates<CAP>& l, int32_t* sh) {
     uint32_t lo = o;               // at least k from here on
-    int32_t have = kCap + 1;       // how many (or more)
-    const int32_t above = count_from(s, lo + 1, sh);
+    int32_t have = CAP + 1;       // how many (or more)
+    const int32_t above = count_from<NT>(s, lo + 1, sh);
     uint32_t hi = lo + 1;          // fewer than k from here on
     if (above >= k) {
         lo = lo + 1;
         have = above;
         hi = top + 1;
-        while (have > kCap && hi - lo > 1) {
+        while (have > CAP && hi - lo > 1) {
             const uint32_t mid = lo + (hi - lo) / 2;
-            const int32_t c = count_from(s, mid, sh);
+            const int32_t c = count_from<NT>(s, mid, sh);
             if (c >= k) lo = mid, have = c;
             else hi = mid;
         }
     }
     if (threadIdx.x == 0) l.count = 0;
     __syncthreads();
-    if (have <= kCap) {
-        offer_from(s, lo, l);
+    if (have <= CAP) {
+        offer_from<NT>(s, lo, l);
         __syncthreads();
         return;
     }
-    offer_from(s, lo + 1, l);  // fewer than k
+    offer_from<NT>(s, lo + 1, l);  // fewer than k
     __syncthreads();
     // the others are equal to lo: the lowest classes of them
     int32_t filled = l.count;
@@ -503,11 +545,11 @@ __device__ __noinline__ void select_exactly(const Slice<T>& s, int32_t rank, uin
     const int32_t begin[2] = {rank == 0 ? 0 : s.first(0), s.part.head + s.part.vecs * kE<T>};
     const int32_t end[2] = {s.first(s.count), rank == 0 ? s.part.head + s.part.vecs * kE<T> + s.part.tail : begin[1]};
     for (int p = 0; p < 2; ++p)
-        for (int32_t c0 = begin[p]; c0 < end[p] && filled < k; c0 += kThreads) {
+        for (int32_t c0 = begin[p]; c0 < end[p] && filled < k; c0 += NT) {
             const int32_t c = c0 + (int32_t)threadIdx.x;
             const bool eq = c < end[p] && order_of(to_f(s.row[c])) == lo;
             int32_t total;
-            const int32_t at = filled + block_excl_scan<kThreads, int32_t>(eq, sh, total);
+            const int32_t at = filled + block_excl_scan<NT, int32_t>(eq, sh, total);
             if (eq && at < k) l.e[at] = entry_of(lo, c);
             filled += total;
         }
@@ -529,23 +571,30 @@ __device__ __forceinline__ float warp_sort(float x) {
     return x;
 }
 
-template <typename T, int S>
-__global__ void __launch_bounds__(kThreads, 4) k_logprobs_row(Args<T> a, int32_t turns) {
-    extern __shared__ __align__(16) uint4 ring[];  // kRing turns; CTA 0's candidates of all; then the groups' maxima
+constexpr int kRefine = 16;  // classes a warp from which the bound is refined
+// Maxima of a row that take part in its bound, W warps' (k <= 32 W): each gives 32 at
+// most.
+template <int W>
+constexpr int kTops = 32 * W < 256 ? 32 * W : 256;
+
+template <typename T, int NT, int S>
+__global__ void __launch_bounds__(NT, 1024 / NT) k_logprobs_row(Args<T> a, int32_t turns) {
+    extern __shared__ __align__(16) uint4 ring[];  // kRing turns, in the end CTA 0's candidates of all; the groups' maxima
     pdl_start();
-    constexpr int W = S * kWarps;
+    constexpr int kWarps = NT / 32, W = S * kWarps, CAP = kCap<NT>;
     __shared__ __align__(16) float4 parts[W];
-    __shared__ __align__(16) float tops[kThreads];
-    __shared__ Candidates list;
-    __shared__ int32_t hits[kHits], hit_count;
+    __shared__ __align__(16) float tops[kTops<W>];
+    __shared__ Candidates<CAP> list;
+    __shared__ int32_t hits[CAP], hit_count;
     __shared__ float bound;
-    __shared__ int32_t scan[kThreads / 32 + 1];
+    __shared__ int32_t reach[3];  // groups that reach a bound, counted in turn
+    __shared__ int32_t scan[NT / 32 + 1];
     const int warp = (int)(threadIdx.x >> 5), lane = (int)lane_id();
     const int32_t first = (int32_t)(blockIdx.x / S), rank = (int32_t)(blockIdx.x % S), step = (int32_t)(gridDim.x / S);
     const int32_t n = rows_of(a.d_n, a.n_cap);
     if (first >= n) return;  // the whole cluster
     if constexpr (S > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
-    float* gmax = reinterpret_cast<float*>(ring + (S > 1 && S * kCap > 2 * kRing * kTurn * kThreads ? S * kCap / 2 : kRing * kTurn * kThreads)) + threadIdx.x;
+    float* gmax = reinterpret_cast<float*>(ring + (S > 1 && S * CAP > 2 * kRing * kTurn * NT ? S * CAP / 2 : kRing * kTurn * NT)) + threadIdx.x;
     const auto slice_of = [&](int32_t r) {
         const T* row = a.x + (int64_t)r * a.ld;
         const RowParts<T> part(row, a.classes);
@@ -565,10 +614,10 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs_row(Args<T> a, int32_t
         if (fr < n) {
 #pragma unroll
             for (int k = 0; k < kTurn; ++k) {
-                const int32_t i = (ft * kTurn + k) * kThreads;
-                if (i < fcount) copy_async(ring + (at * kTurn + k) * kThreads + threadIdx.x, from + i * kE<T>);
+                const int32_t i = (ft * kTurn + k) * NT;
+                if (i < fcount) copy_async(ring + (at * kTurn + k) * NT + threadIdx.x, from + i * kE<T>);
             }
-            if (++ft * kTurn * kThreads >= fcount + (int32_t)threadIdx.x) {  // the same in the whole block
+            if (++ft * kTurn * NT >= fcount + (int32_t)threadIdx.x) {  // the same in the whole block
                 fr += step;
                 ft = 0;
                 enter();
@@ -592,17 +641,17 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs_row(Args<T> a, int32_t
         }
         Stat s = stat_of(sl.xe);
         float most = sl.xe;
-        const int32_t span = turns * kTurn * kThreads;  // vectors of a group, over the block
+        const int32_t span = turns * kTurn * NT;  // vectors of a group, over the block
         for (int32_t g0 = 0, g = 0; g0 < sl.count; g0 += span, ++g) {
             float gm = -INFINITY;
-            for (int32_t i0 = g0; i0 < min(sl.count, g0 + span); i0 += kTurn * kThreads) {
+            for (int32_t i0 = g0; i0 < min(sl.count, g0 + span); i0 += kTurn * NT) {
                 fetch(at ? at - 1 : kRing - 1);
                 copies_wait<kRing - 1>();
                 uint4 u[kTurn];
 #pragma unroll
                 for (int k = 0; k < kTurn; ++k) {
-                    const int32_t i = i0 + k * kThreads + (int32_t)threadIdx.x;
-                    u[k] = i < sl.count ? ring[(at * kTurn + k) * kThreads + threadIdx.x] : empty_part<T>();
+                    const int32_t i = i0 + k * NT + (int32_t)threadIdx.x;
+                    u[k] = i < sl.count ? ring[(at * kTurn + k) * NT + threadIdx.x] : empty_part<T>();
                 }
                 if (++at == kRing) at = 0;
                 const float top = parts_max<T>(u);
@@ -621,13 +670,16 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs_row(Args<T> a, int32_t
                 s.z += z1;
                 s.t += t1;
             }
-            gmax[g * kThreads] = gm;
+            gmax[g * NT] = gm;
             most = fmaxf(most, gm);
         }
         s = warp_join(s);
         // the warp's j largest of its lanes' maxima: half as many again as k needs, so that
-        // an uneven share of the warps does not lower the bound
-        const int32_t need = (a.k + W - 1) / W, j = min(need + (need + 1) / 2, kThreads / W), M = W * j;
+        // an uneven share of the warps does not lower the bound (M is a multiple of 4)
+        const int32_t need = (a.k + W - 1) / W;
+        int32_t j = min(need + (need + 1) / 2, kTops<W> / W);
+        if (W == 2) j += j & 1;
+        const int32_t M = W * j;
         if (j == 1) most = s.m;
         else if (j > 1) most = warp_sort(most);
         const int32_t w = rank * kWarps + warp;
@@ -667,37 +719,62 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs_row(Args<T> a, int32_t
             __syncthreads();  // before the next row's parts
             continue;
         }
-        if ((int32_t)threadIdx.x < M) {  // the k-th largest of tops
-            const float v = tops[threadIdx.x];
+        for (int32_t i0 = (int32_t)threadIdx.x; i0 < M; i0 += NT) {  // the k-th largest of tops
+            const float v = tops[i0];
             int32_t before = 0;
 #pragma unroll 2
             for (int32_t q = 0; q < M; q += 4) {
                 const float4 o = *reinterpret_cast<const float4*>(tops + q);
-                const int32_t i = (int32_t)threadIdx.x - q;
+                const int32_t i = i0 - q;
                 before += (o.x > v || (o.x == v && i > 0)) + (o.y > v || (o.y == v && i > 1)) +
                           (o.z > v || (o.z == v && i > 2)) + (o.w > v || (o.w == v && i > 3));
             }
             if (before == a.k - 1) bound = v;
         }
-        if (threadIdx.x == 0) list.count = hit_count = 0;
+        if (threadIdx.x == 0) list.count = hit_count = reach[0] = 0;
         __syncthreads();
-        const float tau = bound;
+        float tau = bound;
         const bool bad = s.z != s.z;
+        if constexpr (S == 1) {
+            // For many classes the threads' maxima are too few for a close bound: more
+            // groups' maxima, by bisection (16,000 x 5000 bf16, k = 100: SPEED_REFINE us)
+            if (a.k > kRefine * W && !bad && tau < s.m) {
+                uint32_t lo = order_of(tau), hi = order_of(s.m) + 1;
+                for (int i = 0; i < 24 && hi - lo > 1; ++i) {
+                    const uint32_t mid = lo + (hi - lo) / 2;
+                    const float v = value_of(mid);
+                    int32_t c = 0;
+                    for (int32_t g0 = 0, g = 0; g0 < sl.count; g0 += span, ++g) c += gmax[g * NT] >= v;
+                    c = __reduce_add_sync(0xFFFFFFFFu, c);
+                    if (lane == 0) atomicAdd(&reach[i % 3], c);
+                    if (threadIdx.x == 0) reach[(i + 1) % 3] = 0;  // (read two barriers ago)
+                    __syncthreads();
+                    c = reach[i % 3];
+                    if (c < a.k) {
+                        hi = mid;
+                    } else {
+                        lo = mid;
+                        if (c <= a.k + a.k / 8) break;
+                    }
+                }
+                tau = value_of(lo);
+            }
+        }
         if (!bad) {
             if (sl.xe >= tau && sl.xe > -INFINITY) offer(list, sl.xe, sl.edge);
             for (int32_t g0 = 0, g = 0; g0 < sl.count; g0 += span, ++g) {
-                const float gm = gmax[g * kThreads];
+                const float gm = gmax[g * NT];
                 if (gm < tau || gm == -INFINITY) continue;
                 const int32_t h = atomicAdd(&hit_count, 1);
-                if (h < kHits) hits[h] = g * kThreads + (int32_t)threadIdx.x;
+                if (h < CAP) hits[h] = g * NT + (int32_t)threadIdx.x;
             }
         }
         __syncthreads();
         // the groups that reach the bound, their vectors over all threads
-        const int32_t each = turns * kTurn, items = min(hit_count, kHits) * each;
-        for (int32_t q = (int32_t)threadIdx.x; q < items; q += kThreads) {
+        const int32_t each = turns * kTurn, items = min(hit_count, CAP) * each;
+        for (int32_t q = (int32_t)threadIdx.x; q < items; q += NT) {
             const int32_t h = hits[q / each];
-            const int32_t i = (h / kThreads * each + q % each) * kThreads + h % kThreads;
+            const int32_t i = (h / NT * each + q % each) * NT + h % NT;
             if (i >= sl.count) continue;
             const uint4 u = sl.load(i);
             if (part_max<T>(u) < tau) continue;
@@ -708,8 +785,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs_row(Args<T> a, int32_t
                 if (f[e] >= tau && f[e] > -INFINITY) offer(list, f[e], sl.first(i) + e);
         }
         __syncthreads();
-        if (list.count > kCap || hit_count > kHits)
-            select_exactly(sl, rank, max(order_of(tau), kOrderNone + 1), order_of(s.m), a.k, list, scan);
+        if (list.count > CAP || hit_count > CAP)
+            select_exactly<NT>(sl, rank, max(order_of(tau), kOrderNone + 1), order_of(s.m), a.k, list, scan);
         const unsigned long long* all = list.e;
         int32_t total = list.count;
         if constexpr (S > 1) {  // CTA 0 takes everybody's
@@ -719,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs_row(Args<T> a, int32_t
                 total = 0;
                 for (uint32_t q = 0; q < S; ++q) {
                     const int32_t c = __float_as_int(ld_cluster(map_rank(smem_addr(&list.count), q)));
-                    for (int32_t i = threadIdx.x; i < c; i += kThreads) {
+                    for (int32_t i = threadIdx.x; i < c; i += NT) {
                         const uint32_t src = map_rank(smem_addr(&list.e[i]), q);
                         asm volatile("ld.shared::cluster.b64 %0, [%1];\n" : "=l"(to[total + i]) : "r"(src) : "memory");
                     }
@@ -732,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs_row(Args<T> a, int32_t
         }
         int32_t* ids = a.top_ids + (int64_t)r * a.k;
         float* lps = a.top_logp + (int64_t)r * a.k;
-        for (int32_t i = threadIdx.x; i < total; i += kThreads) {
+        for (int32_t i = threadIdx.x; i < total; i += NT) {
             const unsigned long long e = all[i];
             int32_t before = total % 2 && all[total - 1] > e;
 #pragma unroll 4
@@ -745,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs_row(Args<T> a, int32_t
                 lps[before] = logp_of(value_of((uint32_t)(e >> 32)), s.m, log_z);
             }
         }
-        for (int32_t i = total + (int32_t)threadIdx.x; i < a.k; i += kThreads) {
+        for (int32_t i = total + (int32_t)threadIdx.x; i < a.k; i += NT) {
             ids[i] = -1;
             lps[i] = bad ? s.z : -INFINITY;
         }
@@ -759,36 +836,57 @@ sg_status run_warp(const Args<T>& a, cudaStream_t s) {
     return SG_OK;
 }
 
-template <typename T, int S>
+template <typename T, int NT, int S>
 sg_status run_row(const Args<T>& a, int64_t nv, cudaStream_t s) {
-    const int64_t per = cdiv(nv, S), all_turns = cdiv(per, kTurn * kThreads);
+    const int64_t per = cdiv(nv, S), all_turns = cdiv(per, kTurn * NT);
     const int64_t turns = all_turns > kGroups ? cdiv(all_turns, kGroups) : 1;
-    int64_t lists = kRing * kTurn * kThreads * 16;
-    if (S > 1 && lists < S * kCap * 8) lists = S * kCap * 8;
-    const int64_t smem = lists + cdiv(all_turns, turns) * kThreads * 4;
+    int64_t lists = kRing * kTurn * NT * 16;
+    if (S > 1 && lists < S * kCap<NT> * 8) lists = S * kCap<NT> * 8;
+    const int64_t smem = lists + cdiv(all_turns, turns) * NT * 4;
     static OncePerDevice set;
-    SG_CUDA(allow_smem(set, k_logprobs_row<T, S>, (int)(lists + kGroups * kThreads * 4)));
+    SG_CUDA(allow_smem(set, k_logprobs_row<T, NT, S>, (int)(lists + kGroups * NT * 4)));
     int64_t clusters = a.n_cap;  // a cluster of several CTAs has one row
-    if (S == 1 && clusters > 4 * num_sms()) clusters = 4 * num_sms();
-    SG_CUDA(launch_cluster(k_logprobs_row<T, S>, (unsigned)(clusters * S), kThreads, S, s, (int)smem, a, (int32_t)turns));
+    if (S == 1 && clusters > (1024 / NT) * num_sms()) clusters = (1024 / NT) * num_sms();
+    SG_CUDA(launch_cluster(k_logprobs_row<T, NT, S>, (unsigned)(clusters * S), NT, S, s, (int)smem, a, (int32_t)turns));
     return SG_OK;
 }
 
+// How rows of few classes reach shared memory.
+template <typename T>
+Few few_of(const Args<T>& a) {
+    const bool on16 = (uintptr_t)a.x % 16 == 0;
+    if (on16 && a.ld % kE<T> == 0) return kByVectors;
+    return on16 && a.ld == a.classes ? kWhole : kByValues;
+}
+
+template <typename T, int K, Few HOW>
+sg_status run_few_as(const Args<T>& a, cudaStream_t s) {
+    const int32_t vecs = (int32_t)cdiv(a.classes, kE<T>);
+    const int32_t pitch = HOW == kWhole ? a.classes : HOW == kByVectors ? vecs | 1 : a.classes | 1;
+    const size_t smem = kFewRows * (size_t)pitch * (HOW == kWhole ? sizeof(T) : HOW == kByVectors ? 16 : 4);
+    const int32_t d = HOW == kByVectors ? a.classes / kE<T> : a.classes;
+    const uint32_t magic = d > 1 ? (uint32_t)((((uint64_t)1 << 32) + d - 1) / d) : 0;  // (1: not used)
+    static OncePerDevice set;
+    SG_CUDA(allow_smem(set, k_logprobs_few<T, K, HOW>, kFewRows * (kFewClasses / 4 + 1) * 16));
+    SG_CUDA(launch_pdl(k_logprobs_few<T, K, HOW>, dim3((unsigned)cdiv(a.n_cap, kFewRows)), dim3(kFewRows), smem, s, a, pitch,
+                       magic));
+    return SG_OK;
+}
 template <typename T, int K>
 sg_status run_few(const Args<T>& a, cudaStream_t s) {
-    const bool raw = a.ld == a.classes && a.classes % 2 == 1 && (uintptr_t)a.x % 16 == 0;
-    const uint32_t magic = (uint32_t)((((uint64_t)1 << 32) + a.classes - 1) / a.classes);
-    const dim3 grid((unsigned)cdiv(a.n_cap, kFewRows)), block(kFewRows);
-    if (raw) SG_CUDA(launch_pdl(k_logprobs_few<T, K, true>, grid, block, kFewRows * (size_t)a.classes * sizeof(T), s, a, magic));
-    else SG_CUDA(launch_pdl(k_logprobs_few<T, K, false>, grid, block, kFewRows * (size_t)(a.classes | 1) * 4, s, a, magic));
-    return SG_OK;
+    switch (few_of(a)) {
+        case kWhole: return run_few_as<T, K, kWhole>(a, s);
+        case kByVectors: return run_few_as<T, K, kByVectors>(a, s);
+        default: return run_few_as<T, K, kByValues>(a, s);
+    }
 }
 
 template <typename T>
 sg_status run(const Args<T>& a, cudaStream_t s) {
     if (a.n_cap == 0) return SG_OK;
     // (a block for every SM at least)
-    if (a.classes > 1 && a.classes <= kFewClasses && a.k <= kFewTop && a.n_cap >= kFewRows * num_sms()) {
+    if (a.classes > 1 && a.classes <= (few_of(a) == kByValues ? kFewByValues : kFewClasses) && a.k <= kFewTop &&
+        a.n_cap >= kFewRows * num_sms()) {
         switch (a.k) {
             case 0:
             case 1: return run_few<T, 1>(a, s);
@@ -805,14 +903,19 @@ sg_status run(const Args<T>& a, cudaStream_t s) {
     if (nv <= 32) return run_warp<T, 1>(a, s);
     if (nv <= 64) return run_warp<T, 2>(a, s);
     if (nv <= 128) return run_warp<T, 4>(a, s);
+    if (nv <= 256) return run_warp<T, 8>(a, s);
+    // small CTAs for rows of a few thousand classes: what every warp does for a row, and
+    // its barriers, cost less
+    if (a.n_cap >= 16 * num_sms() && nv <= 2048 && a.k <= 32) return run_row<T, 64, 1>(a, nv, s);
+    if (a.n_cap >= (nv <= 4096 ? 8 : 16) * num_sms()) return run_row<T, 128, 1>(a, nv, s);
     // clusters while the rows leave SMs idle and every CTA has a turn to do
     int split = 1;
     while (split < 8 && (int64_t)a.n_cap * split * 2 <= 2 * num_sms() && nv >= split * 2 * kThreads) split *= 2;
     switch (split) {
-        case 1: return run_row<T, 1>(a, nv, s);
-        case 2: return run_row<T, 2>(a, nv, s);
-        case 4: return run_row<T, 4>(a, nv, s);
-        default: return run_row<T, 8>(a, nv, s);
+        case 1: return run_row<T, 256, 1>(a, nv, s);
+        case 2: return run_row<T, 256, 2>(a, nv, s);
+        case 4: return run_row<T, 256, 4>(a, nv, s);
+        default: return run_row<T, 256, 8>(a, nv, s);
     }
 }
 

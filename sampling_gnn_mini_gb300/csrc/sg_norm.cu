@@ -19,6 +19,7 @@
 // forward: SPEED_ODD us, all in single values 50.
 #include "sg_internal.cuh"
 #include "sg_rows.cuh"
+#include "sg_tc.cuh"
 
 using namespace sgi;
 
@@ -276,6 +277,8 @@ struct BwdArgs {
     const int32_t* d_n;
     int32_t n_cap, dim, w_bf16, alike;
     float* parts;  // per block: sums of g h, then of g, kLead before the first vector's; NULL: not wanted
+    void* dweight;
+    void* dbias;
 };
 // A block's sums of dim columns: kLead - head before the head's first, so that vectors
 // are on 16 bytes; the two rows are `pitch` apart.
@@ -386,7 +389,12 @@ __device__ __forceinline__ void grad_row(const BwdArgs<T>& a, const Part<T, V, L
 template <typename T, int NT>
 constexpr int kBwdBlocks = NT == kThreads ? (sizeof(T) == 2 ? 2 : 3) : 1;
 
-template <typename T, int V, int L, int NT, int R>
+// SMALL: the whole of a small call in one cluster, whose CTAs' sums meet in distributed
+// shared memory (1,024 x 128 fp32: SPEED_SMALL us with the host's time, with a second
+// launch for the sums 11.3).
+constexpr int kSmallCtas = 8, kSmallTurns = 8;  // turns of a cluster's groups at most
+
+template <typename T, int V, int L, int NT, int R, bool SMALL>
 __global__ void __launch_bounds__(NT, kBwdBlocks<T, NT>) k_norm_bwd(BwdArgs<T> a) {
     pdl_start();
     constexpr int kRows = L <= 32 ? NT / L : 1;
@@ -444,9 +452,11 @@ __global__ void __launch_bounds__(NT, kBwdBlocks<T, NT>) k_norm_bwd(BwdArgs<T> a
     if constexpr (L > 32) {
         sums.put_block(p, a);
     } else {
-        if (!a.parts) return;
-        float* to = a.parts + (int64_t)blockIdx.x * 2 * pitch_of(a.dim) + kLead;
+        if (!SMALL && !a.parts) return;
         constexpr int W = L * V * kE<T> + 16;  // columns of a group
+        __shared__ float block[SMALL ? 2 * W : 1];
+        float* to = SMALL ? block : a.parts + (int64_t)blockIdx.x * 2 * pitch_of(a.dim) + kLead;
+        const int32_t pitch = SMALL ? W : pitch_of(a.dim);
         for (int k = 0; k < 2; ++k) {
             __syncthreads();
             sums.template put<false>(p, k != 0, cols + ((int)threadIdx.x / L) * W);
@@ -455,8 +465,21 @@ __global__ void __launch_bounds__(NT, kBwdBlocks<T, NT>) k_norm_bwd(BwdArgs<T> a
                 float s = 0.f;
 #pragma unroll 8
                 for (int q = 0; q < kRows; ++q) s += cols[q * W + c];
-                to[k * pitch_of(a.dim) + c] = s;
+                to[k * pitch + c] = s;
             }
+        }
+        if constexpr (SMALL) {
+            cluster_sync();
+            for (int32_t o = (int32_t)(blockIdx.x * NT + threadIdx.x); o < 2 * a.dim; o += kSmallCtas * NT) {
+                const int k = o >= a.dim, c = o - k * a.dim;
+                float s = 0.f;
+                for (uint32_t q = 0; q < kSmallCtas; ++q) s += ld_cluster(map_rank(smem_addr(block + k * W + c), q));
+                void* d = k ? a.dbias : a.dweight;
+                if (!d) continue;
+                if (a.w_bf16) put((__nv_bfloat16*)d + c, s);
+                else put((float*)d + c, s);
+            }
+            cluster_sync();  // the sums stay until they are read
         }
     }
 }
@@ -617,10 +640,17 @@ sg_status go(const FwdArgs<T>& a, cudaStream_t s) {
 }
 template <typename T, int V, int L, int NT, int R>
 sg_status go(const BwdArgs<T>& a, cudaStream_t s, int64_t* count, int32_t* heads) {
-    const unsigned blocks = grid_of(a, cdiv(a.n_cap, (L <= 32 ? NT / L : 1) * R), kBwdBlocks<T, NT>);
-    *count = blocks;
+    constexpr int kRows = (L <= 32 ? NT / L : 1) * R;
     *heads = 0;  // (by columns, or rows that are moved value by value)
-    SG_CUDA(launch_pdl(k_norm_bwd<T, V, L, NT, R>, dim3(blocks), dim3(NT), 0, s, a));
+    if constexpr (L <= 32)
+        if (a.n_cap <= kSmallTurns * kSmallCtas * kRows && a.parts) {
+            *count = 0;  // the sums are done
+            SG_CUDA(launch_cluster(k_norm_bwd<T, V, L, NT, R, true>, kSmallCtas, NT, kSmallCtas, s, 0, a));
+            return SG_OK;
+        }
+    const unsigned blocks = grid_of(a, cdiv(a.n_cap, kRows), kBwdBlocks<T, NT>);
+    *count = blocks;
+    SG_CUDA(launch_pdl(k_norm_bwd<T, V, L, NT, R, false>, dim3(blocks), dim3(NT), 0, s, a));
     return SG_OK;
 }
 
@@ -664,17 +694,17 @@ bool known(int32_t dtype) { return dtype == SG_F32 || dtype == SG_BF16; }
 int size_of(int32_t dtype) { return dtype == SG_F32 ? 4 : 2; }
 
 template <typename T>
-sg_status bwd(BwdArgs<T> a, void* dw, void* db, cudaStream_t s) {
+sg_status bwd(const BwdArgs<T>& a, cudaStream_t s) {
     int64_t count = 0;
     int32_t heads = 0;
     if (a.n_cap > 0) {
         const sg_status st = by_size<T>(a, s, &count, &heads);
-        if (st != SG_OK) return st;
+        if (st != SG_OK || count == 0) return st;
     }
     if (!a.parts) return SG_OK;
     SG_CUDA(launch_pdl(k_norm_join, dim3((unsigned)cdiv(2 * (int64_t)a.dim, 32)), dim3(1024), 0, s, (const float*)a.parts,
-                       (int32_t)count, a.dim, dw, db, a.w_bf16, (uintptr_t)a.x, a.ld * (int64_t)sizeof(T), (int32_t)sizeof(T),
-                       heads));
+                       (int32_t)count, a.dim, a.dweight, a.dbias, a.w_bf16, (uintptr_t)a.x, a.ld * (int64_t)sizeof(T),
+                       (int32_t)sizeof(T), heads));
     return SG_OK;
 }
 
@@ -741,10 +771,10 @@ extern "C" sg_status sg_layernorm_bwd(const void* d_g, const void* d_x, int32_t 
     float* parts = d_dweight || d_dbias ? (float*)d_workspace : nullptr;
     if (dtype == SG_F32) {
         const BwdArgs<float> a = {(const float*)d_g, (const float*)d_x, (float*)d_dx, ld_g, ld, ld_dx, d_weight, d_mean,
-                                  d_rstd, d_n, n_cap, dim, dtype_w == SG_BF16, alike, parts};
-        return bwd<float>(a, d_dweight, d_dbias, s);
+                                  d_rstd, d_n, n_cap, dim, dtype_w == SG_BF16, alike, parts, d_dweight, d_dbias};
+        return bwd<float>(a, s);
     }
     const BwdArgs<__nv_bfloat16> a = {(const __nv_bfloat16*)d_g, (const __nv_bfloat16*)d_x, (__nv_bfloat16*)d_dx, ld_g, ld,
-                                      ld_dx, d_weight, d_mean, d_rstd, d_n, n_cap, dim, dtype_w == SG_BF16, alike, parts};
-    return bwd<__nv_bfloat16>(a, d_dweight, d_dbias, s);
+                                      ld_dx, d_weight, d_mean, d_rstd, d_n, n_cap, dim, dtype_w == SG_BF16, alike, parts, d_dweight, d_dbias};
+    return bwd<__nv_bfloat16>(a, s);
 }

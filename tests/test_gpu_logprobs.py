@@ -113,6 +113,51 @@ def test_rows(n, c, k, dt):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("c", [1, 2, 3, 4, 5, 7, 8, 9, 12, 16, 17, 31, 40, 47, 63, 64, 65, 90, 100, 127, 128, 129])
+@pytest.mark.parametrize("gap", [0, 3, 8])
+def test_many_rows_of_few_classes(c, gap, dt):
+    # a thread a row: rows that follow one another, rows on 16 bytes, others
+    n = 20011
+    wide = _logits(n, c + gap, dt, c)
+    x = wide[:, :c]
+    x[5], x[6, c // 2:], x[7] = -INF, -INF, 1.0
+    if c > 2:
+        x[8, 1:] = torch.finfo(DT[dt]).min
+    y = _labels(n, c, c)
+    for k in (0, 1, 2, 3, 4, 5, 6, 7, 8, 9):
+        got = _run(x, y, k)
+        _hold(x, y, got, k)
+        if not k:
+            got = got[:2]
+        if k in (1, 8):
+            m = n - 77
+            part = _run(x, y, k, d_n=torch.tensor([m], dtype=torch.int32, device="cuda"))
+            assert all(torch.equal(a[:m], b[:m]) for a, b in zip(part, got))
+            assert all(bool((t[m:] == (77 if t.dtype == torch.int32 else 7)).all()) for t in part)
+    z = x.clone() if gap == 0 else wide.clone()[:, :c]
+    z[11, c - 1] = float("nan")
+    z[12, 0] = INF
+    bad = _run(z, y, 3)
+    keep = torch.ones(n, dtype=torch.bool, device="cuda")
+    keep[11:13] = False
+    assert all(torch.equal(a[keep], b[keep]) for a, b in zip(bad, _run(x, y, 3)))
+    assert bool((bad[2][11:13] == -1).all()) and bool(torch.isnan(bad[3][11:13]).all()) and bool(torch.isnan(bad[1][11:13]).all())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n,c,k", [(2500, 1300, 5), (2500, 2100, 32), (2500, 3001, 20), (2600, 5003, 100), (2600, 12001, 128), (2500, 16001, 40)])
+@pytest.mark.parametrize("mask", [None, -1e9])
+def test_many_rows_of_some_thousand_classes(n, c, k, mask, dt):
+    # small CTAs that walk over their rows
+    x = _logits(n, c, dt, c + k)
+    if mask is not None:
+        x[::3, k // 2:] = mask  # most classes of every third row are equal
+        x[1::7, 3:] = -INF
+    y = _labels(n, c, k)
+    _hold(x, y, _run(x, y, k), k)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("n,c,k", [(40, 100, 5), (40, 600, 20), (20, 3000, 64), (700, 5000, 20), (6, 40001, 64),
                                    (400, 20003, 100)])
 @pytest.mark.parametrize("kept", [0, 1, 3, 50, "many"])
