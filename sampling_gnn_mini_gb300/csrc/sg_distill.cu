@@ -116,6 +116,7 @@ __device__ __forceinline__ Scale scale_entries(const Args<T>& a, Entries& n) {
     float m = -INFINITY, z = 0.f, q[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
+        if (32 * e >= a.k) break;  // (the same in every lane)
         q[e] = lane + 32 * e < a.k ? n.v[lane + 32 * e] : -INFINITY;
         m = fmaxf(m, q[e]);
     }
@@ -123,13 +124,15 @@ __device__ __forceinline__ Scale scale_entries(const Args<T>& a, Entries& n) {
     if (m == -INFINITY) m = 0.f;  // all of them NaN
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
+        if (32 * e >= a.k) break;
         q[e] = exp_from(q[e], m, a.l);
         z += q[e];
     }
     z = warp_sum(z);
+    const float inv = 1.f / z;
 #pragma unroll
     for (int e = 0; e < kPer; ++e)
-        if (lane + 32 * e < a.k) n.q[lane + 32 * e] = q[e] / z;
+        if (lane + 32 * e < a.k) n.q[lane + 32 * e] = q[e] * inv;
     return {m, logf(z)};
 }
 // The row's loss (one warp, the same in every lane), from the row's maximum M and sum Z.
@@ -149,22 +152,37 @@ __device__ __forceinline__ float loss_of(const Args<T>& a, const Scale& c, const
     }
     return warp_sum(s) * (a.temp * a.temp);
 }
-// One warp: all entries of a row, for itself.
-template <typename T>
-__device__ __forceinline__ void load_entries(const Args<T>& a, int32_t r, const T* row, bool report, Entries& n) {
-    int32_t id[kPer];
-    float v[kPer], x[kPer];
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) load_entry(a, r, (int32_t)lane_id() + 32 * e, report, id[e], v[e]);
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) x[e] = id[e] >= 0 ? to_f(row[id[e]]) : 0.f;
+// One warp: all entries of the R rows r, r + step, .. below n, for itself.
+template <int R, typename T>
+__device__ __forceinline__ void load_entries(const Args<T>& a, int32_t r, int32_t step, int32_t n, Entries* to, bool report = true) {
+    const int lane = (int)lane_id();
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
-        const int32_t j = (int32_t)lane_id() + 32 * e;
-        n.id[j] = id[e];
-        n.v[j] = v[e];
-        n.x[j] = x[e];
+        if (32 * e >= a.k) {  // (the same in every lane)
+#pragma unroll
+            for (int q = 0; q < R; ++q) to[q].id[lane + 32 * e] = -1;
+            continue;
+        }
+        int32_t id[R];
+        float v[R], x[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            id[q] = -1, v[q] = -INFINITY;
+            if (r + q * step < n) load_entry(a, r + q * step, lane + 32 * e, report, id[q], v[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < R; ++q) x[q] = id[q] >= 0 ? to_f(a.x[(int64_t)(r + q * step) * a.ld + id[q]]) : 0.f;
+#pragma unroll
+        for (int q = 0; q < R; ++q) to[q].id[lane + 32 * e] = id[q], to[q].v[lane + 32 * e] = v[q], to[q].x[lane + 32 * e] = x[q];
     }
+}
+// One warp: whether a class occurs more than once; the table is clear.
+template <typename T>
+__device__ __forceinline__ bool any_twice(const Args<T>& a, const Entries& n, Table& table) {
+    bool twice = false;
+    for (int32_t j = (int32_t)lane_id(); j < a.k; j += 32)
+        if (n.id[j] >= 0) twice |= table.insert(n.id[j]);
+    return __any_sync(0xFFFFFFFFu, twice);
 }
 // The gradient at entry j's class; false where there is none.  twice: classes may occur
 // more than once
@@ -196,42 +214,53 @@ __device__ __forceinline__ void put_total(const Args<T>& a, int32_t n) {
 }
 
 // ------------------------------------------------------------ rows by warps
-// A row in NV vectors a lane; returns its loss (in every lane).
+// A row in NV vectors a lane, as loaded.
+template <int NV>
+struct WarpRow {
+    uint4 x[NV];
+    float xe;  // this lane's edge element
+    bool used;
+};
 template <typename T, int NV>
-__device__ __forceinline__ float warp_row(const Args<T>& a, int32_t r, float w, Entries& mine, Table& table) {
+__device__ __forceinline__ void load_row(const Args<T>& a, int32_t r, WarpRow<NV>& d) {
+    const int lane = (int)lane_id();
+    const T* row = a.x + (int64_t)r * a.ld;
+    const RowParts<T> part(row, a.classes);
+    d.used = row_used(a, r);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int32_t v = lane + 32 * k;
+        d.x[k] = v < part.vecs ? *reinterpret_cast<const uint4*>(row + part.head + v * kE<T>) : empty_part<T>();
+    }
+    const int32_t ce = part.edge(lane);
+    d.xe = ce >= 0 ? to_f(row[ce]) : -INFINITY;
+}
+// The row's loss (in every lane) and gradient; mine: its entries.
+template <typename T, int NV>
+__device__ __forceinline__ float finish_row(const Args<T>& a, int32_t r, float w, WarpRow<NV>& d, Entries& mine, Table& table) {
     const int lane = (int)lane_id();
     const T* row = a.x + (int64_t)r * a.ld;
     T* out = a.grad ? a.grad + (int64_t)r * a.ld_grad : nullptr;
-    const bool used = row_used(a, r);
-    load_entries(a, r, row, true, mine);
-    if (!used) {
+    if (!d.used) {
         if (lane == 0) a.loss[r] = 0.f;
         if (out)
             for (int32_t c = lane; c < a.classes; c += 32) put(out + c, 0.f);
         return 0.f;
     }
     const RowParts<T> part(row, a.classes);
-    uint4 x[NV];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int32_t v = lane + 32 * k;
-        x[k] = v < part.vecs ? *reinterpret_cast<const uint4*>(row + part.head + v * kE<T>) : empty_part<T>();
-    }
-    const int32_t ce = part.edge(lane);
-    const float xe = ce >= 0 ? to_f(row[ce]) : -INFINITY;
     const Scale scale = scale_entries(a, mine);  // (each lane's own entries)
-    float m = xe;
+    float m = d.xe;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) m = fmaxf(m, part_max<T>(x[k]));
+    for (int k = 0; k < NV; ++k) m = fmaxf(m, part_max<T>(d.x[k]));
     m = warp_max(m);
     if (m == -INFINITY) m = 0.f;
     const Base base(m, a.l);
     f2 sum = pair(0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) part_exp<T>(x[k], base, sum);
+    for (int k = 0; k < NV; ++k) part_exp<T>(d.x[k], base, sum);
     float z, z1;
     unpair(sum, z, z1);
-    z = warp_sum(z + z1 + base.of(xe));
+    z = warp_sum(z + z1 + base.of(d.xe));
     const float loss = loss_of(a, scale, mine, m, z);
     if (lane == 0) a.loss[r] = loss;
     if (!out) return loss;
@@ -241,15 +270,13 @@ __device__ __forceinline__ float warp_row(const Args<T>& a, int32_t r, float w, 
     for (int k = 0; k < NV; ++k) {
         const int32_t v = lane + 32 * k;
         if (v < part.vecs)
-            store_part(out + part.head + v * kE<T>, same, part_grad<T>(x[k], base, pair(inv, inv)));
+            store_part(out + part.head + v * kE<T>, same, part_grad<T>(d.x[k], base, pair(inv, inv)));
     }
-    if (ce >= 0) put(out + ce, inv * base.of(xe));
+    const int32_t ce = part.edge(lane);
+    if (ce >= 0) put(out + ce, inv * base.of(d.xe));
     table.clear(lane, 32);
     __syncwarp();  // the entries are there, the vectors stored
-    bool twice = false;
-    for (int32_t j = lane; j < a.k; j += 32)
-        if (mine.id[j] >= 0) twice |= table.insert(mine.id[j]);
-    twice = __any_sync(0xFFFFFFFFu, twice);
+    const bool twice = any_twice(a, mine, table);
     for (int32_t j = lane; j < a.k; j += 32) {
         float g;
         if (entry_grad(a, mine, j, twice, w, m, z, g)) put(out + mine.id[j], g);
@@ -269,8 +296,12 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill_warp(Args<T> a) {
     const int32_t n = rows_of(a.d_n, a.n_cap), blocks = min((int32_t)gridDim.x, (n + kWarps - 1) / kWarps);
     if ((int32_t)blockIdx.x >= blocks) return;
     const float w = weight_of(a);
-    for (int32_t r = (int32_t)blockIdx.x * kWarps + warp; r < n; r += (int32_t)gridDim.x * kWarps)
-        warp_row<T, NV>(a, r, w, entries[warp], tables[warp]);
+    for (int32_t r = (int32_t)blockIdx.x * kWarps + warp; r < n; r += (int32_t)gridDim.x * kWarps) {
+        WarpRow<NV> d;
+        load_row(a, r, d);
+        load_entries<1>(a, r, 0, n, &entries[warp]);
+        finish_row(a, r, w, d, entries[warp], tables[warp]);
+    }
     if (!a.total) return;
     __threadfence();
     __syncthreads();
@@ -283,26 +314,40 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill_warp(Args<T> a) {
 }
 
 // The whole of a small call in one cluster: each CTA counts the rows with a teacher, the
-// cluster's warps take the rows in turn, the warps' sums meet in CTA 0.  256 rows of
-// 128 fp32, 8 entries: SPEED_SMALL us with the host's time, by two launches 9.7.
+// cluster's warps take up to R rows each, all their loads in flight together, the
+// warps' sums meet in CTA 0.  256 rows of 128 fp32, 8 entries: SPEED_SMALL us with the
+// host's time (by two launches, and a row after the other, 9.7).
 constexpr int kSmallCtas = 8;
+constexpr int kSmallThreads = 512;
+template <int NV>
+constexpr int kSmallRows = NV <= 2 ? 2 : 1;  // a warp's
+template <int NV>
+constexpr int kSmallBytes = kSmallThreads / 32 * kSmallRows<NV> * (int)sizeof(Entries);
+
 template <typename T, int NV>
-__global__ void __launch_bounds__(kThreads) k_distill_small(Args<T> a) {
+__global__ void __launch_bounds__(kSmallThreads) k_distill_small(Args<T> a) {
+    extern __shared__ __align__(16) uint8_t dsm[];
     pdl_start();
-    constexpr int kWarps = kThreads / 32;
-    __shared__ Entries entries[kWarps];
+    constexpr int kWarps = kSmallThreads / 32, R = kSmallRows<NV>;
     __shared__ Table tables[kWarps];
     __shared__ int32_t sh[kWarps + 1];
     __shared__ float part[kWarps];
     const int warp = (int)(threadIdx.x >> 5);
-    const int32_t n = rows_of(a.d_n, a.n_cap);
+    Entries* entries = reinterpret_cast<Entries*>(dsm) + warp * R;
+    const int32_t n = rows_of(a.d_n, a.n_cap), r0 = (int32_t)blockIdx.x * kWarps + warp, step = kSmallCtas * kWarps;
     int32_t v = 0;
-    for (int32_t i = (int32_t)threadIdx.x; i < n; i += kThreads) v += row_used(a, i);
-    v = block_sum<kThreads, int32_t>(v, sh);
+    for (int32_t i = (int32_t)threadIdx.x; i < n; i += kSmallThreads) v += row_used(a, i);
+    WarpRow<NV> d[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q)
+        if (r0 + q * step < n) load_row(a, r0 + q * step, d[q]);
+    load_entries<R>(a, r0, step, n, entries);
+    v = block_sum<kSmallThreads, int32_t>(v, sh);
     const float w = a.gs * a.temp / (a.mean ? (float)max(1, v) : 1.f);
     float sum = 0.f;
-    for (int32_t r = (int32_t)blockIdx.x * kWarps + warp; r < n; r += kSmallCtas * kWarps)
-        sum += warp_row<T, NV>(a, r, w, entries[warp], tables[warp]);
+#pragma unroll
+    for (int q = 0; q < R; ++q)
+        if (r0 + q * step < n) sum += finish_row(a, r0 + q * step, w, d[q], entries[q], tables[warp]);
     if (lane_id() == 0) part[warp] = sum;
     cluster_sync();
     if (blockIdx.x == 0 && warp == 0 && a.total) {
@@ -358,7 +403,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_row(Args<T> a) {
     Scale scale = {0.f, 0.f};
     Held<T, NT> h;
     h.m = 0.f, h.z = 0.f;
-    if (mine) load_entries(a, r, row, rank == 0, entries);
+    if (mine) load_entries<1>(a, r, 0, n, &entries, rank == 0);
     if (used) {
 #pragma unroll
         for (int k = 0; k < kVecs; ++k)
@@ -421,59 +466,62 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_row(Args<T> a) {
 // Many long rows: the same, with each cluster walking over its rows and the next two
 // rows' slices on their way into shared memory while the current row is worked on.
 //
-// The last warps of a block do nothing but the entries, beside the others: the classes
-// are loaded two rows ahead, their logits one row ahead, q is formed while the row is
-// reduced, and the entries' classes are written once the row's vectors are stored
-// (`stored`), while the other warps are at the next row.  (By the warps that hold
+// The last warps of a block do nothing but the entries, beside the others and a row each
+// in turn: the classes and their logits are loaded while the row before is worked on, q
+// is formed while the row is reduced, and the entries' classes are written once the
+// row's vectors are stored (`stored`), while the other warps are at the next row.  (By the warps that hold
 // vectors, at the row's start: 284 us for 4096 x 50,257 bf16 and 64 entries; loaded
 // ahead, with a barrier a row: 198, with a barrier for the entries' warps alone the
 // same: every row waits for the longest warp.  Now SPEED_STREAM; without entries at
 // all, the cross-entropy, 139.)
-constexpr int kStreamVecs = 3300;  // of a CTA's slice: two buffers of it and the entries, two CTAs an SM
+constexpr int kStreamVecs = 3200;  // of a CTA's slice: two buffers of it and the entries, two CTAs an SM
 template <int NT>
-constexpr int kEntryWarps = NT == 512 ? 3 : 1;
+constexpr int kEntryWarps = NT == 512 ? 3 : 2;
 template <int NT>
-constexpr int kVecThreads = NT - 32 * kEntryWarps<NT>;  // kVecs vectors each: 3,328 or 1,792
+constexpr int kVecThreads = NT - 32 * kEntryWarps<NT>;  // kVecs vectors each: 3,328 or 1,536
 
-// A barrier of THREADS of a block's threads, whole warps; true in all if it is in any.
-template <int THREADS>
-__device__ __forceinline__ bool any_of(bool x) {
-    uint32_t r;
-    asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-        : "=r"(r)
-        : "r"((uint32_t)x), "n"(THREADS)
-        : "memory");
-    return r != 0;
+// A count in shared memory: set by one thread, waited for by others (false after kSpins
+// polls).
+__device__ __forceinline__ void set_count(uint32_t* c, uint32_t v) {
+    asm volatile("st.release.cta.shared.u32 [%0], %1;\n" ::"r"(smem_addr(c)), "r"(v) : "memory");
+}
+__device__ __forceinline__ bool wait_count(const uint32_t* c, uint32_t v) {
+    for (int i = 0; i < kSpins; ++i) {
+        uint32_t x;
+        asm volatile("ld.acquire.cta.shared.u32 %0, [%1];\n" : "=r"(x) : "r"(smem_addr(c)) : "memory");
+        if (x >= v) return true;
+        __nanosleep(32);
+    }
+    return false;
 }
 
 template <typename T, int NT, int S>
 __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_stream(Args<T> a, int32_t slots) {
     extern __shared__ __align__(128) uint8_t dsm[];
     pdl_start();
-    constexpr int NV = kVecThreads<NT>, ET = NT - NV, PE = (SG_MAX_TOP + ET - 1) / ET;  // PE: entries of a thread
+    constexpr int NV = kVecThreads<NT>, EW = kEntryWarps<NT>;
     constexpr int kParts = S * NV / 32;
     __shared__ __align__(8) float2 parts[2][kParts];  // (m, z) of every warp of the cluster, of used rows in turn
     __shared__ __align__(8) uint64_t full[2], met[2];  // buffers; parts
-    __shared__ __align__(8) uint64_t stored[2], read[2];  // a row's vectors are stored; the entries' warps have met it
-    __shared__ Entries entries[2];                     // of used rows in turn
-    __shared__ Table tables[2];
+    __shared__ __align__(8) uint64_t stored[2], read[2];  // a row's vectors are stored; its entries' warps have met it
+    __shared__ Entries entries[EW];
+    __shared__ Table tables[EW];
+    __shared__ uint32_t seen;  // used rows whose parts their entries' warp has met, in order
     __shared__ bool last;
     const int32_t rank = (int32_t)(blockIdx.x % S), first = (int32_t)(blockIdx.x / S), step = (int32_t)(gridDim.x / S);
     const int32_t n = rows_of(a.d_n, a.n_cap), classes = a.classes;
     if (first >= n) return;  // the whole cluster
     if (threadIdx.x == 0) {
         last = false;
+        seen = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&met[i], 1);
             mbar_init(&stored[i], NV / 32);
-            mbar_init(&read[i], S * kEntryWarps<NT>);
+            mbar_init(&read[i], S);
         }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
-    tables[0].clear((int)threadIdx.x, NT);
-    tables[1].clear((int)threadIdx.x, NT);
     __syncthreads();
     if constexpr (S > 1) cluster_sync();  // every CTA runs: its shared memory may be written
     const auto has = [&](int32_t r) { return r < n && row_used(a, r); };
@@ -556,73 +604,57 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_stream(Args<T> a, int
             if (lane_id() == 0) mbar_arrive(&stored[slot]);
         }
     } else {
-        const int32_t t = (int32_t)threadIdx.x - NV;
+        const int e = ((int)threadIdx.x - NV) / 32, lane = (int)lane_id();
         const bool mine = rank == 0 || a.grad;
-        int32_t id1[PE], id2[PE];  // of the next row, and the one after it
-        float v1[PE], v2[PE], x1[PE];
-        const auto load = [&](int32_t r, int32_t (&id)[PE], float (&v)[PE]) {
-#pragma unroll
-            for (int e = 0; e < PE; ++e) {
-                id[e] = -1, v[e] = -INFINITY;
-                if (mine && r < n && t + e * ET < SG_MAX_TOP) load_entry(a, r, t + e * ET, rank == 0, id[e], v[e]);
+        Entries& entry = entries[e];
+        // the cluster's rows g, g + step, .. of which this warp has the e-th: which are used
+        const auto used_of = [&](int32_t g) { return lane < EW && has(g + lane * step); };
+        uint32_t flags = __ballot_sync(0xFFFFFFFFu, used_of(first));
+        if (mine && first + e * step < n) load_entries<1>(a, first + e * step, 0, n, &entry, rank == 0);
+        for (int32_t g = first; g < n; g += EW * step) {
+            const int32_t r = g + e * step;
+            const bool after = used_of(g + EW * step);
+            if (flags >> e & 1u) {
+                const uint32_t u = used + (uint32_t)__popc(flags & ((1u << e) - 1u)), slot = u & 1u, turn = (u >> 1) & 1u;
+                T* out = a.grad ? a.grad + (int64_t)r * a.ld_grad : nullptr;
+                Scale scale = {0.f, 0.f};
+                bool twice = false;
+                if (mine) {
+                    tables[e].clear(lane, 32);
+                    scale = scale_entries(a, entry);
+                    __syncwarp();
+                    twice = any_twice(a, entry, tables[e]);
+                }
+                // (a phase of the barrier can be told from the one two before it only when
+                // that one is over: rows are met in order)
+                if (!wait_count(&seen, u) && lane == 0) dev_err(ERR_TIMEOUT);
+                if (!mbar_wait(&met[slot], turn) && lane == 0) dev_err(ERR_TIMEOUT);
+                __syncwarp();
+                if (lane == 0) set_count(&seen, u + 1);
+                float M, Z;
+                join_parts<kParts>(parts[slot], M, Z, a.l);
+                if (rank == 0) {
+                    const float loss = loss_of(a, scale, entry, M, Z);
+                    if (lane == 0) a.loss[r] = loss;
+                }
+                if (out && !mbar_wait(&stored[slot], turn) && lane == 0) dev_err(ERR_TIMEOUT);
+                __syncwarp();
+                if (lane < S)  // in every CTA of the cluster
+                    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(
+                                     map_rank(smem_addr(&read[slot]), (uint32_t)lane))
+                                 : "memory");
+                if (out) {
+                    const T* row = a.x + (int64_t)r * a.ld;
+                    const RowParts<T> part(row, classes);
+                    const int32_t per = (part.vecs + S - 1) / S, v0 = min(part.vecs, rank * per),
+                                  count = min(part.vecs, v0 + per) - v0;
+                    for (int32_t j = lane; j < a.k; j += 32) put_entries(a, entry, out, part, v0, count, rank, j, twice, w, M, Z);
+                }
+                __syncwarp();  // before the next row's entries
             }
-        };
-        const auto logits = [&](int32_t r) {  // of the entries id1 (-1 when row r is not there)
-#pragma unroll
-            for (int e = 0; e < PE; ++e) x1[e] = id1[e] >= 0 ? to_f(a.x[(int64_t)r * a.ld + id1[e]]) : 0.f;
-        };
-        load(first, id1, v1);
-        load(first + step, id2, v2);
-        logits(first);
-        bool u0 = has(first), u1;
-        for (int32_t r = first; r < n; r += step, u0 = u1) {
-            u1 = has(r + step);
-            T* out = a.grad ? a.grad + (int64_t)r * a.ld_grad : nullptr;
-            const uint32_t slot = used & 1u, turn = (used >> 1) & 1u;
-            // (the slot's last readers met the used row between at the entries' barrier)
-            Entries& entry = entries[slot];
-            bool twice = false;
-            if (u0) {
-#pragma unroll
-                for (int e = 0; e < PE; ++e)
-                    if (id1[e] >= 0) twice |= tables[slot].insert(id1[e]);
-                // for the next used row (all have met the barrier after the last one's inserts)
-                tables[slot ^ 1u].clear(t, ET);
-#pragma unroll
-                for (int e = 0; e < PE; ++e)
-                    if (t + e * ET < SG_MAX_TOP) entry.id[t + e * ET] = id1[e], entry.v[t + e * ET] = v1[e], entry.x[t + e * ET] = x1[e];
-            }
-#pragma unroll
-            for (int e = 0; e < PE; ++e) id1[e] = id2[e], v1[e] = v2[e];
-            logits(r + step);
-            load(r + 2 * step, id2, v2);
-            if (!u0) continue;
-            Scale scale = {0.f, 0.f};
-            if (mine) {  // each warp scales all entries (they write the same)
-                twice = any_of<ET>(twice);
-                scale = scale_entries(a, entry);
-            }
-            if (!mbar_wait(&met[slot], turn) && lane_id() == 0) dev_err(ERR_TIMEOUT);
-            float M, Z;
-            join_parts<kParts>(parts[slot], M, Z, a.l);
-            if (rank == 0 && t < 32) {
-                const float loss = loss_of(a, scale, entry, M, Z);
-                if (t == 0) a.loss[r] = loss;
-            }
-            if (out && !mbar_wait(&stored[slot], turn) && lane_id() == 0) dev_err(ERR_TIMEOUT);
-            __syncwarp();
-            if (lane_id() < S)  // in every CTA of the cluster
-                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(
-                                 map_rank(smem_addr(&read[slot]), lane_id()))
-                             : "memory");
-            ++used;
-            if (!out) continue;
-            const T* row = a.x + (int64_t)r * a.ld;
-            const RowParts<T> part(row, classes);
-            const int32_t per = (part.vecs + S - 1) / S, v0 = min(part.vecs, rank * per),
-                          count = min(part.vecs, v0 + per) - v0;
-#pragma unroll
-            for (int e = 0; e < PE; ++e) put_entries(a, entry, out, part, v0, count, rank, t + e * ET, twice, w, M, Z);
+            used += (uint32_t)__popc(flags);
+            flags = __ballot_sync(0xFFFFFFFFu, after);
+            if (mine && r + EW * step < n) load_entries<1>(a, r + EW * step, 0, n, &entry, rank == 0);
         }
     }
     __threadfence();
@@ -667,7 +699,9 @@ __global__ void __launch_bounds__(kCountThreads) k_distill_count(const int32_t* 
 template <typename T, int NV>
 sg_status run_warp(const Args<T>& a, bool small, cudaStream_t s) {
     if (small) {
-        SG_CUDA(launch_cluster(k_distill_small<T, NV>, kSmallCtas, kThreads, kSmallCtas, s, 0, a));
+        static OncePerDevice set;
+        SG_CUDA(allow_smem(set, k_distill_small<T, NV>, kSmallBytes<NV>));
+        SG_CUDA(launch_cluster(k_distill_small<T, NV>, kSmallCtas, kSmallThreads, kSmallCtas, s, kSmallBytes<NV>, a));
         return SG_OK;
     }
     int64_t blocks = cdiv(a.n_cap, kThreads / 32);
@@ -697,8 +731,9 @@ template <typename T>
 sg_status run(Args<T> a, cudaStream_t s) {
     const int64_t nv = cdiv((int64_t)a.classes, kE<T>);  // vectors of a row, at most
     const bool by_warp = nv <= 256;
-    // one cluster serves a call whose rows its warps take in a few turns
-    const bool small = by_warp && a.n_cap <= 256 && a.n_cap * nv <= kSmallCtas * kThreads * kVecs;
+    // one cluster serves a call whose rows its warps hold at once
+    const int64_t rows = kSmallCtas * (kSmallThreads / 32) * (nv <= 64 ? kSmallRows<2> : kSmallRows<8>);
+    const bool small = by_warp && a.n_cap <= rows;
     if (!small) {
         a.counts = (int32_t)cdiv(a.n_cap, 2 * kCountThreads);
         if (a.counts < 1) a.counts = 1;
@@ -711,7 +746,7 @@ sg_status run(Args<T> a, cudaStream_t s) {
     if (nv <= 64) return run_warp<T, 2>(a, small, s);
     if (nv <= 128) return run_warp<T, 4>(a, small, s);
     if (nv <= 256) return run_warp<T, 8>(a, small, s);
-    const int wide = nv <= 7 * kThreads ? 1 : nv <= kStreamVecs ? 2 : nv <= 2 * kStreamVecs ? 4 : nv <= 4 * kStreamVecs ? 8 : 16;
+    const int wide = nv <= kVecThreads<kThreads> * kVecs ? 1 : nv <= kStreamVecs ? 2 : nv <= 2 * kStreamVecs ? 4 : nv <= 4 * kStreamVecs ? 8 : 16;
     if (nv <= 8 * kStreamVecs && (int64_t)a.n_cap * wide >= (wide <= 4 ? 6 : 12) * num_sms()) {
         switch (wide) {
             case 1: return run_stream<T, kThreads, 1>(a, nv, s);
