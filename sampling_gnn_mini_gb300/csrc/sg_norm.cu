@@ -17,6 +17,8 @@
 // within 16 bytes (rows a multiple of 8 apart), so a thread's columns stay the same.
 // Arrays whose rows do not start alike are moved value by value.  30,011 x 1001 bf16
 // forward: SPEED_ODD us, all in single values 50.
+#include <type_traits>
+
 #include "sg_internal.cuh"
 #include "sg_rows.cuh"
 #include "sg_tc.cuh"
@@ -167,11 +169,11 @@ struct FwdArgs {
     float* rstd;
 };
 
-// One row, from its vectors (get(v)) and ends; held(): called when all are in registers.
-template <typename T, int V, int L, typename Get, typename Held>
+// One row, from its vectors (get(v)) and ends.
+template <typename T, int V, int L, typename Get>
 __device__ __forceinline__ void norm_row(const FwdArgs<T>& a, const Part<T, V, L>& p, const Param<T, V, L>& w,
                                          const Param<T, V, L>& b, int64_t r, int32_t n, float inv, float* sh, int& turn,
-                                         const float (&ends)[Part<T, V, L>::NE], Get get, Held held) {
+                                         const float (&ends)[Part<T, V, L>::NE], Get get) {
     constexpr int P = kE<T> / 2, NE = Part<T, V, L>::NE;
     f2 f[V][P], t = both(0.f);
     float fe[NE], s[1] = {0.f};
@@ -185,7 +187,6 @@ __device__ __forceinline__ void norm_row(const FwdArgs<T>& a, const Part<T, V, L
     for (int e = 0; e < NE; ++e) s[0] += fe[e] = ends[e];
     s[0] += total_of(t);
     group_sum<L, 1>(s, sh, turn);
-    held();
     const float mu = s[0] * inv;
     t = both(0.f);
     s[0] = 0.f;
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(NT, NT == kThreads ? 4 : 1) k_norm_fwd(FwdArgs
 #pragma unroll
         for (int q = 0; q < R; ++q)
             norm_row<T, V, L>(a, p, w, b, b0 + q * kRows + (int)threadIdx.x / L, n, inv, sh, turn, cur.ends[q],
-                              [&](int v) { return cur.x[q][v]; }, [] {});
+                              [&](int v) { return cur.x[q][v]; });
     }
 }
 
@@ -329,6 +330,46 @@ struct Sums {
     }
 };
 
+// The sums of a block's groups of L threads, added up in order: into the workspace or,
+// SMALL, with those of the cluster's other blocks.  cols: room for a group's columns
+// each, not in use.
+constexpr int kSmallCtas = 8, kSmallTurns = 8;  // turns of a cluster's groups at most
+template <typename T, int V, int L>
+constexpr int kGroupColumns = L * V * kE<T> + 16;
+
+template <typename T, int V, int L, int NT, bool SMALL>
+__device__ __forceinline__ void join_groups(const Sums<T, V, L>& sums, const Part<T, V, L>& p, const BwdArgs<T>& a, float* cols) {
+    if (!SMALL && !a.parts) return;
+    constexpr int W = kGroupColumns<T, V, L>;
+    __shared__ float block[SMALL ? 2 * W : 1];
+    float* to = SMALL ? block : a.parts + (int64_t)blockIdx.x * 2 * pitch_of(a.dim) + kLead;
+    const int32_t pitch = SMALL ? W : pitch_of(a.dim);
+    for (int k = 0; k < 2; ++k) {
+        __syncthreads();
+        sums.template put<false>(p, k != 0, cols + ((int)threadIdx.x / L) * W);
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.dim; c += NT) {
+            float s = 0.f;
+#pragma unroll 8
+            for (int q = 0; q < NT / L; ++q) s += cols[q * W + c];
+            to[k * pitch + c] = s;
+        }
+    }
+    if constexpr (SMALL) {
+        cluster_sync();
+        for (int32_t o = (int32_t)(blockIdx.x * NT + threadIdx.x); o < 2 * a.dim; o += kSmallCtas * NT) {
+            const int k = o >= a.dim, c = o - k * a.dim;
+            float s = 0.f;
+            for (uint32_t q = 0; q < kSmallCtas; ++q) s += ld_cluster(map_rank(smem_addr(block + k * W + c), q));
+            void* d = k ? a.dbias : a.dweight;
+            if (!d) continue;
+            if (a.w_bf16) put((__nv_bfloat16*)d + c, s);
+            else put((float*)d + c, s);
+        }
+        cluster_sync();  // the sums stay until they are read
+    }
+}
+
 // One row: the columns' sums and dx.  The row's values are asked for twice (x(v), g(v)
 // and the ends): held over the sums they would take the registers of half the threads.
 // between(): called when the group's sums are there.
@@ -392,7 +433,6 @@ constexpr int kBwdBlocks = NT == kThreads ? (sizeof(T) == 2 ? 2 : 3) : 1;
 // SMALL: the whole of a small call in one cluster, whose CTAs' sums meet in distributed
 // shared memory (1,024 x 128 fp32: SPEED_SMALL us with the host's time, with a second
 // launch for the sums 11.3).
-constexpr int kSmallCtas = 8, kSmallTurns = 8;  // turns of a cluster's groups at most
 
 template <typename T, int V, int L, int NT, int R, bool SMALL>
 __global__ void __launch_bounds__(NT, kBwdBlocks<T, NT>) k_norm_bwd(BwdArgs<T> a) {
@@ -400,7 +440,7 @@ __global__ void __launch_bounds__(NT, kBwdBlocks<T, NT>) k_norm_bwd(BwdArgs<T> a
     constexpr int kRows = L <= 32 ? NT / L : 1;
     constexpr int NE = Part<T, V, L>::NE;
     __shared__ float sh[L > 32 ? 4 * (L / 32) : 1];
-    __shared__ float cols[L > 32 ? 1 : NT * (V * kE<T> + (16 + L - 1) / L)];  // the groups' sums of a column
+    __shared__ float cols[L > 32 ? 1 : NT / L * kGroupColumns<T, V, L>];
     int turn = 0;
     const int32_t n = rows_of(a.d_n, a.n_cap);
     const int64_t step = (int64_t)gridDim.x * (kRows * R);
@@ -452,35 +492,7 @@ __global__ void __launch_bounds__(NT, kBwdBlocks<T, NT>) k_norm_bwd(BwdArgs<T> a
     if constexpr (L > 32) {
         sums.put_block(p, a);
     } else {
-        if (!SMALL && !a.parts) return;
-        constexpr int W = L * V * kE<T> + 16;  // columns of a group
-        __shared__ float block[SMALL ? 2 * W : 1];
-        float* to = SMALL ? block : a.parts + (int64_t)blockIdx.x * 2 * pitch_of(a.dim) + kLead;
-        const int32_t pitch = SMALL ? W : pitch_of(a.dim);
-        for (int k = 0; k < 2; ++k) {
-            __syncthreads();
-            sums.template put<false>(p, k != 0, cols + ((int)threadIdx.x / L) * W);
-            __syncthreads();
-            for (int c = threadIdx.x; c < a.dim; c += NT) {
-                float s = 0.f;
-#pragma unroll 8
-                for (int q = 0; q < kRows; ++q) s += cols[q * W + c];
-                to[k * pitch + c] = s;
-            }
-        }
-        if constexpr (SMALL) {
-            cluster_sync();
-            for (int32_t o = (int32_t)(blockIdx.x * NT + threadIdx.x); o < 2 * a.dim; o += kSmallCtas * NT) {
-                const int k = o >= a.dim, c = o - k * a.dim;
-                float s = 0.f;
-                for (uint32_t q = 0; q < kSmallCtas; ++q) s += ld_cluster(map_rank(smem_addr(block + k * W + c), q));
-                void* d = k ? a.dbias : a.dweight;
-                if (!d) continue;
-                if (a.w_bf16) put((__nv_bfloat16*)d + c, s);
-                else put((float*)d + c, s);
-            }
-            cluster_sync();  // the sums stay until they are read
-        }
+        join_groups<T, V, L, NT, SMALL>(sums, p, a, cols);
     }
 }
 
@@ -489,27 +501,32 @@ __global__ void __launch_bounds__(NT, kBwdBlocks<T, NT>) k_norm_bwd(BwdArgs<T> a
 // shared memory, asynchronously, and waits for its own copies alone; the ends are
 // loaded a row ahead.
 constexpr int kRingBytes = 208 * 1024;  // of an SM
-// Blocks an SM.  A: arrays that are read (1 forward, 2 backward).
-template <int NT, int A>
-constexpr int kRingBlocks = (A == 1 ? 768 : 512) / NT > 0 ? (A == 1 ? 768 : 512) / NT : 1;
+// Threads an SM, by the registers for HELD values of a row a thread.  A: arrays that are
+// read (1 forward, 2 backward).  Backward, 16 values a thread: 512 of 128 registers 80
+// us for 16,384 x 4096 bf16, 768 of 80 105, 1,024 of 64 140.
+template <int HELD, int A>
+constexpr int kRingThreads = A == 1 ? (HELD <= 16 ? 768 : 512) : (HELD <= 8 ? 768 : 512);
+template <int HELD, int A, int NT>
+constexpr int kRingBlocks = kRingThreads<HELD, A> / NT > 0 ? kRingThreads<HELD, A> / NT : 1;
 // Slots: as many as there is room for, four at most.
-template <int V, int NT, int A>
-constexpr int kRoom = kRingBytes / kRingBlocks<NT, A> / (NT * V * A * 16);
-template <int V, int NT, int A>
-constexpr int kDepth = kRoom<V, NT, A> > 4 ? 4 : kRoom<V, NT, A>;
-template <int V, int NT, int A>
-constexpr int kRingSize = kDepth<V, NT, A> * NT * V * A * 16;
+template <typename T, int V, int A, int NT>
+constexpr int kRoom = kRingBytes / kRingBlocks<V * kE<T>, A, NT> / (NT * V * A * 16);
+template <typename T, int V, int A, int NT>
+constexpr int kDepth = kRoom<T, V, A, NT> > 4 ? 4 : kRoom<T, V, A, NT>;
+template <typename T, int V, int A, int NT>
+constexpr int kRingSize = kDepth<T, V, A, NT> * NT * V * A * 16;
 
-template <typename T, int V, int NT>
-__global__ void __launch_bounds__(NT, kRingBlocks<NT, 1>) k_norm_fwd_ring(FwdArgs<T> a) {
+template <typename T, int V, int L, int NT>
+__global__ void __launch_bounds__(NT, kRingBlocks<V * kE<T>, 1, NT>) k_norm_fwd_ring(FwdArgs<T> a) {
     extern __shared__ __align__(128) uint4 ring[];
     pdl_start();
-    constexpr int D = kDepth<V, NT, 1>;
-    __shared__ float sh[4 * (NT / 32)];
+    constexpr int D = kDepth<T, V, 1, NT>, kRows = NT / L;  // kRows: of a block at once
+    __shared__ float sh[L > 32 ? 4 * (L / 32) : 1];
     int turn = 0;
-    const int32_t n = rows_of(a.d_n, a.n_cap), first = (int32_t)blockIdx.x, step = (int32_t)gridDim.x;
-    if (first >= n) return;
-    const Part<T, V, NT> p(a.x, a.ld, first, a.dim, true);
+    const int32_t n = rows_of(a.d_n, a.n_cap), first = (int32_t)blockIdx.x * kRows + (int)threadIdx.x / L;
+    const int32_t step = (int32_t)gridDim.x * kRows;
+    if (first >= n) return;  // whole groups
+    const Part<T, V, L> p(a.x, a.ld, first, a.dim, true);
     const auto slot = [&](int at, int v) { return ring + (at * V + v) * NT + (int)threadIdx.x; };
     const auto fetch = [&](int64_t r, int at) {
         if (r < n) {
@@ -521,7 +538,7 @@ __global__ void __launch_bounds__(NT, kRingBlocks<NT, 1>) k_norm_fwd_ring(FwdArg
     };
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) fetch(first + (int64_t)i * step, i);
-    const Param<T, V, NT> w(p, a.weight, a.w_bf16, 1.f), b(p, a.bias, a.w_bf16, 0.f);
+    const Param<T, V, L> w(p, a.weight, a.w_bf16, 1.f), b(p, a.bias, a.w_bf16, 0.f);
     const float inv = 1.f / (float)a.dim;
     int at = 0;
     float next = p.load_end(a.x + first * a.ld, 0);
@@ -530,21 +547,22 @@ __global__ void __launch_bounds__(NT, kRingBlocks<NT, 1>) k_norm_fwd_ring(FwdArg
         const float end[1] = {next};
         if (r + step < n) next = p.load_end(a.x + (r + step) * a.ld, 0);
         copies_wait<D - 1>();
-        norm_row<T, V, NT>(a, p, w, b, r, n, inv, sh, turn, end,
-                           [&](int v) { return p.has(v) ? *slot(at, v) : make_uint4(0, 0, 0, 0); }, [] {});
+        norm_row<T, V, L>(a, p, w, b, r, n, inv, sh, turn, end,
+                          [&](int v) { return p.has(v) ? *slot(at, v) : make_uint4(0, 0, 0, 0); });
         if (++at == D) at = 0;
     }
 }
 
-template <typename T, int V, int NT>
-__global__ void __launch_bounds__(NT, kRingBlocks<NT, 2>) k_norm_bwd_ring(BwdArgs<T> a) {
+template <typename T, int V, int L, int NT>
+__global__ void __launch_bounds__(NT, kRingBlocks<V * kE<T>, 2, NT>) k_norm_bwd_ring(BwdArgs<T> a) {
     extern __shared__ __align__(128) uint4 ring[];
     pdl_start();
-    constexpr int D = kDepth<V, NT, 2>;
-    __shared__ float sh[4 * (NT / 32)];
+    constexpr int D = kDepth<T, V, 2, NT>, kRows = NT / L;
+    __shared__ float sh[L > 32 ? 4 * (L / 32) : 1];
     int turn = 0;
-    const int32_t n = rows_of(a.d_n, a.n_cap), first = (int32_t)blockIdx.x, step = (int32_t)gridDim.x;
-    const Part<T, V, NT> p(a.x, a.ld, first, a.dim, true);
+    const int32_t n = rows_of(a.d_n, a.n_cap), first = (int32_t)blockIdx.x * kRows + (int)threadIdx.x / L;
+    const int32_t step = (int32_t)gridDim.x * kRows;
+    const Part<T, V, L> p(a.x, a.ld, first, a.dim, true);
     const auto slot = [&](int at, int v) { return ring + (at * 2 * V + v) * NT + (int)threadIdx.x; };  // (g: v + V)
     const auto fetch = [&](int64_t r, int at) {
         if (r < n) {
@@ -559,8 +577,8 @@ __global__ void __launch_bounds__(NT, kRingBlocks<NT, 2>) k_norm_bwd_ring(BwdArg
     };
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) fetch(first + (int64_t)i * step, i);
-    const Param<T, V, NT> w(p, a.weight, a.w_bf16, 1.f);
-    Sums<T, V, NT> sums;
+    const Param<T, V, L> w(p, a.weight, a.w_bf16, 1.f);
+    Sums<T, V, L> sums;
     const float inv = 1.f / (float)a.dim;
     int at = 0;
     struct Next {
@@ -570,19 +588,20 @@ __global__ void __launch_bounds__(NT, kRingBlocks<NT, 2>) k_norm_bwd_ring(BwdArg
         if (r < n) next = {__ldg(a.mean + r), __ldg(a.rstd + r), p.load_end(a.x + r * a.ld, 0), p.load_end(a.g + r * a.ld_g, 0)};
     };
     load(first);
-    for (int64_t r = first; r < n; r += step) {
+    for (int64_t r = first; r < n; r += step) {  // (the same in the whole group)
         fetch(r + (int64_t)(D - 1) * step, at ? at - 1 : D - 1);
         const Next cur = next;
         load(r + step);
         copies_wait<D - 1>();
         const float xe[1] = {cur.xe}, ge[1] = {cur.ge};
-        grad_row<T, V, NT>(
+        grad_row<T, V, L>(
             a, p, w, sums, r, n, inv, sh, turn, cur.mu, cur.rs, xe, ge,
             [&](int v) { return p.has(v) ? *slot(at, v) : make_uint4(0, 0, 0, 0); },
             [&](int v) { return p.has(v) ? *slot(at, v + V) : make_uint4(0, 0, 0, 0); }, [] {});
         if (++at == D) at = 0;
     }
-    sums.put_block(p, a);
+    if constexpr (L == NT) sums.put_block(p, a);
+    else join_groups<T, V, L, NT, false>(sums, p, a, reinterpret_cast<float*>(ring));  // (its copies are all used)
 }
 
 // The blocks' sums in order: 32 columns a block, a 32nd of the blocks' sums a warp.
@@ -654,21 +673,23 @@ sg_status go(const BwdArgs<T>& a, cudaStream_t s, int64_t* count, int32_t* heads
     return SG_OK;
 }
 
-template <typename T, int V, int NT>
+template <typename T, int V, int NT, int L = NT>
 sg_status go_ring(const FwdArgs<T>& a, cudaStream_t s) {
     static OncePerDevice set;
-    SG_CUDA(allow_smem(set, k_norm_fwd_ring<T, V, NT>, kRingSize<V, NT, 1>));
-    SG_CUDA(launch_pdl(k_norm_fwd_ring<T, V, NT>, dim3(grid_of(a.n_cap, kRingBlocks<NT, 1>)), dim3(NT), kRingSize<V, NT, 1>, s, a));
+    SG_CUDA(allow_smem(set, k_norm_fwd_ring<T, V, L, NT>, kRingSize<T, V, 1, NT>));
+    SG_CUDA(launch_pdl(k_norm_fwd_ring<T, V, L, NT>, dim3(grid_of(cdiv(a.n_cap, NT / L), kRingBlocks<V * kE<T>, 1, NT>)), dim3(NT),
+                       kRingSize<T, V, 1, NT>, s, a));
     return SG_OK;
 }
-template <typename T, int V, int NT>
+template <typename T, int V, int NT, int L = NT>
 sg_status go_ring(const BwdArgs<T>& a, cudaStream_t s, int64_t* count, int32_t* heads) {
+    static_assert(L == NT || NT / L * kGroupColumns<T, V, L> * 4 <= kRingSize<T, V, 2, NT>, "room for the groups' sums");
     static OncePerDevice set;
-    SG_CUDA(allow_smem(set, k_norm_bwd_ring<T, V, NT>, kRingSize<V, NT, 2>));
-    const unsigned blocks = grid_of(a, a.n_cap, kRingBlocks<NT, 2>);
+    SG_CUDA(allow_smem(set, k_norm_bwd_ring<T, V, L, NT>, kRingSize<T, V, 2, NT>));
+    const unsigned blocks = grid_of(a, cdiv(a.n_cap, NT / L), kRingBlocks<V * kE<T>, 2, NT>);
     *count = blocks;
-    *heads = 1;
-    SG_CUDA(launch_pdl(k_norm_bwd_ring<T, V, NT>, dim3(blocks), dim3(NT), kRingSize<V, NT, 2>, s, a));
+    *heads = L == NT;
+    SG_CUDA(launch_pdl(k_norm_bwd_ring<T, V, L, NT>, dim3(blocks), dim3(NT), kRingSize<T, V, 2, NT>, s, a));
     return SG_OK;
 }
 
@@ -681,8 +702,24 @@ sg_status by_size(const A& a, More... more) {
     if (vecs <= 8) return go<T, 1, 8, kThreads, 1>(a, more...);
     if (vecs <= 16) return go<T, 1, 16, kThreads, 2>(a, more...);
     if (vecs <= 32) return go<T, 1, 32, kThreads, 2>(a, more...);
-    if (vecs <= 64) return go<T, 2, 32, kThreads, 1>(a, more...);
-    if (!a.alike) return go<T, V, 1024, 1024, 1>(a, more...);
+    if (!a.alike) {
+        if (vecs <= 64) return go<T, 2, 32, kThreads, 1>(a, more...);
+        return go<T, V, 1024, 1024, 1>(a, more...);
+    }
+    if constexpr (std::is_same_v<A, FwdArgs<T>>) {
+        if (vecs <= 64) return go_ring<T, 2, kThreads, 32>(a, more...);
+        if (a.n_cap >= 16 * num_sms()) {
+            if (vecs <= 48 * V) return go_ring<T, 3 * V / 2, kThreads, 32>(a, more...);
+            if (vecs <= 64 * V) return go_ring<T, 2 * V, kThreads, 32>(a, more...);
+        }
+    } else {
+        const bool many = a.n_cap >= 16 * num_sms();
+        if (vecs <= 64 && !many) return go<T, 2, 32, kThreads, 1>(a, more...);
+        if (vecs <= 64) return go_ring<T, 2, kThreads, 32>(a, more...);
+        if (vecs <= 32 * V && many) return go_ring<T, V, kThreads, 32>(a, more...);
+        if constexpr (V == 4)
+            if (vecs > 48 * V && vecs <= 64 * V) return go_ring<T, 2, 128>(a, more...);
+    }
     if (vecs <= 64 * V) return go_ring<T, V, 64>(a, more...);
     if (vecs <= 128 * V) return go_ring<T, V, 128>(a, more...);
     if (vecs <= 256 * V) return go_ring<T, V, 256>(a, more...);
