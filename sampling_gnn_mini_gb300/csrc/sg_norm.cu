@@ -31,9 +31,10 @@ constexpr int kHeld = 16;      // values of a row a thread holds
 constexpr int kThreads = 256;  // of a block of groups' rows
 
 // -------------------------------------------------------- sums over a group
-// Sums of C values over the L threads that share a row, in every one of them.
-// L > 32: the whole block; sh holds two sets of warps' sums, used in turn (a set is
-// written again after the barrier of the other one, which follows its last reading).
+// Sums of C values over the L threads that share a row, in every one of them.  L > 32: a
+// block of L threads, 0: a block of any size; sh holds two sets of warps' sums, used in turn (a set is written
+// again after the barrier of the other one, which follows its last reading).
+constexpr int kSums = 2 * 2 * 32;  // of sh
 template <int L, int C>
 __device__ __forceinline__ void lane_sum(float (&x)[C]) {
 #pragma unroll
@@ -43,21 +44,33 @@ __device__ __forceinline__ void lane_sum(float (&x)[C]) {
 }
 template <int L, int C>
 __device__ __forceinline__ void group_sum(float (&x)[C], float* sh, int& turn) {
-    if constexpr (L <= 32) {
+    if constexpr (L > 0 && L <= 32) {
         lane_sum<L, C>(x);
     } else {
-        constexpr int W = L / 32;
         lane_sum<32, C>(x);
-        float* to = sh + turn * 2 * W;
+        float* to = sh + turn * 2 * 32;
         turn ^= 1;
         if (lane_id() == 0)
 #pragma unroll
-            for (int c = 0; c < C; ++c) to[c * W + (threadIdx.x >> 5)] = x[c];
+            for (int c = 0; c < C; ++c) to[c * 32 + (threadIdx.x >> 5)] = x[c];
         __syncthreads();
+        if constexpr (L > 0) {
+            constexpr int W = L / 32;
 #pragma unroll
-        for (int c = 0; c < C; ++c) x[c] = to[c * W + (int)lane_id() % W];
-        lane_sum<W, C>(x);
+            for (int c = 0; c < C; ++c) x[c] = to[c * 32 + (int)lane_id() % W];
+            lane_sum<W, C>(x);
+        } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c) x[c] = lane_id() < blockDim.x / 32 ? to[c * 32 + lane_id()] : 0.f;
+            lane_sum<32, C>(x);
+        }
     }
+}
+
+// This thread's group in its block.
+template <int L>
+__device__ __forceinline__ int group_of() {
+    return L ? (int)threadIdx.x / (L ? L : 1) : 0;
 }
 
 // ------------------------------------------------- a thread's part of a row
@@ -76,28 +89,29 @@ __device__ __forceinline__ void pop_front(uint4& v, __nv_bfloat16& x) {
     v = make_uint4(__funnelshift_r(v.x, v.y, 16), __funnelshift_r(v.y, v.z, 16), __funnelshift_r(v.z, v.w, 16), v.w >> 16);
 }
 
-// What thread l of a group of L holds of each of its rows: vectors l, l + L, .. (V of
-// them at most) and ends l, l + L, .. (of 16: 8 lanes for the head, 8 for the tail).
+// What thread l of a group of L (0: the block) holds of each of its rows: vectors l, l +
+// L, .. (V of them at most) and ends l, l + L, .. (of 16: 8 for the head, 8 for the tail).
 // alike: every array's rows start at the same place within 16 bytes; if not, all
 // vectors are moved by values and the ends are the tail's.
 template <typename T, int V, int L>
 struct Part {
     static constexpr int P = kE<T> / 2;                // pairs of a vector
-    static constexpr int NE = L >= 16 ? 1 : 16 / L;    // ends of a thread
+    static constexpr int NE = L == 0 || L >= 16 ? 1 : 16 / L;  // ends of a thread
     int32_t head, vecs, l;
     int32_t ends[NE];  // columns, or -1
     bool alike;
     // rows of x from r on, 8 apart
     __device__ __forceinline__ Part(const T* x, int64_t ld, int64_t r, int32_t dim, bool alike_)
-        : l((int)threadIdx.x % L), alike(alike_) {
+        : l(L ? (int)threadIdx.x % (L ? L : 1) : (int)threadIdx.x), alike(alike_) {
         const RowParts<T> part(alike ? x + r * ld : (const T*)nullptr, dim);
         head = part.head;
         vecs = part.vecs;
 #pragma unroll
         for (int e = 0; e < NE; ++e) ends[e] = l + e * L < 16 ? part.edge(l + e * L) : -1;
     }
-    __device__ __forceinline__ bool has(int v) const { return l + v * L < vecs; }
-    __device__ __forceinline__ int32_t column(int v) const { return head + (l + v * L) * kE<T>; }
+    __device__ __forceinline__ int stride() const { return L ? L : (int)blockDim.x; }
+    __device__ __forceinline__ bool has(int v) const { return l + v * stride() < vecs; }
+    __device__ __forceinline__ int32_t column(int v) const { return head + (l + v * stride()) * kE<T>; }
     __device__ __forceinline__ uint4 load(const T* row, int v) const {
         uint4 u = make_uint4(0, 0, 0, 0);
         if (!has(v)) return u;
@@ -107,7 +121,8 @@ struct Part {
         for (int i = kE<T> - 1; i >= 0; --i) push_front(u, p[i]);
         return u;
     }
-    __device__ __forceinline__ float load_end(const T* row, int e) const { return ends[e] >= 0 ? to_f(row[ends[e]]) : 0.f; }
+    // (as it is: its conversion would wait for the load)
+    __device__ __forceinline__ T load_end(const T* row, int e) const { return ends[e] >= 0 ? row[ends[e]] : T(0.f); }
     __device__ __forceinline__ void store(T* row, int v, const f2 (&f)[P]) const {
         if (!has(v)) return;
         T* p = row + column(v);
@@ -173,7 +188,7 @@ struct FwdArgs {
 template <typename T, int V, int L, typename Get>
 __device__ __forceinline__ void norm_row(const FwdArgs<T>& a, const Part<T, V, L>& p, const Param<T, V, L>& w,
                                          const Param<T, V, L>& b, int64_t r, int32_t n, float inv, float* sh, int& turn,
-                                         const float (&ends)[Part<T, V, L>::NE], Get get) {
+                                         const T (&ends)[Part<T, V, L>::NE], Get get) {
     constexpr int P = kE<T> / 2, NE = Part<T, V, L>::NE;
     f2 f[V][P], t = both(0.f);
     float fe[NE], s[1] = {0.f};
@@ -184,7 +199,7 @@ __device__ __forceinline__ void norm_row(const FwdArgs<T>& a, const Part<T, V, L
         for (int i = 0; i < P; ++i) t = add2(t, f[v][i]);
     }
 #pragma unroll
-    for (int e = 0; e < NE; ++e) s[0] += fe[e] = ends[e];
+    for (int e = 0; e < NE; ++e) s[0] += fe[e] = to_f(ends[e]);
     s[0] += total_of(t);
     group_sum<L, 1>(s, sh, turn);
     const float mu = s[0] * inv;
@@ -229,28 +244,28 @@ __device__ __forceinline__ void norm_row(const FwdArgs<T>& a, const Part<T, V, L
 template <typename T, int V, int L, int NT, int R>
 __global__ void __launch_bounds__(NT, NT == kThreads ? 4 : 1) k_norm_fwd(FwdArgs<T> a) {
     pdl_start();
-    constexpr int kRows = L <= 32 ? NT / L : 1;  // of a block at once
+    constexpr int kRows = L ? NT / (L ? L : 1) : 1;  // of a block at once
     constexpr int NE = Part<T, V, L>::NE;
-    __shared__ float sh[L > 32 ? 4 * (L / 32) : 1];
+    __shared__ float sh[L == 0 || L > 32 ? kSums : 1];
     int turn = 0;
     const int32_t n = rows_of(a.d_n, a.n_cap);
     const int64_t step = (int64_t)gridDim.x * (kRows * R);
     int64_t b0 = (int64_t)blockIdx.x * (kRows * R);
     if (b0 >= n) return;
-    const Part<T, V, L> p(a.x, a.ld, b0 + (int)threadIdx.x / L, a.dim, a.alike != 0);
+    const Part<T, V, L> p(a.x, a.ld, b0 + group_of<L>(), a.dim, a.alike != 0);
     const Param<T, V, L> w(p, a.weight, a.w_bf16, 1.f), b(p, a.bias, a.w_bf16, 0.f);
     struct Rows {
         uint4 x[R][V];
-        float ends[R][NE];
+        T ends[R][NE];
     } next;
     const auto load = [&](int64_t b1, Rows& o) {
 #pragma unroll
         for (int q = 0; q < R; ++q) {
-            const int64_t r = b1 + q * kRows + (int)threadIdx.x / L;
+            const int64_t r = b1 + q * kRows + group_of<L>();
 #pragma unroll
             for (int v = 0; v < V; ++v) o.x[q][v] = r < n ? p.load(a.x + r * a.ld, v) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int e = 0; e < NE; ++e) o.ends[q][e] = r < n ? p.load_end(a.x + r * a.ld, e) : 0.f;
+            for (int e = 0; e < NE; ++e) o.ends[q][e] = r < n ? p.load_end(a.x + r * a.ld, e) : T(0.f);
         }
     };
     const float inv = 1.f / (float)a.dim;
@@ -260,7 +275,7 @@ __global__ void __launch_bounds__(NT, NT == kThreads ? 4 : 1) k_norm_fwd(FwdArgs
         load(b0 + step, next);
 #pragma unroll
         for (int q = 0; q < R; ++q)
-            norm_row<T, V, L>(a, p, w, b, b0 + q * kRows + (int)threadIdx.x / L, n, inv, sh, turn, cur.ends[q],
+            norm_row<T, V, L>(a, p, w, b, b0 + q * kRows + group_of<L>(), n, inv, sh, turn, cur.ends[q],
                               [&](int v) { return cur.x[q][v]; });
     }
 }
@@ -346,7 +361,7 @@ __device__ __forceinline__ void join_groups(const Sums<T, V, L>& sums, const Par
     const int32_t pitch = SMALL ? W : pitch_of(a.dim);
     for (int k = 0; k < 2; ++k) {
         __syncthreads();
-        sums.template put<false>(p, k != 0, cols + ((int)threadIdx.x / L) * W);
+        sums.template put<false>(p, k != 0, cols + (group_of<L>()) * W);
         __syncthreads();
         for (int c = threadIdx.x; c < a.dim; c += NT) {
             float s = 0.f;
@@ -376,9 +391,12 @@ __device__ __forceinline__ void join_groups(const Sums<T, V, L>& sums, const Par
 template <typename T, int V, int L, typename GetX, typename GetG, typename Between>
 __device__ __forceinline__ void grad_row(const BwdArgs<T>& a, const Part<T, V, L>& p, const Param<T, V, L>& w,
                                          Sums<T, V, L>& sums, int64_t r, int32_t n, float inv, float* sh, int& turn,
-                                         float mean, float rstd, const float (&xe)[Part<T, V, L>::NE],
-                                         const float (&ge)[Part<T, V, L>::NE], GetX x, GetG g, Between between) {
+                                         float mean, float rstd, const T (&x_ends)[Part<T, V, L>::NE],
+                                         const T (&g_ends)[Part<T, V, L>::NE], GetX x, GetG g, Between between) {
     constexpr int P = kE<T> / 2, NE = Part<T, V, L>::NE;
+    float xe[NE], ge[NE];
+#pragma unroll
+    for (int e = 0; e < NE; ++e) xe[e] = to_f(x_ends[e]), ge[e] = to_f(g_ends[e]);
     const f2 mu = both(-mean), rs = both(rstd);
     f2 t0 = both(0.f), t1 = both(0.f);
 #pragma unroll
@@ -437,26 +455,26 @@ constexpr int kBwdBlocks = NT == kThreads ? (sizeof(T) == 2 ? 2 : 3) : 1;
 template <typename T, int V, int L, int NT, int R, bool SMALL>
 __global__ void __launch_bounds__(NT, kBwdBlocks<T, NT>) k_norm_bwd(BwdArgs<T> a) {
     pdl_start();
-    constexpr int kRows = L <= 32 ? NT / L : 1;
+    constexpr int kRows = L ? NT / (L ? L : 1) : 1;
     constexpr int NE = Part<T, V, L>::NE;
-    __shared__ float sh[L > 32 ? 4 * (L / 32) : 1];
-    __shared__ float cols[L > 32 ? 1 : NT / L * kGroupColumns<T, V, L>];
+    __shared__ float sh[L == 0 || L > 32 ? kSums : 1];
+    __shared__ float cols[L ? kRows * kGroupColumns<T, V, L> : 1];
     int turn = 0;
     const int32_t n = rows_of(a.d_n, a.n_cap);
     const int64_t step = (int64_t)gridDim.x * (kRows * R);
     int64_t b0 = (int64_t)blockIdx.x * (kRows * R);
-    const Part<T, V, L> p(a.x, a.ld, b0 + (int)threadIdx.x / L, a.dim, a.alike != 0);
+    const Part<T, V, L> p(a.x, a.ld, b0 + group_of<L>(), a.dim, a.alike != 0);
     const Param<T, V, L> w(p, a.weight, a.w_bf16, 1.f);
     Sums<T, V, L> sums;
     struct Rows {
         uint4 x[R][V], g[R][V];
-        float xe[R][NE], ge[R][NE];
+        T xe[R][NE], ge[R][NE];
         float mu[R], rs[R];
     } next;
     const auto load = [&](int64_t b1, Rows& o) {
 #pragma unroll
         for (int q = 0; q < R; ++q) {
-            const int64_t r = b1 + q * kRows + (int)threadIdx.x / L;
+            const int64_t r = b1 + q * kRows + group_of<L>();
             o.mu[q] = r < n ? __ldg(a.mean + r) : 0.f;
             o.rs[q] = r < n ? __ldg(a.rstd + r) : 0.f;
 #pragma unroll
@@ -466,8 +484,8 @@ __global__ void __launch_bounds__(NT, kBwdBlocks<T, NT>) k_norm_bwd(BwdArgs<T> a
             }
 #pragma unroll
             for (int e = 0; e < NE; ++e) {
-                o.xe[q][e] = r < n ? p.load_end(a.x + r * a.ld, e) : 0.f;
-                o.ge[q][e] = r < n ? p.load_end(a.g + r * a.ld_g, e) : 0.f;
+                o.xe[q][e] = r < n ? p.load_end(a.x + r * a.ld, e) : T(0.f);
+                o.ge[q][e] = r < n ? p.load_end(a.g + r * a.ld_g, e) : T(0.f);
             }
         }
     };
@@ -479,7 +497,7 @@ __global__ void __launch_bounds__(NT, kBwdBlocks<T, NT>) k_norm_bwd(BwdArgs<T> a
 #pragma unroll
         for (int q = 0; q < R; ++q)
             grad_row<T, V, L>(
-                a, p, w, sums, b0 + q * kRows + (int)threadIdx.x / L, n, inv, sh, turn, cur.mu[q], cur.rs[q], cur.xe[q], cur.ge[q],
+                a, p, w, sums, b0 + q * kRows + group_of<L>(), n, inv, sh, turn, cur.mu[q], cur.rs[q], cur.xe[q], cur.ge[q],
                 [&](int v) { return cur.x[q][v]; }, [&](int v) { return cur.g[q][v]; },
                 [&] {
 #pragma unroll
@@ -489,7 +507,7 @@ __global__ void __launch_bounds__(NT, kBwdBlocks<T, NT>) k_norm_bwd(BwdArgs<T> a
                     }
                 });
     }
-    if constexpr (L > 32) {
+    if constexpr (L == 0 || L > 32) {
         sums.put_block(p, a);
     } else {
         join_groups<T, V, L, NT, SMALL>(sums, p, a, cols);
@@ -500,34 +518,36 @@ __global__ void __launch_bounds__(NT, kBwdBlocks<T, NT>) k_norm_bwd(BwdArgs<T> a
 // Each thread copies its own vectors of the block's next rows into a ring of slots in
 // shared memory, asynchronously, and waits for its own copies alone; the ends are
 // loaded a row ahead.
+// A group is a warp (L = 32, blocks of NT = 256 threads) or the block: of L threads, or (L
+// = 0) of as many, up to NT, as the row needs.  The constant size is worth its
+// instances: 19,531 x 4096 bf16 forward SPEED_FIXED us, of any size 64.
 constexpr int kRingBytes = 208 * 1024;  // of an SM
-// Threads an SM, by the registers for HELD values of a row a thread.  A: arrays that are
-// read (1 forward, 2 backward).  Backward, 16 values a thread: 512 of 128 registers 80
-// us for 16,384 x 4096 bf16, 768 of 80 105, 1,024 of 64 140.
-template <int HELD, int A>
-constexpr int kRingThreads = A == 1 ? (HELD <= 16 ? 768 : 512) : (HELD <= 8 ? 768 : 512);
+// Threads an SM, by the registers for HELD values of a row a thread (NT = 1024: 64).  A:
+// arrays that are read (1 forward, 2 backward).  Backward, 16 values a thread: 512 of
+// 128 registers 80 us for 16,384 x 4096 bf16, 768 of 80 105, 1,024 of 64 140.
 template <int HELD, int A, int NT>
-constexpr int kRingBlocks = kRingThreads<HELD, A> / NT > 0 ? kRingThreads<HELD, A> / NT : 1;
+constexpr int kRingThreads = NT == 1024 ? 1024 : A == 1 && HELD <= 16 ? 768 : 512;
 // Slots: as many as there is room for, four at most.
 template <typename T, int V, int A, int NT>
-constexpr int kRoom = kRingBytes / kRingBlocks<V * kE<T>, A, NT> / (NT * V * A * 16);
+constexpr int kRoom = kRingBytes / (kRingThreads<V * kE<T>, A, NT> * V * A * 16);
 template <typename T, int V, int A, int NT>
-constexpr int kDepth = kRoom<T, V, A, NT> > 4 ? 4 : kRoom<T, V, A, NT>;
-template <typename T, int V, int A, int NT>
-constexpr int kRingSize = kDepth<T, V, A, NT> * NT * V * A * 16;
+constexpr int kDepth = kRoom<T, V, A, NT> > 4 ? 4 : kRoom<T, V, A, NT> > 0 ? kRoom<T, V, A, NT> : 1;
+// Threads of the longest rows' blocks: 16 values each.
+template <int A>
+constexpr int kBlockThreads = A == 1 ? 384 : 512;  // two blocks or one an SM; above: 1024
 
 template <typename T, int V, int L, int NT>
-__global__ void __launch_bounds__(NT, kRingBlocks<V * kE<T>, 1, NT>) k_norm_fwd_ring(FwdArgs<T> a) {
+__global__ void __launch_bounds__(NT, kRingThreads<V * kE<T>, 1, NT> / NT) k_norm_fwd_ring(FwdArgs<T> a) {
     extern __shared__ __align__(128) uint4 ring[];
     pdl_start();
-    constexpr int D = kDepth<T, V, 1, NT>, kRows = NT / L;  // kRows: of a block at once
-    __shared__ float sh[L > 32 ? 4 * (L / 32) : 1];
+    constexpr int D = kDepth<T, V, 1, NT>, kRows = L == 32 ? NT / 32 : 1;  // kRows: of a block at once
+    __shared__ float sh[L == 0 || L > 32 ? kSums : 1];
     int turn = 0;
-    const int32_t n = rows_of(a.d_n, a.n_cap), first = (int32_t)blockIdx.x * kRows + (int)threadIdx.x / L;
+    const int32_t n = rows_of(a.d_n, a.n_cap), first = (int32_t)blockIdx.x * kRows + group_of<L>();
     const int32_t step = (int32_t)gridDim.x * kRows;
     if (first >= n) return;  // whole groups
     const Part<T, V, L> p(a.x, a.ld, first, a.dim, true);
-    const auto slot = [&](int at, int v) { return ring + (at * V + v) * NT + (int)threadIdx.x; };
+    const auto slot = [&](int at, int v) { return ring + (at * V + v) * (L > 32 ? L : (int)blockDim.x) + (int)threadIdx.x; };
     const auto fetch = [&](int64_t r, int at) {
         if (r < n) {
 #pragma unroll
@@ -541,10 +561,10 @@ __global__ void __launch_bounds__(NT, kRingBlocks<V * kE<T>, 1, NT>) k_norm_fwd_
     const Param<T, V, L> w(p, a.weight, a.w_bf16, 1.f), b(p, a.bias, a.w_bf16, 0.f);
     const float inv = 1.f / (float)a.dim;
     int at = 0;
-    float next = p.load_end(a.x + first * a.ld, 0);
+    T next = p.load_end(a.x + first * a.ld, 0);
     for (int64_t r = first; r < n; r += step) {
         fetch(r + (int64_t)(D - 1) * step, at ? at - 1 : D - 1);
-        const float end[1] = {next};
+        const T end[1] = {next};
         if (r + step < n) next = p.load_end(a.x + (r + step) * a.ld, 0);
         copies_wait<D - 1>();
         norm_row<T, V, L>(a, p, w, b, r, n, inv, sh, turn, end,
@@ -554,16 +574,16 @@ __global__ void __launch_bounds__(NT, kRingBlocks<V * kE<T>, 1, NT>) k_norm_fwd_
 }
 
 template <typename T, int V, int L, int NT>
-__global__ void __launch_bounds__(NT, kRingBlocks<V * kE<T>, 2, NT>) k_norm_bwd_ring(BwdArgs<T> a) {
+__global__ void __launch_bounds__(NT, kRingThreads<V * kE<T>, 2, NT> / NT) k_norm_bwd_ring(BwdArgs<T> a) {
     extern __shared__ __align__(128) uint4 ring[];
     pdl_start();
-    constexpr int D = kDepth<T, V, 2, NT>, kRows = NT / L;
-    __shared__ float sh[L > 32 ? 4 * (L / 32) : 1];
+    constexpr int D = kDepth<T, V, 2, NT>, kRows = L == 32 ? NT / 32 : 1;
+    __shared__ float sh[L == 0 || L > 32 ? kSums : 1];
     int turn = 0;
-    const int32_t n = rows_of(a.d_n, a.n_cap), first = (int32_t)blockIdx.x * kRows + (int)threadIdx.x / L;
+    const int32_t n = rows_of(a.d_n, a.n_cap), first = (int32_t)blockIdx.x * kRows + group_of<L>();
     const int32_t step = (int32_t)gridDim.x * kRows;
     const Part<T, V, L> p(a.x, a.ld, first, a.dim, true);
-    const auto slot = [&](int at, int v) { return ring + (at * 2 * V + v) * NT + (int)threadIdx.x; };  // (g: v + V)
+    const auto slot = [&](int at, int v) { return ring + (at * 2 * V + v) * (L > 32 ? L : (int)blockDim.x) + (int)threadIdx.x; };  // (g: v + V)
     const auto fetch = [&](int64_t r, int at) {
         if (r < n) {
 #pragma unroll
@@ -582,7 +602,8 @@ __global__ void __launch_bounds__(NT, kRingBlocks<V * kE<T>, 2, NT>) k_norm_bwd_
     const float inv = 1.f / (float)a.dim;
     int at = 0;
     struct Next {
-        float mu, rs, xe, ge;
+        float mu, rs;
+        T xe, ge;
     } next = {};
     const auto load = [&](int64_t r) {
         if (r < n) next = {__ldg(a.mean + r), __ldg(a.rstd + r), p.load_end(a.x + r * a.ld, 0), p.load_end(a.g + r * a.ld_g, 0)};
@@ -593,14 +614,14 @@ __global__ void __launch_bounds__(NT, kRingBlocks<V * kE<T>, 2, NT>) k_norm_bwd_
         const Next cur = next;
         load(r + step);
         copies_wait<D - 1>();
-        const float xe[1] = {cur.xe}, ge[1] = {cur.ge};
+        const T xe[1] = {cur.xe}, ge[1] = {cur.ge};
         grad_row<T, V, L>(
             a, p, w, sums, r, n, inv, sh, turn, cur.mu, cur.rs, xe, ge,
             [&](int v) { return p.has(v) ? *slot(at, v) : make_uint4(0, 0, 0, 0); },
             [&](int v) { return p.has(v) ? *slot(at, v + V) : make_uint4(0, 0, 0, 0); }, [] {});
         if (++at == D) at = 0;
     }
-    if constexpr (L == NT) sums.put_block(p, a);
+    if constexpr (L == 0 || L > 32) sums.put_block(p, a);
     else join_groups<T, V, L, NT, false>(sums, p, a, reinterpret_cast<float*>(ring));  // (its copies are all used)
 }
 
@@ -653,15 +674,15 @@ unsigned grid_of(const BwdArgs<T>& a, int64_t rows, int per_sm) {
 
 template <typename T, int V, int L, int NT, int R>
 sg_status go(const FwdArgs<T>& a, cudaStream_t s) {
-    const unsigned blocks = grid_of(cdiv(a.n_cap, (L <= 32 ? NT / L : 1) * R), NT == kThreads ? 4 : 1);
+    const unsigned blocks = grid_of(cdiv(a.n_cap, (L ? NT / (L ? L : 1) : 1) * R), NT == kThreads ? 4 : 1);
     SG_CUDA(launch_pdl(k_norm_fwd<T, V, L, NT, R>, dim3(blocks), dim3(NT), 0, s, a));
     return SG_OK;
 }
 template <typename T, int V, int L, int NT, int R>
 sg_status go(const BwdArgs<T>& a, cudaStream_t s, int64_t* count, int32_t* heads) {
-    constexpr int kRows = (L <= 32 ? NT / L : 1) * R;
+    constexpr int kRows = (L ? NT / (L ? L : 1) : 1) * R;
     *heads = 0;  // (by columns, or rows that are moved value by value)
-    if constexpr (L <= 32)
+    if constexpr (L > 0)
         if (a.n_cap <= kSmallTurns * kSmallCtas * kRows && a.parts) {
             *count = 0;  // the sums are done
             SG_CUDA(launch_cluster(k_norm_bwd<T, V, L, NT, R, true>, kSmallCtas, NT, kSmallCtas, s, 0, a));
@@ -673,23 +694,35 @@ sg_status go(const BwdArgs<T>& a, cudaStream_t s, int64_t* count, int32_t* heads
     return SG_OK;
 }
 
-template <typename T, int V, int NT, int L = NT>
+// Threads and shared memory of a ring's block, and blocks an SM.
+struct Ring {
+    int threads, bytes, per_sm;
+};
+template <typename T, int V, int L, int NT, int A>
+Ring ring_of(int32_t dim) {
+    const int vecs = dim / kE<T>, t = L == 32 ? NT : L ? L : (int)cdiv(vecs, 32 * V) * 32;  // (vectors at most)
+    return {t, t * kDepth<T, V, A, NT> * V * A * 16, kRingThreads<V * kE<T>, A, NT> / t};
+}
+template <typename T, int V, int L, int NT>
 sg_status go_ring(const FwdArgs<T>& a, cudaStream_t s) {
+    const Ring r = ring_of<T, V, L, NT, 1>(a.dim);
     static OncePerDevice set;
-    SG_CUDA(allow_smem(set, k_norm_fwd_ring<T, V, L, NT>, kRingSize<T, V, 1, NT>));
-    SG_CUDA(launch_pdl(k_norm_fwd_ring<T, V, L, NT>, dim3(grid_of(cdiv(a.n_cap, NT / L), kRingBlocks<V * kE<T>, 1, NT>)), dim3(NT),
-                       kRingSize<T, V, 1, NT>, s, a));
+    SG_CUDA(allow_smem(set, k_norm_fwd_ring<T, V, L, NT>, NT * kDepth<T, V, 1, NT> * V * 16));
+    SG_CUDA(launch_pdl(k_norm_fwd_ring<T, V, L, NT>, dim3(grid_of(cdiv(a.n_cap, L == 32 ? NT / 32 : 1), r.per_sm)),
+                       dim3(r.threads), r.bytes, s, a));
     return SG_OK;
 }
-template <typename T, int V, int NT, int L = NT>
+template <typename T, int V, int L, int NT>
 sg_status go_ring(const BwdArgs<T>& a, cudaStream_t s, int64_t* count, int32_t* heads) {
-    static_assert(L == NT || NT / L * kGroupColumns<T, V, L> * 4 <= kRingSize<T, V, 2, NT>, "room for the groups' sums");
+    const Ring r = ring_of<T, V, L, NT, 2>(a.dim);
+    constexpr int kBytes = NT * kDepth<T, V, 2, NT> * V * 2 * 16;
+    static_assert(L != 32 || NT / 32 * kGroupColumns<T, V, L> * 4 <= kBytes, "room for the groups' sums");
     static OncePerDevice set;
-    SG_CUDA(allow_smem(set, k_norm_bwd_ring<T, V, L, NT>, kRingSize<T, V, 2, NT>));
-    const unsigned blocks = grid_of(a, cdiv(a.n_cap, NT / L), kRingBlocks<V * kE<T>, 2, NT>);
+    SG_CUDA(allow_smem(set, k_norm_bwd_ring<T, V, L, NT>, kBytes));
+    const unsigned blocks = grid_of(a, cdiv(a.n_cap, L == 32 ? NT / 32 : 1), r.per_sm);
     *count = blocks;
-    *heads = L == NT;
-    SG_CUDA(launch_pdl(k_norm_bwd_ring<T, V, L, NT>, dim3(blocks), dim3(NT), kRingSize<T, V, 2, NT>, s, a));
+    *heads = L != 32;
+    SG_CUDA(launch_pdl(k_norm_bwd_ring<T, V, L, NT>, dim3(blocks), dim3(r.threads), r.bytes, s, a));
     return SG_OK;
 }
 
@@ -704,27 +737,29 @@ sg_status by_size(const A& a, More... more) {
     if (vecs <= 32) return go<T, 1, 32, kThreads, 2>(a, more...);
     if (!a.alike) {
         if (vecs <= 64) return go<T, 2, 32, kThreads, 1>(a, more...);
-        return go<T, V, 1024, 1024, 1>(a, more...);
+        return go<T, V, 0, 1024, 1>(a, more...);
     }
+    // a warp a row while there are rows for all warps: no barrier, and the ring
+    const bool many = a.n_cap >= 16 * num_sms();
     if constexpr (std::is_same_v<A, FwdArgs<T>>) {
-        if (vecs <= 64) return go_ring<T, 2, kThreads, 32>(a, more...);
-        if (a.n_cap >= 16 * num_sms()) {
-            if (vecs <= 48 * V) return go_ring<T, 3 * V / 2, kThreads, 32>(a, more...);
-            if (vecs <= 64 * V) return go_ring<T, 2 * V, kThreads, 32>(a, more...);
-        }
+        if (vecs <= 64) return go_ring<T, 2, 32, kThreads>(a, more...);
+        if (vecs <= 48 * V && many) return go_ring<T, 3 * V / 2, 32, kThreads>(a, more...);
+        if (vecs <= 64 * V && many) return go_ring<T, 2 * V, 32, kThreads>(a, more...);
+        if (vecs <= 64 * V && vecs > 48 * V) return go_ring<T, V, 64, kBlockThreads<1>>(a, more...);
+        if (vecs <= 128 * V && vecs > 96 * V) return go_ring<T, V, 128, kBlockThreads<1>>(a, more...);
+        if (vecs <= 256 * V && vecs > 192 * V) return go_ring<T, V, 256, kBlockThreads<1>>(a, more...);
+        if (vecs <= kBlockThreads<1> * V) return go_ring<T, V, 0, kBlockThreads<1>>(a, more...);
     } else {
-        const bool many = a.n_cap >= 16 * num_sms();
         if (vecs <= 64 && !many) return go<T, 2, 32, kThreads, 1>(a, more...);
-        if (vecs <= 64) return go_ring<T, 2, kThreads, 32>(a, more...);
-        if (vecs <= 32 * V && many) return go_ring<T, V, kThreads, 32>(a, more...);
-        if constexpr (V == 4)
-            if (vecs > 48 * V && vecs <= 64 * V) return go_ring<T, 2, 128>(a, more...);
+        if (vecs <= 64) return go_ring<T, 2, 32, kThreads>(a, more...);
+        if (vecs <= 32 * V && many) return go_ring<T, V, 32, kThreads>(a, more...);
+        if (vecs <= 64 * V && vecs > 48 * V) return go_ring<T, V, 64, kBlockThreads<2>>(a, more...);
+        if (vecs <= 128 * V && vecs > 96 * V) return go_ring<T, V, 128, kBlockThreads<2>>(a, more...);
+        if (vecs <= 256 * V && vecs > 192 * V) return go_ring<T, V, 256, kBlockThreads<2>>(a, more...);
+        if (vecs <= 512 * V && vecs > 384 * V) return go_ring<T, V, 512, kBlockThreads<2>>(a, more...);
+        if (vecs <= kBlockThreads<2> * V) return go_ring<T, V, 0, kBlockThreads<2>>(a, more...);
     }
-    if (vecs <= 64 * V) return go_ring<T, V, 64>(a, more...);
-    if (vecs <= 128 * V) return go_ring<T, V, 128>(a, more...);
-    if (vecs <= 256 * V) return go_ring<T, V, 256>(a, more...);
-    if (vecs <= 512 * V) return go_ring<T, V, 512>(a, more...);
-    return go_ring<T, V, 1024>(a, more...);
+    return go_ring<T, V, 0, 1024>(a, more...);
 }
 
 bool known(int32_t dtype) { return dtype == SG_F32 || dtype == SG_BF16; }
