@@ -612,10 +612,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprobs_row(Args<T> a, int32
     };
     const auto fetch = [&](int at) {
         if (fr < n) {
+            const bool whole = (ft + 1) * kTurn * NT <= fcount + (int32_t)threadIdx.x;  // the same in the whole block
 #pragma unroll
             for (int k = 0; k < kTurn; ++k) {
                 const int32_t i = (ft * kTurn + k) * NT;
-                if (i < fcount) copy_async(ring + (at * kTurn + k) * NT + threadIdx.x, from + i * kE<T>);
+                if (whole || i < fcount) copy_async(ring + (at * kTurn + k) * NT + threadIdx.x, from + i * kE<T>);
             }
             if (++ft * kTurn * NT >= fcount + (int32_t)threadIdx.x) {  // the same in the whole block
                 fr += step;
@@ -648,10 +649,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprobs_row(Args<T> a, int32
                 fetch(at ? at - 1 : kRing - 1);
                 copies_wait<kRing - 1>();
                 uint4 u[kTurn];
+                if (i0 + kTurn * NT <= sl.count) {  // a whole turn
 #pragma unroll
-                for (int k = 0; k < kTurn; ++k) {
-                    const int32_t i = i0 + k * NT + (int32_t)threadIdx.x;
-                    u[k] = i < sl.count ? ring[(at * kTurn + k) * NT + threadIdx.x] : empty_part<T>();
+                    for (int k = 0; k < kTurn; ++k) u[k] = ring[(at * kTurn + k) * NT + threadIdx.x];
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kTurn; ++k)
+                        u[k] = i0 + k * NT + (int32_t)threadIdx.x < sl.count ? ring[(at * kTurn + k) * NT + threadIdx.x] : empty_part<T>();
                 }
                 if (++at == kRing) at = 0;
                 const float top = parts_max<T>(u);

@@ -526,7 +526,7 @@ constexpr int kRingBytes = 208 * 1024;  // of an SM
 // arrays that are read (1 forward, 2 backward).  Backward, 16 values a thread: 512 of
 // 128 registers 80 us for 16,384 x 4096 bf16, 768 of 80 105, 1,024 of 64 140.
 template <int HELD, int A, int NT>
-constexpr int kRingThreads = NT == 1024 ? 1024 : A == 1 && HELD <= 16 ? 768 : 512;
+constexpr int kRingThreads = NT == 1024 ? 1024 : A == 1 && HELD <= 16 ? 768 : A == 1 || HELD <= 16 ? 512 : 384;
 // Slots: as many as there is room for, four at most.
 template <typename T, int V, int A, int NT>
 constexpr int kRoom = kRingBytes / (kRingThreads<V * kE<T>, A, NT> * V * A * 16);
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(NT, kRingThreads<V * kE<T>, 1, NT> / NT) k_nor
     for (int64_t r = first; r < n; r += step) {
         fetch(r + (int64_t)(D - 1) * step, at ? at - 1 : D - 1);
         const T end[1] = {next};
-        if (r + step < n) next = p.load_end(a.x + (r + step) * a.ld, 0);
+        if (r + step < n && p.ends[0] >= 0) next = a.x[(r + step) * a.ld + p.ends[0]];
         copies_wait<D - 1>();
         norm_row<T, V, L>(a, p, w, b, r, n, inv, sh, turn, end,
                           [&](int v) { return p.has(v) ? *slot(at, v) : make_uint4(0, 0, 0, 0); });
@@ -757,6 +757,8 @@ sg_status by_size(const A& a, More... more) {
         if (vecs <= 128 * V && vecs > 96 * V) return go_ring<T, V, 128, kBlockThreads<2>>(a, more...);
         if (vecs <= 256 * V && vecs > 192 * V) return go_ring<T, V, 256, kBlockThreads<2>>(a, more...);
         if (vecs <= 512 * V && vecs > 384 * V) return go_ring<T, V, 512, kBlockThreads<2>>(a, more...);
+        // (24 values a thread leave room for two blocks: 9,746 x 4104 fp32 140 -> 95 us)
+        if (vecs <= 288 * V && vecs > 256 * V) return go_ring<T, 3 * V / 2, 0, 192>(a, more...);
         if (vecs <= kBlockThreads<2> * V) return go_ring<T, V, 0, kBlockThreads<2>>(a, more...);
     }
     return go_ring<T, V, 0, 1024>(a, more...);
