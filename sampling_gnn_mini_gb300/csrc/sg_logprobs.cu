@@ -3,20 +3,23 @@
 // d_c = m - x[c], z = sum_c exp(-d_c), t = sum_c exp(-d_c) (-d_c):
 //   logp = -d_label - log z,  entropy = log z - t / z,
 //   the k largest by (x descending, class ascending) with their log probabilities.
-// Bound by memory: the logits are read once and next to nothing is written.
+// The logits are read once and next to nothing is written; beside the bytes an
+// exponential a logit counts (16 a cycle and SM: at 2 bytes a logit three quarters of the
+// copy rate's time).
 //
-// Many rows of up to 64 classes go through shared memory to a thread each
-// (k_logprobs_few), rows of a few hundred stay in a warp's registers
-// (k_logprobs_warp).  Longer ones stream past 256 threads, or a cluster of 2 to 8 such
-// CTAs when rows are few (k_logprobs_row): each thread copies its own vectors
-// asynchronously, those of the next row already while this row's classes are chosen.
-// A thread keeps (m, z, t) of what it has seen, relative to its own running maximum,
-// and the maximum of each group of vectors.  The k-th largest of some of the threads'
-// maxima is a lower bound of the k-th largest logit, so only groups that reach it are
-// read again (from L2), and only the logits that reach it become candidates: about k
-// of them, whatever the row's length.  Where they are many all the same (equal
-// logits, masks by one value), the bound is raised by bisection, and logits equal to it
-// are taken in order.
+// Many rows of up to 128 classes go through shared memory to a thread each
+// (k_logprobs_few).  Rows of up to 2,048 vectors of 16 bytes stay in the registers of 1,
+// 2 or 4 warps (k_logprobs_warp).  Longer ones stream past 128 or 256 threads, or a
+// cluster of 2 to 8 such CTAs when rows are few (k_logprobs_row): each thread copies its
+// own vectors asynchronously, those of the next row already while this row's classes are
+// chosen, and keeps (m, z, t) of what it has seen, relative to its own running maximum.
+//
+// The k best are chosen through a bound: the k-th largest of some maxima (of lanes,
+// threads or groups of vectors) is a lower bound of the k-th largest logit, so only
+// vectors that reach it are read again (from L2), and only the logits that reach it
+// become candidates: about k of them, whatever the row's length.  Where they are more
+// than the list holds (equal logits, masks by one value), the bound is raised by bisection
+// over the row, and logits equal to it are taken in order.
 //
 // Logits of -inf take no part.  x - m is formed before the scaling by log2(e), so
 // a row's level costs no accuracy, and exponents are cut off at -200, where the
@@ -137,6 +140,20 @@ __device__ __forceinline__ void put_row(const Args<T>& a, int32_t r, const Stat&
     if (a.entropy) a.entropy[r] = s.z == 0.f ? 0.f : log_z - s.t / s.z * 0.69314718055994531f;
 }
 
+// Descending over the warp's lanes.
+__device__ __forceinline__ float warp_sort(float x) {
+    const int lane = (int)lane_id();
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+        for (int d = size / 2; d > 0; d /= 2) {
+            const float o = __shfl_xor_sync(0xFFFFFFFFu, x, d);
+            const bool larger = ((lane & d) == 0) == ((lane & size) == 0);  // this lane keeps the larger one
+            x = larger ? fmaxf(x, o) : fminf(x, o);
+        }
+    return x;
+}
+
 // The largest element of several vectors (bf16: pairwise on the packed elements).
 template <typename T, int N>
 __device__ __forceinline__ float parts_max(const uint4 (&u)[N]) {
@@ -173,8 +190,9 @@ __device__ __forceinline__ void unpack(const uint4& u, float (&f)[kE<T>]) {
 //              of 16 bytes);
 //   by values  if neither, at an odd pitch (up to kFewByValues classes: the index
 //              arithmetic costs more than a warp a row from there on).
-// us, 100,000 rows of fp32, k = 5, this / a warp a row: 47 classes 12 / 60, 101 21 / 61,
-// 128 30 / 60 (k = 8: 44 / 61).
+// us, fp32, this / a warp a row: 200,000 x 47 k = 1 9.6 / 80, k = 3 14 / 102, k = 8 29 /
+// 115; 100,000 x 128 k = 1 15 / 42, k = 5 30 / 54, k = 8 44 / 56; 25,000 x 128 k = 1 7.3 /
+// 11, k = 8 17 / 15.  What is left is the insertion: two instructions a class and place.
 constexpr int kFewRows = 128, kFewClasses = 128, kFewByValues = 64, kFewTop = 8;
 enum Few { kWhole, kByVectors, kByValues };
 
@@ -288,41 +306,37 @@ __global__ void __launch_bounds__(kFewRows) k_logprobs_few(Args<T> a, int32_t pi
         }
 }
 
-// ------------------------------------------------------------ rows by warps
-// The logits of a lane as orders: 0 once taken.
-template <typename T, int NV>
-struct LaneOrders {
-    static constexpr int E = NV * kE<T>;
-    uint32_t o[E], edge;
-    int32_t first, edge_class;  // class of o[0]; element e's is first + (e / kE) 32 kE + e % kE
-    __device__ __forceinline__ int32_t class_at(int e) const { return first + e / kE<T> * 32 * kE<T> + e % kE<T>; }
-};
-// The k best one by one, each the best of what the lanes offer, into ids and lps.
-template <typename T, int NV>
-__device__ __forceinline__ void take_in_turn(LaneOrders<T, NV>& l, int32_t k, float m, float log_z, int32_t* ids, float* lps) {
-    constexpr int E = LaneOrders<T, NV>::E;
-    const int lane = (int)lane_id();
-    for (int32_t j = 0; j < k; ++j) {
-        uint32_t best = l.edge;
+// -------------------------------------------------------------- rows by warps
+// A candidate as a number (the larger one is the better): the value's order, then the
+// class from the last one on.  bf16 values have 16 bits, rows of warps fewer than 2^16
+// classes.
+template <typename T>
+using Key = std::conditional_t<sizeof(T) == 2, uint32_t, unsigned long long>;
+template <typename T>
+__device__ __forceinline__ Key<T> key_of(float x, int32_t c) {
+    if constexpr (sizeof(T) == 2) return (order_of(x) & 0xFFFF0000u) | (0xFFFFu - (uint32_t)c);
+    else return entry_of(order_of(x), c);
+}
+__device__ __forceinline__ int32_t key_class(uint32_t e) { return (int32_t)(0xFFFFu - (e & 0xFFFFu)); }
+__device__ __forceinline__ int32_t key_class(unsigned long long e) { return class_of(e); }
+// (a negative value's order has ones below its 16 bits)
+__device__ __forceinline__ float key_value(uint32_t e) { return value_of(e & 0x80000000u ? e & 0xFFFF0000u : e | 0xFFFFu); }
+__device__ __forceinline__ float key_value(unsigned long long e) { return value_of((uint32_t)(e >> 32)); }
+
+// The maxima of a lane's vectors' parts of PER elements, G in all, as orders.
+template <typename T, int PER, int NV, int G>
+__device__ __forceinline__ void group_orders(const uint4 (&x)[NV], uint32_t (&g)[G]) {
+    constexpr int EACH = kE<T> / PER;
 #pragma unroll
-        for (int e = 0; e < E; ++e) best = max(best, l.o[e]);
-        best = __reduce_max_sync(0xFFFFFFFFu, best);
-        if (best <= kOrderNone) {  // nothing is left
-            for (int32_t i = j + lane; i < k; i += 32) ids[i] = -1, lps[i] = -INFINITY;
-            return;
-        }
-        uint32_t c = l.edge == best ? (uint32_t)l.edge_class : 0xFFFFFFFFu;
+    for (int k = 0; k < NV; ++k) {
+        float f[kE<T>];
+        unpack<T>(x[k], f);
 #pragma unroll
-        for (int e = E - 1; e >= 0; --e)
-            if (l.o[e] == best) c = min(c, (uint32_t)l.class_at(e));
-        c = __reduce_min_sync(0xFFFFFFFFu, c);
-        if (l.edge == best && l.edge_class == (int32_t)c) l.edge = 0;
+        for (int i = 0; i < EACH; ++i) {
+            float m = f[i * PER];
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (l.o[e] == best && l.class_at(e) == (int32_t)c) l.o[e] = 0;
-        if (lane == 0) {
-            ids[j] = (int32_t)c;
-            lps[j] = logp_of(value_of(best), m, log_z);
+            for (int e = 1; e < PER; ++e) m = fmaxf(m, f[i * PER + e]);
+            g[k * EACH + i] = order_of(m);
         }
     }
 }
@@ -333,11 +347,17 @@ __device__ __forceinline__ uint32_t bound_of(const uint32_t (&g)[G], int32_t k, 
     const auto reach = [&](uint32_t o) {
         int32_t c = 0;
 #pragma unroll
-        for (int i = 0; i < G; ++i) c += __popc(__ballot_sync(0xFFFFFFFFu, g[i] >= o));
-        return c;
+        for (int i = 0; i < G; ++i) c += g[i] >= o;
+        return __reduce_add_sync(0xFFFFFFFFu, c);
     };
-    uint32_t lo = kOrderNone + 1, hi = top + 1;
-    if (reach(lo) < k) return lo;
+    uint32_t lo = g[0], hi = top + 1;
+#pragma unroll
+    for (int i = 1; i < G; ++i) lo = min(lo, g[i]);
+    lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+    if (lo <= kOrderNone) {
+        lo = kOrderNone + 1;
+        if (reach(lo) < k) return lo;
+    }
     while (hi - lo > 1) {
         const uint32_t mid = lo + (hi - lo) / 2;
         const int32_t c = reach(mid);
@@ -351,39 +371,134 @@ __device__ __forceinline__ uint32_t bound_of(const uint32_t (&g)[G], int32_t k, 
     return lo;
 }
 
-// A warp a row, in NV vectors a lane.  Up to kInTurn top classes are taken one by one;
-// for more, the logits that reach a bound are listed and ranked.
-constexpr int kInTurn = 4;
+// The k best of a row of which more than kWarpCap logits have order o and above, as
+// keys in `list`, which they fit; returns their number.  top: an order that none is
+// above.  Each pass reads the row again.
+template <typename T>
+__device__ __noinline__ int32_t select_by_warp(const T* row, int32_t classes, int32_t k, uint32_t o, uint32_t top, Key<T>* list) {
+    const int lane = (int)lane_id();
+    const uint32_t below = (1u << lane) - 1u;
+    const auto order_at = [&](int32_t c) { return c < classes ? order_of(to_f(row[c])) : 0u; };
+    const auto count = [&](uint32_t from) {
+        int32_t c = 0;
+#pragma unroll 4
+        for (int32_t i = lane; i < classes; i += 32) c += order_at(i) >= from;
+        return __reduce_add_sync(0xFFFFFFFFu, c);
+    };
+    uint32_t lo = o, hi = top + 1;  // at least k from lo on, fewer from hi on
+    int32_t have = kWarpCap + 1;
+    for (uint32_t mid = lo + 1; have > kWarpCap && hi - lo > 1; mid = lo + (hi - lo) / 2) {
+        const int32_t c = count(mid);
+        if (c >= k) lo = mid, have = c;
+        else hi = mid;
+    }
+    // all from lo on or, of those that are equal to lo, the lowest classes
+    const bool all = have <= kWarpCap;
+    int32_t found = 0;
+    for (int pass = 0; pass < (all ? 1 : 2); ++pass)
+        for (int32_t c0 = 0; c0 < classes && (pass == 0 || found < k); c0 += 32) {
+            const uint32_t at = order_at(c0 + lane);
+            const bool take = all ? at >= lo : pass == 0 ? at > lo : at == lo;
+            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, take);
+            const int32_t to = found + __popc(mask & below);
+            if (take && to < (pass ? k : kWarpCap)) list[to] = key_of<T>(value_of(at), c0 + lane);
+            found += __popc(mask);
+        }
+    __syncwarp();
+    return all ? found : min(found, k);
+}
 
-template <typename T, int NV>
-__global__ void __launch_bounds__(kThreads) k_logprobs_warp(Args<T> a) {
+// A warp's list in order, P keys a lane (bitonic; key lane P + i in e[i]), its first k
+// written.
+template <typename T, int P>
+__device__ __forceinline__ void put_sorted(const Key<T>* list, int32_t found, int32_t k, float m, float log_z, int32_t* ids,
+                                           float* lps) {
+    const int lane = (int)lane_id();
+    Key<T> e[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) e[i] = lane * P + i < found ? list[lane * P + i] : 0;
+#pragma unroll
+    for (int size = 2; size <= 32 * P; size *= 2)
+#pragma unroll
+        for (int d = size / 2; d > 0; d /= 2) {
+            if (d >= P) {
+                const bool larger = ((lane & d / P) == 0) == ((lane * P & size) == 0);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const Key<T> o = __shfl_xor_sync(0xFFFFFFFFu, e[i], d / P);
+                    e[i] = larger == (o > e[i]) ? o : e[i];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+                    if ((i & d) == 0) {
+                        const bool down = ((lane * P + i) & size) == 0;
+                        const Key<T> x = e[i], y = e[i + d];
+                        e[i] = down == (x > y) ? x : y;
+                        e[i + d] = down == (x > y) ? y : x;
+                    }
+            }
+        }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const int32_t j = lane * P + i;
+        if (j < min(found, k)) {
+            ids[j] = key_class(e[i]);
+            lps[j] = logp_of(key_value(e[i]), m, log_z);
+        }
+    }
+}
+
+// W warps a row, in NV vectors a lane.  The bound of the k best: each warp's k-th of
+// its lanes' maxima is one, and the lowest of the warps' ceil(k / W)-th is one, by a
+// sort for up to kBySort, else by bisection over a warp's 256 or 512 groups' maxima.
+// The vectors that reach the better one are read again, a lane each, and their logits
+// that do are listed and put in order.  us, 40,000 x 2000 bf16: 33 without top classes, 43
+// for 1, 49 for 5, 58 for 20, 126 for 100 (taken one by one from orders of all logits in
+// registers, at half the warps an SM: 69, 119, 174, 210, 429).  By bisection 20 take
+// 72, by a sort 32 take 122 (78): too many logits reach the lowest of 32 maxima.
+constexpr int kBySort = 24;
+template <int W>
+constexpr int kWarpThreads = W == 1 ? kThreads : 32 * W;  // of a block: 8 rows or one
+
+template <typename T, int NV, int W>
+__global__ void __launch_bounds__(kWarpThreads<W>, (NV <= 2 ? 48 : NV == 4 ? 40 : NV == 8 ? 32 : NV == 12 ? 28 : 24) * 32 / kWarpThreads<W>)
+    k_logprobs_warp(Args<T> a) {
     pdl_start();
-    constexpr int E = NV * kE<T>;
-    __shared__ unsigned long long lists[kWarps][kWarpCap];
-    __shared__ int32_t counts[kWarps];
-    const int lane = (int)lane_id(), warp = (int)(threadIdx.x >> 5);
-    const int32_t n = rows_of(a.d_n, a.n_cap), r = (int32_t)blockIdx.x * kWarps + warp;
-    if (r >= n) return;
+    constexpr int kRows = kWarpThreads<W> / 32 / W;
+    __shared__ Key<T> lists[kRows][kWarpCap];
+    __shared__ uint16_t hit_lists[kRows * W][32 * NV];
+    __shared__ float4 parts[W];
+    __shared__ float2 bounds[W];
+    __shared__ int32_t counts[kRows];
+    const int lane = (int)lane_id(), warp = (int)(threadIdx.x >> 5), rank = W == 1 ? 0 : warp;
+    const int32_t n = rows_of(a.d_n, a.n_cap), r = (int32_t)blockIdx.x * kRows + warp / W;
+    if (r >= n) return;  // all of the row's warps
     const T* row = a.x + (int64_t)r * a.ld;
     const RowParts<T> part(row, a.classes);
+    const int32_t first = rank * 32 + lane;  // vector of x[0], the others 32 W apart
     uint4 x[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int32_t v = lane + 32 * k;
+        const int32_t v = first + 32 * W * k;
         x[k] = v < part.vecs ? *reinterpret_cast<const uint4*>(row + part.head + v * kE<T>) : empty_part<T>();
     }
-    const int32_t ce = part.edge(lane);
+    const int32_t ce = rank == 0 ? part.edge(lane) : -1;
     const float xe = ce >= 0 ? to_f(row[ce]) : -INFINITY;
     int32_t y = -1;
     float xy = 0.f;
-    if (lane == 0) {
+    if (rank == 0 && lane == 0) {
+        counts[warp / W] = 0;
         y = label_of(a, r);
         if (y >= 0) xy = to_f(row[y]);
     }
     Stat s = stat_of(xe);
-    float top = xe;
+    float vm[NV], top = xe;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) top = fmaxf(top, part_max<T>(x[k]));
+    for (int k = 0; k < NV; ++k) {
+        vm[k] = part_max<T>(x[k]);
+        top = fmaxf(top, vm[k]);
+    }
     rebase(s, warp_max(top));
     f2 z = pair(s.z, 0.f), t = pair(s.t, 0.f);
     const float b = -finite_base(s.m);
@@ -394,68 +509,137 @@ __global__ void __launch_bounds__(kThreads) k_logprobs_warp(Args<T> a) {
     unpair(t, t0, t1);
     s.z = warp_sum(z0 + z1);
     s.t = warp_sum(t0 + t1);
+    const int32_t need = (a.k + W - 1) / W;
+    float tau = s.m;
+    const auto bisect = [&] {
+        constexpr int PER = NV > 8 ? kE<T> : kE<T> * NV >= 8 ? kE<T> * NV / 8 : 1;
+        uint32_t g[kE<T> * NV / PER];
+        if constexpr (PER == kE<T>) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) g[k] = order_of(vm[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) repack(x[k]);
+            group_orders<T, PER>(x, g);
+        }
+        g[0] = max(g[0], order_of(xe));
+        tau = value_of(bound_of(g, need, order_of(s.m)));
+    };
+    if constexpr (W > 1) {
+        float other = -INFINITY;  // the other bound
+        if (a.k > 1) {
+            const float in_order = warp_sort(top);
+            if (a.k <= 32) other = __shfl_sync(0xFFFFFFFFu, in_order, a.k - 1);
+            if (need <= kBySort) tau = __shfl_sync(0xFFFFFFFFu, in_order, need - 1);
+            else bisect();
+        } else {
+            other = s.m;
+        }
+        if (lane == 0) {
+            parts[rank] = make_float4(s.m, s.z, s.t, 0.f);
+            bounds[rank] = make_float2(tau, other);
+        }
+        __syncthreads();
+        s = {-INFINITY, 0.f, 0.f};
+        tau = INFINITY, other = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const float4 p = parts[i];
+            Stat o = {p.x, p.y, p.z};
+            const float m = fmaxf(s.m, o.m);
+            rebase(s, m);
+            rebase(o, m);
+            s.z += o.z;
+            s.t += o.t;
+            tau = fminf(tau, bounds[i].x);
+            other = fmaxf(other, bounds[i].y);
+        }
+        tau = fmaxf(tau, other);
+    }
     const float log_z = logf(s.z);
-    if (lane == 0) put_row(a, r, s, log_z, y, xy);
+    if (rank == 0 && lane == 0) put_row(a, r, s, log_z, y, xy);
     if (a.k == 0) return;
     int32_t* ids = a.top_ids + (int64_t)r * a.k;
     float* lps = a.top_logp + (int64_t)r * a.k;
     if (s.z != s.z) {
-        for (int32_t i = lane; i < a.k; i += 32) ids[i] = -1, lps[i] = s.z;
+        if (rank == 0)
+            for (int32_t i = lane; i < a.k; i += 32) ids[i] = -1, lps[i] = s.z;
         return;
     }
-    LaneOrders<T, NV> l;
-    l.first = part.head + lane * kE<T>;
-    l.edge = order_of(xe);
-    l.edge_class = ce;
+    if (W == 1 && a.k > 1) {
+        if (a.k > kBySort) bisect();
+        else tau = __shfl_sync(0xFFFFFFFFu, warp_sort(top), a.k - 1);
+    }
+    tau = fmaxf(tau, -3.402823466e38f);  // (-inf takes no part)
+    uint16_t* hits = hit_lists[warp];
+    Key<T>* list = lists[warp / W];
+    int32_t hit = 0, found = 0;  // found: of this warp, W = 1
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        float f[kE<T>];
-        unpack<T>(x[k], f);
-#pragma unroll
-        for (int e = 0; e < kE<T>; ++e) l.o[k * kE<T> + e] = order_of(f[e]);
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, vm[k] >= tau);
+        if (vm[k] >= tau) hits[hit + __popc(mask & ((1u << lane) - 1u))] = (uint16_t)(first + 32 * W * k);
+        hit += __popc(mask);
     }
-    if (a.k <= kInTurn) {
-        take_in_turn(l, a.k, s.m, log_z, ids, lps);
-        return;
-    }
-    // groups: the lanes for few classes, up to 8 a lane for more
-    constexpr int G = E < 8 ? E : 8;
-    uint32_t g[G], all = l.edge;
-#pragma unroll
-    for (int i = 0; i < G; ++i) {
-        g[i] = i == 0 ? l.edge : 0u;
-#pragma unroll
-        for (int e = 0; e < E / G; ++e) g[i] = max(g[i], l.o[i * (E / G) + e]);
-        all = max(all, g[i]);
-    }
-    const uint32_t one[1] = {all};
-    const uint32_t most = order_of(s.m);
-    const uint32_t tau = a.k <= 16 ? bound_of<1>(one, a.k, most) : bound_of<G>(g, a.k, most);
-    if (lane == 0) counts[warp] = 0;
-    __syncwarp();
-    unsigned long long* list = lists[warp];
-    const auto offer = [&](uint32_t o, int32_t c) {
-        if (o < tau) return;
-        const int32_t at = atomicAdd(&counts[warp], 1);
-        if (at < kWarpCap) list[at] = entry_of(o, c);
-    };
-    offer(l.edge, ce);
-#pragma unroll
-    for (int e = 0; e < E; ++e) offer(l.o[e], l.class_at(e));
-    __syncwarp();
-    const int32_t found = counts[warp];
-    if (found > kWarpCap) {  // equal logits by the hundred
-        take_in_turn(l, a.k, s.m, log_z, ids, lps);
-        return;
-    }
-    for (int32_t i = lane; i < found; i += 32) {
-        const unsigned long long e = list[i];
-        int32_t before = 0;
-        for (int32_t q = 0; q < found; ++q) before += list[q] > e;
-        if (before < a.k) {
-            ids[before] = class_of(e);
-            lps[before] = logp_of(value_of((uint32_t)(e >> 32)), s.m, log_z);
+    // room for this warp's keys, `mine` of them this lane's
+    const auto reserve = [&](int32_t mine) {
+        const int32_t upto = warp_incl_scan(mine), all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+        int32_t at = found;
+        if constexpr (W == 1) {
+            found += all;
+        } else {
+            if (lane == 0) at = atomicAdd(&counts[0], all);
+            at = __shfl_sync(0xFFFFFFFFu, at, 0);
         }
+        return at + upto - mine;
+    };
+    if (rank == 0 && part.head + part.tail > 0) {
+        const int32_t at = reserve(xe >= tau);
+        if (xe >= tau && at < kWarpCap) list[at] = key_of<T>(xe, ce);
+    }
+    __syncwarp();
+    for (int32_t q = 0; q < hit; q += 32) {
+        uint4 u = empty_part<T>();
+        int32_t c = 0;
+        if (q + lane < hit) {
+            c = part.head + hits[q + lane] * kE<T>;
+            u = *reinterpret_cast<const uint4*>(row + c);
+        }
+        float f[kE<T>];
+        unpack<T>(u, f);
+        int32_t mine = 0;
+#pragma unroll
+        for (int e = 0; e < kE<T>; ++e) mine += f[e] >= tau;
+        int32_t at = reserve(mine);
+#pragma unroll
+        for (int e = 0; e < kE<T>; ++e)
+            if (f[e] >= tau) {
+                if (at < kWarpCap) list[at] = key_of<T>(f[e], c + e);
+                ++at;
+            }
+    }
+    if constexpr (W == 1) {
+        __syncwarp();
+    } else {
+        __syncthreads();
+        if (rank != 0) return;
+        found = counts[0];
+    }
+    if (found > kWarpCap) found = select_by_warp<T>(row, a.classes, a.k, order_of(tau), order_of(s.m), list);
+    if (found <= 32) {  // by counting: a lane's key and the ones before it
+        const Key<T> e = lane < found ? list[lane] : 0;
+        int32_t before = 0;
+#pragma unroll 4
+        for (int32_t q = 0; q < found; ++q) before += list[q] > e;
+        if (lane < found && before < a.k) {
+            ids[before] = key_class(e);
+            lps[before] = logp_of(key_value(e), s.m, log_z);
+        }
+    } else if (found <= 64) {
+        put_sorted<T, 2>(list, found, a.k, s.m, log_z, ids, lps);
+    } else if (found <= 128) {
+        put_sorted<T, 4>(list, found, a.k, s.m, log_z, ids, lps);
+    } else {
+        put_sorted<T, 8>(list, found, a.k, s.m, log_z, ids, lps);
     }
     for (int32_t i = found + lane; i < a.k; i += 32) ids[i] = -1, lps[i] = -INFINITY;
 }
@@ -555,20 +739,6 @@ __device__ __noinline__ void select_exactly(const Slice<T>& s, int32_t rank, uin
         }
     if (threadIdx.x == 0) l.count = min(filled, k);
     __syncthreads();
-}
-
-// Descending over the warp's lanes.
-__device__ __forceinline__ float warp_sort(float x) {
-    const int lane = (int)lane_id();
-#pragma unroll
-    for (int size = 2; size <= 32; size *= 2)
-#pragma unroll
-        for (int d = size / 2; d > 0; d /= 2) {
-            const float o = __shfl_xor_sync(0xFFFFFFFFu, x, d);
-            const bool larger = ((lane & d) == 0) == ((lane & size) == 0);  // this lane keeps the larger one
-            x = larger ? fmaxf(x, o) : fminf(x, o);
-        }
-    return x;
 }
 
 constexpr int kRefine = 16;  // classes a warp from which the bound is refined
@@ -682,7 +852,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprobs_row(Args<T> a, int32
         // an uneven share of the warps does not lower the bound (M is a multiple of 4)
         const int32_t need = (a.k + W - 1) / W;
         int32_t j = min(need + (need + 1) / 2, kTops<W> / W);
-        if (W == 2) j += j & 1;
         const int32_t M = W * j;
         if (j == 1) most = s.m;
         else if (j > 1) most = warp_sort(most);
@@ -741,7 +910,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprobs_row(Args<T> a, int32
         const bool bad = s.z != s.z;
         if constexpr (S == 1) {
             // For many classes the threads' maxima are too few for a close bound: more
-            // groups' maxima, by bisection (16,000 x 5000 bf16, k = 100: SPEED_REFINE us)
+            // groups' maxima, by bisection (4096 x 50,257 bf16: k = 128 150 us, without
+            // it 650; k = 100 140, 200; k = 80 134, 129)
             if (a.k > kRefine * W && !bad && tau < s.m) {
                 uint32_t lo = order_of(tau), hi = order_of(s.m) + 1;
                 for (int i = 0; i < 24 && hi - lo > 1; ++i) {
@@ -834,9 +1004,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprobs_row(Args<T> a, int32
 }
 
 // -------------------------------------------------------------------- host
-template <typename T, int NV>
+template <typename T, int NV, int W = 1>
 sg_status run_warp(const Args<T>& a, cudaStream_t s) {
-    SG_CUDA(launch_pdl(k_logprobs_warp<T, NV>, dim3((unsigned)cdiv(a.n_cap, kWarps)), dim3(kThreads), 0, s, a));
+    const int64_t rows = kWarpThreads<W> / 32 / W;  // of a block
+    SG_CUDA(launch_pdl(k_logprobs_warp<T, NV, W>, dim3((unsigned)cdiv(a.n_cap, rows)), dim3(kWarpThreads<W>), 0, s, a));
     return SG_OK;
 }
 
@@ -904,14 +1075,26 @@ sg_status run(const Args<T>& a, cudaStream_t s) {
         }
     }
     const int64_t nv = cdiv((int64_t)a.classes, kE<T>);  // vectors of a row, at most
+    // In registers, as few as hold the row: 12 a lane where 16 would leave a quarter and
+    // more of them empty (us, k = 5: 25,000 x 3000 bf16 43, with 16 53), the fewest warps
+    // (20,000 x 4000 bf16 k = 20 by 1 x 16 52, by 2 x 8 55).  By CTAs of 64 threads from the
+    // ring 16,000 x 5000 bf16 k = 1, 20, 100 take 74, 102, 291 (45, 56, 114), by 128 threads
+    // 8000 x 10,000 k = 1, 20, 100 53, 63, 148 (42, 52, 96).  8 warps lose: 3000 x 30,000 k = 1
+    // 48, by the ring 43.
     if (nv <= 32) return run_warp<T, 1>(a, s);
     if (nv <= 64) return run_warp<T, 2>(a, s);
     if (nv <= 128) return run_warp<T, 4>(a, s);
     if (nv <= 256) return run_warp<T, 8>(a, s);
-    // small CTAs for rows of a few thousand classes: what every warp does for a row, and
-    // its barriers, cost less
-    if (a.n_cap >= 16 * num_sms() && nv <= 2048 && a.k <= 32) return run_row<T, 64, 1>(a, nv, s);
-    if (a.n_cap >= (nv <= 4096 ? 8 : 16) * num_sms()) return run_row<T, 128, 1>(a, nv, s);
+    if (nv <= 384) return run_warp<T, 12>(a, s);
+    if (nv <= 512) return run_warp<T, 16>(a, s);
+    if (nv <= 768) return run_warp<T, 12, 2>(a, s);
+    if (nv <= 1024) return run_warp<T, 16, 2>(a, s);
+    if (nv <= 1536) return run_warp<T, 12, 4>(a, s);
+    if (nv <= 2048) return run_warp<T, 16, 4>(a, s);
+    // half the threads a CTA from two rows an SM on: what every warp does for a row, and
+    // its barriers, cost less (4096 x 50,257 bf16 k = 64: 112 us, by 256 threads 122; 800 x
+    // 20,000 k = 20 13, 17; 400 x 30,000 fp32 the same; 220 x 150,000 bf16 24, 20)
+    if (a.n_cap >= 2 * num_sms()) return run_row<T, 128, 1>(a, nv, s);
     // clusters while the rows leave SMs idle and every CTA has a turn to do
     int split = 1;
     while (split < 8 && (int64_t)a.n_cap * split * 2 <= 2 * num_sms() && nv >= split * 2 * kThreads) split *= 2;

@@ -158,6 +158,22 @@ def test_many_rows_of_some_thousand_classes(n, c, k, mask, dt):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("vecs", [31, 32, 33, 64, 65, 128, 129, 256, 257, 384, 385, 512, 513, 768, 769, 1024, 1025, 1536, 1537,
+                                  2048, 2049])
+@pytest.mark.parametrize("start", [0, 3])
+def test_rows_at_the_ends_of_the_forms(vecs, start, dt):
+    # 1, 2 or 4 warps a row, as many vectors a lane as hold it; longer rows by blocks
+    n, c = 21, vecs * (4 if dt == "f32" else 8)
+    x = _logits(n, start + c + 1, dt, vecs)[:, start:start + c]
+    x[3, 2:], x[4], x[5, : c // 2] = -INF, -INF, -INF
+    x[6, c // 3:] = -7.0
+    x[7, 1::2] = torch.finfo(DT[dt]).min
+    y = _labels(n, c, c)
+    for k in (1, 2, 24, 25, 32, 48, 49, 96, 97, 128):
+        _hold(x, y, _run(x, y, k), k)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("n,c,k", [(40, 100, 5), (40, 600, 20), (20, 3000, 64), (700, 5000, 20), (6, 40001, 64),
                                    (400, 20003, 100)])
 @pytest.mark.parametrize("kept", [0, 1, 3, 50, "many"])
