@@ -38,7 +38,7 @@ struct Args {
     const int32_t* d_n;
     int32_t n_cap, classes, k;
     int32_t mean;
-    float gs, temp, l;  // l = log2(e) / temp
+    float gs, temp, inv_temp, l;  // l = log2(e) / temp
     float* loss;
     float* total;
     int32_t* done;   // rows or blocks that are done; then `counts` counts of rows with a teacher
@@ -139,7 +139,7 @@ __device__ __forceinline__ Scale scale_entries(const Args<T>& a, Entries& n) {
 template <typename T>
 __device__ __forceinline__ float loss_of(const Args<T>& a, const Scale& c, const Entries& n, float M, float Z) {
     const int lane = (int)lane_id();
-    const float log_z = logf(Z), inv = 1.f / a.temp;
+    const float log_z = logf(Z), inv = a.inv_temp;
     float s = 0.f;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
@@ -176,18 +176,26 @@ __device__ __forceinline__ void load_entries(const Args<T>& a, int32_t r, int32_
         for (int q = 0; q < R; ++q) to[q].id[lane + 32 * e] = id[q], to[q].v[lane + 32 * e] = v[q], to[q].x[lane + 32 * e] = x[q];
     }
 }
-// One warp: whether a class occurs more than once; the table is clear.
+// One warp: whether a class occurs more than once.
 template <typename T>
 __device__ __forceinline__ bool any_twice(const Args<T>& a, const Entries& n, Table& table) {
+    const int lane = (int)lane_id();
+    if (a.k <= 32) {
+        const int32_t id = n.id[lane];
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);  // (by every lane)
+        return __any_sync(0xFFFFFFFFu, id >= 0 && __popc(same) > 1);
+    }
+    table.clear(lane, 32);
+    __syncwarp();
     bool twice = false;
-    for (int32_t j = (int32_t)lane_id(); j < a.k; j += 32)
+    for (int32_t j = lane; j < a.k; j += 32)
         if (n.id[j] >= 0) twice |= table.insert(n.id[j]);
     return __any_sync(0xFFFFFFFFu, twice);
 }
 // The gradient at entry j's class; false where there is none.  twice: classes may occur
-// more than once
+// more than once; w_z: w / Z
 template <typename T>
-__device__ __forceinline__ bool entry_grad(const Args<T>& a, const Entries& n, int32_t j, bool twice, float w, float M,
+__device__ __forceinline__ bool entry_grad(const Args<T>& a, const Entries& n, int32_t j, bool twice, float w, float w_z, float M,
                                            float Z, float& g) {
     const int32_t id = n.id[j];
     if (id < 0) return false;
@@ -197,7 +205,7 @@ __device__ __forceinline__ bool entry_grad(const Args<T>& a, const Entries& n, i
         for (int32_t i = 0; i < a.k; ++i)
             if (n.id[i] == id) q += n.q[i];
     }
-    g = Z == 0.f ? 0.f : fmaf(w / Z, exp_from(n.x[j], M, a.l), -w * q);
+    g = Z == 0.f ? 0.f : fmaf(w_z, exp_from(n.x[j], M, a.l), -w * q);
     return true;
 }
 
@@ -274,19 +282,21 @@ __device__ __forceinline__ float finish_row(const Args<T>& a, int32_t r, float w
     }
     const int32_t ce = part.edge(lane);
     if (ce >= 0) put(out + ce, inv * base.of(d.xe));
-    table.clear(lane, 32);
     __syncwarp();  // the entries are there, the vectors stored
     const bool twice = any_twice(a, mine, table);
     for (int32_t j = lane; j < a.k; j += 32) {
         float g;
-        if (entry_grad(a, mine, j, twice, w, m, z, g)) put(out + mine.id[j], g);
+        if (entry_grad(a, mine, j, twice, w, inv, m, z, g)) put(out + mine.id[j], g);
     }
     __syncwarp();  // before the next row's entries
     return loss;
 }
 
+template <int NV>
+constexpr int kWarpBlocks = NV <= 2 ? 5 : NV == 4 ? 4 : NV == 8 ? 3 : 2;  // an SM
+
 template <typename T, int NV>
-__global__ void __launch_bounds__(kThreads, 3) k_distill_warp(Args<T> a) {
+__global__ void __launch_bounds__(kThreads, kWarpBlocks<NV>) k_distill_warp(Args<T> a) {
     pdl_start();
     constexpr int kWarps = kThreads / 32;
     __shared__ Entries entries[kWarps];
@@ -326,7 +336,7 @@ constexpr int kSmallBytes = kSmallThreads / 32 * kSmallRows<NV> * (int)sizeof(En
 
 template <typename T, int NV>
 __global__ void __launch_bounds__(kSmallThreads) k_distill_small(Args<T> a) {
-    extern __shared__ __align__(16) uint8_t dsm[];
+    extern __shared__ __align__(128) uint8_t dsm[];
     pdl_start();
     constexpr int kWarps = kSmallThreads / 32, R = kSmallRows<NV>;
     __shared__ Table tables[kWarps];
@@ -377,7 +387,7 @@ __device__ __forceinline__ void put_entries(const Args<T>& a, const Entries& n, 
     const int32_t at = part.place(n.id[j]);
     if (at < 0 ? rank != 0 : at < v0 || at >= v0 + count) return;
     float g;
-    if (entry_grad(a, n, j, twice, w, M, Z, g)) put(out + n.id[j], g);
+    if (entry_grad(a, n, j, twice, w, w / Z, M, Z, g)) put(out + n.id[j], g);
 }
 
 template <typename T, int NT, int S>
@@ -386,7 +396,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_row(Args<T> a) {
     constexpr int kParts = S * NT / 32;
     __shared__ __align__(8) float2 parts[kParts];  // (m, z) of every warp of the cluster
     __shared__ Entries entries;
-    __shared__ bool last;
+    __shared__ Table table;
+    __shared__ bool last, twice;
     const int32_t r = (int32_t)(blockIdx.x / S), rank = (int32_t)(blockIdx.x % S);
     const int32_t n = rows_of(a.d_n, a.n_cap), classes = a.classes;
     if (r >= n) return;  // the whole cluster
@@ -410,7 +421,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_row(Args<T> a) {
             h.x[k] = (int32_t)threadIdx.x + k * NT < count ? *reinterpret_cast<const uint4*>(p + k * NT * kE<T>)
                                                            : empty_part<T>();
         h.xe = edge >= 0 ? to_f(row[edge]) : -INFINITY;
-        if (mine) scale = scale_entries(a, entries);
+        if (mine) {
+            scale = scale_entries(a, entries);
+            __syncwarp();
+            const bool t = out && any_twice(a, entries, table);
+            if (threadIdx.x == 0) twice = t;
+        }
         float mr = -INFINITY, zr = 0.f;  // the part past the registers
         for (int32_t i = (int32_t)threadIdx.x + kVecs * NT; i < count; i += NT) {
             const T* q = row + part.head + (v0 + i) * kE<T>;
@@ -446,7 +462,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_row(Args<T> a) {
             if (threadIdx.x == 0) a.loss[r] = loss;
         }
         __syncthreads();  // the vectors are stored
-        if (out) put_entries(a, entries, out, part, v0, count, rank, (int32_t)threadIdx.x, true, w, M, Z);
+        if (out) put_entries(a, entries, out, part, v0, count, rank, (int32_t)threadIdx.x, twice, w, M, Z);
     } else {
         if (rank == 0 && threadIdx.x == 0) a.loss[r] = 0.f;
         if (out) zero_row<T, NT>(out, classes, rank, S);
@@ -620,7 +636,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_stream(Args<T> a, int
                 Scale scale = {0.f, 0.f};
                 bool twice = false;
                 if (mine) {
-                    tables[e].clear(lane, 32);
                     scale = scale_entries(a, entry);
                     __syncwarp();
                     twice = any_twice(a, entry, tables[e]);
@@ -698,14 +713,14 @@ __global__ void __launch_bounds__(kCountThreads) k_distill_count(const int32_t* 
 // -------------------------------------------------------------------- host
 template <typename T, int NV>
 sg_status run_warp(const Args<T>& a, bool small, cudaStream_t s) {
-    if (small) {
+    if constexpr (NV <= 8) if (small) {
         static OncePerDevice set;
         SG_CUDA(allow_smem(set, k_distill_small<T, NV>, kSmallBytes<NV>));
         SG_CUDA(launch_cluster(k_distill_small<T, NV>, kSmallCtas, kSmallThreads, kSmallCtas, s, kSmallBytes<NV>, a));
         return SG_OK;
     }
     int64_t blocks = cdiv(a.n_cap, kThreads / 32);
-    if (blocks > (int64_t)num_sms() * 3) blocks = (int64_t)num_sms() * 3;
+    if (blocks > (int64_t)num_sms() * kWarpBlocks<NV>) blocks = (int64_t)num_sms() * kWarpBlocks<NV>;
     SG_CUDA(launch_pdl(k_distill_warp<T, NV>, dim3((unsigned)blocks), dim3(kThreads), 0, s, a));
     return SG_OK;
 }
@@ -746,6 +761,10 @@ sg_status run(Args<T> a, cudaStream_t s) {
     if (nv <= 64) return run_warp<T, 2>(a, small, s);
     if (nv <= 128) return run_warp<T, 4>(a, small, s);
     if (nv <= 256) return run_warp<T, 8>(a, small, s);
+    if (a.n_cap >= 4 * num_sms()) {
+        if (nv <= 384) return run_warp<T, 12>(a, false, s);
+        if (nv <= 512) return run_warp<T, 16>(a, false, s);
+    }
     const int wide = nv <= kVecThreads<kThreads> * kVecs ? 1 : nv <= kStreamVecs ? 2 : nv <= 2 * kStreamVecs ? 4 : nv <= 4 * kStreamVecs ? 8 : 16;
     if (nv <= 8 * kStreamVecs && (int64_t)a.n_cap * wide >= (wide <= 4 ? 6 : 12) * num_sms()) {
         switch (wide) {
@@ -803,11 +822,11 @@ extern "C" sg_status sg_distill(const void* d_logits, int32_t dtype, int32_t n_c
     const float l = kLog2e / temperature;
     if (dtype == SG_F32) {
         const Args<float> a = {(const float*)d_logits, (float*)d_grad, ld, ld_grad, d_ids, d_values, d_n, n_cap, n_classes,
-                               k, mean ? 1 : 0, grad_scale, temperature, l, d_loss, d_total, (int32_t*)d_workspace, 0};
+                               k, mean ? 1 : 0, grad_scale, temperature, 1.f / temperature, l, d_loss, d_total, (int32_t*)d_workspace, 0};
         return run(a, s);
     }
     const Args<__nv_bfloat16> a = {(const __nv_bfloat16*)d_logits, (__nv_bfloat16*)d_grad, ld, ld_grad, d_ids, d_values,
-                                   d_n, n_cap, n_classes, k, mean ? 1 : 0, grad_scale, temperature, l, d_loss, d_total,
+                                   d_n, n_cap, n_classes, k, mean ? 1 : 0, grad_scale, temperature, 1.f / temperature, l, d_loss, d_total,
                                    (int32_t*)d_workspace, 0};
     return run(a, s);
 }

@@ -37,7 +37,6 @@ using namespace sgi;
 namespace {
 
 constexpr int kThreads = 256;  // of a block of warps' rows
-constexpr int kWarps = kThreads / 32;
 constexpr int kTurn = 4;      // vectors a thread takes at a time
 constexpr int kRing = 2;      // turns of them in shared memory
 constexpr int kGroups = 16;   // groups of a thread's vectors, at most

@@ -31,9 +31,9 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float exp_from(float x, float m, float l = kLog2e) { return ex2((x - m) * l); }
 
 __device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
-    return x;
+    float m;  // (without NaN, as fmaxf)
+    asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(m) : "f"(x));
+    return m;
 }
 
 // --------------------------------------------------- 16-byte parts of a row

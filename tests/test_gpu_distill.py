@@ -155,6 +155,20 @@ def test_loss_and_gradient(n, c, k, dt):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("vecs", [256, 257, 384, 385, 512, 513])
+@pytest.mark.parametrize("k", [1, 32, 33, 128])
+def test_many_rows_at_the_ends_of_the_forms(vecs, k, dt):
+    # a warp a row in 8, 12 or 16 vectors a lane, blocks from there on
+    n, c = 701, vecs * (4 if dt == "f32" else 8)
+    x, ids, v = _case(n, c, k, dt, vecs + k)
+    if k > 2:
+        ids[11, 2:] = ids[11, 1:2]  # one class many times
+        ids[12, 1] = ids[12, 0]
+    x[13], x[14, c // 2:] = -INF, -INF
+    _hold(x, ids, v, 2.0, True, 1.0, _run(x, ids, v, 2.0))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("n,c,k", [(40, 60, 12), (20, 900, 64), (9, 3000, 100), (6, 40001, 40), (400, 9001, 16), (1300, 2500, 8)])
 def test_classes_that_occur_more_than_once(n, c, k, dt):
     x, ids, v = _case(n, c, k, dt, c)
