@@ -868,12 +868,13 @@ def sg_muon_step(w: torch.Tensor, g: torch.Tensor, m: torch.Tensor, w_out: torch
 # ------------------------------------------- answers, distillation, layer norm
 def _own_stream(what: str, stream, dev: int) -> int:
     """The raw stream of a call whose tensors are on device dev, which has to
-    be the current one (a stream given by its address is taken as it is)."""
+    be the current one."""
     if stream is None:
         if torch._C._cuda_getDevice() == dev:
             return torch._C._cuda_getCurrentRawStream(dev)
-    elif not isinstance(stream, torch.cuda.Stream):
-        return int(stream)
+    elif not isinstance(stream, torch.cuda.Stream):  # its address
+        if not torch.cuda.is_initialized() or torch._C._cuda_getDevice() == dev:
+            return int(stream)
     elif torch._C._cuda_getDevice() == dev and stream.device_index == dev:
         return stream.cuda_stream
     _invalid("%s: the tensors must be on the current device, and on the stream's" % what)

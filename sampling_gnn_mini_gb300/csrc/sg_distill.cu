@@ -8,11 +8,13 @@
 // (k_distill_warp) or a cluster of CTAs (k_distill_row), and many long rows are
 // streamed through shared memory ahead of their use (k_distill_stream).
 //
-// The entries are a row's small part: one warp of each CTA takes them (up to 4 a
-// lane) and forms q while the row is on its way.  Each thread first stores w T p of
-// its vectors; after a block's barrier the entries' classes are written again, from
-// their own logits.  An entry adds up all q of its class, so classes that occur more
-// than once are right, whichever of them writes last (they write the same).
+// The entries are a row's small part.  One warp of a CTA takes a row's (up to 4 a lane)
+// and forms q while the row is on its way: the row's own warp, the first of a cluster's
+// CTAs, or in the streaming form extra warps that do nothing else.  The vectors' w T p
+// is stored first; then the entries' classes are written again, from their own logits.
+// An entry adds up all q of its class where classes occur more than once (a match over
+// the warp for up to 32 entries, a table for more, tells whether any does), so they are
+// right whichever of them writes last (they write the same).
 #include "sg_internal.cuh"
 #include "sg_rows.cuh"
 #include "sg_softmax.cuh"
@@ -292,6 +294,11 @@ __device__ __forceinline__ float finish_row(const Args<T>& a, int32_t r, float w
     return loss;
 }
 
+// A warp a row, with as many vectors a lane as hold it.  Rows of few classes are bound by
+// instructions, some 600 a row whatever its length (200,000 x 47 fp32: 115 us, 18 for the
+// bytes); the next row's loads ahead in registers, or more warps, gain nothing (115 and
+// 123).  us, k = 20: 60,000 x 400 fp32 52 (floor 30), 40,000 x 2000 bf16 73 (48), 20,000 x
+// 4000 bf16 76 (by blocks of 256 threads from shared memory 123, of 64 from registers 124).
 template <int NV>
 constexpr int kWarpBlocks = NV <= 2 ? 5 : NV == 4 ? 4 : NV == 8 ? 3 : 2;  // an SM
 
@@ -325,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, kWarpBlocks<NV>) k_distill_warp(Args
 
 // The whole of a small call in one cluster: each CTA counts the rows with a teacher, the
 // cluster's warps take up to R rows each, all their loads in flight together, the
-// warps' sums meet in CTA 0.  256 rows of 128 fp32, 8 entries: SPEED_SMALL us with the
+// warps' sums meet in CTA 0.  256 rows of 128 fp32, 8 entries: 8.0 us with the
 // host's time (by two launches, and a row after the other, 9.7).
 constexpr int kSmallCtas = 8;
 constexpr int kSmallThreads = 512;
@@ -482,14 +489,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_row(Args<T> a) {
 // Many long rows: the same, with each cluster walking over its rows and the next two
 // rows' slices on their way into shared memory while the current row is worked on.
 //
-// The last warps of a block do nothing but the entries, beside the others and a row each
-// in turn: the classes and their logits are loaded while the row before is worked on, q
-// is formed while the row is reduced, and the entries' classes are written once the
-// row's vectors are stored (`stored`), while the other warps are at the next row.  (By the warps that hold
-// vectors, at the row's start: 284 us for 4096 x 50,257 bf16 and 64 entries; loaded
-// ahead, with a barrier a row: 198, with a barrier for the entries' warps alone the
-// same: every row waits for the longest warp.  Now SPEED_STREAM; without entries at
-// all, the cross-entropy, 139.)
+// The last warps of a block (3 of 16 or 2 of 8) do nothing but the entries, beside the
+// others and a row each in turn: the classes and their logits are loaded while the row
+// before is worked on, q is formed while the row is reduced, and the entries' classes are
+// written once the row's vectors are stored (`stored`), while the other warps are at the
+// next row.  us, 4096 x 50,257 bf16 and 64 entries: 151 (by one such warp 163); by the
+// warps that hold vectors, at the row's start, 284; loaded ahead, with a barrier a row, 198,
+// with a barrier for the entries' warps alone the same: every row waits for the longest
+// warp.  Without entries at all, the cross-entropy, 139.
 constexpr int kStreamVecs = 3200;  // of a CTA's slice: two buffers of it and the entries, two CTAs an SM
 template <int NT>
 constexpr int kEntryWarps = NT == 512 ? 3 : 2;
@@ -746,7 +753,8 @@ template <typename T>
 sg_status run(Args<T> a, cudaStream_t s) {
     const int64_t nv = cdiv((int64_t)a.classes, kE<T>);  // vectors of a row, at most
     const bool by_warp = nv <= 256;
-    // one cluster serves a call whose rows its warps hold at once
+    // one cluster serves a call whose rows its warps hold at once (4 rows a warp, so that
+    // it would serve twice as many, are slower than two launches)
     const int64_t rows = kSmallCtas * (kSmallThreads / 32) * (nv <= 64 ? kSmallRows<2> : kSmallRows<8>);
     const bool small = by_warp && a.n_cap <= rows;
     if (!small) {
@@ -761,12 +769,16 @@ sg_status run(Args<T> a, cudaStream_t s) {
     if (nv <= 64) return run_warp<T, 2>(a, small, s);
     if (nv <= 128) return run_warp<T, 4>(a, small, s);
     if (nv <= 256) return run_warp<T, 8>(a, small, s);
+    // (fewer rows leave warps idle; 700 x 4000 bf16: 12 us, by blocks 14)
     if (a.n_cap >= 4 * num_sms()) {
         if (nv <= 384) return run_warp<T, 12>(a, false, s);
         if (nv <= 512) return run_warp<T, 16>(a, false, s);
     }
     const int wide = nv <= kVecThreads<kThreads> * kVecs ? 1 : nv <= kStreamVecs ? 2 : nv <= 2 * kStreamVecs ? 4 : nv <= 4 * kStreamVecs ? 8 : 16;
-    if (nv <= 8 * kStreamVecs && (int64_t)a.n_cap * wide >= (wide <= 4 ? 6 : 12) * num_sms()) {
+    // from shared memory while each CTA has some rows to stream (us, streamed / not: 900 x
+    // 6000 fp32 14.9 / 17.4, 500 x 6000 12.2 / 11.5; 300 x 20,000 16.7 / 21.0; 120 x 50,257 20 /
+    // 18; 220 x 100,000 55 / 57, 115 x 100,000 37 / 35)
+    if (nv <= 8 * kStreamVecs && (int64_t)a.n_cap * wide >= (wide <= 4 ? 4 : 12) * num_sms()) {
         switch (wide) {
             case 1: return run_stream<T, kThreads, 1>(a, nv, s);
             case 2: return run_stream<T, 512, 1>(a, nv, s);

@@ -2,10 +2,12 @@
 //   mu = mean x,  r = 1 / sqrt(mean (x - mu)^2 + eps),  h = (x - mu) r,  y = h w + b
 //   u = g w:  dx = r (u - mean u - h mean(u h)),  dw = sum over rows of g h,  db = sum over rows of g
 // Bound by memory: forward reads and writes a row once, backward reads two rows and
-// writes one.  A row's values stay in the registers of a group of 4 to 32 lanes (up
-// to 512 values) or of a block (up to 16,384): 16 a thread, so that the gradient of
-// the weight and bias, 32 sums a thread, fits beside them.  The deviation is summed
-// about the mean, in a second pass over the registers.
+// writes one.  A row belongs to a group of 4 to 32 lanes or to a block, 4 to 32 values a
+// thread.  Short rows go from global memory into registers, the next ones ahead; longer
+// ones through a ring in shared memory that every thread fills with its own vectors,
+// rows ahead, and with 16 (24) values a thread the gradient of the weight and bias, two sums a
+// value, still fits beside them.  The deviation is summed about the mean, in a second
+// pass over the values on the chip.
 //
 // Columns belong to threads.  In the gradient a block walks over its rows with the
 // columns' sums in registers, writes them once to the workspace, and a second kernel
@@ -16,7 +18,7 @@
 // group's first lanes, one each.  A group meets only rows that start at the same place
 // within 16 bytes (rows a multiple of 8 apart), so a thread's columns stay the same.
 // Arrays whose rows do not start alike are moved value by value.  30,011 x 1001 bf16
-// forward: SPEED_ODD us, all in single values 50.
+// forward: 26 us, all in single values 50.
 #include <type_traits>
 
 #include "sg_internal.cuh"
@@ -449,9 +451,8 @@ template <typename T, int NT>
 constexpr int kBwdBlocks = NT == kThreads ? (sizeof(T) == 2 ? 2 : 3) : 1;
 
 // SMALL: the whole of a small call in one cluster, whose CTAs' sums meet in distributed
-// shared memory (1,024 x 128 fp32: SPEED_SMALL us with the host's time, with a second
-// launch for the sums 11.3).
-
+// shared memory (1,024 x 128 fp32: 9.8 us with the host's time, with a second
+// launch for the sums 11.3; twice the rows, 16 turns of its groups, 17.5, 11.0).
 template <typename T, int V, int L, int NT, int R, bool SMALL>
 __global__ void __launch_bounds__(NT, kBwdBlocks<T, NT>) k_norm_bwd(BwdArgs<T> a) {
     pdl_start();
@@ -520,7 +521,7 @@ __global__ void __launch_bounds__(NT, kBwdBlocks<T, NT>) k_norm_bwd(BwdArgs<T> a
 // loaded a row ahead.
 // A group is a warp (L = 32, blocks of NT = 256 threads) or the block: of L threads, or (L
 // = 0) of as many, up to NT, as the row needs.  The constant size is worth its
-// instances: 19,531 x 4096 bf16 forward SPEED_FIXED us, of any size 64.
+// instances: 19,531 x 4096 bf16 forward 61 us, of any size 64.
 constexpr int kRingBytes = 208 * 1024;  // of an SM
 // Threads an SM, by the registers for HELD values of a row a thread (NT = 1024: 64).  A:
 // arrays that are read (1 forward, 2 backward).  Backward, 16 values a thread: 512 of
@@ -657,7 +658,6 @@ __global__ void __launch_bounds__(1024) k_norm_join(const float* __restrict__ pa
 // -------------------------------------------------------------------- host
 constexpr int kMaxDim = SG_MAX_NORM_DIM;
 
-
 // Blocks that fill the device, a multiple of 8.
 int64_t all_blocks(int per_sm) { return (int64_t)num_sms() * per_sm / 8 * 8; }
 // Blocks of the gradient at most, whatever the form: the workspace has room for them.
@@ -739,8 +739,10 @@ sg_status by_size(const A& a, More... more) {
         if (vecs <= 64) return go<T, 2, 32, kThreads, 1>(a, more...);
         return go<T, V, 0, 1024, 1>(a, more...);
     }
-    // a warp a row while there are rows for all warps: no barrier, and the ring
-    const bool many = a.n_cap >= 16 * num_sms();
+    // a warp a row while there are rows for all warps: no barrier (us, by warps / by
+    // blocks: backward 2000 x 400 fp32 11.9 / 14.5, 9000 x 400 11.9 / 21.0, 1000 x 400 12.2 /
+    // 11.3; forward 5000 x 1000 fp32 9.4 / 8.6, 9000 x 1000 15.1 / 15.2)
+    const bool many = a.n_cap >= (std::is_same_v<A, FwdArgs<T>> ? 64 : 8) * num_sms();
     if constexpr (std::is_same_v<A, FwdArgs<T>>) {
         if (vecs <= 64) return go_ring<T, 2, 32, kThreads>(a, more...);
         if (vecs <= 48 * V && many) return go_ring<T, 3 * V / 2, 32, kThreads>(a, more...);

@@ -149,3 +149,15 @@ def test_binding_refuses_tensors_of_another_device(monkeypatch):
         with pytest.raises(sg.SgError) as e:
             call()
         assert e.value.status == INVALID and "current device" in str(e.value)
+
+
+def test_binding_refuses_a_stream_address_of_another_device(monkeypatch):
+    monkeypatch.setattr(sg, "_lib", _Refuses())
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)  # the tensors are on 0
+    x, f = _on_device(4, 8), _on_device(4)
+    for call in (lambda: sg.sg_logprobs(x, None, 4, None, None, f, stream=0),
+                 lambda: sg.sg_layernorm_fwd(x, None, None, 4, None, x, stream=0)):
+        with pytest.raises(sg.SgError) as e:
+            call()
+        assert e.value.status == INVALID and "current device" in str(e.value)
