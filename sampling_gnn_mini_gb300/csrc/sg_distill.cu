@@ -295,7 +295,7 @@ __device__ __forceinline__ float finish_row(const Args<T>& a, int32_t r, float w
 }
 
 // A warp a row, with as many vectors a lane as hold it.  Rows of few classes are bound by
-// instructions, some 700 issue slots a row whatever its length (200,000 x 47 fp32: 115 us, 18 for the
+// instructions, some 700 issue slots a row whatever its length (200,000 x 47 fp32: 115 us, 11 for the
 // bytes); the next row's loads ahead in registers, or more warps, gain nothing (115 and
 // 123).  us, k = 20: 60,000 x 400 fp32 52 (floor 30), 40,000 x 2000 bf16 73 (48), 20,000 x
 // 4000 bf16 76 (by blocks of 256 threads from shared memory 123, of 64 from registers 124).

@@ -180,8 +180,11 @@ __device__ __forceinline__ void unpack(const uint4& u, float (&f)[kE<T>]) {
 // ------------------------------------------------------------ rows by threads
 // kFewRows rows of up to kFewClasses classes to a block, in shared memory, then a
 // thread a row.  A thread's top K sit in registers in order: a logit moves in where it
-// is larger, so that equal ones stay in the order of their classes.  The rows are
-// copied
+// is larger, so that equal ones stay in the order of their classes.  For K > 1 only the
+// logits that reach the K-th largest of 8 or 16 groups' maxima are tried, some K + 2 of
+// them: the pass that finds the row's maximum finds the groups', the pass that adds up the
+// exponentials marks them (us, 200,001 x 47 fp32 k = 3 15.3, each logit tried 17.9; k = 8
+// 24, 32).  The rows are copied
 //   by vectors when every row is on 16 bytes, at an odd pitch of vectors, filled up
 //              with -inf (threads that read a vector each meet different banks);
 //   whole      when they follow one another from a 16-byte boundary (threads that
@@ -189,10 +192,10 @@ __device__ __forceinline__ void unpack(const uint4& u, float (&f)[kE<T>]) {
 //              of 16 bytes);
 //   by values  if neither, at an odd pitch (up to kFewByValues classes: the index
 //              arithmetic costs more than a warp a row from there on).
-// us, fp32, this / a warp a row: 200,000 x 47 k = 1 9.6 / 80, k = 3 14 / 102, k = 8 29 /
-// 115; 100,000 x 128 k = 1 15 / 42, k = 5 30 / 54, k = 8 44 / 56; 25,000 x 128 k = 1 7.3 /
-// 11, k = 8 17 / 15.  What is left is the insertion: two instructions a class and place.
-constexpr int kFewRows = 128, kFewClasses = 128, kFewByValues = 64, kFewTop = 8;
+// us, fp32, this / a warp a row: 200,000 x 47 k = 1 9.6 / 80, k = 3 15 / 102, k = 8 24 /
+// 115; 100,000 x 128 k = 1 15 / 42, k = 5 24 / 54; 25,000 x 128 k = 1 7.3 / 11, k = 8 11 / 15.
+// It does not matter how many rows a block has (32 to 192).
+constexpr int kFewRows = 64, kFewClasses = 128, kFewByValues = 64, kFewTop = 8;
 enum Few { kWhole, kByVectors, kByValues };
 
 // Rows in shared memory: elements to f(value, class), in order.
@@ -212,6 +215,77 @@ __device__ __forceinline__ void few_each(const uint4* smem, int32_t pitch, int32
         const M* row = reinterpret_cast<const M*>(smem) + (int32_t)threadIdx.x * pitch;
 #pragma unroll 4
         for (int32_t c = 0; c < classes; ++c) f(to_f(row[c]), c);
+    }
+}
+
+// This thread's element of a class.
+template <typename T, Few HOW>
+__device__ __forceinline__ float few_at(const uint4* smem, int32_t pitch, int32_t c) {
+    typedef std::conditional_t<HOW == kByValues, float, T> M;
+    return to_f(reinterpret_cast<const M*>(smem)[(int32_t)threadIdx.x * pitch * (HOW == kByVectors ? kE<T> : 1) + c]);
+}
+// Elements to f(value, class mod G).
+template <typename T, Few HOW, int G, typename F>
+__device__ __forceinline__ void few_groups(const uint4* smem, int32_t pitch, int32_t classes, F f) {
+    int32_t c = 0;
+    if constexpr (HOW == kByVectors) {
+        const uint4* row = smem + (int32_t)threadIdx.x * pitch;
+        for (; c < classes; c += G)
+#pragma unroll
+            for (int v = 0; v < G / kE<T>; ++v) {
+                if (v > 0 && c + v * kE<T> >= classes) break;
+                float e[kE<T>];
+                unpack<T>(row[c / kE<T> + v], e);
+#pragma unroll
+                for (int i = 0; i < kE<T>; ++i) f(e[i], v * kE<T> + i);
+            }
+    } else {
+        for (; c + G <= classes; c += G)
+#pragma unroll
+            for (int j = 0; j < G; ++j) f(few_at<T, HOW>(smem, pitch, c + j), j);
+#pragma unroll
+        for (int j = 0; j < G; ++j)
+            if (c + j < classes) f(few_at<T, HOW>(smem, pitch, c + j), j);
+    }
+}
+// Elements to take(value); those for which it is true to f(value, class), in order.
+template <typename T, Few HOW, typename Take, typename F>
+__device__ __forceinline__ void few_bits(const uint4* smem, int32_t pitch, int32_t classes, Take take, F f) {
+    for (int32_t c0 = 0; c0 < classes; c0 += 32) {
+        uint32_t bits = 0;
+        const int32_t most = min(32, classes - c0);
+        if constexpr (HOW == kByVectors) {
+            const uint4* row = smem + (int32_t)threadIdx.x * pitch + c0 / kE<T>;
+            for (int32_t q = 0; q < most; q += 8) {
+                uint32_t part = 0;
+#pragma unroll
+                for (int v = 0; v < 8 / kE<T>; ++v) {
+                    if (v > 0 && q + v * kE<T> >= most) break;
+                    float e[kE<T>];
+                    unpack<T>(row[q / kE<T> + v], e);
+#pragma unroll
+                    for (int i = 0; i < kE<T>; ++i)
+                        if (take(e[i])) part |= 1u << (v * kE<T> + i);
+                }
+                bits |= part << q;
+            }
+        } else {
+            int32_t q = 0;
+            for (; q + 8 <= most; q += 8) {
+                uint32_t part = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (take(few_at<T, HOW>(smem, pitch, c0 + q + i))) part |= 1u << i;
+                bits |= part << q;
+            }
+            for (; q < most; ++q)
+                if (take(few_at<T, HOW>(smem, pitch, c0 + q))) bits |= 1u << q;
+        }
+        while (bits) {
+            const int32_t c = c0 + __ffs((int)bits) - 1;
+            bits &= bits - 1;
+            f(few_at<T, HOW>(smem, pitch, c), c);
+        }
     }
 }
 
@@ -274,7 +348,7 @@ __global__ void __launch_bounds__(kFewRows) k_logprobs_few(Args<T> a, int32_t pi
     int32_t at[K];
 #pragma unroll
     for (int j = 0; j < K; ++j) top[j] = -INFINITY, at[j] = -1;
-    few_each<T, HOW>(few_smem, pitch, classes, [&](float v, int32_t c) {
+    const auto insert = [&](float v, int32_t c) {
         if (v > top[K - 1]) {  // the entries below it move down, equal ones above it stay
 #pragma unroll
             for (int j = K - 1; j > 0; --j) {
@@ -284,14 +358,43 @@ __global__ void __launch_bounds__(kFewRows) k_logprobs_few(Args<T> a, int32_t pi
             }
             if (v > top[0]) top[0] = v, at[0] = c;
         }
-    });
-    Stat s = {top[0], 0.f, 0.f};
-    const float b = finite_base(s.m);
-    few_each<T, HOW>(few_smem, pitch, classes, [&](float v, int32_t) {
-        const float d = max_nan((v - b) * kLog2e, kNone), e = ex2(d);
-        s.z += e;
-        s.t = fmaf(e, d, s.t);
-    });
+    };
+    Stat s = {-INFINITY, 0.f, 0.f};
+    if constexpr (K == 1) {
+        few_each<T, HOW>(few_smem, pitch, classes, insert);
+        s.m = top[0];
+        const float b = finite_base(s.m);
+        few_each<T, HOW>(few_smem, pitch, classes, [&](float v, int32_t) {
+            const float d = max_nan((v - b) * kLog2e, kNone), e = ex2(d);
+            s.z += e;
+            s.t = fmaf(e, d, s.t);
+        });
+    } else {
+        constexpr int G = K <= 4 ? 8 : 16;
+        float g[G];
+#pragma unroll
+        for (int j = 0; j < G; ++j) g[j] = -INFINITY;
+        few_groups<T, HOW, G>(few_smem, pitch, classes, [&](float v, int j) { g[j] = fmaxf(g[j], v); });
+#pragma unroll
+        for (int size = 2; size <= G; size *= 2)
+#pragma unroll
+            for (int d = size / 2; d > 0; d /= 2)
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+                    if ((i & d) == 0) {
+                        const float x = g[i], y = g[i + d];
+                        g[i] = (i & size) == 0 ? fmaxf(x, y) : fminf(x, y);
+                        g[i + d] = (i & size) == 0 ? fminf(x, y) : fmaxf(x, y);
+                    }
+        s.m = g[0];
+        const float b = finite_base(s.m), bound = fmaxf(g[K - 1], -3.402823466e38f);
+        few_bits<T, HOW>(few_smem, pitch, classes, [&](float v) {
+            const float d = max_nan((v - b) * kLog2e, kNone), e = ex2(d);
+            s.z += e;
+            s.t = fmaf(e, d, s.t);
+            return v >= bound;
+        }, insert);
+    }
     const float log_z = logf(s.z);
     put_row(a, r, s, log_z, y, xy);
     const bool bad = s.z != s.z;
