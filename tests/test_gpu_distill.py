@@ -314,6 +314,40 @@ def test_two_graphs_share_a_workspace():
     assert all(torch.equal(a, b) for w, o in zip(want, outs) for a, b in zip(w, o))
 
 
+def test_two_streams_at_once():
+    # long rows streamed, few long rows, a small call in one cluster, a row a warp
+    cases = [_case(700, 9001, 8, "bf16", 1), _case(9, 40001, 40, "f32", 2), _case(200, 100, 8, "f32", 3), _case(2000, 2500, 5, "f32", 4)]
+    want = [_run(*t, 2.0) for t in cases]
+    outs = [[torch.empty_like(t) for t in w] for w in want]
+    ws = [_ws(*t[0].shape) for t in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for t, o, s, m in zip(cases, outs, streams, ws):
+            sg.sg_distill(*t, len(t[0]), None, *o, m, temperature=2.0, stream=s)
+    torch.cuda.synchronize()
+    sg.sg_stream_check()
+    assert all(torch.equal(a, b) for w, o in zip(want, outs) for a, b in zip(w, o))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("start,gap", [(1, 3), (3, 8), (0, 1), (0, 0)])
+def test_many_rows_at_any_alignment(start, gap, dt):
+    n, c = 650, 1801 if dt == "f32" else 3601
+    x, ids, v = _case(n, c, 9, dt, start)
+    wide = torch.full((n, start + c + gap), float("nan"), dtype=x.dtype, device="cuda")
+    wide[:, start:start + c] = x
+    out = torch.full((n, 2 + c + gap), 7.0, dtype=x.dtype, device="cuda")
+    loss, total = torch.empty(n, device="cuda"), torch.empty(2, device="cuda")
+    m = n - 13
+    sg.sg_distill(wide[:, start:start + c], ids, v, n, torch.tensor([m], dtype=torch.int32, device="cuda"), loss, total,
+                  out[:, 2:2 + c], _ws(n, c), temperature=2.0)
+    sg.sg_stream_check()
+    _hold(x[:m], ids[:m], v[:m], 2.0, True, 1.0, (loss[:m], total, out[:m, 2:2 + c]))
+    out[:m, 2:2 + c] = 7.0
+    assert bool((out == 7).all())
+
+
 def test_answers_of_a_teacher_train_a_student():
     # a teacher's top logits as sg_logprobs reports them, then the student's loss and
     # gradient: with every class reported, the full divergence and its gradient

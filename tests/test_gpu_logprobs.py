@@ -323,3 +323,33 @@ def test_in_a_graph_and_on_other_streams():
     torch.cuda.synchronize()
     sg.sg_stream_check()
     assert all(torch.equal(a, b) for w, o in zip(want, outs) for a, b in zip(w, o))
+
+
+def test_two_streams_at_once():
+    # a thread, a warp and four warps a row, blocks that walk over rows, a cluster a row
+    cases = [(_logits(20000, 47, "f32", 1), 3), (_logits(3000, 900, "bf16", 2), 20), (_logits(500, 12000, "bf16", 3), 64),
+             (_logits(400, 50257, "bf16", 4), 10), (_logits(3, 140000, "f32", 5), 100)]
+    want = [_run(x, _labels(*x.shape, 6), k) for x, k in cases]
+    outs = [[torch.empty_like(t) for t in w] for w in want]
+    streams = [torch.cuda.Stream() for _ in cases]
+    labels = [_labels(*x.shape, 6) for x, _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for (x, k), y, o, s in zip(cases, labels, outs, streams):
+            sg.sg_logprobs(x, y, len(x), None, *o, stream=s)
+    torch.cuda.synchronize()
+    sg.sg_stream_check()
+    assert all(torch.equal(a, b) for w, o in zip(want, outs) for a, b in zip(w, o))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("start,gap", [(1, 3), (3, 8), (0, 1)])
+@pytest.mark.parametrize("vecs", [300, 600, 1200])
+def test_register_rows_at_any_alignment(vecs, start, gap, dt):
+    n, c, k = 37, vecs * (4 if dt == "f32" else 8) + 5, 30
+    wide = torch.full((n, start + c + gap), float("nan"), dtype=DT[dt], device="cuda")
+    wide[:, start:start + c] = _logits(n, c, dt, vecs)
+    x, y, m = wide[:, start:start + c], _labels(n, c, 2), 30
+    got = _run(x, y, k, d_n=torch.tensor([m], dtype=torch.int32, device="cuda"))
+    _hold(x[:m], y[:m], [t[:m] for t in got], k)
+    assert all(bool((t[m:] == (77 if t.dtype == torch.int32 else 7)).all()) for t in got)

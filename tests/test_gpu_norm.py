@@ -156,6 +156,36 @@ def test_many_rows(n, d, dt):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [1200, 1300, 9700, 9800])
+@pytest.mark.parametrize("d", [257, 300, 400, 513, 700, 1000])
+def test_rows_enough_for_all_warps_or_not(n, d, dt):
+    x, g, w, b = _inputs(n, d, dt, "f32", n + d)
+    y, m, r = _fwd(x, w, b)
+    _hold_fwd(x, w, b, y, m, r)
+    _hold_bwd(g, x, w, m, r, *_bwd(g, x, w, m, r))
+
+
+def test_two_streams_at_once():
+    cases = [_inputs(5000, 1001, "bf16", "f32", 1), _inputs(3000, 4096, "f32", "bf16", 2), _inputs(900, 64, "f32", "f32", 3)]
+    want, outs = [], []
+    for x, g, w, b in cases:
+        y, m, r = _fwd(x, w, b)
+        want.append((y, m, r) + _bwd(g, x, w, m, r))
+        outs.append([torch.empty_like(t) for t in want[-1]])
+    ws = [_ws(*c[0].shape) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for (x, g, w, b), o, s, m in zip(cases, outs, streams, ws):
+            with torch.cuda.stream(s):
+                sg.sg_layernorm_fwd(x, w, b, len(x), None, *o[:3])
+                sg.sg_layernorm_bwd(g, x, w, o[1], o[2], len(x), None, *o[3:], m)
+    torch.cuda.synchronize()
+    sg.sg_stream_check()
+    assert all(torch.equal(a, b) for w, o in zip(want, outs) for a, b in zip(w, o))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("d", [5, 64, 100, 700, 4096])
 def test_without_parameters_and_parts(d, dt):
     x, g, w, b = _inputs(50, d, dt, "f32", d)
