@@ -510,6 +510,14 @@ __device__ __noinline__ int32_t select_by_warp(const T* row, int32_t classes, in
     return all ? found : min(found, k);
 }
 
+// Room in a list for a warp's entries, `mine` of them this lane's: where they begin.
+__device__ __forceinline__ int32_t reserve(int32_t mine, int32_t* count) {
+    const int32_t upto = warp_incl_scan(mine), all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    int32_t at = 0;
+    if (lane_id() == 0 && all > 0) at = atomicAdd(count, all);
+    return __shfl_sync(0xFFFFFFFFu, at, 0) + upto - mine;
+}
+
 // A warp's list in order, P keys a lane (bitonic; key lane P + i in e[i]), its first k
 // written.
 template <typename T, int P>
@@ -682,20 +690,14 @@ __global__ void __launch_bounds__(kWarpThreads<W>, (NV <= 2 ? 48 : NV == 4 ? 40 
         if (vm[k] >= tau) hits[hit + __popc(mask & ((1u << lane) - 1u))] = (uint16_t)(first + 32 * W * k);
         hit += __popc(mask);
     }
-    // room for this warp's keys, `mine` of them this lane's
-    const auto reserve = [&](int32_t mine) {
-        const int32_t upto = warp_incl_scan(mine), all = __shfl_sync(0xFFFFFFFFu, upto, 31);
-        int32_t at = found;
-        if constexpr (W == 1) {
-            found += all;
-        } else {
-            if (lane == 0) at = atomicAdd(&counts[0], all);
-            at = __shfl_sync(0xFFFFFFFFu, at, 0);
-        }
-        return at + upto - mine;
+    const auto room = [&](int32_t mine) {
+        if constexpr (W > 1) return reserve(mine, &counts[0]);
+        const int32_t upto = warp_incl_scan(mine), at = found + upto - mine;
+        found += __shfl_sync(0xFFFFFFFFu, upto, 31);
+        return at;
     };
     if (rank == 0 && part.head + part.tail > 0) {
-        const int32_t at = reserve(xe >= tau);
+        const int32_t at = room(xe >= tau);
         if (xe >= tau && at < kWarpCap) list[at] = key_of<T>(xe, ce);
     }
     __syncwarp();
@@ -711,7 +713,7 @@ __global__ void __launch_bounds__(kWarpThreads<W>, (NV <= 2 ? 48 : NV == 4 ? 40 
         int32_t mine = 0;
 #pragma unroll
         for (int e = 0; e < kE<T>; ++e) mine += f[e] >= tau;
-        int32_t at = reserve(mine);
+        int32_t at = room(mine);
 #pragma unroll
         for (int e = 0; e < kE<T>; ++e)
             if (f[e] >= tau) {
@@ -1036,14 +1038,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprobs_row(Args<T> a, int32
                 tau = value_of(lo);
             }
         }
+        const float lowest = fmaxf(tau, -3.402823466e38f);  // (-inf takes no part)
         if (!bad) {
-            if (sl.xe >= tau && sl.xe > -INFINITY) offer(list, sl.xe, sl.edge);
-            for (int32_t g0 = 0, g = 0; g0 < sl.count; g0 += span, ++g) {
-                const float gm = gmax[g * NT];
-                if (gm < tau || gm == -INFINITY) continue;
-                const int32_t h = atomicAdd(&hit_count, 1);
-                if (h < CAP) hits[h] = g * NT + (int32_t)threadIdx.x;
-            }
+            if (sl.xe >= lowest) offer(list, sl.xe, sl.edge);
+            uint32_t reached = 0;  // of the thread's groups
+            for (int32_t g0 = 0, g = 0; g0 < sl.count; g0 += span, ++g) reached |= gmax[g * NT] >= lowest ? 1u << g : 0u;
+            for (int32_t to = reserve(__popc(reached), &hit_count); reached; ++to, reached &= reached - 1)
+                if (to < CAP) hits[to] = (__ffs((int)reached) - 1) * NT + (int32_t)threadIdx.x;
         }
         __syncthreads();
         // the groups that reach the bound, their vectors over all threads
@@ -1058,7 +1059,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_logprobs_row(Args<T> a, int32
             unpack<T>(u, f);
 #pragma unroll
             for (int e = 0; e < kE<T>; ++e)
-                if (f[e] >= tau && f[e] > -INFINITY) offer(list, f[e], sl.first(i) + e);
+                if (f[e] >= lowest) offer(list, f[e], sl.first(i) + e);
         }
         __syncthreads();
         if (list.count > CAP || hit_count > CAP)
