@@ -192,7 +192,7 @@ __device__ __forceinline__ void unpack(const uint4& u, float (&f)[kE<T>]) {
 //              of 16 bytes);
 //   by values  if neither, at an odd pitch (up to kFewByValues classes: the index
 //              arithmetic costs more than a warp a row from there on).
-// us, fp32, this / a warp a row: 200,000 x 47 k = 1 9.6 / 80, k = 3 15 / 102, k = 8 24 /
+// us, fp32, this / a warp a row: 200,000 x 47 k = 1 13 / 80, k = 3 15 / 102, k = 8 24 /
 // 115; 100,000 x 128 k = 1 15 / 42, k = 5 24 / 54; 25,000 x 128 k = 1 7.3 / 11, k = 8 11 / 15.
 // It does not matter how many rows a block has (32 to 192).
 constexpr int kFewRows = 64, kFewClasses = 128, kFewByValues = 64, kFewTop = 8;
