@@ -15,6 +15,9 @@
 // An entry adds up all q of its class where classes occur more than once (a match over
 // the warp for up to 32 entries, a table for more, tells whether any does), so they are
 // right whichever of them writes last (they write the same).
+//
+// Above a temperature of 4 the loss needs more care than its definition takes
+// (k_distill_loss, which then follows and writes it).
 #include "sg_internal.cuh"
 #include "sg_rows.cuh"
 #include "sg_softmax.cuh"
@@ -45,6 +48,7 @@ struct Args {
     float* total;
     int32_t* done;   // rows or blocks that are done; then `counts` counts of rows with a teacher
     int32_t counts;
+    float2* stats;  // rows' maximum and sum for k_distill_loss, or NULL
 };
 
 // Whether a row has a teacher: its first entry says so.
@@ -107,10 +111,10 @@ __device__ __forceinline__ void load_entry(const Args<T>& a, int32_t r, int32_t 
     else if (i != -1 && report) dev_err(ERR_INDEX);
 }
 
-// One warp: max v and log sum exp((v - max) / T), once the entries are there; q is put
-// beside them (a used row: at least one value is above -inf)
+// One warp: max v and sum exp((v - max) / T) with its logarithm, once the entries are
+// there; q is put beside them (a used row: at least one value is above -inf)
 struct Scale {
-    float m, log_zq;
+    float m, log_zq, zq;
 };
 template <typename T>
 __device__ __forceinline__ Scale scale_entries(const Args<T>& a, Entries& n) {
@@ -135,7 +139,7 @@ __device__ __forceinline__ Scale scale_entries(const Args<T>& a, Entries& n) {
 #pragma unroll
     for (int e = 0; e < kPer; ++e)
         if (lane + 32 * e < a.k) n.q[lane + 32 * e] = q[e] * inv;
-    return {m, logf(z)};
+    return {m, logf(z), z};
 }
 // The row's loss (one warp, the same in every lane), from the row's maximum M and sum Z.
 template <typename T>
@@ -153,6 +157,12 @@ __device__ __forceinline__ float loss_of(const Args<T>& a, const Scale& c, const
         else s = fmaf(q, ((n.v[j] - c.m) * inv - c.log_zq) + (log_z - (x - M) * inv), s);
     }
     return warp_sum(s) * (a.temp * a.temp);
+}
+// One lane of a used row: its loss, and its statistics where they are asked for.
+template <typename T>
+__device__ __forceinline__ void put_loss(const Args<T>& a, int32_t r, float loss, float M, float Z) {
+    a.loss[r] = loss;
+    if (a.stats) a.stats[r] = make_float2(M, Z);
 }
 // One warp: all entries of the R rows r, r + step, .. below n, for itself.
 template <int R, typename T>
@@ -272,7 +282,7 @@ __device__ __forceinline__ float finish_row(const Args<T>& a, int32_t r, float w
     unpair(sum, z, z1);
     z = warp_sum(z + z1 + base.of(d.xe));
     const float loss = loss_of(a, scale, mine, m, z);
-    if (lane == 0) a.loss[r] = loss;
+    if (lane == 0) put_loss(a, r, loss, m, z);
     if (!out) return loss;
     const bool same = same_phase(row, (const T*)out);
     const float inv = z == 0.f ? 0.f : w / z;
@@ -367,6 +377,7 @@ __global__ void __launch_bounds__(kSmallThreads) k_distill_small(Args<T> a) {
         if (r0 + q * step < n) sum += finish_row(a, r0 + q * step, w, d[q], entries[q], tables[warp]);
     if (lane_id() == 0) part[warp] = sum;
     cluster_sync();
+    if (a.stats && blockIdx.x == 0 && threadIdx.x == 0) a.done[0] = 0, a.done[1] = v;
     if (blockIdx.x == 0 && warp == 0 && a.total) {
         float s = 0.f;
 #pragma unroll
@@ -466,7 +477,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_row(Args<T> a) {
         }
         if (rank == 0 && threadIdx.x < 32) {
             const float loss = loss_of(a, scale, entries, M, Z);
-            if (threadIdx.x == 0) a.loss[r] = loss;
+            if (threadIdx.x == 0) put_loss(a, r, loss, M, Z);
         }
         __syncthreads();  // the vectors are stored
         if (out) put_entries(a, entries, out, part, v0, count, rank, (int32_t)threadIdx.x, twice, w, M, Z);
@@ -657,7 +668,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_distill_stream(Args<T> a, int
                 join_parts<kParts>(parts[slot], M, Z, a.l);
                 if (rank == 0) {
                     const float loss = loss_of(a, scale, entry, M, Z);
-                    if (lane == 0) a.loss[r] = loss;
+                    if (lane == 0) put_loss(a, r, loss, M, Z);
                 }
                 if (out && !mbar_wait(&stored[slot], turn) && lane == 0) dev_err(ERR_TIMEOUT);
                 __syncwarp();
@@ -717,6 +728,169 @@ __global__ void __launch_bounds__(kCountThreads) k_distill_count(const int32_t* 
     if (total && n == 0) total[0] = 0.f, total[1] = 0.f;  // nobody else writes it
 }
 
+// ------------------------------------------------ the loss above a temperature
+// T^2 sum q (log q - log p), as it is defined, is off by the rounding of the two
+// logarithms, some 2^-22, times T^2.  Up to T = 4 that is 2^-18; but the higher T, the
+// closer are q and p, and the sum shrinks like 1 / T^2 where the entries have (nearly)
+// all of p: with 128 classes and 128 entries the loss was off by 1e-3 of itself at T =
+// 100 and by 9e-2 at T = 1000 (now 3e-7).
+//
+// So it is made of parts that cannot be below 0 (where no class occurs twice).  With u =
+// log q - log p, p = q exp(-u), and as q and p sum to 1 each,
+//   sum q u = sum q (u + exp(-u) - 1) + rest,  rest = 1 - sum of p over the entries.
+// The bracket is a series in u near 0, and q times it is q (u - 1) + p elsewhere.  What
+// every u is off by alike (log z_q, log z) counts times the rest and its own square now.
+// The rest is the difference it is defined by where the loss is large beside the
+// difference's rounding.  Where it is not, the row is read once more: the rest is the
+// exponentials' sum over the row less the entries', with what each addition rounds off
+// carried along, so that an entry's exponential, the same bits in both, leaves nothing.
+//
+// A warp a row, from the maximum and sum that the row's own kernel left.  A row of up to
+// kByWarp classes is read again by its warp, a longer one by the block (us, by warps / by
+// blocks: 100,000 x 128 fp32, all of them read again, 247 / 378; 5000 x 4000 87 / 104; 1000
+// x 4000 29 / 38).
+constexpr float kPlainTemp = 4.f;
+constexpr int kByWarp = 4096;
+constexpr float kSmallLoss = 0.125f;  // over T^2 (1 - sum p is off by 2^-20 at most: 8e-6 of it)
+
+// A sum and what its additions rounded off (Knuth's two-sum).
+struct Exact {
+    float s, off;
+    __device__ __forceinline__ void add(float x) {
+        const float t = s + x, b = t - s;
+        off += (s - (t - b)) + (x - b);
+        s = t;
+    }
+    __device__ __forceinline__ void add(const Exact& o) {
+        off += o.off;
+        add(o.s);
+    }
+    __device__ __forceinline__ void add_lanes() {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            add(Exact{__shfl_xor_sync(0xFFFFFFFFu, s, d), __shfl_xor_sync(0xFFFFFFFFu, off, d)});
+    }
+};
+
+// Adds up a row's exponentials and `sum`, over n threads of which this is t; each warp's sum
+// in all its lanes.
+template <typename T>
+__device__ __forceinline__ Exact sum_part(const Args<T>& a, int32_t r, float M, int32_t t, int32_t n, Exact sum) {
+    const T* row = a.x + (int64_t)r * a.ld;
+    const RowParts<T> part(row, a.classes);
+    const int32_t ce = t < 32 ? part.edge(t) : -1;
+    if (ce >= 0) sum.add(exp_from(to_f(row[ce]), M, a.l));
+#pragma unroll 4
+    for (int32_t v = t; v < part.vecs; v += n) {
+        const uint4 u = *reinterpret_cast<const uint4*>(row + part.head + v * kE<T>);
+        f2 f[kE<T> / 2];
+        pairs_of(u, f);
+#pragma unroll
+        for (int i = 0; i < kE<T> / 2; ++i) {
+            float x, y;
+            unpair(f[i], x, y);
+            sum.add(exp_from(x, M, a.l));
+            sum.add(exp_from(y, M, a.l));
+        }
+    }
+    sum.add_lanes();
+    return sum;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_distill_loss(Args<T> a) {
+    pdl_start();
+    constexpr int kWarps = kThreads / 32;
+    __shared__ Entries entries[kWarps];
+    struct Again {
+        float s, m, z;
+        Exact out;  // less the entries' exponentials
+        bool is;
+    };
+    __shared__ Again again[kWarps];
+    __shared__ Exact sums[kWarps];
+    __shared__ bool last;
+    const int warp = (int)(threadIdx.x >> 5), lane = (int)lane_id();
+    const int32_t n = rows_of(a.d_n, a.n_cap), groups = (n + kWarps - 1) / kWarps, blocks = min((int32_t)gridDim.x, groups);
+    const float square = a.temp * a.temp;
+    if (n == 0 && a.total && blockIdx.x == 0 && threadIdx.x == 0) a.total[0] = a.total[1] = 0.f;
+    if ((int32_t)blockIdx.x >= blocks) return;
+    Entries& e = entries[warp];
+    for (int32_t g = (int32_t)blockIdx.x; g < groups; g += (int32_t)gridDim.x) {
+        const int32_t r = g * kWarps + warp;
+        bool small = false;
+        if (r < n && row_used(a, r)) {
+            const float2 st = __ldcg(a.stats + r);
+            const float M = st.x, Z = st.y;
+            load_entries<1>(a, r, 0, n, &e, false);
+            const Scale c = scale_entries(a, e);  // (each lane's own entries)
+            const float apart = logf(Z / c.zq);
+            float s = 0.f, sum = 0.f;
+            Exact out = {0.f, 0.f};
+            for (int32_t j = lane; j < a.k; j += 32) {
+                const float q = e.q[j], x = e.x[j];
+                if (q == 0.f) continue;
+                if (x == -INFINITY && Z == Z) {
+                    s += INFINITY;
+                    continue;
+                }
+                const float u = fmaf((e.v[j] - c.m) - (x - M), a.inv_temp, apart), ex = exp_from(x, M, a.l), p = ex / Z;
+                if (fabsf(u) < 0.5f) {  // (what the series leaves out is below 2^-24 of it)
+                    float f = 1.f / 40320.f;
+                    f = fmaf(-u, f, 1.f / 5040.f);
+                    f = fmaf(-u, f, 1.f / 720.f);
+                    f = fmaf(-u, f, 1.f / 120.f);
+                    f = fmaf(-u, f, 1.f / 24.f);
+                    f = fmaf(-u, f, 1.f / 6.f);
+                    f = fmaf(-u, f, 0.5f);
+                    s = fmaf(q * f, u * u, s);
+                } else {
+                    s += fmaf(q, u - 1.f, p);
+                }
+                sum += p;
+                out.add(-ex);
+            }
+            s = warp_sum(s);
+            float loss = s + (1.f - warp_sum(sum));
+            if (loss < kSmallLoss) {
+                if (a.classes <= kByWarp) {
+                    const Exact all = sum_part(a, r, M, lane, 32, out);
+                    loss = s + (all.s + all.off) / Z;
+                } else {
+                    small = true;
+                    out.add_lanes();
+                    if (lane == 0) again[warp] = {s, M, Z, out, true};
+                }
+            }
+            if (!small && lane == 0) a.loss[r] = loss * square;
+        }
+        if (a.classes <= kByWarp) continue;
+        if (!small && lane == 0) again[warp].is = false;
+        if (!__syncthreads_or(small)) continue;
+        for (int w = 0; w < kWarps; ++w) {
+            if (!again[w].is) continue;
+            Exact all = sum_part(a, g * kWarps + w, again[w].m, (int32_t)threadIdx.x, kThreads, Exact{0.f, 0.f});
+            if (lane == 0) sums[warp] = all;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                for (int i = 1; i < kWarps; ++i) all.add(sums[i]);
+                all.add(again[w].out);
+                a.loss[g * kWarps + w] = (again[w].s + (all.s + all.off) / again[w].z) * square;
+            }
+            __syncthreads();
+        }
+    }
+    if (!a.total) return;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(a.done, 1) == blocks - 1;
+    __syncthreads();
+    if (last) {
+        __threadfence();
+        put_total<kThreads>(a, n);
+    }
+}
+
 // -------------------------------------------------------------------- host
 template <typename T, int NV>
 sg_status run_warp(const Args<T>& a, bool small, cudaStream_t s) {
@@ -750,21 +924,7 @@ sg_status run_stream(const Args<T>& a, int64_t nv, cudaStream_t s) {
 }
 
 template <typename T>
-sg_status run(Args<T> a, cudaStream_t s) {
-    const int64_t nv = cdiv((int64_t)a.classes, kE<T>);  // vectors of a row, at most
-    const bool by_warp = nv <= 256;
-    // one cluster serves a call whose rows its warps hold at once (4 rows a warp, so that
-    // it would serve twice as many, are slower than two launches)
-    const int64_t rows = kSmallCtas * (kSmallThreads / 32) * (nv <= 64 ? kSmallRows<2> : kSmallRows<8>);
-    const bool small = by_warp && a.n_cap <= rows;
-    if (!small) {
-        a.counts = (int32_t)cdiv(a.n_cap, 2 * kCountThreads);
-        if (a.counts < 1) a.counts = 1;
-        if (a.counts > kCounts) a.counts = kCounts;
-        SG_CUDA(launch_pdl(k_distill_count, dim3((unsigned)a.counts), dim3(kCountThreads), 0, s, a.ids, a.values, a.k,
-                           a.classes, a.n_cap, a.d_n, a.done, a.total));
-        if (a.n_cap == 0) return SG_OK;
-    }
+sg_status run_rows(const Args<T>& a, bool small, int64_t nv, cudaStream_t s) {
     if (nv <= 32) return run_warp<T, 1>(a, small, s);
     if (nv <= 64) return run_warp<T, 2>(a, small, s);
     if (nv <= 128) return run_warp<T, 4>(a, small, s);
@@ -801,13 +961,45 @@ sg_status run(Args<T> a, cudaStream_t s) {
     }
 }
 
-size_t ws_bytes() { return 2048; }  // (1 + kCounts) counts
+template <typename T>
+sg_status run(Args<T> a, cudaStream_t s) {
+    const int64_t nv = cdiv((int64_t)a.classes, kE<T>);  // vectors of a row, at most
+    const bool by_warp = nv <= 256;
+    // one cluster serves a call whose rows its warps hold at once (4 rows a warp, so that
+    // it would serve twice as many, are slower than two launches)
+    const int64_t rows = kSmallCtas * (kSmallThreads / 32) * (nv <= 64 ? kSmallRows<2> : kSmallRows<8>);
+    const bool small = by_warp && a.n_cap <= rows;
+    float* const total = a.total;
+    if (a.temp > kPlainTemp) a.total = nullptr;  // the losses are not there yet
+    else a.stats = nullptr;
+    if (!small) {
+        a.counts = (int32_t)cdiv(a.n_cap, 2 * kCountThreads);
+        if (a.counts < 1) a.counts = 1;
+        if (a.counts > kCounts) a.counts = kCounts;
+        SG_CUDA(launch_pdl(k_distill_count, dim3((unsigned)a.counts), dim3(kCountThreads), 0, s, a.ids, a.values, a.k,
+                           a.classes, a.n_cap, a.d_n, a.done, total));
+        if (a.n_cap == 0) return SG_OK;
+    }
+    const sg_status st = run_rows<T>(a, small, nv, s);
+    if (st != SG_OK || !a.stats) return st;
+    if (small) a.counts = 1;
+    a.total = total;
+    int64_t blocks = cdiv(a.n_cap, kThreads / 32);
+    if (blocks < 1) blocks = 1;  // (the total)
+    if (blocks > 8 * (int64_t)num_sms()) blocks = 8 * (int64_t)num_sms();
+    SG_CUDA(launch_pdl(k_distill_loss<T>, dim3((unsigned)blocks), dim3(kThreads), 0, s, a));
+    return SG_OK;
+}
+
+// (1 + kCounts) counts; rows' maxima and sums
+constexpr size_t kCountBytes = 2048;
+size_t ws_bytes(int32_t n_cap) { return kCountBytes + (size_t)n_cap * sizeof(float2); }
 
 }  // namespace
 
 extern "C" size_t sg_distill_workspace(int32_t n_cap, int32_t n_classes) {
     if (n_cap < 0 || n_classes <= 0) return 0;
-    return ws_bytes();
+    return ws_bytes(n_cap);
 }
 
 extern "C" sg_status sg_distill(const void* d_logits, int32_t dtype, int32_t n_cap, const int32_t* d_n, int32_t n_classes,
@@ -823,8 +1015,8 @@ extern "C" sg_status sg_distill(const void* d_logits, int32_t dtype, int32_t n_c
     if (ld < n_classes || (d_grad && ld_grad < n_classes))
         return fail(SG_ERR_INVALID_ARG, "sg_distill: a row stride is below n_classes");
     if (n_cap > 0 && (!d_logits || !d_ids || !d_values || !d_loss)) return fail(SG_ERR_INVALID_ARG, "sg_distill: NULL array");
-    if (!d_workspace || (uintptr_t)d_workspace % 256 || workspace_bytes < ws_bytes())
-        return fail(SG_ERR_INVALID_ARG, "sg_distill: workspace needs %zu bytes, 256-byte aligned", ws_bytes());
+    if (!d_workspace || (uintptr_t)d_workspace % 256 || workspace_bytes < ws_bytes(n_cap))
+        return fail(SG_ERR_INVALID_ARG, "sg_distill: workspace needs %zu bytes, 256-byte aligned", ws_bytes(n_cap));
     const int e = dtype == SG_F32 ? 4 : 2;
     if ((uintptr_t)d_logits % e || (uintptr_t)d_grad % e ||
         ((uintptr_t)d_ids | (uintptr_t)d_values | (uintptr_t)d_loss | (uintptr_t)d_total) % 4)
@@ -832,13 +1024,14 @@ extern "C" sg_status sg_distill(const void* d_logits, int32_t dtype, int32_t n_c
     if (d_grad == d_logits && d_grad) return fail(SG_ERR_INVALID_ARG, "sg_distill: the gradient may not replace the logits");
     cudaStream_t s = (cudaStream_t)stream;
     const float l = kLog2e / temperature;
+    float2* const stats = (float2*)((char*)d_workspace + kCountBytes);
     if (dtype == SG_F32) {
         const Args<float> a = {(const float*)d_logits, (float*)d_grad, ld, ld_grad, d_ids, d_values, d_n, n_cap, n_classes,
-                               k, mean ? 1 : 0, grad_scale, temperature, 1.f / temperature, l, d_loss, d_total, (int32_t*)d_workspace, 0};
+                               k, mean ? 1 : 0, grad_scale, temperature, 1.f / temperature, l, d_loss, d_total, (int32_t*)d_workspace, 0, stats};
         return run(a, s);
     }
     const Args<__nv_bfloat16> a = {(const __nv_bfloat16*)d_logits, (__nv_bfloat16*)d_grad, ld, ld_grad, d_ids, d_values,
                                    d_n, n_cap, n_classes, k, mean ? 1 : 0, grad_scale, temperature, 1.f / temperature, l, d_loss, d_total,
-                                   (int32_t*)d_workspace, 0};
+                                   (int32_t*)d_workspace, 0, stats};
     return run(a, s);
 }
