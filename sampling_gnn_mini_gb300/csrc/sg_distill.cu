@@ -153,7 +153,7 @@ __device__ __forceinline__ float loss_of(const Args<T>& a, const Scale& c, const
         if (j >= a.k) break;
         const float q = n.q[j], x = n.x[j];
         if (q == 0.f) continue;
-        if (x == -INFINITY && Z == Z) s += INFINITY;
+        if (x == -INFINITY && q > 0.f && Z == Z) s += INFINITY;  // (not with NaN)
         else s = fmaf(q, ((n.v[j] - c.m) * inv - c.log_zq) + (log_z - (x - M) * inv), s);
     }
     return warp_sum(s) * (a.temp * a.temp);
@@ -830,7 +830,7 @@ __global__ void __launch_bounds__(kThreads) k_distill_loss(Args<T> a) {
             for (int32_t j = lane; j < a.k; j += 32) {
                 const float q = e.q[j], x = e.x[j];
                 if (q == 0.f) continue;
-                if (x == -INFINITY && Z == Z) {
+                if (x == -INFINITY && q > 0.f && Z == Z) {
                     s += INFINITY;
                     continue;
                 }
