@@ -141,11 +141,13 @@ __device__ __forceinline__ Scale scale_entries(const Args<T>& a, Entries& n) {
         if (lane + 32 * e < a.k) n.q[lane + 32 * e] = q[e] * inv;
     return {m, logf(z), z};
 }
-// The row's loss (one warp, the same in every lane), from the row's maximum M and sum Z.
+// The row's loss (one warp, the same in every lane), from the row's maximum M and sum Z:
+// T^2 (log q - log p) as T (difference of the logits) + T^2 (difference of the logarithms).
+// (A difference over T first is past fp32 for a class at the type's lowest value and T < 1.)
 template <typename T>
 __device__ __forceinline__ float loss_of(const Args<T>& a, const Scale& c, const Entries& n, float M, float Z) {
     const int lane = (int)lane_id();
-    const float log_z = logf(Z), inv = a.inv_temp;
+    const float apart = (logf(Z) - c.log_zq) * (a.temp * a.temp);
     float s = 0.f;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
@@ -154,9 +156,9 @@ __device__ __forceinline__ float loss_of(const Args<T>& a, const Scale& c, const
         const float q = n.q[j], x = n.x[j];
         if (q == 0.f) continue;
         if (x == -INFINITY && q > 0.f && Z == Z) s += INFINITY;  // (not with NaN)
-        else s = fmaf(q, ((n.v[j] - c.m) * inv - c.log_zq) + (log_z - (x - M) * inv), s);
+        else s = fmaf(q, fmaf(a.temp, (n.v[j] - c.m) - (x - M), apart), s);
     }
-    return warp_sum(s) * (a.temp * a.temp);
+    return warp_sum(s);
 }
 // One lane of a used row: its loss, and its statistics where they are asked for.
 template <typename T>

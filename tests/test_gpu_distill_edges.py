@@ -3,7 +3,7 @@ import pytest
 import torch
 
 from sampling_gnn_mini_gb300 import binding as sg
-from test_gpu_distill import INF, _case, _run
+from test_gpu_distill import DT, INF, _case, _reference, _run
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +34,20 @@ def test_bad_values_of_classes_without_a_logit(n, c, T, bad):
     # and +inf where the values are good
     v[1, 0] = 1.0
     assert float(_run(x, ids, v, T, mean=False)[0][1]) == INF
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n,c", [(20, 60), (300, 900), (6, 40001), (700, 9001)])
+@pytest.mark.parametrize("T", [0.001, 0.1, 0.7, 1.0])
+def test_a_teachers_class_at_the_types_lowest_value(n, c, T, dt):
+    # the loss is T q times the logits' difference, which T below 1 leaves in range
+    x, ids, v = _case(n, c, 5, dt, c)
+    ids = ids.clamp(min=0)
+    v = torch.nan_to_num(v, neginf=0.0) * T  # q does not fall below the type's range
+    x[1, ids[1, 1].long()] = torch.finfo(DT[dt]).min
+    x[0, ids[0].long()] = torch.finfo(DT[dt]).min
+    got = _run(x, ids, v, T, mean=False)
+    want, tol = _reference(x, ids, v, T, False, 1.0)[:2]
+    fits = want < 3.4e38  # (T = 1: q just below 1 may not)
+    assert bool(fits[1]) and bool((((got[0].double() - want).abs() <= tol) | ~fits).all())
+    assert bool(torch.isfinite(got[0][fits]).all()) and bool(torch.isfinite(got[2]).all())
