@@ -661,7 +661,10 @@ constexpr int kMaxDim = SG_MAX_NORM_DIM;
 // Blocks that fill the device, a multiple of 8.
 int64_t all_blocks(int per_sm) { return (int64_t)num_sms() * per_sm / 8 * 8; }
 // Blocks of the gradient at most, whatever the form: the workspace has room for them.
-int64_t max_parts(int32_t dim) { return all_blocks(dim <= 1024 ? 12 : dim <= 2048 ? 6 : dim <= 4096 ? 3 : 1); }
+// (By the widths where by_size() changes its forms, which go by whole vectors: up to 7
+// values more.  4,097 to 4,608 columns run two blocks an SM: 9,746 x 4104 fp32 79 us, with
+// room for one 94; 19,526 x 4097 bf16 97, 124.)
+int64_t max_parts(int32_t dim) { return all_blocks(dim < 1032 ? 12 : dim < 2056 ? 6 : dim < 4616 ? 3 : 1); }
 unsigned grid_of(int64_t rows, int per_sm) {
     const int64_t most = all_blocks(per_sm);
     return (unsigned)(rows < most ? rows : most);
@@ -759,7 +762,7 @@ sg_status by_size(const A& a, More... more) {
         if (vecs <= 128 * V && vecs > 96 * V) return go_ring<T, V, 128, kBlockThreads<2>>(a, more...);
         if (vecs <= 256 * V && vecs > 192 * V) return go_ring<T, V, 256, kBlockThreads<2>>(a, more...);
         if (vecs <= 512 * V && vecs > 384 * V) return go_ring<T, V, 512, kBlockThreads<2>>(a, more...);
-        // (24 values a thread leave room for two blocks: 9,746 x 4104 fp32 140 -> 95 us)
+        // (24 values a thread leave room for two blocks: 9,746 x 4104 fp32 79 us, by one of 16 140)
         if (vecs <= 288 * V && vecs > 256 * V) return go_ring<T, 3 * V / 2, 0, 192>(a, more...);
         if (vecs <= kBlockThreads<2> * V) return go_ring<T, V, 0, kBlockThreads<2>>(a, more...);
     }
