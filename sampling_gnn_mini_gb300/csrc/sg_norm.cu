@@ -428,8 +428,8 @@ __device__ __forceinline__ void grad_row(const BwdArgs<T>& a, const Part<T, V, L
     group_sum<L, 2>(s, sh, turn);
     between();
     if (r >= n) return;
-    // dx = rstd g w + (x - mean) ch + cg
-    const float cg = -s[0] * inv * rstd, ch = -s[1] * inv * rstd * rstd;
+    // dx = rstd (g w - s0 / dim - h s1 / dim)
+    const float cg = -s[0] * inv, ch = -s[1] * inv;
     T* to = a.dx + r * a.ld_dx;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -438,12 +438,12 @@ __device__ __forceinline__ void grad_row(const BwdArgs<T>& a, const Part<T, V, L
         pairs_of(g(v), f);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            f[i] = fma2(mul2(f[i], w.f[v][i]), rs, fma2(add2(h[i], mu), both(ch), both(cg)));
+            f[i] = mul2(fma2(f[i], w.f[v][i], fma2(mul2(add2(h[i], mu), rs), both(ch), both(cg))), rs);
         }
         p.store(to, v, f);
     }
 #pragma unroll
-    for (int e = 0; e < NE; ++e) p.store_end(to, e, fmaf(ge[e] * w.end[e], rstd, fmaf(xe[e] - mean, ch, cg)));
+    for (int e = 0; e < NE; ++e) p.store_end(to, e, fmaf(ge[e], w.end[e], fmaf((xe[e] - mean) * rstd, ch, cg)) * rstd);
 }
 
 // Blocks an SM: bf16 vectors hold twice the values.

@@ -89,3 +89,20 @@ def test_sums_of_whole_numbers(n, d, apart, dt):
         sg.sg_stream_check()
         assert torch.equal(dw, (x[:count] * g[:count]).sum(0, dtype=torch.int64).float())
         assert torch.equal(db, g[:count].sum(0, dtype=torch.int64).float())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [5, 64, 128, 300, 1001, 4096, 4104, 10000])
+@pytest.mark.parametrize("size", [1e-20, 1e20])
+def test_gradient_of_tiny_and_huge_rows(d, size, dt):
+    # 1 / deviation squared is past fp32's range there, dx is not
+    n = 40
+    x, g, w, _ = _inputs(n, d, dt, "f32", d)
+    x = (x.float() * size).to(DT[dt])
+    m, r = torch.zeros(n, device="cuda"), torch.full((n,), 0.7 / size, device="cuda")
+    for start in (0, 1):  # g like x, and not
+        pg, dx = _Placed(g, start, 0), torch.full_like(x, 7.0)
+        dw, db = torch.full((d,), 7.0, device="cuda"), torch.full((d,), 7.0, device="cuda")
+        sg.sg_layernorm_bwd(pg.t, x, w, m, r, n, None, dx, dw, db, _ws(n, d))
+        sg.sg_stream_check()
+        _hold_bwd(g, x, w, m, r, dx, dw, db)
