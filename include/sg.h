@@ -711,7 +711,9 @@ sg_status sg_distill(const void* d_logits, int32_t dtype, int32_t n_cap, const i
  *   mean[r] = mean of x[r, :],  rstd[r] = 1 / sqrt(mean of (x[r, :] - mean[r])^2 + eps)
  *   y[r, c] = (x[r, c] - mean[r]) rstd[r] weight[c] + bias[c]
  * in fp32 (the deviation about the mean, in a second pass over the row on the
- * chip), rounded once to the output's type.
+ * chip), rounded once to the output's type.  So the mean is off by up to 2^-20 of the
+ * mean of |x|, and y by that times rstd (a row of equal values far from 0 is not quite
+ * its bias); the deviations' squares have to sum up below fp32's largest value.
  *   d_x, d_y   device [n_cap x dim], SG_F32 or SG_BF16, row strides ld and ld_y
  *              elements (>= dim), any element alignment (rows and strides on 16
  *              bytes are fastest); d_y may be d_x with the same stride, but must not

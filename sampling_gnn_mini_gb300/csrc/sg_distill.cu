@@ -307,10 +307,11 @@ __device__ __forceinline__ float finish_row(const Args<T>& a, int32_t r, float w
 }
 
 // A warp a row, with as many vectors a lane as hold it.  Rows of few classes are bound by
-// instructions, some 700 issue slots a row whatever its length (200,000 x 47 fp32: 115 us, 11 for the
-// bytes); the next row's loads ahead in registers, or more warps, gain nothing (115 and
-// 123).  us, k = 20: 60,000 x 400 fp32 52 (floor 30), 40,000 x 2000 bf16 73 (48), 20,000 x
-// 4000 bf16 76 (by blocks of 256 threads from shared memory 123, of 64 from registers 124).
+// instructions, some 500 of them in 700 issue slots a row whatever its length: 200,000 x 47
+// fp32, k = 20: 122 us, 15.8 for the bytes.  The next row's loads ahead in registers take 130, six
+// blocks an SM 126.  us, k = 20: 60,000 x 400 fp32 53 (floor 30), 40,000 x 2000 bf16 74 (48),
+// 20,000 x 4000 bf16 76 (by blocks of 256 threads from shared memory 123, of 64 from
+// registers 124).
 template <int NV>
 constexpr int kWarpBlocks = NV <= 2 ? 5 : NV == 4 ? 4 : NV == 8 ? 3 : 2;  // an SM
 
