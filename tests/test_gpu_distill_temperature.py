@@ -33,7 +33,7 @@ def _tolerance(x, ids, v, T):
     n, c = x.shape
     x, v, ids = x.double(), v.double(), ids.long()
     there = (ids >= 0) & (v > -INF)
-    there &= there[:, :1]
+    there = there & there[:, :1]
     at = ids.clamp(min=0)
     lowest = torch.full_like(v, -INF)
     top = torch.where(there, v, lowest).amax(1, keepdim=True)
@@ -42,7 +42,7 @@ def _tolerance(x, ids, v, T):
     zq = torch.where(there, torch.exp(-a), torch.zeros_like(a)).sum(1, keepdim=True)
     zq = torch.where(zq == 0, torch.ones_like(zq), zq)
     q = torch.where(there, torch.exp(-a), torch.zeros_like(a)) / zq
-    there &= q > 1e-36  # (the others are 0, or nothing)
+    there = there & (q > 1e-36)  # (the others are 0, or nothing)
     d = (x.amax(1, keepdim=True) - x) / T
     z = torch.exp(-d).sum(1, keepdim=True)
     p = torch.exp(-d) / z
