@@ -685,9 +685,9 @@ sg_status sg_logprobs(const void* d_logits, int32_t dtype, int32_t n_cap, const 
  * q > 0 there makes the loss +inf, and in a row whose logits are all -inf the
  * gradient is 0.  +inf or NaN logits give NaN in their row, such values NaN in
  * its loss and at the gradient of its entries' classes.  Statistics are held in
- * fp32; total's order of summation is fixed.  A loss is off by 2^-16 of itself at
- * most and, however close the two distributions come, by some 2^-18 more up to T = 4, by
- * 2^-20 above.
+ * fp32; total's order of summation is fixed.  A loss is off by some 2^-16 of
+ * itself at most and, however close the two distributions come, by some 2^-18 more up
+ * to T = 4, by 2^-20 above.
  *   d_logits   device [n_cap x n_classes], row stride ld elements (>= n_classes),
  *              SG_F32 or SG_BF16, any element alignment; n_cap up to 2^27
  *   d_n        device int32 count (n = *d_n <= n_cap) or NULL (n = n_cap)
@@ -711,7 +711,7 @@ sg_status sg_distill(const void* d_logits, int32_t dtype, int32_t n_cap, const i
  *   mean[r] = mean of x[r, :],  rstd[r] = 1 / sqrt(mean of (x[r, :] - mean[r])^2 + eps)
  *   y[r, c] = (x[r, c] - mean[r]) rstd[r] weight[c] + bias[c]
  * in fp32 (the deviation about the mean, in a second pass over the row on the
- * chip), rounded once to the output's type.  So the mean is off by up to 2^-20 of the
+ * chip), rounded once to the output's type.  So the mean is off by up to 2^-19 of the
  * mean of |x|, and y by that times rstd (a row of equal values far from 0 is not quite
  * its bias); the deviations' squares have to sum up below fp32's largest value.
  *   d_x, d_y   device [n_cap x dim], SG_F32 or SG_BF16, row strides ld and ld_y
